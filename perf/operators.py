@@ -1,0 +1,487 @@
+"""Measured cases of the block-scaled 8-bit operators and of the experts built on them.
+
+Each case names an operator ("op") and its sizes. ``prepare`` makes the tensors that a
+program has in hand, ``run`` makes one pass: in the plain form (elementary torch
+operations in 32 bits, or in 64 where a choice hangs on it) or, with ``own`` set, through
+the package's entry points. ``exact`` gives the definition in 64 bits.
+
+  quantize          X -> Q (8 bits) and one scale for each block of 1 x 128 or 128 x 128
+  product           C = (A as its values) (B as its values)^T, both in 8 bits with block scales
+  experts           the same product for rows sorted by expert, each expert with its own B
+  experts_gradient  the weight gradient of that product: one C for each expert's rows
+  route             scores, choice of k experts, weights, rows sorted by expert; and its gradient
+  combine           the weighted sum of a token's k rows; and its gradients
+"""
+import math
+
+import torch
+
+own = False
+
+BLOCK = 128
+DTYPES = {"f32": torch.float32, "f16": torch.float16, "bf16": torch.bfloat16}
+SIZE = {"f32": 4, "f16": 2, "bf16": 2}
+QTYPES = {"e4m3": torch.float8_e4m3fn, "e5m2": torch.float8_e5m2}
+QMAX = {"e4m3": 448.0, "e5m2": 57344.0}
+AMAX_FLOOR = 2.0 ** -100  # a block's largest magnitude counts as at least this
+
+
+def blocks(n):
+    return -(-n // BLOCK)
+
+
+# ----------------------------------------------------------------------------- cases
+def listed():
+    return [
+        # activations of a few decoding sequences, on their way into a product
+        {"name": "quantize_tokens", "op": "quantize", "M": 16, "K": 4096, "dtype": "bf16", "qtype": "e4m3",
+         "block_rows": 1, "natural": True, "transposed": False, "gather": False},
+        # activations of a training step: the rows for the forward product, their transpose for the weight gradient
+        {"name": "quantize_train", "op": "quantize", "M": 8192, "K": 4096, "dtype": "bf16", "qtype": "e4m3",
+         "block_rows": 1, "natural": True, "transposed": True, "gather": False},
+        # one token through a linear layer
+        {"name": "product_token", "op": "product", "M": 1, "N": 4096, "K": 4096, "a_type": "e4m3", "b_type": "e4m3",
+         "b_block_rows": 128, "out": "bf16"},
+        # the forward product of a training step
+        {"name": "product_forward", "op": "product", "M": 8192, "N": 4096, "K": 4096, "a_type": "e4m3",
+         "b_type": "e4m3", "b_block_rows": 128, "out": "bf16"},
+        # a weight gradient: both operands transposed activations with a scale for each row, odd sizes
+        {"name": "product_gradient", "op": "product", "M": 2056, "N": 4000, "K": 8176, "a_type": "e5m2",
+         "b_type": "e4m3", "b_block_rows": 1, "out": "f32"},
+        # a decoding batch through the experts: a few rows each, the weights' bytes count
+        {"name": "experts_tokens", "op": "experts", "T": 16, "k": 4, "E": 64, "N": 2048, "K": 2048, "align": 1,
+         "a_type": "e4m3", "b_type": "e4m3", "out": "bf16"},
+        # a prompt or a training batch through the experts
+        {"name": "experts_forward", "op": "experts", "T": 4096, "k": 8, "E": 64, "N": 2048, "K": 2048, "align": 128,
+         "a_type": "e4m3", "b_type": "e4m3", "out": "bf16"},
+        # the experts' weight gradients of that batch
+        {"name": "experts_gradient", "op": "experts_gradient", "T": 4096, "k": 8, "E": 64, "M": 2048, "N": 1024,
+         "a_type": "e5m2", "b_type": "e4m3", "out": "f32"},
+        # routing of a decoding batch
+        {"name": "route_tokens", "op": "route", "T": 16, "E": 64, "k": 4, "groups": 1, "top_groups": 1,
+         "group_top": 1, "score": "softmax", "bias": False, "renorm": True, "factor": 1.0, "dtype": "bf16",
+         "align": 1, "backward": False},
+        # routing of a training batch: sigmoid scores, a bias for balance, groups, and the gradient
+        {"name": "route_train", "op": "route", "T": 16384, "E": 256, "k": 8, "groups": 8, "top_groups": 4,
+         "group_top": 2, "score": "sigmoid", "bias": True, "renorm": True, "factor": 2.5, "dtype": "f32",
+         "align": 128, "backward": True},
+        # the experts' rows of a decoding batch back to its tokens
+        {"name": "combine_tokens", "op": "combine", "T": 16, "k": 4, "E": 64, "N": 2048, "align": 1, "dtype": "bf16",
+         "backward": False},
+        # a training batch: forward and both gradients
+        {"name": "combine_train", "op": "combine", "T": 4096, "k": 8, "E": 64, "N": 4096, "align": 128,
+         "dtype": "bf16", "backward": True},
+    ]
+
+
+def _log(rng, low, high):
+    """A whole number spread over the logarithm of low..high."""
+    return max(low, min(high, int(round(math.exp(rng.uniform(math.log(low), math.log(high)))))))
+
+
+def _width(rng, low, high):
+    """A row's length: mostly whole blocks, else a multiple of 16, else any number."""
+    n = _log(rng, low, high)
+    step = rng.choice([BLOCK, BLOCK, 16, 1])
+    return max(low, n // step * step)
+
+
+def draw(rng):
+    op = rng.choice(["quantize", "product", "product", "experts", "experts", "experts_gradient", "route", "combine"])
+    types = {"a_type": rng.choice(["e4m3", "e4m3", "e5m2"]), "b_type": rng.choice(["e4m3", "e4m3", "e5m2"]),
+             "out": rng.choice(["bf16", "bf16", "f16", "f32"])}
+    if op == "quantize":
+        forms = rng.choice([(True, False), (False, True), (True, True)])
+        return {"op": op, "M": _log(rng, 1, 8192), "K": _width(rng, 128, 4096),
+                "dtype": rng.choice(["bf16", "bf16", "f16", "f32"]), "qtype": rng.choice(["e4m3", "e4m3", "e5m2"]),
+                "block_rows": rng.choice([1, 1, 128]), "natural": forms[0], "transposed": forms[1],
+                "gather": rng.random() < 0.25}
+    if op == "product":
+        return {"op": op, "M": _log(rng, 1, 8192), "N": _width(rng, 128, 4096), "K": _width(rng, 128, 4096),
+                "b_block_rows": rng.choice([128, 128, 1]), **types}
+    E = rng.choice([8, 16, 32, 64])
+    k = rng.choice([1, 2, 4, 6, 8])
+    T = _log(rng, 1, 4096)
+    if op == "experts":
+        return {"op": op, "T": T, "k": k, "E": E, "N": _width(rng, 256, 2048), "K": _width(rng, 256, 2048),
+                "align": rng.choice([1, 128]), **types}
+    if op == "experts_gradient":
+        return {"op": op, "T": T, "k": k, "E": E, "M": _width(rng, 256, 2048), "N": _width(rng, 256, 1024), **types}
+    if op == "combine":
+        return {"op": op, "T": T, "k": k, "E": E, "N": _width(rng, 256, 4096), "align": rng.choice([1, 128]),
+                "dtype": rng.choice(["bf16", "bf16", "f16", "f32"]), "backward": rng.random() < 0.5}
+    E = rng.choice([8, 60, 64, 128, 160, 256])
+    groups = rng.choice([1, 1, 4, 2])
+    score = rng.choice(["softmax", "sigmoid"])
+    top_groups = rng.randint(max(1, groups // 2), groups)
+    return {"op": op, "T": _log(rng, 1, 16384), "E": E, "k": min(k, top_groups * (E // groups)), "groups": groups,
+            "top_groups": top_groups, "group_top": rng.choice([1, 2]), "score": score,
+            "bias": rng.random() < 0.5, "renorm": rng.random() < 0.7, "factor": rng.choice([1.0, 2.5]),
+            "dtype": rng.choice(["f32", "bf16", "f16"]), "align": rng.choice([1, 128]),
+            "backward": rng.random() < 0.5}
+
+
+def capacity(case):
+    """Rows that hold every expert's rows, each expert's first at a multiple of `align`."""
+    n, align = case["T"] * case["k"], case["align"]
+    return -(-(n + min(case["E"], n) * (align - 1)) // align) * align
+
+
+def work(case):
+    op = case["op"]
+    if op == "quantize":
+        n, b = case["M"] * case["K"], case["block_rows"]
+        moved = n * SIZE[case["dtype"]] + (4 * case["M"] if case["gather"] else 0)
+        if case["natural"]:
+            moved += n + 4 * -(-case["M"] // b) * blocks(case["K"])
+        if case["transposed"]:
+            moved += n + 4 * -(-case["K"] // b) * blocks(case["M"])
+        return {"bytes": moved, "flops": 3 * n}
+    if op == "product":
+        M, N, K = case["M"], case["N"], case["K"]
+        scales = 4 * blocks(K) * (M + -(-N // case["b_block_rows"]))
+        return {"bytes": M * K + N * K + scales + M * N * SIZE[case["out"]], "flops": 2 * M * N * K}
+    if op == "route":
+        T, E, k = case["T"], case["E"], case["k"]
+        moved = T * E * SIZE[case["dtype"]] + T * k * 16 + 8 * E
+        if case["backward"]:
+            moved += 2 * T * E * SIZE[case["dtype"]] + 8 * T * k
+        return {"bytes": moved, "flops": 8 * T * E}
+    T, k, E = case["T"], case["k"], case["E"]
+    rows = T * k
+    if op == "combine":
+        s = SIZE[case["dtype"]]
+        moved = (rows + T) * case["N"] * s + 8 * rows
+        if case["backward"]:
+            moved += (2 * rows + T) * case["N"] * s + 4 * rows
+        return {"bytes": moved, "flops": (4 if case["backward"] else 2) * rows * case["N"]}
+    active = E * (1 - (1 - min(1, k / E)) ** T)  # experts that get a token, were all equally likely
+    if op == "experts":
+        N, K = case["N"], case["K"]
+        return {"bytes": active * N * K + T * K + rows * N * SIZE[case["out"]] + 4 * T * blocks(K),
+                "flops": 2 * rows * N * K}
+    M, N = case["M"], case["N"]
+    return {"bytes": rows * (M + N) + 4 * blocks(rows) * (M + N) + E * M * N * SIZE[case["out"]],
+            "flops": 2 * rows * M * N}
+
+
+# ----------------------------------------------------------------------------- the data a program has in hand
+def _gen(seed):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    return g
+
+
+def _randn(g, *shape):
+    return torch.randn(*shape, generator=g, device="cuda")
+
+
+def _activations(g, rows, cols):
+    """Normal values whose columns differ in size, as a layer's channels do."""
+    return _randn(g, rows, cols) * torch.exp(0.5 * _randn(g, 1, cols))
+
+
+def _codes(x, qtype, block_rows):
+    """x (..., R, K) in 8 bits with block scales, scales laid out with the rows adjacent."""
+    q, s = plain_quantize(x, qtype, block_rows)
+    return q, s.transpose(-1, -2).contiguous().transpose(-1, -2)
+
+
+def _choice(g, T, E, k):
+    """k experts for each token, some experts more popular than others."""
+    return torch.topk(_randn(g, T, E) + 0.5 * _randn(g, 1, E), k, dim=1).indices.to(torch.int32)
+
+
+def prepare(case, seed):
+    g = _gen(seed)
+    op = case["op"]
+    if op == "quantize":
+        M, K = case["M"], case["K"]
+        x = _activations(g, M, K).to(DTYPES[case["dtype"]])
+        rows = None
+        if case["gather"]:  # rows in another order, some of them padding
+            rows = torch.randperm(M, generator=g, device="cuda").to(torch.int32)
+            rows = torch.where(torch.rand(M, generator=g, device="cuda") < 0.1, -1, rows).to(torch.int32)
+        return {"case": case, "x": x, "rows": rows}
+    if op == "product":
+        a = _codes(_activations(g, case["M"], case["K"]), case["a_type"], 1)
+        b = _codes(_randn(g, case["N"], case["K"]) * 0.02, case["b_type"], case["b_block_rows"])
+        return {"case": case, "a": a, "b": b}
+    if op == "route":
+        T, E, k = case["T"], case["E"], case["k"]
+        logits = (_randn(g, T, E) + 0.5 * _randn(g, 1, E)).to(DTYPES[case["dtype"]])
+        return {"case": case, "logits": logits, "bias": 0.1 * _randn(g, E) if case["bias"] else None,
+                "weight_grad": _randn(g, T, k)}
+    index = _choice(g, case["T"], case["E"], case["k"])
+    if op == "experts_gradient":
+        case = {**case, "align": BLOCK}
+    plan = plain_dispatch(case, index)
+    state = {"case": case, "plan": plan, "host": plan["offsets"].tolist()}
+    P = capacity(case)
+    if op == "experts":
+        state["a"] = _codes(_activations(g, case["T"], case["K"]), case["a_type"], 1)
+        state["b"] = _codes(_randn(g, case["E"], case["N"], case["K"]) * 0.02, case["b_type"], BLOCK)
+    elif op == "experts_gradient":
+        live = (plan["rows"] >= 0).float()[None, :]  # padding rows hold zeros
+        state["a"] = _codes(_randn(g, case["M"], P) * 0.01 * live, case["a_type"], 1)
+        state["b"] = _codes(_activations(g, P, case["N"]).t() * live, case["b_type"], 1)
+    else:
+        dt = DTYPES[case["dtype"]]
+        state["y"] = (_activations(g, P, case["N"]) * (plan["rows"] >= 0)[:, None]).to(dt)
+        w = torch.rand(case["T"], case["k"], generator=g, device="cuda") + 0.1
+        state["weight"] = w / w.sum(1, keepdim=True)
+        state["grad"] = _randn(g, case["T"], case["N"]).to(dt)
+    return state
+
+
+# ----------------------------------------------------------------------------- the plain forms
+def plain_quantize(x, qtype, block_rows):
+    """(Q, S) of x (..., R, K): S = max|x| / qmax over blocks of block_rows x 128, Q = x * (qmax / max|x|)."""
+    *lead, R, K = x.shape
+    kb, rb = blocks(K), -(-R // block_rows)
+    x = x.float()
+    pad = x.new_zeros(*lead, rb * block_rows, kb * BLOCK)
+    pad[..., :R, :K] = x
+    amax = pad.abs().reshape(*lead, rb, block_rows, kb, BLOCK).amax(dim=(-3, -1))
+    amax = amax.clamp(min=AMAX_FLOOR)
+    inv = (QMAX[qtype] / amax).repeat_interleave(block_rows, -2)[..., :R, :].repeat_interleave(BLOCK, -1)[..., :K]
+    return (x * inv).to(QTYPES[qtype]), amax / QMAX[qtype]
+
+
+def values(q, s, block_rows):
+    """The numbers that codes and scales stand for, in 32 bits."""
+    R, K = q.shape[-2:]
+    s = s.repeat_interleave(block_rows, -2)[..., :R, :].repeat_interleave(BLOCK, -1)[..., :K]
+    return q.float() * s
+
+
+def plain_scores(case, logits):
+    """Scores in 64 bits: the choice among them hangs on differences that 32 bits lose."""
+    x = logits.double()
+    if case["score"] == "sigmoid":
+        return torch.sigmoid(x)
+    e = torch.exp(x - x.amax(1, keepdim=True))
+    return e / e.sum(1, keepdim=True)
+
+
+def plain_route(case, logits, bias):
+    T, E, k, G = case["T"], case["E"], case["k"], case["groups"]
+    s = plain_scores(case, logits)
+    choice = s if bias is None else s + bias.double()
+    if G > 1:
+        best = choice.reshape(T, G, E // G).sort(dim=2, descending=True).values[:, :, :case["group_top"]].sum(2)
+        kept = best.sort(dim=1, descending=True, stable=True).indices[:, :case["top_groups"]]
+        mask = torch.zeros(T, G, dtype=torch.bool, device=s.device).scatter_(1, kept, True)
+        choice = choice.masked_fill(~mask.repeat_interleave(E // G, 1), -math.inf)
+    index = choice.sort(dim=1, descending=True, stable=True).indices[:, :k]
+    w = s.gather(1, index)
+    if case["renorm"]:
+        w = w / w.sum(1, keepdim=True)
+    return index.to(torch.int32), (w * case["factor"]).float()
+
+
+def plain_route_backward(case, logits, index, weight_grad):
+    s = plain_scores(case, logits)
+    i = index.long()
+    g = weight_grad.double() * case["factor"]
+    if case["renorm"]:
+        picked = s.gather(1, i)
+        total = picked.sum(1, keepdim=True)
+        g = (g - (g * picked).sum(1, keepdim=True) / total) / total
+    ds = torch.zeros_like(s).scatter_(1, i, g)
+    dx = s * (ds - (ds * s).sum(1, keepdim=True)) if case["score"] == "softmax" else ds * s * (1 - s)
+    return dx.to(logits.dtype)
+
+
+def plain_dispatch(case, index):
+    """Every expert's (token, slot) pairs in their order, an expert's first at a multiple of `align`."""
+    E, k, align, P = case["E"], case["k"], case["align"], capacity(case)
+    flat = index.reshape(-1).long()
+    n = flat.numel()
+    counts = (flat[:, None] == torch.arange(E, device=flat.device)).sum(0)
+    ends = ((counts + align - 1) // align * align).cumsum(0)
+    offsets = torch.cat([ends.new_zeros(1), ends])
+    order = flat.sort(stable=True).indices
+    before = counts.cumsum(0) - counts
+    place = torch.empty_like(flat)
+    place[order] = torch.arange(n, device=flat.device) - before[flat[order]] + offsets[:-1][flat[order]]
+    rows = torch.full((P,), -1, dtype=torch.int64, device=flat.device)
+    rows[place] = torch.arange(n, device=flat.device) // k
+    return {"offsets": offsets.to(torch.int32), "counts": counts.to(torch.int32), "rows": rows.to(torch.int32),
+            "position": place.to(torch.int32).reshape(index.shape)}
+
+
+def plain_run(state):
+    case = state["case"]
+    op = case["op"]
+    if op == "quantize":
+        x = state["x"].float()
+        if state["rows"] is not None:
+            x = x[state["rows"].clamp(min=0).long()] * (state["rows"] >= 0)[:, None]
+        out = {}
+        if case["natural"]:
+            out["q"], out["s"] = plain_quantize(x, case["qtype"], case["block_rows"])
+        if case["transposed"]:
+            out["qt"], out["st"] = plain_quantize(x.t().contiguous(), case["qtype"], case["block_rows"])
+        return out
+    if op == "product":
+        a, b = values(*state["a"], 1), values(*state["b"], case["b_block_rows"])
+        return (a @ b.t()).to(DTYPES[case["out"]])
+    if op == "route":
+        index, weight = plain_route(case, state["logits"], state["bias"])
+        out = {"index": index, "weight": weight, **plain_dispatch(case, index)}
+        if case["backward"]:
+            out["logits_grad"] = plain_route_backward(case, state["logits"], index, state["weight_grad"])
+        return out
+    plan = state["plan"]
+    if op == "combine":
+        at, w = plan["position"].long(), state["weight"]
+        y = state["y"].float()
+        out = {"out": (y[at.reshape(-1)].reshape(*at.shape, -1) * w[:, :, None]).sum(1).to(state["y"].dtype)}
+        if case["backward"]:
+            g = state["grad"].float()
+            picked = y[at.reshape(-1)].reshape(*at.shape, -1)
+            out["weight_grad"] = (picked * g[:, None, :]).sum(2)
+            y_grad = torch.zeros_like(y)
+            y_grad[at.reshape(-1)] = (w[:, :, None] * g[:, None, :]).reshape(-1, g.shape[1])
+            out["y_grad"] = y_grad.to(state["y"].dtype)
+        return out
+    at = state["host"]  # one product for each expert, as a plain program has them
+    if op == "experts":
+        a = values(*state["a"], 1)[plan["rows"].clamp(min=0).long()] * (plan["rows"] >= 0)[:, None]
+        c = torch.zeros(a.shape[0], case["N"], dtype=torch.float32, device=a.device)
+        for e in range(case["E"]):
+            if at[e + 1] > at[e]:
+                b = values(state["b"][0][e], state["b"][1][e], BLOCK)
+                torch.matmul(a[at[e]:at[e + 1]], b.t(), out=c[at[e]:at[e + 1]])
+    else:
+        a, b = values(*state["a"], 1), values(*state["b"], 1)
+        c = torch.zeros(case["E"], case["M"], case["N"], dtype=torch.float32, device=a.device)
+        for e in range(case["E"]):
+            if at[e + 1] > at[e]:
+                torch.matmul(a[:, at[e]:at[e + 1]], b[:, at[e]:at[e + 1]].t(), out=c[e])
+    return c.to(DTYPES[case["out"]])
+
+
+# ----------------------------------------------------------------------------- the package's entry points
+def own_run(state):
+    import dense_gemm_06_amd as dg
+
+    case = state["case"]
+    op = case["op"]
+    if op == "quantize":
+        q, qt = dg.gemm_block_quantize_tensors(state["x"], QTYPES[case["qtype"]], case["block_rows"],
+                                               natural=case["natural"], transposed=case["transposed"],
+                                               rows=state["rows"])
+        return {**({"q": q.data, "s": q.scale} if q else {}), **({"qt": qt.data, "st": qt.scale} if qt else {})}
+    if op == "product":
+        return dg.gemm_block_product_tensors(dg.BlockTensor(*state["a"], 1),
+                                             dg.BlockTensor(*state["b"], case["b_block_rows"]), DTYPES[case["out"]])
+    if op == "route":
+        router = dg.router(top_k=case["k"], score=case["score"], groups=case["groups"],
+                           top_groups=case["top_groups"], group_top=case["group_top"], renorm=case["renorm"],
+                           factor=case["factor"])
+        index, weight = dg.gemm_experts_route_tensors(state["logits"], router, state["bias"])
+        plan = dg.gemm_experts_dispatch_tensors(index, case["E"], case["align"])
+        out = {"index": index, "weight": weight, "offsets": plan.offsets, "counts": plan.counts, "rows": plan.rows,
+               "position": plan.position}
+        if case["backward"]:
+            out["logits_grad"] = dg.gemm_experts_route_backward_tensors(state["logits"], router, index,
+                                                                        state["weight_grad"])
+        return out
+    p = state["plan"]
+    plan = dg.ExpertPlan(p["offsets"], p["counts"], p["rows"], p["position"])
+    if op == "experts":
+        return dg.gemm_experts_product_tensors(dg.BlockTensor(*state["a"], 1), dg.BlockTensor(*state["b"], BLOCK),
+                                               plan, DTYPES[case["out"]], gather=True)
+    if op == "experts_gradient":
+        return dg.gemm_experts_gradient_tensors(dg.BlockTensor(*state["a"], 1), dg.BlockTensor(*state["b"], 1), plan,
+                                                DTYPES[case["out"]])
+    out = {"out": dg.gemm_experts_combine_tensors(state["y"], plan, state["weight"])}
+    if case["backward"]:
+        out["y_grad"], out["weight_grad"] = dg.gemm_experts_combine_backward_tensors(state["y"], plan,
+                                                                                     state["weight"], state["grad"])
+    return out
+
+
+def run(state):
+    if own:
+        return own_run(state)
+    return plain_run(state)
+
+
+# ----------------------------------------------------------------------------- the definitions in 64 bits
+def _spread(s, rows, cols, block_rows):
+    """Scale of each element, in 64 bits."""
+    r = torch.arange(rows, device=s.device) // block_rows
+    c = torch.arange(cols, device=s.device) // BLOCK
+    return s.double()[..., r[:, None], c[None, :]]
+
+
+def _numbers(q, s, block_rows):
+    return q.double() * _spread(s, q.shape[-2], q.shape[-1], block_rows)
+
+
+def _exact_codes(x, qtype, block_rows):
+    """Before its rounding, what a code stands for; and the scale."""
+    R, K = x.shape
+    top = torch.nn.functional.pad(x.abs(), (0, -K % BLOCK, 0, -R % block_rows))
+    top = top.unfold(0, block_rows, block_rows).unfold(1, BLOCK, BLOCK).flatten(2).max(2).values
+    s = torch.maximum(top, torch.full_like(top, AMAX_FLOOR)) / QMAX[qtype]
+    return x / _spread(s, R, K, block_rows), s
+
+
+def exact(case, seed):
+    state = prepare(case, seed)
+    op = case["op"]
+    if op == "quantize":
+        x = state["x"].double()
+        if state["rows"] is not None:
+            kept = state["rows"] >= 0
+            y = torch.zeros_like(x)
+            y[kept] = x[state["rows"][kept].long()]
+            x = y
+        out = {}
+        if case["natural"]:
+            out["q"], out["s"] = _exact_codes(x, case["qtype"], case["block_rows"])
+        if case["transposed"]:
+            out["qt"], out["st"] = _exact_codes(x.t(), case["qtype"], case["block_rows"])
+        return out
+    if op == "product":
+        return _numbers(*state["a"], 1) @ _numbers(*state["b"], case["b_block_rows"]).t().contiguous()
+    if op == "route":
+        x = state["logits"].double()
+        index = plain_route(case, state["logits"], state["bias"])[0].long()  # the choice is compared as whole numbers
+        chosen = torch.zeros_like(x, dtype=torch.bool).scatter_(1, index, True)
+        x.requires_grad_(True)
+        s = 1 / (1 + torch.exp(-x)) if case["score"] == "sigmoid" else torch.exp(x - torch.logsumexp(x, 1, True))
+        total = torch.where(chosen, s, 0.0).sum(1, keepdim=True) if case["renorm"] else 1.0
+        w = torch.gather(s / total, 1, index) * case["factor"]
+        out = {"index": None, "weight": w.detach(), "offsets": None, "counts": None, "rows": None, "position": None}
+        if case["backward"]:
+            w.backward(state["weight_grad"].double())
+            out["logits_grad"] = x.grad
+        return out
+    rows = state["plan"]["rows"].long()
+    if op == "combine":
+        k, N, w = case["k"], case["N"], state["weight"].double()
+        token = torch.where(rows >= 0, rows, 0)
+        slot = (state["plan"]["position"].long()[token] == torch.arange(len(rows), device="cuda")[:, None]).int()
+        share = (w[token] * slot).sum(1) * (rows >= 0)  # the weight with which each row counts
+        y = state["y"].double()
+        out = {"out": torch.zeros(case["T"], N, dtype=torch.float64, device="cuda").index_add_(0, token, y * share[:, None])}
+        if case["backward"]:
+            g = state["grad"].double()[token]
+            out["y_grad"] = g * share[:, None]
+            dots = (y * g).sum(1)
+            out["weight_grad"] = dots[state["plan"]["position"].long().reshape(-1)].reshape(case["T"], k)
+        return out
+    ends = state["host"]
+    E = case["E"]
+    if op == "experts":
+        a = torch.where((rows >= 0)[:, None], _numbers(*state["a"], 1)[rows.clamp(min=0)], 0.0)
+        parts = [a[ends[e]:ends[e + 1]] @ _numbers(state["b"][0][e], state["b"][1][e], BLOCK).t().contiguous()
+                 for e in range(E)]
+        return torch.cat(parts + [torch.zeros(len(rows) - ends[E], case["N"], dtype=torch.float64, device="cuda")])
+    a, b = _numbers(*state["a"], 1), _numbers(*state["b"], 1)
+    return torch.stack([a[:, ends[e]:ends[e + 1]] @ b[:, ends[e]:ends[e + 1]].t().contiguous() for e in range(E)])
