@@ -244,8 +244,9 @@ def plain_quantize(x, qtype, block_rows):
     pad[..., :R, :K] = x
     amax = pad.abs().reshape(*lead, rb, block_rows, kb, BLOCK).amax(dim=(-3, -1))
     amax = amax.clamp(min=AMAX_FLOOR)
-    inv = (QMAX[qtype] / amax).repeat_interleave(block_rows, -2)[..., :R, :].repeat_interleave(BLOCK, -1)[..., :K]
-    return (x * inv).to(QTYPES[qtype]), amax / QMAX[qtype]
+    top = torch.full_like(amax, QMAX[qtype])  # a tensor: one rounded division, not a product with a reciprocal
+    inv = (top / amax).repeat_interleave(block_rows, -2)[..., :R, :].repeat_interleave(BLOCK, -1)[..., :K]
+    return (x * inv).to(QTYPES[qtype]), amax / top
 
 
 def values(q, s, block_rows):
