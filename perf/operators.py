@@ -423,13 +423,20 @@ def _numbers(q, s, block_rows):
     return q.double() * _spread(s, q.shape[-2], q.shape[-1], block_rows)
 
 
+def _grid(v, qtype):
+    """v to the nearest number of the 8-bit type, ties to the even one (none lies past its largest)."""
+    bits, lowest = {"e4m3": (3, -6), "e5m2": (2, -14)}[qtype]
+    step = torch.ldexp(torch.ones_like(v), (torch.frexp(v).exponent - 1).clamp(min=lowest) - bits)
+    return torch.round(v / step) * step
+
+
 def _exact_codes(x, qtype, block_rows):
-    """Before its rounding, what a code stands for; and the scale."""
+    """What the codes stand for without their scale; and the scale."""
     R, K = x.shape
     top = torch.nn.functional.pad(x.abs(), (0, -K % BLOCK, 0, -R % block_rows))
     top = top.unfold(0, block_rows, block_rows).unfold(1, BLOCK, BLOCK).flatten(2).max(2).values
     s = torch.maximum(top, torch.full_like(top, AMAX_FLOOR)) / QMAX[qtype]
-    return x / _spread(s, R, K, block_rows), s
+    return _grid(x / _spread(s, R, K, block_rows), qtype), s
 
 
 def exact(case, seed):
