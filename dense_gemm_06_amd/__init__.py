@@ -7,6 +7,9 @@ gemm_last_error) and only marshal arguments: every step of the product runs in
 the library's HIP kernels. A nonzero status raises
 GemmError carrying the library's own description.
 
+The block-scaled 8-bit products and the experts' operators of include/gemm_experts.h are
+in experts.py, whose names are here too (gemm_block_*, gemm_experts_*).
+
 ``gemm_tensors`` is a convenience for torch tensors: it reads pointers, leading
 dimensions and the current stream off the tensors and calls gemm_ex. Torch
 provides device memory and streams only.
@@ -172,6 +175,7 @@ def _load():
     lib.gemm_status_string.restype = ctypes.c_char_p
     lib.gemm_last_error.argtypes = []
     lib.gemm_last_error.restype = ctypes.c_char_p
+    _experts.declare(lib)
     _lib = lib
     return lib
 
@@ -363,3 +367,13 @@ def gemm_tensors(A, B, C, op_b: str = "N", cfg: gemm_config | None = None, strea
     s = stream if stream is not None else torch.cuda.current_stream(A.device).cuda_stream
     return gemm_ex(GEMM_OP_N, OP_CODE[op_b], M, N, K, A.data_ptr(), max(A.stride(0), 1), B.data_ptr(),
                    max(B.stride(0), 1), C.data_ptr(), max(C.stride(0), 1), _torch_dtype_code(A), cfg, s)
+
+
+# ----------------------------------------------------------------------------- block-scaled products and experts
+from . import experts as _experts  # noqa: E402  (uses the names above)
+from .experts import (  # noqa: E402,F401
+    BLOCK, GEMM_E4M3, GEMM_E5M2, GEMM_SCORE_SIGMOID, GEMM_SCORE_SOFTMAX, SCORE_CODE, BlockTensor, ExpertPlan,
+    gemm_block_matrix, gemm_block_product_tensors, gemm_block_quantize_tensors, gemm_expert_plan,
+    gemm_experts_combine_backward_tensors, gemm_experts_combine_tensors, gemm_experts_dispatch_tensors,
+    gemm_experts_gradient_tensors, gemm_experts_product_tensors, gemm_experts_route_backward_tensors,
+    gemm_experts_route_tensors, gemm_router, router)

@@ -26,8 +26,9 @@ ARCH = "gfx950"
 
 DEVICE_SOURCES = ["inst_lds_f32.hip", "inst_lds_f16.hip", "inst_lds_bf16.hip",
                   "inst_mfma_f32.hip", "inst_mfma_f16.hip", "inst_mfma_bf16.hip", "reduce.hip", "pack.hip",
-                  "noalloc.hip"]
-HOST_SOURCES = ["plan.cpp", "gemm_api.cpp"]
+                  "noalloc.hip", "inst_block_e4m3_e4m3.hip", "inst_block_e4m3_e5m2.hip", "inst_block_e5m2_e4m3.hip",
+                  "inst_block_e5m2_e5m2.hip", "block_quantize.hip", "route.hip", "combine.hip"]
+HOST_SOURCES = ["plan.cpp", "gemm_api.cpp", "block_api.cpp"]
 
 COMMON = ["-O3", "-fPIC", "-std=c++17", "-Wall", "-Wno-unused-function"]
 # Loops start on a 64-byte boundary: the fp32 256 x 128 direct-copy kernel with

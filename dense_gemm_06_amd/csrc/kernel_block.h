@@ -1,0 +1,571 @@
+// kernel_block.h -- products of block-scaled 8-bit matrices, for gfx950.
+//
+//   C[m][n] = sum_b SA(m,b) SB(n,b) sum_{k in block b} a(m,k) b(n,k)
+//
+// with blocks of 128 k. The inner sums run on the matrix cores from a zero accumulator;
+// each block's sum is then multiplied by both scales and added in fp32, since the scales
+// are arbitrary fp32 numbers and the 8-bit instruction's own scales are powers of two.
+//
+// FULL = false, for C of 16 bits: v_mfma_f32_*_f8f6f4 on the codes. Measured on gfx950 (one
+// large and one small product at every distance, and sums of small ones): the products of
+// 8 neighbouring k are cut, towards zero, to whole multiples of 2^-13 of the power of two
+// under the largest before they are added; sums over those groups are fp32. That is at
+// most 7 * 2^-13 of a group's largest product, on random data 1.4e-5 to 4e-5 of the result
+// (2-norm), against 1e-4 (fp16) and 1.1e-3 (bf16) for C's own rounding: fine there, at twice
+// the rate of 16-bit instructions.
+// FULL = true, for fp32 C, where that would be 100 times the type's step: the codes become
+// fp16 (exactly: e5m2 is fp16's upper byte, e4m3 a subset) in registers, and
+// v_mfma_f32_*_f16 has exact products and fp32 sums.
+//
+// The rows of
+// B are the instruction's first operand, so a lane holds one row m of C and four
+// consecutive n per accumulator quad: SA is one value per lane and subtile, and with
+// 128 x 128 blocks of B the scale is one product per subtile and block.
+//
+// The order of k inside a fragment is free as long as both operands share it: the lanes
+// with the same row take 16-byte chunks in whichever order is cheapest to read.
+#pragma once
+#include "device_common.h"
+#include "experts.h"
+#include "lds_layout.h"
+
+#define DG_LDS_ADDR(a) ((__attribute__((address_space(3))) void*)(uintptr_t)(uint32_t)(a))
+
+namespace dg {
+
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+
+// Source of the chunks that lie past the end of a row.
+__device__ const uint32_t block_zeros[4] = {0, 0, 0, 0};
+
+// first operand rows -> D rows (registers), second -> D columns (lanes)
+template <int T1, int T2>
+__device__ __forceinline__ f32x16 mfma_32(i32x8 x, i32x8 y, f32x16 c) {
+    return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(x, y, c, T1, T2, 0, 0, 0, 0);
+}
+template <int T1, int T2>
+__device__ __forceinline__ f32x4 mfma_16(i32x8 x, i32x8 y, f32x4 c) {
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(x, y, c, T1, T2, 0, 0, 0, 0);
+}
+
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+
+// Eight codes as eight fp16 numbers.
+template <int T>
+__device__ __forceinline__ f16x8 widen8(int lo, int hi) {
+    uint32_t w[4];
+    if constexpr (T == 0) {
+        w[0] = __builtin_bit_cast(uint32_t, (f16x2)__builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, 1.0f, false));
+        w[1] = __builtin_bit_cast(uint32_t, (f16x2)__builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, 1.0f, true));
+        w[2] = __builtin_bit_cast(uint32_t, (f16x2)__builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, 1.0f, false));
+        w[3] = __builtin_bit_cast(uint32_t, (f16x2)__builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, 1.0f, true));
+    } else {  // each code becomes the upper byte of a half (selector 12: zero)
+        w[0] = __builtin_amdgcn_perm(0u, (uint32_t)lo, 0x010c000cu);
+        w[1] = __builtin_amdgcn_perm(0u, (uint32_t)lo, 0x030c020cu);
+        w[2] = __builtin_amdgcn_perm(0u, (uint32_t)hi, 0x010c000cu);
+        w[3] = __builtin_amdgcn_perm(0u, (uint32_t)hi, 0x030c020cu);
+    }
+    return __builtin_bit_cast(f16x8, u32x4{w[0], w[1], w[2], w[3]});
+}
+
+// One workgroup's piece of a product: rows m0 .. m_end-1 of C (in whole tiles of BM),
+// columns from n0, blocks kb0 .. kb0+nkb-1 of k, the last one holding krem elements.
+struct BlockTile {
+    int m0, m_end, n0;
+    int m_live;          // experts: rows from here on are padding
+    int expert;
+    int kb0, nkb, krem;
+    bool bad;            // gradient: rows that start inside a block or end inside 16
+};
+
+// Offsets of expert e, kept inside 0 .. P whatever the array holds.
+__device__ __forceinline__ void expert_range(const int* offsets, int e, int P, int& lo, int& hi) {
+    lo = min(max(offsets[e], 0), P);
+    hi = min(max(offsets[e + 1], lo), P);
+}
+
+// Linear tile of this workgroup among `total`, each XCD (hardware id mod 8) taking a
+// contiguous run; -1 if none is left for it. The grid holds at least `total` workgroups.
+__device__ __forceinline__ int xcd_tile(int total) {
+    const int bid = (int)blockIdx.x, x = bid & 7, i = bid >> 3;
+    const int q = total >> 3, rem = total & 7;
+    return i < q + (x < rem ? 1 : 0) ? x * q + min(x, rem) + i : -1;
+}
+
+// The expert that owns a tile of BM rows: every wave adds up the experts' tile counts, 64
+// experts at a time. Returns false when the grid has no tile for this workgroup.
+template <int BM>
+__device__ __forceinline__ bool expert_tile(const BlockArgs& g, BlockTile& t) {
+    const int lane = threadIdx.x & 63;
+    int total = 0;
+    for (int e0 = 0; e0 < g.E; e0 += 64) {
+        int lo = 0, hi = 0;
+        if (e0 + lane < g.E) expert_range(g.offsets, e0 + lane, g.M, lo, hi);
+        int n = (hi - lo + BM - 1) / BM;
+#pragma unroll
+        for (int d = 32; d; d >>= 1) n += __shfl_xor(n, d);
+        total += n;
+    }
+    total = __builtin_amdgcn_readfirstlane(total);
+    const int id = xcd_tile(total * g.tiles_n);
+    if (id < 0) return false;
+    const int q = id / g.tiles_n;  // lies in the tiles of the wanted expert, as all of its row tiles have tiles_n columns
+    int before = 0;
+    for (int e0 = 0; e0 < g.E; e0 += 64) {
+        int lo = 0, hi = 0;
+        if (e0 + lane < g.E) expert_range(g.offsets, e0 + lane, g.M, lo, hi);
+        const int n = (hi - lo + BM - 1) / BM;
+        int sum = n;
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) {
+            const int v = __shfl_up(sum, d);
+            if (lane >= d) sum += v;
+        }
+        const unsigned long long hit = __ballot(q < before + sum);
+        if (hit) {
+            const int l = __builtin_ctzll(hit);
+            const int first = __builtin_amdgcn_readlane(before + sum - n, l);
+            const int tiles = __builtin_amdgcn_readlane(n, l);
+            int tm, tn;
+            raster(id - first * g.tiles_n, tiles, g.tiles_n, min(g.group_m, tiles), tm, tn);
+            t.expert = e0 + l;
+            const int base = __builtin_amdgcn_readlane(lo, l);
+            t.m0 = base + tm * BM;
+            t.m_end = __builtin_amdgcn_readlane(hi, l);
+            t.m_live = min(t.m_end, base + max(__builtin_amdgcn_readfirstlane(g.counts[t.expert]), 0));
+            t.n0 = tn;  // in tiles; the caller scales it
+            return true;
+        }
+        before += __builtin_amdgcn_readlane(sum, 63);
+    }
+    return false;
+}
+
+// The tile of this workgroup; false when there is none (the caller still takes part in
+// clearing the rows past the last expert).
+template <int BM, int BN>
+__device__ __forceinline__ bool block_tile_of(BlockArgs& g, BlockTile& t) {
+    t.bad = false;
+    t.expert = 0;
+    t.kb0 = 0;
+    t.nkb = (g.K + kBlock - 1) / kBlock;
+    t.krem = g.K - (t.nkb - 1) * kBlock;
+    t.m_end = g.M;
+    t.m_live = g.M;
+    if (g.mode == BLOCK_EXPERTS) {
+        if (!expert_tile<BM>(g, t)) return false;
+        t.n0 *= BN;
+        g.B += (size_t)t.expert * (size_t)g.stride_b;
+        g.SB += (size_t)t.expert * (size_t)g.stride_sb;
+        return true;
+    }
+    int id = xcd_tile((int)gridDim.x), tm, tn;
+    const int per = g.tiles_m * g.tiles_n;
+    if (g.mode == BLOCK_GRADIENT) {
+        t.expert = id / per;
+        id -= t.expert * per;
+        int lo, hi;
+        expert_range(g.offsets, t.expert, g.K, lo, hi);
+        lo = __builtin_amdgcn_readfirstlane(lo);
+        hi = __builtin_amdgcn_readfirstlane(hi);
+        t.bad = ((lo & (kBlock - 1)) != 0 || (hi & 15) != 0) && hi > lo;  // chunks are 16 bytes
+        t.kb0 = lo / kBlock;
+        t.nkb = t.bad ? 0 : (hi - lo + kBlock - 1) / kBlock;
+        t.krem = hi - lo - (t.nkb - 1) * kBlock;
+        g.C = static_cast<char*>(g.C) + (size_t)t.expert * (size_t)g.stride_c * (g.out_dt == DT_F32 ? 4 : 2);
+    } else if (g.k_split > 1) {
+        t.kb0 = (int)blockIdx.y * g.kb_chunk;
+        const int left = t.nkb - t.kb0;
+        if (left > g.kb_chunk) {
+            t.nkb = g.kb_chunk;
+            t.krem = kBlock;
+        } else {
+            t.nkb = left;
+        }
+        g.C = g.work + (size_t)blockIdx.y * (size_t)g.work_slice;
+        g.ldc = g.work_ld;
+        g.out_dt = DT_F32;
+    }
+    raster(id, g.tiles_m, g.tiles_n, g.group_m, tm, tn);
+    t.m0 = tm * BM;
+    t.n0 = tn * BN;
+    return true;
+}
+
+// Row of A for row m of C, or -1 for a row of zeros.
+__device__ __forceinline__ int block_a_row(const BlockArgs& g, const BlockTile& t, int m) {
+    if (g.mode != BLOCK_EXPERTS) return m < t.m_end ? m : -1;
+    if (m >= t.m_live) return -1;
+    const int r = g.rows ? g.rows[m] : m;
+    return r >= 0 && r < g.a_rows ? r : -1;
+}
+
+// Columns n .. n+3 of row m of C (columns at or past N skipped).
+__device__ __forceinline__ void block_store4(const BlockArgs& g, int m, int n, f32x4 v) {
+    const size_t at = (size_t)m * (size_t)g.ldc + n;
+    if (n + 4 <= g.N) {
+        store_out4(g.C, g.out_dt, at, v);
+        return;
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+        if (n + e < g.N) store_out(g.C, g.out_dt, at + e, v[e]);
+}
+
+// Zeros in the rows past the last expert's, spread over the whole grid.
+__device__ __forceinline__ void clear_tail(const BlockArgs& g) {
+    const int first = min(max(g.offsets[g.E], 0), g.M);
+    for (int m = first + (int)blockIdx.x; m < g.M; m += (int)gridDim.x)
+        for (int n = (int)threadIdx.x * 4; n < g.N; n += (int)blockDim.x * 4) block_store4(g, m, n, f32x4{0, 0, 0, 0});
+}
+
+// 16 bytes of a row from p, of which the first `valid` lie inside it.
+__device__ __forceinline__ u32x4 load_codes(const uint8_t* p, int valid) {
+    u32x4 v = {0, 0, 0, 0};
+    if (valid >= 16) {
+        __builtin_memcpy(&v, p, 16);
+    } else if (valid > 0) {
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+            uint32_t x = 0;
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (w * 4 + e < valid) x |= (uint32_t)p[w * 4 + e] << (8 * e);
+            v[w] = x;
+        }
+    }
+    return v;
+}
+
+// ---------------------------------------------------------------------------- tiles
+// BM x BN tiles on WM x WN waves, each wave SM x SJ subtiles of 32 x 32. LDS holds two
+// stages of one block of k: rows of 128 bytes whose 16-byte chunks are permuted by
+// (row >> 1) & 7, so that the 16 rows of any phase of a fragment read spread over all 64
+// banks, and the block's scales. DIRECT: the copies go from global memory straight to
+// LDS; otherwise (rows at any byte address) through registers.
+template <int TA, int TB, bool FULL, bool BROW, int BM, int BN, int WM, int WN, bool DIRECT>
+__global__ __launch_bounds__(WM* WN * 64) void block_tile(BlockArgs g) {
+    constexpr int NW = WM * WN, SM = BM / 32 / WM, SJ = BN / 32 / WN;
+    constexpr int CA = BM / 8 / NW, CB = BN / 8 / NW;  // 1 KB copies (8 rows) per wave
+    static_assert((BM + BN) / 64 == NW, "each wave copies 64 scales of a stage");
+    __shared__ __attribute__((aligned(1024))) uint8_t sA[2][BM * kBlock];
+    __shared__ __attribute__((aligned(1024))) uint8_t sB[2][BN * kBlock];
+    __shared__ __attribute__((aligned(1024))) float fS[2][BM + BN];
+
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wm = wave / WN, wn = wave % WN;
+    const int l32 = lane & 31, lh = lane >> 5;
+
+    BlockTile t;
+    const bool any = block_tile_of<BM, BN>(g, t);
+    if (g.mode == BLOCK_EXPERTS) clear_tail(g);
+    if (!any) return;
+    if (t.m0 >= t.m_live) t.nkb = 0;  // nothing but padding: zeros
+
+    // ---- sources of this lane's copies
+    const uint8_t* pa[CA];
+    const uint8_t* pb[CB];
+    int ka[CA], kc[CB];
+#pragma unroll
+    for (int i = 0; i < CA; ++i) {
+        const int row = (wave * CA + i) * 8 + (lane >> 3);
+        ka[i] = ((lane & 7) ^ ((row >> 1) & 7)) * 16;
+        const int r = max(block_a_row(g, t, min(t.m0 + row, t.m_end - 1)), 0);
+        pa[i] = g.A + (size_t)r * (size_t)g.lda + (size_t)t.kb0 * kBlock + ka[i];
+    }
+#pragma unroll
+    for (int i = 0; i < CB; ++i) {
+        const int row = (wave * CB + i) * 8 + (lane >> 3);
+        kc[i] = ((lane & 7) ^ ((row >> 1) & 7)) * 16;
+        pb[i] = g.B + (size_t)min(t.n0 + row, g.N - 1) * (size_t)g.ldb + (size_t)t.kb0 * kBlock + kc[i];
+    }
+    const float* ps;
+    int64_t ps_step;
+    if (wave < BM / 64) {
+        const int r = max(block_a_row(g, t, min(t.m0 + wave * 64 + lane, t.m_end - 1)), 0);
+        ps = g.SA + (size_t)(r >> g.a_shift) * (size_t)g.sa_row + (size_t)t.kb0 * (size_t)g.sa_blk;
+        ps_step = g.sa_blk;
+    } else {
+        const int n = min(t.n0 + (wave - BM / 64) * 64 + lane, g.N - 1);
+        ps = g.SB + (size_t)(n >> g.b_shift) * (size_t)g.sb_row + (size_t)t.kb0 * (size_t)g.sb_blk;
+        ps_step = g.sb_blk;
+    }
+    // LDS destinations as plain numbers: the compiler then does not make every LDS read
+    // wait for all copies in flight; the explicit waits below order them.
+    const uint32_t dA = (uint32_t)reinterpret_cast<uintptr_t>(DG_LDSV(&sA[0][0])) + (uint32_t)wave * (CA * 1024u);
+    const uint32_t dB = (uint32_t)reinterpret_cast<uintptr_t>(DG_LDSV(&sB[0][0])) + (uint32_t)wave * (CB * 1024u);
+    const uint32_t dS = (uint32_t)reinterpret_cast<uintptr_t>(DG_LDSV(&fS[0][0])) + (uint32_t)wave * 256u;
+
+    u32x4 ra[DIRECT ? 1 : CA], rb[DIRECT ? 1 : CB];
+    auto issue = [&](int kb) {
+        const uint32_t st = (uint32_t)(kb & 1);
+        const int rem = kb == t.nkb - 1 ? t.krem : kBlock;
+        __builtin_amdgcn_global_load_lds(DG_GLB(ps + (size_t)kb * (size_t)ps_step), DG_LDS_ADDR(dS + st * ((BM + BN) * 4u)), 4, 0, 0);
+        if constexpr (DIRECT) {
+#pragma unroll
+            for (int i = 0; i < CA; ++i) {
+                const void* src = pa[i] + (size_t)kb * kBlock;
+                if (ka[i] >= rem) src = block_zeros;
+                __builtin_amdgcn_global_load_lds(DG_GLB(src), DG_LDS_ADDR(dA + st * (BM * kBlock) + i * 1024u), 16, 0, 0);
+            }
+#pragma unroll
+            for (int i = 0; i < CB; ++i) {
+                const void* src = pb[i] + (size_t)kb * kBlock;
+                if (kc[i] >= rem) src = block_zeros;
+                __builtin_amdgcn_global_load_lds(DG_GLB(src), DG_LDS_ADDR(dB + st * (BN * kBlock) + i * 1024u), 16, 0, 0);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < CA; ++i) ra[i] = load_codes(pa[i] + (size_t)kb * kBlock, rem - ka[i]);
+#pragma unroll
+            for (int i = 0; i < CB; ++i) rb[i] = load_codes(pb[i] + (size_t)kb * kBlock, rem - kc[i]);
+        }
+    };
+    auto settle = [&](int kb) {  // registers to LDS
+        if constexpr (!DIRECT) {
+            uint8_t* a = &sA[kb & 1][wave * (CA * 1024) + lane * 16];
+            uint8_t* b = &sB[kb & 1][wave * (CB * 1024) + lane * 16];
+#pragma unroll
+            for (int i = 0; i < CA; ++i) *reinterpret_cast<u32x4*>(a + i * 1024) = ra[i];
+#pragma unroll
+            for (int i = 0; i < CB; ++i) *reinterpret_cast<u32x4*>(b + i * 1024) = rb[i];
+        }
+    };
+
+    // ---- fragments: lane (l32, lh) takes chunks 4h + 2lh and 4h + 2lh + 1 of its row
+    int off[2][2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int u = 0; u < 2; ++u) off[h][u] = l32 * kBlock + (((4 * h + 2 * lh + u) ^ ((l32 >> 1) & 7)) << 4);
+    auto frag = [&](const uint8_t* base, int h) {
+        const u32x4 x = *reinterpret_cast<const u32x4*>(base + off[h][0]);
+        const u32x4 y = *reinterpret_cast<const u32x4*>(base + off[h][1]);
+        return i32x8{(int)x[0], (int)x[1], (int)x[2], (int)x[3], (int)y[0], (int)y[1], (int)y[2], (int)y[3]};
+    };
+
+    f32x16 acc[SM][SJ];
+#pragma unroll
+    for (int i = 0; i < SM; ++i)
+#pragma unroll
+        for (int j = 0; j < SJ; ++j) acc[i][j] = f32x16{0};
+
+    if (t.nkb > 0) {
+        issue(0);
+        settle(0);
+    }
+    for (int kb = 0; kb < t.nkb; ++kb) {
+        const int st = kb & 1;
+        // this wave's copies of block kb have landed, and after the barrier everybody's;
+        // everybody has also read the stage that the next copies overwrite
+        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+        if (kb + 1 < t.nkb) issue(kb + 1);
+        const uint8_t* a0 = &sA[st][wm * SM * 32 * kBlock];
+        const uint8_t* b0 = &sB[st][wn * SJ * 32 * kBlock];
+        const float* fa = &fS[st][wm * SM * 32 + l32];
+        const float* fb = &fS[st][BM + wn * SJ * 32];
+        f32x4 sb[SJ][BROW ? 4 : 1];
+#pragma unroll
+        for (int j = 0; j < SJ; ++j) {
+            if constexpr (BROW) {
+#pragma unroll
+                for (int q = 0; q < 4; ++q) sb[j][q] = *reinterpret_cast<const f32x4*>(fb + j * 32 + q * 8 + lh * 4);
+            } else {
+                sb[j][0][0] = fb[j * 32];
+            }
+        }
+        auto add = [&](int i, int j, const f32x16& part) {
+            const float sa = fa[i * 32];
+            if constexpr (BROW) {
+#pragma unroll
+                for (int r = 0; r < 16; ++r) acc[i][j][r] = fmaf(part[r], sa * sb[j][r >> 2][r & 3], acc[i][j][r]);
+            } else {
+                const float s = sa * sb[j][0][0];
+#pragma unroll
+                for (int r = 0; r < 16; ++r) acc[i][j][r] = fmaf(part[r], s, acc[i][j][r]);
+            }
+        };
+        if constexpr (!FULL) {
+            i32x8 bf[SJ][2];
+#pragma unroll
+            for (int j = 0; j < SJ; ++j)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) bf[j][h] = frag(b0 + j * 32 * kBlock, h);
+#pragma unroll
+            for (int i = 0; i < SM; ++i) {
+                const i32x8 af0 = frag(a0 + i * 32 * kBlock, 0), af1 = frag(a0 + i * 32 * kBlock, 1);
+#pragma unroll
+                for (int j = 0; j < SJ; ++j)
+                    add(i, j, mfma_32<TB, TA>(bf[j][1], af1, mfma_32<TB, TA>(bf[j][0], af0, f32x16{0})));
+            }
+        } else {
+            f32x16 part[SM][SJ];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                i32x8 af[SM], bf[SJ];
+#pragma unroll
+                for (int i = 0; i < SM; ++i) af[i] = frag(a0 + i * 32 * kBlock, h);
+#pragma unroll
+                for (int j = 0; j < SJ; ++j) bf[j] = frag(b0 + j * 32 * kBlock, h);
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    f16x8 aw[SM], bw[SJ];
+#pragma unroll
+                    for (int i = 0; i < SM; ++i) aw[i] = widen8<TA>(af[i][2 * u], af[i][2 * u + 1]);
+#pragma unroll
+                    for (int j = 0; j < SJ; ++j) bw[j] = widen8<TB>(bf[j][2 * u], bf[j][2 * u + 1]);
+#pragma unroll
+                    for (int i = 0; i < SM; ++i)
+#pragma unroll
+                        for (int j = 0; j < SJ; ++j)
+                            part[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(
+                                bw[j], aw[i], h == 0 && u == 0 ? f32x16{0} : part[i][j], 0, 0, 0);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < SM; ++i)
+#pragma unroll
+                for (int j = 0; j < SJ; ++j) add(i, j, part[i][j]);
+        }
+        if (kb + 1 < t.nkb) settle(kb + 1);
+    }
+
+    // ---- C: lane l32 holds row m, register quad q the columns 8q + 4lh .. +3
+#pragma unroll
+    for (int i = 0; i < SM; ++i) {
+        const int m = t.m0 + (wm * SM + i) * 32 + l32;
+        if (m >= t.m_end) continue;
+        const bool zero = block_a_row(g, t, m) < 0;
+#pragma unroll
+        for (int j = 0; j < SJ; ++j)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const int n = t.n0 + (wn * SJ + j) * 32 + q * 8 + lh * 4;
+                f32x4 v;
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    v[e] = t.bad ? __builtin_nanf("") : zero ? 0.0f : acc[i][j][q * 4 + e];
+                if (n < g.N) block_store4(g, m, n, v);
+            }
+    }
+}
+
+// ---------------------------------------------------------------------------- few rows
+// At most 16 * SM rows of A: the time is that of reading B once. A workgroup takes 16
+// rows of B, its NW waves every NW-th block of k, fragments straight from global memory
+// (a row's 128 bytes from four lanes); the waves' sums meet in LDS and are added in the
+// waves' order.
+template <int TA, int TB, bool FULL, int SM, bool DIRECT>
+__global__ __launch_bounds__(512) void block_skinny(BlockArgs g) {
+    constexpr int NW = 8, BM = 16 * SM, BN = 16;
+    __shared__ f32x4 sums[NW][SM][64];
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int l16 = lane & 15, lg = lane >> 4;
+    BlockTile t;
+    const bool any = block_tile_of<BM, BN>(g, t);
+    if (g.mode == BLOCK_EXPERTS) clear_tail(g);
+    if (!any) return;
+    if (t.m0 >= t.m_live) t.nkb = 0;
+
+    const uint8_t* pa[SM];
+    const float* fa[SM];
+    const size_t k0 = (size_t)t.kb0 * kBlock;
+#pragma unroll
+    for (int i = 0; i < SM; ++i) {
+        const int r = max(block_a_row(g, t, min(t.m0 + i * 16 + l16, t.m_end - 1)), 0);
+        pa[i] = g.A + (size_t)r * (size_t)g.lda + k0 + lg * 32;
+        fa[i] = g.SA + (size_t)(r >> g.a_shift) * (size_t)g.sa_row + (size_t)t.kb0 * (size_t)g.sa_blk;
+    }
+    const uint8_t* pb = g.B + (size_t)min(t.n0 + l16, g.N - 1) * (size_t)g.ldb + k0 + lg * 32;
+    const float* fb[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const int n = min(t.n0 + lg * 4 + e, g.N - 1);
+        fb[e] = g.SB + (size_t)(n >> g.b_shift) * (size_t)g.sb_row + (size_t)t.kb0 * (size_t)g.sb_blk;
+    }
+    auto frag = [&](const uint8_t* p, int rem) {
+        u32x4 x, y;
+        if constexpr (DIRECT) {
+            const uint8_t* z = reinterpret_cast<const uint8_t*>(block_zeros);
+            x = *reinterpret_cast<const u32x4*>(rem > 0 ? p : z);
+            y = *reinterpret_cast<const u32x4*>(rem > 16 ? p + 16 : z);
+        } else {
+            x = load_codes(p, rem);
+            y = load_codes(p + 16, rem - 16);
+        }
+        return i32x8{(int)x[0], (int)x[1], (int)x[2], (int)x[3], (int)y[0], (int)y[1], (int)y[2], (int)y[3]};
+    };
+    f32x4 acc[SM];
+#pragma unroll
+    for (int i = 0; i < SM; ++i) acc[i] = f32x4{0, 0, 0, 0};
+#pragma unroll(DIRECT ? 4 : 1)
+    for (int kb = wave; kb < t.nkb; kb += NW) {
+        const int rem = (kb == t.nkb - 1 ? t.krem : kBlock) - lg * 32;
+        const i32x8 bf = frag(pb + (size_t)kb * kBlock, rem);
+        f32x4 sb;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sb[e] = fb[e][(size_t)kb * (size_t)g.sb_blk];
+#pragma unroll
+        for (int i = 0; i < SM; ++i) {
+            const i32x8 af = frag(pa[i] + (size_t)kb * kBlock, rem);
+            const float sa = fa[i][(size_t)kb * (size_t)g.sa_blk];
+            f32x4 part = {0, 0, 0, 0};
+            if constexpr (FULL) {
+#pragma unroll
+                for (int u = 0; u < 4; ++u)
+                    part = __builtin_amdgcn_mfma_f32_16x16x32_f16(widen8<TB>(bf[2 * u], bf[2 * u + 1]),
+                                                                  widen8<TA>(af[2 * u], af[2 * u + 1]), part, 0, 0, 0);
+            } else {
+                part = mfma_16<TB, TA>(bf, af, part);
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[i][e] = fmaf(part[e], sa * sb[e], acc[i][e]);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < SM; ++i) sums[wave][i][lane] = acc[i];
+    __syncthreads();
+    if (wave >= SM) return;
+    f32x4 v = sums[0][wave][lane];
+#pragma unroll
+    for (int w = 1; w < NW; ++w) v += sums[w][wave][lane];
+    const int m = t.m0 + wave * 16 + l16, n = t.n0 + lg * 4;
+    if (m >= t.m_end || n >= g.N) return;
+    if (t.bad) v = f32x4{1, 1, 1, 1} * __builtin_nanf("");
+    else if (block_a_row(g, t, m) < 0) v = f32x4{0, 0, 0, 0};
+    block_store4(g, m, n, v);
+}
+
+template <int TA, int TB, bool FULL>
+int launch_block_full(const BlockPlan& p, const BlockArgs& a, dim3 grid, hipStream_t s) {
+    const bool brow = a.b_shift == 0;
+    if constexpr (!FULL)
+        if (p.kernel == BLOCK_TILE256)
+            return launch_status(block_tile<TA, TB, FULL, false, 256, 256, 2, 4, true>, grid, dim3(512), s, a);
+    if (p.kernel == BLOCK_TILE128) {
+        if (p.direct)
+            return brow ? launch_status(block_tile<TA, TB, FULL, true, 128, 128, 2, 2, true>, grid, dim3(256), s, a)
+                        : launch_status(block_tile<TA, TB, FULL, false, 128, 128, 2, 2, true>, grid, dim3(256), s, a);
+        return brow ? launch_status(block_tile<TA, TB, FULL, true, 128, 128, 2, 2, false>, grid, dim3(256), s, a)
+                    : launch_status(block_tile<TA, TB, FULL, false, 128, 128, 2, 2, false>, grid, dim3(256), s, a);
+    }
+    if (p.direct)
+        return p.bm == 16   ? launch_status(block_skinny<TA, TB, FULL, 1, true>, grid, dim3(512), s, a)
+               : p.bm == 32 ? launch_status(block_skinny<TA, TB, FULL, 2, true>, grid, dim3(512), s, a)
+                            : launch_status(block_skinny<TA, TB, FULL, 4, true>, grid, dim3(512), s, a);
+    return p.bm == 16   ? launch_status(block_skinny<TA, TB, FULL, 1, false>, grid, dim3(512), s, a)
+           : p.bm == 32 ? launch_status(block_skinny<TA, TB, FULL, 2, false>, grid, dim3(512), s, a)
+                        : launch_status(block_skinny<TA, TB, FULL, 4, false>, grid, dim3(512), s, a);
+}
+
+template <int TA, int TB>
+int launch_block(const BlockPlan& p, const BlockArgs& a, dim3 grid, hipStream_t s) {
+    return a.out_dt == DT_F32 ? launch_block_full<TA, TB, true>(p, a, grid, s)
+                              : launch_block_full<TA, TB, false>(p, a, grid, s);
+}
+
+}  // namespace dg

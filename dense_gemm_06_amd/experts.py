@@ -1,0 +1,389 @@
+"""Block-scaled 8-bit products, and the experts built on them, for torch tensors.
+
+The functions mirror include/gemm_experts.h: they check the tensors, allocate the results
+and pass pointers, strides and the current stream on; every step runs in the library's HIP
+kernels. Results belong to the current stream of the tensors' device, and the calls can be
+captured into a graph.
+
+  gemm_block_quantize_tensors           values -> codes with block scales, as they are and transposed
+  gemm_block_product_tensors            C = A B^T for block-scaled A and B
+  gemm_experts_route_tensors            scores, choice of experts and their weights
+  gemm_experts_route_backward_tensors   the logits' gradient
+  gemm_experts_dispatch_tensors         the plan: every expert's rows
+  gemm_experts_product_tensors          every row's product with its expert's matrix
+  gemm_experts_gradient_tensors         that product's weight gradients
+  gemm_experts_combine_tensors          the weighted sum of each token's rows
+  gemm_experts_combine_backward_tensors its gradients
+
+Tensors need unit stride along their last dimension; other strides are free.
+"""
+from __future__ import annotations
+
+import ctypes
+
+import dense_gemm_06_amd as _dg
+
+GEMM_E4M3, GEMM_E5M2 = 3, 4
+GEMM_SCORE_SOFTMAX, GEMM_SCORE_SIGMOID = 0, 1
+SCORE_CODE = {"softmax": GEMM_SCORE_SOFTMAX, "sigmoid": GEMM_SCORE_SIGMOID}
+BLOCK = 128
+
+_i64, _i32, _vp, _f = ctypes.c_int64, ctypes.c_int32, ctypes.c_void_p, ctypes.c_float
+
+
+class gemm_block_matrix(ctypes.Structure):
+    """Codes and block scales of a matrix, or of a batch of them (see include/gemm_experts.h)."""
+    _fields_ = [("data", _vp), ("scale", _vp), ("rows", _i64), ("cols", _i64), ("ld", _i64), ("scale_row", _i64),
+                ("scale_block", _i64), ("stride", _i64), ("scale_stride", _i64), ("dtype", _i32),
+                ("block_rows", _i32)]
+
+
+class gemm_router(ctypes.Structure):
+    """How experts are chosen (see include/gemm_experts.h)."""
+    _fields_ = [("top_k", _i32), ("score", _i32), ("groups", _i32), ("top_groups", _i32), ("group_top", _i32),
+                ("renorm", _i32), ("factor", _f)]
+
+
+class gemm_expert_plan(ctypes.Structure):
+    """The arrays of a plan (see include/gemm_experts.h)."""
+    _fields_ = [("offsets", _vp), ("counts", _vp), ("rows", _vp), ("position", _vp), ("experts", _i64),
+                ("tokens", _i64), ("top_k", _i64), ("capacity", _i64)]
+
+
+def router(top_k, score="softmax", groups=1, top_groups=1, group_top=1, renorm=False, factor=1.0) -> gemm_router:
+    return gemm_router(top_k, SCORE_CODE[score] if isinstance(score, str) else score, groups, top_groups, group_top,
+                       int(renorm), factor)
+
+
+def declare(lib):
+    """The argument types of include/gemm_experts.h's functions."""
+    c_int = ctypes.c_int
+    mat, rt, pl = ctypes.POINTER(gemm_block_matrix), ctypes.POINTER(gemm_router), ctypes.POINTER(gemm_expert_plan)
+    for name, args, res in (
+            ("gemm_block_quantize", [_vp, _i64, _i64, _i64, c_int, _vp, _i64, mat, mat, _vp], c_int),
+            ("gemm_block_product", [mat, mat, _vp, _i64, c_int, _vp, _i64, _vp], c_int),
+            ("gemm_block_product_workspace", [_i64, _i64, _i64], _i64),
+            ("gemm_experts_route", [_vp, _i64, _i64, _i64, c_int, rt, _vp, _vp, _vp, _vp], c_int),
+            ("gemm_experts_route_backward", [_vp, _i64, _i64, _i64, c_int, rt, _vp, _vp, _vp, _i64, _vp], c_int),
+            ("gemm_experts_capacity", [_i64, _i64, _i64, _i64], _i64),
+            ("gemm_experts_dispatch", [_vp, _i64, pl, _vp, _i64, _vp], c_int),
+            ("gemm_experts_dispatch_workspace", [_i64, _i64, _i64], _i64),
+            ("gemm_experts_product", [mat, mat, pl, c_int, _vp, _i64, c_int, _vp], c_int),
+            ("gemm_experts_gradient", [mat, mat, pl, _vp, _i64, _i64, c_int, _vp], c_int),
+            ("gemm_experts_combine", [_vp, _i64, _i64, c_int, pl, _vp, _vp, _i64, _vp], c_int),
+            ("gemm_experts_combine_backward", [_vp, _i64, _i64, c_int, pl, _vp, _vp, _i64, _vp, _i64, _vp, _vp],
+             c_int)):
+        fn = getattr(lib, name)
+        fn.argtypes, fn.restype = args, res
+
+
+class BlockTensor:
+    """Codes and scales: data (..., R, K) float8_e4m3fn or float8_e5m2; scale (..., ceil(R / block_rows),
+    ceil(K / 128)) float32, the number at (i, k) being data[i, k] * scale[i // block_rows, k // 128]."""
+    __slots__ = ("data", "scale", "block_rows")
+
+    def __init__(self, data, scale, block_rows=1):
+        self.data, self.scale, self.block_rows = data, scale, block_rows
+
+
+class ExpertPlan:
+    """offsets (E + 1), counts (E), rows (P) and position (T, k), all int32 (see include/gemm_experts.h)."""
+    __slots__ = ("offsets", "counts", "rows", "position", "align")
+
+    def __init__(self, offsets, counts, rows, position, align=None):
+        self.offsets, self.counts, self.rows, self.position, self.align = offsets, counts, rows, position, align
+
+
+# ----------------------------------------------------------------------------- checks
+def _torch():
+    import torch
+    return torch
+
+
+def _code_type(dtype, what):
+    torch = _torch()
+    if dtype == torch.float8_e4m3fn:
+        return GEMM_E4M3
+    if dtype == torch.float8_e5m2:
+        return GEMM_E5M2
+    raise TypeError(f"{what}: {dtype} is not float8_e4m3fn or float8_e5m2")
+
+
+def _wide_type(dtype, what):
+    torch = _torch()
+    if dtype == torch.bfloat16:
+        return _dg.GEMM_BF16
+    if dtype == torch.float32:
+        return _dg.GEMM_F32
+    if dtype == torch.float16:
+        return _dg.GEMM_F16
+    raise TypeError(f"{what}: {dtype} is not float32, float16 or bfloat16")
+
+
+def _matrix(t, what, dims=2):
+    """Leading dimension of t, whose rows have to be contiguous."""
+    if t.dim() != dims:
+        raise ValueError(f"{what} must be {dims}-D, not {tuple(t.shape)}")
+    cols = t.shape[-1]
+    if t.stride(-1) != 1 and cols > 1:
+        raise ValueError(f"{what} needs unit stride along its last dimension, not {t.stride()}")
+    if t.shape[-2] > 1 and t.stride(-2) < cols:
+        raise ValueError(f"{what}: rows overlap (strides {t.stride()})")
+    return max(t.stride(-2), cols, 1) if t.shape[-2] > 1 else max(cols, 1)
+
+
+def _array(t, what, dtype, shape):
+    if t.dtype != dtype:
+        raise TypeError(f"{what} must be {dtype}, not {t.dtype}")
+    if tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise ValueError(f"{what} must be contiguous of shape {tuple(shape)}, not {tuple(t.shape)} with strides {t.stride()}")
+    return t.data_ptr()
+
+
+def _device(*tensors):
+    """The tensors' common GPU."""
+    dev = tensors[0].device
+    for t in tensors:
+        if not t.is_cuda or t.device != dev:
+            raise ValueError(f"tensors must be on one GPU, not {', '.join(str(t.device) for t in tensors)}")
+    return dev
+
+
+def _block(b, what, batch=False):
+    """A BlockTensor as the library takes it."""
+    if not isinstance(b, BlockTensor):
+        raise TypeError(f"{what} must be a BlockTensor, not {type(b).__name__}")
+    data, scale, rows = b.data, b.scale, b.block_rows
+    dims = 3 if batch else 2
+    ld = _matrix(data, f"{what}.data", dims)
+    code = _code_type(data.dtype, f"{what}.data")
+    if rows not in (1, BLOCK):
+        raise ValueError(f"{what}.block_rows must be 1 or {BLOCK}, not {rows}")
+    R, K = data.shape[-2:]
+    want = (*data.shape[:-2], -(-R // rows), -(-K // BLOCK))
+    if scale.dtype != _torch().float32:
+        raise TypeError(f"{what}.scale must be float32, not {scale.dtype}")
+    if tuple(scale.shape) != want:
+        raise ValueError(f"{what}.scale must have shape {want}, not {tuple(scale.shape)}")
+    strides = scale.stride()
+    return gemm_block_matrix(data.data_ptr(), scale.data_ptr(), R, K, ld, strides[-2], strides[-1],
+                             data.stride(0) if batch else 0, strides[0] if batch else 0, code, rows)
+
+
+def _plan(plan, what="plan"):
+    """An ExpertPlan as the library takes it."""
+    if not isinstance(plan, ExpertPlan):
+        raise TypeError(f"{what} must be an ExpertPlan, not {type(plan).__name__}")
+    i32 = _torch().int32
+    if plan.position.dim() != 2 or plan.counts.dim() != 1 or plan.rows.dim() != 1:
+        raise ValueError(f"{what}: position must be 2-D, counts and rows 1-D")
+    T, k = plan.position.shape
+    E, P = plan.counts.shape[0], plan.rows.shape[0]
+    return gemm_expert_plan(_array(plan.offsets, f"{what}.offsets", i32, (E + 1,)),
+                            _array(plan.counts, f"{what}.counts", i32, (E,)),
+                            _array(plan.rows, f"{what}.rows", i32, (P,)),
+                            _array(plan.position, f"{what}.position", i32, (T, k)), E, T, k, P)
+
+
+def _call(name, device, *args):
+    """The library function on the current stream of `device`."""
+    torch = _torch()
+    fn = getattr(_dg.library(), name)
+    if device.index == torch.cuda.current_device():
+        st = fn(*args, torch.cuda.current_stream(device).cuda_stream)
+    else:
+        with torch.cuda.device(device):
+            st = fn(*args, torch.cuda.current_stream(device).cuda_stream)
+    _dg._check(st, name)
+
+
+def _new_block(rows, cols, dtype, block_rows, device):
+    """An empty BlockTensor, its scales laid out with the rows adjacent."""
+    torch = _torch()
+    data = torch.empty((rows, cols), dtype=dtype, device=device)
+    scale = torch.empty((-(-cols // BLOCK), -(-rows // block_rows)), dtype=torch.float32, device=device).t()
+    return BlockTensor(data, scale, block_rows)
+
+
+# ----------------------------------------------------------------------------- block-scaled products
+def gemm_block_quantize_tensors(x, dtype, block_rows=1, natural=True, transposed=False, rows=None):
+    """x (M, K) as (natural, transposed) BlockTensors of the float8 `dtype`, either None where not asked for.
+
+    rows (int32, any length R): row i of the result is row rows[i] of x, zeros where rows[i] is negative
+    or at least M.
+    """
+    ld = _matrix(x, "x")
+    code, wide = _code_type(dtype, "dtype"), _wide_type(x.dtype, "x")
+    if block_rows not in (1, BLOCK):
+        raise ValueError(f"block_rows must be 1 or {BLOCK}, not {block_rows}")
+    if not natural and not transposed:
+        raise ValueError("neither natural nor transposed is asked for")
+    M, K = x.shape
+    R, gather = M, None
+    if rows is not None:
+        R = rows.numel()
+        gather = _array(rows, "rows", _torch().int32, (R,))
+        dev = _device(x, rows)
+    else:
+        dev = _device(x)
+    q = _new_block(R, K, dtype, block_rows, dev) if natural else None
+    t = _new_block(K, R, dtype, block_rows, dev) if transposed else None
+    if R and K:
+        _call("gemm_block_quantize", dev, x.data_ptr(), M, K, ld, wide, gather, R,
+              ctypes.byref(_block(q, "natural")) if natural else None,
+              ctypes.byref(_block(t, "transposed")) if transposed else None)
+    return q, t
+
+
+def gemm_block_product_tensors(a, b, dtype=None):
+    """C (M, N) = A B^T for BlockTensors a (M, K) and b (N, K), stored as `dtype` (bfloat16 by default)."""
+    torch = _torch()
+    dtype = dtype or torch.bfloat16
+    out = _wide_type(dtype, "dtype")
+    A, B = _block(a, "a"), _block(b, "b")
+    if A.cols != B.cols:
+        raise ValueError(f"shape mismatch: a {tuple(a.data.shape)}, b {tuple(b.data.shape)}")
+    dev = _device(a.data, a.scale, b.data, b.scale)
+    M, N, K = A.rows, B.rows, A.cols
+    c = torch.empty((M, N), dtype=dtype, device=dev)
+    if M and N:
+        n = _dg.library().gemm_block_product_workspace(M, N, K)
+        work = torch.empty(n, dtype=torch.uint8, device=dev) if n else None
+        _call("gemm_block_product", dev, ctypes.byref(A), ctypes.byref(B), c.data_ptr(), N, out,
+              work.data_ptr() if n else None, n)
+    return c
+
+
+# ----------------------------------------------------------------------------- experts
+def _logits(logits, router):
+    if not isinstance(router, gemm_router):
+        raise TypeError(f"router must be a gemm_router, not {type(router).__name__}")
+    return _matrix(logits, "logits"), _wide_type(logits.dtype, "logits")
+
+
+def gemm_experts_route_tensors(logits, router, bias=None):
+    """(index, weight), int32 and float32 (T, k), of logits (T, E); bias: float32 (E), for the choice only."""
+    torch = _torch()
+    ld, code = _logits(logits, router)
+    T, E = logits.shape
+    if bias is not None:
+        _array(bias, "bias", torch.float32, (E,))
+        dev = _device(logits, bias)
+    else:
+        dev = _device(logits)
+    index = torch.empty((T, max(router.top_k, 0)), dtype=torch.int32, device=dev)
+    weight = torch.empty((T, max(router.top_k, 0)), dtype=torch.float32, device=dev)
+    _call("gemm_experts_route", dev, logits.data_ptr(), T, E, ld, code, ctypes.byref(router),
+          bias.data_ptr() if bias is not None else None, index.data_ptr(), weight.data_ptr())
+    return index, weight
+
+
+def gemm_experts_route_backward_tensors(logits, router, index, weight_grad):
+    """The gradient of the logits (their type) from that of the weights, the choice held fixed."""
+    torch = _torch()
+    ld, code = _logits(logits, router)
+    T, E = logits.shape
+    i = _array(index, "index", torch.int32, (T, router.top_k))
+    g = _array(weight_grad, "weight_grad", torch.float32, (T, router.top_k))
+    dev = _device(logits, index, weight_grad)
+    grad = torch.empty((T, E), dtype=logits.dtype, device=dev)
+    _call("gemm_experts_route_backward", dev, logits.data_ptr(), T, E, ld, code, ctypes.byref(router), i, g,
+          grad.data_ptr(), E)
+    return grad
+
+
+def gemm_experts_dispatch_tensors(index, experts, align=1):
+    """The ExpertPlan of index (T, k): every expert's (token, slot) pairs in their order, an expert's
+    first row at a multiple of `align` (128 where a gradient of the weights is wanted)."""
+    torch = _torch()
+    if index.dim() != 2:
+        raise ValueError(f"index must be 2-D, not {tuple(index.shape)}")
+    T, k = index.shape
+    i = _array(index, "index", torch.int32, (T, k))
+    if experts < 1 or align < 1:
+        raise ValueError(f"experts = {experts} and align = {align} must be positive")
+    dev = _device(index)
+    lib = _dg.library()
+    P, n = lib.gemm_experts_capacity(T, k, experts, align), lib.gemm_experts_dispatch_workspace(T, k, experts)
+    head = torch.empty(2 * experts + 1, dtype=torch.int32, device=dev)
+    plan = ExpertPlan(head[:experts + 1], head[experts + 1:], torch.empty(P, dtype=torch.int32, device=dev),
+                      torch.empty((T, k), dtype=torch.int32, device=dev), align)
+    work = torch.empty(n, dtype=torch.uint8, device=dev) if n else None
+    _call("gemm_experts_dispatch", dev, i, align, ctypes.byref(_plan(plan)), work.data_ptr() if n else None, n)
+    return plan
+
+
+def gemm_experts_product_tensors(a, b, plan, dtype=None, gather=True):
+    """C (P, N): each row of the plan times its expert's matrix, zeros in padding rows. b (E, N, K); a holds
+    the tokens' rows (T, K) with gather, the plan's (P, K) without."""
+    torch = _torch()
+    dtype = dtype or torch.bfloat16
+    out = _wide_type(dtype, "dtype")
+    A, B, p = _block(a, "a"), _block(b, "b", True), _plan(plan)
+    if A.cols != B.cols or b.data.shape[0] != p.experts or A.rows != (p.tokens if gather else p.capacity):
+        raise ValueError(f"shape mismatch: a {tuple(a.data.shape)}, b {tuple(b.data.shape)}, plan of {p.experts} "
+                         f"experts, {p.tokens} tokens and {p.capacity} rows")
+    dev = _device(a.data, a.scale, b.data, b.scale, plan.offsets, plan.counts, plan.rows)
+    c = torch.empty((p.capacity, B.rows), dtype=dtype, device=dev)
+    if c.numel():
+        _call("gemm_experts_product", dev, ctypes.byref(A), ctypes.byref(B), ctypes.byref(p), int(gather),
+              c.data_ptr(), B.rows, out)
+    return c
+
+
+def gemm_experts_gradient_tensors(a, b, plan, dtype=None):
+    """C (E, M, N) = A_e B_e^T over each expert's rows, for a (M, P) and b (N, P) with the plan's rows along
+    their columns and zeros in padding, as gemm_block_quantize_tensors(..., transposed=True, rows=plan.rows)
+    makes them. The plan's align has to be a multiple of 128; float32 by default."""
+    torch = _torch()
+    dtype = dtype or torch.float32
+    out = _wide_type(dtype, "dtype")
+    A, B, p = _block(a, "a"), _block(b, "b"), _plan(plan)
+    if A.cols != p.capacity or B.cols != p.capacity:
+        raise ValueError(f"shape mismatch: a {tuple(a.data.shape)}, b {tuple(b.data.shape)}, plan of {p.capacity} rows")
+    if plan.align is not None and plan.align % BLOCK:
+        raise ValueError(f"the plan's align is {plan.align}, not a multiple of {BLOCK}")
+    dev = _device(a.data, a.scale, b.data, b.scale, plan.offsets)
+    c = torch.empty((p.experts, A.rows, B.rows), dtype=dtype, device=dev)
+    if c.numel():
+        _call("gemm_experts_gradient", dev, ctypes.byref(A), ctypes.byref(B), ctypes.byref(p), c.data_ptr(), B.rows,
+              A.rows * B.rows, out)
+    return c
+
+
+def _combine(y, plan, weight):
+    torch = _torch()
+    p = _plan(plan)
+    ld, code = _matrix(y, "y"), _wide_type(y.dtype, "y")
+    if y.shape[0] != p.capacity:
+        raise ValueError(f"y has {y.shape[0]} rows, the plan {p.capacity}")
+    _array(weight, "weight", torch.float32, (p.tokens, p.top_k))
+    return p, ld, code
+
+
+def gemm_experts_combine_tensors(y, plan, weight):
+    """out (T, N) = the sum of each token's rows of y (P, N), weighted by weight (T, k) float32."""
+    p, ld, code = _combine(y, plan, weight)
+    dev = _device(y, plan.position, weight)
+    N = y.shape[1]
+    out = _torch().empty((p.tokens, N), dtype=y.dtype, device=dev)
+    if out.numel():
+        _call("gemm_experts_combine", dev, y.data_ptr(), N, ld, code, ctypes.byref(p), weight.data_ptr(),
+              out.data_ptr(), N)
+    return out
+
+
+def gemm_experts_combine_backward_tensors(y, plan, weight, grad):
+    """(y_grad (P, N) of y's type, weight_grad (T, k) float32) from grad (T, N)."""
+    torch = _torch()
+    p, ld, code = _combine(y, plan, weight)
+    ldg = _matrix(grad, "grad")
+    if grad.dtype != y.dtype or tuple(grad.shape) != (p.tokens, y.shape[1]):
+        raise ValueError(f"grad must be {y.dtype} of shape {(p.tokens, y.shape[1])}, not {grad.dtype} {tuple(grad.shape)}")
+    dev = _device(y, plan.position, plan.rows, weight, grad)
+    N = y.shape[1]
+    y_grad = torch.empty((p.capacity, N), dtype=y.dtype, device=dev)
+    weight_grad = torch.empty((p.tokens, p.top_k), dtype=torch.float32, device=dev)
+    _call("gemm_experts_combine_backward", dev, y.data_ptr(), N, ld, code, ctypes.byref(p), weight.data_ptr(),
+          grad.data_ptr(), ldg, y_grad.data_ptr(), N, weight_grad.data_ptr())
+    return y_grad, weight_grad

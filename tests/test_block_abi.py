@@ -1,0 +1,231 @@
+"""CPU tests of include/gemm_experts.h and its torch front: exported symbols, refusals before
+any device access, host-side sizes. No kernel is launched."""
+import ctypes
+import os
+import re
+
+import pytest
+import torch
+
+import dense_gemm_06_amd as dg
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+E4, E5 = torch.float8_e4m3fn, torch.float8_e5m2
+OK, INVALID, NULL, UNSUPPORTED = 0, 1, 2, 3
+
+
+def lib():
+    return dg.library()
+
+
+def test_header_symbols_exported():
+    src = open(os.path.join(ROOT, "include", "gemm_experts.h")).read()
+    src = re.sub(r"/\*.*?\*/", "", src, flags=re.S)
+    names = set(re.findall(r"^\s*(?:int|int64_t)\s+(gemm_\w+)\s*\(", src, flags=re.M))
+    assert names == {"gemm_block_quantize", "gemm_block_product", "gemm_block_product_workspace", "gemm_experts_route",
+                     "gemm_experts_route_backward", "gemm_experts_capacity", "gemm_experts_dispatch",
+                     "gemm_experts_dispatch_workspace", "gemm_experts_product", "gemm_experts_gradient",
+                     "gemm_experts_combine", "gemm_experts_combine_backward"}
+    for n in names:
+        assert hasattr(lib(), n), n
+
+
+def mat(rows, cols, data=1 << 20, scale=1 << 40, **kw):
+    m = dg.gemm_block_matrix(data, scale, rows, cols, cols, 1, rows, rows * cols, 64, dg.GEMM_E4M3, 1)
+    for k, v in kw.items():
+        setattr(m, k, v)
+    return m
+
+
+def ref(x):
+    return ctypes.byref(x) if x is not None else None
+
+
+def product(A, B, C=1 << 50, ldc=None, out=dg.GEMM_BF16, ws=None, n=0):
+    return lib().gemm_block_product(ref(A), ref(B), C, ldc if ldc is not None else (B.rows if B else 1), out, ws, n, None)
+
+
+@pytest.mark.parametrize("want,kw", [
+    (NULL, dict(A=None)), (NULL, dict(B=None)), (NULL, dict(C=None)), (NULL, dict(A=mat(4, 128, data=None))),
+    (NULL, dict(B=mat(8, 128, scale=None))), (INVALID, dict(out=3)), (INVALID, dict(ldc=7)),
+    (INVALID, dict(A=mat(4, 256))), (INVALID, dict(A=mat(-1, 128))), (INVALID, dict(A=mat(4, 128, ld=100))),
+    (INVALID, dict(A=mat(4, 128, dtype=0))), (INVALID, dict(A=mat(4, 128, block_rows=64))),
+    (INVALID, dict(A=mat(4, 128, scale_row=-1))), (UNSUPPORTED, dict(A=mat(1 << 31, 128))),
+    (INVALID, dict(C=1 << 20)), (INVALID, dict(C=(1 << 40) + 4)), (INVALID, dict(ws=8, n=64)), (INVALID, dict(n=-1)),
+    (NULL, dict(n=64))])
+def test_product_refusals(want, kw):
+    args = dict(A=mat(4, 128), B=mat(8, 128, data=1 << 30, scale=1 << 41))
+    args.update(kw)
+    assert product(**args) == want
+    assert dg.gemm_last_error()
+
+
+def test_empty_products_need_no_device():
+    assert product(mat(0, 128, None, None), mat(8, 128)) == OK
+    assert product(mat(4, 128), mat(0, 128, None, None), ldc=1) == OK
+
+
+@pytest.mark.parametrize("want,kw", [
+    (INVALID, dict(dtype=7)), (NULL, dict(nat=None)), (INVALID, dict(nat=mat(5, 128))), (INVALID, dict(tr=mat(4, 128))),
+    (INVALID, dict(rows=5)), (NULL, dict(X=None)), (INVALID, dict(ldx=100)), (INVALID, dict(cols=-1)),
+    (INVALID, dict(X=(1 << 20) + 8)), (INVALID, dict(tr=mat(128, 4, data=(1 << 20) + 16)))])
+def test_quantize_refusals(want, kw):
+    args = dict(X=1 << 50, x_rows=4, cols=128, ldx=128, dtype=dg.GEMM_BF16, gather=None, rows=4, nat=mat(4, 128), tr=None)
+    args.update(kw)
+    a = args
+    assert lib().gemm_block_quantize(a["X"], a["x_rows"], a["cols"], a["ldx"], a["dtype"], a["gather"], a["rows"],
+                                     ref(a["nat"]), ref(a["tr"]), None) == want
+    assert dg.gemm_last_error()
+
+
+@pytest.mark.parametrize("want,kw", [
+    (INVALID, dict(top_k=0)), (INVALID, dict(top_k=65)), (INVALID, dict(top_k=33)), (INVALID, dict(score=2)),
+    (INVALID, dict(groups=7, top_groups=1)), (INVALID, dict(groups=4, top_groups=5)), (INVALID, dict(groups=0)),
+    (INVALID, dict(groups=16, top_groups=1, top_k=5)), (INVALID, dict(group_top=5)),
+    (INVALID, dict(groups=32, top_groups=32, group_top=3))])
+def test_router_refusals(want, kw):
+    r = dg.router(**{**dict(top_k=4), **kw})
+    assert lib().gemm_experts_route(1 << 20, 4, 64, 64, 0, ref(r), None, 1 << 30, 1 << 31, None) == want
+    assert lib().gemm_experts_route_backward(1 << 20, 4, 64, 64, 0, ref(r), 1 << 30, 1 << 31, 1 << 32, 64, None) == want
+
+
+def test_route_refusals():
+    r = dg.router(4)
+    call = lambda x=1 << 20, T=4, E=64, ld=64, dt=0, rt=r, i=1 << 30, w=1 << 31: lib().gemm_experts_route(  # noqa: E731
+        x, T, E, ld, dt, ref(rt), None, i, w, None)
+    assert call(x=None) == NULL and call(i=None) == NULL and call(w=None) == NULL and call(rt=None) == NULL
+    assert call(T=-1) == INVALID and call(ld=63) == INVALID and call(dt=3) == INVALID and call(E=0) == INVALID
+    assert call(E=1025, ld=1025) == UNSUPPORTED and call(i=(1 << 20) + 4) == INVALID and call(w=1 << 30) == INVALID
+    assert call(T=0, x=None) == OK
+
+
+def plan(E=4, T=8, k=2, P=None, **kw):
+    P = lib().gemm_experts_capacity(T, k, E, 1) if P is None else P
+    p = dg.gemm_expert_plan(1 << 20, 1 << 21, 1 << 22, 1 << 23, E, T, k, P)
+    for a, b in kw.items():
+        setattr(p, a, b)
+    return p
+
+
+def test_dispatch_refusals():
+    call = lambda p, align=1, i=1 << 30, ws=None, n=0: lib().gemm_experts_dispatch(i, align, ref(p), ws, n, None)  # noqa: E731
+    assert call(None) == NULL and call(plan(), i=None) == NULL and call(plan(offsets=None)) == NULL
+    assert call(plan(P=15)) == INVALID and call(plan(), align=0) == INVALID and call(plan(E=0)) == INVALID
+    assert call(plan(E=1025, P=10 ** 6)) == UNSUPPORTED and call(plan(T=-1)) == INVALID
+    assert call(plan(T=1 << 20, k=1 << 12, P=1)) == UNSUPPORTED
+    assert call(plan(T=4096, P=8192)) == INVALID        # needs a workspace
+    assert call(plan(counts=1 << 20)) == INVALID        # outputs overlap
+    assert call(plan(), i=1 << 22) == INVALID
+
+
+def test_capacity_and_workspace():
+    f = lib().gemm_experts_capacity
+    assert f(0, 4, 8, 128) == 0 and f(1, 1, 8, 128) == 128 and f(16, 4, 64, 1) == 64
+    assert f(4096, 8, 64, 128) == (32768 + 64 * 127 + 127) // 128 * 128
+    assert lib().gemm_experts_dispatch_workspace(16, 4, 64) == 0
+    assert lib().gemm_experts_dispatch_workspace(1024, 2, 64) == 2 * 64 * 4
+    assert lib().gemm_block_product_workspace(0, 4, 4) == 0 and lib().gemm_block_product_workspace(-1, 4, 4) == 0
+
+
+def test_experts_product_refusals():
+    def call(A=mat(8, 128), B=mat(16, 128, data=1 << 30, scale=1 << 41), p=None, gather=1, C=1 << 50, ldc=16, out=0):
+        return lib().gemm_experts_product(ref(A), ref(B), ref(p or plan()), gather, C, ldc, out, None)
+    assert call(A=None) == NULL and call(C=None) == NULL and call(p=plan(rows=None)) == NULL
+    assert call(A=mat(9, 128)) == INVALID and call(gather=0) == INVALID and call(A=mat(8, 256)) == INVALID
+    assert call(ldc=15) == INVALID and call(out=4) == INVALID
+    assert call(C=(1 << 30) + 3 * 16 * 128) == INVALID   # inside the last expert's matrix
+    assert lib().gemm_experts_product(ref(mat(8, 128)), ref(mat(16, 128)), None, 1, 1 << 50, 16, 0, None) == NULL
+
+
+def test_experts_gradient_refusals():
+    def call(A=mat(16, 128), B=mat(32, 128, data=1 << 30, scale=1 << 41), p=plan(P=128), C=1 << 50, ldc=32, sc=512, out=0):
+        return lib().gemm_experts_gradient(ref(A), ref(B), ref(p), C, ldc, sc, out, None)
+    assert call(A=mat(16, 256)) == INVALID and call(sc=511) == INVALID and call(ldc=31) == INVALID
+    assert call(C=None) == NULL and call(C=1 << 30) == INVALID and call(p=plan(P=128, offsets=None)) == NULL
+
+
+def test_combine_refusals():
+    def fwd(Y=1 << 30, cols=16, ldy=16, dt=2, p=plan(), w=1 << 31, out=1 << 32, ldo=16):
+        return lib().gemm_experts_combine(Y, cols, ldy, dt, ref(p), w, out, ldo, None)
+    assert fwd(Y=None) == NULL and fwd(w=None) == NULL and fwd(out=None) == NULL and fwd(p=None) == NULL
+    assert fwd(ldy=15) == INVALID and fwd(ldo=15) == INVALID and fwd(dt=3) == INVALID and fwd(out=1 << 30) == INVALID
+
+    def bwd(Y=1 << 30, p=plan(), w=1 << 31, G=1 << 32, yg=1 << 33, wg=1 << 34):
+        return lib().gemm_experts_combine_backward(Y, 16, 16, 2, ref(p), w, G, 16, yg, 16, wg, None)
+    assert bwd(G=None) == NULL and bwd(yg=None) == NULL and bwd(wg=None) == NULL and bwd(yg=1 << 30) == INVALID
+    assert bwd(p=plan(k=33)) == UNSUPPORTED and bwd(wg=1 << 31) == INVALID
+
+
+# ----------------------------------------------------------------------------- torch front, on CPU tensors
+def block(r, k, br=1, dtype=E4, **kw):
+    return dg.BlockTensor(torch.zeros(r, k, dtype=torch.uint8).view(dtype), torch.ones(-(-r // br), -(-k // 128)), br)
+
+
+def cpu_plan(E=4, T=8, k=2, P=128):
+    z = lambda *s: torch.zeros(*s, dtype=torch.int32)  # noqa: E731
+    return dg.ExpertPlan(z(E + 1), z(E), z(P), z(T, k), 128)
+
+
+def test_tensor_refusals():
+    x = torch.zeros(4, 128)
+    with pytest.raises(ValueError, match="one GPU"):
+        dg.gemm_block_quantize_tensors(x, E4)
+    with pytest.raises(TypeError, match="float8"):
+        dg.gemm_block_quantize_tensors(x, torch.int8)
+    with pytest.raises(TypeError, match="float32, float16"):
+        dg.gemm_block_quantize_tensors(x.double(), E4)
+    with pytest.raises(ValueError, match="block_rows"):
+        dg.gemm_block_quantize_tensors(x, E4, 64)
+    with pytest.raises(ValueError, match="unit stride"):
+        dg.gemm_block_quantize_tensors(x.t(), E4)
+    with pytest.raises(ValueError, match="neither"):
+        dg.gemm_block_quantize_tensors(x, E4, natural=False)
+    with pytest.raises(ValueError, match="rows overlap"):
+        dg.gemm_block_quantize_tensors(x[:1].expand(4, 128), E4)
+    with pytest.raises(TypeError, match="int32"):
+        dg.gemm_block_quantize_tensors(x, E4, rows=torch.zeros(3, dtype=torch.int64))
+    with pytest.raises(ValueError, match="one GPU"):
+        dg.gemm_block_product_tensors(block(4, 128), block(8, 128))
+    with pytest.raises(ValueError, match="mismatch"):
+        dg.gemm_block_product_tensors(block(4, 128), block(8, 256))
+    with pytest.raises(ValueError, match="scale"):
+        dg.gemm_block_product_tensors(block(4, 128), dg.BlockTensor(block(8, 128).data, torch.ones(1, 1), 1))
+    with pytest.raises(TypeError, match="scale"):
+        dg.gemm_block_product_tensors(block(4, 128), dg.BlockTensor(block(8, 128).data, torch.ones(8, 1).half(), 1))
+    with pytest.raises(TypeError, match="BlockTensor"):
+        dg.gemm_block_product_tensors(x, x)
+    with pytest.raises(TypeError, match="dtype"):
+        dg.gemm_block_product_tensors(block(4, 128), block(8, 128), torch.int32)
+
+
+def test_expert_tensor_refusals():
+    r, w = dg.router(2), torch.zeros(8, 2)
+    with pytest.raises(TypeError, match="gemm_router"):
+        dg.gemm_experts_route_tensors(torch.zeros(8, 4), 2)
+    with pytest.raises(ValueError, match="bias"):
+        dg.gemm_experts_route_tensors(torch.zeros(8, 4), r, torch.zeros(5))
+    with pytest.raises(TypeError, match="index"):
+        dg.gemm_experts_dispatch_tensors(torch.zeros(8, 2), 4)
+    with pytest.raises(ValueError, match="positive"):
+        dg.gemm_experts_dispatch_tensors(torch.zeros(8, 2, dtype=torch.int32), 4, 0)
+    with pytest.raises(ValueError, match="2-D"):
+        dg.gemm_experts_dispatch_tensors(torch.zeros(8, dtype=torch.int32), 4)
+    b = dg.BlockTensor(torch.zeros(4, 16, 128, dtype=torch.uint8).view(E4), torch.ones(4, 1, 1), 128)
+    with pytest.raises(ValueError, match="mismatch"):
+        dg.gemm_experts_product_tensors(block(9, 128), b, cpu_plan())
+    with pytest.raises(ValueError, match="mismatch"):
+        dg.gemm_experts_product_tensors(block(8, 128), b, cpu_plan(E=5))
+    with pytest.raises(ValueError, match="one GPU"):
+        dg.gemm_experts_product_tensors(block(8, 128), b, cpu_plan())
+    with pytest.raises(TypeError, match="ExpertPlan"):
+        dg.gemm_experts_product_tensors(block(8, 128), b, None)
+    p = cpu_plan()
+    p.align = 64
+    with pytest.raises(ValueError, match="align"):
+        dg.gemm_experts_gradient_tensors(block(16, 128), block(16, 128), p)
+    with pytest.raises(ValueError, match="rows"):
+        dg.gemm_experts_combine_tensors(torch.zeros(64, 16), cpu_plan(), w)
+    with pytest.raises(ValueError, match="weight"):
+        dg.gemm_experts_combine_tensors(torch.zeros(128, 16), cpu_plan(), w[:4])
+    with pytest.raises(ValueError, match="grad"):
+        dg.gemm_experts_combine_backward_tensors(torch.zeros(128, 16), cpu_plan(), w, torch.zeros(8, 15))
