@@ -103,7 +103,11 @@ int check_block(const char* name, const gemm_block_matrix* m, int64_t batch = 1)
     DG_TRY(check_pointer(name, m));
     DG_TRY(check_size(field("rows"), m->rows));
     DG_TRY(check_size(field("cols"), m->cols));
-    DG_TRY(check_ld(field("ld"), m->ld, m->cols));
+    if (m->op != GEMM_OP_N && m->op != GEMM_OP_T) {
+        set_error("%s.op = %d is not GEMM_OP_N or GEMM_OP_T", name, m->op);
+        return GEMM_ERR_INVALID_VALUE;
+    }
+    DG_TRY(check_ld(field("ld"), m->ld, m->op == GEMM_OP_T ? m->rows : m->cols));
     if (m->dtype != GEMM_E4M3 && m->dtype != GEMM_E5M2) {
         set_error("%s.dtype = %d is not GEMM_E4M3 or GEMM_E5M2", name, m->dtype);
         return GEMM_ERR_INVALID_VALUE;
@@ -124,8 +128,15 @@ int check_block(const char* name, const gemm_block_matrix* m, int64_t batch = 1)
     return GEMM_OK;
 }
 
+int check_op_n(const char* name, const gemm_block_matrix& m) {
+    if (m.op == GEMM_OP_N) return GEMM_OK;
+    set_error("%s.op = GEMM_OP_T: its rows have to be contiguous here", name);
+    return GEMM_ERR_UNSUPPORTED;
+}
+
 Range data_range(const char* name, const gemm_block_matrix& m, int64_t batch = 1) {
-    return range(name, m.data, span(m.rows, m.cols, m.ld, 1, batch, m.stride));
+    return range(name, m.data, m.op == GEMM_OP_T ? span(m.cols, m.rows, m.ld, 1, batch, m.stride)
+                                                 : span(m.rows, m.cols, m.ld, 1, batch, m.stride));
 }
 
 Range scale_range(const char* name, const gemm_block_matrix& m, int64_t batch = 1) {
@@ -162,7 +173,13 @@ int launched(int rc, const char* what) {
 // ---------------------------------------------------------------- the products' kernels
 // Rows that start at multiples of 16 bytes and hold whole 16-byte chunks.
 bool direct_rows(const gemm_block_matrix& m, int64_t batch) {
-    return ((uintptr_t)m.data & 15) == 0 && m.ld % 16 == 0 && m.cols % 16 == 0 && (batch <= 1 || m.stride % 16 == 0);
+    const int64_t across = m.op == GEMM_OP_T ? m.rows : m.cols;
+    return ((uintptr_t)m.data & 15) == 0 && m.ld % 16 == 0 && across % 16 == 0 && (batch <= 1 || m.stride % 16 == 0);
+}
+
+// BlockPlan::tr of two operands.
+int tr_of(const gemm_block_matrix& A, const gemm_block_matrix& B) {
+    return (A.op == GEMM_OP_T ? 2 : 0) | (B.op == GEMM_OP_T ? 1 : 0);
 }
 
 constexpr int64_t kCus = 256;
@@ -170,13 +187,14 @@ constexpr int64_t kCus = 256;
 // rows: rows of C that share a B (for experts the average); n_products: B's in the call;
 // wide: the 256 x 256 tiles exist for the call (C of 16 bits, a scale for 128 rows of B);
 // may_split: whether K may be split.
-dg::BlockPlan block_plan(int64_t rows, int64_t n_products, int64_t N, int64_t K, bool direct, bool wide,
+dg::BlockPlan block_plan(int64_t rows, int64_t n_products, int64_t N, int64_t K, bool direct, bool wide, int tr,
                          bool may_split) {
     dg::BlockPlan p;
+    p.tr = tr;
     p.direct = direct;
     p.split = 1;
     const int64_t nkb = ceil_div(K, dg::kBlock);
-    if (rows <= 64) {
+    if (rows <= 64 && tr == 0) {
         p.kernel = dg::BLOCK_SKINNY;
         p.bm = rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
         p.bn = 16;
@@ -184,7 +202,7 @@ dg::BlockPlan block_plan(int64_t rows, int64_t n_products, int64_t N, int64_t K,
         if (may_split && wgs < kCus) p.split = (int)std::max<int64_t>(1, std::min<int64_t>(kCus / wgs, nkb / 16));
     } else {
         const int64_t big = n_products * ceil_div(rows, 256) * ceil_div(N, 256);
-        p.kernel = direct && wide && big >= kCus * 3 / 4 ? dg::BLOCK_TILE256 : dg::BLOCK_TILE128;
+        p.kernel = direct && wide && tr == 0 && big >= kCus * 3 / 4 ? dg::BLOCK_TILE256 : dg::BLOCK_TILE128;
         p.bm = p.bn = p.kernel == dg::BLOCK_TILE256 ? 256 : 128;
         const int64_t wgs = n_products * ceil_div(rows, p.bm) * ceil_div(N, p.bn);
         if (may_split && wgs < kCus) p.split = (int)std::max<int64_t>(1, std::min<int64_t>(2 * kCus / wgs, nkb / 4));
@@ -329,6 +347,7 @@ int gemm_block_quantize(const void* X, int64_t x_rows, int64_t cols, int64_t ldx
     }
     if (natural) {
         DG_TRY(check_block("natural", natural));
+        DG_TRY(check_op_n("natural", *natural));
         if (natural->rows != rows || natural->cols != cols) {
             set_error("natural is %lld x %lld, not %lld x %lld", (long long)natural->rows, (long long)natural->cols,
                       (long long)rows, (long long)cols);
@@ -337,6 +356,7 @@ int gemm_block_quantize(const void* X, int64_t x_rows, int64_t cols, int64_t ldx
     }
     if (transposed) {
         DG_TRY(check_block("transposed", transposed));
+        DG_TRY(check_op_n("transposed", *transposed));
         if (transposed->rows != cols || transposed->cols != rows) {
             set_error("transposed is %lld x %lld, not %lld x %lld", (long long)transposed->rows,
                       (long long)transposed->cols, (long long)cols, (long long)rows);
@@ -385,7 +405,8 @@ int64_t gemm_block_product_workspace(int64_t M, int64_t N, int64_t K) {
     int64_t bytes = 0;
     for (bool direct : {false, true})
         for (bool wide : {false, true})
-            bytes = std::max(bytes, split_bytes(block_plan(M, 1, N, K, direct, wide, true).split, M, N));
+            for (int tr : {0, 1})
+                bytes = std::max(bytes, split_bytes(block_plan(M, 1, N, K, direct, wide, tr, true).split, M, N));
     return bytes;
 }
 
@@ -416,8 +437,8 @@ int gemm_block_product(const gemm_block_matrix* A, const gemm_block_matrix* B, v
     DG_TRY(check_device());
     const bool direct = direct_rows(*A, 1) && direct_rows(*B, 1);
     const bool wide = B->block_rows != 1 && out_dtype != GEMM_F32;
-    dg::BlockPlan p = block_plan(M, 1, N, K, direct, wide, true);
-    if (split_bytes(p.split, M, N) > workspace_bytes) p = block_plan(M, 1, N, K, direct, wide, false);
+    dg::BlockPlan p = block_plan(M, 1, N, K, direct, wide, tr_of(*A, *B), true);
+    if (split_bytes(p.split, M, N) > workspace_bytes) p = block_plan(M, 1, N, K, direct, wide, tr_of(*A, *B), false);
     dg::BlockArgs a = block_args(*A, *B, C, ldc, out_dtype);
     a.mode = dg::BLOCK_PLAIN;
     a.tiles_m = (int)ceil_div(M, p.bm);
@@ -568,6 +589,7 @@ int gemm_experts_product(const gemm_block_matrix* A, const gemm_block_matrix* B,
     DG_TRY(check_plan(plan));
     DG_TRY(check_block("A", A));
     DG_TRY(check_block("B", B, plan->experts));
+    DG_TRY(check_op_n("A", *A));
     if (A->cols != B->cols) {
         set_error("A has %lld columns, B %lld", (long long)A->cols, (long long)B->cols);
         return GEMM_ERR_INVALID_VALUE;
@@ -595,7 +617,7 @@ int gemm_experts_product(const gemm_block_matrix* A, const gemm_block_matrix* B,
     const bool direct = direct_rows(*A, 1) && direct_rows(*B, E);
     const int64_t pairs = plan->tokens * plan->top_k, active = std::max<int64_t>(1, std::min(E, pairs));
     const dg::BlockPlan p = block_plan(std::max<int64_t>(1, pairs / active), active, N, A->cols, direct,
-                                       B->block_rows != 1 && out_dtype != GEMM_F32, false);
+                                       B->block_rows != 1 && out_dtype != GEMM_F32, tr_of(*A, *B), false);
     dg::BlockArgs a = block_args(*A, *B, C, ldc, out_dtype);
     a.mode = dg::BLOCK_EXPERTS;
     a.M = (int)P;
@@ -635,7 +657,7 @@ int gemm_experts_gradient(const gemm_block_matrix* A, const gemm_block_matrix* B
                           scale_range("B.scale", *B), range("plan.offsets", plan->offsets, (uint64_t)(E + 1) * 4)}));
     DG_TRY(check_device());
     const bool direct = direct_rows(*A, 1) && direct_rows(*B, 1);
-    const dg::BlockPlan p = block_plan(M, E, N, A->cols, direct, B->block_rows != 1 && out_dtype != GEMM_F32, false);
+    const dg::BlockPlan p = block_plan(M, E, N, A->cols, direct, B->block_rows != 1 && out_dtype != GEMM_F32, tr_of(*A, *B), false);
     dg::BlockArgs a = block_args(*A, *B, C, ldc, out_dtype);
     a.mode = dg::BLOCK_GRADIENT;
     a.E = (int)E;

@@ -49,6 +49,7 @@ struct BlockPlan {
     int bm, bn;
     int direct;       // 16-byte aligned rows: copies straight to LDS (tiles), whole 16-byte loads (skinny)
     int split;        // K slices
+    int tr;           // bit 0: B stored with its rows adjacent, bit 1: A
 };
 
 // Launchers return 0 or the hipError_t of the launch. ta, tb: 0 e4m3, 1 e5m2.

@@ -34,6 +34,7 @@
 namespace dg {
 
 typedef int i32x8 __attribute__((ext_vector_type(8)));
+typedef int i32x2 __attribute__((ext_vector_type(2)));
 
 // Source of the chunks that lie past the end of a row.
 __device__ const uint32_t block_zeros[4] = {0, 0, 0, 0};
@@ -243,11 +244,19 @@ __device__ __forceinline__ u32x4 load_codes(const uint8_t* p, int valid) {
 // (row >> 1) & 7, so that the 16 rows of any phase of a fragment read spread over all 64
 // banks, and the block's scales. DIRECT: the copies go from global memory straight to
 // LDS; otherwise (rows at any byte address) through registers.
-template <int TA, int TB, bool FULL, bool BROW, int BM, int BN, int WM, int WN, bool DIRECT>
+// TR: bit 0, B is stored with its rows adjacent (element (n, k) at k*ldb + n), bit 1 the
+// same for A. Such an operand's stage holds 128 rows of k, chunk c of row k at
+// c ^ 2((k >> 1) & 3), and a fragment's 8 k of one row come from ds_read_b64_tr_b8: in each
+// 16 lanes, lane i addresses 8 bytes of row k0 + i/2 at half i%2 of a chunk and receives
+// column i of the 8 rows. The 32 lanes of a phase then touch 8 rows x 32 bytes in 8
+// different places of the 256-byte bank period.
+template <int TA, int TB, bool FULL, bool BROW, int BM, int BN, int WM, int WN, bool DIRECT, int TR = 0>
 __global__ __launch_bounds__(WM* WN * 64) void block_tile(BlockArgs g) {
     constexpr int NW = WM * WN, SM = BM / 32 / WM, SJ = BN / 32 / WN;
     constexpr int CA = BM / 8 / NW, CB = BN / 8 / NW;  // 1 KB copies (8 rows) per wave
     static_assert((BM + BN) / 64 == NW, "each wave copies 64 scales of a stage");
+    constexpr bool TRB = (TR & 1) != 0, TRA = (TR & 2) != 0;
+    static_assert(TR == 0 || (BM == kBlock && BN == kBlock), "a transposed stage has rows of 128 bytes");
     __shared__ __attribute__((aligned(1024))) uint8_t sA[2][BM * kBlock];
     __shared__ __attribute__((aligned(1024))) uint8_t sB[2][BN * kBlock];
     __shared__ __attribute__((aligned(1024))) float fS[2][BM + BN];
@@ -263,22 +272,39 @@ __global__ __launch_bounds__(WM* WN * 64) void block_tile(BlockArgs g) {
     if (!any) return;
     if (t.m0 >= t.m_live) t.nkb = 0;  // nothing but padding: zeros
 
-    // ---- sources of this lane's copies
+    // ---- sources of this lane's copies: chunk positions lane & 7 of 8 rows. ka, kb: the k
+    // of a chunk within the block; va, vb: the bytes of a transposed chunk inside the matrix
     const uint8_t* pa[CA];
     const uint8_t* pb[CB];
-    int ka[CA], kc[CB];
+    int ka[CA], kc[CB], va[TRA ? CA : 1], vb[TRB ? CB : 1];
+    const size_t step_a = TRA ? (size_t)kBlock * (size_t)g.lda : kBlock;
+    const size_t step_b = TRB ? (size_t)kBlock * (size_t)g.ldb : kBlock;
 #pragma unroll
     for (int i = 0; i < CA; ++i) {
         const int row = (wave * CA + i) * 8 + (lane >> 3);
-        ka[i] = ((lane & 7) ^ ((row >> 1) & 7)) * 16;
-        const int r = max(block_a_row(g, t, min(t.m0 + row, t.m_end - 1)), 0);
-        pa[i] = g.A + (size_t)r * (size_t)g.lda + (size_t)t.kb0 * kBlock + ka[i];
+        if constexpr (TRA) {
+            const int m = t.m0 + ((lane & 7) ^ (2 * ((row >> 1) & 3))) * 16;
+            ka[i] = row;
+            va[i] = g.M - m;
+            pa[i] = g.A + ((size_t)t.kb0 * kBlock + row) * (size_t)g.lda + m;
+        } else {
+            ka[i] = ((lane & 7) ^ ((row >> 1) & 7)) * 16;
+            const int r = max(block_a_row(g, t, min(t.m0 + row, t.m_end - 1)), 0);
+            pa[i] = g.A + (size_t)r * (size_t)g.lda + (size_t)t.kb0 * kBlock + ka[i];
+        }
     }
 #pragma unroll
     for (int i = 0; i < CB; ++i) {
         const int row = (wave * CB + i) * 8 + (lane >> 3);
-        kc[i] = ((lane & 7) ^ ((row >> 1) & 7)) * 16;
-        pb[i] = g.B + (size_t)min(t.n0 + row, g.N - 1) * (size_t)g.ldb + (size_t)t.kb0 * kBlock + kc[i];
+        if constexpr (TRB) {
+            const int n = t.n0 + ((lane & 7) ^ (2 * ((row >> 1) & 3))) * 16;
+            kc[i] = row;
+            vb[i] = g.N - n;
+            pb[i] = g.B + ((size_t)t.kb0 * kBlock + row) * (size_t)g.ldb + n;
+        } else {
+            kc[i] = ((lane & 7) ^ ((row >> 1) & 7)) * 16;
+            pb[i] = g.B + (size_t)min(t.n0 + row, g.N - 1) * (size_t)g.ldb + (size_t)t.kb0 * kBlock + kc[i];
+        }
     }
     const float* ps;
     int64_t ps_step;
@@ -305,21 +331,23 @@ __global__ __launch_bounds__(WM* WN * 64) void block_tile(BlockArgs g) {
         if constexpr (DIRECT) {
 #pragma unroll
             for (int i = 0; i < CA; ++i) {
-                const void* src = pa[i] + (size_t)kb * kBlock;
-                if (ka[i] >= rem) src = block_zeros;
+                const void* src = pa[i] + (size_t)kb * step_a;
+                if (ka[i] >= rem || (TRA && va[TRA ? i : 0] <= 0)) src = block_zeros;
                 __builtin_amdgcn_global_load_lds(DG_GLB(src), DG_LDS_ADDR(dA + st * (BM * kBlock) + i * 1024u), 16, 0, 0);
             }
 #pragma unroll
             for (int i = 0; i < CB; ++i) {
-                const void* src = pb[i] + (size_t)kb * kBlock;
-                if (kc[i] >= rem) src = block_zeros;
+                const void* src = pb[i] + (size_t)kb * step_b;
+                if (kc[i] >= rem || (TRB && vb[TRB ? i : 0] <= 0)) src = block_zeros;
                 __builtin_amdgcn_global_load_lds(DG_GLB(src), DG_LDS_ADDR(dB + st * (BN * kBlock) + i * 1024u), 16, 0, 0);
             }
         } else {
 #pragma unroll
-            for (int i = 0; i < CA; ++i) ra[i] = load_codes(pa[i] + (size_t)kb * kBlock, rem - ka[i]);
+            for (int i = 0; i < CA; ++i)
+                ra[i] = load_codes(pa[i] + (size_t)kb * step_a, !TRA ? rem - ka[i] : ka[i] < rem ? va[TRA ? i : 0] : 0);
 #pragma unroll
-            for (int i = 0; i < CB; ++i) rb[i] = load_codes(pb[i] + (size_t)kb * kBlock, rem - kc[i]);
+            for (int i = 0; i < CB; ++i)
+                rb[i] = load_codes(pb[i] + (size_t)kb * step_b, !TRB ? rem - kc[i] : kc[i] < rem ? vb[TRB ? i : 0] : 0);
         }
     };
     auto settle = [&](int kb) {  // registers to LDS
@@ -345,6 +373,29 @@ __global__ __launch_bounds__(WM* WN * 64) void block_tile(BlockArgs g) {
         return i32x8{(int)x[0], (int)x[1], (int)x[2], (int)x[3], (int)y[0], (int)y[1], (int)y[2], (int)y[3]};
     };
 
+    // a transposed operand: the 8-byte pieces u = 0 .. 3 of a lane's 32 k, at rows
+    // 64h + 32lh + 8u + l16/2; `sub` is the subtile's number within the stage
+    const int l16 = lane & 15, lg = lane >> 4;
+    auto frag_tr = [&](const uint8_t* stage, int sub, int h) {
+        const int at = (32 * lh + (l16 >> 1)) * kBlock + (((2 * sub + (lg & 1)) ^ (2 * ((l16 >> 2) & 3))) << 4) + (l16 & 1) * 8;
+        i32x8 r;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const i32x2 v = __builtin_amdgcn_ds_read_tr8_b64_v2i32(DG_LDS_PTR(i32x2, stage + at + (64 * h + 8 * u) * kBlock));
+            r[2 * u] = v[0];
+            r[2 * u + 1] = v[1];
+        }
+        return r;
+    };
+    auto a_frag = [&](int st, int i, int h) {
+        if constexpr (TRA) return frag_tr(sA[st], wm * SM + i, h);
+        else return frag(&sA[st][(wm * SM + i) * 32 * kBlock], h);
+    };
+    auto b_frag = [&](int st, int j, int h) {
+        if constexpr (TRB) return frag_tr(sB[st], wn * SJ + j, h);
+        else return frag(&sB[st][(wn * SJ + j) * 32 * kBlock], h);
+    };
+
     f32x16 acc[SM][SJ];
 #pragma unroll
     for (int i = 0; i < SM; ++i)
@@ -363,8 +414,6 @@ __global__ __launch_bounds__(WM* WN * 64) void block_tile(BlockArgs g) {
         __builtin_amdgcn_s_barrier();
         asm volatile("" ::: "memory");
         if (kb + 1 < t.nkb) issue(kb + 1);
-        const uint8_t* a0 = &sA[st][wm * SM * 32 * kBlock];
-        const uint8_t* b0 = &sB[st][wn * SJ * 32 * kBlock];
         const float* fa = &fS[st][wm * SM * 32 + l32];
         const float* fb = &fS[st][BM + wn * SJ * 32];
         f32x4 sb[SJ][BROW ? 4 : 1];
@@ -393,10 +442,10 @@ __global__ __launch_bounds__(WM* WN * 64) void block_tile(BlockArgs g) {
 #pragma unroll
             for (int j = 0; j < SJ; ++j)
 #pragma unroll
-                for (int h = 0; h < 2; ++h) bf[j][h] = frag(b0 + j * 32 * kBlock, h);
+                for (int h = 0; h < 2; ++h) bf[j][h] = b_frag(st, j, h);
 #pragma unroll
             for (int i = 0; i < SM; ++i) {
-                const i32x8 af0 = frag(a0 + i * 32 * kBlock, 0), af1 = frag(a0 + i * 32 * kBlock, 1);
+                const i32x8 af0 = a_frag(st, i, 0), af1 = a_frag(st, i, 1);
 #pragma unroll
                 for (int j = 0; j < SJ; ++j)
                     add(i, j, mfma_32<TB, TA>(bf[j][1], af1, mfma_32<TB, TA>(bf[j][0], af0, f32x16{0})));
@@ -407,9 +456,9 @@ __global__ __launch_bounds__(WM* WN * 64) void block_tile(BlockArgs g) {
             for (int h = 0; h < 2; ++h) {
                 i32x8 af[SM], bf[SJ];
 #pragma unroll
-                for (int i = 0; i < SM; ++i) af[i] = frag(a0 + i * 32 * kBlock, h);
+                for (int i = 0; i < SM; ++i) af[i] = a_frag(st, i, h);
 #pragma unroll
-                for (int j = 0; j < SJ; ++j) bf[j] = frag(b0 + j * 32 * kBlock, h);
+                for (int j = 0; j < SJ; ++j) bf[j] = b_frag(st, j, h);
 #pragma unroll
                 for (int u = 0; u < 4; ++u) {
                     f16x8 aw[SM], bw[SJ];
@@ -540,8 +589,18 @@ __global__ __launch_bounds__(512) void block_skinny(BlockArgs g) {
     block_store4(g, m, n, v);
 }
 
+// Operands with adjacent rows: one kernel for either kind of scales, each row's its own.
+template <int TA, int TB, bool FULL, int TR>
+int launch_block_tr(const BlockPlan& p, const BlockArgs& a, dim3 grid, hipStream_t s) {
+    return p.direct ? launch_status(block_tile<TA, TB, FULL, true, 128, 128, 2, 2, true, TR>, grid, dim3(256), s, a)
+                    : launch_status(block_tile<TA, TB, FULL, true, 128, 128, 2, 2, false, TR>, grid, dim3(256), s, a);
+}
+
 template <int TA, int TB, bool FULL>
 int launch_block_full(const BlockPlan& p, const BlockArgs& a, dim3 grid, hipStream_t s) {
+    if (p.tr == 1) return launch_block_tr<TA, TB, FULL, 1>(p, a, grid, s);
+    if (p.tr == 2) return launch_block_tr<TA, TB, FULL, 2>(p, a, grid, s);
+    if (p.tr == 3) return launch_block_tr<TA, TB, FULL, 3>(p, a, grid, s);
     const bool brow = a.b_shift == 0;
     if constexpr (!FULL)
         if (p.kernel == BLOCK_TILE256)

@@ -15,7 +15,8 @@ captured into a graph.
   gemm_experts_combine_tensors          the weighted sum of each token's rows
   gemm_experts_combine_backward_tensors its gradients
 
-Tensors need unit stride along their last dimension; other strides are free.
+Tensors need unit stride along their last dimension (an operand's codes along either); other
+strides are free.
 """
 from __future__ import annotations
 
@@ -35,7 +36,7 @@ class gemm_block_matrix(ctypes.Structure):
     """Codes and block scales of a matrix, or of a batch of them (see include/gemm_experts.h)."""
     _fields_ = [("data", _vp), ("scale", _vp), ("rows", _i64), ("cols", _i64), ("ld", _i64), ("scale_row", _i64),
                 ("scale_block", _i64), ("stride", _i64), ("scale_stride", _i64), ("dtype", _i32),
-                ("block_rows", _i32)]
+                ("block_rows", _i32), ("op", _i32), ("reserved", _i32)]
 
 
 class gemm_router(ctypes.Structure):
@@ -79,11 +80,19 @@ def declare(lib):
 
 class BlockTensor:
     """Codes and scales: data (..., R, K) float8_e4m3fn or float8_e5m2; scale (..., ceil(R / block_rows),
-    ceil(K / 128)) float32, the number at (i, k) being data[i, k] * scale[i // block_rows, k // 128]."""
+    ceil(K / 128)) float32, the number at (i, k) being data[i, k] * scale[i // block_rows, k // 128].
+    Either of data's last two dimensions may be the contiguous one, so that codes in 128 x 128 blocks
+    serve both ways (t())."""
     __slots__ = ("data", "scale", "block_rows")
 
     def __init__(self, data, scale, block_rows=1):
         self.data, self.scale, self.block_rows = data, scale, block_rows
+
+    def t(self):
+        """The transposed numbers, in the same memory (128 x 128 blocks only)."""
+        if self.block_rows != BLOCK:
+            raise ValueError("only codes in 128 x 128 blocks have a transpose")
+        return BlockTensor(self.data.transpose(-1, -2), self.scale.transpose(-1, -2), BLOCK)
 
 
 class ExpertPlan:
@@ -155,7 +164,11 @@ def _block(b, what, batch=False):
         raise TypeError(f"{what} must be a BlockTensor, not {type(b).__name__}")
     data, scale, rows = b.data, b.scale, b.block_rows
     dims = 3 if batch else 2
-    ld = _matrix(data, f"{what}.data", dims)
+    op = _dg.GEMM_OP_N
+    if data.dim() == dims and data.stride(-1) != 1 and data.stride(-2) == 1 and min(data.shape[-2:]) > 1:
+        ld, op = _matrix(data.transpose(-1, -2), f"{what}.data", dims), _dg.GEMM_OP_T
+    else:
+        ld = _matrix(data, f"{what}.data", dims)
     code = _code_type(data.dtype, f"{what}.data")
     if rows not in (1, BLOCK):
         raise ValueError(f"{what}.block_rows must be 1 or {BLOCK}, not {rows}")
@@ -167,7 +180,7 @@ def _block(b, what, batch=False):
         raise ValueError(f"{what}.scale must have shape {want}, not {tuple(scale.shape)}")
     strides = scale.stride()
     return gemm_block_matrix(data.data_ptr(), scale.data_ptr(), R, K, ld, strides[-2], strides[-1],
-                             data.stride(0) if batch else 0, strides[0] if batch else 0, code, rows)
+                             data.stride(0) if batch else 0, strides[0] if batch else 0, code, rows, op, 0)
 
 
 def _plan(plan, what="plan"):

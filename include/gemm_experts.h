@@ -9,7 +9,10 @@
  *  and one fp32 scale for each block of `block_rows` x 128 elements (block_rows 1 or
  *  128; the last block of a row or column may be partial). The number that element
  *  (i, k) stands for is
- *      data[i*ld + k] * scale[(i / block_rows)*scale_row + (k / 128)*scale_block].
+ *      data[i*ld + k] * scale[(i / block_rows)*scale_row + (k / 128)*scale_block]
+ *  with op = GEMM_OP_N; with op = GEMM_OP_T the codes lie transposed, at data[k*ld + i] (a
+ *  matrix of 128 x 128 blocks serves as its own transpose so: swap rows and cols, swap the
+ *  scale's strides and set op).
  *
  * Plans
  * -----
@@ -49,11 +52,13 @@ typedef struct gemm_block_matrix {
     void* data;           /* codes; read as an operand, written by gemm_block_quantize */
     float* scale;
     int64_t rows, cols;   /* R, K */
-    int64_t ld;           /* >= max(1, cols) */
+    int64_t ld;           /* >= max(1, cols); GEMM_OP_T: >= max(1, rows) */
     int64_t scale_row, scale_block;   /* strides of the scale in elements, >= 0 */
     int64_t stride, scale_stride;     /* between the matrices of a batch (one for each expert) */
     int32_t dtype;        /* GEMM_E4M3 or GEMM_E5M2 */
     int32_t block_rows;   /* 1 or 128 */
+    int32_t op;           /* GEMM_OP_N or GEMM_OP_T (operands of products only) */
+    int32_t reserved;     /* 0 */
 } gemm_block_matrix;
 
 /*
@@ -140,7 +145,8 @@ int64_t gemm_experts_dispatch_workspace(int64_t tokens, int64_t top_k, int64_t e
 /*
  * gemm_experts_product -- C[p][j] = sum_k A(r,k) B_e(j,k) for every row p of expert e,
  * r = rows[p] with gather (A holds the tokens' rows) or p without (A holds the sorted
- * rows); padding rows of C are zeros. B is a batch of `experts` matrices N x K.
+ * rows); padding rows of C are zeros. B is a batch of `experts` matrices N x K; A has op
+ * GEMM_OP_N.
  */
 int gemm_experts_product(const gemm_block_matrix* A, const gemm_block_matrix* B, const gemm_expert_plan* plan,
                          int gather, void* C, int64_t ldc, int out_dtype, void* stream);

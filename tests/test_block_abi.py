@@ -50,7 +50,7 @@ def product(A, B, C=1 << 50, ldc=None, out=dg.GEMM_BF16, ws=None, n=0):
     (NULL, dict(B=mat(8, 128, scale=None))), (INVALID, dict(out=3)), (INVALID, dict(ldc=7)),
     (INVALID, dict(A=mat(4, 256))), (INVALID, dict(A=mat(-1, 128))), (INVALID, dict(A=mat(4, 128, ld=100))),
     (INVALID, dict(A=mat(4, 128, dtype=0))), (INVALID, dict(A=mat(4, 128, block_rows=64))),
-    (INVALID, dict(A=mat(4, 128, scale_row=-1))), (UNSUPPORTED, dict(A=mat(1 << 31, 128))),
+    (INVALID, dict(A=mat(4, 128, scale_row=-1))), (INVALID, dict(A=mat(4, 128, op=2))), (INVALID, dict(A=mat(400, 128, op=1))), (UNSUPPORTED, dict(A=mat(1 << 31, 128))),
     (INVALID, dict(C=1 << 20)), (INVALID, dict(C=(1 << 40) + 4)), (INVALID, dict(ws=8, n=64)), (INVALID, dict(n=-1)),
     (NULL, dict(n=64))])
 def test_product_refusals(want, kw):
@@ -68,7 +68,7 @@ def test_empty_products_need_no_device():
 @pytest.mark.parametrize("want,kw", [
     (INVALID, dict(dtype=7)), (NULL, dict(nat=None)), (INVALID, dict(nat=mat(5, 128))), (INVALID, dict(tr=mat(4, 128))),
     (INVALID, dict(rows=5)), (NULL, dict(X=None)), (INVALID, dict(ldx=100)), (INVALID, dict(cols=-1)),
-    (INVALID, dict(X=(1 << 20) + 8)), (INVALID, dict(tr=mat(128, 4, data=(1 << 20) + 16)))])
+    (INVALID, dict(X=(1 << 20) + 8)), (UNSUPPORTED, dict(nat=mat(4, 128, op=1))), (INVALID, dict(tr=mat(128, 4, data=(1 << 20) + 16)))])
 def test_quantize_refusals(want, kw):
     args = dict(X=1 << 50, x_rows=4, cols=128, ldx=128, dtype=dg.GEMM_BF16, gather=None, rows=4, nat=mat(4, 128), tr=None)
     args.update(kw)
@@ -131,7 +131,7 @@ def test_experts_product_refusals():
     def call(A=mat(8, 128), B=mat(16, 128, data=1 << 30, scale=1 << 41), p=None, gather=1, C=1 << 50, ldc=16, out=0):
         return lib().gemm_experts_product(ref(A), ref(B), ref(p or plan()), gather, C, ldc, out, None)
     assert call(A=None) == NULL and call(C=None) == NULL and call(p=plan(rows=None)) == NULL
-    assert call(A=mat(9, 128)) == INVALID and call(gather=0) == INVALID and call(A=mat(8, 256)) == INVALID
+    assert call(A=mat(8, 128, op=1)) == UNSUPPORTED and call(A=mat(9, 128)) == INVALID and call(gather=0) == INVALID and call(A=mat(8, 256)) == INVALID
     assert call(ldc=15) == INVALID and call(out=4) == INVALID
     assert call(C=(1 << 30) + 3 * 16 * 128) == INVALID   # inside the last expert's matrix
     assert lib().gemm_experts_product(ref(mat(8, 128)), ref(mat(16, 128)), None, 1, 1 << 50, 16, 0, None) == NULL

@@ -200,6 +200,25 @@ def test_product_strides():
         check_product(c, values(ad, sa, 1), values(bd, sb, 1), F32)
 
 
+@pytest.mark.parametrize("M,N,K", [(2, 2, 2), (16, 48, 300), (130, 200, 257), (256, 144, 512), (100, 333, 1000), (5, 400, 2048)])
+def test_product_operands_with_adjacent_rows(M, N, K):
+    """Codes stored transposed, for either operand and both, aligned and not; 128 x 128 blocks as their own transpose."""
+    g = gen(M * N)
+    for i, (ta, tb) in enumerate(((E4, E4), (E4, E5), (E5, E4), (E5, E5))):
+        a, b = codes(g, M, K, ta, 1), codes(g, N, K, tb, BLOCK if i & 1 else 1)
+        rb = BLOCK if i & 1 else 1
+        flip = lambda x: x.cuda().t().contiguous().t()  # noqa: E731
+        for fa, fb in ((False, True), (True, False), (True, True)):
+            A = dg.BlockTensor(flip(a[0]) if fa else a[0].cuda(), a[1].cuda(), 1)
+            B = dg.BlockTensor(flip(b[0]) if fb else b[0].cuda(), b[1].cuda(), rb)
+            out = (F32, BF16)[(i + fa) % 2]
+            check_product(dg.gemm_block_product_tensors(A, B, out), values(*a, 1), values(*b, rb), out, (ta, tb, fa, fb))
+    w = codes(g, K, N, E4, BLOCK)
+    W = dg.BlockTensor(w[0].cuda(), w[1].cuda(), BLOCK)
+    a = codes(g, M, K, E4, 1)
+    check_product(dg.gemm_block_product_tensors(dev((*a, 1)), W.t(), BF16), values(*a, 1), values(*w, BLOCK).t().contiguous(), BF16)
+
+
 def test_product_empty():
     z = lambda r, k: dg.BlockTensor(torch.empty(r, k, dtype=E4, device="cuda"),  # noqa: E731
                                     torch.empty(r, blocks(k), device="cuda"), 1)

@@ -243,6 +243,28 @@ def test_experts_gradient(T, k, E, M, N):
             check_product(c[e], A[:, off[e]:off[e + 1]], B[:, off[e]:off[e + 1]], out, e)
 
 
+@pytest.mark.parametrize("T,M,N", [(70, 64, 128), (300, 130, 200)])
+def test_experts_operands_with_adjacent_rows(T, M, N):
+    """The gradient of codes stored (P, N); the data gradient through the experts' own matrices, turned."""
+    g = gen(T)
+    plan = dg.gemm_experts_dispatch_tensors(choice(g, T, 4, 2).cuda(), 4, BLOCK)
+    P, off = plan.rows.numel(), plan.offsets.tolist()
+    a, b = codes(g, M, P, E5, 1), codes(g, N, P, E4, 1)
+    want_a, want_b = values(*a, 1), values(*b, 1)
+    flip = lambda x: x.cuda().t().contiguous().t()  # noqa: E731
+    for fa, fb in ((False, True), (True, False), (True, True)):
+        A = dg.BlockTensor(flip(a[0]) if fa else a[0].cuda(), a[1].cuda(), 1)
+        B = dg.BlockTensor(flip(b[0]) if fb else b[0].cuda(), b[1].cuda(), 1)
+        c = dg.gemm_experts_gradient_tensors(A, B, plan)
+        for e in range(4):
+            check_product(c[e], want_a[:, off[e]:off[e + 1]], want_b[:, off[e]:off[e + 1]], F32, e)
+    w = codes(g, N, M, E4, BLOCK, batch=4)
+    W = dg.BlockTensor(w[0].cuda(), w[1].cuda(), BLOCK)
+    x = codes(g, T, N, E5, 1)
+    c = dg.gemm_experts_product_tensors(dg.BlockTensor(x[0].cuda(), x[1].cuda(), 1), W.t(), plan, BF16)
+    check_experts(c, values(*x, 1), expert_values(w).transpose(1, 2).contiguous(), plan, BF16, True)
+
+
 def test_experts_gradient_rows_inside_a_block_are_nan():
     plan = dg.gemm_experts_dispatch_tensors(torch.tensor([[0], [1]], dtype=torch.int32).cuda(), 2, 64)
     P = plan.rows.numel()
