@@ -12,18 +12,15 @@
 
 namespace dg {
 
-// Eight elements from p, of which `valid` (> 0) exist.
+// Eight elements from p, of which `valid` (> 0) exist (the rest zero).
 template <int DT>
-__device__ __forceinline__ void load8(float (&v)[8], const typename Elem<DT>::type* p, int valid) {
-    typename Elem<DT>::type raw[8];
+__device__ __forceinline__ void load8_raw(typename Elem<DT>::type (&raw)[8], const typename Elem<DT>::type* p, int valid) {
     if (valid >= 8) {
         __builtin_memcpy(raw, p, sizeof raw);
     } else {
 #pragma unroll
         for (int e = 0; e < 8; ++e) raw[e] = e < valid ? p[e] : typename Elem<DT>::type(0);
     }
-#pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = decode<DT>(raw[e]);
 }
 
 template <int DT> __device__ __forceinline__ typename Elem<DT>::type encode(float x);
@@ -47,6 +44,30 @@ __device__ __forceinline__ void store8(typename Elem<DT>::type* p, const float (
     }
 }
 
+// Slots are taken eight at a time, their rows' loads all in flight together: a slot's row
+// and weight are the same for a whole workgroup, a slot without a row reads row 0 and drops
+// what it read.
+constexpr int kSlots = 8;
+
+struct Slots {
+    int p[kSlots];
+    float w[kSlots];
+    bool in[kSlots];
+};
+
+__device__ __forceinline__ Slots slots_of(const CombineArgs& a, int t, int j0) {
+    Slots s;
+#pragma unroll
+    for (int u = 0; u < kSlots; ++u) {
+        const size_t at = (size_t)t * a.top_k + min(j0 + u, a.top_k - 1);
+        const int p = a.position[at];
+        s.in[u] = j0 + u < a.top_k && p >= 0 && p < a.capacity;
+        s.p[u] = s.in[u] ? p : 0;
+        s.w[u] = a.weight[at];
+    }
+    return s;
+}
+
 // One thread per token and eight columns.
 template <int DT>
 __global__ __launch_bounds__(256) void combine(CombineArgs a) {
@@ -58,18 +79,18 @@ __global__ __launch_bounds__(256) void combine(CombineArgs a) {
         const int c = ((int)(u - (int64_t)t * pieces) * 256 + (int)threadIdx.x) * 8, left = a.cols - c;
         if (left <= 0) continue;
         float sum[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-        const int* pos = a.position + (size_t)t * a.top_k;
-        const float* w = a.weight + (size_t)t * a.top_k;
-#pragma unroll 4
-        for (int j = 0; j < a.top_k; ++j) {
-            const int p = pos[j];
-            if (p < 0 || p >= a.capacity) continue;
-            float y[8];
-            load8<DT>(y, static_cast<const T*>(a.Y) + (size_t)p * (size_t)a.ldy + c, left);
-            const float x = w[j];
+        if (a.capacity > 0)
+            for (int j0 = 0; j0 < a.top_k; j0 += kSlots) {
+                const Slots s = slots_of(a, t, j0);
+                typename Elem<DT>::type raw[kSlots][8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) sum[e] = fmaf(x, y[e], sum[e]);
-        }
+                for (int v = 0; v < kSlots; ++v)
+                    load8_raw<DT>(raw[v], static_cast<const T*>(a.Y) + (size_t)s.p[v] * (size_t)a.ldy + c, left);
+#pragma unroll
+                for (int v = 0; v < kSlots; ++v)
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) sum[e] = s.in[v] ? fmaf(s.w[v], decode<DT>(raw[v][e]), sum[e]) : sum[e];
+            }
         store8<DT>(static_cast<T*>(a.out) + (size_t)t * (size_t)a.ldo + c, sum, left);
     }
 }
@@ -79,7 +100,7 @@ __global__ __launch_bounds__(256) void combine(CombineArgs a) {
 template <int DT>
 __global__ __launch_bounds__(256) void combine_backward(CombineArgs a, int workers) {
     typedef typename Elem<DT>::type T;
-    __shared__ float dots[kMaxTopK][4];
+    __shared__ float dots[kSlots][4];
     const int tid = threadIdx.x;
     T* yg = static_cast<T*>(a.y_grad);
     if ((int)blockIdx.x >= workers) {
@@ -93,30 +114,42 @@ __global__ __launch_bounds__(256) void combine_backward(CombineArgs a, int worke
     }
     for (int t = blockIdx.x; t < a.tokens; t += workers) {
         const T* g = static_cast<const T*>(a.G) + (size_t)t * (size_t)a.ldg;
-        for (int j = 0; j < a.top_k; ++j) {
-            const int p = a.position[(size_t)t * a.top_k + j];
-            float dot = 0;
-            if (p >= 0 && p < a.capacity) {
-                const float w = a.weight[(size_t)t * a.top_k + j];
-                const T* y = static_cast<const T*>(a.Y) + (size_t)p * (size_t)a.ldy;
-                for (int c = tid * 8; c < a.cols; c += 2048) {
-                    float gv[8], yv[8];
-                    load8<DT>(gv, g + c, a.cols - c);
-                    load8<DT>(yv, y + c, a.cols - c);
-    #pragma unroll
-                    for (int e = 0; e < 8; ++e) dot = fmaf(gv[e], yv[e], dot);
-    #pragma unroll
-                    for (int e = 0; e < 8; ++e) gv[e] *= w;
-                    store8<DT>(yg + (size_t)p * (size_t)a.ldyg + c, gv, a.cols - c);
+        for (int j0 = 0; j0 < a.top_k; j0 += kSlots) {
+            const Slots s = slots_of(a, t, j0);
+            float dot[kSlots] = {0, 0, 0, 0, 0, 0, 0, 0};
+            for (int c = tid * 8; c < a.cols; c += 2048) {
+                const int left = a.cols - c;
+                T raw[kSlots][8], graw[8];
+                load8_raw<DT>(graw, g + c, left);
+                if (a.capacity > 0)
+#pragma unroll
+                    for (int v = 0; v < kSlots; ++v)
+                        load8_raw<DT>(raw[v], static_cast<const T*>(a.Y) + (size_t)s.p[v] * (size_t)a.ldy + c, left);
+#pragma unroll
+                for (int v = 0; v < kSlots; ++v) {
+                    if (!s.in[v]) continue;
+                    float out[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const float x = decode<DT>(graw[e]);
+                        dot[v] = fmaf(x, decode<DT>(raw[v][e]), dot[v]);
+                        out[e] = x * s.w[v];
+                    }
+                    store8<DT>(yg + (size_t)s.p[v] * (size_t)a.ldyg + c, out, left);
                 }
             }
-    #pragma unroll
-            for (int d = 32; d; d >>= 1) dot += __shfl_xor(dot, d);
-            if ((tid & 63) == 0) dots[j][tid >> 6] = dot;
+#pragma unroll
+            for (int v = 0; v < kSlots; ++v) {
+#pragma unroll
+                for (int d = 32; d; d >>= 1) dot[v] += __shfl_xor(dot[v], d);
+                if ((tid & 63) == 0) dots[v][tid >> 6] = dot[v];
+            }
+            __syncthreads();
+            if (tid < kSlots && j0 + tid < a.top_k)
+                a.weight_grad[(size_t)t * a.top_k + j0 + tid] =
+                    (dots[tid][0] + dots[tid][1]) + (dots[tid][2] + dots[tid][3]);
+            __syncthreads();
         }
-        __syncthreads();
-        if (tid < a.top_k) a.weight_grad[(size_t)t * a.top_k + tid] = (dots[tid][0] + dots[tid][1]) + (dots[tid][2] + dots[tid][3]);
-        __syncthreads();
     }
 }
 

@@ -9,9 +9,9 @@
 namespace dg {
 
 constexpr int kBlock = 128;          // elements of k (or of a row) that share a scale
-constexpr int kMaxExperts = 1024;    // routing: 16 experts per lane of a wave
+constexpr int kMaxExperts = 1024;    // routing: 16 experts for each lane of a wave
 constexpr int kMaxTopK = 32;
-constexpr int kDispatchChunk = 1024; // (token, slot) pairs per workgroup of the dispatch
+constexpr int kDispatchChunk = 4096; // (token, slot) pairs per workgroup of the dispatch
 
 enum BlockMode { BLOCK_PLAIN = 0, BLOCK_EXPERTS = 1, BLOCK_GRADIENT = 2 };
 
@@ -82,6 +82,7 @@ struct RouteArgs {
     int tokens, experts, top_k;
     int score, groups, top_groups, group_top, renorm;
     float factor;
+    int group_lanes;           // lanes that hold a group, 0 where groups cut lanes (set by the launcher)
     const float* bias;
     int* index;
     float* weight;

@@ -123,7 +123,7 @@ def test_capacity_and_workspace():
     assert f(0, 4, 8, 128) == 0 and f(1, 1, 8, 128) == 128 and f(16, 4, 64, 1) == 64
     assert f(4096, 8, 64, 128) == (32768 + 64 * 127 + 127) // 128 * 128
     assert lib().gemm_experts_dispatch_workspace(16, 4, 64) == 0
-    assert lib().gemm_experts_dispatch_workspace(1024, 2, 64) == 2 * 64 * 4
+    assert lib().gemm_experts_dispatch_workspace(4096, 2, 64) == 2 * 64 * 4
     assert lib().gemm_block_product_workspace(0, 4, 4) == 0 and lib().gemm_block_product_workspace(-1, 4, 4) == 0
 
 
