@@ -182,10 +182,15 @@ int tr_of(const gemm_block_matrix& A, const gemm_block_matrix& B) {
     return (A.op == GEMM_OP_T ? 2 : 0) | (B.op == GEMM_OP_T ? 1 : 0);
 }
 
+// Whether the 256 x 256 tiles exist for a call: C of 16 bits, byte offsets within a matrix of 32 bits.
+bool wide_call(const gemm_block_matrix& A, const gemm_block_matrix& B, int out_dtype) {
+    return out_dtype != GEMM_F32 && A.rows * A.ld < ((int64_t)1 << 32) && B.rows * B.ld < ((int64_t)1 << 32);
+}
+
 constexpr int64_t kCus = 256;
 
 // rows: rows of C that share a B (for experts the average); n_products: B's in the call;
-// wide: the 256 x 256 tiles exist for the call (C of 16 bits, a scale for 128 rows of B);
+// wide: the 256 x 256 tiles exist for the call (C of 16 bits);
 // may_split: whether K may be split.
 dg::BlockPlan block_plan(int64_t rows, int64_t n_products, int64_t N, int64_t K, bool direct, bool wide, int tr,
                          bool may_split) {
@@ -436,7 +441,7 @@ int gemm_block_product(const gemm_block_matrix* A, const gemm_block_matrix* B, v
                           scale_range("B.scale", *B)}));
     DG_TRY(check_device());
     const bool direct = direct_rows(*A, 1) && direct_rows(*B, 1);
-    const bool wide = B->block_rows != 1 && out_dtype != GEMM_F32;
+    const bool wide = wide_call(*A, *B, out_dtype);
     dg::BlockPlan p = block_plan(M, 1, N, K, direct, wide, tr_of(*A, *B), true);
     if (split_bytes(p.split, M, N) > workspace_bytes) p = block_plan(M, 1, N, K, direct, wide, tr_of(*A, *B), false);
     dg::BlockArgs a = block_args(*A, *B, C, ldc, out_dtype);
@@ -617,7 +622,7 @@ int gemm_experts_product(const gemm_block_matrix* A, const gemm_block_matrix* B,
     const bool direct = direct_rows(*A, 1) && direct_rows(*B, E);
     const int64_t pairs = plan->tokens * plan->top_k, active = std::max<int64_t>(1, std::min(E, pairs));
     const dg::BlockPlan p = block_plan(std::max<int64_t>(1, pairs / active), active, N, A->cols, direct,
-                                       B->block_rows != 1 && out_dtype != GEMM_F32, tr_of(*A, *B), false);
+                                       wide_call(*A, *B, out_dtype), tr_of(*A, *B), false);
     dg::BlockArgs a = block_args(*A, *B, C, ldc, out_dtype);
     a.mode = dg::BLOCK_EXPERTS;
     a.M = (int)P;
@@ -657,7 +662,7 @@ int gemm_experts_gradient(const gemm_block_matrix* A, const gemm_block_matrix* B
                           scale_range("B.scale", *B), range("plan.offsets", plan->offsets, (uint64_t)(E + 1) * 4)}));
     DG_TRY(check_device());
     const bool direct = direct_rows(*A, 1) && direct_rows(*B, 1);
-    const dg::BlockPlan p = block_plan(M, E, N, A->cols, direct, B->block_rows != 1 && out_dtype != GEMM_F32, tr_of(*A, *B), false);
+    const dg::BlockPlan p = block_plan(M, E, N, A->cols, direct, wide_call(*A, *B, out_dtype), tr_of(*A, *B), false);
     dg::BlockArgs a = block_args(*A, *B, C, ldc, out_dtype);
     a.mode = dg::BLOCK_GRADIENT;
     a.E = (int)E;

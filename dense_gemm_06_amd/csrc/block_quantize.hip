@@ -28,18 +28,15 @@ __device__ __forceinline__ uint32_t encode4(float a, float b, float c, float d, 
     return (uint32_t)r;
 }
 
-// Eight elements of a row from p, of which `valid` lie inside it (the rest zero).
-template <int DT>
-__device__ __forceinline__ void load8(float (&v)[8], const typename Elem<DT>::type* p, int valid) {
-    typename Elem<DT>::type raw[8];
+// Eight elements of a row from p, of which `valid` (> 0) lie inside it (the rest zero).
+template <typename T>
+__device__ __forceinline__ void load8(T (&raw)[8], const T* p, int valid) {
     if (valid >= 8) {
         __builtin_memcpy(raw, p, sizeof raw);
     } else {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) raw[e] = e < valid ? p[e] : typename Elem<DT>::type(0);
+        for (int e = 0; e < 8; ++e) raw[e] = e < valid ? p[e] : T(0);
     }
-#pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = decode<DT>(raw[e]);
 }
 
 // One workgroup: a 128 x 128 block of X in registers, thread (rg, cg) holding rows
@@ -58,15 +55,24 @@ __global__ __launch_bounds__(256) void block_quantize(QuantArgs a) {
     const int left = a.cols - c0;
     const T* X = static_cast<const T*>(a.X);
 
-    float v[8][8];
+    // every load is issued before the first is used: rows outside the matrix read row 0 and
+    // become zeros
+    T raw[8][8];
+    bool in[8];
 #pragma unroll
     for (int p = 0; p < 8; ++p) {
         int r = r0 + p;
-        bool in = r < a.rows;
-        if (in && a.gather) r = a.gather[r];
-        in = in && r >= 0 && r < a.x_rows;
-        load8<DT>(v[p], X + (size_t)(in ? r : 0) * (size_t)a.ldx + c0, in ? left : 0);
+        in[p] = r < a.rows;
+        if (a.gather) r = a.gather[min(r, a.rows - 1)];
+        in[p] = in[p] && r >= 0 && r < a.x_rows && left > 0;
+        if (a.x_rows > 0)  // there is a row 0
+            load8<T>(raw[p], X + (size_t)(in[p] ? r : 0) * (size_t)a.ldx + (left > 0 ? c0 : 0), left > 0 ? left : a.cols);
     }
+    float v[8][8];
+#pragma unroll
+    for (int p = 0; p < 8; ++p)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[p][e] = in[p] ? decode<DT>(raw[p][e]) : 0.0f;
     uint32_t rmax[8], cmax[8];
 #pragma unroll
     for (int p = 0; p < 8; ++p) rmax[p] = cmax[p] = kAmaxFloor;

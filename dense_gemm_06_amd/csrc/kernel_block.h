@@ -25,6 +25,8 @@
 // The order of k inside a fragment is free as long as both operands share it: the lanes
 // with the same row take 16-byte chunks in whichever order is cheapest to read.
 #pragma once
+#include <type_traits>
+
 #include "device_common.h"
 #include "experts.h"
 #include "lds_layout.h"
@@ -156,6 +158,7 @@ __device__ __forceinline__ bool block_tile_of(BlockArgs& g, BlockTile& t) {
     if (g.mode == BLOCK_EXPERTS) {
         if (!expert_tile<BM>(g, t)) return false;
         t.n0 *= BN;
+        if (t.m0 >= t.m_live || g.a_rows == 0) t.nkb = 0;  // nothing but padding: zeros, and nothing is read
         g.B += (size_t)t.expert * (size_t)g.stride_b;
         g.SB += (size_t)t.expert * (size_t)g.stride_sb;
         return true;
@@ -213,6 +216,21 @@ __device__ __forceinline__ void block_store4(const BlockArgs& g, int m, int n, f
         if (n + e < g.N) store_out(g.C, g.out_dt, at + e, v[e]);
 }
 
+// The same out of line, for unrolled loops: inlined there, its branches on types and edges
+// made 1300 blocks of code.
+__device__ __attribute__((noinline)) void block_store4_call(void* C, int64_t ldc, int N, int out_dt, int m, int n,
+                                                            f32x4 v) {
+    const size_t at = (size_t)m * (size_t)ldc + n;
+    const int dt = (int)uni32((uint32_t)out_dt);
+    if (n + 4 <= N) {
+        store_out4(C, dt, at, v);
+        return;
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+        if (n + e < N) store_out(C, dt, at + e, v[e]);
+}
+
 // Zeros in the rows past the last expert's, spread over the whole grid.
 __device__ __forceinline__ void clear_tail(const BlockArgs& g) {
     const int first = min(max(g.offsets[g.E], 0), g.M);
@@ -238,6 +256,213 @@ __device__ __forceinline__ u32x4 load_codes(const uint8_t* p, int valid) {
     return v;
 }
 
+// ---------------------------------------------------------------------------- wide tiles
+// 256 x 256 tiles for C of 16 bits and 16-byte aligned rows: eight waves of 128 x 64, each 8
+// x 4 tiles of v_mfma_f32_16x16x128_f8f6f4, whose one instruction is one block of k. The
+// accumulators (128 registers) have to be ordinary ones, as the scaled additions are done by
+// the vector unit, which rules out larger wave tiles; with 32 x 32 instructions the parts and
+// fragments in flight spilled.
+//
+// A wave keeps the block's 4 fragments of B, reads the 8 of A one ahead of their use, and
+// adds a row of parts while the matrix core computes the next. LDS holds two stages of a
+// block (layout as below; lane (l16, lg) takes chunks lg and lg + 4 of its row, so that the
+// phases of a read see two chunks that differ in the lowest bit and cover all banks). Before
+// the last fragment row of a block its reads are done: the barrier there publishes the next
+// block, the freed stage is refilled with the one after it, and the next block's fragments
+// replace those of B behind their last use.
+template <int TA, int TB, bool BROW>
+__global__ __launch_bounds__(512) void block_wide(BlockArgs g) {
+    constexpr int BM = 256, BN = 256, NW = 8, FM = 8, FN = 4;
+    constexpr int STAGE = BM * kBlock, STAGE_S = (BM + BN) * 4, ROW = 68;
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[4 * STAGE + 2 * STAGE_S];
+    uint8_t* const sA = lds;
+    uint8_t* const sB = lds + 2 * STAGE;
+    float* const fS = reinterpret_cast<float*>(lds + 4 * STAGE);
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wm = wave >> 2, wn = wave & 3;
+    const int l16 = lane & 15, lg = lane >> 4;
+
+    BlockTile t;
+    const bool any = block_tile_of<BM, BN>(g, t);
+    if (g.mode == BLOCK_EXPERTS) clear_tail(g);
+    if (!any) return;
+
+    // ---- sources: lane's chunk of copy c is row (4 wave + c)*8 + lane/8, 16-byte chunk
+    // (lane & 7) ^ ((row >> 1) & 7); 32-bit offsets from the block's first byte (the host
+    // takes this kernel where they suffice)
+    const uint8_t* ba = g.A + (size_t)t.kb0 * kBlock;
+    const uint8_t* bb = g.B + (size_t)t.kb0 * kBlock;
+    uint32_t oa[4], ob[4];
+    int kc[2];
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+        const int row = (wave * 4 + c) * 8 + (lane >> 3);
+        const int k = ((lane & 7) ^ ((row >> 1) & 7)) * 16;
+        kc[c & 1] = k;  // the same for c and c + 2
+        const int r = max(block_a_row(g, t, min(t.m0 + row, t.m_end - 1)), 0);
+        oa[c] = (uint32_t)r * (uint32_t)g.lda + (uint32_t)k;
+        ob[c] = (uint32_t)min(t.n0 + row, g.N - 1) * (uint32_t)g.ldb + (uint32_t)k;
+    }
+    const float* ps;
+    int64_t ps_step;
+    if (wave < 4) {
+        const int r = max(block_a_row(g, t, min(t.m0 + wave * 64 + lane, t.m_end - 1)), 0);
+        ps = g.SA + (size_t)(r >> g.a_shift) * (size_t)g.sa_row + (size_t)t.kb0 * (size_t)g.sa_blk;
+        ps_step = g.sa_blk;
+    } else {
+        const int n = min(t.n0 + (wave - 4) * 64 + lane, g.N - 1);
+        ps = g.SB + (size_t)(n >> g.b_shift) * (size_t)g.sb_row + (size_t)t.kb0 * (size_t)g.sb_blk;
+        ps_step = g.sb_blk;
+    }
+    const uint32_t dA = (uint32_t)reinterpret_cast<uintptr_t>(DG_LDSV(sA)) + (uint32_t)wave * 4096u;
+    const uint32_t dB = (uint32_t)reinterpret_cast<uintptr_t>(DG_LDSV(sB)) + (uint32_t)wave * 4096u;
+    const uint32_t dS = (uint32_t)reinterpret_cast<uintptr_t>(DG_LDSV(fS)) + (uint32_t)wave * 256u;
+    auto issue = [&](int kb) {
+        const uint32_t st = (uint32_t)(kb & 1);
+        __builtin_amdgcn_global_load_lds(DG_GLB(ps), DG_LDS_ADDR(dS + st * STAGE_S), 4, 0, 0);
+        ps += ps_step;
+        if (kb < t.nkb - 1 || t.krem == kBlock) {
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                __builtin_amdgcn_global_load_lds(DG_GLB(ba + oa[c]), DG_LDS_ADDR(dA + st * STAGE + c * 1024u), 16, 0, 0);
+                __builtin_amdgcn_global_load_lds(DG_GLB(bb + ob[c]), DG_LDS_ADDR(dB + st * STAGE + c * 1024u), 16, 0, 0);
+            }
+        } else {
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                const bool in = kc[c & 1] < t.krem;
+                const void* a = in ? static_cast<const void*>(ba + oa[c]) : block_zeros;
+                const void* b = in ? static_cast<const void*>(bb + ob[c]) : block_zeros;
+                __builtin_amdgcn_global_load_lds(DG_GLB(a), DG_LDS_ADDR(dA + st * STAGE + c * 1024u), 16, 0, 0);
+                __builtin_amdgcn_global_load_lds(DG_GLB(b), DG_LDS_ADDR(dB + st * STAGE + c * 1024u), 16, 0, 0);
+            }
+        }
+        ba += kBlock;
+        bb += kBlock;
+    };
+    auto published = [&]() {  // this wave's copies have landed, and after the barrier everybody's
+        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+    };
+
+    const int off = l16 * kBlock + ((lg ^ ((l16 >> 1) & 7)) << 4);
+    auto frag = [&](const uint8_t* base) {
+        const u32x4 x = *reinterpret_cast<const u32x4*>(base + off);
+        const u32x4 y = *reinterpret_cast<const u32x4*>(base + (off ^ 64));
+        return i32x8{(int)x[0], (int)x[1], (int)x[2], (int)x[3], (int)y[0], (int)y[1], (int)y[2], (int)y[3]};
+    };
+    const uint8_t* const aw = sA + wm * 128 * kBlock;
+    const uint8_t* const bw = sB + wn * 64 * kBlock;
+    const float* const fa = fS + wm * 128 + l16;
+    const float* const fb = fS + BM + wn * 64;
+
+    f32x4 acc[FM][FN];
+#pragma unroll
+    for (int i = 0; i < FM; ++i)
+#pragma unroll
+        for (int j = 0; j < FN; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
+    const bool mine = t.m0 + wm * 128 < t.m_end;  // this wave has rows of C
+
+    i32x8 bf[FN], af[2];
+    f32x4 part[2][FN], sb[BROW ? FN : 1];
+    float sa[4];
+    auto read_sb = [&](int st) {
+        const float* f = fb + st * (BM + BN);
+        if constexpr (BROW) {
+#pragma unroll
+            for (int j = 0; j < FN; ++j) sb[j] = *reinterpret_cast<const f32x4*>(f + j * 16 + lg * 4);
+        } else {
+            sb[0][0] = f[0];
+        }
+    };
+    auto add = [&](int i) {  // the scaled parts of fragment row i
+        const float s = sa[i & 3];
+#pragma unroll
+        for (int j = 0; j < FN; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                acc[i][j][e] = fmaf(part[i & 1][j][e], BROW ? s * sb[BROW ? j : 0][e] : s * sb[0][0], acc[i][j][e]);
+    };
+
+    if (t.nkb > 0) {
+        issue(0);
+        published();
+        if (t.nkb > 1) issue(1);
+        if (mine) {
+#pragma unroll
+            for (int j = 0; j < FN; ++j) bf[j] = frag(bw + j * 16 * kBlock);
+            af[0] = frag(aw);
+            sa[0] = fa[0];
+            read_sb(0);
+        }
+    }
+    for (int kb = 0; kb < t.nkb; ++kb) {
+        const int st = kb & 1, next = st ^ 1;
+        if (mine) {
+#pragma unroll
+            for (int i = 0; i < FM - 1; ++i) {
+                // the next fragment is read behind the first instruction that uses this one, and
+                // pinned there: the compiler waits for all LDS reads in flight where it waits
+                // for one, so reads issued before that wait would be waited for at once, and
+                // left to itself it puts them at the end, too late to hide their latency
+                part[i & 1][0] = mfma_16<TB, TA>(bf[0], af[i & 1], f32x4{0, 0, 0, 0});
+                __builtin_amdgcn_sched_barrier(0);
+                af[(i + 1) & 1] = frag(aw + st * STAGE + (i + 1) * 16 * kBlock);
+                sa[(i + 1) & 3] = fa[st * (BM + BN) + (i + 1) * 16];
+                __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                for (int j = 1; j < FN; ++j) part[i & 1][j] = mfma_16<TB, TA>(bf[j], af[i & 1], f32x4{0, 0, 0, 0});
+                if (i > 0) add(i - 1);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        }
+        if (kb + 1 < t.nkb) {
+            published();
+            if (kb + 2 < t.nkb) issue(kb + 2);
+        }
+        if (mine) {
+            // past the end of k these reads find old data, which nothing uses
+#pragma unroll
+            for (int j = 0; j < FN; ++j) {
+                part[1][j] = mfma_16<TB, TA>(bf[j], af[1], f32x4{0, 0, 0, 0});
+                bf[j] = frag(bw + next * STAGE + j * 16 * kBlock);
+            }
+            af[0] = frag(aw + next * STAGE);
+            add(FM - 2);
+            const float first = fa[next * (BM + BN)];
+            add(FM - 1);
+            sa[0] = first;
+            read_sb(next);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    }
+
+    // ---- C through LDS, 16 rows of the wave's 64 columns at a time
+    __builtin_amdgcn_s_barrier();  // every wave has read its last fragments
+    asm volatile("" ::: "memory");
+    if (!mine) return;
+    float* const stage = reinterpret_cast<float*>(lds) + wave * (16 * ROW);
+    const int n = t.n0 + wn * 64 + l16 * 4;
+#pragma unroll
+    for (int i = 0; i < FM; ++i) {
+#pragma unroll
+        for (int j = 0; j < FN; ++j) *reinterpret_cast<f32x4*>(stage + l16 * ROW + j * 16 + lg * 4) = acc[i][j];
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+#pragma unroll
+        for (int p = 0; p < 4; ++p) {
+            const int row = p * 4 + lg, m = t.m0 + wm * 128 + i * 16 + row;
+            f32x4 v = *reinterpret_cast<const f32x4*>(stage + row * ROW + l16 * 4);
+            if (m >= t.m_end || n >= g.N) continue;
+            if (t.bad) v = f32x4{1, 1, 1, 1} * __builtin_nanf("");
+            else if (g.mode == BLOCK_EXPERTS && block_a_row(g, t, m) < 0) v = f32x4{0, 0, 0, 0};
+            block_store4_call(g.C, g.ldc, g.N, g.out_dt, m, n, v);
+        }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    }
+}
+
 // ---------------------------------------------------------------------------- tiles
 // BM x BN tiles on WM x WN waves, each wave SM x SJ subtiles of 32 x 32. LDS holds two
 // stages of one block of k: rows of 128 bytes whose 16-byte chunks are permuted by
@@ -257,9 +482,14 @@ __global__ __launch_bounds__(WM* WN * 64) void block_tile(BlockArgs g) {
     static_assert((BM + BN) / 64 == NW, "each wave copies 64 scales of a stage");
     constexpr bool TRB = (TR & 1) != 0, TRA = (TR & 2) != 0;
     static_assert(TR == 0 || (BM == kBlock && BN == kBlock), "a transposed stage has rows of 128 bytes");
-    __shared__ __attribute__((aligned(1024))) uint8_t sA[2][BM * kBlock];
-    __shared__ __attribute__((aligned(1024))) uint8_t sB[2][BN * kBlock];
-    __shared__ __attribute__((aligned(1024))) float fS[2][BM + BN];
+    // two stages of A, of B and of their scales; after the k loop each wave's part of C
+    constexpr int STAGE_A = BM * kBlock, STAGE_B = BN * kBlock, STAGE_S = (BM + BN) * 4;
+    constexpr int ROW = SJ * 32 + 4;  // floats of a staged row of C: 16 rows start in 16 different places of the banks
+    static_assert(NW * 32 * ROW * 4 <= 2 * (STAGE_A + STAGE_B), "C is staged where A and B were");
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * (STAGE_A + STAGE_B + STAGE_S)];
+    uint8_t* const sA = lds;
+    uint8_t* const sB = lds + 2 * STAGE_A;
+    float* const fS = reinterpret_cast<float*>(lds + 2 * (STAGE_A + STAGE_B));
 
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -270,7 +500,6 @@ __global__ __launch_bounds__(WM* WN * 64) void block_tile(BlockArgs g) {
     const bool any = block_tile_of<BM, BN>(g, t);
     if (g.mode == BLOCK_EXPERTS) clear_tail(g);
     if (!any) return;
-    if (t.m0 >= t.m_live) t.nkb = 0;  // nothing but padding: zeros
 
     // ---- sources of this lane's copies: chunk positions lane & 7 of 8 rows. ka, kb: the k
     // of a chunk within the block; va, vb: the bytes of a transposed chunk inside the matrix
@@ -319,27 +548,27 @@ __global__ __launch_bounds__(WM* WN * 64) void block_tile(BlockArgs g) {
     }
     // LDS destinations as plain numbers: the compiler then does not make every LDS read
     // wait for all copies in flight; the explicit waits below order them.
-    const uint32_t dA = (uint32_t)reinterpret_cast<uintptr_t>(DG_LDSV(&sA[0][0])) + (uint32_t)wave * (CA * 1024u);
-    const uint32_t dB = (uint32_t)reinterpret_cast<uintptr_t>(DG_LDSV(&sB[0][0])) + (uint32_t)wave * (CB * 1024u);
-    const uint32_t dS = (uint32_t)reinterpret_cast<uintptr_t>(DG_LDSV(&fS[0][0])) + (uint32_t)wave * 256u;
+    const uint32_t dA = (uint32_t)reinterpret_cast<uintptr_t>(DG_LDSV(sA)) + (uint32_t)wave * (CA * 1024u);
+    const uint32_t dB = (uint32_t)reinterpret_cast<uintptr_t>(DG_LDSV(sB)) + (uint32_t)wave * (CB * 1024u);
+    const uint32_t dS = (uint32_t)reinterpret_cast<uintptr_t>(DG_LDSV(fS)) + (uint32_t)wave * 256u;
 
     u32x4 ra[DIRECT ? 1 : CA], rb[DIRECT ? 1 : CB];
     auto issue = [&](int kb) {
         const uint32_t st = (uint32_t)(kb & 1);
         const int rem = kb == t.nkb - 1 ? t.krem : kBlock;
-        __builtin_amdgcn_global_load_lds(DG_GLB(ps + (size_t)kb * (size_t)ps_step), DG_LDS_ADDR(dS + st * ((BM + BN) * 4u)), 4, 0, 0);
+        __builtin_amdgcn_global_load_lds(DG_GLB(ps + (size_t)kb * (size_t)ps_step), DG_LDS_ADDR(dS + st * STAGE_S), 4, 0, 0);
         if constexpr (DIRECT) {
 #pragma unroll
             for (int i = 0; i < CA; ++i) {
                 const void* src = pa[i] + (size_t)kb * step_a;
                 if (ka[i] >= rem || (TRA && va[TRA ? i : 0] <= 0)) src = block_zeros;
-                __builtin_amdgcn_global_load_lds(DG_GLB(src), DG_LDS_ADDR(dA + st * (BM * kBlock) + i * 1024u), 16, 0, 0);
+                __builtin_amdgcn_global_load_lds(DG_GLB(src), DG_LDS_ADDR(dA + st * STAGE_A + i * 1024u), 16, 0, 0);
             }
 #pragma unroll
             for (int i = 0; i < CB; ++i) {
                 const void* src = pb[i] + (size_t)kb * step_b;
                 if (kc[i] >= rem || (TRB && vb[TRB ? i : 0] <= 0)) src = block_zeros;
-                __builtin_amdgcn_global_load_lds(DG_GLB(src), DG_LDS_ADDR(dB + st * (BN * kBlock) + i * 1024u), 16, 0, 0);
+                __builtin_amdgcn_global_load_lds(DG_GLB(src), DG_LDS_ADDR(dB + st * STAGE_B + i * 1024u), 16, 0, 0);
             }
         } else {
 #pragma unroll
@@ -352,8 +581,8 @@ __global__ __launch_bounds__(WM* WN * 64) void block_tile(BlockArgs g) {
     };
     auto settle = [&](int kb) {  // registers to LDS
         if constexpr (!DIRECT) {
-            uint8_t* a = &sA[kb & 1][wave * (CA * 1024) + lane * 16];
-            uint8_t* b = &sB[kb & 1][wave * (CB * 1024) + lane * 16];
+            uint8_t* a = sA + (kb & 1) * STAGE_A + wave * (CA * 1024) + lane * 16;
+            uint8_t* b = sB + (kb & 1) * STAGE_B + wave * (CB * 1024) + lane * 16;
 #pragma unroll
             for (int i = 0; i < CA; ++i) *reinterpret_cast<u32x4*>(a + i * 1024) = ra[i];
 #pragma unroll
@@ -388,12 +617,12 @@ __global__ __launch_bounds__(WM* WN * 64) void block_tile(BlockArgs g) {
         return r;
     };
     auto a_frag = [&](int st, int i, int h) {
-        if constexpr (TRA) return frag_tr(sA[st], wm * SM + i, h);
-        else return frag(&sA[st][(wm * SM + i) * 32 * kBlock], h);
+        if constexpr (TRA) return frag_tr(sA + st * STAGE_A, wm * SM + i, h);
+        else return frag(sA + st * STAGE_A + (wm * SM + i) * 32 * kBlock, h);
     };
     auto b_frag = [&](int st, int j, int h) {
-        if constexpr (TRB) return frag_tr(sB[st], wn * SJ + j, h);
-        else return frag(&sB[st][(wn * SJ + j) * 32 * kBlock], h);
+        if constexpr (TRB) return frag_tr(sB + st * STAGE_B, wn * SJ + j, h);
+        else return frag(sB + st * STAGE_B + (wn * SJ + j) * 32 * kBlock, h);
     };
 
     f32x16 acc[SM][SJ];
@@ -401,6 +630,10 @@ __global__ __launch_bounds__(WM* WN * 64) void block_tile(BlockArgs g) {
     for (int i = 0; i < SM; ++i)
 #pragma unroll
         for (int j = 0; j < SJ; ++j) acc[i][j] = f32x16{0};
+
+    // subtiles of 32 rows of this wave that hold rows of C: an expert's last tile, or a
+    // matrix's, does not multiply what lies past its rows
+    const int subs = min(max((t.m_end - t.m0 + 31) / 32 - wm * SM, 0), SM);
 
     if (t.nkb > 0) {
         issue(0);
@@ -414,8 +647,8 @@ __global__ __launch_bounds__(WM* WN * 64) void block_tile(BlockArgs g) {
         __builtin_amdgcn_s_barrier();
         asm volatile("" ::: "memory");
         if (kb + 1 < t.nkb) issue(kb + 1);
-        const float* fa = &fS[st][wm * SM * 32 + l32];
-        const float* fb = &fS[st][BM + wn * SJ * 32];
+        const float* fa = fS + st * (BM + BN) + wm * SM * 32 + l32;
+        const float* fb = fS + st * (BM + BN) + BM + wn * SJ * 32;
         f32x4 sb[SJ][BROW ? 4 : 1];
 #pragma unroll
         for (int j = 0; j < SJ; ++j) {
@@ -437,68 +670,89 @@ __global__ __launch_bounds__(WM* WN * 64) void block_tile(BlockArgs g) {
                 for (int r = 0; r < 16; ++r) acc[i][j][r] = fmaf(part[r], s, acc[i][j][r]);
             }
         };
-        if constexpr (!FULL) {
-            i32x8 bf[SJ][2];
-#pragma unroll
-            for (int j = 0; j < SJ; ++j)
-#pragma unroll
-                for (int h = 0; h < 2; ++h) bf[j][h] = b_frag(st, j, h);
-#pragma unroll
-            for (int i = 0; i < SM; ++i) {
-                const i32x8 af0 = a_frag(st, i, 0), af1 = a_frag(st, i, 1);
+        // WHOLE: all of this wave's subtiles hold rows of C (the usual case, without branches
+        // between its instructions)
+        auto block = [&](auto whole_tag) {
+            constexpr bool WHOLE = decltype(whole_tag)::value;
+            if constexpr (!FULL) {
+                i32x8 bf[SJ][2];
 #pragma unroll
                 for (int j = 0; j < SJ; ++j)
-                    add(i, j, mfma_32<TB, TA>(bf[j][1], af1, mfma_32<TB, TA>(bf[j][0], af0, f32x16{0})));
-            }
-        } else {
-            f32x16 part[SM][SJ];
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                i32x8 af[SM], bf[SJ];
+                    for (int h = 0; h < 2; ++h) bf[j][h] = b_frag(st, j, h);
 #pragma unroll
-                for (int i = 0; i < SM; ++i) af[i] = a_frag(st, i, h);
-#pragma unroll
-                for (int j = 0; j < SJ; ++j) bf[j] = b_frag(st, j, h);
-#pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                    f16x8 aw[SM], bw[SJ];
-#pragma unroll
-                    for (int i = 0; i < SM; ++i) aw[i] = widen8<TA>(af[i][2 * u], af[i][2 * u + 1]);
-#pragma unroll
-                    for (int j = 0; j < SJ; ++j) bw[j] = widen8<TB>(bf[j][2 * u], bf[j][2 * u + 1]);
-#pragma unroll
-                    for (int i = 0; i < SM; ++i)
+                for (int i = 0; i < SM; ++i) {
+                    if (WHOLE || i < subs) {
+                        const i32x8 af0 = a_frag(st, i, 0), af1 = a_frag(st, i, 1);
 #pragma unroll
                         for (int j = 0; j < SJ; ++j)
-                            part[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(
-                                bw[j], aw[i], h == 0 && u == 0 ? f32x16{0} : part[i][j], 0, 0, 0);
+                            add(i, j, mfma_32<TB, TA>(bf[j][1], af1, mfma_32<TB, TA>(bf[j][0], af0, f32x16{0})));
+                    }
                 }
+            } else {
+                f32x16 part[SM][SJ];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    i32x8 af[SM], bf[SJ];
+#pragma unroll
+                    for (int i = 0; i < SM; ++i) af[i] = a_frag(st, i, h);
+#pragma unroll
+                    for (int j = 0; j < SJ; ++j) bf[j] = b_frag(st, j, h);
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) {
+                        f16x8 aw[SM], bw[SJ];
+#pragma unroll
+                        for (int i = 0; i < SM; ++i) aw[i] = widen8<TA>(af[i][2 * u], af[i][2 * u + 1]);
+#pragma unroll
+                        for (int j = 0; j < SJ; ++j) bw[j] = widen8<TB>(bf[j][2 * u], bf[j][2 * u + 1]);
+#pragma unroll
+                        for (int i = 0; i < SM; ++i)
+#pragma unroll
+                            for (int j = 0; j < SJ; ++j)
+                                if (WHOLE || i < subs)
+                                    part[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(
+                                        bw[j], aw[i], h == 0 && u == 0 ? f32x16{0} : part[i][j], 0, 0, 0);
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < SM; ++i)
+#pragma unroll
+                    for (int j = 0; j < SJ; ++j)
+                        if (WHOLE || i < subs) add(i, j, part[i][j]);
             }
-#pragma unroll
-            for (int i = 0; i < SM; ++i)
-#pragma unroll
-                for (int j = 0; j < SJ; ++j) add(i, j, part[i][j]);
-        }
+        };
+        if (subs == SM) block(std::true_type{});
+        else if (subs > 0) block(std::false_type{});
         if (kb + 1 < t.nkb) settle(kb + 1);
     }
 
-    // ---- C: lane l32 holds row m, register quad q the columns 8q + 4lh .. +3
+    // ---- C: a lane's accumulators are row l32 and four-column runs 8q + 4lh; through LDS, 32
+    // rows at a time, each store instruction then writes whole rows of the wave's columns
+    __builtin_amdgcn_s_barrier();  // every wave has read its last fragments
+    asm volatile("" ::: "memory");
+    float* const stage = reinterpret_cast<float*>(lds) + wave * (32 * ROW);
+    constexpr int LANES = SJ * 8;  // lanes to a row
+    const int n = t.n0 + wn * SJ * 32 + (lane % LANES) * 4;
 #pragma unroll
     for (int i = 0; i < SM; ++i) {
-        const int m = t.m0 + (wm * SM + i) * 32 + l32;
-        if (m >= t.m_end) continue;
-        const bool zero = block_a_row(g, t, m) < 0;
+        if (i >= subs) continue;
 #pragma unroll
         for (int j = 0; j < SJ; ++j)
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const int n = t.n0 + (wn * SJ + j) * 32 + q * 8 + lh * 4;
-                f32x4 v;
+            for (int q = 0; q < 4; ++q)
+                *reinterpret_cast<f32x4*>(stage + l32 * ROW + j * 32 + q * 8 + lh * 4) =
+                    f32x4{acc[i][j][q * 4], acc[i][j][q * 4 + 1], acc[i][j][q * 4 + 2], acc[i][j][q * 4 + 3]};
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    v[e] = t.bad ? __builtin_nanf("") : zero ? 0.0f : acc[i][j][q * 4 + e];
-                if (n < g.N) block_store4(g, m, n, v);
-            }
+        for (int p = 0; p < 32 * LANES / 64; ++p) {
+            const int row = p * (64 / LANES) + lane / LANES, m = t.m0 + (wm * SM + i) * 32 + row;
+            f32x4 v = *reinterpret_cast<const f32x4*>(stage + row * ROW + (lane % LANES) * 4);
+            if (m >= t.m_end || n >= g.N) continue;
+            if (t.bad) v = f32x4{1, 1, 1, 1} * __builtin_nanf("");
+            else if (g.mode == BLOCK_EXPERTS && block_a_row(g, t, m) < 0) v = f32x4{0, 0, 0, 0};
+            block_store4(g, m, n, v);
+        }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     }
 }
 
@@ -518,7 +772,6 @@ __global__ __launch_bounds__(512) void block_skinny(BlockArgs g) {
     const bool any = block_tile_of<BM, BN>(g, t);
     if (g.mode == BLOCK_EXPERTS) clear_tail(g);
     if (!any) return;
-    if (t.m0 >= t.m_live) t.nkb = 0;
 
     const uint8_t* pa[SM];
     const float* fa[SM];
@@ -604,7 +857,8 @@ int launch_block_full(const BlockPlan& p, const BlockArgs& a, dim3 grid, hipStre
     const bool brow = a.b_shift == 0;
     if constexpr (!FULL)
         if (p.kernel == BLOCK_TILE256)
-            return launch_status(block_tile<TA, TB, FULL, false, 256, 256, 2, 4, true>, grid, dim3(512), s, a);
+            return brow ? launch_status(block_wide<TA, TB, true>, grid, dim3(512), s, a)
+                        : launch_status(block_wide<TA, TB, false>, grid, dim3(512), s, a);
     if (p.kernel == BLOCK_TILE128) {
         if (p.direct)
             return brow ? launch_status(block_tile<TA, TB, FULL, true, 128, 128, 2, 2, true>, grid, dim3(256), s, a)

@@ -104,130 +104,155 @@ class ExpertPlan:
 
 
 # ----------------------------------------------------------------------------- checks
-def _torch():
-    import torch
-    return torch
+# A call on a few tokens takes a few microseconds on the GPU, so what is looked up for every
+# call is kept here: torch (imported with the first use) and its types' codes.
+torch = None
+_CODES, _WIDE = {}, {}
+_raw_stream = None
+
+
+def _use_torch():
+    global torch, _raw_stream
+    import torch as t
+    _CODES.update({t.float8_e4m3fn: GEMM_E4M3, t.float8_e5m2: GEMM_E5M2})
+    _WIDE.update({t.float32: _dg.GEMM_F32, t.float16: _dg.GEMM_F16, t.bfloat16: _dg.GEMM_BF16})
+    _raw_stream = getattr(t._C, "_cuda_getCurrentRawStream", None) or (
+        lambda index: t.cuda.current_stream(index).cuda_stream)
+    torch = t
 
 
 def _code_type(dtype, what):
-    torch = _torch()
-    if dtype == torch.float8_e4m3fn:
-        return GEMM_E4M3
-    if dtype == torch.float8_e5m2:
-        return GEMM_E5M2
-    raise TypeError(f"{what}: {dtype} is not float8_e4m3fn or float8_e5m2")
+    code = _CODES.get(dtype)
+    if code is None:
+        raise TypeError(f"{what}: {dtype} is not float8_e4m3fn or float8_e5m2")
+    return code
 
 
 def _wide_type(dtype, what):
-    torch = _torch()
-    if dtype == torch.bfloat16:
-        return _dg.GEMM_BF16
-    if dtype == torch.float32:
-        return _dg.GEMM_F32
-    if dtype == torch.float16:
-        return _dg.GEMM_F16
-    raise TypeError(f"{what}: {dtype} is not float32, float16 or bfloat16")
+    code = _WIDE.get(dtype)
+    if code is None:
+        raise TypeError(f"{what}: {dtype} is not float32, float16 or bfloat16")
+    return code
 
 
-def _matrix(t, what, dims=2):
-    """Leading dimension of t, whose rows have to be contiguous."""
-    if t.dim() != dims:
-        raise ValueError(f"{what} must be {dims}-D, not {tuple(t.shape)}")
-    cols = t.shape[-1]
-    if t.stride(-1) != 1 and cols > 1:
-        raise ValueError(f"{what} needs unit stride along its last dimension, not {t.stride()}")
-    if t.shape[-2] > 1 and t.stride(-2) < cols:
-        raise ValueError(f"{what}: rows overlap (strides {t.stride()})")
-    return max(t.stride(-2), cols, 1) if t.shape[-2] > 1 else max(cols, 1)
+def _ld(shape, strides, what):
+    """Leading dimension of rows that have to be contiguous: the last two dimensions of shape and strides."""
+    cols = shape[-1]
+    if strides[-1] != 1 and cols > 1:
+        raise ValueError(f"{what} needs unit stride along its last dimension, not {tuple(strides)}")
+    if shape[-2] <= 1:
+        return cols or 1
+    if strides[-2] < cols:
+        raise ValueError(f"{what}: rows overlap (strides {tuple(strides)})")
+    return strides[-2] or 1
+
+
+def _matrix(t, what):
+    """Leading dimension of a 2-D tensor with contiguous rows."""
+    shape = t.shape
+    if len(shape) != 2:
+        raise ValueError(f"{what} must be 2-D, not {tuple(shape)}")
+    return _ld(shape, t.stride(), what)
 
 
 def _array(t, what, dtype, shape):
     if t.dtype != dtype:
         raise TypeError(f"{what} must be {dtype}, not {t.dtype}")
-    if tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+    if t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{what} must be contiguous of shape {tuple(shape)}, not {tuple(t.shape)} with strides {t.stride()}")
     return t.data_ptr()
 
 
 def _device(*tensors):
-    """The tensors' common GPU."""
-    dev = tensors[0].device
+    """The index of the tensors' common GPU."""
+    at = tensors[0].get_device()
     for t in tensors:
-        if not t.is_cuda or t.device != dev:
+        if not t.is_cuda or t.get_device() != at:
             raise ValueError(f"tensors must be on one GPU, not {', '.join(str(t.device) for t in tensors)}")
-    return dev
+    return at
 
 
-def _block(b, what, batch=False):
+def _block(b, what, dims=2):
     """A BlockTensor as the library takes it."""
     if not isinstance(b, BlockTensor):
         raise TypeError(f"{what} must be a BlockTensor, not {type(b).__name__}")
     data, scale, rows = b.data, b.scale, b.block_rows
-    dims = 3 if batch else 2
-    op = _dg.GEMM_OP_N
-    if data.dim() == dims and data.stride(-1) != 1 and data.stride(-2) == 1 and min(data.shape[-2:]) > 1:
-        ld, op = _matrix(data.transpose(-1, -2), f"{what}.data", dims), _dg.GEMM_OP_T
+    code = _CODES.get(data.dtype) or _code_type(data.dtype, f"{what}.data")
+    shape, strides = data.shape, data.stride()
+    if len(shape) != dims:
+        raise ValueError(f"{what}.data must be {dims}-D, not {tuple(shape)}")
+    R, K = shape[-2], shape[-1]
+    op = 0
+    if strides[-1] == 1 and strides[-2] >= K > 0 and R > 1:
+        ld = strides[-2]
+    elif strides[-2] == 1 and strides[-1] != 1 and R > 1 and K > 1:
+        ld, op = _ld((K, R), (strides[-1], 1), f"{what}.data"), 1
     else:
-        ld = _matrix(data, f"{what}.data", dims)
-    code = _code_type(data.dtype, f"{what}.data")
-    if rows not in (1, BLOCK):
+        ld = _ld(shape, strides, f"{what}.data")
+    if rows != 1 and rows != BLOCK:
         raise ValueError(f"{what}.block_rows must be 1 or {BLOCK}, not {rows}")
-    R, K = data.shape[-2:]
-    want = (*data.shape[:-2], -(-R // rows), -(-K // BLOCK))
-    if scale.dtype != _torch().float32:
+    if scale.dtype != torch.float32:
         raise TypeError(f"{what}.scale must be float32, not {scale.dtype}")
-    if tuple(scale.shape) != want:
-        raise ValueError(f"{what}.scale must have shape {want}, not {tuple(scale.shape)}")
-    strides = scale.stride()
-    return gemm_block_matrix(data.data_ptr(), scale.data_ptr(), R, K, ld, strides[-2], strides[-1],
-                             data.stride(0) if batch else 0, strides[0] if batch else 0, code, rows, op, 0)
+    have = scale.shape
+    if len(have) != dims or have[-2] != (R + rows - 1) // rows or have[-1] != (K + 127) // 128 or (
+            dims == 3 and have[0] != shape[0]):
+        want = (*shape[:-2], -(-R // rows), -(-K // BLOCK))
+        raise ValueError(f"{what}.scale must have shape {want}, not {tuple(have)}")
+    at = scale.stride()
+    if dims == 3:
+        return gemm_block_matrix(data.data_ptr(), scale.data_ptr(), R, K, ld, at[-2], at[-1], strides[0], at[0], code,
+                                 rows, op, 0)
+    return gemm_block_matrix(data.data_ptr(), scale.data_ptr(), R, K, ld, at[-2], at[-1], 0, 0, code, rows, op, 0)
 
 
-def _plan(plan, what="plan"):
+def _plan(plan):
     """An ExpertPlan as the library takes it."""
     if not isinstance(plan, ExpertPlan):
-        raise TypeError(f"{what} must be an ExpertPlan, not {type(plan).__name__}")
-    i32 = _torch().int32
-    if plan.position.dim() != 2 or plan.counts.dim() != 1 or plan.rows.dim() != 1:
-        raise ValueError(f"{what}: position must be 2-D, counts and rows 1-D")
-    T, k = plan.position.shape
-    E, P = plan.counts.shape[0], plan.rows.shape[0]
-    return gemm_expert_plan(_array(plan.offsets, f"{what}.offsets", i32, (E + 1,)),
-                            _array(plan.counts, f"{what}.counts", i32, (E,)),
-                            _array(plan.rows, f"{what}.rows", i32, (P,)),
-                            _array(plan.position, f"{what}.position", i32, (T, k)), E, T, k, P)
+        raise TypeError(f"plan must be an ExpertPlan, not {type(plan).__name__}")
+    offsets, counts, rows, position = plan.offsets, plan.counts, plan.rows, plan.position
+    if position.dim() != 2 or counts.dim() != 1 or rows.dim() != 1:
+        raise ValueError("plan: position must be 2-D, counts and rows 1-D")
+    i32 = torch.int32
+    T, k = position.shape
+    E, P = counts.shape[0], rows.shape[0]
+    return gemm_expert_plan(_array(offsets, "plan.offsets", i32, (E + 1,)), _array(counts, "plan.counts", i32, (E,)),
+                            _array(rows, "plan.rows", i32, (P,)), _array(position, "plan.position", i32, (T, k)),
+                            E, T, k, P)
 
 
 def _call(name, device, *args):
-    """The library function on the current stream of `device`."""
-    torch = _torch()
-    fn = getattr(_dg.library(), name)
-    if device.index == torch.cuda.current_device():
-        st = fn(*args, torch.cuda.current_stream(device).cuda_stream)
+    """The library function on the current stream of GPU `device`."""
+    fn = getattr(_dg._lib or _dg.library(), name)
+    if device == torch.cuda.current_device():
+        st = fn(*args, _raw_stream(device))
     else:
         with torch.cuda.device(device):
-            st = fn(*args, torch.cuda.current_stream(device).cuda_stream)
-    _dg._check(st, name)
-
-
-def _new_block(rows, cols, dtype, block_rows, device):
-    """An empty BlockTensor, its scales laid out with the rows adjacent."""
-    torch = _torch()
-    data = torch.empty((rows, cols), dtype=dtype, device=device)
-    scale = torch.empty((-(-cols // BLOCK), -(-rows // block_rows)), dtype=torch.float32, device=device).t()
-    return BlockTensor(data, scale, block_rows)
+            st = fn(*args, _raw_stream(device))
+    if st:
+        _dg._check(st, name)
 
 
 # ----------------------------------------------------------------------------- block-scaled products
+def _new_block(rows, cols, dtype, code, block_rows, device):
+    """An empty BlockTensor, its scales laid out with the rows adjacent, and as the library takes it."""
+    data = torch.empty((rows, cols), dtype=dtype, device=device)
+    r = (rows + block_rows - 1) // block_rows
+    scale = torch.empty(((cols + 127) // 128, r), dtype=torch.float32, device=device).t()
+    return BlockTensor(data, scale, block_rows), gemm_block_matrix(
+        data.data_ptr(), scale.data_ptr(), rows, cols, cols or 1, 1, r, 0, 0, code, block_rows, 0, 0)
+
+
 def gemm_block_quantize_tensors(x, dtype, block_rows=1, natural=True, transposed=False, rows=None):
     """x (M, K) as (natural, transposed) BlockTensors of the float8 `dtype`, either None where not asked for.
 
     rows (int32, any length R): row i of the result is row rows[i] of x, zeros where rows[i] is negative
     or at least M.
     """
+    if torch is None:
+        _use_torch()
     ld = _matrix(x, "x")
     code, wide = _code_type(dtype, "dtype"), _wide_type(x.dtype, "x")
-    if block_rows not in (1, BLOCK):
+    if block_rows != 1 and block_rows != BLOCK:
         raise ValueError(f"block_rows must be 1 or {BLOCK}, not {block_rows}")
     if not natural and not transposed:
         raise ValueError("neither natural nor transposed is asked for")
@@ -235,35 +260,35 @@ def gemm_block_quantize_tensors(x, dtype, block_rows=1, natural=True, transposed
     R, gather = M, None
     if rows is not None:
         R = rows.numel()
-        gather = _array(rows, "rows", _torch().int32, (R,))
-        dev = _device(x, rows)
+        gather = _array(rows, "rows", torch.int32, (R,))
+        at = _device(x, rows)
     else:
-        dev = _device(x)
-    q = _new_block(R, K, dtype, block_rows, dev) if natural else None
-    t = _new_block(K, R, dtype, block_rows, dev) if transposed else None
+        at = _device(x)
+    dev = x.device
+    q, nat = _new_block(R, K, dtype, code, block_rows, dev) if natural else (None, None)
+    t, tr = _new_block(K, R, dtype, code, block_rows, dev) if transposed else (None, None)
     if R and K:
-        _call("gemm_block_quantize", dev, x.data_ptr(), M, K, ld, wide, gather, R,
-              ctypes.byref(_block(q, "natural")) if natural else None,
-              ctypes.byref(_block(t, "transposed")) if transposed else None)
+        _call("gemm_block_quantize", at, x.data_ptr(), M, K, ld, wide, gather, R, nat, tr)
     return q, t
 
 
 def gemm_block_product_tensors(a, b, dtype=None):
     """C (M, N) = A B^T for BlockTensors a (M, K) and b (N, K), stored as `dtype` (bfloat16 by default)."""
-    torch = _torch()
+    if torch is None:
+        _use_torch()
     dtype = dtype or torch.bfloat16
     out = _wide_type(dtype, "dtype")
     A, B = _block(a, "a"), _block(b, "b")
-    if A.cols != B.cols:
-        raise ValueError(f"shape mismatch: a {tuple(a.data.shape)}, b {tuple(b.data.shape)}")
-    dev = _device(a.data, a.scale, b.data, b.scale)
     M, N, K = A.rows, B.rows, A.cols
+    if K != B.cols:
+        raise ValueError(f"shape mismatch: a {tuple(a.data.shape)}, b {tuple(b.data.shape)}")
+    at = _device(a.data, a.scale, b.data, b.scale)
+    dev = a.data.device
     c = torch.empty((M, N), dtype=dtype, device=dev)
     if M and N:
-        n = _dg.library().gemm_block_product_workspace(M, N, K)
+        n = (_dg._lib or _dg.library()).gemm_block_product_workspace(M, N, K)
         work = torch.empty(n, dtype=torch.uint8, device=dev) if n else None
-        _call("gemm_block_product", dev, ctypes.byref(A), ctypes.byref(B), c.data_ptr(), N, out,
-              work.data_ptr() if n else None, n)
+        _call("gemm_block_product", at, A, B, c.data_ptr(), N, out, work.data_ptr() if n else None, n)
     return c
 
 
@@ -276,71 +301,79 @@ def _logits(logits, router):
 
 def gemm_experts_route_tensors(logits, router, bias=None):
     """(index, weight), int32 and float32 (T, k), of logits (T, E); bias: float32 (E), for the choice only."""
-    torch = _torch()
+    if torch is None:
+        _use_torch()
     ld, code = _logits(logits, router)
     T, E = logits.shape
+    k = max(router.top_k, 0)
+    b = None
     if bias is not None:
-        _array(bias, "bias", torch.float32, (E,))
-        dev = _device(logits, bias)
+        b = _array(bias, "bias", torch.float32, (E,))
+        at = _device(logits, bias)
     else:
-        dev = _device(logits)
-    index = torch.empty((T, max(router.top_k, 0)), dtype=torch.int32, device=dev)
-    weight = torch.empty((T, max(router.top_k, 0)), dtype=torch.float32, device=dev)
-    _call("gemm_experts_route", dev, logits.data_ptr(), T, E, ld, code, ctypes.byref(router),
-          bias.data_ptr() if bias is not None else None, index.data_ptr(), weight.data_ptr())
+        at = _device(logits)
+    dev = logits.device
+    index = torch.empty((T, k), dtype=torch.int32, device=dev)
+    weight = torch.empty((T, k), dtype=torch.float32, device=dev)
+    _call("gemm_experts_route", at, logits.data_ptr(), T, E, ld, code, router, b, index.data_ptr(), weight.data_ptr())
     return index, weight
 
 
 def gemm_experts_route_backward_tensors(logits, router, index, weight_grad):
     """The gradient of the logits (their type) from that of the weights, the choice held fixed."""
-    torch = _torch()
+    if torch is None:
+        _use_torch()
     ld, code = _logits(logits, router)
     T, E = logits.shape
     i = _array(index, "index", torch.int32, (T, router.top_k))
     g = _array(weight_grad, "weight_grad", torch.float32, (T, router.top_k))
-    dev = _device(logits, index, weight_grad)
-    grad = torch.empty((T, E), dtype=logits.dtype, device=dev)
-    _call("gemm_experts_route_backward", dev, logits.data_ptr(), T, E, ld, code, ctypes.byref(router), i, g,
-          grad.data_ptr(), E)
+    at = _device(logits, index, weight_grad)
+    grad = torch.empty((T, E), dtype=logits.dtype, device=logits.device)
+    _call("gemm_experts_route_backward", at, logits.data_ptr(), T, E, ld, code, router, i, g, grad.data_ptr(), E or 1)
     return grad
 
 
 def gemm_experts_dispatch_tensors(index, experts, align=1):
     """The ExpertPlan of index (T, k): every expert's (token, slot) pairs in their order, an expert's
     first row at a multiple of `align` (128 where a gradient of the weights is wanted)."""
-    torch = _torch()
+    if torch is None:
+        _use_torch()
     if index.dim() != 2:
         raise ValueError(f"index must be 2-D, not {tuple(index.shape)}")
     T, k = index.shape
     i = _array(index, "index", torch.int32, (T, k))
     if experts < 1 or align < 1:
         raise ValueError(f"experts = {experts} and align = {align} must be positive")
-    dev = _device(index)
-    lib = _dg.library()
+    at = _device(index)
+    dev = index.device
+    lib = _dg._lib or _dg.library()
     P, n = lib.gemm_experts_capacity(T, k, experts, align), lib.gemm_experts_dispatch_workspace(T, k, experts)
-    head = torch.empty(2 * experts + 1, dtype=torch.int32, device=dev)
-    plan = ExpertPlan(head[:experts + 1], head[experts + 1:], torch.empty(P, dtype=torch.int32, device=dev),
-                      torch.empty((T, k), dtype=torch.int32, device=dev), align)
-    work = torch.empty(n, dtype=torch.uint8, device=dev) if n else None
-    _call("gemm_experts_dispatch", dev, i, align, ctypes.byref(_plan(plan)), work.data_ptr() if n else None, n)
+    # the plan's arrays in one allocation; the workspace behind them
+    E1, head = experts + 1, 2 * experts + 1
+    buf = torch.empty(head + P + T * k + n // 4, dtype=torch.int32, device=dev)
+    p0 = buf.data_ptr()
+    plan = ExpertPlan(buf[:E1], buf[E1:head], buf[head:head + P], buf[head + P:head + P + T * k].view(T, k), align)
+    c = gemm_expert_plan(p0, p0 + 4 * E1, p0 + 4 * head, p0 + 4 * (head + P), experts, T, k, P)
+    _call("gemm_experts_dispatch", at, i, align, c, p0 + 4 * (head + P + T * k) if n else None, n)
     return plan
 
 
 def gemm_experts_product_tensors(a, b, plan, dtype=None, gather=True):
     """C (P, N): each row of the plan times its expert's matrix, zeros in padding rows. b (E, N, K); a holds
     the tokens' rows (T, K) with gather, the plan's (P, K) without."""
-    torch = _torch()
+    if torch is None:
+        _use_torch()
     dtype = dtype or torch.bfloat16
     out = _wide_type(dtype, "dtype")
-    A, B, p = _block(a, "a"), _block(b, "b", True), _plan(plan)
+    A, B, p = _block(a, "a"), _block(b, "b", 3), _plan(plan)
     if A.cols != B.cols or b.data.shape[0] != p.experts or A.rows != (p.tokens if gather else p.capacity):
         raise ValueError(f"shape mismatch: a {tuple(a.data.shape)}, b {tuple(b.data.shape)}, plan of {p.experts} "
                          f"experts, {p.tokens} tokens and {p.capacity} rows")
-    dev = _device(a.data, a.scale, b.data, b.scale, plan.offsets, plan.counts, plan.rows)
-    c = torch.empty((p.capacity, B.rows), dtype=dtype, device=dev)
-    if c.numel():
-        _call("gemm_experts_product", dev, ctypes.byref(A), ctypes.byref(B), ctypes.byref(p), int(gather),
-              c.data_ptr(), B.rows, out)
+    at = _device(a.data, a.scale, b.data, b.scale, plan.offsets, plan.counts, plan.rows)
+    P, N = p.capacity, B.rows
+    c = torch.empty((P, N), dtype=dtype, device=a.data.device)
+    if P and N:
+        _call("gemm_experts_product", at, A, B, p, int(gather), c.data_ptr(), N, out)
     return c
 
 
@@ -348,7 +381,8 @@ def gemm_experts_gradient_tensors(a, b, plan, dtype=None):
     """C (E, M, N) = A_e B_e^T over each expert's rows, for a (M, P) and b (N, P) with the plan's rows along
     their columns and zeros in padding, as gemm_block_quantize_tensors(..., transposed=True, rows=plan.rows)
     makes them. The plan's align has to be a multiple of 128; float32 by default."""
-    torch = _torch()
+    if torch is None:
+        _use_torch()
     dtype = dtype or torch.float32
     out = _wide_type(dtype, "dtype")
     A, B, p = _block(a, "a"), _block(b, "b"), _plan(plan)
@@ -356,47 +390,47 @@ def gemm_experts_gradient_tensors(a, b, plan, dtype=None):
         raise ValueError(f"shape mismatch: a {tuple(a.data.shape)}, b {tuple(b.data.shape)}, plan of {p.capacity} rows")
     if plan.align is not None and plan.align % BLOCK:
         raise ValueError(f"the plan's align is {plan.align}, not a multiple of {BLOCK}")
-    dev = _device(a.data, a.scale, b.data, b.scale, plan.offsets)
-    c = torch.empty((p.experts, A.rows, B.rows), dtype=dtype, device=dev)
-    if c.numel():
-        _call("gemm_experts_gradient", dev, ctypes.byref(A), ctypes.byref(B), ctypes.byref(p), c.data_ptr(), B.rows,
-              A.rows * B.rows, out)
+    at = _device(a.data, a.scale, b.data, b.scale, plan.offsets)
+    M, N = A.rows, B.rows
+    c = torch.empty((p.experts, M, N), dtype=dtype, device=a.data.device)
+    if p.experts and M and N:
+        _call("gemm_experts_gradient", at, A, B, p, c.data_ptr(), N, M * N, out)
     return c
 
 
 def _combine(y, plan, weight):
-    torch = _torch()
     p = _plan(plan)
     ld, code = _matrix(y, "y"), _wide_type(y.dtype, "y")
     if y.shape[0] != p.capacity:
         raise ValueError(f"y has {y.shape[0]} rows, the plan {p.capacity}")
-    _array(weight, "weight", torch.float32, (p.tokens, p.top_k))
-    return p, ld, code
+    return p, ld, code, _array(weight, "weight", torch.float32, (p.tokens, p.top_k))
 
 
 def gemm_experts_combine_tensors(y, plan, weight):
     """out (T, N) = the sum of each token's rows of y (P, N), weighted by weight (T, k) float32."""
-    p, ld, code = _combine(y, plan, weight)
-    dev = _device(y, plan.position, weight)
-    N = y.shape[1]
-    out = _torch().empty((p.tokens, N), dtype=y.dtype, device=dev)
-    if out.numel():
-        _call("gemm_experts_combine", dev, y.data_ptr(), N, ld, code, ctypes.byref(p), weight.data_ptr(),
-              out.data_ptr(), N)
+    if torch is None:
+        _use_torch()
+    p, ld, code, w = _combine(y, plan, weight)
+    at = _device(y, plan.position, weight)
+    T, N = p.tokens, y.shape[1]
+    out = torch.empty((T, N), dtype=y.dtype, device=y.device)
+    if T and N:
+        _call("gemm_experts_combine", at, y.data_ptr(), N, ld, code, p, w, out.data_ptr(), N)
     return out
 
 
 def gemm_experts_combine_backward_tensors(y, plan, weight, grad):
     """(y_grad (P, N) of y's type, weight_grad (T, k) float32) from grad (T, N)."""
-    torch = _torch()
-    p, ld, code = _combine(y, plan, weight)
+    if torch is None:
+        _use_torch()
+    p, ld, code, w = _combine(y, plan, weight)
     ldg = _matrix(grad, "grad")
-    if grad.dtype != y.dtype or tuple(grad.shape) != (p.tokens, y.shape[1]):
+    if grad.dtype != y.dtype or grad.shape != (p.tokens, y.shape[1]):
         raise ValueError(f"grad must be {y.dtype} of shape {(p.tokens, y.shape[1])}, not {grad.dtype} {tuple(grad.shape)}")
-    dev = _device(y, plan.position, plan.rows, weight, grad)
+    at = _device(y, plan.position, plan.rows, weight, grad)
     N = y.shape[1]
-    y_grad = torch.empty((p.capacity, N), dtype=y.dtype, device=dev)
-    weight_grad = torch.empty((p.tokens, p.top_k), dtype=torch.float32, device=dev)
-    _call("gemm_experts_combine_backward", dev, y.data_ptr(), N, ld, code, ctypes.byref(p), weight.data_ptr(),
-          grad.data_ptr(), ldg, y_grad.data_ptr(), N, weight_grad.data_ptr())
+    y_grad = torch.empty((p.capacity, N), dtype=y.dtype, device=y.device)
+    weight_grad = torch.empty((p.tokens, p.top_k), dtype=torch.float32, device=y.device)
+    _call("gemm_experts_combine_backward", at, y.data_ptr(), N, ld, code, p, w, grad.data_ptr(), ldg,
+          y_grad.data_ptr(), N or 1, weight_grad.data_ptr())
     return y_grad, weight_grad

@@ -96,6 +96,13 @@ def test_quantize_gather(block_rows):
     check_quantized(t, picked.t().contiguous(), E4, block_rows)
 
 
+def test_quantize_gather_from_no_rows():
+    rows = torch.zeros(130, dtype=torch.int32, device="cuda")
+    q, t = dg.gemm_block_quantize_tensors(torch.empty(0, 200, device="cuda"), E4, transposed=True, rows=rows)
+    check_quantized(q, torch.zeros(130, 200), E4, 1)
+    check_quantized(t, torch.zeros(200, 130), E4, 1)
+
+
 def test_quantize_strided_input():
     x = torch.randn(100, 333, generator=gen(3)).to(BF16).cuda()
     view = x[5:77, 3:290]

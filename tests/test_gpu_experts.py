@@ -215,6 +215,18 @@ def test_experts_product_empty_experts_and_nan_padding():
         check_experts(c, values(*a, 1), expert_values(b), plan, F32, True)
 
 
+def test_experts_product_without_tokens():
+    """A plan with rows, and no token for them to name: zeros, and A is not read."""
+    i32 = lambda *x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    b = codes(gen(1), 64, 128, E4, BLOCK, batch=2)
+    B = dg.BlockTensor(b[0].cuda(), b[1].cuda(), BLOCK)
+    a = dg.BlockTensor(torch.empty(0, 128, device="cuda").to(E4), torch.empty(0, 1, device="cuda"), 1)
+    for P in (8, 300):
+        plan = dg.ExpertPlan(i32(0, 2, P), i32(2, P - 2), torch.zeros(P, dtype=torch.int32, device="cuda"),
+                             torch.empty(0, 2, dtype=torch.int32, device="cuda"))
+        assert (dg.gemm_experts_product_tensors(a, B, plan, F32) == 0).all()
+
+
 def test_experts_product_many_experts():
     g = gen(6)
     plan = dg.gemm_experts_dispatch_tensors(choice(g, 90, 200, 3).cuda(), 200, 1)
