@@ -216,19 +216,19 @@ __device__ __forceinline__ void block_store4(const BlockArgs& g, int m, int n, f
         if (n + e < g.N) store_out(g.C, g.out_dt, at + e, v[e]);
 }
 
-// The same out of line, for unrolled loops: inlined there, its branches on types and edges
-// made 1300 blocks of code.
-__device__ __attribute__((noinline)) void block_store4_call(void* C, int64_t ldc, int N, int out_dt, int m, int n,
-                                                            f32x4 v) {
-    const size_t at = (size_t)m * (size_t)ldc + n;
-    const int dt = (int)uni32((uint32_t)out_dt);
-    if (n + 4 <= N) {
-        store_out4(C, dt, at, v);
-        return;
-    }
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-        if (n + e < N) store_out(C, dt, at + e, v[e]);
+// Two fp32 values as two 16-bit ones of type DT, the first in the low half.
+template <int DT>
+__device__ __forceinline__ uint32_t pack16(float x, float y) {
+    if constexpr (DT == DT_F16)
+        return (uint32_t)__builtin_bit_cast(uint16_t, (_Float16)x) | ((uint32_t)__builtin_bit_cast(uint16_t, (_Float16)y) << 16);
+    else return (uint32_t)f32_to_bf16_rne(x) | ((uint32_t)f32_to_bf16_rne(y) << 16);
+}
+
+// Whether row m of C (below m_end) is computed: the others, padding, become zeros. One bit a lane.
+__device__ __forceinline__ uint64_t live_rows(const BlockArgs& g, const BlockTile& t, int first) {
+    if (g.mode != BLOCK_EXPERTS) return ~0ull;
+    const int m = first + ((int)threadIdx.x & 63);
+    return __ballot(m < t.m_end && block_a_row(g, t, m) >= 0);
 }
 
 // Zeros in the rows past the last expert's, spread over the whole grid.
@@ -318,28 +318,29 @@ __global__ __launch_bounds__(512) void block_wide(BlockArgs g) {
     const uint32_t dA = (uint32_t)reinterpret_cast<uintptr_t>(DG_LDSV(sA)) + (uint32_t)wave * 4096u;
     const uint32_t dB = (uint32_t)reinterpret_cast<uintptr_t>(DG_LDSV(sB)) + (uint32_t)wave * 4096u;
     const uint32_t dS = (uint32_t)reinterpret_cast<uintptr_t>(DG_LDSV(fS)) + (uint32_t)wave * 256u;
-    auto issue = [&](int kb) {
+    // copy c (0 .. 3) of A and of B of block kb
+    auto issue = [&](int kb, int c) {
         const uint32_t st = (uint32_t)(kb & 1);
-        __builtin_amdgcn_global_load_lds(DG_GLB(ps), DG_LDS_ADDR(dS + st * STAGE_S), 4, 0, 0);
-        ps += ps_step;
+        const size_t k = (size_t)kb * kBlock;
         if (kb < t.nkb - 1 || t.krem == kBlock) {
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                __builtin_amdgcn_global_load_lds(DG_GLB(ba + oa[c]), DG_LDS_ADDR(dA + st * STAGE + c * 1024u), 16, 0, 0);
-                __builtin_amdgcn_global_load_lds(DG_GLB(bb + ob[c]), DG_LDS_ADDR(dB + st * STAGE + c * 1024u), 16, 0, 0);
-            }
+            __builtin_amdgcn_global_load_lds(DG_GLB(ba + k + oa[c]), DG_LDS_ADDR(dA + st * STAGE + c * 1024u), 16, 0, 0);
+            __builtin_amdgcn_global_load_lds(DG_GLB(bb + k + ob[c]), DG_LDS_ADDR(dB + st * STAGE + c * 1024u), 16, 0, 0);
         } else {
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                const bool in = kc[c & 1] < t.krem;
-                const void* a = in ? static_cast<const void*>(ba + oa[c]) : block_zeros;
-                const void* b = in ? static_cast<const void*>(bb + ob[c]) : block_zeros;
-                __builtin_amdgcn_global_load_lds(DG_GLB(a), DG_LDS_ADDR(dA + st * STAGE + c * 1024u), 16, 0, 0);
-                __builtin_amdgcn_global_load_lds(DG_GLB(b), DG_LDS_ADDR(dB + st * STAGE + c * 1024u), 16, 0, 0);
-            }
+            const bool in = kc[c & 1] < t.krem;
+            const void* a = in ? static_cast<const void*>(ba + k + oa[c]) : block_zeros;
+            const void* b = in ? static_cast<const void*>(bb + k + ob[c]) : block_zeros;
+            __builtin_amdgcn_global_load_lds(DG_GLB(a), DG_LDS_ADDR(dA + st * STAGE + c * 1024u), 16, 0, 0);
+            __builtin_amdgcn_global_load_lds(DG_GLB(b), DG_LDS_ADDR(dB + st * STAGE + c * 1024u), 16, 0, 0);
         }
-        ba += kBlock;
-        bb += kBlock;
+    };
+    auto issue_scales = [&](int kb) {
+        __builtin_amdgcn_global_load_lds(DG_GLB(ps), DG_LDS_ADDR(dS + (uint32_t)(kb & 1) * STAGE_S), 4, 0, 0);
+        ps += ps_step;
+    };
+    auto issue_all = [&](int kb) {
+        issue_scales(kb);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) issue(kb, c);
     };
     auto published = [&]() {  // this wave's copies have landed, and after the barrier everybody's
         asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
@@ -364,9 +365,15 @@ __global__ __launch_bounds__(512) void block_wide(BlockArgs g) {
 #pragma unroll
         for (int j = 0; j < FN; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
     const bool mine = t.m0 + wm * 128 < t.m_end;  // this wave has rows of C
+    if (t.bad) {
+#pragma unroll
+        for (int i = 0; i < FM; ++i)
+#pragma unroll
+            for (int j = 0; j < FN; ++j) acc[i][j] = f32x4{1, 1, 1, 1} * __builtin_nanf("");
+    }
 
     i32x8 bf[FN], af[2];
-    f32x4 part[2][FN], sb[BROW ? FN : 1];
+    f32x4 part[FN], sb[BROW ? FN : 1];
     float sa[4];
     auto read_sb = [&](int st) {
         const float* f = fb + st * (BM + BN);
@@ -377,19 +384,16 @@ __global__ __launch_bounds__(512) void block_wide(BlockArgs g) {
             sb[0][0] = f[0];
         }
     };
-    auto add = [&](int i) {  // the scaled parts of fragment row i
-        const float s = sa[i & 3];
+    // the scaled part of fragment row i, column j
+    auto add = [&](int i, int j, float s) {
 #pragma unroll
-        for (int j = 0; j < FN; ++j)
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                acc[i][j][e] = fmaf(part[i & 1][j][e], BROW ? s * sb[BROW ? j : 0][e] : s * sb[0][0], acc[i][j][e]);
+        for (int e = 0; e < 4; ++e)
+            acc[i][j][e] = fmaf(part[j][e], BROW ? s * sb[BROW ? j : 0][e] : s, acc[i][j][e]);
     };
 
     if (t.nkb > 0) {
-        issue(0);
+        issue_all(0);
         published();
-        if (t.nkb > 1) issue(1);
         if (mine) {
 #pragma unroll
             for (int j = 0; j < FN; ++j) bf[j] = frag(bw + j * 16 * kBlock);
@@ -397,69 +401,125 @@ __global__ __launch_bounds__(512) void block_wide(BlockArgs g) {
             sa[0] = fa[0];
             read_sb(0);
         }
+        if (t.nkb > 1) {
+            issue_scales(1);
+            issue(1, 0);
+        }
     }
     for (int kb = 0; kb < t.nkb; ++kb) {
         const int st = kb & 1, next = st ^ 1;
-        if (mine) {
 #pragma unroll
-            for (int i = 0; i < FM - 1; ++i) {
-                // the next fragment is read behind the first instruction that uses this one, and
-                // pinned there: the compiler waits for all LDS reads in flight where it waits
-                // for one, so reads issued before that wait would be waited for at once, and
-                // left to itself it puts them at the end, too late to hide their latency
-                part[i & 1][0] = mfma_16<TB, TA>(bf[0], af[i & 1], f32x4{0, 0, 0, 0});
-                __builtin_amdgcn_sched_barrier(0);
-                af[(i + 1) & 1] = frag(aw + st * STAGE + (i + 1) * 16 * kBlock);
-                sa[(i + 1) & 3] = fa[st * (BM + BN) + (i + 1) * 16];
-                __builtin_amdgcn_sched_barrier(0);
+        for (int i = 0; i < FM - 1; ++i) {
+            if (mine) {
+                // a part is added just before the instruction that replaces it, four
+                // instructions after it was asked for; pinned, as are the reads of the next
+                // fragment behind the first instruction that uses this one: the compiler waits
+                // for all LDS reads in flight where it waits for one, so reads issued before
+                // that wait would be waited for at once, and left to itself it puts them at the
+                // end, too late to hide their latency
+                const float s = i > 0 ? (BROW ? sa[(i - 1) & 3] : sa[(i - 1) & 3] * sb[0][0]) : 0.0f;
 #pragma unroll
-                for (int j = 1; j < FN; ++j) part[i & 1][j] = mfma_16<TB, TA>(bf[j], af[i & 1], f32x4{0, 0, 0, 0});
-                if (i > 0) add(i - 1);
-                __builtin_amdgcn_sched_barrier(0);
+                for (int j = 0; j < FN; ++j) {
+                    if (i > 0) add(i - 1, j, s);
+                    part[j] = mfma_16<TB, TA>(bf[j], af[i & 1], f32x4{0, 0, 0, 0});
+                    __builtin_amdgcn_sched_barrier(0);
+                    if (j == 0) {
+                        af[(i + 1) & 1] = frag(aw + st * STAGE + (i + 1) * 16 * kBlock);
+                        sa[(i + 1) & 3] = fa[st * (BM + BN) + (i + 1) * 16];
+                        __builtin_amdgcn_sched_barrier(0);
+                    }
+                }
             }
+            // the copies of the next block, a few at a time: all at once they hold up every wave
+            // until the address unit has taken them
+            if (i < 3 && kb + 1 < t.nkb) issue(kb + 1, i + 1);
         }
         if (kb + 1 < t.nkb) {
             published();
-            if (kb + 2 < t.nkb) issue(kb + 2);
+            if (kb + 2 < t.nkb) {
+                issue_scales(kb + 2);
+                issue(kb + 2, 0);
+            }
         }
         if (mine) {
             // past the end of k these reads find old data, which nothing uses
+            const float s6 = BROW ? sa[2] : sa[2] * sb[0][0], s7 = BROW ? sa[3] : sa[3] * sb[0][0];
 #pragma unroll
             for (int j = 0; j < FN; ++j) {
-                part[1][j] = mfma_16<TB, TA>(bf[j], af[1], f32x4{0, 0, 0, 0});
-                bf[j] = frag(bw + next * STAGE + j * 16 * kBlock);
+                add(FM - 2, j, s6);
+                part[j] = mfma_16<TB, TA>(bf[j], af[1], f32x4{0, 0, 0, 0});
+                __builtin_amdgcn_sched_barrier(0);
+                if (j > 0) bf[j - 1] = frag(bw + next * STAGE + (j - 1) * 16 * kBlock);
+                __builtin_amdgcn_sched_barrier(0);
             }
+            bf[FN - 1] = frag(bw + next * STAGE + (FN - 1) * 16 * kBlock);
             af[0] = frag(aw + next * STAGE);
-            add(FM - 2);
-            const float first = fa[next * (BM + BN)];
-            add(FM - 1);
-            sa[0] = first;
+            sa[0] = fa[next * (BM + BN)];
+#pragma unroll
+            for (int j = 0; j < FN; ++j) add(FM - 1, j, s7);
             read_sb(next);
             __builtin_amdgcn_sched_barrier(0);
         }
     }
 
-    // ---- C through LDS, 16 rows of the wave's 64 columns at a time
+    // ---- C through LDS, so that each store instruction writes whole 128-byte rows
     __builtin_amdgcn_s_barrier();  // every wave has read its last fragments
     asm volatile("" ::: "memory");
     if (!mine) return;
-    float* const stage = reinterpret_cast<float*>(lds) + wave * (16 * ROW);
-    const int n = t.n0 + wn * 64 + l16 * 4;
+    const int m0 = t.m0 + wm * 128, n0 = t.n0 + wn * 64;
+    const uint64_t live[2] = {live_rows(g, t, m0), live_rows(g, t, m0 + 64)};
+    if (g.out_dt == DT_F32) {  // a K slice's sums
+        float* const stage = reinterpret_cast<float*>(lds) + wave * (16 * ROW);
+        float* const C = static_cast<float*>(g.C);
+        const int n = n0 + l16 * 4;
 #pragma unroll
-    for (int i = 0; i < FM; ++i) {
+        for (int i = 0; i < FM; ++i) {
 #pragma unroll
-        for (int j = 0; j < FN; ++j) *reinterpret_cast<f32x4*>(stage + l16 * ROW + j * 16 + lg * 4) = acc[i][j];
-        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+            for (int j = 0; j < FN; ++j) *reinterpret_cast<f32x4*>(stage + l16 * ROW + j * 16 + lg * 4) = acc[i][j];
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
 #pragma unroll
-        for (int p = 0; p < 4; ++p) {
-            const int row = p * 4 + lg, m = t.m0 + wm * 128 + i * 16 + row;
-            f32x4 v = *reinterpret_cast<const f32x4*>(stage + row * ROW + l16 * 4);
-            if (m >= t.m_end || n >= g.N) continue;
-            if (t.bad) v = f32x4{1, 1, 1, 1} * __builtin_nanf("");
-            else if (g.mode == BLOCK_EXPERTS && block_a_row(g, t, m) < 0) v = f32x4{0, 0, 0, 0};
-            block_store4_call(g.C, g.ldc, g.N, g.out_dt, m, n, v);
+            for (int p = 0; p < 4; ++p) {
+                const int row = p * 4 + lg, m = m0 + i * 16 + row;
+                const f32x4 v = *reinterpret_cast<const f32x4*>(stage + row * ROW + l16 * 4);
+                float* const c = C + (size_t)m * (size_t)g.ldc + n;
+                if (m < t.m_end && n + 4 <= g.ldc) __builtin_memcpy(c, &v, 16);  // the slices' rows are padded to 4
+            }
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
         }
-        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        return;
+    }
+    // all 128 rows as 16-bit numbers: 128 bytes a row, 16-byte chunks permuted by (row >> 1) & 7
+    uint8_t* const stage = lds + wave * (128 * 128);
+    auto to_lds = [&](auto dt) {
+#pragma unroll
+        for (int i = 0; i < FM; ++i)
+#pragma unroll
+            for (int j = 0; j < FN; ++j) {
+                const f32x4 v = acc[i][j];
+                const u32x2 h = {pack16<decltype(dt)::value>(v[0], v[1]), pack16<decltype(dt)::value>(v[2], v[3])};
+                *reinterpret_cast<u32x2*>(stage + (i * 16 + l16) * 128 + (((2 * j + (lg >> 1)) ^ ((l16 >> 1) & 7)) << 4) +
+                                          (lg & 1) * 8) = h;
+            }
+    };
+    if (g.out_dt == DT_F16) to_lds(std::integral_constant<int, DT_F16>{});
+    else to_lds(std::integral_constant<int, DT_BF16>{});
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    uint16_t* const C = static_cast<uint16_t*>(g.C);
+    const int n = n0 + (lane & 7) * 8;
+#pragma unroll 4
+    for (int p = 0; p < 16; ++p) {
+        const int row = p * 8 + (lane >> 3), m = m0 + row;
+        u32x4 v = *reinterpret_cast<const u32x4*>(stage + row * 128 + (((lane & 7) ^ ((row >> 1) & 7)) << 4));
+        if (!((live[p >> 3] >> (row & 63)) & 1)) v = u32x4{0, 0, 0, 0};
+        if (m >= t.m_end || n >= g.N) continue;
+        uint16_t* const c = C + (size_t)m * (size_t)g.ldc + n;
+        if (n + 8 <= g.N) {
+            __builtin_memcpy(c, &v, 16);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (n + e < g.N) c[e] = (uint16_t)(v[e >> 1] >> (16 * (e & 1)));
+        }
     }
 }
 
@@ -733,25 +793,36 @@ __global__ __launch_bounds__(WM* WN * 64) void block_tile(BlockArgs g) {
     float* const stage = reinterpret_cast<float*>(lds) + wave * (32 * ROW);
     constexpr int LANES = SJ * 8;  // lanes to a row
     const int n = t.n0 + wn * SJ * 32 + (lane % LANES) * 4;
+    const bool whole = t.n0 + BN <= g.N;
 #pragma unroll
     for (int i = 0; i < SM; ++i) {
         if (i >= subs) continue;
+        const int first = t.m0 + (wm * SM + i) * 32;
+        const uint64_t live = live_rows(g, t, first);
 #pragma unroll
         for (int j = 0; j < SJ; ++j)
 #pragma unroll
-            for (int q = 0; q < 4; ++q)
-                *reinterpret_cast<f32x4*>(stage + l32 * ROW + j * 32 + q * 8 + lh * 4) =
-                    f32x4{acc[i][j][q * 4], acc[i][j][q * 4 + 1], acc[i][j][q * 4 + 2], acc[i][j][q * 4 + 3]};
+            for (int q = 0; q < 4; ++q) {
+                f32x4 v = {acc[i][j][q * 4], acc[i][j][q * 4 + 1], acc[i][j][q * 4 + 2], acc[i][j][q * 4 + 3]};
+                if (t.bad) v = f32x4{1, 1, 1, 1} * __builtin_nanf("");
+                *reinterpret_cast<f32x4*>(stage + l32 * ROW + j * 32 + q * 8 + lh * 4) = v;
+            }
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        auto rows_out = [&](auto put) {
 #pragma unroll
-        for (int p = 0; p < 32 * LANES / 64; ++p) {
-            const int row = p * (64 / LANES) + lane / LANES, m = t.m0 + (wm * SM + i) * 32 + row;
-            f32x4 v = *reinterpret_cast<const f32x4*>(stage + row * ROW + (lane % LANES) * 4);
-            if (m >= t.m_end || n >= g.N) continue;
-            if (t.bad) v = f32x4{1, 1, 1, 1} * __builtin_nanf("");
-            else if (g.mode == BLOCK_EXPERTS && block_a_row(g, t, m) < 0) v = f32x4{0, 0, 0, 0};
-            block_store4(g, m, n, v);
-        }
+            for (int p = 0; p < 32 * LANES / 64; ++p) {
+                const int row = p * (64 / LANES) + lane / LANES, m = first + row;
+                f32x4 v = *reinterpret_cast<const f32x4*>(stage + row * ROW + (lane % LANES) * 4);
+                if (!((live >> row) & 1)) v = f32x4{0, 0, 0, 0};
+                if (m < t.m_end && n < g.N) put((size_t)m * (size_t)g.ldc + n, m, v);
+            }
+        };
+        // by type outside the unrolled rows; the tiles that the last column cuts, element-wise
+        if (!whole) rows_out([&](size_t, int m, f32x4 v) { block_store4(g, m, n, v); });
+        else if (g.out_dt == DT_F32)
+            rows_out([&](size_t at, int, f32x4 v) { store_out4(g.C, DT_F32, at, v); });
+        else if (g.out_dt == DT_F16) rows_out([&](size_t at, int, f32x4 v) { store_out4(g.C, DT_F16, at, v); });
+        else rows_out([&](size_t at, int, f32x4 v) { store_out4(g.C, DT_BF16, at, v); });
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     }
 }
