@@ -182,20 +182,21 @@ int tr_of(const gemm_block_matrix& A, const gemm_block_matrix& B) {
     return (A.op == GEMM_OP_T ? 2 : 0) | (B.op == GEMM_OP_T ? 1 : 0);
 }
 
-// Whether the 256 x 256 tiles exist for a call: C of 16 bits, byte offsets within a matrix of 32 bits.
-bool wide_call(const gemm_block_matrix& A, const gemm_block_matrix& B, int out_dtype) {
-    return out_dtype != GEMM_F32 && A.rows * A.ld < ((int64_t)1 << 32) && B.rows * B.ld < ((int64_t)1 << 32);
+// Whether byte offsets within an operand fit 32 bits.
+bool small_call(const gemm_block_matrix& A, const gemm_block_matrix& B) {
+    return A.rows * A.ld < ((int64_t)1 << 32) && B.rows * B.ld < ((int64_t)1 << 32);
 }
 
 constexpr int64_t kCus = 256;
 
 // rows: rows of C that share a B (for experts the average); n_products: B's in the call;
-// wide: the 256 x 256 tiles exist for the call (C of 16 bits);
+// small: byte offsets within an operand fit 32 bits; full: fp32 C; tr: BlockPlan::tr;
 // may_split: whether K may be split.
-dg::BlockPlan block_plan(int64_t rows, int64_t n_products, int64_t N, int64_t K, bool direct, bool wide, int tr,
+dg::BlockPlan block_plan(int64_t rows, int64_t n_products, int64_t N, int64_t K, bool direct, bool small, bool full, int tr,
                          bool may_split) {
     dg::BlockPlan p;
     p.tr = tr;
+    p.small = small;
     p.direct = direct;
     p.split = 1;
     const int64_t nkb = ceil_div(K, dg::kBlock);
@@ -206,9 +207,13 @@ dg::BlockPlan block_plan(int64_t rows, int64_t n_products, int64_t N, int64_t K,
         const int64_t wgs = n_products * ceil_div(N, 16);
         if (may_split && wgs < kCus) p.split = (int)std::max<int64_t>(1, std::min<int64_t>(kCus / wgs, nkb / 16));
     } else {
-        const int64_t big = n_products * ceil_div(rows, 256) * ceil_div(N, 256);
-        p.kernel = direct && wide && tr == 0 && big >= kCus * 3 / 4 ? dg::BLOCK_TILE256 : dg::BLOCK_TILE128;
-        p.bm = p.bn = p.kernel == dg::BLOCK_TILE256 ? 256 : 128;
+        // 256 rows (and 256 columns for C of 16 bits, 128 for fp32) where that leaves most
+        // compute units a tile
+        const int64_t big = n_products * ceil_div(rows, 256) * ceil_div(N, full ? 128 : 256);
+        const bool large = direct && small && tr == 0 && big >= kCus * 3 / 4;
+        p.kernel = large ? dg::BLOCK_TILE256 : dg::BLOCK_TILE128;
+        p.bm = large ? 256 : 128;
+        p.bn = large && !full ? 256 : 128;
         const int64_t wgs = n_products * ceil_div(rows, p.bm) * ceil_div(N, p.bn);
         if (may_split && wgs < kCus) p.split = (int)std::max<int64_t>(1, std::min<int64_t>(2 * kCus / wgs, nkb / 4));
     }
@@ -409,9 +414,9 @@ int64_t gemm_block_product_workspace(int64_t M, int64_t N, int64_t K) {
     if (M <= 0 || N <= 0 || K <= 0 || M > kMaxDim || N > kMaxDim || K > kMaxDim) return 0;
     int64_t bytes = 0;
     for (bool direct : {false, true})
-        for (bool wide : {false, true})
+        for (bool full : {false, true})
             for (int tr : {0, 1})
-                bytes = std::max(bytes, split_bytes(block_plan(M, 1, N, K, direct, wide, tr, true).split, M, N));
+                bytes = std::max(bytes, split_bytes(block_plan(M, 1, N, K, direct, direct, full, tr, true).split, M, N));
     return bytes;
 }
 
@@ -441,9 +446,9 @@ int gemm_block_product(const gemm_block_matrix* A, const gemm_block_matrix* B, v
                           scale_range("B.scale", *B)}));
     DG_TRY(check_device());
     const bool direct = direct_rows(*A, 1) && direct_rows(*B, 1);
-    const bool wide = wide_call(*A, *B, out_dtype);
-    dg::BlockPlan p = block_plan(M, 1, N, K, direct, wide, tr_of(*A, *B), true);
-    if (split_bytes(p.split, M, N) > workspace_bytes) p = block_plan(M, 1, N, K, direct, wide, tr_of(*A, *B), false);
+    const bool small = small_call(*A, *B), full = out_dtype == GEMM_F32;
+    dg::BlockPlan p = block_plan(M, 1, N, K, direct, small, full, tr_of(*A, *B), true);
+    if (split_bytes(p.split, M, N) > workspace_bytes) p = block_plan(M, 1, N, K, direct, small, full, tr_of(*A, *B), false);
     dg::BlockArgs a = block_args(*A, *B, C, ldc, out_dtype);
     a.mode = dg::BLOCK_PLAIN;
     a.tiles_m = (int)ceil_div(M, p.bm);
@@ -619,10 +624,10 @@ int gemm_experts_product(const gemm_block_matrix* A, const gemm_block_matrix* B,
                           range("plan.counts", plan->counts, (uint64_t)E * 4),
                           range("plan.rows", plan->rows, gather ? (uint64_t)P * 4 : 0)}));
     DG_TRY(check_device());
-    const bool direct = direct_rows(*A, 1) && direct_rows(*B, E);
+    const bool direct = direct_rows(*A, 1) && direct_rows(*B, E), small = small_call(*A, *B);
     const int64_t pairs = plan->tokens * plan->top_k, active = std::max<int64_t>(1, std::min(E, pairs));
     const dg::BlockPlan p = block_plan(std::max<int64_t>(1, pairs / active), active, N, A->cols, direct,
-                                       wide_call(*A, *B, out_dtype), tr_of(*A, *B), false);
+                                       small, out_dtype == GEMM_F32, tr_of(*A, *B), false);
     dg::BlockArgs a = block_args(*A, *B, C, ldc, out_dtype);
     a.mode = dg::BLOCK_EXPERTS;
     a.M = (int)P;
@@ -661,8 +666,8 @@ int gemm_experts_gradient(const gemm_block_matrix* A, const gemm_block_matrix* B
                          {data_range("A.data", *A), scale_range("A.scale", *A), data_range("B.data", *B),
                           scale_range("B.scale", *B), range("plan.offsets", plan->offsets, (uint64_t)(E + 1) * 4)}));
     DG_TRY(check_device());
-    const bool direct = direct_rows(*A, 1) && direct_rows(*B, 1);
-    const dg::BlockPlan p = block_plan(M, E, N, A->cols, direct, wide_call(*A, *B, out_dtype), tr_of(*A, *B), false);
+    const bool direct = direct_rows(*A, 1) && direct_rows(*B, 1), small = small_call(*A, *B);
+    const dg::BlockPlan p = block_plan(M, E, N, A->cols, direct, small, out_dtype == GEMM_F32, tr_of(*A, *B), false);
     dg::BlockArgs a = block_args(*A, *B, C, ldc, out_dtype);
     a.mode = dg::BLOCK_GRADIENT;
     a.E = (int)E;

@@ -48,6 +48,7 @@ struct BlockPlan {
     int kernel;       // BlockKernel
     int bm, bn;
     int direct;       // 16-byte aligned rows: copies straight to LDS (tiles), whole 16-byte loads (skinny)
+    int small;        // byte offsets within an operand fit 32 bits
     int split;        // K slices
     int tr;           // bit 0: B stored with its rows adjacent, bit 1: A
 };

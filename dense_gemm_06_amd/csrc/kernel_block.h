@@ -144,6 +144,23 @@ __device__ __forceinline__ bool expert_tile(const BlockArgs& g, BlockTile& t) {
     return false;
 }
 
+// Narrows a tile to this workgroup's slice of K (grid y), whose sums go to its plane of the
+// workspace in fp32.
+__device__ __forceinline__ void split_k(BlockArgs& g, BlockTile& t) {
+    if (g.k_split <= 1) return;
+    t.kb0 = (int)blockIdx.y * g.kb_chunk;
+    const int left = t.nkb - t.kb0;
+    if (left > g.kb_chunk) {
+        t.nkb = g.kb_chunk;
+        t.krem = kBlock;
+    } else {
+        t.nkb = left;
+    }
+    g.C = g.work + (size_t)blockIdx.y * (size_t)g.work_slice;
+    g.ldc = g.work_ld;
+    g.out_dt = DT_F32;
+}
+
 // The tile of this workgroup; false when there is none (the caller still takes part in
 // clearing the rows past the last expert).
 template <int BM, int BN>
@@ -163,8 +180,26 @@ __device__ __forceinline__ bool block_tile_of(BlockArgs& g, BlockTile& t) {
         g.SB += (size_t)t.expert * (size_t)g.stride_sb;
         return true;
     }
-    int id = xcd_tile((int)gridDim.x), tm, tn;
     const int per = g.tiles_m * g.tiles_n;
+    int tm, tn;
+    if (g.mode == BLOCK_PLAIN && g.M % BM != 0 && g.tiles_m > 1) {
+        // tiles of the cut last row, which are less work, start last on each XCD: in front of
+        // whole ones they would leave those to a round of their own
+        const int x = (int)blockIdx.x & 7, i = (int)blockIdx.x >> 3;
+        const int whole = per - g.tiles_n, hq = whole >> 3, hr = whole & 7, q = per >> 3, r = per & 7;
+        const int mine = hq + (x < hr ? 1 : 0);
+        if (i < mine) {
+            raster(x * hq + min(x, hr) + i, g.tiles_m - 1, g.tiles_n, min(g.group_m, g.tiles_m - 1), tm, tn);
+        } else {
+            tm = g.tiles_m - 1;
+            tn = (x * q + min(x, r)) - (x * hq + min(x, hr)) + i - mine;
+        }
+        split_k(g, t);
+        t.m0 = tm * BM;
+        t.n0 = tn * BN;
+        return true;
+    }
+    int id = xcd_tile((int)gridDim.x);
     if (g.mode == BLOCK_GRADIENT) {
         t.expert = id / per;
         id -= t.expert * per;
@@ -177,18 +212,8 @@ __device__ __forceinline__ bool block_tile_of(BlockArgs& g, BlockTile& t) {
         t.nkb = t.bad ? 0 : (hi - lo + kBlock - 1) / kBlock;
         t.krem = hi - lo - (t.nkb - 1) * kBlock;
         g.C = static_cast<char*>(g.C) + (size_t)t.expert * (size_t)g.stride_c * (g.out_dt == DT_F32 ? 4 : 2);
-    } else if (g.k_split > 1) {
-        t.kb0 = (int)blockIdx.y * g.kb_chunk;
-        const int left = t.nkb - t.kb0;
-        if (left > g.kb_chunk) {
-            t.nkb = g.kb_chunk;
-            t.krem = kBlock;
-        } else {
-            t.nkb = left;
-        }
-        g.C = g.work + (size_t)blockIdx.y * (size_t)g.work_slice;
-        g.ldc = g.work_ld;
-        g.out_dt = DT_F32;
+    } else {
+        split_k(g, t);
     }
     raster(id, g.tiles_m, g.tiles_n, g.group_m, tm, tn);
     t.m0 = tm * BM;
@@ -523,6 +548,483 @@ __global__ __launch_bounds__(512) void block_wide(BlockArgs g) {
     }
 }
 
+// ---------------------------------------------------------------------------- fp32 sums, aligned rows
+// (64 WM) x 128 tiles for fp32 C and 16-byte aligned rows on 2 WM waves of 64 x 64, each 4 x 4
+// tiles of v_mfma_f32_16x16x32_f16, four instructions to a block of k. Codes are copied
+// straight to LDS (S stages laid out as in the wide tiles) S - 1 blocks ahead and widened in
+// the fragments: a wave holds the block's four fragments of B as halves (64 registers),
+// widens those of A one ahead and, behind the last use of each of B's, the next block's.
+// Vector and matrix instructions are even (with a scale for each row of B: 256 of 4 cycles
+// and 64 of 16 for each wave and block); widening on the way into LDS instead halves the
+// conversions, but its writes and conflicts kept LDS busy 80% longer than the matrix cores
+// (272 against 237 us at 2056 x 4000 x 8176).
+template <int TA, int TB, bool BROW, int WM, int S>
+__global__ __launch_bounds__(WM * 128, 2) void block_full_direct(BlockArgs g) {
+    constexpr int NW = 2 * WM, BM = 64 * WM, BN = 128, FM = 4, FN = 4, ROW = 68;
+    constexpr int CB = BN / 8 / NW;  // copies of 1 KB (8 rows) of B for each wave; 4 of A
+    constexpr int STAGE_A = BM * kBlock, STAGE_B = BN * kBlock, STAGE_S = (BM + BN) * 4;
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[S * (STAGE_A + STAGE_B + STAGE_S)];
+    uint8_t* const sA = lds;
+    uint8_t* const sB = lds + S * STAGE_A;
+    float* const fS = reinterpret_cast<float*>(lds + S * (STAGE_A + STAGE_B));
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wm = wave >> 1, wn = wave & 1;
+    const int l16 = lane & 15, lg = lane >> 4;
+
+    BlockTile t;
+    const bool any = block_tile_of<BM, BN>(g, t);
+    if (g.mode == BLOCK_EXPERTS) clear_tail(g);
+    if (!any) return;
+
+    const uint8_t* ba = g.A + (size_t)t.kb0 * kBlock;
+    const uint8_t* bb = g.B + (size_t)t.kb0 * kBlock;
+    uint32_t oa[4], ob[CB];
+    int ka[2], kb2[2];  // the k of a chunk: the same for every other copy
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+        const int row = (wave * 4 + c) * 8 + (lane >> 3);
+        ka[c & 1] = ((lane & 7) ^ ((row >> 1) & 7)) * 16;
+        const int r = max(block_a_row(g, t, min(t.m0 + row, t.m_end - 1)), 0);
+        oa[c] = (uint32_t)r * (uint32_t)g.lda + (uint32_t)ka[c & 1];
+    }
+#pragma unroll
+    for (int c = 0; c < CB; ++c) {
+        const int row = (wave * CB + c) * 8 + (lane >> 3);
+        kb2[c & 1] = ((lane & 7) ^ ((row >> 1) & 7)) * 16;
+        ob[c] = (uint32_t)min(t.n0 + row, g.N - 1) * (uint32_t)g.ldb + (uint32_t)kb2[c & 1];
+    }
+    // scales: the first WM waves copy those of A's rows, two those of B's, the others none
+    const bool scales = wave < WM + 2;
+    const float* ps;
+    int64_t ps_step;
+    if (wave < WM) {
+        const int r = max(block_a_row(g, t, min(t.m0 + tid, t.m_end - 1)), 0);
+        ps = g.SA + (size_t)(r >> g.a_shift) * (size_t)g.sa_row + (size_t)t.kb0 * (size_t)g.sa_blk;
+        ps_step = g.sa_blk;
+    } else {
+        const int n = min(t.n0 + (tid - BM) % BN, g.N - 1);
+        ps = g.SB + (size_t)(n >> g.b_shift) * (size_t)g.sb_row + (size_t)t.kb0 * (size_t)g.sb_blk;
+        ps_step = g.sb_blk;
+    }
+    const uint32_t dA = (uint32_t)reinterpret_cast<uintptr_t>(DG_LDSV(sA)) + (uint32_t)wave * 4096u;
+    const uint32_t dB = (uint32_t)reinterpret_cast<uintptr_t>(DG_LDSV(sB)) + (uint32_t)wave * (CB * 1024u);
+    const uint32_t dS = (uint32_t)reinterpret_cast<uintptr_t>(DG_LDSV(fS)) + (uint32_t)wave * 256u;
+    auto issue = [&](int kb, int st) {  // block kb into stage st: 4 + CB (+ 1) copies
+        const size_t k = (size_t)kb * kBlock;
+        const int rem = kb < t.nkb - 1 ? kBlock : t.krem;
+        if (scales) __builtin_amdgcn_global_load_lds(DG_GLB(ps), DG_LDS_ADDR(dS + st * STAGE_S), 4, 0, 0);
+        ps += ps_step;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            const void* a = ka[c & 1] < rem ? static_cast<const void*>(ba + k + oa[c]) : block_zeros;
+            __builtin_amdgcn_global_load_lds(DG_GLB(a), DG_LDS_ADDR(dA + st * STAGE_A + c * 1024u), 16, 0, 0);
+        }
+#pragma unroll
+        for (int c = 0; c < CB; ++c) {
+            const void* b = kb2[c & 1] < rem ? static_cast<const void*>(bb + k + ob[c]) : block_zeros;
+            __builtin_amdgcn_global_load_lds(DG_GLB(b), DG_LDS_ADDR(dB + st * STAGE_B + c * 1024u), 16, 0, 0);
+        }
+    };
+    // this wave's copies but those of the `behind` newest blocks have landed (0 or S - 2), and
+    // after the barrier everybody's
+    auto published = [&](bool behind) {
+        if (S > 2 && behind) {
+            if (scales) asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"((S - 2) * (5 + CB)) : "memory");
+            else asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"((S - 2) * (4 + CB)) : "memory");
+        } else {
+            asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+        }
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+    };
+
+    // a lane's 32 codes of a fragment row: chunks lg and lg + 4, 16 codes each; halves u = 0 .. 3
+    const int off = l16 * kBlock + ((lg ^ ((l16 >> 1) & 7)) << 4);
+    auto codes_of = [&](const uint8_t* base) {
+        const u32x4 x = *reinterpret_cast<const u32x4*>(base + off);
+        const u32x4 y = *reinterpret_cast<const u32x4*>(base + (off ^ 64));
+        return i32x8{(int)x[0], (int)x[1], (int)x[2], (int)x[3], (int)y[0], (int)y[1], (int)y[2], (int)y[3]};
+    };
+    const uint8_t* const aw = sA + wm * 64 * kBlock;
+    const uint8_t* const bw = sB + wn * 64 * kBlock;
+    const float* const fa = fS + wm * 64 + l16;
+    const float* const fb = fS + BM + wn * 64;
+
+    f32x4 acc[FM][FN];
+#pragma unroll
+    for (int i = 0; i < FM; ++i)
+#pragma unroll
+        for (int j = 0; j < FN; ++j) acc[i][j] = t.bad ? f32x4{1, 1, 1, 1} * __builtin_nanf("") : f32x4{0, 0, 0, 0};
+    // subtiles of 16 rows of this wave that hold rows of C: the others are not multiplied
+    const int subs = min(max((t.m_end - t.m0 + 15) / 16 - wm * FM, 0), FM);
+
+    f16x8 af[4], bf[FN][4];
+    i32x8 raw;
+    f32x4 part[FN], sb[BROW ? FN : 1];
+    float sa[4];
+    auto read_sb = [&](int st) {
+        const float* f = fb + st * (BM + BN);
+        if constexpr (BROW) {
+#pragma unroll
+            for (int j = 0; j < FN; ++j) sb[j] = *reinterpret_cast<const f32x4*>(f + j * 16 + lg * 4);
+        } else {
+            sb[0][0] = f[0];
+        }
+    };
+    auto add = [&](int i, int j, float s) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            acc[i][j][e] = fmaf(part[j][e], BROW ? s * sb[BROW ? j : 0][e] : s, acc[i][j][e]);
+    };
+
+    if (t.nkb > 0) {
+        issue(0, 0);
+        if (t.nkb > 1) issue(1, 1);
+        if (S > 2 && t.nkb > 2) {
+            issue(2, 2);
+            asm volatile("s_waitcnt vmcnt(%0)" ::"n"(2 * (4 + CB)) : "memory");  // at least block 0's
+            __builtin_amdgcn_s_barrier();
+            asm volatile("" ::: "memory");
+        } else {
+            published(false);
+        }
+        if (subs > 0) {
+#pragma unroll
+            for (int j = 0; j < FN; ++j) {
+                const i32x8 r = codes_of(bw + j * 16 * kBlock);
+#pragma unroll
+                for (int u = 0; u < 4; ++u) bf[j][u] = widen8<TB>(r[2 * u], r[2 * u + 1]);
+            }
+            raw = codes_of(aw);
+            sa[0] = fa[0];
+            read_sb(0);
+        }
+    }
+    int st = 0;
+    for (int kb = 0; kb < t.nkb; ++kb) {
+        const int next = st + 1 == S ? 0 : st + 1;
+#pragma unroll
+        for (int i = 0; i < FM - 1; ++i) {
+            if (i < subs) {
+#pragma unroll
+                for (int u = 0; u < 4; ++u) af[u] = widen8<TA>(raw[2 * u], raw[2 * u + 1]);
+                raw = codes_of(aw + st * STAGE_A + (i + 1) * 16 * kBlock);
+                sa[i + 1] = fa[st * (BM + BN) + (i + 1) * 16];
+                const float s = BROW ? sa[i] : sa[i] * sb[0][0];
+#pragma unroll
+                for (int u = 0; u < 4; ++u)
+#pragma unroll
+                    for (int j = 0; j < FN; ++j)
+                        part[j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(bf[j][u], af[u], u ? part[j] : f32x4{0, 0, 0, 0}, 0, 0, 0);
+#pragma unroll
+                for (int j = 0; j < FN; ++j) add(i, j, s);
+            }
+        }
+        if (subs == FM) {
+#pragma unroll
+            for (int u = 0; u < 4; ++u) af[u] = widen8<TA>(raw[2 * u], raw[2 * u + 1]);
+        }
+        const float s3 = BROW ? sa[3] : sa[3] * sb[0][0];
+        if (kb + 1 < t.nkb) {
+            // block kb + 1 is there, and everybody has read the last of block kb from its stage
+            published(kb + S - 1 < t.nkb);
+            if (kb + S < t.nkb) issue(kb + S, st);
+        }
+        if (subs > 0) {
+            // past the end of k the reads find old data, which nothing uses
+            raw = codes_of(aw + next * STAGE_A);
+#pragma unroll
+            for (int j = 0; j < FN; ++j) {
+                const i32x8 r = codes_of(bw + next * STAGE_B + j * 16 * kBlock);
+                if (subs == FM) {
+#pragma unroll
+                    for (int u = 0; u < 4; ++u)
+                        part[j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(bf[j][u], af[u], u ? part[j] : f32x4{0, 0, 0, 0}, 0, 0, 0);
+                }
+#pragma unroll
+                for (int u = 0; u < 4; ++u) bf[j][u] = widen8<TB>(r[2 * u], r[2 * u + 1]);
+            }
+            if (subs == FM) {
+#pragma unroll
+                for (int j = 0; j < FN; ++j) add(FM - 1, j, s3);
+            }
+            sa[0] = fa[next * (BM + BN)];
+            read_sb(next);
+        }
+        st = next;
+    }
+
+    // ---- C through LDS, 16 rows of the wave's 64 columns at a time
+    __builtin_amdgcn_s_barrier();  // every wave has read its last fragments
+    asm volatile("" ::: "memory");
+    float* const stage = reinterpret_cast<float*>(lds) + wave * (16 * ROW);
+    float* const C = static_cast<float*>(g.C);
+    const int n = t.n0 + wn * 64 + l16 * 4;
+    const bool whole = t.n0 + BN <= g.N;
+    const uint64_t live = live_rows(g, t, t.m0 + wm * 64);
+#pragma unroll
+    for (int i = 0; i < FM; ++i) {
+        if (i >= subs) continue;
+#pragma unroll
+        for (int j = 0; j < FN; ++j) *reinterpret_cast<f32x4*>(stage + l16 * ROW + j * 16 + lg * 4) = acc[i][j];
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+#pragma unroll
+        for (int p = 0; p < 4; ++p) {
+            const int row = p * 4 + lg, m = t.m0 + wm * 64 + i * 16 + row;
+            f32x4 v = *reinterpret_cast<const f32x4*>(stage + row * ROW + l16 * 4);
+            if (!((live >> (i * 16 + row)) & 1)) v = f32x4{0, 0, 0, 0};
+            float* const c = C + (size_t)m * (size_t)g.ldc + n;
+            if (m >= t.m_end) continue;
+            if (whole) {
+                __builtin_memcpy(c, &v, 16);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (n + e < g.N) c[e] = v[e];
+            }
+        }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    }
+}
+
+// ---------------------------------------------------------------------------- fp32 sums, any layout
+// The same tiles for rows at any byte address and for operands with adjacent rows, on 2 x 2
+// tiles of v_mfma_f32_32x32x16_f16 for each wave: the codes go through registers and are
+// widened on their way into LDS, once for the whole workgroup. LDS holds one
+// block of k (64 KB of halves, so that two workgroups share a compute unit and each fills
+// the other's waits), the next block's codes wait in registers.
+//
+// Rows of 256 bytes, 16-byte chunk c of row r at c ^ (r & 15): the 16 lanes of a read phase
+// see one chunk of 16 rows that differ in the low bits, so all places. An operand with
+// adjacent rows (TR, as below) is held as 128 rows of k, its 32-byte units of 16 rows
+// permuted by 2 (k & 3), and read through ds_read_b64_tr_b16.
+template <int TA, int TB, bool BROW, int TR>
+__global__ __launch_bounds__(256, 2) void block_full(BlockArgs g) {
+    constexpr int BM = 128, BN = 128, FM = 2, FN = 2, ROW = 68;
+    constexpr bool TRB = (TR & 1) != 0, TRA = (TR & 2) != 0;
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * 128 * 256 + (BM + BN) * 4];
+    uint8_t* const sA = lds;
+    uint8_t* const sB = lds + 128 * 256;
+    float* const fS = reinterpret_cast<float*>(lds + 2 * 128 * 256);
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wm = wave >> 1, wn = wave & 1;
+    const int l32 = lane & 31, lh = lane >> 5, l16 = lane & 15, lg = lane >> 4;
+
+    BlockTile t;
+    const bool any = block_tile_of<BM, BN>(g, t);
+    if (g.mode == BLOCK_EXPERTS) clear_tail(g);
+    if (!any) return;
+
+    // ---- this thread's codes: chunk tid & 7 of rows (tid >> 3) + 32 c, c = 0 .. 3; rows of C
+    // and columns of k, or the other way round for an operand with adjacent rows
+    const int chunk = (tid & 7) * 16;
+    const uint8_t* pa[4];
+    const uint8_t* pb[4];
+    const size_t step_a = TRA ? (size_t)kBlock * (size_t)g.lda : kBlock;
+    const size_t step_b = TRB ? (size_t)kBlock * (size_t)g.ldb : kBlock;
+    const int va = g.M - t.m0 - chunk, vb = g.N - t.n0 - chunk;  // bytes of a transposed chunk inside the matrix
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+        const int row = (tid >> 3) + 32 * c;
+        if constexpr (TRA) {
+            pa[c] = g.A + ((size_t)t.kb0 * kBlock + row) * (size_t)g.lda + (t.m0 + chunk);
+        } else {
+            const int r = max(block_a_row(g, t, min(t.m0 + row, t.m_end - 1)), 0);
+            pa[c] = g.A + (size_t)r * (size_t)g.lda + (size_t)t.kb0 * kBlock + chunk;
+        }
+        if constexpr (TRB) pb[c] = g.B + ((size_t)t.kb0 * kBlock + row) * (size_t)g.ldb + (t.n0 + chunk);
+        else pb[c] = g.B + (size_t)min(t.n0 + row, g.N - 1) * (size_t)g.ldb + (size_t)t.kb0 * kBlock + chunk;
+    }
+    const float* ps;
+    int64_t ps_step;
+    if (wave < 2) {
+        const int r = max(block_a_row(g, t, min(t.m0 + tid, t.m_end - 1)), 0);
+        ps = g.SA + (size_t)(r >> g.a_shift) * (size_t)g.sa_row + (size_t)t.kb0 * (size_t)g.sa_blk;
+        ps_step = g.sa_blk;
+    } else {
+        const int n = min(t.n0 + tid - 128, g.N - 1);
+        ps = g.SB + (size_t)(n >> g.b_shift) * (size_t)g.sb_row + (size_t)t.kb0 * (size_t)g.sb_blk;
+        ps_step = g.sb_blk;
+    }
+
+    u32x4 ra[4], rb[4];
+    float rs;
+    auto load = [&](int kb) {
+        const int rem = kb == t.nkb - 1 ? t.krem : kBlock;
+        rs = *ps;
+        ps += ps_step;
+        const bool plain = rem == kBlock && (!TRA || t.m0 + BM <= g.M) && (!TRB || t.n0 + BN <= g.N);
+        if (plain) {  // whole chunks, without a branch for each
+#pragma unroll
+            for (int c = 0; c < 4; ++c) __builtin_memcpy(&ra[c], pa[c], 16);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) __builtin_memcpy(&rb[c], pb[c], 16);
+        } else {
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                const int row = (tid >> 3) + 32 * c;
+                ra[c] = load_codes(pa[c], TRA ? (row < rem ? va : 0) : rem - chunk);
+                rb[c] = load_codes(pb[c], TRB ? (row < rem ? vb : 0) : rem - chunk);
+            }
+        }
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            pa[c] += step_a;
+            pb[c] += step_b;
+        }
+    };
+    auto widen_to = [&](uint8_t* s, u32x4 v, int row, auto type, bool tr) {
+        constexpr int T = decltype(type)::value;
+        const f16x8 x = widen8<T>((int)v[0], (int)v[1]), y = widen8<T>((int)v[2], (int)v[3]);
+        if (tr) {
+            uint8_t* p = s + row * 256 + (((tid & 7) ^ (2 * (row & 3))) << 5);
+            *reinterpret_cast<f16x8*>(p) = x;
+            *reinterpret_cast<f16x8*>(p + 16) = y;
+        } else {
+            const int at = ((2 * (tid & 7)) ^ (row & 15)) << 4;
+            *reinterpret_cast<f16x8*>(s + row * 256 + at) = x;
+            *reinterpret_cast<f16x8*>(s + row * 256 + (at ^ 16)) = y;
+        }
+    };
+    auto settle = [&]() {
+        fS[tid] = rs;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            const int row = (tid >> 3) + 32 * c;
+            widen_to(sA, ra[c], row, std::integral_constant<int, TA>{}, TRA);
+            widen_to(sB, rb[c], row, std::integral_constant<int, TB>{}, TRB);
+        }
+    };
+
+    // ---- fragments: step u, lane (l32, lh): k 16u + 8lh .. +7 of row l32 of a subtile
+    auto frag = [&](const uint8_t* s, int sub, int u) {
+        return *reinterpret_cast<const f16x8*>(s + (sub * 32 + l32) * 256 + (((2 * u + lh) ^ l16) << 4));
+    };
+    auto frag_tr = [&](const uint8_t* s, int sub, int u) {
+        const int k = 8 * lh + (l16 >> 2);  // of rows 16u + k and + 4
+        const uint8_t* p = s + (16 * u + k) * 256 + (((2 * sub + (lg & 1)) ^ (2 * (k & 3))) << 5) + (l16 & 3) * 8;
+        const fp16x4_t x = __builtin_amdgcn_ds_read_tr16_b64_v4f16(DG_LDS_PTR(fp16x4_t, p));
+        const fp16x4_t y = __builtin_amdgcn_ds_read_tr16_b64_v4f16(DG_LDS_PTR(fp16x4_t, p + 4 * 256));
+        const u32x2 a = __builtin_bit_cast(u32x2, x), b = __builtin_bit_cast(u32x2, y);
+        return __builtin_bit_cast(f16x8, u32x4{a[0], a[1], b[0], b[1]});
+    };
+    auto a_frag = [&](int i, int u) {
+        if constexpr (TRA) return frag_tr(sA, wm * FM + i, u);
+        else return frag(sA, wm * FM + i, u);
+    };
+    auto b_frag = [&](int j, int u) {
+        if constexpr (TRB) return frag_tr(sB, wn * FN + j, u);
+        else return frag(sB, wn * FN + j, u);
+    };
+
+    f32x16 acc[FM][FN];
+#pragma unroll
+    for (int i = 0; i < FM; ++i)
+#pragma unroll
+        for (int j = 0; j < FN; ++j) acc[i][j] = f32x16{0};
+    // subtiles of 32 rows of this wave that hold rows of C
+    const int subs = min(max((t.m_end - t.m0 + 31) / 32 - wm * FM, 0), FM);
+
+    if (t.nkb > 0) {
+        load(0);
+        settle();
+    }
+    for (int kb = 0; kb < t.nkb; ++kb) {
+        __syncthreads();
+        if (kb + 1 < t.nkb) load(kb + 1);
+        auto block = [&](auto whole_tag) {
+            constexpr bool WHOLE = decltype(whole_tag)::value;
+            f32x16 part[FM][FN];
+            f16x8 af[2][FM], bf[2][FN];
+#pragma unroll
+            for (int j = 0; j < FN; ++j) bf[0][j] = b_frag(j, 0);
+#pragma unroll
+            for (int i = 0; i < FM; ++i) af[0][i] = a_frag(i, 0);
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+#pragma unroll
+                for (int i = 0; i < FM; ++i)
+#pragma unroll
+                    for (int j = 0; j < FN; ++j) {
+                        if (WHOLE || i < subs)
+                            part[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(bf[u & 1][j], af[u & 1][i],
+                                                                                u ? part[i][j] : f32x16{0}, 0, 0, 0);
+                        if (i == 0 && j == 0 && u < 7) {
+                            // the next step's fragments, behind the wait for this one's
+                            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                            for (int q = 0; q < FN; ++q) bf[(u + 1) & 1][q] = b_frag(q, u + 1);
+#pragma unroll
+                            for (int q = 0; q < FM; ++q) af[(u + 1) & 1][q] = a_frag(q, u + 1);
+                            __builtin_amdgcn_sched_barrier(0);
+                        }
+                    }
+            }
+#pragma unroll
+            for (int i = 0; i < FM; ++i) {
+                const float sa = fS[wm * 64 + i * 32 + l32];
+#pragma unroll
+                for (int j = 0; j < FN; ++j) {
+                    if (!(WHOLE || i < subs)) continue;
+                    const float* sb = fS + BM + wn * 64 + j * 32 + lh * 4;
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        f32x4 s;
+                        if constexpr (BROW) s = *reinterpret_cast<const f32x4*>(sb + q * 8) * sa;
+                        else s = f32x4{1, 1, 1, 1} * (sa * fS[BM + wn * 64]);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) acc[i][j][4 * q + e] = fmaf(part[i][j][4 * q + e], s[e], acc[i][j][4 * q + e]);
+                    }
+                }
+            }
+        };
+        if (subs == FM) block(std::true_type{});
+        else if (subs > 0) block(std::false_type{});
+        __syncthreads();
+        if (kb + 1 < t.nkb) settle();
+    }
+
+    // ---- C through LDS, 32 rows of the wave's 64 columns at a time (no wave reads or writes
+    // the operands' stage any more)
+    float* const stage = reinterpret_cast<float*>(lds) + wave * (32 * ROW);
+    float* const C = static_cast<float*>(g.C);
+    const int n = t.n0 + wn * 64 + l16 * 4;
+    const bool whole = t.n0 + BN <= g.N;
+#pragma unroll
+    for (int i = 0; i < FM; ++i) {
+        if (i >= subs) continue;
+        const int first = t.m0 + wm * 64 + i * 32;
+        const uint64_t live = live_rows(g, t, first);
+#pragma unroll
+        for (int j = 0; j < FN; ++j)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                f32x4 v = {acc[i][j][q * 4], acc[i][j][q * 4 + 1], acc[i][j][q * 4 + 2], acc[i][j][q * 4 + 3]};
+                if (t.bad) v = f32x4{1, 1, 1, 1} * __builtin_nanf("");
+                *reinterpret_cast<f32x4*>(stage + l32 * ROW + j * 32 + q * 8 + lh * 4) = v;
+            }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+#pragma unroll
+        for (int p = 0; p < 8; ++p) {
+            const int row = p * 4 + lg, m = first + row;
+            f32x4 v = *reinterpret_cast<const f32x4*>(stage + row * ROW + l16 * 4);
+            if (!((live >> row) & 1)) v = f32x4{0, 0, 0, 0};
+            float* const c = C + (size_t)m * (size_t)g.ldc + n;
+            if (m >= t.m_end) continue;
+            if (whole) {
+                __builtin_memcpy(c, &v, 16);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (n + e < g.N) c[e] = v[e];
+            }
+        }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    }
+}
+
 // ---------------------------------------------------------------------------- tiles
 // BM x BN tiles on WM x WN waves, each wave SM x SJ subtiles of 32 x 32. LDS holds two
 // stages of one block of k: rows of 128 bytes whose 16-byte chunks are permuted by
@@ -535,7 +1037,7 @@ __global__ __launch_bounds__(512) void block_wide(BlockArgs g) {
 // 16 lanes, lane i addresses 8 bytes of row k0 + i/2 at half i%2 of a chunk and receives
 // column i of the 8 rows. The 32 lanes of a phase then touch 8 rows x 32 bytes in 8
 // different places of the 256-byte bank period.
-template <int TA, int TB, bool FULL, bool BROW, int BM, int BN, int WM, int WN, bool DIRECT, int TR = 0>
+template <int TA, int TB, bool BROW, int BM, int BN, int WM, int WN, bool DIRECT, int TR = 0>
 __global__ __launch_bounds__(WM* WN * 64) void block_tile(BlockArgs g) {
     constexpr int NW = WM * WN, SM = BM / 32 / WM, SJ = BN / 32 / WN;
     constexpr int CA = BM / 8 / NW, CB = BN / 8 / NW;  // 1 KB copies (8 rows) per wave
@@ -734,51 +1236,19 @@ __global__ __launch_bounds__(WM* WN * 64) void block_tile(BlockArgs g) {
         // between its instructions)
         auto block = [&](auto whole_tag) {
             constexpr bool WHOLE = decltype(whole_tag)::value;
-            if constexpr (!FULL) {
-                i32x8 bf[SJ][2];
+            i32x8 bf[SJ][2];
 #pragma unroll
-                for (int j = 0; j < SJ; ++j)
+            for (int j = 0; j < SJ; ++j)
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) bf[j][h] = b_frag(st, j, h);
+                for (int h = 0; h < 2; ++h) bf[j][h] = b_frag(st, j, h);
 #pragma unroll
-                for (int i = 0; i < SM; ++i) {
-                    if (WHOLE || i < subs) {
-                        const i32x8 af0 = a_frag(st, i, 0), af1 = a_frag(st, i, 1);
-#pragma unroll
-                        for (int j = 0; j < SJ; ++j)
-                            add(i, j, mfma_32<TB, TA>(bf[j][1], af1, mfma_32<TB, TA>(bf[j][0], af0, f32x16{0})));
-                    }
-                }
-            } else {
-                f32x16 part[SM][SJ];
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    i32x8 af[SM], bf[SJ];
-#pragma unroll
-                    for (int i = 0; i < SM; ++i) af[i] = a_frag(st, i, h);
-#pragma unroll
-                    for (int j = 0; j < SJ; ++j) bf[j] = b_frag(st, j, h);
-#pragma unroll
-                    for (int u = 0; u < 4; ++u) {
-                        f16x8 aw[SM], bw[SJ];
-#pragma unroll
-                        for (int i = 0; i < SM; ++i) aw[i] = widen8<TA>(af[i][2 * u], af[i][2 * u + 1]);
-#pragma unroll
-                        for (int j = 0; j < SJ; ++j) bw[j] = widen8<TB>(bf[j][2 * u], bf[j][2 * u + 1]);
-#pragma unroll
-                        for (int i = 0; i < SM; ++i)
-#pragma unroll
-                            for (int j = 0; j < SJ; ++j)
-                                if (WHOLE || i < subs)
-                                    part[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(
-                                        bw[j], aw[i], h == 0 && u == 0 ? f32x16{0} : part[i][j], 0, 0, 0);
-                    }
-                }
-#pragma unroll
-                for (int i = 0; i < SM; ++i)
+            for (int i = 0; i < SM; ++i) {
+                if (WHOLE || i < subs) {
+                    const i32x8 af0 = a_frag(st, i, 0), af1 = a_frag(st, i, 1);
 #pragma unroll
                     for (int j = 0; j < SJ; ++j)
-                        if (WHOLE || i < subs) add(i, j, part[i][j]);
+                        add(i, j, mfma_32<TB, TA>(bf[j][1], af1, mfma_32<TB, TA>(bf[j][0], af0, f32x16{0})));
+                }
             }
         };
         if (subs == SM) block(std::true_type{});
@@ -914,28 +1384,42 @@ __global__ __launch_bounds__(512) void block_skinny(BlockArgs g) {
 }
 
 // Operands with adjacent rows: one kernel for either kind of scales, each row's its own.
-template <int TA, int TB, bool FULL, int TR>
+template <int TA, int TB, int TR>
 int launch_block_tr(const BlockPlan& p, const BlockArgs& a, dim3 grid, hipStream_t s) {
-    return p.direct ? launch_status(block_tile<TA, TB, FULL, true, 128, 128, 2, 2, true, TR>, grid, dim3(256), s, a)
-                    : launch_status(block_tile<TA, TB, FULL, true, 128, 128, 2, 2, false, TR>, grid, dim3(256), s, a);
+    return p.direct ? launch_status(block_tile<TA, TB, true, 128, 128, 2, 2, true, TR>, grid, dim3(256), s, a)
+                    : launch_status(block_tile<TA, TB, true, 128, 128, 2, 2, false, TR>, grid, dim3(256), s, a);
 }
 
 template <int TA, int TB, bool FULL>
 int launch_block_full(const BlockPlan& p, const BlockArgs& a, dim3 grid, hipStream_t s) {
-    if (p.tr == 1) return launch_block_tr<TA, TB, FULL, 1>(p, a, grid, s);
-    if (p.tr == 2) return launch_block_tr<TA, TB, FULL, 2>(p, a, grid, s);
-    if (p.tr == 3) return launch_block_tr<TA, TB, FULL, 3>(p, a, grid, s);
     const bool brow = a.b_shift == 0;
-    if constexpr (!FULL)
+    if constexpr (FULL) {
+        if (p.tr == 1) return launch_status(block_full<TA, TB, true, 1>, grid, dim3(256), s, a);
+        if (p.tr == 2) return launch_status(block_full<TA, TB, true, 2>, grid, dim3(256), s, a);
+        if (p.tr == 3) return launch_status(block_full<TA, TB, true, 3>, grid, dim3(256), s, a);
+        if (p.kernel == BLOCK_TILE128 && p.direct && p.small)
+            return brow ? launch_status(block_full_direct<TA, TB, true, 2, 2>, grid, dim3(256), s, a)
+                        : launch_status(block_full_direct<TA, TB, false, 2, 2>, grid, dim3(256), s, a);
+        if (p.kernel == BLOCK_TILE256)
+            return brow ? launch_status(block_full_direct<TA, TB, true, 4, 3>, grid, dim3(512), s, a)
+                        : launch_status(block_full_direct<TA, TB, false, 4, 3>, grid, dim3(512), s, a);
+        if (p.kernel == BLOCK_TILE128)
+            return brow ? launch_status(block_full<TA, TB, true, 0>, grid, dim3(256), s, a)
+                        : launch_status(block_full<TA, TB, false, 0>, grid, dim3(256), s, a);
+    } else {
+        if (p.tr == 1) return launch_block_tr<TA, TB, 1>(p, a, grid, s);
+        if (p.tr == 2) return launch_block_tr<TA, TB, 2>(p, a, grid, s);
+        if (p.tr == 3) return launch_block_tr<TA, TB, 3>(p, a, grid, s);
         if (p.kernel == BLOCK_TILE256)
             return brow ? launch_status(block_wide<TA, TB, true>, grid, dim3(512), s, a)
                         : launch_status(block_wide<TA, TB, false>, grid, dim3(512), s, a);
-    if (p.kernel == BLOCK_TILE128) {
-        if (p.direct)
-            return brow ? launch_status(block_tile<TA, TB, FULL, true, 128, 128, 2, 2, true>, grid, dim3(256), s, a)
-                        : launch_status(block_tile<TA, TB, FULL, false, 128, 128, 2, 2, true>, grid, dim3(256), s, a);
-        return brow ? launch_status(block_tile<TA, TB, FULL, true, 128, 128, 2, 2, false>, grid, dim3(256), s, a)
-                    : launch_status(block_tile<TA, TB, FULL, false, 128, 128, 2, 2, false>, grid, dim3(256), s, a);
+        if (p.kernel == BLOCK_TILE128) {
+            if (p.direct)
+                return brow ? launch_status(block_tile<TA, TB, true, 128, 128, 2, 2, true>, grid, dim3(256), s, a)
+                            : launch_status(block_tile<TA, TB, false, 128, 128, 2, 2, true>, grid, dim3(256), s, a);
+            return brow ? launch_status(block_tile<TA, TB, true, 128, 128, 2, 2, false>, grid, dim3(256), s, a)
+                        : launch_status(block_tile<TA, TB, false, 128, 128, 2, 2, false>, grid, dim3(256), s, a);
+        }
     }
     if (p.direct)
         return p.bm == 16   ? launch_status(block_skinny<TA, TB, FULL, 1, true>, grid, dim3(512), s, a)
