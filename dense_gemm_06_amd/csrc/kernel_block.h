@@ -71,6 +71,15 @@ __device__ __forceinline__ f16x8 widen8(int lo, int hi) {
     return __builtin_bit_cast(f16x8, u32x4{w[0], w[1], w[2], w[3]});
 }
 
+// Two codes (of the low or the high half of a dword) as two fp16 numbers.
+template <int T>
+__device__ __forceinline__ uint32_t widen2(int v, bool high) {
+    if constexpr (T == 0)
+        return high ? __builtin_bit_cast(uint32_t, (f16x2)__builtin_amdgcn_cvt_scalef32_pk_f16_fp8(v, 1.0f, true))
+                    : __builtin_bit_cast(uint32_t, (f16x2)__builtin_amdgcn_cvt_scalef32_pk_f16_fp8(v, 1.0f, false));
+    else return __builtin_amdgcn_perm(0u, (uint32_t)v, high ? 0x030c020cu : 0x010c000cu);
+}
+
 // One workgroup's piece of a product: rows m0 .. m_end-1 of C (in whole tiles of BM),
 // columns from n0, blocks kb0 .. kb0+nkb-1 of k, the last one holding krem elements.
 struct BlockTile {
@@ -557,11 +566,12 @@ __global__ __launch_bounds__(512) void block_wide(BlockArgs g) {
 // Vector and matrix instructions are even (with a scale for each row of B: 256 of 4 cycles
 // and 64 of 16 for each wave and block); widening on the way into LDS instead halves the
 // conversions, but its writes and conflicts kept LDS busy 80% longer than the matrix cores
-// (272 against 237 us at 2056 x 4000 x 8176).
+// (271 against 219 us at 2056 x 4000 x 8176 with one workgroup of each).
 template <int TA, int TB, bool BROW, int WM, int S>
 __global__ __launch_bounds__(WM * 128, 2) void block_full_direct(BlockArgs g) {
     constexpr int NW = 2 * WM, BM = 64 * WM, BN = 128, FM = 4, FN = 4, ROW = 68;
     constexpr int CB = BN / 8 / NW;  // copies of 1 KB (8 rows) of B for each wave; 4 of A
+    constexpr int AHEAD = WM == 2 ? 1 : 2;  // fragments of codes read ahead (as registers allow)
     constexpr int STAGE_A = BM * kBlock, STAGE_B = BN * kBlock, STAGE_S = (BM + BN) * 4;
     __shared__ __attribute__((aligned(1024))) uint8_t lds[S * (STAGE_A + STAGE_B + STAGE_S)];
     uint8_t* const sA = lds;
@@ -656,13 +666,12 @@ __global__ __launch_bounds__(WM * 128, 2) void block_full_direct(BlockArgs g) {
     for (int i = 0; i < FM; ++i)
 #pragma unroll
         for (int j = 0; j < FN; ++j) acc[i][j] = t.bad ? f32x4{1, 1, 1, 1} * __builtin_nanf("") : f32x4{0, 0, 0, 0};
-    // subtiles of 16 rows of this wave that hold rows of C: the others are not multiplied
-    const int subs = min(max((t.m_end - t.m0 + 15) / 16 - wm * FM, 0), FM);
+    const bool active = t.m0 + wm * 64 < t.m_end;  // this wave has rows of C
 
-    f16x8 af[4], bf[FN][4];
-    i32x8 raw;
-    f32x4 part[FN], sb[BROW ? FN : 1];
-    float sa[4];
+    u32x4 af[4], bf[FN][4];    // halves: step u (32 k) of a fragment
+    i32x8 raw[2], rawb[2];     // codes
+    f32x4 part[2][FN], sb[BROW ? FN : 1];
+    float sa[2];
     auto read_sb = [&](int st) {
         const float* f = fb + st * (BM + BN);
         if constexpr (BROW) {
@@ -672,10 +681,18 @@ __global__ __launch_bounds__(WM * 128, 2) void block_full_direct(BlockArgs g) {
             sb[0][0] = f[0];
         }
     };
-    auto add = [&](int i, int j, float s) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-            acc[i][j][e] = fmaf(part[j][e], BROW ? s * sb[BROW ? j : 0][e] : s, acc[i][j][e]);
+    // one number of a part, scaled and added
+    auto add1 = [&](int i, int q, float s) {
+        const int j = q >> 2, e = q & 3;
+        acc[i][j][e] = fmaf(part[i & 1][j][e], BROW ? s * sb[BROW ? j : 0][e] : s, acc[i][j][e]);
+    };
+    // dword d (two codes) of step u of a fragment
+    auto widen_a = [&](const i32x8& r, int u, int d) { af[u][d] = widen2<TA>(r[2 * u + (d >> 1)], d & 1); };
+    auto widen_b = [&](const i32x8& r, int j, int u, int d) { bf[j][u][d] = widen2<TB>(r[2 * u + (d >> 1)], d & 1); };
+    auto mfma = [&](int i, int j, int u) {
+        part[i & 1][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, bf[j][u]),
+                                                                __builtin_bit_cast(f16x8, af[u]),
+                                                                u ? part[i & 1][j] : f32x4{0, 0, 0, 0}, 0, 0, 0);
     };
 
     if (t.nkb > 0) {
@@ -689,70 +706,97 @@ __global__ __launch_bounds__(WM * 128, 2) void block_full_direct(BlockArgs g) {
         } else {
             published(false);
         }
-        if (subs > 0) {
+        if (active) {
 #pragma unroll
             for (int j = 0; j < FN; ++j) {
                 const i32x8 r = codes_of(bw + j * 16 * kBlock);
 #pragma unroll
-                for (int u = 0; u < 4; ++u) bf[j][u] = widen8<TB>(r[2 * u], r[2 * u + 1]);
+                for (int q = 0; q < 16; ++q) widen_b(r, j, q >> 2, q & 3);
             }
-            raw = codes_of(aw);
+            raw[0] = codes_of(aw);
+            if (AHEAD > 1) raw[1] = codes_of(aw + 16 * kBlock);
             sa[0] = fa[0];
+#pragma unroll
+            for (int q = 0; q < 16; ++q) widen_a(raw[0], q >> 2, q & 3);
             read_sb(0);
         }
     }
+    // A step is 16 instructions of the matrix core, and behind each a few of the vector unit
+    // that run in its shadow, pinned there: a number of the step before's part (first of the
+    // block: of the last block's) scaled and added, two codes of the next fragment widened
+    // over those just used. (In one piece each, with the other wave of the SIMD left to fill
+    // the gaps, the two units hardly overlapped: 5300 cycles a block for 2048 of matrix and
+    // 2400 of vector instructions.)
+    float s_last = 0;  // scale of the last step's part
     int st = 0;
     for (int kb = 0; kb < t.nkb; ++kb) {
         const int next = st + 1 == S ? 0 : st + 1;
+        if (active) {
 #pragma unroll
-        for (int i = 0; i < FM - 1; ++i) {
-            if (i < subs) {
+            for (int i = 0; i < FM - 1; ++i) {
+                // codes AHEAD fragments ahead; the scale of the next
+                if (i + AHEAD < FM) raw[(i + AHEAD) & 1] = codes_of(aw + st * STAGE_A + (i + AHEAD) * 16 * kBlock);
+                const float s = sa[i & 1];
+                sa[(i + 1) & 1] = fa[st * (BM + BN) + (i + 1) * 16];
 #pragma unroll
-                for (int u = 0; u < 4; ++u) af[u] = widen8<TA>(raw[2 * u], raw[2 * u + 1]);
-                raw = codes_of(aw + st * STAGE_A + (i + 1) * 16 * kBlock);
-                sa[i + 1] = fa[st * (BM + BN) + (i + 1) * 16];
-                const float s = BROW ? sa[i] : sa[i] * sb[0][0];
+                for (int q = 0; q < 16; ++q) {
+                    mfma(i, q & 3, q >> 2);
+                    if (i > 0) add1(i - 1, q, s_last);
+                    else if (kb > 0) add1(FM - 1, q, s_last);
+                    if (q >= 4) widen_a(raw[(i + 1) & 1], (q >> 2) - 1, q & 3);
+                    __builtin_amdgcn_sched_barrier(0);
+                }
 #pragma unroll
-                for (int u = 0; u < 4; ++u)
-#pragma unroll
-                    for (int j = 0; j < FN; ++j)
-                        part[j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(bf[j][u], af[u], u ? part[j] : f32x4{0, 0, 0, 0}, 0, 0, 0);
-#pragma unroll
-                for (int j = 0; j < FN; ++j) add(i, j, s);
+                for (int q = 0; q < 4; ++q) widen_a(raw[(i + 1) & 1], 3, q);
+                if (i == 0) read_sb(st);
+                s_last = BROW ? s : s * sb[0][0];
+                __builtin_amdgcn_sched_barrier(0);
             }
         }
-        if (subs == FM) {
-#pragma unroll
-            for (int u = 0; u < 4; ++u) af[u] = widen8<TA>(raw[2 * u], raw[2 * u + 1]);
-        }
-        const float s3 = BROW ? sa[3] : sa[3] * sb[0][0];
         if (kb + 1 < t.nkb) {
             // block kb + 1 is there, and everybody has read the last of block kb from its stage
             published(kb + S - 1 < t.nkb);
             if (kb + S < t.nkb) issue(kb + S, st);
         }
-        if (subs > 0) {
+        if (active) {
             // past the end of k the reads find old data, which nothing uses
-            raw = codes_of(aw + next * STAGE_A);
+            rawb[0] = codes_of(bw + next * STAGE_B);
+            rawb[1] = codes_of(bw + next * STAGE_B + 16 * kBlock);
+            const float s = sa[(FM - 1) & 1];
+            __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
             for (int j = 0; j < FN; ++j) {
-                const i32x8 r = codes_of(bw + next * STAGE_B + j * 16 * kBlock);
-                if (subs == FM) {
 #pragma unroll
-                    for (int u = 0; u < 4; ++u)
-                        part[j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(bf[j][u], af[u], u ? part[j] : f32x4{0, 0, 0, 0}, 0, 0, 0);
+                for (int u = 0; u < 4; ++u) {
+                    mfma(FM - 1, j, u);
+                    add1(FM - 2, 4 * j + u, s_last);
+                    if (j > 0) {
+#pragma unroll
+                        for (int d = 0; d < 4; ++d) widen_b(rawb[(j - 1) & 1], j - 1, u, d);
+                    }
+                    __builtin_amdgcn_sched_barrier(0);
                 }
-#pragma unroll
-                for (int u = 0; u < 4; ++u) bf[j][u] = widen8<TB>(r[2 * u], r[2 * u + 1]);
+                if (j == 1) rawb[0] = codes_of(bw + next * STAGE_B + 2 * 16 * kBlock);
+                if (j == 2) {
+                    rawb[1] = codes_of(bw + next * STAGE_B + 3 * 16 * kBlock);
+                    raw[0] = codes_of(aw + next * STAGE_A);
+                    if (AHEAD > 1) raw[1] = codes_of(aw + next * STAGE_A + 16 * kBlock);
+                    sa[0] = fa[next * (BM + BN)];
+                }
+                __builtin_amdgcn_sched_barrier(0);
             }
-            if (subs == FM) {
 #pragma unroll
-                for (int j = 0; j < FN; ++j) add(FM - 1, j, s3);
-            }
-            sa[0] = fa[next * (BM + BN)];
-            read_sb(next);
+            for (int q = 0; q < 16; ++q) widen_b(rawb[1], 3, q >> 2, q & 3);
+#pragma unroll
+            for (int q = 0; q < 16; ++q) widen_a(raw[0], q >> 2, q & 3);
+            s_last = BROW ? s : s * sb[0][0];
+            __builtin_amdgcn_sched_barrier(0);
         }
         st = next;
+    }
+    if (active && t.nkb > 0) {
+#pragma unroll
+        for (int q = 0; q < 16; ++q) add1(FM - 1, q, s_last);
     }
 
     // ---- C through LDS, 16 rows of the wave's 64 columns at a time
@@ -765,7 +809,7 @@ __global__ __launch_bounds__(WM * 128, 2) void block_full_direct(BlockArgs g) {
     const uint64_t live = live_rows(g, t, t.m0 + wm * 64);
 #pragma unroll
     for (int i = 0; i < FM; ++i) {
-        if (i >= subs) continue;
+        if (!active) continue;
 #pragma unroll
         for (int j = 0; j < FN; ++j) *reinterpret_cast<f32x4*>(stage + l16 * ROW + j * 16 + lg * 4) = acc[i][j];
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
