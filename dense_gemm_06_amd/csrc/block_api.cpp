@@ -184,7 +184,8 @@ int tr_of(const gemm_block_matrix& A, const gemm_block_matrix& B) {
 
 // Whether byte offsets within an operand fit 32 bits.
 bool small_call(const gemm_block_matrix& A, const gemm_block_matrix& B) {
-    return A.rows * A.ld < ((int64_t)1 << 32) && B.rows * B.ld < ((int64_t)1 << 32);
+    auto bytes = [](const gemm_block_matrix& m) { return (m.op == GEMM_OP_T ? m.cols : m.rows) * m.ld; };
+    return bytes(A) < ((int64_t)1 << 32) && bytes(B) < ((int64_t)1 << 32);
 }
 
 constexpr int64_t kCus = 256;
@@ -203,14 +204,16 @@ dg::BlockPlan block_plan(int64_t rows, int64_t n_products, int64_t N, int64_t K,
     if (rows <= 64 && tr == 0) {
         p.kernel = dg::BLOCK_SKINNY;
         p.bm = rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
-        p.bn = 16;
-        const int64_t wgs = n_products * ceil_div(N, 16);
+        p.bn = direct && p.bm == 16 && n_products * ceil_div(N, 64) >= 2 * kCus ? 64 : 16;
+        const int64_t wgs = n_products * ceil_div(N, p.bn);
         if (may_split && wgs < kCus) p.split = (int)std::max<int64_t>(1, std::min<int64_t>(kCus / wgs, nkb / 16));
     } else {
         // 256 rows (and 256 columns for C of 16 bits, 128 for fp32) where that leaves most
-        // compute units a tile
+        // compute units a tile; with few blocks of k two smaller fp32 tiles to a compute unit,
+        // one of which computes while the other loads or stores, are ahead (64 products of 2048 x
+        // 1024 over 512: 243 against 275 us)
         const int64_t big = n_products * ceil_div(rows, 256) * ceil_div(N, full ? 128 : 256);
-        const bool large = direct && small && tr == 0 && big >= kCus * 3 / 4;
+        const bool large = direct && small && (tr == 0 || (tr == 1 && full)) && big >= kCus * 3 / 4 && !(full && K <= 1024);
         p.kernel = large ? dg::BLOCK_TILE256 : dg::BLOCK_TILE128;
         p.bm = large ? 256 : 128;
         p.bn = large && !full ? 256 : 128;
@@ -259,7 +262,7 @@ int launch(const dg::BlockPlan& p, dg::BlockArgs& a, int64_t tiles, int type_a, 
         set_error("the product needs %lld workgroups, more than a launch holds", (long long)tiles);
         return GEMM_ERR_UNSUPPORTED;
     }
-    a.group_m = std::max(1, std::min(dg::default_group_m(a.tiles_m, a.tiles_n), a.tiles_m));
+    if (a.group_m == 0) a.group_m = std::max(1, std::min(dg::default_group_m(a.tiles_m, a.tiles_n), a.tiles_m));
     const dim3 grid((unsigned)tiles, (unsigned)a.k_split);
     const int rc = type_a == GEMM_E4M3 ? (type_b == GEMM_E4M3 ? dg::launch_block_e4m3_e4m3(p, a, grid, s)
                                                               : dg::launch_block_e4m3_e5m2(p, a, grid, s))
@@ -691,7 +694,7 @@ int gemm_experts_gradient(const gemm_block_matrix* A, const gemm_block_matrix* B
                           scale_range("B.scale", *B), range("plan.offsets", plan->offsets, (uint64_t)(E + 1) * 4)}));
     DG_TRY(check_device());
     const bool direct = direct_rows(*A, 1) && direct_rows(*B, 1), small = small_call(*A, *B);
-    const dg::BlockPlan p = block_plan(M, E, N, A->cols, direct, small, out_dtype == GEMM_F32, tr_of(*A, *B), false);
+    const dg::BlockPlan p = block_plan(M, E, N, ceil_div(plan->capacity, E), direct, small, out_dtype == GEMM_F32, tr_of(*A, *B), false);
     dg::BlockArgs a = block_args(*A, *B, C, ldc, out_dtype);
     a.mode = dg::BLOCK_GRADIENT;
     a.E = (int)E;
@@ -699,7 +702,8 @@ int gemm_experts_gradient(const gemm_block_matrix* A, const gemm_block_matrix* B
     a.stride_c = stride_c;
     a.tiles_m = (int)ceil_div(M, p.bm);
     a.tiles_n = (int)ceil_div(N, p.bn);
-    return launch(p, a, (int64_t)a.tiles_m * a.tiles_n * E, A->dtype, B->dtype, (hipStream_t)stream);
+    a.group_m = 1;
+    return launch(p, a, ceil_div((int64_t)a.tiles_m * a.tiles_n, 8) * 8 * E, A->dtype, B->dtype, (hipStream_t)stream);
 }
 
 int gemm_experts_combine(const void* Y, int64_t cols, int64_t ldy, int dtype, const gemm_expert_plan* plan,

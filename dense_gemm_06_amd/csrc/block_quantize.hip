@@ -59,14 +59,23 @@ __global__ __launch_bounds__(256) void block_quantize(QuantArgs a) {
     // become zeros
     T raw[8][8];
     bool in[8];
+    size_t at[8];
 #pragma unroll
     for (int p = 0; p < 8; ++p) {
         int r = r0 + p;
         in[p] = r < a.rows;
         if (a.gather) r = a.gather[min(r, a.rows - 1)];
         in[p] = in[p] && r >= 0 && r < a.x_rows && left > 0;
-        if (a.x_rows > 0)  // there is a row 0
-            load8<T>(raw[p], X + (size_t)(in[p] ? r : 0) * (size_t)a.ldx + (left > 0 ? c0 : 0), left > 0 ? left : a.cols);
+        at[p] = (size_t)(in[p] ? r : 0) * (size_t)a.ldx;
+    }
+    if (a.x_rows > 0) {  // there is a row 0
+        if (bx * 128 + 128 <= a.cols) {  // whole columns, without a branch at each load
+#pragma unroll
+            for (int p = 0; p < 8; ++p) __builtin_memcpy(raw[p], X + at[p] + c0, sizeof raw[p]);
+        } else {
+#pragma unroll
+            for (int p = 0; p < 8; ++p) load8<T>(raw[p], X + at[p] + (left > 0 ? c0 : 0), left > 0 ? left : a.cols);
+        }
     }
     float v[8][8];
 #pragma unroll

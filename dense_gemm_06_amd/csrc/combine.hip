@@ -5,6 +5,7 @@
 //
 // Memory-bound: every row of Y is read once; sums in fp32, in the slots' order.
 #include <algorithm>
+#include <type_traits>
 
 #include "device_common.h"
 #include "experts.h"
@@ -68,30 +69,33 @@ __device__ __forceinline__ Slots slots_of(const CombineArgs& a, int t, int j0) {
     return s;
 }
 
-// One thread per token and eight columns.
+// One workgroup per token, eight columns to a thread and 2048 to a pass. (Two workgroups to
+// a token of 4096 columns, with half rows each: 90 us against 86 at 4096 tokens x 8 rows.)
 template <int DT>
 __global__ __launch_bounds__(256) void combine(CombineArgs a) {
     typedef typename Elem<DT>::type T;
-    const int pieces = (a.cols + 2047) >> 11;
-    const int64_t total = (int64_t)a.tokens * pieces;
-    for (int64_t u = blockIdx.x; u < total; u += gridDim.x) {
-        const int t = (int)(u / pieces);
-        const int c = ((int)(u - (int64_t)t * pieces) * 256 + (int)threadIdx.x) * 8, left = a.cols - c;
-        if (left <= 0) continue;
-        float sum[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-        if (a.capacity > 0)
-            for (int j0 = 0; j0 < a.top_k; j0 += kSlots) {
-                const Slots s = slots_of(a, t, j0);
-                typename Elem<DT>::type raw[kSlots][8];
+    for (int t = blockIdx.x; t < a.tokens; t += gridDim.x) {
+        auto piece = [&](int c, auto whole_tag) {
+            const int left = decltype(whole_tag)::value ? 8 : a.cols - c;
+            float sum[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+            if (a.capacity > 0)
+                for (int j0 = 0; j0 < a.top_k; j0 += kSlots) {
+                    const Slots s = slots_of(a, t, j0);
+                    T raw[kSlots][8];
 #pragma unroll
-                for (int v = 0; v < kSlots; ++v)
-                    load8_raw<DT>(raw[v], static_cast<const T*>(a.Y) + (size_t)s.p[v] * (size_t)a.ldy + c, left);
+                    for (int v = 0; v < kSlots; ++v)
+                        load8_raw<DT>(raw[v], static_cast<const T*>(a.Y) + (size_t)s.p[v] * (size_t)a.ldy + c, left);
 #pragma unroll
-                for (int v = 0; v < kSlots; ++v)
+                    for (int v = 0; v < kSlots; ++v)
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) sum[e] = s.in[v] ? fmaf(s.w[v], decode<DT>(raw[v][e]), sum[e]) : sum[e];
-            }
-        store8<DT>(static_cast<T*>(a.out) + (size_t)t * (size_t)a.ldo + c, sum, left);
+                        for (int e = 0; e < 8; ++e) sum[e] = s.in[v] ? fmaf(s.w[v], decode<DT>(raw[v][e]), sum[e]) : sum[e];
+                }
+            store8<DT>(static_cast<T*>(a.out) + (size_t)t * (size_t)a.ldo + c, sum, left);
+        };
+        // whole passes without a branch at each load
+        int c0 = 0;
+        for (; c0 + 2048 <= a.cols; c0 += 2048) piece(c0 + (int)threadIdx.x * 8, std::true_type{});
+        if (c0 + (int)threadIdx.x * 8 < a.cols) piece(c0 + (int)threadIdx.x * 8, std::false_type{});
     }
 }
 
@@ -117,8 +121,8 @@ __global__ __launch_bounds__(256) void combine_backward(CombineArgs a, int worke
         for (int j0 = 0; j0 < a.top_k; j0 += kSlots) {
             const Slots s = slots_of(a, t, j0);
             float dot[kSlots] = {0, 0, 0, 0, 0, 0, 0, 0};
-            for (int c = tid * 8; c < a.cols; c += 2048) {
-                const int left = a.cols - c;
+            auto piece = [&](int c, auto whole_tag) {
+                const int left = decltype(whole_tag)::value ? 8 : a.cols - c;
                 T raw[kSlots][8], graw[8];
                 load8_raw<DT>(graw, g + c, left);
                 if (a.capacity > 0)
@@ -137,7 +141,10 @@ __global__ __launch_bounds__(256) void combine_backward(CombineArgs a, int worke
                     }
                     store8<DT>(yg + (size_t)s.p[v] * (size_t)a.ldyg + c, out, left);
                 }
-            }
+            };
+            int c0 = 0;
+            for (; c0 + 2048 <= a.cols; c0 += 2048) piece(c0 + tid * 8, std::true_type{});
+            if (c0 + tid * 8 < a.cols) piece(c0 + tid * 8, std::false_type{});
 #pragma unroll
             for (int v = 0; v < kSlots; ++v) {
 #pragma unroll
@@ -154,7 +161,7 @@ __global__ __launch_bounds__(256) void combine_backward(CombineArgs a, int worke
 }
 
 int launch_combine(const CombineArgs& a, int dtype, hipStream_t s) {
-    const dim3 grid((unsigned)std::min<int64_t>((int64_t)a.tokens * ((a.cols + 2047) / 2048), 1 << 20));
+    const dim3 grid((unsigned)std::min(a.tokens, 1 << 20));
     if (dtype == DT_F32) return launch_status(combine<DT_F32>, grid, dim3(256), s, a);
     if (dtype == DT_F16) return launch_status(combine<DT_F16>, grid, dim3(256), s, a);
     return launch_status(combine<DT_BF16>, grid, dim3(256), s, a);

@@ -208,10 +208,16 @@ __device__ __forceinline__ bool block_tile_of(BlockArgs& g, BlockTile& t) {
         t.n0 = tn * BN;
         return true;
     }
-    int id = xcd_tile((int)gridDim.x);
+    int id;
     if (g.mode == BLOCK_GRADIENT) {
-        t.expert = id / per;
-        id -= t.expert * per;
+        // each XCD takes a run of every expert's tiles, row by row, so that experts of many and
+        // of few rows are shared out evenly; a run reads its own rows of A and all of B (the
+        // experts in turn to the XCDs: 350 us instead of 2XX at 64 experts of 20 to 2310 rows)
+        const int x = (int)blockIdx.x & 7, i = (int)blockIdx.x >> 3, q = per >> 3, r = per & 7, most = (per + 7) >> 3;
+        t.expert = i / most;
+        const int k = i - t.expert * most;
+        if (k >= q + (x < r ? 1 : 0)) return false;
+        id = x * q + min(x, r) + k;
         int lo, hi;
         expert_range(g.offsets, t.expert, g.K, lo, hi);
         lo = __builtin_amdgcn_readfirstlane(lo);
@@ -222,6 +228,7 @@ __device__ __forceinline__ bool block_tile_of(BlockArgs& g, BlockTile& t) {
         t.krem = hi - lo - (t.nkb - 1) * kBlock;
         g.C = static_cast<char*>(g.C) + (size_t)t.expert * (size_t)g.stride_c * (g.out_dt == DT_F32 ? 4 : 2);
     } else {
+        id = xcd_tile((int)gridDim.x);
         split_k(g, t);
     }
     raster(id, g.tiles_m, g.tiles_n, g.group_m, tm, tn);
@@ -567,11 +574,15 @@ __global__ __launch_bounds__(512) void block_wide(BlockArgs g) {
 // and 64 of 16 for each wave and block); widening on the way into LDS instead halves the
 // conversions, but its writes and conflicts kept LDS busy 80% longer than the matrix cores
 // (271 against 219 us at 2056 x 4000 x 8176 with one workgroup of each).
-template <int TA, int TB, bool BROW, int WM, int S>
+// TRB: B is stored with its rows adjacent; its stage then holds 128 rows of k, 16-byte chunk c
+// of row k at c ^ (((k >> 1) & 3) | ((k >> 2) & 4)), and 8 k of a row of B come from
+// ds_read_b64_tr_b8 (see the tiles below): the 32 lanes of a phase see 16 rows of k, two groups
+// of 8 that lie 16 apart, at one chunk, in 16 different places.
+template <int TA, int TB, bool BROW, int WM, int S, bool TRB = false>
 __global__ __launch_bounds__(WM * 128, 2) void block_full_direct(BlockArgs g) {
-    constexpr int NW = 2 * WM, BM = 64 * WM, BN = 128, FM = 4, FN = 4, ROW = 68;
+    constexpr int NW = 2 * WM, BM = 64 * WM, BN = 128, FM = 4, FN = 4;
     constexpr int CB = BN / 8 / NW;  // copies of 1 KB (8 rows) of B for each wave; 4 of A
-    constexpr int AHEAD = WM == 2 ? 1 : 2;  // fragments of codes read ahead (as registers allow)
+    constexpr int AHEAD = WM == 2 || TRB ? 1 : 2;  // fragments of codes read ahead (as registers allow)
     constexpr int STAGE_A = BM * kBlock, STAGE_B = BN * kBlock, STAGE_S = (BM + BN) * 4;
     __shared__ __attribute__((aligned(1024))) uint8_t lds[S * (STAGE_A + STAGE_B + STAGE_S)];
     uint8_t* const sA = lds;
@@ -588,7 +599,8 @@ __global__ __launch_bounds__(WM * 128, 2) void block_full_direct(BlockArgs g) {
     if (!any) return;
 
     const uint8_t* ba = g.A + (size_t)t.kb0 * kBlock;
-    const uint8_t* bb = g.B + (size_t)t.kb0 * kBlock;
+    const size_t step_b = TRB ? (size_t)kBlock * (size_t)g.ldb : kBlock;
+    const uint8_t* bb = g.B + (size_t)t.kb0 * step_b;
     uint32_t oa[4], ob[CB];
     int ka[2], kb2[2];  // the k of a chunk: the same for every other copy
 #pragma unroll
@@ -601,8 +613,14 @@ __global__ __launch_bounds__(WM * 128, 2) void block_full_direct(BlockArgs g) {
 #pragma unroll
     for (int c = 0; c < CB; ++c) {
         const int row = (wave * CB + c) * 8 + (lane >> 3);
-        kb2[c & 1] = ((lane & 7) ^ ((row >> 1) & 7)) * 16;
-        ob[c] = (uint32_t)min(t.n0 + row, g.N - 1) * (uint32_t)g.ldb + (uint32_t)kb2[c & 1];
+        if constexpr (TRB) {  // rows of k at chunk n; past N (a multiple of 16) the last, which is not stored
+            const int n = t.n0 + ((lane & 7) ^ (((row >> 1) & 3) | ((row >> 2) & 4))) * 16;
+            // n is the same for the copies of 16 rows: rows 8 c are added at the copy (registers)
+            ob[c >> 1] = (uint32_t)(row - 8 * c) * (uint32_t)g.ldb + (uint32_t)min(n, g.N - 16);
+        } else {
+            kb2[c & 1] = ((lane & 7) ^ ((row >> 1) & 7)) * 16;
+            ob[c] = (uint32_t)min(t.n0 + row, g.N - 1) * (uint32_t)g.ldb + (uint32_t)kb2[c & 1];
+        }
     }
     // scales: the first WM waves copy those of A's rows, two those of B's, the others none
     const bool scales = wave < WM + 2;
@@ -632,7 +650,10 @@ __global__ __launch_bounds__(WM * 128, 2) void block_full_direct(BlockArgs g) {
         }
 #pragma unroll
         for (int c = 0; c < CB; ++c) {
-            const void* b = kb2[c & 1] < rem ? static_cast<const void*>(bb + k + ob[c]) : block_zeros;
+            const bool in = (TRB ? (wave * CB + c) * 8 + (lane >> 3) : kb2[c & 1]) < rem;
+            const void* b = in ? static_cast<const void*>(bb + (size_t)kb * step_b +
+                                                            (TRB ? ob[c >> 1] + (uint32_t)(8 * c) * (uint32_t)g.ldb : ob[c]))
+                              : block_zeros;
             __builtin_amdgcn_global_load_lds(DG_GLB(b), DG_LDS_ADDR(dB + st * STAGE_B + c * 1024u), 16, 0, 0);
         }
     };
@@ -657,7 +678,26 @@ __global__ __launch_bounds__(WM * 128, 2) void block_full_direct(BlockArgs g) {
         return i32x8{(int)x[0], (int)x[1], (int)x[2], (int)x[3], (int)y[0], (int)y[1], (int)y[2], (int)y[3]};
     };
     const uint8_t* const aw = sA + wm * 64 * kBlock;
-    const uint8_t* const bw = sB + wn * 64 * kBlock;
+    // fragment j of B from a stage
+    const int tr_row = (l16 >> 1) + 16 * lg, tr_swz = ((l16 >> 2) & 3) | ((lg & 1) << 2);
+    auto b_codes = [&](int stage, int j) {
+        const uint8_t* b = sB + stage * STAGE_B;
+        if constexpr (TRB) {
+            // 8 rows of k from 64 (u / 2) + 16 lg + 8 (u % 2); the rows' (k >> 1) & 3 and bit 4 are the lane's
+            const uint8_t* p = b + tr_row * kBlock + (((wn * 4 + j) ^ tr_swz) << 4) + (l16 & 1) * 8;
+            i32x8 r;
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const i32x2 v = __builtin_amdgcn_ds_read_tr8_b64_v2i32(
+                    DG_LDS_PTR(i32x2, p + (64 * (u >> 1) + 8 * (u & 1)) * kBlock));
+                r[2 * u] = v[0];
+                r[2 * u + 1] = v[1];
+            }
+            return r;
+        } else {
+            return codes_of(b + (wn * 64 + j * 16) * kBlock);
+        }
+    };
     const float* const fa = fS + wm * 64 + l16;
     const float* const fb = fS + BM + wn * 64;
 
@@ -709,7 +749,7 @@ __global__ __launch_bounds__(WM * 128, 2) void block_full_direct(BlockArgs g) {
         if (active) {
 #pragma unroll
             for (int j = 0; j < FN; ++j) {
-                const i32x8 r = codes_of(bw + j * 16 * kBlock);
+                const i32x8 r = b_codes(0, j);
 #pragma unroll
                 for (int q = 0; q < 16; ++q) widen_b(r, j, q >> 2, q & 3);
             }
@@ -760,8 +800,8 @@ __global__ __launch_bounds__(WM * 128, 2) void block_full_direct(BlockArgs g) {
         }
         if (active) {
             // past the end of k the reads find old data, which nothing uses
-            rawb[0] = codes_of(bw + next * STAGE_B);
-            rawb[1] = codes_of(bw + next * STAGE_B + 16 * kBlock);
+            rawb[0] = b_codes(next, 0);
+            rawb[1] = b_codes(next, 1);
             const float s = sa[(FM - 1) & 1];
             __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
@@ -776,9 +816,9 @@ __global__ __launch_bounds__(WM * 128, 2) void block_full_direct(BlockArgs g) {
                     }
                     __builtin_amdgcn_sched_barrier(0);
                 }
-                if (j == 1) rawb[0] = codes_of(bw + next * STAGE_B + 2 * 16 * kBlock);
+                if (j == 1) rawb[0] = b_codes(next, 2);
                 if (j == 2) {
-                    rawb[1] = codes_of(bw + next * STAGE_B + 3 * 16 * kBlock);
+                    rawb[1] = b_codes(next, 3);
                     raw[0] = codes_of(aw + next * STAGE_A);
                     if (AHEAD > 1) raw[1] = codes_of(aw + next * STAGE_A + 16 * kBlock);
                     sa[0] = fa[next * (BM + BN)];
@@ -799,36 +839,28 @@ __global__ __launch_bounds__(WM * 128, 2) void block_full_direct(BlockArgs g) {
         for (int q = 0; q < 16; ++q) add1(FM - 1, q, s_last);
     }
 
-    // ---- C through LDS, 16 rows of the wave's 64 columns at a time
-    __builtin_amdgcn_s_barrier();  // every wave has read its last fragments
-    asm volatile("" ::: "memory");
-    float* const stage = reinterpret_cast<float*>(lds) + wave * (16 * ROW);
+    // ---- C from the registers: a lane's four columns are 16 bytes, four lanes' 64 of a row
+    if (!active) return;
     float* const C = static_cast<float*>(g.C);
-    const int n = t.n0 + wn * 64 + l16 * 4;
     const bool whole = t.n0 + BN <= g.N;
     const uint64_t live = live_rows(g, t, t.m0 + wm * 64);
 #pragma unroll
     for (int i = 0; i < FM; ++i) {
-        if (!active) continue;
+        const int m = t.m0 + wm * 64 + i * 16 + l16;
+        const bool zero = !((live >> (i * 16 + l16)) & 1);
+        float* const c = C + (size_t)m * (size_t)g.ldc + t.n0 + wn * 64 + lg * 4;
+        if (m >= t.m_end) continue;
 #pragma unroll
-        for (int j = 0; j < FN; ++j) *reinterpret_cast<f32x4*>(stage + l16 * ROW + j * 16 + lg * 4) = acc[i][j];
-        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-#pragma unroll
-        for (int p = 0; p < 4; ++p) {
-            const int row = p * 4 + lg, m = t.m0 + wm * 64 + i * 16 + row;
-            f32x4 v = *reinterpret_cast<const f32x4*>(stage + row * ROW + l16 * 4);
-            if (!((live >> (i * 16 + row)) & 1)) v = f32x4{0, 0, 0, 0};
-            float* const c = C + (size_t)m * (size_t)g.ldc + n;
-            if (m >= t.m_end) continue;
+        for (int j = 0; j < FN; ++j) {
+            const f32x4 v = zero ? f32x4{0, 0, 0, 0} : acc[i][j];
             if (whole) {
-                __builtin_memcpy(c, &v, 16);
+                __builtin_memcpy(c + j * 16, &v, 16);
             } else {
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                    if (n + e < g.N) c[e] = v[e];
+                    if (t.n0 + wn * 64 + j * 16 + lg * 4 + e < g.N) c[j * 16 + e] = v[e];
             }
         }
-        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     }
 }
 
@@ -1342,14 +1374,15 @@ __global__ __launch_bounds__(WM* WN * 64) void block_tile(BlockArgs g) {
 }
 
 // ---------------------------------------------------------------------------- few rows
-// At most 16 * SM rows of A: the time is that of reading B once. A workgroup takes 16
+// At most 16 * SM rows of A: the time is that of reading B once. A workgroup takes 16 * NT
 // rows of B, its NW waves every NW-th block of k, fragments straight from global memory
 // (a row's 128 bytes from four lanes); the waves' sums meet in LDS and are added in the
-// waves' order.
-template <int TA, int TB, bool FULL, int SM, bool DIRECT>
+// waves' order. NT = 4 where that leaves enough workgroups: a wave then has four times the
+// bytes in flight behind one search for its expert and one reading of A.
+template <int TA, int TB, bool FULL, int SM, int NT, bool DIRECT>
 __global__ __launch_bounds__(512) void block_skinny(BlockArgs g) {
-    constexpr int NW = 8, BM = 16 * SM, BN = 16;
-    __shared__ f32x4 sums[NW][SM][64];
+    constexpr int NW = 8, BM = 16 * SM, BN = 16 * NT;
+    __shared__ f32x4 sums[NW][SM * NT][64];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int l16 = lane & 15, lg = lane >> 4;
@@ -1367,12 +1400,16 @@ __global__ __launch_bounds__(512) void block_skinny(BlockArgs g) {
         pa[i] = g.A + (size_t)r * (size_t)g.lda + k0 + lg * 32;
         fa[i] = g.SA + (size_t)(r >> g.a_shift) * (size_t)g.sa_row + (size_t)t.kb0 * (size_t)g.sa_blk;
     }
-    const uint8_t* pb = g.B + (size_t)min(t.n0 + l16, g.N - 1) * (size_t)g.ldb + k0 + lg * 32;
-    const float* fb[4];
+    const uint8_t* pb[NT];
+    const float* fb[NT][4];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        const int n = min(t.n0 + lg * 4 + e, g.N - 1);
-        fb[e] = g.SB + (size_t)(n >> g.b_shift) * (size_t)g.sb_row + (size_t)t.kb0 * (size_t)g.sb_blk;
+    for (int j = 0; j < NT; ++j) {
+        pb[j] = g.B + (size_t)min(t.n0 + j * 16 + l16, g.N - 1) * (size_t)g.ldb + k0 + lg * 32;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int n = min(t.n0 + j * 16 + lg * 4 + e, g.N - 1);
+            fb[j][e] = g.SB + (size_t)(n >> g.b_shift) * (size_t)g.sb_row + (size_t)t.kb0 * (size_t)g.sb_blk;
+        }
     }
     auto frag = [&](const uint8_t* p, int rem) {
         u32x4 x, y;
@@ -1386,41 +1423,52 @@ __global__ __launch_bounds__(512) void block_skinny(BlockArgs g) {
         }
         return i32x8{(int)x[0], (int)x[1], (int)x[2], (int)x[3], (int)y[0], (int)y[1], (int)y[2], (int)y[3]};
     };
-    f32x4 acc[SM];
+    f32x4 acc[SM][NT];
 #pragma unroll
-    for (int i = 0; i < SM; ++i) acc[i] = f32x4{0, 0, 0, 0};
-#pragma unroll(DIRECT ? 4 : 1)
+    for (int i = 0; i < SM; ++i)
+#pragma unroll
+        for (int j = 0; j < NT; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
+#pragma unroll(DIRECT ? (NT == 1 ? 4 : 2) : 1)
     for (int kb = wave; kb < t.nkb; kb += NW) {
         const int rem = (kb == t.nkb - 1 ? t.krem : kBlock) - lg * 32;
-        const i32x8 bf = frag(pb + (size_t)kb * kBlock, rem);
-        f32x4 sb;
+        i32x8 bf[NT];
+        f32x4 sb[NT];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) sb[e] = fb[e][(size_t)kb * (size_t)g.sb_blk];
+        for (int j = 0; j < NT; ++j) bf[j] = frag(pb[j] + (size_t)kb * kBlock, rem);
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) sb[j][e] = fb[j][e][(size_t)kb * (size_t)g.sb_blk];
 #pragma unroll
         for (int i = 0; i < SM; ++i) {
             const i32x8 af = frag(pa[i] + (size_t)kb * kBlock, rem);
             const float sa = fa[i][(size_t)kb * (size_t)g.sa_blk];
-            f32x4 part = {0, 0, 0, 0};
-            if constexpr (FULL) {
 #pragma unroll
-                for (int u = 0; u < 4; ++u)
-                    part = __builtin_amdgcn_mfma_f32_16x16x32_f16(widen8<TB>(bf[2 * u], bf[2 * u + 1]),
-                                                                  widen8<TA>(af[2 * u], af[2 * u + 1]), part, 0, 0, 0);
-            } else {
-                part = mfma_16<TB, TA>(bf, af, part);
+            for (int j = 0; j < NT; ++j) {
+                f32x4 part = {0, 0, 0, 0};
+                if constexpr (FULL) {
+#pragma unroll
+                    for (int u = 0; u < 4; ++u)
+                        part = __builtin_amdgcn_mfma_f32_16x16x32_f16(widen8<TB>(bf[j][2 * u], bf[j][2 * u + 1]),
+                                                                      widen8<TA>(af[2 * u], af[2 * u + 1]), part, 0, 0, 0);
+                } else {
+                    part = mfma_16<TB, TA>(bf[j], af, part);
+                }
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[i][j][e] = fmaf(part[e], sa * sb[j][e], acc[i][j][e]);
             }
-#pragma unroll
-            for (int e = 0; e < 4; ++e) acc[i][e] = fmaf(part[e], sa * sb[e], acc[i][e]);
         }
     }
 #pragma unroll
-    for (int i = 0; i < SM; ++i) sums[wave][i][lane] = acc[i];
+    for (int i = 0; i < SM; ++i)
+#pragma unroll
+        for (int j = 0; j < NT; ++j) sums[wave][i * NT + j][lane] = acc[i][j];
     __syncthreads();
-    if (wave >= SM) return;
+    if (wave >= SM * NT) return;
     f32x4 v = sums[0][wave][lane];
 #pragma unroll
     for (int w = 1; w < NW; ++w) v += sums[w][wave][lane];
-    const int m = t.m0 + wave * 16 + l16, n = t.n0 + lg * 4;
+    const int m = t.m0 + (wave / NT) * 16 + l16, n = t.n0 + (wave % NT) * 16 + lg * 4;
     if (m >= t.m_end || n >= g.N) return;
     if (t.bad) v = f32x4{1, 1, 1, 1} * __builtin_nanf("");
     else if (block_a_row(g, t, m) < 0) v = f32x4{0, 0, 0, 0};
@@ -1438,6 +1486,8 @@ template <int TA, int TB, bool FULL>
 int launch_block_full(const BlockPlan& p, const BlockArgs& a, dim3 grid, hipStream_t s) {
     const bool brow = a.b_shift == 0;
     if constexpr (FULL) {
+        if (p.tr == 1 && p.kernel == BLOCK_TILE256)
+            return launch_status(block_full_direct<TA, TB, true, 4, 3, true>, grid, dim3(512), s, a);
         if (p.tr == 1) return launch_status(block_full<TA, TB, true, 1>, grid, dim3(256), s, a);
         if (p.tr == 2) return launch_status(block_full<TA, TB, true, 2>, grid, dim3(256), s, a);
         if (p.tr == 3) return launch_status(block_full<TA, TB, true, 3>, grid, dim3(256), s, a);
@@ -1465,13 +1515,15 @@ int launch_block_full(const BlockPlan& p, const BlockArgs& a, dim3 grid, hipStre
                         : launch_status(block_tile<TA, TB, false, 128, 128, 2, 2, false>, grid, dim3(256), s, a);
         }
     }
-    if (p.direct)
-        return p.bm == 16   ? launch_status(block_skinny<TA, TB, FULL, 1, true>, grid, dim3(512), s, a)
-               : p.bm == 32 ? launch_status(block_skinny<TA, TB, FULL, 2, true>, grid, dim3(512), s, a)
-                            : launch_status(block_skinny<TA, TB, FULL, 4, true>, grid, dim3(512), s, a);
-    return p.bm == 16   ? launch_status(block_skinny<TA, TB, FULL, 1, false>, grid, dim3(512), s, a)
-           : p.bm == 32 ? launch_status(block_skinny<TA, TB, FULL, 2, false>, grid, dim3(512), s, a)
-                        : launch_status(block_skinny<TA, TB, FULL, 4, false>, grid, dim3(512), s, a);
+    if (p.direct) {
+        if (p.bn == 64) return launch_status(block_skinny<TA, TB, FULL, 1, 4, true>, grid, dim3(512), s, a);
+        return p.bm == 16   ? launch_status(block_skinny<TA, TB, FULL, 1, 1, true>, grid, dim3(512), s, a)
+               : p.bm == 32 ? launch_status(block_skinny<TA, TB, FULL, 2, 1, true>, grid, dim3(512), s, a)
+                            : launch_status(block_skinny<TA, TB, FULL, 4, 1, true>, grid, dim3(512), s, a);
+    }
+    return p.bm == 16   ? launch_status(block_skinny<TA, TB, FULL, 1, 1, false>, grid, dim3(512), s, a)
+           : p.bm == 32 ? launch_status(block_skinny<TA, TB, FULL, 2, 1, false>, grid, dim3(512), s, a)
+                        : launch_status(block_skinny<TA, TB, FULL, 4, 1, false>, grid, dim3(512), s, a);
 }
 
 template <int TA, int TB>
