@@ -196,9 +196,12 @@ __global__ __launch_bounds__(256) void route(RouteArgs a) {
     __shared__ double values[4][64 * R];
     __shared__ uint8_t kept[4][64 * R];
     __shared__ uint16_t picks[4][PER * kMaxTopK];
+    __shared__ float shift[W * R];  // the bias
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, l = lane & (W - 1), sub = lane / W;
     double* mine = &values[wave][sub * W * R];
     const int left = a.experts - l * R;
+    for (int e = threadIdx.x; e < a.experts; e += 256) shift[e] = a.bias ? a.bias[e] : 0.0f;
+    __syncthreads();
     const ExpTerms terms;
     const int64_t step = (int64_t)gridDim.x * 4 * PER;
     for (int64_t first = ((int64_t)blockIdx.x * 4 + wave) * PER; first < a.tokens; first += step) {
@@ -206,16 +209,7 @@ __global__ __launch_bounds__(256) void route(RouteArgs a) {
         const int t = (int)(on ? first + sub : a.tokens - 1);
         float key[R], bias[R];
 #pragma unroll
-        for (int j = 0; j < R; ++j) bias[j] = 0;
-        if (a.bias) {
-            if (left >= R) {
-                __builtin_memcpy(bias, a.bias + l * R, sizeof bias);
-            } else {
-#pragma unroll
-                for (int j = 0; j < R; ++j)
-                    if (j < left) bias[j] = a.bias[l * R + j];
-            }
-        }
+        for (int j = 0; j < R; ++j) bias[j] = j < left ? shift[l * R + j] : 0.0f;
         double v0 = kAbsent, v1 = kAbsent;  // the lane's two largest choice values
         {
             double s[R];
@@ -264,9 +258,10 @@ __global__ __launch_bounds__(256) void route(RouteArgs a) {
                     const int grp = l * R + j;
                     double v[4] = {kAbsent, kAbsent, kAbsent, kAbsent};
                     if (grp < a.groups)
+#pragma unroll 4
                         for (int i = 0; i < per; ++i) {
                             const int e = grp * per + i;
-                            double x = order_key(a.bias ? mine[e] + (double)a.bias[e] : mine[e]);
+                            double x = order_key(mine[e] + (double)shift[e]);
 #pragma unroll
                             for (int q = 0; q < 4; ++q) {
                                 const double lower = __builtin_fmin(v[q], x);

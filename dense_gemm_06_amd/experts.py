@@ -352,7 +352,8 @@ def gemm_experts_dispatch_tensors(index, experts, align=1):
     E1, head = experts + 1, 2 * experts + 1
     buf = torch.empty(head + P + T * k + n // 4, dtype=torch.int32, device=dev)
     p0 = buf.data_ptr()
-    plan = ExpertPlan(buf[:E1], buf[E1:head], buf[head:head + P], buf[head + P:head + P + T * k].view(T, k), align)
+    offsets, counts, rows, position, _ = buf.split_with_sizes((E1, experts, P, T * k, n // 4))
+    plan = ExpertPlan(offsets, counts, rows, position.view(T, k), align)
     c = gemm_expert_plan(p0, p0 + 4 * E1, p0 + 4 * head, p0 + 4 * (head + P), experts, T, k, P)
     _call("gemm_experts_dispatch", at, i, align, c, p0 + 4 * (head + P + T * k) if n else None, n)
     return plan
