@@ -373,3 +373,17 @@ def test_whole_layer_on_a_graph():
         torch.cuda.synchronize()
         for a, b2 in zip(kept, layer()):
             assert torch.equal(a, b2)
+
+
+def test_training_step_example():
+    """The example's step against full precision: the only differences are the codes' roundings. A code is off by at
+    most 2^-4 (e4m3) or 2^-3 (e5m2) of its value, so a product of two by less than (1 + 2^-4)(1 + 2^-3) - 1 = 0.2 of
+    the terms' 2-norm; the out's gradient meets one more rounding to 16 bits."""
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "experts_step.py")
+    spec = importlib.util.spec_from_file_location("experts_step", path)
+    step = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(step)
+    off = step.main(tokens=300, experts=6, top_k=2, inputs=256, outputs=384, repeat=1)
+    assert off["out"] < 0.13 and off["x_grad"] < 0.2 and off["W_grad"] < 0.2 and off["logits_grad"] < 0.2, off
