@@ -188,9 +188,11 @@ __device__ __forceinline__ void token_scores(const RouteArgs& a, const ExpTerms&
 // fp64 takes three times as many): rounding keeps their order but for ties, and where any
 // token's largest is not alone the wave decides by the fp64 values. -inf stands for what the
 // groups mask, NaN (which max and == pass over) for what is picked or does not exist.
+// ANY_GROUPS: groups that cut lanes, or more than the two largest of a group (a kernel of its
+// own, for the others' registers).
 // 16384 tokens x 256 experts, sigmoid, 8 groups: 100 us with a wave to a token and fp64
-// picks, 32 us with 16 lanes to a token.
-template <int W, int R, int DT>
+// picks, 32 us with 16 lanes to a token, 27 us with fp32 picks, 22 us with 123 registers.
+template <int W, int R, int DT, bool ANY_GROUPS>
 __global__ __launch_bounds__(256) void route(RouteArgs a) {
     constexpr int PER = 64 / W;
     __shared__ double values[4][64 * R];
@@ -227,7 +229,7 @@ __global__ __launch_bounds__(256) void route(RouteArgs a) {
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
         if (a.groups > 1) {
             const int per = a.experts / a.groups;
-            if (a.group_lanes > 0 && a.group_top <= 2) {
+            if constexpr (!ANY_GROUPS) {
                 // a group is group_lanes whole lanes: its two largest by exchanges among them
                 auto merge = [&](double o0, double o1) {
                     v1 = __builtin_fmax(__builtin_fmin(v0, o0), v0 > o0 ? v1 : o1);
@@ -321,6 +323,7 @@ __global__ __launch_bounds__(256) void route(RouteArgs a) {
                     full[j] = kAbsent;
                     if (key[j] == best)
                         full[j] = key[j] == -__builtin_inff() ? kMasked : order_key(mine[e] + (double)bias[j]);
+                    if ((j & 3) == 3) __builtin_amdgcn_sched_barrier(0);
                 }
                 lanes_argmax<W, R>(full, lane, at, reg);
             }
@@ -437,7 +440,8 @@ int launch_route_as(RouteArgs a, bool backward, hipStream_t s) {
     // groups that are 1, 2, 4 or 8 whole lanes (of a token's 16)
     const int per = a.experts / a.groups, lanes = per / R;
     a.group_lanes = W == 16 && a.groups > 1 && per % R == 0 && (lanes & (lanes - 1)) == 0 && lanes <= 8 ? lanes : 0;
-    return launch_status(route<W, R, DT>, grid, block, s, a);
+    if (a.groups > 1 && (a.group_lanes == 0 || a.group_top > 2)) return launch_status(route<W, R, DT, true>, grid, block, s, a);
+    return launch_status(route<W, R, DT, false>, grid, block, s, a);
 }
 
 template <int DT>
