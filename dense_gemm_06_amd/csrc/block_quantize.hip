@@ -41,7 +41,9 @@ __device__ __forceinline__ void load8(T (&raw)[8], const T* p, int valid) {
 
 // One workgroup: a 128 x 128 block of X in registers, thread (rg, cg) holding rows
 // 8 rg .. 8 rg + 7 at columns 8 cg .. 8 cg + 7. The transposed codes go through LDS (rows
-// of 128 bytes, 8-byte pieces permuted by the column's low bits against bank conflicts).
+// of 128 bytes, 16-byte pieces permuted by the column's bits 3 to 5 against bank conflicts).
+// Bound by memory: 8192 x 4096 bf16 into codes both ways moves 136 MB in 30 us, 4.5 TB/s of
+// the 5.1 that a copy reaches; the fewest rows take 5 us, of which a launch is 2.5.
 template <int DT>
 __global__ __launch_bounds__(256) void block_quantize(QuantArgs a) {
     typedef typename Elem<DT>::type T;

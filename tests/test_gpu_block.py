@@ -226,6 +226,27 @@ def test_product_operands_with_adjacent_rows(M, N, K):
     check_product(dg.gemm_block_product_tensors(dev((*a, 1)), W.t(), BF16), values(*a, 1), values(*w, BLOCK).t().contiguous(), BF16)
 
 
+@pytest.mark.parametrize("M,ld", [(40, 1 << 27), (150, 1 << 25), (300, 1 << 24)])
+def test_offsets_past_32_bits(M, ld):
+    """Rows so far apart that byte offsets pass 2^32, for operands and for the quantizer's input."""
+    g = gen(M)
+    a, b = codes(g, M, 256, E4, 1), codes(g, 270, 256, E4, BLOCK)
+    far = torch.empty(M * ld, dtype=torch.uint8, device="cuda").view(E4).view(M, ld)[:, :256]
+    far.view(torch.uint8).copy_(a[0].view(torch.uint8))
+    for out in (BF16, F32):
+        c = dg.gemm_block_product_tensors(dg.BlockTensor(far, a[1].cuda(), 1), dev((*b, BLOCK)), out)
+        check_product(c, values(*a, 1), values(*b, BLOCK), out)
+        c = dg.gemm_block_product_tensors(dev((*b, BLOCK)), dg.BlockTensor(far, a[1].cuda(), 1), out)
+        check_product(c, values(*b, BLOCK), values(*a, 1), out)
+    del far
+    x = torch.randn(M, 256, generator=g).to(BF16)
+    far = torch.empty(M * ld // 2, dtype=BF16, device="cuda").view(M, ld // 2)[:, :256]
+    far.copy_(x)
+    q, t = dg.gemm_block_quantize_tensors(far, E4, transposed=True)
+    check_quantized(q, x, E4, 1)
+    check_quantized(t, x.t().contiguous(), E4, 1)
+
+
 def test_product_empty():
     z = lambda r, k: dg.BlockTensor(torch.empty(r, k, dtype=E4, device="cuda"),  # noqa: E731
                                     torch.empty(r, blocks(k), device="cuda"), 1)

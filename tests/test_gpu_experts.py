@@ -320,6 +320,43 @@ def test_combine(T, k, E, N, dtype, align):
     assert (y_grad.cpu()[plan.rows.cpu() < 0] == 0).all()
 
 
+def test_combine_rows_past_32_bits():
+    """Rows of y whose byte offsets pass 2^32."""
+    P, N = 70000, 32768
+    y = torch.empty(P, N, dtype=BF16, device="cuda")
+    at = torch.tensor([[3, P - 1], [P - 2, 40000], [35000, -1]], dtype=torch.int32)
+    g = gen(5)
+    part = torch.randn(6, N, generator=g).to(BF16)
+    for i, p in enumerate(at.reshape(-1).tolist()):
+        if p >= 0:
+            y[p] = part[i].cuda()
+    rows = torch.full((P,), -1, dtype=torch.int32)
+    for t in range(3):
+        for p in at[t].tolist():
+            if p >= 0:
+                rows[p] = t
+    i32 = lambda *x: torch.zeros(*x, dtype=torch.int32, device="cuda")  # noqa: E731
+    plan = dg.ExpertPlan(i32(2), i32(1), rows.cuda(), at.cuda())
+    w, grad = torch.rand(3, 2, generator=g), torch.randn(3, N, generator=g).to(BF16)
+    out = dg.gemm_experts_combine_tensors(y, plan, w.cuda()).cpu().double()
+    yg, wg = dg.gemm_experts_combine_backward_tensors(y, plan, w.cuda(), grad.cuda())
+    W = w.double() * (at >= 0)
+    terms = part.double().reshape(3, 2, N) * W[:, :, None]
+    ref = terms.sum(1)
+    assert ((out - ref).abs() <= terms.abs().sum(1) * 2 * 2.0 ** -24 + ref.abs() * HALF[BF16] * (1 + 2.0 ** -9) + TINY[BF16]).all()
+    for t in range(3):
+        for j in range(2):
+            p = at[t, j].item()
+            if p < 0:
+                assert wg[t, j].item() == 0
+                continue
+            want = W[t, j] * grad[t].double()
+            assert ((yg[p].cpu().double() - want).abs() <= want.abs() * (HALF[BF16] * (1 + 2.0 ** -9) + 2.0 ** -24) + TINY[BF16]).all()
+            size = (part[2 * t + j].double() * grad[t].double()).abs().sum()
+            assert abs(wg[t, j].item() - (part[2 * t + j].double() * grad[t].double()).sum()) <= size * (N + 1) * 2.0 ** -24
+    assert (yg[P - 3] == 0).all() and (yg[0] == 0).all()
+
+
 def test_combine_backward_against_differences():
     g = gen(12)
     plan = dg.gemm_experts_dispatch_tensors(choice(g, 6, 5, 2).cuda(), 5, 1)
