@@ -1,9 +1,11 @@
 // block_api.cpp -- the C ABI declared in include/gemm_experts.h: validation, the choice of
 // kernel, and the launches. Everything is validated before the first launch.
 #include <hip/hip_runtime.h>
+#include <stdio.h>
 #include <string.h>
 
 #include <algorithm>
+#include <atomic>
 #include <initializer_list>
 
 #include "experts.h"
@@ -147,7 +149,9 @@ Range scale_range(const char* name, const gemm_block_matrix& m, int64_t batch = 
                                     span(1, (batch - 1) * std::min<int64_t>(m.scale_stride, (int64_t)1 << 30), 0, 4));
 }
 
-// The current device, which has to be a gfx950.
+// The current device, which has to be a gfx950 (asked once for each of the first 64).
+std::atomic<uint64_t> g_checked{0};
+
 int check_device() {
     int dev = 0, cus = 0;
     char arch[64];
@@ -156,11 +160,14 @@ int check_device() {
         set_error("hipGetDevice failed: %s", hipGetErrorString(e));
         return GEMM_ERR_DEVICE;
     }
+    const uint64_t bit = dev < 64 ? (uint64_t)1 << dev : 0;
+    if (g_checked.load(std::memory_order_relaxed) & bit) return GEMM_OK;
     DG_TRY(gemm_device_info(dev, &cus, arch, (int)sizeof arch));
     if (strncmp(arch, "gfx950", 6) != 0) {
         set_error("device architecture '%s' is not gfx950; the kernels are built for gfx950 only", arch);
         return GEMM_ERR_DEVICE;
     }
+    g_checked.fetch_or(bit, std::memory_order_relaxed);
     return GEMM_OK;
 }
 

@@ -108,16 +108,17 @@ class ExpertPlan:
 # call is kept here: torch (imported with the first use) and its types' codes.
 torch = None
 _CODES, _WIDE = {}, {}
-_raw_stream = None
+_raw_stream = _current_device = None
 
 
 def _use_torch():
-    global torch, _raw_stream
+    global torch, _raw_stream, _current_device
     import torch as t
     _CODES.update({t.float8_e4m3fn: GEMM_E4M3, t.float8_e5m2: GEMM_E5M2})
     _WIDE.update({t.float32: _dg.GEMM_F32, t.float16: _dg.GEMM_F16, t.bfloat16: _dg.GEMM_BF16})
     _raw_stream = getattr(t._C, "_cuda_getCurrentRawStream", None) or (
         lambda index: t.cuda.current_stream(index).cuda_stream)
+    _current_device = getattr(t._C, "_cuda_getDevice", None) or t.cuda.current_device
     torch = t
 
 
@@ -223,7 +224,7 @@ def _plan(plan):
 def _call(name, device, *args):
     """The library function on the current stream of GPU `device`."""
     fn = getattr(_dg._lib or _dg.library(), name)
-    if device == torch.cuda.current_device():
+    if device == _current_device():
         st = fn(*args, _raw_stream(device))
     else:
         with torch.cuda.device(device):
@@ -237,7 +238,7 @@ def _new_block(rows, cols, dtype, code, block_rows, device):
     """An empty BlockTensor, its scales laid out with the rows adjacent, and as the library takes it."""
     data = torch.empty((rows, cols), dtype=dtype, device=device)
     r = (rows + block_rows - 1) // block_rows
-    scale = torch.empty(((cols + 127) // 128, r), dtype=torch.float32, device=device).t()
+    scale = torch.empty_strided((r, (cols + 127) // 128), (1, r), dtype=torch.float32, device=device)
     return BlockTensor(data, scale, block_rows), gemm_block_matrix(
         data.data_ptr(), scale.data_ptr(), rows, cols, cols or 1, 1, r, 0, 0, code, block_rows, 0, 0)
 
