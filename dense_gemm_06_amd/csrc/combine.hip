@@ -4,8 +4,8 @@
 //   y_grad[position[t][j]] = w[t][j] G[t]      w_grad[t][j] = G[t] . Y[position[t][j]]
 //
 // Memory-bound: every row of Y is read once; sums in fp32, in the slots' order. 4096 tokens
-// x 8 rows of 4096 bf16: 300 MB in 54 to 78 us forward (5.5 to 3.9 TB/s, with Y partly in
-// the caches or not), 700 MB in 119 us backward (5.9 TB/s, padding rows' zeros among it).
+// x 8 rows of 4096 bf16: 300 MB in 55 to 78 us forward (5.5 to 3.9 TB/s, with Y partly in
+// the caches or not), 700 MB in 115 us backward (6.1 TB/s, padding rows' zeros among it).
 #include <algorithm>
 #include <type_traits>
 
@@ -33,13 +33,26 @@ template <> __device__ __forceinline__ uint16_t encode<DT_F16>(float x) {
 }
 template <> __device__ __forceinline__ uint16_t encode<DT_BF16>(float x) { return f32_to_bf16_rne(x); }
 
-template <int DT>
+// PASSING: y_grad, whose stores go past the caches: 300 MB that would take Y and G out of them.
+// 4096 tokens x 8 rows of 4096 bf16, both directions: 180 us against 203; with the gradient
+// quantized right behind, 277 against 276 (38 against 39 for 128 tokens x 4 rows of 2048). out
+// is small and read next, so it stays.
+template <int DT, bool PASSING = false>
 __device__ __forceinline__ void store8(typename Elem<DT>::type* p, const float (&v)[8], int valid) {
     typename Elem<DT>::type raw[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) raw[e] = encode<DT>(v[e]);
     if (valid >= 8) {
-        __builtin_memcpy(p, raw, sizeof raw);
+        if constexpr (PASSING) {
+#pragma unroll
+            for (int e = 0; e < 8; e += 16 / (int)sizeof raw[0]) {
+                u32x4 q;
+                __builtin_memcpy(&q, raw + e, 16);
+                store_passing(p + e, q);
+            }
+        } else {
+            __builtin_memcpy(p, raw, sizeof raw);
+        }
     } else {
 #pragma unroll
         for (int e = 0; e < 8; ++e)
@@ -119,7 +132,7 @@ __global__ __launch_bounds__(256) void combine_backward(CombineArgs a, int worke
             const int r = p < a.capacity ? a.rows[p] : 0;
             for (uint64_t pad = __ballot(p < a.capacity && (r < 0 || r >= a.tokens)) & 0xf; pad; pad &= pad - 1) {
                 T* const row = yg + (size_t)(p0 + __builtin_ctzll(pad)) * (size_t)a.ldyg;
-                for (int c = tid * 8; c < a.cols; c += 2048) store8<DT>(row + c, zero, a.cols - c);
+                for (int c = tid * 8; c < a.cols; c += 2048) store8<DT, true>(row + c, zero, a.cols - c);
             }
         }
         return;
@@ -147,7 +160,7 @@ __global__ __launch_bounds__(256) void combine_backward(CombineArgs a, int worke
                         dot[v] = fmaf(x, decode<DT>(raw[v][e]), dot[v]);
                         out[e] = x * s.w[v];
                     }
-                    store8<DT>(yg + (size_t)s.p[v] * (size_t)a.ldyg + c, out, left);
+                    store8<DT, true>(yg + (size_t)s.p[v] * (size_t)a.ldyg + c, out, left);
                 }
             };
             int c0 = 0;

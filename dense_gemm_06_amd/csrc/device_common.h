@@ -17,6 +17,14 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef __fp16 fp16x4_t __attribute__((__vector_size__(4 * sizeof(__fp16))));
 typedef __bf16 bf16x4_t __attribute__((__vector_size__(4 * sizeof(__bf16))));
 
+// Stores a vector at any address, marked as not read again soon, so that it leaves the caches
+// to what is.
+template <typename V>
+__device__ __forceinline__ void store_passing(void* p, V v) {
+    typedef V any_address __attribute__((aligned(1)));
+    __builtin_nontemporal_store(v, static_cast<any_address*>(p));
+}
+
 #define DG_LDS_PTR(T, p) ((__attribute__((address_space(3))) T*)(p))
 
 // Input element storage: fp32 as float, fp16/bf16 as raw 16-bit patterns.

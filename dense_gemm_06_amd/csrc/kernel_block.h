@@ -1095,7 +1095,9 @@ __global__ __launch_bounds__(256, 2) void block_full(BlockArgs g) {
             float* const c = C + (size_t)m * (size_t)g.ldc + n;
             if (m >= t.m_end) continue;
             if (whole) {
-                __builtin_memcpy(c, &v, 16);
+                // a weight's gradient is far larger than the codes, which other tiles read again:
+                // past the caches (64 experts, 512 rows each, 2048 x 1024: 273 against 279 us)
+                store_passing(c, v);
             } else {
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
