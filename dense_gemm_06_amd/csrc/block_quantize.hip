@@ -184,8 +184,8 @@ __global__ __launch_bounds__(256) void block_quantize(QuantArgs a) {
         uint8_t* dst = a.tr.q + (size_t)col * (size_t)a.tr.ld + row;
         if (valid >= 16) {
             // read by a later pass, if at all: past the caches (both ways 8192 x 4096: 30.4 against
-            // 32.1 us). The others' reader comes next; past the caches they would come in 26.7 us,
-            // but two products with their quantizing take 304 instead of 300.
+            // 32.1 us). The others' reader comes next: with them and the products' C past the caches
+            // too this takes 26.7 us, but two products with their quantizing 305 instead of 300.
             store_passing(dst, q);
         } else {
 #pragma unroll
