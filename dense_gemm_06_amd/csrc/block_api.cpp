@@ -198,9 +198,9 @@ bool small_call(const gemm_block_matrix& A, const gemm_block_matrix& B) {
 constexpr int64_t kCus = 256;
 
 // rows: rows of C that share a B (for experts the average); n_products: B's in the call;
-// small: byte offsets within an operand fit 32 bits; full: fp32 C; tr: BlockPlan::tr;
+// small: byte offsets within an operand fit 32 bits; tr: BlockPlan::tr;
 // may_split: whether K may be split.
-dg::BlockPlan block_plan(int64_t rows, int64_t n_products, int64_t N, int64_t K, bool direct, bool small, bool full, int tr,
+dg::BlockPlan block_plan(int64_t rows, int64_t n_products, int64_t N, int64_t K, bool direct, bool small, int tr,
                          bool may_split) {
     dg::BlockPlan p;
     p.tr = tr;
@@ -215,15 +215,14 @@ dg::BlockPlan block_plan(int64_t rows, int64_t n_products, int64_t N, int64_t K,
         const int64_t wgs = n_products * ceil_div(N, p.bn);
         if (may_split && wgs < kCus) p.split = (int)std::max<int64_t>(1, std::min<int64_t>(kCus / wgs, nkb / 16));
     } else {
-        // 256 rows (and 256 columns for C of 16 bits, 128 for fp32) where that leaves most
-        // compute units a tile; with few blocks of k two smaller fp32 tiles to a compute unit,
-        // one of which computes while the other loads or stores, are ahead (64 products of 2048 x
-        // 1024 over 512: 243 against 275 us)
-        const int64_t big = n_products * ceil_div(rows, 256) * ceil_div(N, full ? 128 : 256);
-        const bool large = direct && small && (tr == 0 || (tr == 1 && full)) && big >= kCus * 3 / 4 && !(full && K <= 1024);
+        // 256 rows where that leaves most compute units a tile; with few blocks of k two smaller
+        // tiles to a compute unit, one of which computes while the other loads or stores, are
+        // ahead (64 products of 2048 x 1024 over 512: 243 against 275 us)
+        const int64_t big = n_products * ceil_div(rows, 256) * ceil_div(N, 128);
+        const bool large = direct && small && tr <= 1 && big >= kCus * 3 / 4 && K > 1024;
         p.kernel = large ? dg::BLOCK_TILE256 : dg::BLOCK_TILE128;
         p.bm = large ? 256 : 128;
-        p.bn = large && !full ? 256 : 128;
+        p.bn = 128;
         const int64_t wgs = n_products * ceil_div(rows, p.bm) * ceil_div(N, p.bn);
         if (may_split && wgs < kCus) p.split = (int)std::max<int64_t>(1, std::min<int64_t>(2 * kCus / wgs, nkb / 4));
     }
@@ -283,9 +282,9 @@ int run_block(const gemm_block_matrix& A, const gemm_block_matrix& B, int64_t M,
               void* workspace, int64_t workspace_bytes, hipStream_t stream) {
     const int64_t N = B.rows, K = A.cols;
     const int tr = tr_of(A, B);
-    const bool direct = direct_rows(A, 1) && direct_rows(B, 1), small = small_call(A, B), full = out_dtype == GEMM_F32;
-    dg::BlockPlan p = block_plan(M, 1, N, K, direct, small, full, tr, true);
-    if (split_bytes(p.split, M, N) > workspace_bytes) p = block_plan(M, 1, N, K, direct, small, full, tr, false);
+    const bool direct = direct_rows(A, 1) && direct_rows(B, 1), small = small_call(A, B);
+    dg::BlockPlan p = block_plan(M, 1, N, K, direct, small, tr, true);
+    if (split_bytes(p.split, M, N) > workspace_bytes) p = block_plan(M, 1, N, K, direct, small, tr, false);
     dg::BlockArgs a = block_args(A, B, C, ldc, out_dtype);
     a.mode = dg::BLOCK_PLAIN;
     a.M = (int)M;
@@ -457,9 +456,8 @@ int64_t gemm_block_product_workspace(int64_t M, int64_t N, int64_t K) {
     // every plan that the call may make, for all rows or for whole tiles of them
     for (int64_t rows : {M, M - M % 128, M - M % 256})
         for (bool direct : {false, true})
-            for (bool full : {false, true})
-                for (int tr : {0, 1})
-                    if (rows > 0) bytes = std::max(bytes, split_bytes(block_plan(rows, 1, N, K, direct, direct, full, tr, true).split, rows, N));
+            for (int tr : {0, 1})
+                if (rows > 0) bytes = std::max(bytes, split_bytes(block_plan(rows, 1, N, K, direct, direct, tr, true).split, rows, N));
     return bytes;
 }
 
@@ -492,8 +490,8 @@ int gemm_block_product(const gemm_block_matrix* A, const gemm_block_matrix* B, v
     // tile of theirs takes a third of a whole one's time, behind all the others (2056 x 4000 x
     // 8176 to fp32: 217 us in one launch, 186 in two).
     const int tr = tr_of(*A, *B);
-    const bool direct = direct_rows(*A, 1) && direct_rows(*B, 1), small = small_call(*A, *B), full = out_dtype == GEMM_F32;
-    const int64_t bm = block_plan(M, 1, N, K, direct, small, full, tr, true).bm;
+    const bool direct = direct_rows(*A, 1) && direct_rows(*B, 1), small = small_call(*A, *B);
+    const int64_t bm = block_plan(M, 1, N, K, direct, small, tr, true).bm;
     const int64_t rest = bm >= 128 && tr == 0 && M > bm && M % bm <= 64 ? M % bm : 0;
     DG_TRY(run_block(*A, *B, M - rest, C, ldc, out_dtype, workspace, workspace_bytes, (hipStream_t)stream));
     if (rest == 0) return GEMM_OK;
@@ -661,7 +659,7 @@ int gemm_experts_product(const gemm_block_matrix* A, const gemm_block_matrix* B,
     const bool direct = direct_rows(*A, 1) && direct_rows(*B, E), small = small_call(*A, *B);
     const int64_t pairs = plan->tokens * plan->top_k, active = std::max<int64_t>(1, std::min(E, pairs));
     const dg::BlockPlan p = block_plan(std::max<int64_t>(1, pairs / active), active, N, A->cols, direct,
-                                       small, out_dtype == GEMM_F32, tr_of(*A, *B), false);
+                                       small, tr_of(*A, *B), false);
     dg::BlockArgs a = block_args(*A, *B, C, ldc, out_dtype);
     a.mode = dg::BLOCK_EXPERTS;
     a.M = (int)P;
@@ -701,7 +699,7 @@ int gemm_experts_gradient(const gemm_block_matrix* A, const gemm_block_matrix* B
                           scale_range("B.scale", *B), range("plan.offsets", plan->offsets, (uint64_t)(E + 1) * 4)}));
     DG_TRY(check_device());
     const bool direct = direct_rows(*A, 1) && direct_rows(*B, 1), small = small_call(*A, *B);
-    const dg::BlockPlan p = block_plan(M, E, N, ceil_div(plan->capacity, E), direct, small, out_dtype == GEMM_F32, tr_of(*A, *B), false);
+    const dg::BlockPlan p = block_plan(M, E, N, ceil_div(plan->capacity, E), direct, small, tr_of(*A, *B), false);
     dg::BlockArgs a = block_args(*A, *B, C, ldc, out_dtype);
     a.mode = dg::BLOCK_GRADIENT;
     a.E = (int)E;

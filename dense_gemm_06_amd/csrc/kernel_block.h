@@ -6,16 +6,12 @@
 // each block's sum is then multiplied by both scales and added in fp32, since the scales
 // are arbitrary fp32 numbers and the 8-bit instruction's own scales are powers of two.
 //
-// FULL = false, for C of 16 bits: v_mfma_f32_*_f8f6f4 on the codes. Measured on gfx950 (one
-// large and one small product at every distance, and sums of small ones): the products of
-// 8 neighbouring k are cut, towards zero, to whole multiples of 2^-13 of the power of two
-// under the largest before they are added; sums over those groups are fp32. That is at
-// most 7 * 2^-13 of a group's largest product, on random data 1.4e-5 to 4e-5 of the result
-// (2-norm), against 1e-4 (fp16) and 1.1e-3 (bf16) for C's own rounding: fine there, at twice
-// the rate of 16-bit instructions.
-// FULL = true, for fp32 C, where that would be 100 times the type's step: the codes become
-// fp16 (exactly: e5m2 is fp16's upper byte, e4m3 a subset) in registers, and
-// v_mfma_f32_*_f16 has exact products and fp32 sums.
+// The codes become fp16 (exactly: e5m2 is fp16's upper byte, e4m3 a subset) in registers, and
+// v_mfma_f32_*_f16 has exact products and fp32 sums. The 8-bit instructions, twice as fast,
+// do not hold such sums: measured on gfx950 (v_mfma_f32_32x32x16_fp8_fp8 and both f8f6f4
+// shapes, bit for bit alike), the products of 8 neighbouring k are cut, towards zero, to whole
+// multiples of 2^-13 of the power of two under the largest before they are added, so
+// 448 * 448 - 448 * 448 + 1 is 0. 8192 x 4096 x 4096 to bf16 took 128 us on them.
 //
 // The rows of
 // B are the instruction's first operand, so a lane holds one row m of C and four
@@ -40,16 +36,6 @@ typedef int i32x2 __attribute__((ext_vector_type(2)));
 
 // Source of the chunks that lie past the end of a row.
 __device__ const uint32_t block_zeros[4] = {0, 0, 0, 0};
-
-// first operand rows -> D rows (registers), second -> D columns (lanes)
-template <int T1, int T2>
-__device__ __forceinline__ f32x16 mfma_32(i32x8 x, i32x8 y, f32x16 c) {
-    return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(x, y, c, T1, T2, 0, 0, 0, 0);
-}
-template <int T1, int T2>
-__device__ __forceinline__ f32x4 mfma_16(i32x8 x, i32x8 y, f32x4 c) {
-    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(x, y, c, T1, T2, 0, 0, 0, 0);
-}
 
 typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 
@@ -297,282 +283,11 @@ __device__ __forceinline__ u32x4 load_codes(const uint8_t* p, int valid) {
     return v;
 }
 
-// ---------------------------------------------------------------------------- wide tiles
-// 256 x 256 tiles for C of 16 bits and 16-byte aligned rows: eight waves of 128 x 64, each 8
-// x 4 tiles of v_mfma_f32_16x16x128_f8f6f4, whose one instruction is one block of k. The
-// accumulators (128 registers) have to be ordinary ones, as the scaled additions are done by
-// the vector unit, which rules out larger wave tiles; with 32 x 32 instructions the parts and
-// fragments in flight spilled.
-//
-// A wave keeps the block's 4 fragments of B, reads the 8 of A one ahead of their use, and
-// adds a row of parts while the matrix core computes the next. LDS holds two stages of a
-// block (layout as below; lane (l16, lg) takes chunks lg and lg + 4 of its row, so that the
-// phases of a read see two chunks that differ in the lowest bit and cover all banks). Before
-// the last fragment row of a block its reads are done: the barrier there publishes the next
-// block, the freed stage is refilled with the one after it, and the next block's fragments
-// replace those of B behind their last use.
-//
-// 8192 x 4096 x 4096: 125 us, 2200 TFLOP/s at 2.0 GHz; matrix instructions alone would take
-// 65 us, the same loop without its scaled additions and without its copies 97 us (so 24 us
-// go to what additions do not hide behind matrix instructions and 23 to the copies), C and
-// the first copies of the two tiles of each compute unit 17 us.
-template <int TA, int TB, bool BROW>
-__global__ __launch_bounds__(512) void block_wide(BlockArgs g) {
-    constexpr int BM = 256, BN = 256, NW = 8, FM = 8, FN = 4;
-    constexpr int STAGE = BM * kBlock, STAGE_S = (BM + BN) * 4, ROW = 68;
-    __shared__ __attribute__((aligned(1024))) uint8_t lds[4 * STAGE + 2 * STAGE_S];
-    uint8_t* const sA = lds;
-    uint8_t* const sB = lds + 2 * STAGE;
-    float* const fS = reinterpret_cast<float*>(lds + 4 * STAGE);
-    const int tid = threadIdx.x, lane = tid & 63;
-    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int wm = wave >> 2, wn = wave & 3;
-    const int l16 = lane & 15, lg = lane >> 4;
-
-    BlockTile t;
-    const bool any = block_tile_of<BM, BN>(g, t);
-    if (g.mode == BLOCK_EXPERTS) clear_tail(g);
-    if (!any) return;
-
-    // ---- sources: lane's chunk of copy c is row (4 wave + c)*8 + lane/8, 16-byte chunk
-    // (lane & 7) ^ ((row >> 1) & 7); 32-bit offsets from the block's first byte (the host
-    // takes this kernel where they suffice)
-    const uint8_t* ba = g.A + (size_t)t.kb0 * kBlock;
-    const uint8_t* bb = g.B + (size_t)t.kb0 * kBlock;
-    uint32_t oa[4], ob[4];
-    int kc[2];
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
-        const int row = (wave * 4 + c) * 8 + (lane >> 3);
-        const int k = ((lane & 7) ^ ((row >> 1) & 7)) * 16;
-        kc[c & 1] = k;  // the same for c and c + 2
-        const int r = max(block_a_row(g, t, min(t.m0 + row, t.m_end - 1)), 0);
-        oa[c] = (uint32_t)r * (uint32_t)g.lda + (uint32_t)k;
-        ob[c] = (uint32_t)min(t.n0 + row, g.N - 1) * (uint32_t)g.ldb + (uint32_t)k;
-    }
-    const float* ps;
-    int64_t ps_step;
-    if (wave < 4) {
-        const int r = max(block_a_row(g, t, min(t.m0 + wave * 64 + lane, t.m_end - 1)), 0);
-        ps = g.SA + (size_t)(r >> g.a_shift) * (size_t)g.sa_row + (size_t)t.kb0 * (size_t)g.sa_blk;
-        ps_step = g.sa_blk;
-    } else {
-        const int n = min(t.n0 + (wave - 4) * 64 + lane, g.N - 1);
-        ps = g.SB + (size_t)(n >> g.b_shift) * (size_t)g.sb_row + (size_t)t.kb0 * (size_t)g.sb_blk;
-        ps_step = g.sb_blk;
-    }
-    const uint32_t dA = (uint32_t)reinterpret_cast<uintptr_t>(DG_LDSV(sA)) + (uint32_t)wave * 4096u;
-    const uint32_t dB = (uint32_t)reinterpret_cast<uintptr_t>(DG_LDSV(sB)) + (uint32_t)wave * 4096u;
-    const uint32_t dS = (uint32_t)reinterpret_cast<uintptr_t>(DG_LDSV(fS)) + (uint32_t)wave * 256u;
-    // copy c (0 .. 3) of A and of B of block kb
-    auto issue = [&](int kb, int c) {
-        const uint32_t st = (uint32_t)(kb & 1);
-        const size_t k = (size_t)kb * kBlock;
-        if (kb < t.nkb - 1 || t.krem == kBlock) {
-            __builtin_amdgcn_global_load_lds(DG_GLB(ba + k + oa[c]), DG_LDS_ADDR(dA + st * STAGE + c * 1024u), 16, 0, 0);
-            __builtin_amdgcn_global_load_lds(DG_GLB(bb + k + ob[c]), DG_LDS_ADDR(dB + st * STAGE + c * 1024u), 16, 0, 0);
-        } else {
-            const bool in = kc[c & 1] < t.krem;
-            const void* a = in ? static_cast<const void*>(ba + k + oa[c]) : block_zeros;
-            const void* b = in ? static_cast<const void*>(bb + k + ob[c]) : block_zeros;
-            __builtin_amdgcn_global_load_lds(DG_GLB(a), DG_LDS_ADDR(dA + st * STAGE + c * 1024u), 16, 0, 0);
-            __builtin_amdgcn_global_load_lds(DG_GLB(b), DG_LDS_ADDR(dB + st * STAGE + c * 1024u), 16, 0, 0);
-        }
-    };
-    auto issue_scales = [&](int kb) {
-        __builtin_amdgcn_global_load_lds(DG_GLB(ps), DG_LDS_ADDR(dS + (uint32_t)(kb & 1) * STAGE_S), 4, 0, 0);
-        ps += ps_step;
-    };
-    auto issue_all = [&](int kb) {
-        issue_scales(kb);
-#pragma unroll
-        for (int c = 0; c < 4; ++c) issue(kb, c);
-    };
-    auto published = [&]() {  // this wave's copies have landed, and after the barrier everybody's
-        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
-        __builtin_amdgcn_s_barrier();
-        asm volatile("" ::: "memory");
-    };
-
-    const int off = l16 * kBlock + ((lg ^ ((l16 >> 1) & 7)) << 4);
-    auto frag = [&](const uint8_t* base) {
-        const u32x4 x = *reinterpret_cast<const u32x4*>(base + off);
-        const u32x4 y = *reinterpret_cast<const u32x4*>(base + (off ^ 64));
-        return i32x8{(int)x[0], (int)x[1], (int)x[2], (int)x[3], (int)y[0], (int)y[1], (int)y[2], (int)y[3]};
-    };
-    const uint8_t* const aw = sA + wm * 128 * kBlock;
-    const uint8_t* const bw = sB + wn * 64 * kBlock;
-    const float* const fa = fS + wm * 128 + l16;
-    const float* const fb = fS + BM + wn * 64;
-
-    f32x4 acc[FM][FN];
-#pragma unroll
-    for (int i = 0; i < FM; ++i)
-#pragma unroll
-        for (int j = 0; j < FN; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
-    const bool mine = t.m0 + wm * 128 < t.m_end;  // this wave has rows of C
-    if (t.bad) {
-#pragma unroll
-        for (int i = 0; i < FM; ++i)
-#pragma unroll
-            for (int j = 0; j < FN; ++j) acc[i][j] = f32x4{1, 1, 1, 1} * __builtin_nanf("");
-    }
-
-    i32x8 bf[FN], af[2];
-    f32x4 part[FN], sb[BROW ? FN : 1];
-    float sa[4];
-    auto read_sb = [&](int st) {
-        const float* f = fb + st * (BM + BN);
-        if constexpr (BROW) {
-#pragma unroll
-            for (int j = 0; j < FN; ++j) sb[j] = *reinterpret_cast<const f32x4*>(f + j * 16 + lg * 4);
-        } else {
-            sb[0][0] = f[0];
-        }
-    };
-    // the scaled part of fragment row i, column j
-    auto add = [&](int i, int j, float s) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-            acc[i][j][e] = fmaf(part[j][e], BROW ? s * sb[BROW ? j : 0][e] : s, acc[i][j][e]);
-    };
-
-    if (t.nkb > 0) {
-        issue_all(0);
-        published();
-        if (mine) {
-#pragma unroll
-            for (int j = 0; j < FN; ++j) bf[j] = frag(bw + j * 16 * kBlock);
-            af[0] = frag(aw);
-            sa[0] = fa[0];
-            read_sb(0);
-        }
-        if (t.nkb > 1) {
-            issue_scales(1);
-            issue(1, 0);
-        }
-    }
-    for (int kb = 0; kb < t.nkb; ++kb) {
-        const int st = kb & 1, next = st ^ 1;
-#pragma unroll
-        for (int i = 0; i < FM - 1; ++i) {
-            if (mine) {
-                // a part is added just before the instruction that replaces it, four
-                // instructions after it was asked for; pinned, as are the reads of the next
-                // fragment behind the first instruction that uses this one: the compiler waits
-                // for all LDS reads in flight where it waits for one, so reads issued before
-                // that wait would be waited for at once, and left to itself it puts them at the
-                // end, too late to hide their latency
-                const float s = i > 0 ? (BROW ? sa[(i - 1) & 3] : sa[(i - 1) & 3] * sb[0][0]) : 0.0f;
-#pragma unroll
-                for (int j = 0; j < FN; ++j) {
-                    if (i > 0) add(i - 1, j, s);
-                    part[j] = mfma_16<TB, TA>(bf[j], af[i & 1], f32x4{0, 0, 0, 0});
-                    __builtin_amdgcn_sched_barrier(0);
-                    if (j == 0) {
-                        af[(i + 1) & 1] = frag(aw + st * STAGE + (i + 1) * 16 * kBlock);
-                        sa[(i + 1) & 3] = fa[st * (BM + BN) + (i + 1) * 16];
-                        __builtin_amdgcn_sched_barrier(0);
-                    }
-                }
-            }
-            // the copies of the next block, a few at a time: all at once they hold up every wave
-            // until the address unit has taken them
-            if (i < 3 && kb + 1 < t.nkb) issue(kb + 1, i + 1);
-        }
-        if (kb + 1 < t.nkb) {
-            published();
-            if (kb + 2 < t.nkb) {
-                issue_scales(kb + 2);
-                issue(kb + 2, 0);
-            }
-        }
-        if (mine) {
-            // past the end of k these reads find old data, which nothing uses
-            const float s6 = BROW ? sa[2] : sa[2] * sb[0][0], s7 = BROW ? sa[3] : sa[3] * sb[0][0];
-#pragma unroll
-            for (int j = 0; j < FN; ++j) {
-                add(FM - 2, j, s6);
-                part[j] = mfma_16<TB, TA>(bf[j], af[1], f32x4{0, 0, 0, 0});
-                __builtin_amdgcn_sched_barrier(0);
-                if (j > 0) bf[j - 1] = frag(bw + next * STAGE + (j - 1) * 16 * kBlock);
-                __builtin_amdgcn_sched_barrier(0);
-            }
-            bf[FN - 1] = frag(bw + next * STAGE + (FN - 1) * 16 * kBlock);
-            af[0] = frag(aw + next * STAGE);
-            sa[0] = fa[next * (BM + BN)];
-#pragma unroll
-            for (int j = 0; j < FN; ++j) add(FM - 1, j, s7);
-            read_sb(next);
-            __builtin_amdgcn_sched_barrier(0);
-        }
-    }
-
-    // ---- C through LDS, so that each store instruction writes whole 128-byte rows
-    __builtin_amdgcn_s_barrier();  // every wave has read its last fragments
-    asm volatile("" ::: "memory");
-    if (!mine) return;
-    const int m0 = t.m0 + wm * 128, n0 = t.n0 + wn * 64;
-    const uint64_t live[2] = {live_rows(g, t, m0), live_rows(g, t, m0 + 64)};
-    if (g.out_dt == DT_F32) {  // a K slice's sums
-        float* const stage = reinterpret_cast<float*>(lds) + wave * (16 * ROW);
-        float* const C = static_cast<float*>(g.C);
-        const int n = n0 + l16 * 4;
-#pragma unroll
-        for (int i = 0; i < FM; ++i) {
-#pragma unroll
-            for (int j = 0; j < FN; ++j) *reinterpret_cast<f32x4*>(stage + l16 * ROW + j * 16 + lg * 4) = acc[i][j];
-            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-#pragma unroll
-            for (int p = 0; p < 4; ++p) {
-                const int row = p * 4 + lg, m = m0 + i * 16 + row;
-                const f32x4 v = *reinterpret_cast<const f32x4*>(stage + row * ROW + l16 * 4);
-                float* const c = C + (size_t)m * (size_t)g.ldc + n;
-                if (m < t.m_end && n + 4 <= g.ldc) __builtin_memcpy(c, &v, 16);  // the slices' rows are padded to 4
-            }
-            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-        }
-        return;
-    }
-    // all 128 rows as 16-bit numbers: 128 bytes a row, 16-byte chunks permuted by (row >> 1) & 7
-    uint8_t* const stage = lds + wave * (128 * 128);
-    auto to_lds = [&](auto dt) {
-#pragma unroll
-        for (int i = 0; i < FM; ++i)
-#pragma unroll
-            for (int j = 0; j < FN; ++j) {
-                const f32x4 v = acc[i][j];
-                const u32x2 h = {pack16<decltype(dt)::value>(v[0], v[1]), pack16<decltype(dt)::value>(v[2], v[3])};
-                *reinterpret_cast<u32x2*>(stage + (i * 16 + l16) * 128 + (((2 * j + (lg >> 1)) ^ ((l16 >> 1) & 7)) << 4) +
-                                          (lg & 1) * 8) = h;
-            }
-    };
-    if (g.out_dt == DT_F16) to_lds(std::integral_constant<int, DT_F16>{});
-    else to_lds(std::integral_constant<int, DT_BF16>{});
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    uint16_t* const C = static_cast<uint16_t*>(g.C);
-    const int n = n0 + (lane & 7) * 8;
-#pragma unroll 4
-    for (int p = 0; p < 16; ++p) {
-        const int row = p * 8 + (lane >> 3), m = m0 + row;
-        u32x4 v = *reinterpret_cast<const u32x4*>(stage + row * 128 + (((lane & 7) ^ ((row >> 1) & 7)) << 4));
-        if (!((live[p >> 3] >> (row & 63)) & 1)) v = u32x4{0, 0, 0, 0};
-        if (m >= t.m_end || n >= g.N) continue;
-        uint16_t* const c = C + (size_t)m * (size_t)g.ldc + n;
-        if (n + 8 <= g.N) {
-            __builtin_memcpy(c, &v, 16);
-        } else {
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-                if (n + e < g.N) c[e] = (uint16_t)(v[e >> 1] >> (16 * (e & 1)));
-        }
-    }
-}
-
-// ---------------------------------------------------------------------------- fp32 sums, aligned rows
-// (64 WM) x 128 tiles for fp32 C and 16-byte aligned rows on 2 WM waves of 64 x 64, each 4 x 4
+// ---------------------------------------------------------------------------- aligned rows
+// (64 WM) x 128 tiles for 16-byte aligned rows on 2 WM waves of 64 x 64, each 4 x 4
 // tiles of v_mfma_f32_16x16x32_f16, four instructions to a block of k. Codes are copied
-// straight to LDS (S stages laid out as in the wide tiles) S - 1 blocks ahead and widened in
+// straight to LDS (S stages of rows of 128 bytes, 16-byte chunk c of row r at c ^ ((r >> 1) & 7),
+// so that the phases of a read cover all banks) S - 1 blocks ahead and widened in
 // the fragments: a wave holds the block's four fragments of B as halves (64 registers),
 // widens those of A one ahead and, behind the last use of each of B's, the next block's.
 // Vector and matrix instructions are even (with a scale for each row of B: 256 of 4 cycles
@@ -581,10 +296,11 @@ __global__ __launch_bounds__(512) void block_wide(BlockArgs g) {
 // (271 against 219 us at 2056 x 4000 x 8176 with one workgroup of each).
 // TRB: B is stored with its rows adjacent; its stage then holds 128 rows of k, 16-byte chunk c
 // of row k at c ^ (((k >> 1) & 3) | ((k >> 2) & 4)), and 8 k of a row of B come from
-// ds_read_b64_tr_b8 (see the tiles below): the 32 lanes of a phase see 16 rows of k, two groups
+// ds_read_b64_tr_b8: in each 16 lanes, lane i addresses 8 bytes of row k0 + i/2 at half i%2 of a
+// chunk and receives column i of the 8 rows. The 32 lanes of a phase see 16 rows of k, two groups
 // of 8 that lie 16 apart, at one chunk, in 16 different places.
 template <int TA, int TB, bool BROW, int WM, int S, bool TRB = false>
-__global__ __launch_bounds__(WM * 128, 2) void block_full_direct(BlockArgs g) {
+__global__ __launch_bounds__(WM * 128, 2) void block_direct(BlockArgs g) {
     constexpr int NW = 2 * WM, BM = 64 * WM, BN = 128, FM = 4, FN = 4;
     constexpr int CB = BN / 8 / NW;  // copies of 1 KB (8 rows) of B for each wave; 4 of A
     constexpr int AHEAD = WM == 2 || TRB ? 1 : 2;  // fragments of codes read ahead (as registers allow)
@@ -844,16 +560,60 @@ __global__ __launch_bounds__(WM * 128, 2) void block_full_direct(BlockArgs g) {
         for (int q = 0; q < 16; ++q) add1(FM - 1, q, s_last);
     }
 
-    // ---- C from the registers: a lane's four columns are 16 bytes, four lanes' 64 of a row
+    // lanes counted anew, so that nothing of this waits in registers through the loop
+    int at = (int)__builtin_amdgcn_mbcnt_hi(~0u, __builtin_amdgcn_mbcnt_lo(~0u, 0u));
+    asm("" : "+v"(at));
+    const int r16 = at & 15, rg = at >> 4;
+    const uint64_t live = live_rows(g, t, t.m0 + wm * 64);
+    if (g.out_dt != DT_F32) {
+        // ---- C of 16 bits through LDS, so that each store instruction writes whole 128-byte
+        // rows: the wave's 64 rows, 16-byte chunks permuted by (row >> 1) & 7
+        __builtin_amdgcn_s_barrier();  // every wave has read its last fragments
+        asm volatile("" ::: "memory");
+        if (!active) return;
+        uint8_t* const stage = lds + wave * (64 * 128);
+        auto to_lds = [&](auto dt) {
+#pragma unroll
+            for (int i = 0; i < FM; ++i)
+#pragma unroll
+                for (int j = 0; j < FN; ++j) {
+                    const f32x4 v = acc[i][j];
+                    const u32x2 h = {pack16<decltype(dt)::value>(v[0], v[1]), pack16<decltype(dt)::value>(v[2], v[3])};
+                    *reinterpret_cast<u32x2*>(stage + (i * 16 + r16) * 128 + (((2 * j + (rg >> 1)) ^ ((r16 >> 1) & 7)) << 4) +
+                                              (rg & 1) * 8) = h;
+                }
+        };
+        if (g.out_dt == DT_F16) to_lds(std::integral_constant<int, DT_F16>{});
+        else to_lds(std::integral_constant<int, DT_BF16>{});
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        uint16_t* const C = static_cast<uint16_t*>(g.C);
+        const int n = t.n0 + wn * 64 + (at & 7) * 8;
+#pragma unroll 4
+        for (int p = 0; p < 8; ++p) {
+            const int row = p * 8 + (at >> 3), m = t.m0 + wm * 64 + row;
+            u32x4 v = *reinterpret_cast<const u32x4*>(stage + row * 128 + (((at & 7) ^ ((row >> 1) & 7)) << 4));
+            if (!((live >> row) & 1)) v = u32x4{0, 0, 0, 0};
+            if (m >= t.m_end || n >= g.N) continue;
+            uint16_t* const c = C + (size_t)m * (size_t)g.ldc + n;
+            if (n + 8 <= g.N) {
+                __builtin_memcpy(c, &v, 16);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    if (n + e < g.N) c[e] = (uint16_t)(v[e >> 1] >> (16 * (e & 1)));
+            }
+        }
+        return;
+    }
+    // ---- fp32 C from the registers: a lane's four columns are 16 bytes, four lanes' 64 of a row
     if (!active) return;
     float* const C = static_cast<float*>(g.C);
     const bool whole = t.n0 + BN <= g.N;
-    const uint64_t live = live_rows(g, t, t.m0 + wm * 64);
 #pragma unroll
     for (int i = 0; i < FM; ++i) {
-        const int m = t.m0 + wm * 64 + i * 16 + l16;
-        const bool zero = !((live >> (i * 16 + l16)) & 1);
-        float* const c = C + (size_t)m * (size_t)g.ldc + t.n0 + wn * 64 + lg * 4;
+        const int m = t.m0 + wm * 64 + i * 16 + r16;
+        const bool zero = !((live >> (i * 16 + r16)) & 1);
+        float* const c = C + (size_t)m * (size_t)g.ldc + t.n0 + wn * 64 + rg * 4;
         if (m >= t.m_end) continue;
 #pragma unroll
         for (int j = 0; j < FN; ++j) {
@@ -863,13 +623,13 @@ __global__ __launch_bounds__(WM * 128, 2) void block_full_direct(BlockArgs g) {
             } else {
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                    if (t.n0 + wn * 64 + j * 16 + lg * 4 + e < g.N) c[j * 16 + e] = v[e];
+                    if (t.n0 + wn * 64 + j * 16 + rg * 4 + e < g.N) c[j * 16 + e] = v[e];
             }
         }
     }
 }
 
-// ---------------------------------------------------------------------------- fp32 sums, any layout
+// ---------------------------------------------------------------------------- any layout
 // The same tiles for rows at any byte address and for operands with adjacent rows, on 2 x 2
 // tiles of v_mfma_f32_32x32x16_f16 for each wave: the codes go through registers and are
 // widened on their way into LDS, once for the whole workgroup. LDS holds one
@@ -881,7 +641,7 @@ __global__ __launch_bounds__(WM * 128, 2) void block_full_direct(BlockArgs g) {
 // adjacent rows (TR, as below) is held as 128 rows of k, its 32-byte units of 16 rows
 // permuted by 2 (k & 3), and read through ds_read_b64_tr_b16.
 template <int TA, int TB, bool BROW, int TR>
-__global__ __launch_bounds__(256, 2) void block_full(BlockArgs g) {
+__global__ __launch_bounds__(256, 2) void block_staged(BlockArgs g) {
     constexpr int BM = 128, BN = 128, FM = 2, FN = 2, ROW = 68;
     constexpr bool TRB = (TR & 1) != 0, TRA = (TR & 2) != 0;
     __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * 128 * 256 + (BM + BN) * 4];
@@ -1069,9 +829,12 @@ __global__ __launch_bounds__(256, 2) void block_full(BlockArgs g) {
 
     // ---- C through LDS, 32 rows of the wave's 64 columns at a time (no wave reads or writes
     // the operands' stage any more)
+    // lanes counted anew, so that nothing of this waits in registers through the loop
+    int at = (int)__builtin_amdgcn_mbcnt_hi(~0u, __builtin_amdgcn_mbcnt_lo(~0u, 0u));
+    asm("" : "+v"(at));
+    const int r32 = at & 31, rh = at >> 5, r16 = at & 15, rg = at >> 4;
     float* const stage = reinterpret_cast<float*>(lds) + wave * (32 * ROW);
-    float* const C = static_cast<float*>(g.C);
-    const int n = t.n0 + wn * 64 + l16 * 4;
+    const int n = t.n0 + wn * 64 + r16 * 4;
     const bool whole = t.n0 + BN <= g.N;
 #pragma unroll
     for (int i = 0; i < FM; ++i) {
@@ -1084,298 +847,24 @@ __global__ __launch_bounds__(256, 2) void block_full(BlockArgs g) {
             for (int q = 0; q < 4; ++q) {
                 f32x4 v = {acc[i][j][q * 4], acc[i][j][q * 4 + 1], acc[i][j][q * 4 + 2], acc[i][j][q * 4 + 3]};
                 if (t.bad) v = f32x4{1, 1, 1, 1} * __builtin_nanf("");
-                *reinterpret_cast<f32x4*>(stage + l32 * ROW + j * 32 + q * 8 + lh * 4) = v;
-            }
-        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-#pragma unroll
-        for (int p = 0; p < 8; ++p) {
-            const int row = p * 4 + lg, m = first + row;
-            f32x4 v = *reinterpret_cast<const f32x4*>(stage + row * ROW + l16 * 4);
-            if (!((live >> row) & 1)) v = f32x4{0, 0, 0, 0};
-            float* const c = C + (size_t)m * (size_t)g.ldc + n;
-            if (m >= t.m_end) continue;
-            if (whole) {
-                // a weight's gradient is far larger than the codes, which other tiles read again:
-                // past the caches (64 experts, 512 rows each, 2048 x 1024: 273 against 279 us)
-                store_passing(c, v);
-            } else {
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    if (n + e < g.N) c[e] = v[e];
-            }
-        }
-        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    }
-}
-
-// ---------------------------------------------------------------------------- tiles
-// BM x BN tiles on WM x WN waves, each wave SM x SJ subtiles of 32 x 32. LDS holds two
-// stages of one block of k: rows of 128 bytes whose 16-byte chunks are permuted by
-// (row >> 1) & 7, so that the 16 rows of any phase of a fragment read spread over all 64
-// banks, and the block's scales. DIRECT: the copies go from global memory straight to
-// LDS; otherwise (rows at any byte address) through registers.
-// TR: bit 0, B is stored with its rows adjacent (element (n, k) at k*ldb + n), bit 1 the
-// same for A. Such an operand's stage holds 128 rows of k, chunk c of row k at
-// c ^ 2((k >> 1) & 3), and a fragment's 8 k of one row come from ds_read_b64_tr_b8: in each
-// 16 lanes, lane i addresses 8 bytes of row k0 + i/2 at half i%2 of a chunk and receives
-// column i of the 8 rows. The 32 lanes of a phase then touch 8 rows x 32 bytes in 8
-// different places of the 256-byte bank period.
-template <int TA, int TB, bool BROW, int BM, int BN, int WM, int WN, bool DIRECT, int TR = 0>
-__global__ __launch_bounds__(WM* WN * 64) void block_tile(BlockArgs g) {
-    constexpr int NW = WM * WN, SM = BM / 32 / WM, SJ = BN / 32 / WN;
-    constexpr int CA = BM / 8 / NW, CB = BN / 8 / NW;  // 1 KB copies (8 rows) per wave
-    static_assert((BM + BN) / 64 == NW, "each wave copies 64 scales of a stage");
-    constexpr bool TRB = (TR & 1) != 0, TRA = (TR & 2) != 0;
-    static_assert(TR == 0 || (BM == kBlock && BN == kBlock), "a transposed stage has rows of 128 bytes");
-    // two stages of A, of B and of their scales; after the k loop each wave's part of C
-    constexpr int STAGE_A = BM * kBlock, STAGE_B = BN * kBlock, STAGE_S = (BM + BN) * 4;
-    constexpr int ROW = SJ * 32 + 4;  // floats of a staged row of C: 16 rows start in 16 different places of the banks
-    static_assert(NW * 32 * ROW * 4 <= 2 * (STAGE_A + STAGE_B), "C is staged where A and B were");
-    __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * (STAGE_A + STAGE_B + STAGE_S)];
-    uint8_t* const sA = lds;
-    uint8_t* const sB = lds + 2 * STAGE_A;
-    float* const fS = reinterpret_cast<float*>(lds + 2 * (STAGE_A + STAGE_B));
-
-    const int tid = threadIdx.x, lane = tid & 63;
-    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int wm = wave / WN, wn = wave % WN;
-    const int l32 = lane & 31, lh = lane >> 5;
-
-    BlockTile t;
-    const bool any = block_tile_of<BM, BN>(g, t);
-    if (g.mode == BLOCK_EXPERTS) clear_tail(g);
-    if (!any) return;
-
-    // ---- sources of this lane's copies: chunk positions lane & 7 of 8 rows. ka, kb: the k
-    // of a chunk within the block; va, vb: the bytes of a transposed chunk inside the matrix
-    const uint8_t* pa[CA];
-    const uint8_t* pb[CB];
-    int ka[CA], kc[CB], va[TRA ? CA : 1], vb[TRB ? CB : 1];
-    const size_t step_a = TRA ? (size_t)kBlock * (size_t)g.lda : kBlock;
-    const size_t step_b = TRB ? (size_t)kBlock * (size_t)g.ldb : kBlock;
-#pragma unroll
-    for (int i = 0; i < CA; ++i) {
-        const int row = (wave * CA + i) * 8 + (lane >> 3);
-        if constexpr (TRA) {
-            const int m = t.m0 + ((lane & 7) ^ (2 * ((row >> 1) & 3))) * 16;
-            ka[i] = row;
-            va[i] = g.M - m;
-            pa[i] = g.A + ((size_t)t.kb0 * kBlock + row) * (size_t)g.lda + m;
-        } else {
-            ka[i] = ((lane & 7) ^ ((row >> 1) & 7)) * 16;
-            const int r = max(block_a_row(g, t, min(t.m0 + row, t.m_end - 1)), 0);
-            pa[i] = g.A + (size_t)r * (size_t)g.lda + (size_t)t.kb0 * kBlock + ka[i];
-        }
-    }
-#pragma unroll
-    for (int i = 0; i < CB; ++i) {
-        const int row = (wave * CB + i) * 8 + (lane >> 3);
-        if constexpr (TRB) {
-            const int n = t.n0 + ((lane & 7) ^ (2 * ((row >> 1) & 3))) * 16;
-            kc[i] = row;
-            vb[i] = g.N - n;
-            pb[i] = g.B + ((size_t)t.kb0 * kBlock + row) * (size_t)g.ldb + n;
-        } else {
-            kc[i] = ((lane & 7) ^ ((row >> 1) & 7)) * 16;
-            pb[i] = g.B + (size_t)min(t.n0 + row, g.N - 1) * (size_t)g.ldb + (size_t)t.kb0 * kBlock + kc[i];
-        }
-    }
-    const float* ps;
-    int64_t ps_step;
-    if (wave < BM / 64) {
-        const int r = max(block_a_row(g, t, min(t.m0 + wave * 64 + lane, t.m_end - 1)), 0);
-        ps = g.SA + (size_t)(r >> g.a_shift) * (size_t)g.sa_row + (size_t)t.kb0 * (size_t)g.sa_blk;
-        ps_step = g.sa_blk;
-    } else {
-        const int n = min(t.n0 + (wave - BM / 64) * 64 + lane, g.N - 1);
-        ps = g.SB + (size_t)(n >> g.b_shift) * (size_t)g.sb_row + (size_t)t.kb0 * (size_t)g.sb_blk;
-        ps_step = g.sb_blk;
-    }
-    // LDS destinations as plain numbers: the compiler then does not make every LDS read
-    // wait for all copies in flight; the explicit waits below order them.
-    const uint32_t dA = (uint32_t)reinterpret_cast<uintptr_t>(DG_LDSV(sA)) + (uint32_t)wave * (CA * 1024u);
-    const uint32_t dB = (uint32_t)reinterpret_cast<uintptr_t>(DG_LDSV(sB)) + (uint32_t)wave * (CB * 1024u);
-    const uint32_t dS = (uint32_t)reinterpret_cast<uintptr_t>(DG_LDSV(fS)) + (uint32_t)wave * 256u;
-
-    u32x4 ra[DIRECT ? 1 : CA], rb[DIRECT ? 1 : CB];
-    auto issue = [&](int kb) {
-        const uint32_t st = (uint32_t)(kb & 1);
-        const int rem = kb == t.nkb - 1 ? t.krem : kBlock;
-        __builtin_amdgcn_global_load_lds(DG_GLB(ps + (size_t)kb * (size_t)ps_step), DG_LDS_ADDR(dS + st * STAGE_S), 4, 0, 0);
-        if constexpr (DIRECT) {
-#pragma unroll
-            for (int i = 0; i < CA; ++i) {
-                const void* src = pa[i] + (size_t)kb * step_a;
-                if (ka[i] >= rem || (TRA && va[TRA ? i : 0] <= 0)) src = block_zeros;
-                __builtin_amdgcn_global_load_lds(DG_GLB(src), DG_LDS_ADDR(dA + st * STAGE_A + i * 1024u), 16, 0, 0);
-            }
-#pragma unroll
-            for (int i = 0; i < CB; ++i) {
-                const void* src = pb[i] + (size_t)kb * step_b;
-                if (kc[i] >= rem || (TRB && vb[TRB ? i : 0] <= 0)) src = block_zeros;
-                __builtin_amdgcn_global_load_lds(DG_GLB(src), DG_LDS_ADDR(dB + st * STAGE_B + i * 1024u), 16, 0, 0);
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < CA; ++i)
-                ra[i] = load_codes(pa[i] + (size_t)kb * step_a, !TRA ? rem - ka[i] : ka[i] < rem ? va[TRA ? i : 0] : 0);
-#pragma unroll
-            for (int i = 0; i < CB; ++i)
-                rb[i] = load_codes(pb[i] + (size_t)kb * step_b, !TRB ? rem - kc[i] : kc[i] < rem ? vb[TRB ? i : 0] : 0);
-        }
-    };
-    auto settle = [&](int kb) {  // registers to LDS
-        if constexpr (!DIRECT) {
-            uint8_t* a = sA + (kb & 1) * STAGE_A + wave * (CA * 1024) + lane * 16;
-            uint8_t* b = sB + (kb & 1) * STAGE_B + wave * (CB * 1024) + lane * 16;
-#pragma unroll
-            for (int i = 0; i < CA; ++i) *reinterpret_cast<u32x4*>(a + i * 1024) = ra[i];
-#pragma unroll
-            for (int i = 0; i < CB; ++i) *reinterpret_cast<u32x4*>(b + i * 1024) = rb[i];
-        }
-    };
-
-    // ---- fragments: lane (l32, lh) takes chunks 4h + 2lh and 4h + 2lh + 1 of its row
-    int off[2][2];
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int u = 0; u < 2; ++u) off[h][u] = l32 * kBlock + (((4 * h + 2 * lh + u) ^ ((l32 >> 1) & 7)) << 4);
-    auto frag = [&](const uint8_t* base, int h) {
-        const u32x4 x = *reinterpret_cast<const u32x4*>(base + off[h][0]);
-        const u32x4 y = *reinterpret_cast<const u32x4*>(base + off[h][1]);
-        return i32x8{(int)x[0], (int)x[1], (int)x[2], (int)x[3], (int)y[0], (int)y[1], (int)y[2], (int)y[3]};
-    };
-
-    // a transposed operand: the 8-byte pieces u = 0 .. 3 of a lane's 32 k, at rows
-    // 64h + 32lh + 8u + l16/2; `sub` is the subtile's number within the stage
-    const int l16 = lane & 15, lg = lane >> 4;
-    auto frag_tr = [&](const uint8_t* stage, int sub, int h) {
-        const int at = (32 * lh + (l16 >> 1)) * kBlock + (((2 * sub + (lg & 1)) ^ (2 * ((l16 >> 2) & 3))) << 4) + (l16 & 1) * 8;
-        i32x8 r;
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            const i32x2 v = __builtin_amdgcn_ds_read_tr8_b64_v2i32(DG_LDS_PTR(i32x2, stage + at + (64 * h + 8 * u) * kBlock));
-            r[2 * u] = v[0];
-            r[2 * u + 1] = v[1];
-        }
-        return r;
-    };
-    auto a_frag = [&](int st, int i, int h) {
-        if constexpr (TRA) return frag_tr(sA + st * STAGE_A, wm * SM + i, h);
-        else return frag(sA + st * STAGE_A + (wm * SM + i) * 32 * kBlock, h);
-    };
-    auto b_frag = [&](int st, int j, int h) {
-        if constexpr (TRB) return frag_tr(sB + st * STAGE_B, wn * SJ + j, h);
-        else return frag(sB + st * STAGE_B + (wn * SJ + j) * 32 * kBlock, h);
-    };
-
-    f32x16 acc[SM][SJ];
-#pragma unroll
-    for (int i = 0; i < SM; ++i)
-#pragma unroll
-        for (int j = 0; j < SJ; ++j) acc[i][j] = f32x16{0};
-
-    // subtiles of 32 rows of this wave that hold rows of C: an expert's last tile, or a
-    // matrix's, does not multiply what lies past its rows
-    const int subs = min(max((t.m_end - t.m0 + 31) / 32 - wm * SM, 0), SM);
-
-    if (t.nkb > 0) {
-        issue(0);
-        settle(0);
-    }
-    for (int kb = 0; kb < t.nkb; ++kb) {
-        const int st = kb & 1;
-        // this wave's copies of block kb have landed, and after the barrier everybody's;
-        // everybody has also read the stage that the next copies overwrite
-        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
-        __builtin_amdgcn_s_barrier();
-        asm volatile("" ::: "memory");
-        if (kb + 1 < t.nkb) issue(kb + 1);
-        const float* fa = fS + st * (BM + BN) + wm * SM * 32 + l32;
-        const float* fb = fS + st * (BM + BN) + BM + wn * SJ * 32;
-        f32x4 sb[SJ][BROW ? 4 : 1];
-#pragma unroll
-        for (int j = 0; j < SJ; ++j) {
-            if constexpr (BROW) {
-#pragma unroll
-                for (int q = 0; q < 4; ++q) sb[j][q] = *reinterpret_cast<const f32x4*>(fb + j * 32 + q * 8 + lh * 4);
-            } else {
-                sb[j][0][0] = fb[j * 32];
-            }
-        }
-        auto add = [&](int i, int j, const f32x16& part) {
-            const float sa = fa[i * 32];
-            if constexpr (BROW) {
-#pragma unroll
-                for (int r = 0; r < 16; ++r) acc[i][j][r] = fmaf(part[r], sa * sb[j][r >> 2][r & 3], acc[i][j][r]);
-            } else {
-                const float s = sa * sb[j][0][0];
-#pragma unroll
-                for (int r = 0; r < 16; ++r) acc[i][j][r] = fmaf(part[r], s, acc[i][j][r]);
-            }
-        };
-        // WHOLE: all of this wave's subtiles hold rows of C (the usual case, without branches
-        // between its instructions)
-        auto block = [&](auto whole_tag) {
-            constexpr bool WHOLE = decltype(whole_tag)::value;
-            i32x8 bf[SJ][2];
-#pragma unroll
-            for (int j = 0; j < SJ; ++j)
-#pragma unroll
-                for (int h = 0; h < 2; ++h) bf[j][h] = b_frag(st, j, h);
-#pragma unroll
-            for (int i = 0; i < SM; ++i) {
-                if (WHOLE || i < subs) {
-                    const i32x8 af0 = a_frag(st, i, 0), af1 = a_frag(st, i, 1);
-#pragma unroll
-                    for (int j = 0; j < SJ; ++j)
-                        add(i, j, mfma_32<TB, TA>(bf[j][1], af1, mfma_32<TB, TA>(bf[j][0], af0, f32x16{0})));
-                }
-            }
-        };
-        if (subs == SM) block(std::true_type{});
-        else if (subs > 0) block(std::false_type{});
-        if (kb + 1 < t.nkb) settle(kb + 1);
-    }
-
-    // ---- C: a lane's accumulators are row l32 and four-column runs 8q + 4lh; through LDS, 32
-    // rows at a time, each store instruction then writes whole rows of the wave's columns
-    __builtin_amdgcn_s_barrier();  // every wave has read its last fragments
-    asm volatile("" ::: "memory");
-    float* const stage = reinterpret_cast<float*>(lds) + wave * (32 * ROW);
-    constexpr int LANES = SJ * 8;  // lanes to a row
-    const int n = t.n0 + wn * SJ * 32 + (lane % LANES) * 4;
-    const bool whole = t.n0 + BN <= g.N;
-#pragma unroll
-    for (int i = 0; i < SM; ++i) {
-        if (i >= subs) continue;
-        const int first = t.m0 + (wm * SM + i) * 32;
-        const uint64_t live = live_rows(g, t, first);
-#pragma unroll
-        for (int j = 0; j < SJ; ++j)
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                f32x4 v = {acc[i][j][q * 4], acc[i][j][q * 4 + 1], acc[i][j][q * 4 + 2], acc[i][j][q * 4 + 3]};
-                if (t.bad) v = f32x4{1, 1, 1, 1} * __builtin_nanf("");
-                *reinterpret_cast<f32x4*>(stage + l32 * ROW + j * 32 + q * 8 + lh * 4) = v;
+                *reinterpret_cast<f32x4*>(stage + r32 * ROW + j * 32 + q * 8 + rh * 4) = v;
             }
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
         auto rows_out = [&](auto put) {
 #pragma unroll
-            for (int p = 0; p < 32 * LANES / 64; ++p) {
-                const int row = p * (64 / LANES) + lane / LANES, m = first + row;
-                f32x4 v = *reinterpret_cast<const f32x4*>(stage + row * ROW + (lane % LANES) * 4);
+            for (int p = 0; p < 8; ++p) {
+                const int row = p * 4 + rg, m = first + row;
+                f32x4 v = *reinterpret_cast<const f32x4*>(stage + row * ROW + r16 * 4);
                 if (!((live >> row) & 1)) v = f32x4{0, 0, 0, 0};
                 if (m < t.m_end && n < g.N) put((size_t)m * (size_t)g.ldc + n, m, v);
             }
         };
-        // by type outside the unrolled rows; the tiles that the last column cuts, element-wise
         if (!whole) rows_out([&](size_t, int m, f32x4 v) { block_store4(g, m, n, v); });
         else if (g.out_dt == DT_F32)
-            rows_out([&](size_t at, int, f32x4 v) { store_out4(g.C, DT_F32, at, v); });
-        else if (g.out_dt == DT_F16) rows_out([&](size_t at, int, f32x4 v) { store_out4(g.C, DT_F16, at, v); });
-        else rows_out([&](size_t at, int, f32x4 v) { store_out4(g.C, DT_BF16, at, v); });
+            // a weight's gradient is far larger than the codes, which other tiles read again:
+            // past the caches (64 experts, 512 rows each, 2048 x 1024: 273 against 279 us)
+            rows_out([&](size_t c, int, f32x4 v) { store_passing(static_cast<float*>(g.C) + c, v); });
+        else rows_out([&](size_t c, int, f32x4 v) { store_out4(g.C, g.out_dt, c, v); });
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     }
 }
@@ -1388,7 +877,7 @@ __global__ __launch_bounds__(WM* WN * 64) void block_tile(BlockArgs g) {
 // bytes in flight behind one search for its expert and one reading of A (16 tokens x 4 of 64
 // experts of 2048 x 2048: 50 -> 45 us, 3.9 TB/s of their matrices; one token x 4096 x 4096,
 // NT = 1: 6 us).
-template <int TA, int TB, bool FULL, int SM, int NT, bool DIRECT>
+template <int TA, int TB, int SM, int NT, bool DIRECT>
 __global__ __launch_bounds__(512) void block_skinny(BlockArgs g) {
     constexpr int NW = 8, BM = 16 * SM, BN = 16 * NT;
     __shared__ f32x4 sums[NW][SM * NT][64];
@@ -1455,14 +944,10 @@ __global__ __launch_bounds__(512) void block_skinny(BlockArgs g) {
 #pragma unroll
             for (int j = 0; j < NT; ++j) {
                 f32x4 part = {0, 0, 0, 0};
-                if constexpr (FULL) {
 #pragma unroll
-                    for (int u = 0; u < 4; ++u)
-                        part = __builtin_amdgcn_mfma_f32_16x16x32_f16(widen8<TB>(bf[j][2 * u], bf[j][2 * u + 1]),
-                                                                      widen8<TA>(af[2 * u], af[2 * u + 1]), part, 0, 0, 0);
-                } else {
-                    part = mfma_16<TB, TA>(bf[j], af, part);
-                }
+                for (int u = 0; u < 4; ++u)
+                    part = __builtin_amdgcn_mfma_f32_16x16x32_f16(widen8<TB>(bf[j][2 * u], bf[j][2 * u + 1]),
+                                                                  widen8<TA>(af[2 * u], af[2 * u + 1]), part, 0, 0, 0);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) acc[i][j][e] = fmaf(part[e], sa * sb[j][e], acc[i][j][e]);
             }
@@ -1484,61 +969,33 @@ __global__ __launch_bounds__(512) void block_skinny(BlockArgs g) {
     block_store4(g, m, n, v);
 }
 
-// Operands with adjacent rows: one kernel for either kind of scales, each row's its own.
-template <int TA, int TB, int TR>
-int launch_block_tr(const BlockPlan& p, const BlockArgs& a, dim3 grid, hipStream_t s) {
-    return p.direct ? launch_status(block_tile<TA, TB, true, 128, 128, 2, 2, true, TR>, grid, dim3(256), s, a)
-                    : launch_status(block_tile<TA, TB, true, 128, 128, 2, 2, false, TR>, grid, dim3(256), s, a);
-}
-
-template <int TA, int TB, bool FULL>
-int launch_block_full(const BlockPlan& p, const BlockArgs& a, dim3 grid, hipStream_t s) {
-    const bool brow = a.b_shift == 0;
-    if constexpr (FULL) {
-        if (p.tr == 1 && p.kernel == BLOCK_TILE256)
-            return launch_status(block_full_direct<TA, TB, true, 4, 3, true>, grid, dim3(512), s, a);
-        if (p.tr == 1) return launch_status(block_full<TA, TB, true, 1>, grid, dim3(256), s, a);
-        if (p.tr == 2) return launch_status(block_full<TA, TB, true, 2>, grid, dim3(256), s, a);
-        if (p.tr == 3) return launch_status(block_full<TA, TB, true, 3>, grid, dim3(256), s, a);
-        if (p.kernel == BLOCK_TILE128 && p.direct && p.small)
-            return brow ? launch_status(block_full_direct<TA, TB, true, 2, 2>, grid, dim3(256), s, a)
-                        : launch_status(block_full_direct<TA, TB, false, 2, 2>, grid, dim3(256), s, a);
-        if (p.kernel == BLOCK_TILE256)
-            return brow ? launch_status(block_full_direct<TA, TB, true, 4, 3>, grid, dim3(512), s, a)
-                        : launch_status(block_full_direct<TA, TB, false, 4, 3>, grid, dim3(512), s, a);
-        if (p.kernel == BLOCK_TILE128)
-            return brow ? launch_status(block_full<TA, TB, true, 0>, grid, dim3(256), s, a)
-                        : launch_status(block_full<TA, TB, false, 0>, grid, dim3(256), s, a);
-    } else {
-        if (p.tr == 1) return launch_block_tr<TA, TB, 1>(p, a, grid, s);
-        if (p.tr == 2) return launch_block_tr<TA, TB, 2>(p, a, grid, s);
-        if (p.tr == 3) return launch_block_tr<TA, TB, 3>(p, a, grid, s);
-        if (p.kernel == BLOCK_TILE256)
-            return brow ? launch_status(block_wide<TA, TB, true>, grid, dim3(512), s, a)
-                        : launch_status(block_wide<TA, TB, false>, grid, dim3(512), s, a);
-        if (p.kernel == BLOCK_TILE128) {
-            if (p.direct)
-                return brow ? launch_status(block_tile<TA, TB, true, 128, 128, 2, 2, true>, grid, dim3(256), s, a)
-                            : launch_status(block_tile<TA, TB, false, 128, 128, 2, 2, true>, grid, dim3(256), s, a);
-            return brow ? launch_status(block_tile<TA, TB, true, 128, 128, 2, 2, false>, grid, dim3(256), s, a)
-                        : launch_status(block_tile<TA, TB, false, 128, 128, 2, 2, false>, grid, dim3(256), s, a);
-        }
-    }
-    if (p.direct) {
-        if (p.bn == 64) return launch_status(block_skinny<TA, TB, FULL, 1, 4, true>, grid, dim3(512), s, a);
-        return p.bm == 16   ? launch_status(block_skinny<TA, TB, FULL, 1, 1, true>, grid, dim3(512), s, a)
-               : p.bm == 32 ? launch_status(block_skinny<TA, TB, FULL, 2, 1, true>, grid, dim3(512), s, a)
-                            : launch_status(block_skinny<TA, TB, FULL, 4, 1, true>, grid, dim3(512), s, a);
-    }
-    return p.bm == 16   ? launch_status(block_skinny<TA, TB, FULL, 1, 1, false>, grid, dim3(512), s, a)
-           : p.bm == 32 ? launch_status(block_skinny<TA, TB, FULL, 2, 1, false>, grid, dim3(512), s, a)
-                        : launch_status(block_skinny<TA, TB, FULL, 4, 1, false>, grid, dim3(512), s, a);
-}
-
 template <int TA, int TB>
 int launch_block(const BlockPlan& p, const BlockArgs& a, dim3 grid, hipStream_t s) {
-    return a.out_dt == DT_F32 ? launch_block_full<TA, TB, true>(p, a, grid, s)
-                              : launch_block_full<TA, TB, false>(p, a, grid, s);
+    const bool brow = a.b_shift == 0;
+    // operands with adjacent rows: one kernel for either kind of scales, each row's its own
+    if (p.tr == 1 && p.kernel == BLOCK_TILE256)
+        return launch_status(block_direct<TA, TB, true, 4, 3, true>, grid, dim3(512), s, a);
+    if (p.tr == 1) return launch_status(block_staged<TA, TB, true, 1>, grid, dim3(256), s, a);
+    if (p.tr == 2) return launch_status(block_staged<TA, TB, true, 2>, grid, dim3(256), s, a);
+    if (p.tr == 3) return launch_status(block_staged<TA, TB, true, 3>, grid, dim3(256), s, a);
+    if (p.kernel == BLOCK_TILE256)
+        return brow ? launch_status(block_direct<TA, TB, true, 4, 3>, grid, dim3(512), s, a)
+                    : launch_status(block_direct<TA, TB, false, 4, 3>, grid, dim3(512), s, a);
+    if (p.kernel == BLOCK_TILE128 && p.direct && p.small)
+        return brow ? launch_status(block_direct<TA, TB, true, 2, 2>, grid, dim3(256), s, a)
+                    : launch_status(block_direct<TA, TB, false, 2, 2>, grid, dim3(256), s, a);
+    if (p.kernel == BLOCK_TILE128)
+        return brow ? launch_status(block_staged<TA, TB, true, 0>, grid, dim3(256), s, a)
+                    : launch_status(block_staged<TA, TB, false, 0>, grid, dim3(256), s, a);
+    if (p.direct) {
+        if (p.bn == 64) return launch_status(block_skinny<TA, TB, 1, 4, true>, grid, dim3(512), s, a);
+        return p.bm == 16   ? launch_status(block_skinny<TA, TB, 1, 1, true>, grid, dim3(512), s, a)
+               : p.bm == 32 ? launch_status(block_skinny<TA, TB, 2, 1, true>, grid, dim3(512), s, a)
+                            : launch_status(block_skinny<TA, TB, 4, 1, true>, grid, dim3(512), s, a);
+    }
+    return p.bm == 16   ? launch_status(block_skinny<TA, TB, 1, 1, false>, grid, dim3(512), s, a)
+           : p.bm == 32 ? launch_status(block_skinny<TA, TB, 2, 1, false>, grid, dim3(512), s, a)
+                        : launch_status(block_skinny<TA, TB, 4, 1, false>, grid, dim3(512), s, a);
 }
 
 }  // namespace dg

@@ -81,13 +81,10 @@ int gemm_block_quantize(const void* X, int64_t x_rows, int64_t cols, int64_t ldx
 /*
  * gemm_block_product -- C[i][j] = sum_k A(i,k) B(j,k) for block-scaled A (M x K) and
  * B (N x K, i.e. column-major as gemm_ex's GEMM_OP_T), any pair of types and block_rows.
- * Each block's sum over 128 k is multiplied by both scales and added in fp32. Within a
- * block, products of codes are exact; for fp32 C they are summed in fp32. For C of 16 bits
- * the 8-bit matrix cores sum them, which cut the products of each 8 neighbouring k to
- * multiples of 2^-13 of the group's largest (groups are added in fp32): at most 7 * 2^-13
- * of each group's largest product, far below C's own rounding. The experts' products below
- * do the same. C is stored in out_dtype (GEMM_F32, GEMM_F16 or GEMM_BF16, round to nearest
- * even), leading dimension ldc.
+ * Products of codes are exact, their sum over a block of 128 k is in fp32, and each block's
+ * sum is multiplied by both scales and added in fp32, whatever C's type; the experts'
+ * products below do the same. C is stored in out_dtype (GEMM_F32, GEMM_F16 or GEMM_BF16,
+ * round to nearest even), leading dimension ldc.
  * K == 0 writes zeros. With a workspace (16-byte aligned; gemm_block_product_workspace
  * tells the bytes that help, 0 when none do) K may be split over workgroups, the parts
  * added in a fixed order; without one (NULL, 0) it is not split.
