@@ -25,6 +25,7 @@
 
 #include "device_common.h"
 #include "experts.h"
+#include "extents.h"
 #include "lds_layout.h"
 
 #define DG_LDS_ADDR(a) ((__attribute__((address_space(3))) void*)(uintptr_t)(uint32_t)(a))
@@ -99,7 +100,7 @@ __device__ __forceinline__ bool expert_tile(const BlockArgs& g, BlockTile& t) {
     for (int e0 = 0; e0 < g.E; e0 += 64) {
         int lo = 0, hi = 0;
         if (e0 + lane < g.E) expert_range(g.offsets, e0 + lane, g.M, lo, hi);
-        int n = (hi - lo + BM - 1) / BM;
+        int n = pieces<BM>(hi - lo);
 #pragma unroll
         for (int d = 32; d; d >>= 1) n += __shfl_xor(n, d);
         total += n;
@@ -112,7 +113,7 @@ __device__ __forceinline__ bool expert_tile(const BlockArgs& g, BlockTile& t) {
     for (int e0 = 0; e0 < g.E; e0 += 64) {
         int lo = 0, hi = 0;
         if (e0 + lane < g.E) expert_range(g.offsets, e0 + lane, g.M, lo, hi);
-        const int n = (hi - lo + BM - 1) / BM;
+        const int n = pieces<BM>(hi - lo);
         int sum = n;
 #pragma unroll
         for (int d = 1; d < 64; d <<= 1) {
@@ -163,7 +164,7 @@ __device__ __forceinline__ bool block_tile_of(BlockArgs& g, BlockTile& t) {
     t.bad = false;
     t.expert = 0;
     t.kb0 = 0;
-    t.nkb = (g.K + kBlock - 1) / kBlock;
+    t.nkb = pieces<kBlock>(g.K);
     t.krem = g.K - (t.nkb - 1) * kBlock;
     t.m_end = g.M;
     t.m_live = g.M;
@@ -210,7 +211,7 @@ __device__ __forceinline__ bool block_tile_of(BlockArgs& g, BlockTile& t) {
         hi = __builtin_amdgcn_readfirstlane(hi);
         t.bad = ((lo & (kBlock - 1)) != 0 || (hi & 15) != 0) && hi > lo;  // chunks are 16 bytes
         t.kb0 = lo / kBlock;
-        t.nkb = t.bad ? 0 : (hi - lo + kBlock - 1) / kBlock;
+        t.nkb = t.bad ? 0 : pieces<kBlock>(hi - lo);
         t.krem = hi - lo - (t.nkb - 1) * kBlock;
         g.C = static_cast<char*>(g.C) + (size_t)t.expert * (size_t)g.stride_c * (g.out_dt == DT_F32 ? 4 : 2);
     } else {
