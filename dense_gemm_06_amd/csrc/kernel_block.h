@@ -262,8 +262,9 @@ __device__ __forceinline__ uint64_t live_rows(const BlockArgs& g, const BlockTil
 // Zeros in the rows past the last expert's, spread over the whole grid.
 __device__ __forceinline__ void clear_tail(const BlockArgs& g) {
     const int first = min(max(g.offsets[g.E], 0), g.M);
-    for (int m = first + (int)blockIdx.x; m < g.M; m += (int)gridDim.x)
-        for (int n = (int)threadIdx.x * 4; n < g.N; n += (int)blockDim.x * 4) block_store4(g, m, n, f32x4{0, 0, 0, 0});
+    stride_walk((int64_t)first + blockIdx.x, g.M, gridDim.x, [&](int m) {
+        stride_walk(threadIdx.x * 4, g.N, blockDim.x * 4, [&](int n) { block_store4(g, m, n, f32x4{0, 0, 0, 0}); });
+    });
 }
 
 // 16 bytes of a row from p, of which the first `valid` lie inside it.

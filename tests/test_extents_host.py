@@ -30,3 +30,13 @@ def source(name):
 def test_products_count_through_extents():
     """`(size + 127) / 128` wraps near 2^31, pieces<128>(size) does not."""
     assert not re.findall(r"\((?:g\.[MNK]|hi - lo) \+ \w+ - 1\) / ", source("kernel_block.h"))
+
+
+# kernels whose loops over sizes go by steps of the grid or the workgroup
+WALKS = ["kernel_block.h"]
+
+
+@pytest.mark.parametrize("name", WALKS)
+def test_kernels_walk_through_extents(name):
+    """A 32-bit counter wraps past an end within one step of 2^31 and reads or writes out of range."""
+    assert not re.findall(r"for \(int \w+ = [^;]*;[^;]*;\s*\w+ \+= [^)]*(?:gridDim|blockDim|workers|\d{2,})", source(name))
