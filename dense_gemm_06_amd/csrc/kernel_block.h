@@ -97,9 +97,9 @@ template <int BM>
 __device__ __forceinline__ bool expert_tile(const BlockArgs& g, BlockTile& t) {
     const int lane = threadIdx.x & 63;
     int total = 0;
-    for (int e0 = 0; e0 < g.E; e0 += 64) {
+    for (int64_t e0 = 0; e0 < g.E; e0 += 64) {
         int lo = 0, hi = 0;
-        if (e0 + lane < g.E) expert_range(g.offsets, e0 + lane, g.M, lo, hi);
+        if (e0 + lane < g.E) expert_range(g.offsets, (int)(e0 + lane), g.M, lo, hi);
         int n = pieces<BM>(hi - lo);
 #pragma unroll
         for (int d = 32; d; d >>= 1) n += __shfl_xor(n, d);
@@ -110,9 +110,9 @@ __device__ __forceinline__ bool expert_tile(const BlockArgs& g, BlockTile& t) {
     if (id < 0) return false;
     const int q = id / g.tiles_n;  // lies in the tiles of the wanted expert, as all of its row tiles have tiles_n columns
     int before = 0;
-    for (int e0 = 0; e0 < g.E; e0 += 64) {
+    for (int64_t e0 = 0; e0 < g.E; e0 += 64) {
         int lo = 0, hi = 0;
-        if (e0 + lane < g.E) expert_range(g.offsets, e0 + lane, g.M, lo, hi);
+        if (e0 + lane < g.E) expert_range(g.offsets, (int)(e0 + lane), g.M, lo, hi);
         const int n = pieces<BM>(hi - lo);
         int sum = n;
 #pragma unroll
@@ -127,7 +127,7 @@ __device__ __forceinline__ bool expert_tile(const BlockArgs& g, BlockTile& t) {
             const int tiles = __builtin_amdgcn_readlane(n, l);
             int tm, tn;
             raster(id - first * g.tiles_n, tiles, g.tiles_n, min(g.group_m, tiles), tm, tn);
-            t.expert = e0 + l;
+            t.expert = (int)(e0 + l);
             const int base = __builtin_amdgcn_readlane(lo, l);
             t.m0 = base + tm * BM;
             t.m_end = __builtin_amdgcn_readlane(hi, l);
