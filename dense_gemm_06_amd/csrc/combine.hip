@@ -11,6 +11,7 @@
 
 #include "device_common.h"
 #include "experts.h"
+#include "extents.h"
 #include "launch.h"
 
 namespace dg {
@@ -89,12 +90,12 @@ __device__ __forceinline__ Slots slots_of(const CombineArgs& a, int t, int j0) {
 template <int DT>
 __global__ __launch_bounds__(256) void combine(CombineArgs a) {
     typedef typename Elem<DT>::type T;
-    for (int t = blockIdx.x; t < a.tokens; t += gridDim.x) {
+    stride_walk(blockIdx.x, a.tokens, gridDim.x, [&](int t) {
         auto piece = [&](int c, auto whole_tag) {
             const int left = decltype(whole_tag)::value ? 8 : a.cols - c;
             float sum[8] = {0, 0, 0, 0, 0, 0, 0, 0};
             if (a.capacity > 0)
-                for (int j0 = 0; j0 < a.top_k; j0 += kSlots) {
+                stride_walk(0, a.top_k, kSlots, [&](int j0) {
                     const Slots s = slots_of(a, t, j0);
                     T raw[kSlots][8];
 #pragma unroll
@@ -104,14 +105,14 @@ __global__ __launch_bounds__(256) void combine(CombineArgs a) {
                     for (int v = 0; v < kSlots; ++v)
 #pragma unroll
                         for (int e = 0; e < 8; ++e) sum[e] = s.in[v] ? fmaf(s.w[v], decode<DT>(raw[v][e]), sum[e]) : sum[e];
-                }
+                });
             store8<DT>(static_cast<T*>(a.out) + (size_t)t * (size_t)a.ldo + c, sum, left);
         };
         // whole passes without a branch at each load
         int c0 = 0;
-        for (; c0 + 2048 <= a.cols; c0 += 2048) piece(c0 + (int)threadIdx.x * 8, std::true_type{});
-        if (c0 + (int)threadIdx.x * 8 < a.cols) piece(c0 + (int)threadIdx.x * 8, std::false_type{});
-    }
+        for (; a.cols - c0 >= 2048; c0 += 2048) piece(c0 + (int)threadIdx.x * 8, std::true_type{});
+        if ((int)threadIdx.x * 8 < a.cols - c0) piece(c0 + (int)threadIdx.x * 8, std::false_type{});
+    });
 }
 
 // The first `workers` workgroups take a token each in turn, the others clear the padding
@@ -132,12 +133,12 @@ __global__ __launch_bounds__(256) void combine_backward(CombineArgs a, int worke
             const int r = p < a.capacity ? a.rows[p] : 0;
             for (uint64_t pad = __ballot(p < a.capacity && (r < 0 || r >= a.tokens)) & 0xf; pad; pad &= pad - 1) {
                 T* const row = yg + (size_t)(p0 + __builtin_ctzll(pad)) * (size_t)a.ldyg;
-                for (int c = tid * 8; c < a.cols; c += 2048) store8<DT, true>(row + c, zero, a.cols - c);
+                stride_walk(tid * 8, a.cols, 2048, [&](int c) { store8<DT, true>(row + c, zero, a.cols - c); });
             }
         }
         return;
     }
-    for (int t = blockIdx.x; t < a.tokens; t += workers) {
+    stride_walk(blockIdx.x, a.tokens, workers, [&](int t) {
         const T* g = static_cast<const T*>(a.G) + (size_t)t * (size_t)a.ldg;
         for (int j0 = 0; j0 < a.top_k; j0 += kSlots) {
             const Slots s = slots_of(a, t, j0);
@@ -164,8 +165,8 @@ __global__ __launch_bounds__(256) void combine_backward(CombineArgs a, int worke
                 }
             };
             int c0 = 0;
-            for (; c0 + 2048 <= a.cols; c0 += 2048) piece(c0 + tid * 8, std::true_type{});
-            if (c0 + tid * 8 < a.cols) piece(c0 + tid * 8, std::false_type{});
+            for (; a.cols - c0 >= 2048; c0 += 2048) piece(c0 + tid * 8, std::true_type{});
+            if (tid * 8 < a.cols - c0) piece(c0 + tid * 8, std::false_type{});
 #pragma unroll
             for (int v = 0; v < kSlots; ++v) {
 #pragma unroll
@@ -178,7 +179,7 @@ __global__ __launch_bounds__(256) void combine_backward(CombineArgs a, int worke
                     (dots[tid][0] + dots[tid][1]) + (dots[tid][2] + dots[tid][3]);
             __syncthreads();
         }
-    }
+    });
 }
 
 int launch_combine(const CombineArgs& a, int dtype, hipStream_t s) {

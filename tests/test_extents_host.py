@@ -32,11 +32,13 @@ def test_products_count_through_extents():
     assert not re.findall(r"\((?:g\.[MNK]|hi - lo) \+ \w+ - 1\) / ", source("kernel_block.h"))
 
 
-# kernels whose loops over sizes go by steps of the grid or the workgroup
-WALKS = ["kernel_block.h"]
+# kernels whose loops over sizes up to 2^31 go by steps of the grid, of the workgroup or of a wave
+WALKS = ["kernel_block.h", "combine.hip"]
 
 
 @pytest.mark.parametrize("name", WALKS)
 def test_kernels_walk_through_extents(name):
     """A 32-bit counter wraps past an end within one step of 2^31 and reads or writes out of range."""
-    assert not re.findall(r"for \(int \w+ = [^;]*;[^;]*;\s*\w+ \+= [^)]*(?:gridDim|blockDim|workers|\d{2,})", source(name))
+    size = r"(?:a\.(?:tokens|cols|capacity|n)|g\.[MNKE])\b|start\["
+    assert not re.findall(r"for \(int \w+ = [^;]*;[^;]*(?:%s)[^;]*; \w+ \+=" % size, source(name))
+    assert not re.findall(r"\w+ \+ \d{2,} <= (?:%s)" % size, source(name))  # `at + 2048 <= size` wraps too

@@ -20,3 +20,19 @@ def test_product_of_the_longest_rows():
     a = dg.BlockTensor(one.view(E4), scale, 1)
     for out in (F32, BF16):
         assert dg.gemm_block_product_tensors(a, a, out).item() == len(at)
+
+
+def test_combine_of_the_longest_rows():
+    """2^31 - 1 columns: the last whole pass of a workgroup ends within one pass of 2^31."""
+    N = 2 ** 31 - 1
+    i32 = lambda *x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    plan = dg.ExpertPlan(i32(0, 1), i32(1), i32(0), i32(0).reshape(1, 1))
+    at = [0, 2047, 2048, 2 ** 30, N - 2048, N - 2047, N - 1]
+    y = torch.zeros(1, N, dtype=BF16, device="cuda")
+    y[0, at] = 3.0
+    weight = torch.full((1, 1), 0.5, device="cuda")
+    out = dg.gemm_experts_combine_tensors(y, plan, weight)
+    assert out[0, at].tolist() == [1.5] * len(at) and int(torch.count_nonzero(out[0])) == len(at)
+    y_grad, weight_grad = dg.gemm_experts_combine_backward_tensors(y, plan, weight, out)
+    assert y_grad[0, at].tolist() == [0.75] * len(at) and int(torch.count_nonzero(y_grad[0])) == len(at)
+    assert weight_grad.item() == 4.5 * len(at)
