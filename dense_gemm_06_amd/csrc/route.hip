@@ -11,6 +11,7 @@
 
 #include "device_common.h"
 #include "experts.h"
+#include "extents.h"
 #include "launch.h"
 
 namespace dg {
@@ -436,8 +437,7 @@ __global__ __launch_bounds__(256) void route_backward(RouteArgs a) {
 // Lanes to a token and experts to a lane: 16 lanes up to 256 experts, 64 above.
 template <int W, int R, int DT>
 int launch_route_as(RouteArgs a, bool backward, hipStream_t s) {
-    const int tokens = 4 * (64 / W);
-    const dim3 grid((unsigned)std::min((a.tokens + tokens - 1) / tokens, 1 << 20)), block(256);
+    const dim3 grid((unsigned)std::min(pieces<4 * (64 / W)>(a.tokens), 1 << 20)), block(256);
     if (backward) return launch_status(route_backward<W, R, DT>, grid, block, s, a);
     // groups that are 1, 2, 4 or 8 whole lanes (of a token's 16)
     const int per = a.experts / a.groups, lanes = per / R;
@@ -579,9 +579,9 @@ __global__ __launch_bounds__(1024) void dispatch_place(DispatchArgs a) {
     // padding: an expert's by one wave
     const int waves = (int)gridDim.x * kDispatchWaves;
     for (int e = (int)blockIdx.x * kDispatchWaves + wave; e < E; e += waves)
-        for (int p = start[e] + count[e] + lane; p < start[e + 1]; p += 64) a.rows[p] = -1;
-    for (int64_t p = (int64_t)start[E] + (int64_t)blockIdx.x * 1024 + tid; p < a.capacity; p += (int64_t)gridDim.x * 1024)
-        a.rows[p] = -1;
+        stride_walk((int64_t)start[e] + count[e] + lane, start[e + 1], 64, [&](int p) { a.rows[p] = -1; });
+    stride_walk((int64_t)start[E] + (int64_t)blockIdx.x * 1024 + tid, a.capacity, (int64_t)gridDim.x * 1024,
+                [&](int p) { a.rows[p] = -1; });
     if (blockIdx.x == 0) {
         for (int e = tid; e <= E; e += 1024) a.offsets[e] = start[e];
         for (int e = tid; e < E; e += 1024) a.counts[e] = count[e];

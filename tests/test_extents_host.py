@@ -30,10 +30,11 @@ def source(name):
 def test_products_count_through_extents():
     """`(size + 127) / 128` wraps near 2^31, pieces<128>(size) does not."""
     assert not re.findall(r"\((?:g\.[MNK]|hi - lo) \+ \w+ - 1\) / ", source("kernel_block.h"))
+    assert not re.findall(r"\(a\.tokens \+ \w+ - 1\) / ", source("route.hip"))
 
 
 # kernels whose loops over sizes up to 2^31 go by steps of the grid, of the workgroup or of a wave
-WALKS = ["kernel_block.h", "combine.hip"]
+WALKS = ["kernel_block.h", "combine.hip", "route.hip"]
 
 
 @pytest.mark.parametrize("name", WALKS)
