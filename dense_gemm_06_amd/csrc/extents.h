@@ -19,6 +19,12 @@ DG_HD int pieces(int n) {
     return n / of + (n % of != 0 ? 1 : 0);
 }
 
+// a + b or, where that is more, cap.
+DG_HD int capped_sum(int a, int b, int cap) {
+    const int64_t sum = (int64_t)a + b;
+    return sum < cap ? (int)sum : cap;
+}
+
 // Calls f(at) for at = first, first + step, .. below end: a 32-bit counter would wrap past an
 // end within one step of 2^31.
 template <typename F>

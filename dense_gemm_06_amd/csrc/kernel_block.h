@@ -103,7 +103,7 @@ __device__ __forceinline__ bool expert_tile(const BlockArgs& g, BlockTile& t) {
         int n = pieces<BM>(hi - lo);
 #pragma unroll
         for (int d = 32; d; d >>= 1) n += __shfl_xor(n, d);
-        total += n;
+        total = capped_sum(total, n, g.tiles_m);  // a plan's never pass tiles_m, overlapping offsets may
     }
     total = __builtin_amdgcn_readfirstlane(total);
     const int id = xcd_tile(total * g.tiles_n);

@@ -46,6 +46,12 @@ int main() {
     for (int64_t end : {kTop, kTop - 1, kTop - 63, kTop - 2047, kTop - (1 << 20), (int64_t)5, (int64_t)0})
         for (int64_t step : {(int64_t)2048, (int64_t)1 << 20, ((int64_t)1 << 24) - 7})
             for (int64_t first : {(int64_t)0, (int64_t)1, step - 1, kTop - 3 * step, kTop - 1, kTop}) walk_at(first, end, step);
+    // 2^20 experts whose offsets alternate between the first row and the last of 2^20, 64 at a time
+    const int tiles = (1 << 20) / 128 + (1 << 20);
+    int total = 0;
+    for (int e = 0; e < 1 << 20; e += 64) total = dg::capped_sum(total, 32 * ((1 << 20) / 128), tiles);
+    CHECK(total == tiles, "capped sum %d, not %d\n", total, tiles);
+    CHECK(dg::capped_sum(5, 6, 12) == 11 && dg::capped_sum(5, 8, 12) == 12, "capped sum\n");
     printf("%d failures\n", fails);
     return fails != 0;
 }

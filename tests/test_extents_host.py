@@ -33,6 +33,11 @@ def test_products_count_through_extents():
     assert not re.findall(r"\(a\.tokens \+ \w+ - 1\) / ", source("route.hip"))
 
 
+def test_experts_tiles_are_capped():
+    """Offsets that do not grow make ranges overlap, and their tiles' sum pass 2^31."""
+    assert not re.findall(r"total \+= ", source("kernel_block.h"))
+
+
 # kernels whose loops over sizes up to 2^31 go by steps of the grid, of the workgroup or of a wave
 WALKS = ["kernel_block.h", "combine.hip", "route.hip"]
 

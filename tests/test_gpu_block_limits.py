@@ -36,3 +36,27 @@ def test_combine_of_the_longest_rows():
     y_grad, weight_grad = dg.gemm_experts_combine_backward_tensors(y, plan, weight, out)
     assert y_grad[0, at].tolist() == [0.75] * len(at) and int(torch.count_nonzero(y_grad[0])) == len(at)
     assert weight_grad.item() == 4.5 * len(at)
+
+
+@pytest.mark.parametrize("T,N", [(8, 64), (300, 200)])
+def test_offsets_that_overlap_stay_inside(T, N):
+    """A plan whose offsets go back and forth: whatever comes out, nothing beside C is written."""
+    P, E = 2 * T, 40
+    g = torch.Generator().manual_seed(T)
+    offsets = torch.tensor([0, P] * (E // 2) + [P], dtype=torch.int32)
+    offsets[5], offsets[7], offsets[9] = -3, 2 ** 31 - 1, -2 ** 31
+    rows = torch.randint(-2, T + 2, (P,), generator=g).to(torch.int32)
+    counts = torch.full((E,), P + 9, dtype=torch.int32)
+    plan = dg.ExpertPlan(offsets.cuda(), counts.cuda(), rows.cuda(), torch.zeros(T, 2, dtype=torch.int32, device="cuda"))
+    one = lambda *s: torch.full(s, 0x38, dtype=torch.uint8, device="cuda").view(E4)  # noqa: E731
+    a = dg.BlockTensor(one(T, 128), torch.ones(T, 1, device="cuda"), 1)
+    b = dg.BlockTensor(one(E, N, 128), torch.ones(E, 2 if N > 128 else 1, 1, device="cuda"), 128)
+    for out in (F32, BF16):
+        wide = torch.full((P + 512, N + 64), 7.0, dtype=out, device="cuda")
+        A, B, p = dg.experts._block(a, "a"), dg.experts._block(b, "b", 3), dg.experts._plan(plan)
+        dg.experts._call("gemm_experts_product", 0, A, B, p, 1, wide[256].data_ptr(), N + 64, dg.experts._WIDE[out])
+        c = wide[256:256 + P, :N]
+        live = torch.tensor([0 <= r < T for r in rows.tolist()])
+        assert set(c[live.cuda()].unique().tolist()) <= {0.0, 128.0} and (c[~live.cuda()] == 0).all()
+        wide[256:256 + P, :N] = 7.0
+        assert (wide == 7.0).all()
