@@ -124,7 +124,6 @@ __device__ __forceinline__ double order_key(double x) {
     const double top = 1.7976931348623157e308;
     return x != x ? __builtin_inf() : __builtin_fmin(__builtin_fmax(x, -top), top);
 }
-constexpr double kMasked = -1.7976931348623157e308;  // the key of -infinity
 
 // The largest of each W lanes' keys, and where: the lane within the W and the register.
 // Ties go to the lowest lane, then the lowest register.
@@ -187,8 +186,9 @@ __device__ __forceinline__ void token_scores(const RouteArgs& a, const ExpTerms&
 // 64 / W tokens to a wave, four waves to a workgroup. The scores wait in LDS; the picks
 // go by the choice values rounded to fp32 (16 registers, one instruction a comparison, where
 // fp64 takes three times as many): rounding keeps their order but for ties, and where any
-// token's largest is not alone the wave decides by the fp64 values. -inf stands for what the
-// groups mask, NaN (which max and == pass over) for what is picked or does not exist.
+// token's largest is not alone the wave decides by the fp64 values. NaN (which max and == pass
+// over) stands for what is picked, masked by the groups or does not exist: -inf would tie with
+// an expert that a bias of -inf excludes.
 // ANY_GROUPS: groups that cut lanes, or more than the two largest of a group (a kernel of its
 // own, for the others' registers).
 // 16384 tokens x 256 experts, sigmoid, 8 groups: 100 us with a wave to a token and fp64
@@ -251,7 +251,7 @@ __global__ __launch_bounds__(256) void route(RouteArgs a) {
                 }
 #pragma unroll
                 for (int j = 0; j < R; ++j)
-                    if (!in && j < left) key[j] = -__builtin_inff();
+                    if (!in) key[j] = __builtin_nanf("");
             } else {
                 // any group: lane l sums the largest values of groups l*R .. l*R + R-1
                 uint8_t* keep = &kept[wave][sub * W * R];
@@ -296,7 +296,7 @@ __global__ __launch_bounds__(256) void route(RouteArgs a) {
                 __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
 #pragma unroll
                 for (int j = 0; j < R; ++j)
-                    if (j < left && !keep[(l * R + j) / per]) key[j] = -__builtin_inff();
+                    if (j < left && !keep[(l * R + j) / per]) key[j] = __builtin_nanf("");
             }
         }
         // picks in descending order; lane i of the token keeps pick i (and W + i)
@@ -322,8 +322,7 @@ __global__ __launch_bounds__(256) void route(RouteArgs a) {
                 for (int j = 0; j < R; ++j) {
                     const int e = l * R + j;
                     full[j] = kAbsent;
-                    if (key[j] == best)
-                        full[j] = key[j] == -__builtin_inff() ? kMasked : order_key(mine[e] + (double)bias[j]);
+                    if (key[j] == best) full[j] = order_key(mine[e] + (double)bias[j]);
                     if ((j & 3) == 3) __builtin_amdgcn_sched_barrier(0);
                 }
                 lanes_argmax<W, R>(full, lane, at, reg);
