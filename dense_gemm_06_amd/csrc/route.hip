@@ -125,6 +125,14 @@ __device__ __forceinline__ double order_key(double x) {
     return x != x ? __builtin_inf() : __builtin_fmin(__builtin_fmax(x, -top), top);
 }
 
+// The key of a group: the sum of its largest values' keys, `top` the largest of them and `low`
+// the smallest. NaN where top is one, or where infinities of both signs meet.
+__device__ __forceinline__ double group_key(double sum, double top, double low) {
+    const double most = 1.7976931348623157e308;  // infinity's key
+    const bool nan = top == __builtin_inf() || (top == most && low == -most);
+    return nan ? __builtin_inf() : order_key(sum);
+}
+
 // The largest of each W lanes' keys, and where: the lane within the W and the register.
 // Ties go to the lowest lane, then the lowest register.
 template <int W, int R>
@@ -239,7 +247,7 @@ __global__ __launch_bounds__(256) void route(RouteArgs a) {
                 if (a.group_lanes > 1) merge(lane_swap<1>(v0), lane_swap<1>(v1));
                 if (a.group_lanes > 2) merge(lane_swap<2>(v0), lane_swap<2>(v1));
                 if (a.group_lanes > 4) merge(lane_swap<4>(v0), lane_swap<4>(v1));
-                double best[1] = {left > 0 ? order_key(a.group_top == 2 ? v0 + v1 : v0) : kAbsent};
+                double best[1] = {left > 0 ? group_key(a.group_top == 2 ? v0 + v1 : v0, v0, a.group_top == 2 ? v1 : v0) : kAbsent};
                 bool in = false;
                 for (int i = 0; i < a.top_groups; ++i) {
                     int at, reg;
@@ -272,11 +280,14 @@ __global__ __launch_bounds__(256) void route(RouteArgs a) {
                                 x = lower;
                             }
                         }
-                    double sum = v[0];
+                    double sum = v[0], low = v[0];
 #pragma unroll
                     for (int q = 1; q < 4; ++q)
-                        if (q < a.group_top) sum += v[q];
-                    const double b = grp < a.groups ? order_key(sum) : kAbsent;
+                        if (q < a.group_top) {
+                            sum += v[q];
+                            low = v[q];
+                        }
+                    const double b = grp < a.groups ? group_key(sum, v[0], low) : kAbsent;
 #pragma unroll
                     for (int q = 0; q < R; ++q)
                         if (q == j) best[q] = b;
