@@ -186,7 +186,7 @@ def _block(b, what, dims=2):
     op = 0
     if strides[-1] == 1 and strides[-2] >= K > 0 and R > 1:
         ld = strides[-2]
-    elif strides[-2] == 1 and strides[-1] != 1 and R > 1 and K > 1:
+    elif (strides[-2] == 1 or R == 1) and strides[-1] != 1 and K > 1:
         ld, op = _ld((K, R), (strides[-1], 1), f"{what}.data"), 1
     else:
         ld = _ld(shape, strides, f"{what}.data")
