@@ -82,8 +82,9 @@ int gemm_block_quantize(const void* X, int64_t x_rows, int64_t cols, int64_t ldx
  * gemm_block_product -- C[i][j] = sum_k A(i,k) B(j,k) for block-scaled A (M x K) and
  * B (N x K, i.e. column-major as gemm_ex's GEMM_OP_T), any pair of types and block_rows.
  * Products of codes are exact, their sum over a block of 128 k is in fp32, and each block's
- * sum is multiplied by both scales and added in fp32, whatever C's type; the experts'
- * products below do the same. C is stored in out_dtype (GEMM_F32, GEMM_F16 or GEMM_BF16,
+ * sum is multiplied by A's scale and then by B's and added in fp32, whatever C's type (the
+ * scales' own product may lie outside fp32's normal numbers); the experts' products below do
+ * the same. C is stored in out_dtype (GEMM_F32, GEMM_F16 or GEMM_BF16,
  * round to nearest even), leading dimension ldc.
  * K == 0 writes zeros. With a workspace (16-byte aligned; gemm_block_product_workspace
  * tells the bytes that help, 0 when none do) K may be split over workgroups, the parts
