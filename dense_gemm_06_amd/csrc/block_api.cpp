@@ -15,12 +15,13 @@
 
 namespace {
 
+using dg::block_plan;
+using dg::ceil_div;
 using dg::set_error;
 
 constexpr int64_t kMaxDim = ((int64_t)1 << 31) - 1;
 constexpr int64_t kMaxThreads = ((int64_t)1 << 32) - 1;  // of one launch
 
-int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 int64_t elem_size(int dtype) { return dtype == GEMM_F32 ? 4 : dtype == GEMM_F16 || dtype == GEMM_BF16 ? 2 : 1; }
 bool is_wide(int dtype) { return dtype == GEMM_F32 || dtype == GEMM_F16 || dtype == GEMM_BF16; }
 
@@ -195,43 +196,6 @@ bool small_call(const gemm_block_matrix& A, const gemm_block_matrix& B) {
     return bytes(A) < ((int64_t)1 << 32) && bytes(B) < ((int64_t)1 << 32);
 }
 
-constexpr int64_t kCus = 256;
-
-// rows: rows of C that share a B (for experts the average); n_products: B's in the call;
-// small: byte offsets within an operand fit 32 bits; tr: BlockPlan::tr;
-// may_split: whether K may be split.
-dg::BlockPlan block_plan(int64_t rows, int64_t n_products, int64_t N, int64_t K, bool direct, bool small, int tr,
-                         bool may_split) {
-    dg::BlockPlan p;
-    p.tr = tr;
-    p.small = small;
-    p.direct = direct;
-    p.split = 1;
-    const int64_t nkb = ceil_div(K, dg::kBlock);
-    if (rows <= 64 && tr == 0) {
-        p.kernel = dg::BLOCK_SKINNY;
-        p.bm = rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
-        p.bn = direct && p.bm == 16 && n_products * ceil_div(N, 64) >= 2 * kCus ? 64 : 16;
-        const int64_t wgs = n_products * ceil_div(N, p.bn);
-        if (may_split && wgs < kCus) p.split = (int)std::max<int64_t>(1, std::min<int64_t>(kCus / wgs, nkb / 16));
-    } else {
-        // 256 rows where that leaves most compute units a tile; with few blocks of k two smaller
-        // tiles to a compute unit, one of which computes while the other loads or stores, are
-        // ahead (64 products of 2048 x 1024 over 512: 243 against 275 us)
-        const int64_t big = n_products * ceil_div(rows, 256) * ceil_div(N, 128);
-        const bool large = direct && small && tr <= 1 && big >= kCus * 3 / 4 && K > 1024;
-        p.kernel = large ? dg::BLOCK_TILE256 : dg::BLOCK_TILE128;
-        p.bm = large ? 256 : 128;
-        p.bn = 128;
-        const int64_t wgs = n_products * ceil_div(rows, p.bm) * ceil_div(N, p.bn);
-        if (may_split && wgs < kCus) p.split = (int)std::max<int64_t>(1, std::min<int64_t>(2 * kCus / wgs, nkb / 4));
-    }
-    // whole slices
-    const int64_t chunk = ceil_div(std::max<int64_t>(nkb, 1), p.split);
-    p.split = (int)std::max<int64_t>(1, ceil_div(nkb, chunk));
-    return p;
-}
-
 int64_t split_bytes(int split, int64_t M, int64_t N) { return split <= 1 ? 0 : split * M * ceil_div(N, 4) * 16; }
 
 dg::BlockArgs block_args(const gemm_block_matrix& A, const gemm_block_matrix& B, void* C, int64_t ldc, int out_dtype) {
@@ -263,7 +227,7 @@ dg::BlockArgs block_args(const gemm_block_matrix& A, const gemm_block_matrix& B,
 }
 
 int launch(const dg::BlockPlan& p, dg::BlockArgs& a, int64_t tiles, int type_a, int type_b, hipStream_t s) {
-    const int64_t threads = p.kernel == dg::BLOCK_TILE128 ? 256 : 512;
+    const int64_t threads = p.kernel == dg::BLOCK_DIRECT || p.kernel == dg::BLOCK_STAGED ? 256 : 512;
     if (tiles * threads > kMaxThreads) {
         set_error("the product needs %lld workgroups, more than a launch holds", (long long)tiles);
         return GEMM_ERR_UNSUPPORTED;
@@ -283,8 +247,8 @@ int run_block(const gemm_block_matrix& A, const gemm_block_matrix& B, int64_t M,
     const int64_t N = B.rows, K = A.cols;
     const int tr = tr_of(A, B);
     const bool direct = direct_rows(A, 1) && direct_rows(B, 1), small = small_call(A, B);
-    dg::BlockPlan p = block_plan(M, 1, N, K, direct, small, tr, true);
-    if (split_bytes(p.split, M, N) > workspace_bytes) p = block_plan(M, 1, N, K, direct, small, tr, false);
+    dg::BlockPlan p = block_plan(dg::BLOCK_PLAIN, M, 1, N, K, direct, small, tr, true);
+    if (split_bytes(p.split, M, N) > workspace_bytes) p = block_plan(dg::BLOCK_PLAIN, M, 1, N, K, direct, small, tr, false);
     dg::BlockArgs a = block_args(A, B, C, ldc, out_dtype);
     a.mode = dg::BLOCK_PLAIN;
     a.M = (int)M;
@@ -454,10 +418,11 @@ int64_t gemm_block_product_workspace(int64_t M, int64_t N, int64_t K) {
     if (M <= 0 || N <= 0 || K <= 0 || M > kMaxDim || N > kMaxDim || K > kMaxDim) return 0;
     int64_t bytes = 0;
     // every plan that the call may make, for all rows or for whole tiles of them
-    for (int64_t rows : {M, M - M % 128, M - M % 256})
+    for (int64_t rows : {M, M - M % 128})
         for (bool direct : {false, true})
             for (int tr : {0, 1})
-                if (rows > 0) bytes = std::max(bytes, split_bytes(block_plan(rows, 1, N, K, direct, direct, tr, true).split, rows, N));
+                if (rows > 0)
+                    bytes = std::max(bytes, split_bytes(block_plan(dg::BLOCK_PLAIN, rows, 1, N, K, direct, direct, tr, true).split, rows, N));
     return bytes;
 }
 
@@ -486,13 +451,9 @@ int gemm_block_product(const gemm_block_matrix* A, const gemm_block_matrix* B, v
                          {data_range("A.data", *A), scale_range("A.scale", *A), data_range("B.data", *B),
                           scale_range("B.scale", *B)}));
     DG_TRY(check_device());
-    // A few rows past whole tiles run as a launch of their own, on the kernel for few rows: a
-    // tile of theirs takes a third of a whole one's time, behind all the others (2056 x 4000 x
-    // 8176 to fp32: 217 us in one launch, 186 in two).
-    const int tr = tr_of(*A, *B);
-    const bool direct = direct_rows(*A, 1) && direct_rows(*B, 1), small = small_call(*A, *B);
-    const int64_t bm = block_plan(M, 1, N, K, direct, small, tr, true).bm;
-    const int64_t rest = bm >= 128 && tr == 0 && M > bm && M % bm <= 64 ? M % bm : 0;
+    const bool direct = direct_rows(*A, 1) && direct_rows(*B, 1);
+    const dg::BlockPlan whole = block_plan(dg::BLOCK_PLAIN, M, 1, N, K, direct, small_call(*A, *B), tr_of(*A, *B), true);
+    const int64_t rest = dg::rest_rows(whole, M, N, K);
     DG_TRY(run_block(*A, *B, M - rest, C, ldc, out_dtype, workspace, workspace_bytes, (hipStream_t)stream));
     if (rest == 0) return GEMM_OK;
     gemm_block_matrix last = *A;
@@ -658,7 +619,7 @@ int gemm_experts_product(const gemm_block_matrix* A, const gemm_block_matrix* B,
     DG_TRY(check_device());
     const bool direct = direct_rows(*A, 1) && direct_rows(*B, E), small = small_call(*A, *B);
     const int64_t pairs = plan->tokens * plan->top_k, active = std::max<int64_t>(1, std::min(E, pairs));
-    const dg::BlockPlan p = block_plan(std::max<int64_t>(1, pairs / active), active, N, A->cols, direct,
+    const dg::BlockPlan p = block_plan(dg::BLOCK_EXPERTS, std::max<int64_t>(1, pairs / active), active, N, A->cols, direct,
                                        small, tr_of(*A, *B), false);
     dg::BlockArgs a = block_args(*A, *B, C, ldc, out_dtype);
     a.mode = dg::BLOCK_EXPERTS;
@@ -699,7 +660,8 @@ int gemm_experts_gradient(const gemm_block_matrix* A, const gemm_block_matrix* B
                           scale_range("B.scale", *B), range("plan.offsets", plan->offsets, (uint64_t)(E + 1) * 4)}));
     DG_TRY(check_device());
     const bool direct = direct_rows(*A, 1) && direct_rows(*B, 1), small = small_call(*A, *B);
-    const dg::BlockPlan p = block_plan(M, E, N, ceil_div(plan->capacity, E), direct, small, tr_of(*A, *B), false);
+    const dg::BlockPlan p = block_plan(dg::BLOCK_GRADIENT, M, E, N, ceil_div(plan->capacity, E), direct, small,
+                                       tr_of(*A, *B), false);
     dg::BlockArgs a = block_args(*A, *B, C, ldc, out_dtype);
     a.mode = dg::BLOCK_GRADIENT;
     a.E = (int)E;

@@ -5,15 +5,13 @@
 #include <stdint.h>
 
 #include "../../include/gemm_experts.h"
+#include "block_plan.h"
 
 namespace dg {
 
-constexpr int kBlock = 128;          // elements of k (or of a row) that share a scale
 constexpr int kMaxExperts = 1024;    // routing: 16 experts for each lane of a wave
 constexpr int kMaxTopK = 32;
 constexpr int kDispatchChunk = 4096; // (token, slot) pairs per workgroup of the dispatch
-
-enum BlockMode { BLOCK_PLAIN = 0, BLOCK_EXPERTS = 1, BLOCK_GRADIENT = 2 };
 
 struct BlockArgs {
     const uint8_t* A;
@@ -39,18 +37,6 @@ struct BlockArgs {
     float* work;
     int64_t work_slice;
     int work_ld;
-};
-
-enum BlockKernel { BLOCK_SKINNY = 0, BLOCK_TILE128 = 1, BLOCK_TILE256 = 2 };
-
-// What a call launches: filled by block_plan (host only).
-struct BlockPlan {
-    int kernel;       // BlockKernel
-    int bm, bn;
-    int direct;       // 16-byte aligned rows: copies straight to LDS (tiles), whole 16-byte loads (skinny)
-    int small;        // byte offsets within an operand fit 32 bits
-    int split;        // K slices
-    int tr;           // bit 0: B stored with its rows adjacent, bit 1: A
 };
 
 // Launchers return 0 or the hipError_t of the launch. ta, tb: 0 e4m3, 1 e5m2.

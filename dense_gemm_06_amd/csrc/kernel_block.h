@@ -346,8 +346,9 @@ __device__ __forceinline__ void block_again(const BlockArgs& g, const BlockTile&
 }
 
 // ---------------------------------------------------------------------------- aligned rows
-// (64 WM) x 128 tiles for 16-byte aligned rows on 2 WM waves of 64 x 64, each 4 x 4
-// tiles of v_mfma_f32_16x16x32_f16, four instructions to a block of k. Codes are copied
+// (64 WM) x 128 tiles for 16-byte aligned rows on 2 WM waves of 64 x 64 (WM = 2, S = 2: two
+// workgroups to a compute unit; with B turned WM = 4, S = 3: one), each 4 x 4 tiles of
+// v_mfma_f32_16x16x32_f16, four instructions to a block of k. Codes are copied
 // straight to LDS (S stages of rows of 128 bytes, 16-byte chunk c of row r at c ^ ((r >> 1) & 7),
 // so that the phases of a read cover all banks) S - 1 blocks ahead and widened in
 // the fragments: a wave holds the block's four fragments of B as halves (64 registers),
@@ -1058,21 +1059,18 @@ __global__ __launch_bounds__(512) void block_skinny(BlockArgs g) {
 template <int TA, int TB>
 int launch_block(const BlockPlan& p, const BlockArgs& a, dim3 grid, hipStream_t s) {
     const bool brow = a.b_shift == 0;
-    // operands with adjacent rows: one kernel for either kind of scales, each row's its own
-    if (p.tr == 1 && p.kernel == BLOCK_TILE256)
-        return launch_status(block_direct<TA, TB, true, 4, 3, true>, grid, dim3(512), s, a);
-    if (p.tr == 1) return launch_status(block_staged<TA, TB, true, 1>, grid, dim3(256), s, a);
-    if (p.tr == 2) return launch_status(block_staged<TA, TB, true, 2>, grid, dim3(256), s, a);
-    if (p.tr == 3) return launch_status(block_staged<TA, TB, true, 3>, grid, dim3(256), s, a);
-    if (p.kernel == BLOCK_TILE256)
-        return brow ? launch_status(block_direct<TA, TB, true, 4, 3>, grid, dim3(512), s, a)
-                    : launch_status(block_direct<TA, TB, false, 4, 3>, grid, dim3(512), s, a);
-    if (p.kernel == BLOCK_TILE128 && p.direct && p.small)
+    if (p.kernel == BLOCK_DIRECT)
         return brow ? launch_status(block_direct<TA, TB, true, 2, 2>, grid, dim3(256), s, a)
                     : launch_status(block_direct<TA, TB, false, 2, 2>, grid, dim3(256), s, a);
-    if (p.kernel == BLOCK_TILE128)
+    // operands with adjacent rows: one kernel for either kind of scales, each row's its own
+    if (p.kernel == BLOCK_TURNED) return launch_status(block_direct<TA, TB, true, 4, 3, true>, grid, dim3(512), s, a);
+    if (p.kernel == BLOCK_STAGED) {
+        if (p.tr == 1) return launch_status(block_staged<TA, TB, true, 1>, grid, dim3(256), s, a);
+        if (p.tr == 2) return launch_status(block_staged<TA, TB, true, 2>, grid, dim3(256), s, a);
+        if (p.tr == 3) return launch_status(block_staged<TA, TB, true, 3>, grid, dim3(256), s, a);
         return brow ? launch_status(block_staged<TA, TB, true, 0>, grid, dim3(256), s, a)
                     : launch_status(block_staged<TA, TB, false, 0>, grid, dim3(256), s, a);
+    }
     if (p.direct) {
         if (p.bn == 64) return launch_status(block_skinny<TA, TB, 1, 4, true>, grid, dim3(512), s, a);
         return p.bm == 16   ? launch_status(block_skinny<TA, TB, 1, 1, true>, grid, dim3(512), s, a)
