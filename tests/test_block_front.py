@@ -22,7 +22,7 @@ def passed(data, block_rows=1):
 @pytest.mark.parametrize("data,ld,op", [
     (codes(5, 300), 300, 0), (codes(5, 320)[:, :300], 320, 0), (codes(1, 300), 300, 0), (codes(7, 1), 1, 0),
     (codes(300, 5).t(), 5, 1), (codes(300, 8).t()[:5], 8, 1), (codes(300, 8).t()[:1], 8, 1), (codes(300, 1).t(), 300, 0),
-    (codes(2, 300, 8).transpose(1, 2)[:, 2:3], 8, 1), (codes(1, 1), 1, 0)], ids=lambda x: str(x))
+    (codes(2, 300, 8).transpose(1, 2)[:, 2:3], 8, 1), (codes(1, 1), 1, 0)], ids=lambda x: "x".join(map(str, x.shape)) if torch.is_tensor(x) else str(x))
 def test_either_dimension_contiguous(data, ld, op):
     """Rows that are contiguous, or columns; a matrix of one row lies both ways."""
     m = passed(data)
