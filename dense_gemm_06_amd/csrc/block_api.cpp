@@ -628,7 +628,7 @@ int gemm_experts_product(const gemm_block_matrix* A, const gemm_block_matrix* B,
     a.offsets = plan->offsets;
     a.counts = plan->counts;
     a.rows = gather ? plan->rows : nullptr;
-    a.tiles_m = (int)(P / p.bm + std::min(E, P));  // no plan has more
+    a.tiles_m = (int)std::max<int64_t>(1, P / p.bm + std::min(E, P));  // no plan has more; one clears rows without experts
     a.tiles_n = (int)ceil_div(N, p.bn);
     return launch(p, a, (int64_t)a.tiles_m * a.tiles_n, A->dtype, B->dtype, (hipStream_t)stream);
 }

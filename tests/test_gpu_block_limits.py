@@ -60,3 +60,15 @@ def test_offsets_that_overlap_stay_inside(T, N):
         assert set(c[live.cuda()].unique().tolist()) <= {0.0, 128.0} and (c[~live.cuda()] == 0).all()
         wide[256:256 + P, :N] = 7.0
         assert (wide == 7.0).all()
+
+
+def test_rows_without_experts():
+    """A plan of no experts: its rows are padding."""
+    i32 = lambda *x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    for P, N in ((5, 40), (300, 200)):
+        plan = dg.ExpertPlan(i32(0), i32(), i32(*[-1] * P), i32(-1).reshape(1, 1))
+        a = dg.BlockTensor(torch.ones(1, 128, device="cuda").to(E4), torch.ones(1, 1, device="cuda"), 1)
+        b = dg.BlockTensor(torch.empty(0, N, 128, device="cuda").to(E4), torch.empty(0, -(-N // 128), 1, device="cuda"), 128)
+        for out in (F32, BF16):
+            c = dg.gemm_experts_product_tensors(a, b, plan, out)
+            assert c.shape == (P, N) and (c == 0).all()
