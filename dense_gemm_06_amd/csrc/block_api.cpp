@@ -609,7 +609,7 @@ int gemm_experts_product(const gemm_block_matrix* A, const gemm_block_matrix* B,
     }
     DG_TRY(check_c(C, ldc, N, out_dtype));
     DG_TRY(check_pointer("plan.offsets", plan->offsets));
-    DG_TRY(check_pointer("plan.counts", plan->counts));
+    if (E > 0) DG_TRY(check_pointer("plan.counts", plan->counts));
     if (gather) DG_TRY(check_pointer("plan.rows", plan->rows));
     DG_TRY(check_overlap({range("C", C, span(P, N, ldc, elem_size(out_dtype)))},
                          {data_range("A.data", *A), scale_range("A.scale", *A), data_range("B.data", *B, E),
