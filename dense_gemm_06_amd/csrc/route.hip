@@ -200,7 +200,10 @@ __device__ __forceinline__ void token_scores(const RouteArgs& a, const ExpTerms&
 // ANY_GROUPS: groups that cut lanes, or more than the two largest of a group (a kernel of its
 // own, for the others' registers).
 // 16384 tokens x 256 experts, sigmoid, 8 groups: 100 us with a wave to a token and fp64
-// picks, 32 us with 16 lanes to a token, 27 us with fp32 picks, 22 us with 123 registers.
+// picks, 32 us with 16 lanes to a token, 27 us with fp32 picks, 22 us with 123 registers. Half
+// of its cycles issue the 2000 vector instructions of each wave (four tokens; four waves to a
+// SIMD, all at once; a fifth in fp64, at the same rate); the rest is the launch and latency: of
+// the logits, of LDS, and of the picks, each of which waits for the one before.
 template <int W, int R, int DT, bool ANY_GROUPS>
 __global__ __launch_bounds__(256) void route(RouteArgs a) {
     constexpr int PER = 64 / W;

@@ -16,7 +16,9 @@ captured into a graph.
   gemm_experts_combine_backward_tensors its gradients
 
 Tensors need unit stride along their last dimension (an operand's codes along either); other
-strides are free.
+strides are free. Results carry no gradient, also of tensors that require one: a training step
+calls the gradients' operators itself (examples/experts_step.py) or from its own
+torch.autograd.Function.
 """
 from __future__ import annotations
 

@@ -95,11 +95,11 @@ int gemm_block_product(const gemm_block_matrix* A, const gemm_block_matrix* B, v
 int64_t gemm_block_product_workspace(int64_t M, int64_t N, int64_t K);
 
 /*
- * Routing. Scores are softmax or sigmoid of the logits, computed in fp64. Each token's
- * choice value is its score plus bias (fp32, NULL: none). With groups > 1 the experts
- * are cut into `groups` equal runs; a run's value is the sum of its group_top largest
- * choice values, and only the top_groups best runs stay. The top_k experts of largest
- * choice value are taken in descending order, ties to the lowest index (a NaN counts as
+ * Routing. Scores are softmax or sigmoid of the logits, computed in fp64 (0 below e^-708).
+ * Each token's choice value is its score plus bias (fp32, NULL: none). With groups > 1 the
+ * experts are cut into `groups` equal runs; a run's value is the sum of its group_top largest
+ * choice values, and only the top_groups best runs stay. The top_k experts of largest choice
+ * value are taken in descending order, ties to the lowest index (a NaN counts as
  * largest). Their weights are the scores, divided by their sum with renorm, times factor.
  */
 typedef enum { GEMM_SCORE_SOFTMAX = 0, GEMM_SCORE_SIGMOID = 1 } gemm_score;
