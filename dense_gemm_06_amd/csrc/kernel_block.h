@@ -584,12 +584,12 @@ __global__ __launch_bounds__(WM * 128, 2) void block_direct(BlockArgs g) {
                     read_sb(st);
                     if constexpr (!BROW) row_scale = fS[st * (BM + BN) + wm * 64 + lane];
                 }
-                if constexpr (!BROW)
-                    if (i == 1) odd |= __ballot(!__builtin_amdgcn_classf(row_scale * sb[0][0], 0x108));
                 s_last = BROW ? s : s * sb[0][0];
                 __builtin_amdgcn_sched_barrier(0);
             }
         }
+        // in the shadow of the wait for the next block
+        if constexpr (!BROW) odd |= __ballot(!__builtin_amdgcn_classf(row_scale * sb[0][0], 0x108));
         if (kb + 1 < t.nkb) {
             // block kb + 1 is there, and everybody has read the last of block kb from its stage
             published(kb + S - 1 < t.nkb);
@@ -885,32 +885,45 @@ __global__ __launch_bounds__(256, 2) void block_staged(BlockArgs g) {
                         }
                     }
             }
+            // A's scale and B's of each row of B; or, where B has one for the tile, both as one factor,
+            // unless that is no normal number in some lane: then one after the other too
+            float f[FM];
+            uint64_t odd = 0;
 #pragma unroll
             for (int i = 0; i < FM; ++i) {
-                const float sa = fS[wm * 64 + i * 32 + l32];
+                f[i] = fS[wm * 64 + i * 32 + l32];
+                if constexpr (!BROW) {
+                    f[i] *= fS[BM + wn * 64];
+                    odd |= __ballot(!__builtin_amdgcn_classf(f[i], 0x108));
+                }
+            }
+            if (odd != 0) {
+#pragma unroll
+                for (int i = 0; i < FM; ++i) {
+                    const float sa = fS[wm * 64 + i * 32 + l32];
+#pragma unroll
+                    for (int j = 0; j < FN; ++j) part[i][j] *= sa;
+                    f[i] = fS[BM + wn * 64];
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < FM; ++i)
 #pragma unroll
                 for (int j = 0; j < FN; ++j) {
                     if (!(WHOLE || i < subs)) continue;
                     const float* sb = fS + BM + wn * 64 + j * 32 + lh * 4;
-                    // one factor, or one after the other where their product is no normal number
-                    float f = BROW ? 0.0f : sa * fS[BM + wn * 64];
-                    if (!BROW && __ballot(!__builtin_amdgcn_classf(f, 0x108)) != 0) {
-                        part[i][j] *= sa;
-                        f = fS[BM + wn * 64];
-                    }
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
-                        f32x4 s = {1, 1, 1, 1};
-                        if constexpr (BROW) s = *reinterpret_cast<const f32x4*>(sb + q * 8);
+                        f32x4 t = {1, 1, 1, 1};
+                        if constexpr (BROW) t = *reinterpret_cast<const f32x4*>(sb + q * 8);
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
                             const int r = 4 * q + e;
-                            if constexpr (BROW) acc[i][j][r] = fmaf(part[i][j][r] * sa, s[e], acc[i][j][r]);
-                            else acc[i][j][r] = fmaf(part[i][j][r], f, acc[i][j][r]);
+                            if constexpr (BROW) acc[i][j][r] = fmaf(part[i][j][r] * f[i], t[e], acc[i][j][r]);
+                            else acc[i][j][r] = fmaf(part[i][j][r], f[i], acc[i][j][r]);
                         }
                     }
                 }
-            }
         };
         if (subs == FM) block(std::true_type{});
         else if (subs > 0) block(std::false_type{});
