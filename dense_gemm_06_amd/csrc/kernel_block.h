@@ -358,7 +358,7 @@ __device__ __forceinline__ void block_again(const BlockArgs& g, const BlockTile&
 // kernel does, halves the conversions, but its writes and conflicts keep LDS busy longer than
 // the matrix cores. 8192 x 4096 x 4096 to bf16: 252 us, 1090 TFLOP/s (a library's product in
 // bf16 reaches 1290 at 8192 x 8192 x 8192), 49% of the SIMDs' cycles in matrix instructions and
-// 64% in vector ones; 2056 x 4000 x 8176 to fp32, scales for each row of B: 149 us.
+// 63% in vector ones; 2056 x 4000 x 8176 to fp32, scales for each row of B: 149 us.
 // TRB: B is stored with its rows adjacent; its stage then holds 128 rows of k, 16-byte chunk c
 // of row k at c ^ (((k >> 1) & 3) | ((k >> 2) & 4)), and 8 k of a row of B come from
 // ds_read_b64_tr_b8: in each 16 lanes, lane i addresses 8 bytes of row k0 + i/2 at half i%2 of a
@@ -720,8 +720,8 @@ __global__ __launch_bounds__(WM * 128, 2) void block_direct(BlockArgs g) {
 // see one chunk of 16 rows that differ in the low bits, so all places. TR: bit 0, B is
 // stored with its rows adjacent (element (n, k) at k*ldb + n), bit 1 the same for A; such an
 // operand is held as 128 rows of k, its 32-byte units of 16 rows permuted by 2 (k & 3), and
-// read through ds_read_b64_tr_b16. 8192 x 4096 x 4090 to bf16: 378 us, of which LDS conflicts
-// take a third of its active cycles.
+// read through ds_read_b64_tr_b16. 8192 x 4096 x 4090 to bf16: 354 us, LDS busy with conflicts
+// in a third of its active cycles.
 template <int TA, int TB, bool BROW, int TR>
 __global__ __launch_bounds__(256, 2) void block_staged(BlockArgs g) {
     constexpr int BM = 128, BN = 128, FM = 2, FN = 2, ROW = 68;
