@@ -8,7 +8,9 @@ the library's HIP kernels. A nonzero status raises
 GemmError carrying the library's own description.
 
 The block-scaled 8-bit products and the experts' operators of include/gemm_experts.h are
-in experts.py, whose names are here too (gemm_block_*, gemm_experts_*).
+in experts.py, whose names are here too (gemm_block_*, gemm_experts_*); the adapters, the
+loss over a vocabulary and the activations of include/gemm_layers.h are in layers.py
+(gemm_adapters_*, gemm_loss_*, gemm_activation_*).
 
 ``gemm_tensors`` is a convenience for torch tensors: it reads pointers, leading
 dimensions and the current stream off the tensors and calls gemm_ex. Torch
@@ -176,6 +178,7 @@ def _load():
     lib.gemm_last_error.argtypes = []
     lib.gemm_last_error.restype = ctypes.c_char_p
     _experts.declare(lib)
+    _layers.declare(lib)
     _lib = lib
     return lib
 
@@ -377,3 +380,9 @@ from .experts import (  # noqa: E402,F401
     gemm_experts_combine_backward_tensors, gemm_experts_combine_tensors, gemm_experts_dispatch_tensors,
     gemm_experts_gradient_tensors, gemm_experts_product_tensors, gemm_experts_route_backward_tensors,
     gemm_experts_route_tensors, gemm_router, router)
+
+# ----------------------------------------------------------------------------- operators around a layer's products
+from . import layers as _layers  # noqa: E402
+from .layers import (  # noqa: E402,F401
+    GEMM_ACT_SILU, gemm_activation_backward_tensors, gemm_activation_tensors, gemm_adapter_set,
+    gemm_adapters_backward_tensors, gemm_adapters_tensors, gemm_loss_backward_tensors, gemm_loss_tensors)

@@ -1,0 +1,117 @@
+// adapters.hip -- low-rank adapters of many requests beside a shared product.
+//
+//   u[t] = scale a_i x[t]      (shrink)        out[t] = base[t] + scale b_i u[t]   (expand)
+//   a_grad_i = sum_t v[t] x[t]^T over adapter i's rows                             (gradient)
+//
+// The same kernels serve the backward pass with the roles of a and b exchanged, which differ
+// in the direction that lies along memory (`turned`).
+#include "device_common.h"
+#include "layers.h"
+#include "launch.h"
+
+namespace dg {
+
+namespace {
+
+template <int DT>
+__device__ __forceinline__ float element(const void* p, size_t i) {
+    return decode<DT>(static_cast<const typename Elem<DT>::type*>(p)[i]);
+}
+
+__device__ __forceinline__ size_t m_at(const AdapterArgs& a, int i, int j, int64_t k) {
+    return (size_t)i * (size_t)a.stride_m +
+           (a.turned ? (size_t)k * (size_t)a.ldm + (size_t)j : (size_t)j * (size_t)a.ldm + (size_t)k);
+}
+
+}  // namespace
+
+// One wave: one token and one of its rank numbers.
+template <int DT>
+__global__ __launch_bounds__(256) void adapter_shrink(AdapterArgs a) {
+    const int64_t unit = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+    const int lane = threadIdx.x & 63;
+    if (unit >= (int64_t)a.tokens * a.rank) return;
+    const int t = (int)(unit / a.rank), j = (int)(unit - (int64_t)t * a.rank);
+    const int i = a.index[t];
+    float sum = 0.0f;
+    if (i >= 0 && i < a.adapters) {
+        for (int64_t k = lane; k < a.cols; k += 64)
+            sum = fmaf(element<DT>(a.x, (size_t)t * (size_t)a.ldx + k), element<DT>(a.m, m_at(a, i, j, k)), sum);
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) sum += __shfl_xor(sum, d);
+        if (a.scale) sum *= a.scale[i];
+    }
+    if (lane == 0) a.u[unit] = sum;
+}
+
+// One thread: one element.
+template <int DT>
+__global__ __launch_bounds__(256) void adapter_expand(AdapterArgs a, int64_t n) {
+    for (int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x; at < n; at += (int64_t)gridDim.x * 256) {
+        const int t = (int)(at / a.cols);
+        const int64_t k = at - (int64_t)t * a.cols;
+        const int i = a.index[t];
+        float sum = 0.0f;
+        if (i >= 0 && i < a.adapters) {
+            for (int j = 0; j < a.rank; ++j)
+                sum = fmaf(a.u[(size_t)t * a.rank + j], element<DT>(a.m, m_at(a, i, j, k)), sum);
+            if (a.scale) sum *= a.scale[i];
+        }
+        store_out(a.out, DT, (size_t)t * (size_t)a.ldo + k, a.base[(size_t)t * (size_t)a.ld_base + k] + sum);
+    }
+}
+
+// One thread: one element of one adapter's gradient. Indices from the device are kept inside
+// their arrays.
+template <int DT>
+__global__ __launch_bounds__(256) void adapter_gradient(AdapterArgs a, int64_t n) {
+    const int64_t each = (int64_t)a.rank * a.cols;
+    for (int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x; at < n; at += (int64_t)gridDim.x * 256) {
+        const int i = (int)(at / each);
+        const int64_t in = at - i * each;
+        const int64_t k = a.turned ? in / a.rank : in % a.cols;
+        const int j = (int)(a.turned ? in % a.rank : in / a.cols);
+        const int64_t from = max(0, min(a.offsets[i], a.capacity));
+        const int64_t to = min((int64_t)a.capacity, from + max(0, a.counts[i]));
+        float sum = 0.0f;
+        for (int64_t p = from; p < to; ++p) {
+            const int t = a.rows[p];
+            if (t < 0 || t >= a.tokens) continue;
+            sum = fmaf(a.u[(size_t)t * a.rank + j], element<DT>(a.x, (size_t)t * (size_t)a.ldx + k), sum);
+        }
+        if (a.scale) sum *= a.scale[i];
+        store_out(a.out, DT, (size_t)at, sum);
+    }
+}
+
+namespace {
+
+dim3 walk_grid(int64_t n) {
+    const int64_t wgs = (n + 255) / 256;
+    return dim3((unsigned)(wgs < (1 << 20) ? wgs : (1 << 20)));
+}
+
+}  // namespace
+
+int launch_adapter_shrink(const AdapterArgs& a, int dtype, hipStream_t s) {
+    const dim3 grid((unsigned)(((int64_t)a.tokens * a.rank + 3) / 4));
+    if (dtype == DT_F32) return launch_status(adapter_shrink<DT_F32>, grid, dim3(256), s, a);
+    if (dtype == DT_F16) return launch_status(adapter_shrink<DT_F16>, grid, dim3(256), s, a);
+    return launch_status(adapter_shrink<DT_BF16>, grid, dim3(256), s, a);
+}
+
+int launch_adapter_expand(const AdapterArgs& a, int dtype, hipStream_t s) {
+    const int64_t n = (int64_t)a.tokens * a.cols;
+    if (dtype == DT_F32) return launch_status(adapter_expand<DT_F32>, walk_grid(n), dim3(256), s, a, n);
+    if (dtype == DT_F16) return launch_status(adapter_expand<DT_F16>, walk_grid(n), dim3(256), s, a, n);
+    return launch_status(adapter_expand<DT_BF16>, walk_grid(n), dim3(256), s, a, n);
+}
+
+int launch_adapter_gradient(const AdapterArgs& a, int dtype, hipStream_t s) {
+    const int64_t n = (int64_t)a.adapters * a.rank * a.cols;
+    if (dtype == DT_F32) return launch_status(adapter_gradient<DT_F32>, walk_grid(n), dim3(256), s, a, n);
+    if (dtype == DT_F16) return launch_status(adapter_gradient<DT_F16>, walk_grid(n), dim3(256), s, a, n);
+    return launch_status(adapter_gradient<DT_BF16>, walk_grid(n), dim3(256), s, a, n);
+}
+
+}  // namespace dg

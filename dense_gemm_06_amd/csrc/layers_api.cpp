@@ -1,0 +1,628 @@
+// layers_api.cpp -- the C ABI declared in include/gemm_layers.h: validation, workspaces and
+// the launches. Everything is validated before the first launch.
+#include <hip/hip_runtime.h>
+#include <string.h>
+
+#include <algorithm>
+
+#include "checks.h"
+#include "launch.h"
+#include "layers.h"
+#include "plan.h"
+#include "product.h"
+
+namespace {
+
+// Workspace that a plain product inside an operator may split K or pack its operands in.
+constexpr int64_t kProductWorkspace = (int64_t)32 << 20;
+
+int64_t align256(int64_t n) { return (n + 255) / 256 * 256; }
+
+// Hands out the parts of a workspace; with a NULL base it only counts them.
+struct Parts {
+    char* base;
+    int64_t at = 0;
+    void* take(int64_t bytes) {
+        char* p = base ? base + at : nullptr;
+        at += align256(bytes);
+        return p;
+    }
+};
+
+int check_workspace(const void* workspace, int64_t bytes, int64_t need) {
+    if (bytes < need) {
+        set_error("workspace_bytes = %lld is less than the %lld that the call needs", (long long)bytes, (long long)need);
+        return GEMM_ERR_INVALID_VALUE;
+    }
+    if (need == 0) return GEMM_OK;
+    DG_TRY(check_pointer("workspace", workspace));
+    if (((uintptr_t)workspace & 15) != 0) {
+        set_error("the workspace must be 16-byte aligned (got %p)", workspace);
+        return GEMM_ERR_INVALID_VALUE;
+    }
+    return GEMM_OK;
+}
+
+int check_threads(const char* what, int64_t a, int64_t b, int64_t each) {
+    if ((unsigned __int128)a * (uint64_t)b * (uint64_t)each <= (unsigned __int128)kMaxThreads) return GEMM_OK;
+    set_error("%s = %lld * %lld needs more threads than a launch holds", what, (long long)a, (long long)b);
+    return GEMM_ERR_UNSUPPORTED;
+}
+
+// A product inside an operator: C of type out_dtype, plus beta C for fp32 C.
+int product(int opB, int64_t M, int64_t N, int64_t K, const void* A, int64_t lda, const void* B, int64_t ldb, void* C,
+            int64_t ldc, int dtype, int out_dtype, float beta, void* ws, int64_t ws_bytes, void* stream) {
+    dg::Epilogue ep = dg::plain_epilogue();
+    if (out_dtype != GEMM_F32 || beta != 0.0f) {
+        ep.kind = 1;
+        ep.out_dt = out_dtype;
+        ep.beta = beta;
+        ep.R = beta != 0.0f ? C : nullptr;
+        ep.ldr = ldc;
+    }
+    return dg::run_product(GEMM_OP_N, opB, M, N, K, A, std::max<int64_t>(1, lda), B, std::max<int64_t>(1, ldb), C, ldc,
+                           dtype, ep, nullptr, ws, ws_bytes, stream);
+}
+
+bool sizes_ok(std::initializer_list<int64_t> sizes) {
+    for (int64_t n : sizes)
+        if (n < 0 || n > kMaxDim) return false;
+    return true;
+}
+
+// ---------------------------------------------------------------- adapters
+int check_adapters(const gemm_adapter_set* s, int64_t N, int64_t K) {
+    DG_TRY(check_pointer("set", s));
+    DG_TRY(check_size("set.adapters", s->adapters));
+    if (s->rank < (s->adapters > 0 ? 1 : 0) || s->rank > dg::kMaxRank) {
+        set_error("set.rank = %lld must be 1 .. %d", (long long)s->rank, dg::kMaxRank);
+        return s->rank > dg::kMaxRank ? GEMM_ERR_UNSUPPORTED : GEMM_ERR_INVALID_VALUE;
+    }
+    DG_TRY(check_ld("set.lda", s->lda, K));
+    DG_TRY(check_ld("set.ldb", s->ldb, s->rank));
+    if (s->stride_a < 0 || s->stride_b < 0 || s->stride_a >= ((int64_t)1 << 40) || s->stride_b >= ((int64_t)1 << 40)) {
+        set_error("set: strides must be non-negative and below 2^40");
+        return GEMM_ERR_INVALID_VALUE;
+    }
+    if (s->adapters > 0) {
+        if (K > 0) DG_TRY(check_pointer("set.a", s->a));
+        if (N > 0) DG_TRY(check_pointer("set.b", s->b));
+    }
+    return GEMM_OK;
+}
+
+Range a_range(const gemm_adapter_set& s, int64_t K, int64_t es) {
+    return range("set.a", s.a, span(s.rank, K, s.lda, es, s.adapters, s.stride_a));
+}
+Range b_range(const gemm_adapter_set& s, int64_t N, int64_t es) {
+    return range("set.b", s.b, span(N, s.rank, s.ldb, es, s.adapters, s.stride_b));
+}
+Range scale_of(const gemm_adapter_set& s) { return range("set.scale", s.scale, (uint64_t)s.adapters * 4); }
+
+dg::AdapterArgs adapter_args(const gemm_adapter_set& s, int64_t tokens, const int32_t* index) {
+    dg::AdapterArgs a;
+    memset(&a, 0, sizeof a);
+    a.tokens = (int)tokens;
+    a.rank = (int)s.rank;
+    a.adapters = (int)s.adapters;
+    a.index = index;
+    return a;
+}
+
+void with_a(dg::AdapterArgs& a, const gemm_adapter_set& s, int64_t K) {
+    a.m = s.a;
+    a.ldm = s.lda;
+    a.stride_m = s.stride_a;
+    a.turned = 0;
+    a.cols = (int)K;
+}
+
+void with_b(dg::AdapterArgs& a, const gemm_adapter_set& s, int64_t N) {
+    a.m = s.b;
+    a.ldm = s.ldb;
+    a.stride_m = s.stride_b;
+    a.turned = 1;
+    a.cols = (int)N;
+}
+
+struct AdapterSpace {
+    float* base = nullptr;  // the shared product (16-bit matrices)
+    float* v = nullptr;
+    void* product = nullptr;
+    int64_t bytes = 0;
+};
+
+AdapterSpace adapter_space(void* workspace, int64_t tokens, int64_t cols, int64_t rank, int dtype, bool backward) {
+    AdapterSpace s;
+    Parts p{static_cast<char*>(workspace)};
+    if (dtype != GEMM_F32) s.base = static_cast<float*>(p.take(tokens * cols * 4));
+    if (backward) s.v = static_cast<float*>(p.take(tokens * rank * 4));
+    s.product = p.take(kProductWorkspace);
+    s.bytes = p.at;
+    return s;
+}
+
+// ---------------------------------------------------------------- loss
+constexpr int64_t kPieceBytes = (int64_t)128 << 20;
+
+// Columns of a piece: whole blocks of 256, as many as kPieceBytes hold.
+int64_t piece_of(int64_t tokens, int64_t vocabulary, int64_t each) {
+    const int64_t n = kPieceBytes / std::max<int64_t>(1, tokens * each);
+    return std::max<int64_t>(1, std::min(std::max<int64_t>(256, n / 256 * 256), vocabulary));
+}
+
+struct LossSpace {
+    float* logits = nullptr;
+    float* top = nullptr;
+    float* sum = nullptr;
+    float* picked = nullptr;
+    float* factor = nullptr;
+    void* d = nullptr;
+    void* dt = nullptr;
+    float* x_acc = nullptr;
+    float* w_acc = nullptr;
+    void* product = nullptr;
+    int64_t piece = 0, lddt = 0, bytes = 0;
+};
+
+LossSpace loss_space(void* workspace, int64_t tokens, int64_t vocabulary) {
+    LossSpace s;
+    Parts p{static_cast<char*>(workspace)};
+    s.piece = piece_of(tokens, vocabulary, 4);
+    s.logits = static_cast<float*>(p.take(tokens * s.piece * 4));
+    s.top = static_cast<float*>(p.take(tokens * 4));
+    s.sum = static_cast<float*>(p.take(tokens * 4));
+    s.picked = static_cast<float*>(p.take(tokens * 4));
+    s.product = p.take(kProductWorkspace);
+    s.bytes = p.at;
+    return s;
+}
+
+LossSpace loss_backward_space(void* workspace, int64_t tokens, int64_t vocabulary, int64_t K, int dtype, bool x_grad,
+                              bool w_grad, int64_t piece) {
+    LossSpace s;
+    Parts p{static_cast<char*>(workspace)};
+    const int64_t es = elem_size(dtype);
+    s.piece = piece > 0 ? std::min(piece, std::max<int64_t>(1, vocabulary)) : piece_of(tokens, vocabulary, 4 + 2 * es);
+    s.lddt = (tokens + 31) / 32 * 32;
+    s.factor = static_cast<float*>(p.take(8));
+    s.logits = static_cast<float*>(p.take(tokens * s.piece * 4));
+    if (x_grad) s.d = p.take(tokens * s.piece * es);
+    if (w_grad) s.dt = p.take(s.piece * s.lddt * es);
+    if (x_grad && dtype != GEMM_F32) s.x_acc = static_cast<float*>(p.take(tokens * K * 4));
+    if (w_grad && dtype != GEMM_F32) s.w_acc = static_cast<float*>(p.take(s.piece * K * 4));
+    s.product = p.take(kProductWorkspace);
+    s.bytes = p.at;
+    return s;
+}
+
+// ---------------------------------------------------------------- activations
+int check_activation(int activation, int64_t cols, int gated) {
+    if (activation != GEMM_ACT_RELU && activation != GEMM_ACT_GELU_TANH && activation != GEMM_ACT_SILU) {
+        set_error("activation = %d is not GEMM_ACT_RELU, GEMM_ACT_GELU_TANH or GEMM_ACT_SILU", activation);
+        return GEMM_ERR_INVALID_VALUE;
+    }
+    if (gated && cols > kMaxDim / 2) {
+        set_error("2 cols = %lld must be below 2^31", (long long)(2 * cols));
+        return GEMM_ERR_UNSUPPORTED;
+    }
+    return GEMM_OK;
+}
+
+int check_codes(const gemm_block_matrix& m, int64_t rows, int64_t zcols) {
+    DG_TRY(check_op_n("codes", m));
+    if (m.rows == rows && m.cols == zcols) return GEMM_OK;
+    set_error("codes is %lld x %lld, not %lld x %lld", (long long)m.rows, (long long)m.cols, (long long)rows,
+              (long long)zcols);
+    return GEMM_ERR_INVALID_VALUE;
+}
+
+dg::QuantOut codes_of(const gemm_block_matrix& m) {
+    dg::QuantOut o;
+    o.q = static_cast<uint8_t*>(m.data);
+    o.s = m.scale;
+    o.ld = m.ld;
+    o.s_row = m.scale_row;
+    o.s_blk = m.scale_block;
+    o.type = m.dtype == GEMM_E4M3 ? 0 : 1;
+    o.block_rows = m.block_rows;
+    return o;
+}
+
+}  // namespace
+
+extern "C" {
+
+// ---------------------------------------------------------------- adapters
+int64_t gemm_adapters_workspace(int64_t tokens, int64_t N, int64_t K, int64_t rank, int dtype) {
+    if (!sizes_ok({tokens, N, K, rank}) || !is_wide(dtype)) return 0;
+    return adapter_space(nullptr, tokens, N, rank, dtype, false).bytes;
+}
+
+int gemm_adapters_product(const void* x, int64_t tokens, int64_t K, int64_t ldx, const void* w, int64_t N, int64_t ldw,
+                          int dtype, const gemm_adapter_set* set, const int32_t* index, void* y, int64_t ldy, float* u,
+                          void* workspace, int64_t workspace_bytes, void* stream) {
+    dg::clear_error();
+    DG_TRY(check_dtype("dtype", dtype));
+    DG_TRY(check_size("tokens", tokens));
+    DG_TRY(check_size("K", K));
+    DG_TRY(check_size("N", N));
+    DG_TRY(check_ld("ldx", ldx, K));
+    DG_TRY(check_ld("ldw", ldw, K));
+    DG_TRY(check_ld("ldy", ldy, N));
+    DG_TRY(check_adapters(set, N, K));
+    if (tokens == 0) return GEMM_OK;
+    const int64_t es = elem_size(dtype);
+    const AdapterSpace sp = adapter_space(workspace, tokens, N, set->rank, dtype, false);
+    if (K > 0) DG_TRY(check_pointer("x", x));
+    if (K > 0 && N > 0) DG_TRY(check_pointer("w", w));
+    if (N > 0) DG_TRY(check_pointer("y", y));
+    if (set->rank > 0) DG_TRY(check_pointer("u", u));
+    DG_TRY(check_pointer("index", index));
+    DG_TRY(check_workspace(workspace, workspace_bytes, sp.bytes));
+    DG_TRY(check_overlap({range("y", y, span(tokens, N, ldy, es)), range("u", u, (uint64_t)tokens * set->rank * 4),
+                          range("workspace", workspace, (uint64_t)workspace_bytes)},
+                         {range("x", x, span(tokens, K, ldx, es)), range("w", w, span(N, K, ldw, es)),
+                          a_range(*set, K, es), b_range(*set, N, es), scale_of(*set),
+                          range("index", index, (uint64_t)tokens * 4)}));
+    DG_TRY(check_threads("tokens * rank", tokens, set->rank, 64));
+    DG_TRY(check_device());
+    const hipStream_t s = (hipStream_t)stream;
+    dg::AdapterArgs a = adapter_args(*set, tokens, index);
+    a.x = x;
+    a.ldx = ldx;
+    a.u = u;
+    with_a(a, *set, K);
+    if (set->rank > 0) DG_TRY(launched(dg::launch_adapter_shrink(a, dtype, s), "adapters' first product"));
+    if (N == 0) return GEMM_OK;
+    float* base = dtype == GEMM_F32 ? static_cast<float*>(y) : sp.base;
+    const int64_t ldb = dtype == GEMM_F32 ? ldy : N;
+    DG_TRY(product(GEMM_OP_T, tokens, N, K, x, ldx, w, ldw, base, ldb, dtype, GEMM_F32, 0.0f, sp.product,
+                   kProductWorkspace, stream));
+    with_b(a, *set, N);
+    a.scale = set->scale;
+    a.base = base;
+    a.ld_base = ldb;
+    a.out = y;
+    a.ldo = ldy;
+    return launched(dg::launch_adapter_expand(a, dtype, s), "adapters' second product");
+}
+
+int64_t gemm_adapters_backward_workspace(int64_t tokens, int64_t N, int64_t K, int64_t adapters, int64_t rank,
+                                         int dtype) {
+    if (!sizes_ok({tokens, N, K, adapters, rank}) || !is_wide(dtype)) return 0;
+    return adapter_space(nullptr, tokens, K, rank, dtype, true).bytes;
+}
+
+int gemm_adapters_backward(const void* grad, int64_t tokens, int64_t N, int64_t ldg, const void* x, int64_t K,
+                           int64_t ldx, const float* u, const void* w, int64_t ldw, int dtype,
+                           const gemm_adapter_set* set, const int32_t* index, const gemm_expert_plan* plan, void* x_grad,
+                           int64_t ldxg, void* a_grad, void* b_grad, void* workspace, int64_t workspace_bytes,
+                           void* stream) {
+    dg::clear_error();
+    DG_TRY(check_dtype("dtype", dtype));
+    DG_TRY(check_size("tokens", tokens));
+    DG_TRY(check_size("K", K));
+    DG_TRY(check_size("N", N));
+    DG_TRY(check_ld("ldg", ldg, N));
+    DG_TRY(check_ld("ldx", ldx, K));
+    DG_TRY(check_ld("ldw", ldw, K));
+    if (x_grad) DG_TRY(check_ld("ldxg", ldxg, K));
+    DG_TRY(check_adapters(set, N, K));
+    if ((a_grad == nullptr) != (b_grad == nullptr) && set->adapters > 0 && N > 0 && K > 0) {
+        set_error("a_grad and b_grad come together or are both NULL");
+        return GEMM_ERR_NULL_POINTER;
+    }
+    const bool adapters = (a_grad || b_grad) && set->adapters > 0;
+    const int64_t es = elem_size(dtype);
+    if (adapters) {
+        DG_TRY(check_plan(plan));
+        if (plan->experts != set->adapters || plan->tokens != tokens || plan->top_k != 1) {
+            set_error("plan of %lld experts, %lld tokens, top_k %lld, not of %lld adapters, %lld tokens, 1",
+                      (long long)plan->experts, (long long)plan->tokens, (long long)plan->top_k,
+                      (long long)set->adapters, (long long)tokens);
+            return GEMM_ERR_INVALID_VALUE;
+        }
+        DG_TRY(check_pointer("plan.offsets", plan->offsets));
+        DG_TRY(check_pointer("plan.counts", plan->counts));
+        if (plan->capacity > 0) DG_TRY(check_pointer("plan.rows", plan->rows));
+    }
+    if (tokens == 0 && !adapters) return GEMM_OK;
+    const AdapterSpace sp = adapter_space(workspace, tokens, K, set->rank, dtype, true);
+    if (tokens > 0) {
+        if (N > 0) DG_TRY(check_pointer("grad", grad));
+        if (K > 0) DG_TRY(check_pointer("x", x));
+        if (x_grad && N > 0 && K > 0) DG_TRY(check_pointer("w", w));
+        if (set->rank > 0) DG_TRY(check_pointer("u", u));
+        DG_TRY(check_pointer("index", index));
+    }
+    DG_TRY(check_workspace(workspace, workspace_bytes, sp.bytes));
+    const Range none = range("", nullptr, 0);
+    const uint64_t each = (uint64_t)set->adapters * set->rank * es;
+    DG_TRY(check_overlap(
+        {range("x_grad", x_grad, span(tokens, K, ldxg, es)), range("a_grad", a_grad, each * K),
+         range("b_grad", b_grad, each * N), range("workspace", workspace, (uint64_t)workspace_bytes)},
+        {range("grad", grad, span(tokens, N, ldg, es)), range("x", x, span(tokens, K, ldx, es)),
+         range("u", u, (uint64_t)tokens * set->rank * 4), range("w", w, span(N, K, ldw, es)), a_range(*set, K, es),
+         b_range(*set, N, es), scale_of(*set), range("index", index, (uint64_t)tokens * 4),
+         adapters ? range("plan.offsets", plan->offsets, (uint64_t)(plan->experts + 1) * 4) : none,
+         adapters ? range("plan.counts", plan->counts, (uint64_t)plan->experts * 4) : none,
+         adapters ? range("plan.rows", plan->rows, (uint64_t)plan->capacity * 4) : none}));
+    DG_TRY(check_threads("tokens * rank", tokens, set->rank, 64));
+    DG_TRY(check_device());
+    const hipStream_t s = (hipStream_t)stream;
+    dg::AdapterArgs a = adapter_args(*set, tokens, index);
+    // v = scale grad b
+    a.x = grad;
+    a.ldx = ldg;
+    a.u = sp.v;
+    a.scale = set->scale;
+    with_b(a, *set, N);
+    if (tokens > 0 && set->rank > 0) DG_TRY(launched(dg::launch_adapter_shrink(a, dtype, s), "adapters' v"));
+    if (x_grad && tokens > 0 && K > 0) {
+        float* base = dtype == GEMM_F32 ? static_cast<float*>(x_grad) : sp.base;
+        const int64_t ldb = dtype == GEMM_F32 ? ldxg : K;
+        DG_TRY(product(GEMM_OP_N, tokens, K, N, grad, ldg, w, ldw, base, ldb, dtype, GEMM_F32, 0.0f, sp.product,
+                       kProductWorkspace, stream));
+        with_a(a, *set, K);
+        a.scale = nullptr;
+        a.base = base;
+        a.ld_base = ldb;
+        a.out = x_grad;
+        a.ldo = ldxg;
+        DG_TRY(launched(dg::launch_adapter_expand(a, dtype, s), "adapters' x_grad"));
+    }
+    if (!adapters) return GEMM_OK;
+    a.offsets = plan->offsets;
+    a.counts = plan->counts;
+    a.rows = plan->rows;
+    a.capacity = (int)plan->capacity;
+    if (K > 0) {
+        a.x = x;
+        a.ldx = ldx;
+        a.scale = nullptr;
+        with_a(a, *set, K);
+        a.out = a_grad;
+        DG_TRY(launched(dg::launch_adapter_gradient(a, dtype, s), "adapters' a_grad"));
+    }
+    if (N > 0) {
+        a.x = grad;
+        a.ldx = ldg;
+        a.u = const_cast<float*>(u);
+        a.scale = set->scale;
+        with_b(a, *set, N);
+        a.out = b_grad;
+        DG_TRY(launched(dg::launch_adapter_gradient(a, dtype, s), "adapters' b_grad"));
+    }
+    return GEMM_OK;
+}
+
+// ---------------------------------------------------------------- loss
+int64_t gemm_loss_workspace(int64_t tokens, int64_t vocabulary, int64_t K, int dtype) {
+    if (!sizes_ok({tokens, vocabulary, K}) || !is_wide(dtype)) return 0;
+    return loss_space(nullptr, tokens, vocabulary).bytes;
+}
+
+int gemm_loss(const void* x, int64_t tokens, int64_t K, int64_t ldx, const void* w, int64_t vocabulary, int64_t ldw,
+              int dtype, const int64_t* target, float* loss, float* lse, void* workspace, int64_t workspace_bytes,
+              void* stream) {
+    dg::clear_error();
+    DG_TRY(check_dtype("dtype", dtype));
+    DG_TRY(check_size("tokens", tokens));
+    DG_TRY(check_size("K", K));
+    DG_TRY(check_size("vocabulary", vocabulary));
+    DG_TRY(check_ld("ldx", ldx, K));
+    DG_TRY(check_ld("ldw", ldw, K));
+    if (tokens == 0) return GEMM_OK;
+    const int64_t es = elem_size(dtype);
+    const LossSpace sp = loss_space(workspace, tokens, vocabulary);
+    if (K > 0) DG_TRY(check_pointer("x", x));
+    if (K > 0 && vocabulary > 0) DG_TRY(check_pointer("w", w));
+    DG_TRY(check_pointer("target", target));
+    DG_TRY(check_pointer("loss", loss));
+    DG_TRY(check_pointer("lse", lse));
+    DG_TRY(check_workspace(workspace, workspace_bytes, sp.bytes));
+    const uint64_t n4 = (uint64_t)tokens * 4;
+    DG_TRY(check_overlap({range("loss", loss, n4), range("lse", lse, n4),
+                          range("workspace", workspace, (uint64_t)workspace_bytes)},
+                         {range("x", x, span(tokens, K, ldx, es)), range("w", w, span(vocabulary, K, ldw, es)),
+                          range("target", target, n4 * 2)}));
+    DG_TRY(check_threads("tokens", tokens, 1, 256));
+    DG_TRY(check_device());
+    dg::LossArgs a;
+    memset(&a, 0, sizeof a);
+    a.logits = sp.logits;
+    a.tokens = (int)tokens;
+    a.vocabulary = (int)vocabulary;
+    a.target = target;
+    a.top = sp.top;
+    a.sum = sp.sum;
+    a.picked = sp.picked;
+    a.loss = loss;
+    a.lse = lse;
+    int64_t v0 = 0;
+    do {
+        a.n = (int)std::min(sp.piece, vocabulary - v0);
+        a.ld = std::max(1, a.n);
+        a.v0 = (int)v0;
+        a.first = v0 == 0;
+        a.last = v0 + a.n >= vocabulary;
+        DG_TRY(product(GEMM_OP_T, tokens, a.n, K, x, ldx, static_cast<const char*>(w) + (size_t)v0 * ldw * es, ldw,
+                       sp.logits, a.ld, dtype, GEMM_F32, 0.0f, sp.product, kProductWorkspace, stream));
+        DG_TRY(launched(dg::launch_loss_stats(a, (hipStream_t)stream), "loss"));
+        v0 += a.n;
+    } while (v0 < vocabulary);
+    return GEMM_OK;
+}
+
+int64_t gemm_loss_backward_workspace(int64_t tokens, int64_t vocabulary, int64_t K, int dtype, int want_x_grad,
+                                     int want_w_grad, int64_t piece) {
+    if (!sizes_ok({tokens, vocabulary, K, piece}) || !is_wide(dtype)) return 0;
+    return loss_backward_space(nullptr, tokens, vocabulary, K, dtype, want_x_grad != 0, want_w_grad != 0, piece).bytes;
+}
+
+int gemm_loss_backward(const float* grad, const void* x, int64_t tokens, int64_t K, int64_t ldx, const void* w,
+                       int64_t vocabulary, int64_t ldw, int dtype, const int64_t* target, const float* lse, void* x_grad,
+                       int64_t ldxg, void* w_grad, int64_t ldwg, int64_t piece, void* workspace,
+                       int64_t workspace_bytes, void* stream) {
+    dg::clear_error();
+    DG_TRY(check_dtype("dtype", dtype));
+    DG_TRY(check_size("tokens", tokens));
+    DG_TRY(check_size("K", K));
+    DG_TRY(check_size("vocabulary", vocabulary));
+    DG_TRY(check_size("piece", piece));
+    DG_TRY(check_ld("ldx", ldx, K));
+    DG_TRY(check_ld("ldw", ldw, K));
+    if (x_grad) DG_TRY(check_ld("ldxg", ldxg, K));
+    if (w_grad) DG_TRY(check_ld("ldwg", ldwg, K));
+    if (K == 0 || (x_grad == nullptr && w_grad == nullptr)) return GEMM_OK;
+    if ((tokens == 0 || x_grad == nullptr) && (vocabulary == 0 || w_grad == nullptr)) return GEMM_OK;
+    const int64_t es = elem_size(dtype);
+    const LossSpace sp =
+        loss_backward_space(workspace, tokens, vocabulary, K, dtype, x_grad != nullptr, w_grad != nullptr, piece);
+    if (tokens > 0) {
+        DG_TRY(check_pointer("grad", grad));
+        DG_TRY(check_pointer("x", x));
+        DG_TRY(check_pointer("target", target));
+        DG_TRY(check_pointer("lse", lse));
+    }
+    if (vocabulary > 0) DG_TRY(check_pointer("w", w));
+    DG_TRY(check_workspace(workspace, workspace_bytes, sp.bytes));
+    const uint64_t n4 = (uint64_t)tokens * 4;
+    DG_TRY(check_overlap({range("x_grad", x_grad, span(tokens, K, ldxg, es)),
+                          range("w_grad", w_grad, span(vocabulary, K, ldwg, es)),
+                          range("workspace", workspace, (uint64_t)workspace_bytes)},
+                         {range("grad", grad, n4), range("x", x, span(tokens, K, ldx, es)),
+                          range("w", w, span(vocabulary, K, ldw, es)), range("target", target, n4 * 2),
+                          range("lse", lse, n4)}));
+    DG_TRY(check_threads("blocks of tokens * piece", ceil_div(tokens, 64), ceil_div(sp.piece, 64), 256));
+    DG_TRY(check_device());
+    const hipStream_t s = (hipStream_t)stream;
+    // fp16 holds d times a power of two that brings the largest |grad| near 2^14
+    const bool wide = dtype == GEMM_F32, scaled = dtype == GEMM_F16;
+    dg::LossArgs a;
+    memset(&a, 0, sizeof a);
+    a.logits = sp.logits;
+    a.tokens = (int)tokens;
+    a.vocabulary = (int)vocabulary;
+    a.target = target;
+    a.lse_in = lse;
+    a.grad = grad;
+    a.factor = scaled ? sp.factor : nullptr;
+    a.d = sp.d;
+    a.dt = sp.dt;
+    a.lddt = sp.lddt;
+    if (scaled) DG_TRY(launched(dg::launch_loss_factor(grad, (int)tokens, sp.factor, s), "loss gradient's factor"));
+    float* xa = wide ? static_cast<float*>(x_grad) : sp.x_acc;
+    const int64_t ldxa = wide ? ldxg : K;
+    int64_t v0 = 0;
+    do {
+        a.n = (int)std::min(sp.piece, vocabulary - v0);
+        a.ld = a.ldd = std::max(1, a.n);
+        a.v0 = (int)v0;
+        const char* wp = static_cast<const char*>(w) + (size_t)v0 * ldw * es;
+        if (tokens > 0 && a.n > 0) {
+            DG_TRY(product(GEMM_OP_T, tokens, a.n, K, x, ldx, wp, ldw, sp.logits, a.ld, dtype, GEMM_F32, 0.0f,
+                           sp.product, kProductWorkspace, stream));
+            DG_TRY(launched(dg::launch_loss_grad(a, dtype, s), "loss gradient"));
+        }
+        if (x_grad)
+            DG_TRY(product(GEMM_OP_N, tokens, K, a.n, sp.d, a.ldd, wp, ldw, xa, ldxa, dtype, GEMM_F32,
+                           v0 == 0 ? 0.0f : 1.0f, sp.product, kProductWorkspace, stream));
+        if (w_grad) {
+            char* wg = static_cast<char*>(w_grad) + (size_t)v0 * ldwg * es;
+            DG_TRY(product(GEMM_OP_N, a.n, K, tokens, sp.dt, sp.lddt, x, ldx, scaled ? (void*)sp.w_acc : wg,
+                           scaled ? K : ldwg, dtype, scaled ? GEMM_F32 : dtype, 0.0f, sp.product, kProductWorkspace,
+                           stream));
+            if (scaled && a.n > 0)
+                DG_TRY(launched(dg::launch_scaled_cast(sp.w_acc, K, a.n, (int)K, sp.factor, wg, ldwg, dtype, s),
+                                "loss gradient's rounding"));
+        }
+        v0 += a.n;
+    } while (v0 < vocabulary);
+    if (x_grad && !wide && tokens > 0)
+        DG_TRY(launched(dg::launch_scaled_cast(sp.x_acc, K, (int)tokens, (int)K, a.factor, x_grad, ldxg, dtype, s),
+                        "loss gradient's rounding"));
+    return GEMM_OK;
+}
+
+// ---------------------------------------------------------------- activations
+int gemm_activation_forward(const void* z, int64_t rows, int64_t cols, int64_t ldz, int dtype, int activation,
+                            int gated, void* y, int64_t ldy, const gemm_block_matrix* codes, void* stream) {
+    dg::clear_error();
+    DG_TRY(check_dtype("dtype", dtype));
+    DG_TRY(check_size("rows", rows));
+    DG_TRY(check_size("cols", cols));
+    DG_TRY(check_activation(activation, cols, gated));
+    const int64_t zcols = gated ? 2 * cols : cols, es = elem_size(dtype);
+    DG_TRY(check_ld("ldz", ldz, zcols));
+    DG_TRY(check_ld("ldy", ldy, cols));
+    if (codes) {
+        DG_TRY(check_block("codes", codes));
+        DG_TRY(check_codes(*codes, rows, zcols));
+        if (codes->block_rows != 1) {
+            set_error("codes.block_rows = %d must be 1", codes->block_rows);
+            return GEMM_ERR_INVALID_VALUE;
+        }
+    }
+    if (rows == 0 || cols == 0) return GEMM_OK;
+    DG_TRY(check_pointer("z", z));
+    DG_TRY(check_pointer("y", y));
+    const Range none = range("", nullptr, 0);
+    DG_TRY(check_overlap({range("y", y, span(rows, cols, ldy, es)), codes ? data_range("codes.data", *codes) : none,
+                          codes ? scale_range("codes.scale", *codes) : none},
+                         {range("z", z, span(rows, zcols, ldz, es))}));
+    DG_TRY(check_device());
+    dg::ActArgs a;
+    memset(&a, 0, sizeof a);
+    a.z = z;
+    a.ldz = ldz;
+    if (codes) a.codes = codes_of(*codes);
+    a.rows = (int)rows;
+    a.cols = (int)cols;
+    a.act = activation;
+    a.gated = gated != 0;
+    a.y = y;
+    a.ldy = ldy;
+    return launched(dg::launch_activation(a, dtype, (hipStream_t)stream), "activation");
+}
+
+int gemm_activation_backward(const gemm_block_matrix* codes, const void* grad, int64_t rows, int64_t cols, int64_t ldg,
+                             int dtype, int activation, int gated, void* z_grad, int64_t ldzg, void* y, int64_t ldy,
+                             void* stream) {
+    dg::clear_error();
+    DG_TRY(check_dtype("dtype", dtype));
+    DG_TRY(check_size("rows", rows));
+    DG_TRY(check_size("cols", cols));
+    DG_TRY(check_activation(activation, cols, gated));
+    const int64_t zcols = gated ? 2 * cols : cols, es = elem_size(dtype);
+    DG_TRY(check_ld("ldg", ldg, cols));
+    DG_TRY(check_ld("ldzg", ldzg, zcols));
+    if (y) DG_TRY(check_ld("ldy", ldy, cols));
+    DG_TRY(check_block("codes", codes));
+    DG_TRY(check_codes(*codes, rows, zcols));
+    if (rows == 0 || cols == 0) return GEMM_OK;
+    DG_TRY(check_pointer("grad", grad));
+    DG_TRY(check_pointer("z_grad", z_grad));
+    DG_TRY(check_overlap({range("z_grad", z_grad, span(rows, zcols, ldzg, es)),
+                          range("y", y, span(rows, cols, ldy, es))},
+                         {range("grad", grad, span(rows, cols, ldg, es)), data_range("codes.data", *codes),
+                          scale_range("codes.scale", *codes)}));
+    DG_TRY(check_device());
+    dg::ActArgs a;
+    memset(&a, 0, sizeof a);
+    a.codes = codes_of(*codes);
+    a.rows = (int)rows;
+    a.cols = (int)cols;
+    a.act = activation;
+    a.gated = gated != 0;
+    a.y = y;
+    a.ldy = ldy;
+    a.grad = grad;
+    a.ldg = ldg;
+    a.z_grad = z_grad;
+    a.ldzg = ldzg;
+    return launched(dg::launch_activation_backward(a, dtype, (hipStream_t)stream), "activation's backward pass");
+}
+
+}  // extern "C"
