@@ -112,8 +112,17 @@ __device__ __forceinline__ u32x4 keep_first8(u32x4 w, int v) {
 // tile raster as for the register-staged grouped kernels); each tile carries its own
 // operands, leading dimensions, M, N, K and C, and the copy stream runs on across
 // problems as across tiles. g then holds only xcd_remap (and no fused epilogue).
-template <int DT, int OPB, int NW, bool REG, bool PERSIST, bool GROUPED>
-__device__ __forceinline__ void mfma32_sp_body(GemmArgs& g, const GroupArgs* ga) {
+//
+// HOOK: what an operator built on the one-tile forms does with a finished wave tile. With
+// kReplace, h.finish(acc, m, n, wm, wn, lds, lds2) takes the accumulators (row 32 i + lane % 32 of
+// the wave tile at row m, columns as laid out at full_epilogue, from column n) in place of the
+// store, with the whole LDS (two halves of 64 KB) to itself; else h.add(acc, m, n) adds to them before it.
+struct NoHook {
+    static constexpr bool kReplace = false, kAdd = false;
+};
+
+template <int DT, int OPB, int NW, bool REG, bool PERSIST, bool GROUPED, class HOOK = NoHook>
+__device__ __forceinline__ void mfma32_sp_body(GemmArgs& g, const GroupArgs* ga, const HOOK& h = HOOK{}) {
     static_assert(NW == 4 || NW == 8, "waves");
     static_assert(!GROUPED || (PERSIST && !REG && NW == 8), "grouped: the persistent direct-copy form");
     constexpr int BM = 256, BN = 256, BK = 32, S = 4, D = S - 1;  // D: copy distance in tiles
@@ -537,6 +546,12 @@ __device__ __forceinline__ void mfma32_sp_body(GemmArgs& g, const GroupArgs* ga)
     auto full_epilogue = [&](const Src& s) {
         asm volatile("s_nop 7\n\ts_nop 7\n\ts_nop 3" ::: "memory");
         __syncthreads();
+        if constexpr (HOOK::kReplace) {
+            h.finish(acc, s.m0 + wrow0, s.n0 + wcol0, wm, wn, reinterpret_cast<char*>(&sA[0][0]),
+                     reinterpret_cast<char*>(&sB[0][0]));
+            return;
+        }
+        if constexpr (HOOK::kAdd) h.add(acc, s.m0 + wrow0, s.n0 + wcol0);
         constexpr int WT = 32 * SJ * 4;           // bytes per wave-tile row
         constexpr int CPR = WT / 16;              // 16-byte chunks per row
         constexpr int RPI = 64 / CPR;             // rows per read instruction

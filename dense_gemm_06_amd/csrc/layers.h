@@ -11,6 +11,7 @@
 namespace dg {
 
 constexpr int kMaxRank = 128;
+constexpr int kMaxAdapters = 32768;  // of a grid's second direction, with room for the chunks of their rows
 
 // ---------------------------------------------------------------- activations
 struct ActArgs {
@@ -68,6 +69,7 @@ struct AdapterArgs {
     const void* m;          // adapters' matrices: turned 0: rank x cols, 1: cols x rank
     int64_t ldm, stride_m;
     int turned;
+    int rank_m;             // numbers in a row of a turned m (zeros past the rank)
     int tokens, cols, rank, adapters;
     const int* index;
     const float* scale;     // NULL: 1
@@ -82,7 +84,42 @@ struct AdapterArgs {
     const int* counts;
     const int* rows;
     int capacity;
+    int chunk;              // rows of the plan that a workgroup of the gradient takes
+    float* work;            // their sums
 };
+
+// What the 16-bit kernels for a shared product x w^T (turned 1: x w) with adapters take.
+struct AdapterProduct {
+    const void* x;
+    const void* w;
+    int64_t ldx, ldw;
+    int N, K;               // columns of the result, length of the sum
+    int opb;                // GEMM_OP_T: w is N x K, GEMM_OP_N: K x N
+    int direct;             // rows of whole 16-byte pieces, 16-byte aligned
+};
+
+// The adapters' transposes: in is rows x cols, out cols x out_ld.
+struct TurnArgs {
+    const void* in;
+    int64_t ld, stride;
+    int rows, cols;
+    void* out;              // each matrix cols x out_ld, contiguous
+    int out_ld;
+    int tiles_r, tiles_c;
+};
+
+// 16-bit matrices, on the matrix instructions, one function for each type:
+// out = x w + scale u m in one kernel, for up to 64 tokens (x w^T only) or in 256 x 256 tiles
+#define DG_16BIT(name, params)                                    \
+    int name##_f16 params;                                             \
+    int name##_bf16 params;
+DG_16BIT(launch_adapter_skinny, (const AdapterProduct& p, const AdapterArgs& a, hipStream_t s))
+DG_16BIT(launch_adapter_tiles, (const AdapterProduct& p, const AdapterArgs& a, int group_m, hipStream_t s))
+// the operators below, m with its long direction along memory in shrink and across it in expand
+DG_16BIT(launch_adapter_shrink16, (const AdapterArgs& a, hipStream_t s))
+DG_16BIT(launch_adapter_expand16, (const AdapterArgs& a, hipStream_t s))
+DG_16BIT(launch_adapter_gradient16, (const AdapterArgs& a, int slots, hipStream_t s))
+int launch_adapter_turn(const TurnArgs& p, const TurnArgs& q, int adapters, hipStream_t s);
 
 // u[t][j] = scale sum_k x[t][k] m(j,k)
 int launch_adapter_shrink(const AdapterArgs& a, int dtype, hipStream_t s);

@@ -74,6 +74,10 @@ bool sizes_ok(std::initializer_list<int64_t> sizes) {
 int check_adapters(const gemm_adapter_set* s, int64_t N, int64_t K) {
     DG_TRY(check_pointer("set", s));
     DG_TRY(check_size("set.adapters", s->adapters));
+    if (s->adapters > dg::kMaxAdapters) {
+        set_error("set.adapters = %lld must be at most %d", (long long)s->adapters, dg::kMaxAdapters);
+        return GEMM_ERR_UNSUPPORTED;
+    }
     if (s->rank < (s->adapters > 0 ? 1 : 0) || s->rank > dg::kMaxRank) {
         set_error("set.rank = %lld must be 1 .. %d", (long long)s->rank, dg::kMaxRank);
         return s->rank > dg::kMaxRank ? GEMM_ERR_UNSUPPORTED : GEMM_ERR_INVALID_VALUE;
@@ -89,6 +93,11 @@ int check_adapters(const gemm_adapter_set* s, int64_t N, int64_t K) {
         if (N > 0) DG_TRY(check_pointer("set.b", s->b));
     }
     return GEMM_OK;
+}
+
+int check_adapter_threads(int64_t tokens, int64_t cols, int64_t rank, int dtype) {
+    if (dtype == GEMM_F32) return check_threads("tokens * rank", tokens, rank, 64);
+    return check_threads("blocks of tokens * columns", ceil_div(tokens, 32), ceil_div(cols, 256), 256);
 }
 
 Range a_range(const gemm_adapter_set& s, int64_t K, int64_t es) {
@@ -122,25 +131,86 @@ void with_b(dg::AdapterArgs& a, const gemm_adapter_set& s, int64_t N) {
     a.ldm = s.ldb;
     a.stride_m = s.stride_b;
     a.turned = 1;
+    a.rank_m = (int)s.rank;
     a.cols = (int)N;
 }
 
+// Tokens up to which one workgroup has all of them (kernel_skinny.h).
+constexpr int64_t kSkinny = 64;
+
+// Whether 256 x 256 tiles of the result give enough compute units work for the kernel that adds
+// the adapters to the product in its tiles.
+bool adapter_tiles(int64_t tokens, int64_t cols) { return ceil_div(tokens, 256) * ceil_div(cols, 256) >= 128; }
+
 struct AdapterSpace {
-    float* base = nullptr;  // the shared product (16-bit matrices)
-    float* v = nullptr;
+    float* base = nullptr;    // the shared product (16-bit matrices without a kernel for both)
     void* product = nullptr;
-    int64_t bytes = 0;
+    float* v = nullptr;       // backward
+    void* a_turned = nullptr; // adapters x K x rank_m, adapters x rank x N (16-bit matrices)
+    void* b_turned = nullptr;
+    float* sums = nullptr;    // the gradients' slots
+    int64_t rank_m = 0, chunk = 0, slots = 0, bytes = 0;
 };
 
-AdapterSpace adapter_space(void* workspace, int64_t tokens, int64_t cols, int64_t rank, int dtype, bool backward) {
+void product_space(AdapterSpace& s, Parts& p, int64_t tokens, int64_t cols, int dtype, bool one_kernel) {
+    if (one_kernel) return;
+    if (dtype != GEMM_F32) s.base = static_cast<float*>(p.take(tokens * cols * 4));
+    s.product = p.take(kProductWorkspace);
+}
+
+int tile_group(int64_t rows, int64_t cols) {
+    const int64_t m = ceil_div(rows, 256);
+    return (int)std::max<int64_t>(1, std::min<int64_t>(dg::default_group_m(m, ceil_div(cols, 256)), m));
+}
+
+// How the kernels for both products read x (rows x len) and w (op T: cols x len, op N: len x cols):
+// 0 not at all, 1 through registers, 2 straight to LDS.
+int tiles_form(const void* x, int64_t ldx, const void* w, int64_t ldw, int64_t cols, int64_t len, int opb, int dtype) {
+    if (dtype == GEMM_F32 || len < 8 || (opb == GEMM_OP_N && cols < 8)) return 0;
+    const bool direct = (((uintptr_t)x | (uintptr_t)w) & 15) == 0 && ldx % 8 == 0 && ldw % 8 == 0 && len % 8 == 0 &&
+                        (opb == GEMM_OP_T || cols % 8 == 0);
+    return direct ? 2 : 1;
+}
+
+// A forward call of 16-bit matrices takes one kernel for both products, of few rows or in tiles.
+bool forward_fused(int64_t tokens, int64_t N, int64_t K, int dtype) {
+    return dtype != GEMM_F32 && K > 0 && (tokens <= kSkinny || (K >= 8 && adapter_tiles(tokens, N)));
+}
+bool backward_fused(int64_t tokens, int64_t N, int64_t K, int dtype) {
+    return dtype != GEMM_F32 && N >= 8 && K >= 8 && adapter_tiles(tokens, K);
+}
+
+AdapterSpace adapter_space(void* workspace, int64_t tokens, int64_t N, int64_t K, int64_t rank, int dtype) {
     AdapterSpace s;
     Parts p{static_cast<char*>(workspace)};
-    if (dtype != GEMM_F32) s.base = static_cast<float*>(p.take(tokens * cols * 4));
-    if (backward) s.v = static_cast<float*>(p.take(tokens * rank * 4));
-    s.product = p.take(kProductWorkspace);
+    product_space(s, p, tokens, N, dtype, forward_fused(tokens, N, K, dtype));
     s.bytes = p.at;
     return s;
 }
+
+AdapterSpace adapter_backward_space(void* workspace, int64_t tokens, int64_t N, int64_t K, int64_t adapters,
+                                    int64_t rank, int dtype) {
+    AdapterSpace s;
+    Parts p{static_cast<char*>(workspace)};
+    product_space(s, p, tokens, K, dtype, backward_fused(tokens, N, K, dtype));
+    s.v = static_cast<float*>(p.take(tokens * rank * 4));
+    if (dtype != GEMM_F32) {
+        s.rank_m = ceil_div(rank, 16) * 16;
+        s.a_turned = p.take(adapters * K * s.rank_m * 2);
+        s.b_turned = p.take(adapters * N * rank * 2);
+        // chunks of 512 rows, fewer where that leaves compute units idle; at most 2^14 of them
+        s.chunk = 512;
+        while (s.chunk > 64 && ceil_div(tokens, s.chunk) * ceil_div(std::min(N, K), 64) < 512) s.chunk /= 2;
+        while (ceil_div(tokens, s.chunk) > (1 << 14)) s.chunk *= 2;
+        s.slots = adapters + ceil_div(tokens, s.chunk);
+        s.sums = static_cast<float*>(p.take(s.slots * rank * std::max(N, K) * 4));
+    }
+    s.bytes = p.at;
+    return s;
+}
+
+#define DG_BY_TYPE(name, dtype, ...) \
+    ((dtype) == GEMM_F16 ? dg::name##_f16(__VA_ARGS__) : dg::name##_bf16(__VA_ARGS__))
 
 // ---------------------------------------------------------------- loss
 constexpr int64_t kPieceBytes = (int64_t)128 << 20;
@@ -236,7 +306,7 @@ extern "C" {
 // ---------------------------------------------------------------- adapters
 int64_t gemm_adapters_workspace(int64_t tokens, int64_t N, int64_t K, int64_t rank, int dtype) {
     if (!sizes_ok({tokens, N, K, rank}) || !is_wide(dtype)) return 0;
-    return adapter_space(nullptr, tokens, N, rank, dtype, false).bytes;
+    return adapter_space(nullptr, tokens, N, K, rank, dtype).bytes;
 }
 
 int gemm_adapters_product(const void* x, int64_t tokens, int64_t K, int64_t ldx, const void* w, int64_t N, int64_t ldw,
@@ -253,7 +323,7 @@ int gemm_adapters_product(const void* x, int64_t tokens, int64_t K, int64_t ldx,
     DG_TRY(check_adapters(set, N, K));
     if (tokens == 0) return GEMM_OK;
     const int64_t es = elem_size(dtype);
-    const AdapterSpace sp = adapter_space(workspace, tokens, N, set->rank, dtype, false);
+    const AdapterSpace sp = adapter_space(workspace, tokens, N, K, set->rank, dtype);
     if (K > 0) DG_TRY(check_pointer("x", x));
     if (K > 0 && N > 0) DG_TRY(check_pointer("w", w));
     if (N > 0) DG_TRY(check_pointer("y", y));
@@ -265,7 +335,7 @@ int gemm_adapters_product(const void* x, int64_t tokens, int64_t K, int64_t ldx,
                          {range("x", x, span(tokens, K, ldx, es)), range("w", w, span(N, K, ldw, es)),
                           a_range(*set, K, es), b_range(*set, N, es), scale_of(*set),
                           range("index", index, (uint64_t)tokens * 4)}));
-    DG_TRY(check_threads("tokens * rank", tokens, set->rank, 64));
+    DG_TRY(check_adapter_threads(tokens, N, set->rank, dtype));
     DG_TRY(check_device());
     const hipStream_t s = (hipStream_t)stream;
     dg::AdapterArgs a = adapter_args(*set, tokens, index);
@@ -273,8 +343,22 @@ int gemm_adapters_product(const void* x, int64_t tokens, int64_t K, int64_t ldx,
     a.ldx = ldx;
     a.u = u;
     with_a(a, *set, K);
-    if (set->rank > 0) DG_TRY(launched(dg::launch_adapter_shrink(a, dtype, s), "adapters' first product"));
+    const bool wide = dtype == GEMM_F32;
+    if (set->rank > 0)
+        DG_TRY(launched(wide ? dg::launch_adapter_shrink(a, dtype, s) : DG_BY_TYPE(launch_adapter_shrink16, dtype, a, s),
+                        "adapters' first product"));
     if (N == 0) return GEMM_OK;
+    if (forward_fused(tokens, N, K, dtype)) {
+        with_b(a, *set, N);
+        a.scale = set->scale;
+        a.out = y;
+        a.ldo = ldy;
+        dg::AdapterProduct p{x, w, ldx, ldw, (int)N, (int)K, GEMM_OP_T,
+                             tiles_form(x, ldx, w, ldw, N, K, GEMM_OP_T, dtype) == 2};
+        return launched(tokens <= kSkinny ? DG_BY_TYPE(launch_adapter_skinny, dtype, p, a, s)
+                                          : DG_BY_TYPE(launch_adapter_tiles, dtype, p, a, tile_group(tokens, N), s),
+                        "adapters' products");
+    }
     float* base = dtype == GEMM_F32 ? static_cast<float*>(y) : sp.base;
     const int64_t ldb = dtype == GEMM_F32 ? ldy : N;
     DG_TRY(product(GEMM_OP_T, tokens, N, K, x, ldx, w, ldw, base, ldb, dtype, GEMM_F32, 0.0f, sp.product,
@@ -285,13 +369,14 @@ int gemm_adapters_product(const void* x, int64_t tokens, int64_t K, int64_t ldx,
     a.ld_base = ldb;
     a.out = y;
     a.ldo = ldy;
-    return launched(dg::launch_adapter_expand(a, dtype, s), "adapters' second product");
+    return launched(wide ? dg::launch_adapter_expand(a, dtype, s) : DG_BY_TYPE(launch_adapter_expand16, dtype, a, s),
+                    "adapters' second product");
 }
 
 int64_t gemm_adapters_backward_workspace(int64_t tokens, int64_t N, int64_t K, int64_t adapters, int64_t rank,
                                          int dtype) {
     if (!sizes_ok({tokens, N, K, adapters, rank}) || !is_wide(dtype)) return 0;
-    return adapter_space(nullptr, tokens, K, rank, dtype, true).bytes;
+    return adapter_backward_space(nullptr, tokens, N, K, adapters, rank, dtype).bytes;
 }
 
 int gemm_adapters_backward(const void* grad, int64_t tokens, int64_t N, int64_t ldg, const void* x, int64_t K,
@@ -323,12 +408,17 @@ int gemm_adapters_backward(const void* grad, int64_t tokens, int64_t N, int64_t 
                       (long long)set->adapters, (long long)tokens);
             return GEMM_ERR_INVALID_VALUE;
         }
+        if (plan->capacity > tokens) {
+            set_error("plan.capacity = %lld must be at most the %lld tokens (a plan with align 1)",
+                      (long long)plan->capacity, (long long)tokens);
+            return GEMM_ERR_INVALID_VALUE;
+        }
         DG_TRY(check_pointer("plan.offsets", plan->offsets));
         DG_TRY(check_pointer("plan.counts", plan->counts));
         if (plan->capacity > 0) DG_TRY(check_pointer("plan.rows", plan->rows));
     }
     if (tokens == 0 && !adapters) return GEMM_OK;
-    const AdapterSpace sp = adapter_space(workspace, tokens, K, set->rank, dtype, true);
+    const AdapterSpace sp = adapter_backward_space(workspace, tokens, N, K, set->adapters, set->rank, dtype);
     if (tokens > 0) {
         if (N > 0) DG_TRY(check_pointer("grad", grad));
         if (K > 0) DG_TRY(check_pointer("x", x));
@@ -352,38 +442,78 @@ int gemm_adapters_backward(const void* grad, int64_t tokens, int64_t N, int64_t 
     DG_TRY(check_device());
     const hipStream_t s = (hipStream_t)stream;
     dg::AdapterArgs a = adapter_args(*set, tokens, index);
+    const bool wide = dtype == GEMM_F32, any = set->adapters > 0 && set->rank > 0;
+    if (!wide && any && (N > 0 || K > 0)) {
+        // the adapters' other layout: a as K x rank_m for x_grad, b as rank x N for v
+        auto turn = [](const void* in, int64_t ld, int64_t stride, int64_t rows, int64_t cols, void* out, int64_t out_ld) {
+            return dg::TurnArgs{in,          ld, stride, (int)rows, (int)cols, out, (int)out_ld, (int)ceil_div(out_ld, 64),
+                                (int)ceil_div(cols, 64)};
+        };
+        const dg::TurnArgs p = turn(set->a, set->lda, set->stride_a, set->rank, x_grad ? K : 0, sp.a_turned, sp.rank_m);
+        const dg::TurnArgs q = turn(set->b, set->ldb, set->stride_b, N, set->rank, sp.b_turned, N);
+        if (p.tiles_r * p.tiles_c + q.tiles_r * q.tiles_c > 0)
+            DG_TRY(launched(dg::launch_adapter_turn(p, q, (int)set->adapters, s), "adapters' layout"));
+    }
     // v = scale grad b
     a.x = grad;
     a.ldx = ldg;
     a.u = sp.v;
     a.scale = set->scale;
     with_b(a, *set, N);
-    if (tokens > 0 && set->rank > 0) DG_TRY(launched(dg::launch_adapter_shrink(a, dtype, s), "adapters' v"));
+    if (!wide) {
+        a.m = sp.b_turned;
+        a.ldm = N;
+        a.stride_m = set->rank * N;
+        a.turned = 0;
+    }
+    if (tokens > 0 && set->rank > 0)
+        DG_TRY(launched(wide ? dg::launch_adapter_shrink(a, dtype, s) : DG_BY_TYPE(launch_adapter_shrink16, dtype, a, s),
+                        "adapters' v"));
     if (x_grad && tokens > 0 && K > 0) {
-        float* base = dtype == GEMM_F32 ? static_cast<float*>(x_grad) : sp.base;
-        const int64_t ldb = dtype == GEMM_F32 ? ldxg : K;
-        DG_TRY(product(GEMM_OP_N, tokens, K, N, grad, ldg, w, ldw, base, ldb, dtype, GEMM_F32, 0.0f, sp.product,
-                       kProductWorkspace, stream));
         with_a(a, *set, K);
+        if (!wide) {
+            a.m = sp.a_turned;
+            a.ldm = sp.rank_m;
+            a.stride_m = K * sp.rank_m;
+            a.rank_m = (int)sp.rank_m;
+            a.turned = 1;
+        }
         a.scale = nullptr;
-        a.base = base;
-        a.ld_base = ldb;
         a.out = x_grad;
         a.ldo = ldxg;
-        DG_TRY(launched(dg::launch_adapter_expand(a, dtype, s), "adapters' x_grad"));
+        if (backward_fused(tokens, N, K, dtype)) {
+            dg::AdapterProduct p{grad, w, ldg, ldw, (int)K, (int)N, GEMM_OP_N,
+                                 tiles_form(grad, ldg, w, ldw, K, N, GEMM_OP_N, dtype) == 2};
+            DG_TRY(launched(DG_BY_TYPE(launch_adapter_tiles, dtype, p, a, tile_group(tokens, K), s), "adapters' x_grad"));
+        } else {
+            float* base = wide ? static_cast<float*>(x_grad) : sp.base;
+            const int64_t ldb = wide ? ldxg : K;
+            DG_TRY(product(GEMM_OP_N, tokens, K, N, grad, ldg, w, ldw, base, ldb, dtype, GEMM_F32, 0.0f, sp.product,
+                           kProductWorkspace, stream));
+            a.base = base;
+            a.ld_base = ldb;
+            DG_TRY(launched(wide ? dg::launch_adapter_expand(a, dtype, s) : DG_BY_TYPE(launch_adapter_expand16, dtype, a, s),
+                            "adapters' x_grad"));
+        }
     }
     if (!adapters) return GEMM_OK;
     a.offsets = plan->offsets;
     a.counts = plan->counts;
     a.rows = plan->rows;
     a.capacity = (int)plan->capacity;
+    a.chunk = (int)sp.chunk;
+    a.work = sp.sums;
+    auto gradient = [&](const char* what) {
+        return launched(wide ? dg::launch_adapter_gradient(a, dtype, s)
+                             : DG_BY_TYPE(launch_adapter_gradient16, dtype, a, (int)sp.slots, s), what);
+    };
     if (K > 0) {
         a.x = x;
         a.ldx = ldx;
         a.scale = nullptr;
         with_a(a, *set, K);
         a.out = a_grad;
-        DG_TRY(launched(dg::launch_adapter_gradient(a, dtype, s), "adapters' a_grad"));
+        DG_TRY(gradient("adapters' a_grad"));
     }
     if (N > 0) {
         a.x = grad;
@@ -392,7 +522,7 @@ int gemm_adapters_backward(const void* grad, int64_t tokens, int64_t N, int64_t 
         a.scale = set->scale;
         with_b(a, *set, N);
         a.out = b_grad;
-        DG_TRY(launched(dg::launch_adapter_gradient(a, dtype, s), "adapters' b_grad"));
+        DG_TRY(gradient("adapters' b_grad"));
     }
     return GEMM_OK;
 }

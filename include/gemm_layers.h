@@ -40,7 +40,7 @@ typedef struct gemm_adapter_set {
     const void* a;            /* adapters x rank x K */
     const void* b;            /* adapters x N x rank */
     const float* scale;       /* adapters values, or NULL: all 1 */
-    int64_t adapters, rank;   /* rank 1 .. 128 (0 without adapters) */
+    int64_t adapters, rank;   /* at most 32768; rank 1 .. 128 (0 without adapters) */
     int64_t lda, stride_a;    /* >= max(1, K); between adapters, >= 0 */
     int64_t ldb, stride_b;    /* >= max(1, rank) */
 } gemm_adapter_set;
@@ -62,7 +62,7 @@ int64_t gemm_adapters_workspace(int64_t tokens, int64_t N, int64_t K, int64_t ra
  *     x_grad[t] = w^T grad[t] + a_i^T v[t]                  (tokens x K; NULL: not wanted)
  *     a_grad_i = sum over the rows t of adapter i of v[t] x[t]^T           (as a, contiguous)
  *     b_grad_i = sum over them of scale_i grad[t] u[t]^T                   (as b, contiguous)
- * plan is gemm_experts_dispatch's of index as tokens x 1 (top_k 1); an adapter without rows
+ * plan is gemm_experts_dispatch's of index as tokens x 1 (top_k 1, align 1); an adapter without rows
  * gets zeros. a_grad and b_grad come together or are both NULL. Sums are fp32 in a fixed order.
  */
 int gemm_adapters_backward(const void* grad, int64_t tokens, int64_t N, int64_t ldg, const void* x, int64_t K,

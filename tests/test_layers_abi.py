@@ -56,7 +56,7 @@ def forward(**kw):
     (INVALID, dict(set=adapters(rank=0))), (INVALID, dict(set=adapters(rank=-1))),
     (UNSUPPORTED, dict(set=adapters(rank=129))), (NULL, dict(set=adapters(a=None))),
     (NULL, dict(set=adapters(b=None))), (INVALID, dict(set=adapters(lda=63))), (INVALID, dict(set=adapters(ldb=15))),
-    (INVALID, dict(set=adapters(stride_a=-1))), (INVALID, dict(set=adapters(adapters=-1)))])
+    (INVALID, dict(set=adapters(stride_a=-1))), (INVALID, dict(set=adapters(adapters=-1))), (UNSUPPORTED, dict(set=adapters(adapters=32769)))])
 def test_adapters_refusals(want, kw):
     assert forward(**kw) == want
     assert dg.gemm_last_error()
@@ -82,7 +82,7 @@ def plan(offsets=12 * G, counts=13 * G, rows=14 * G, experts=2, tokens=8, top_k=
     (NULL, dict(plan=None)), (NULL, dict(a_grad=None)), (NULL, dict(b_grad=None)), (NULL, dict(ws=None)),
     (NULL, dict(plan=plan(offsets=None))), (NULL, dict(plan=plan(counts=None))), (NULL, dict(plan=plan(rows=None))),
     (INVALID, dict(plan=plan(experts=3))), (INVALID, dict(plan=plan(tokens=9))), (INVALID, dict(plan=plan(top_k=2))),
-    (INVALID, dict(plan=plan(capacity=-1))), (INVALID, dict(n=16)), (INVALID, dict(ldg=31)), (INVALID, dict(ldxg=63)),
+    (INVALID, dict(plan=plan(capacity=-1))), (INVALID, dict(plan=plan(capacity=9))), (INVALID, dict(n=16)), (INVALID, dict(ldg=31)), (INVALID, dict(ldxg=63)),
     (INVALID, dict(x_grad=G)), (INVALID, dict(a_grad=18 * G)), (INVALID, dict(b_grad=14 * G)), (INVALID, dict(ws=16 * G))])
 def test_adapters_backward_refusals(want, kw):
     assert backward(**kw) == want
