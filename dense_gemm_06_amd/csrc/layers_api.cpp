@@ -34,7 +34,7 @@ int check_workspace(const void* workspace, int64_t bytes, int64_t need) {
         set_error("workspace_bytes = %lld is less than the %lld that the call needs", (long long)bytes, (long long)need);
         return GEMM_ERR_INVALID_VALUE;
     }
-    if (need == 0) return GEMM_OK;
+    if (bytes == 0) return GEMM_OK;
     DG_TRY(check_pointer("workspace", workspace));
     if (((uintptr_t)workspace & 15) != 0) {
         set_error("the workspace must be 16-byte aligned (got %p)", workspace);

@@ -76,8 +76,11 @@ def _lib():
 
 
 def _work(n, device):
-    """A workspace of n bytes, which the caller keeps until the call is made."""
-    return torch.empty(n, dtype=torch.uint8, device=device)
+    """A workspace of n bytes, which the caller keeps until the call is made (None for 0), and its address."""
+    if not n:
+        return None, None
+    work = torch.empty(n, dtype=torch.uint8, device=device)
+    return work, work.data_ptr()
 
 
 def _same(t, what, dtype, shape):
@@ -130,9 +133,9 @@ def gemm_adapters_tensors(x, w, a, b, index, scale=None, keep=False):
     u = torch.empty((T, rank), dtype=torch.float32, device=dev)
     if T:
         n = _lib().gemm_adapters_workspace(T, N, K, rank, code)
-        work = _work(n, dev)
+        work, wp = _work(n, dev)
         _call("gemm_adapters_product", at, x.data_ptr(), T, K, ldx, w.data_ptr(), N, ldw, code, adapters, i,
-              y.data_ptr(), N or 1, u.data_ptr(), work.data_ptr(), n)
+              y.data_ptr(), N or 1, u.data_ptr(), wp, n)
     return (y, u) if keep else y
 
 
@@ -159,9 +162,9 @@ def gemm_adapters_backward_tensors(grad, x, u, w, a, b, index, plan, scale=None,
     ag = torch.empty((R, rank, K), dtype=x.dtype, device=dev)
     bg = torch.empty((R, N, rank), dtype=x.dtype, device=dev)
     n = _lib().gemm_adapters_backward_workspace(T, N, K, R, rank, code)
-    work = _work(n, dev)
+    work, wp = _work(n, dev)
     _call("gemm_adapters_backward", at, grad.data_ptr(), T, N, ldg, x.data_ptr(), K, ldx, up, w.data_ptr(), ldw, code,
-          adapters, i, p, xg.data_ptr() if x_grad else None, K or 1, ag.data_ptr(), bg.data_ptr(), work.data_ptr(), n)
+          adapters, i, p, xg.data_ptr() if x_grad else None, K or 1, ag.data_ptr(), bg.data_ptr(), wp, n)
     return xg, ag, bg
 
 
@@ -189,9 +192,9 @@ def gemm_loss_tensors(x, w, target):
     lse = torch.empty(T, dtype=torch.float32, device=dev)
     if T:
         n = _lib().gemm_loss_workspace(T, V, K, code)
-        work = _work(n, dev)
+        work, wp = _work(n, dev)
         _call("gemm_loss", at, x.data_ptr(), T, K, ldx, w.data_ptr(), V, ldw, code, t, loss.data_ptr(),
-              lse.data_ptr(), work.data_ptr(), n)
+              lse.data_ptr(), wp, n)
     return loss, lse
 
 
@@ -210,10 +213,10 @@ def gemm_loss_backward_tensors(grad, x, w, target, lse, x_grad=True, w_grad=True
     xg = torch.empty((T, K), dtype=x.dtype, device=dev) if x_grad else None
     wg = torch.empty((V, K), dtype=x.dtype, device=dev) if w_grad else None
     n = _lib().gemm_loss_backward_workspace(T, V, K, code, int(x_grad), int(w_grad), piece)
-    work = _work(n, dev)
+    work, wp = _work(n, dev)
     _call("gemm_loss_backward", at, g, x.data_ptr(), T, K, ldx, w.data_ptr(), V, ldw, code, t, l,
           xg.data_ptr() if x_grad else None, K or 1, wg.data_ptr() if w_grad else None, K or 1, piece,
-          work.data_ptr(), n)
+          wp, n)
     return xg, wg
 
 

@@ -49,7 +49,8 @@ def forward(**kw):
 
 @pytest.mark.parametrize("want,kw", [
     (NULL, dict(x=None)), (NULL, dict(w=None)), (NULL, dict(y=None)), (NULL, dict(u=None)), (NULL, dict(index=None)),
-    (NULL, dict(set=None)), (NULL, dict(ws=None)), (INVALID, dict(n=16)), (INVALID, dict(ws=9 * G + 4)),
+    (NULL, dict(set=None)), (NULL, dict(ws=None)), (INVALID, dict(n=16, dtype=dg.GEMM_F32)),
+    (INVALID, dict(ws=9 * G + 4)),
     (INVALID, dict(dtype=3)), (INVALID, dict(ldx=63)), (INVALID, dict(ldw=63)), (INVALID, dict(ldy=31)),
     (INVALID, dict(T=-1)), (UNSUPPORTED, dict(T=1 << 31)), (UNSUPPORTED, dict(K=1 << 31)), (INVALID, dict(y=G)),
     (INVALID, dict(u=7 * G + 16)), (INVALID, dict(ws=2 * G)), (INVALID, dict(u=4 * G)), (INVALID, dict(y=6 * G)),
