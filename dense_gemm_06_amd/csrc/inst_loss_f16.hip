@@ -1,0 +1,16 @@
+// The loss's kernels for fp16.
+#define DG_DT dg::DT_F16
+#define DG_SUFFIX f16
+#include "inst_loss.inc"
+
+namespace dg {
+
+int launch_loss_finish(const void* part, int strips, int tokens, const int64_t* target, int vocabulary,
+                       const float* picked, float* loss, float* lse, hipStream_t s) {
+    int width = 1;
+    while (width < 64 && width < tokens) width *= 2;
+    return launch_status(loss_finish, dim3((unsigned)((tokens + width - 1) / width)), dim3(1024), s,
+                         static_cast<const LossPart*>(part), strips, tokens, width, target, vocabulary, picked, loss, lse);
+}
+
+}  // namespace dg

@@ -1,0 +1,263 @@
+// kernel_loss.h -- the loss over a vocabulary for fp16 and bf16: products whose epilogue turns a
+// tile of logits into what is kept of it, so that no logits are stored.
+//
+// Forward: of each row and tile the maximum m and s = sum exp(l - m). A lane holds 32 logits of
+// one row, so they take two passes over registers and one exchange; the four waves along a row
+// are joined in LDS. Backward: d = (exp(l - lse) - [target]) grad, rounded to the matrices' type
+// (fp16 after a power of two that keeps it in range), stored by rows for the product with w and
+// turned for the product with x.
+#pragma once
+#include "device_common.h"
+#include "kernel_skinny.h"
+#include "kernel_sp.h"
+#include "layers.h"
+
+namespace dg {
+
+constexpr float kLog2e = 1.44269504f;
+
+// (m, s) joined with (m2, s2); a part without anything is (-inf, 0). Equal infinities count 1.
+__device__ __forceinline__ void loss_join(float& m, float& s, float m2, float s2) {
+    const float M = fmaxf(m, m2);
+    const float a = m == M ? 1.0f : __builtin_amdgcn_exp2f((m - M) * kLog2e);
+    const float b = m2 == M ? 1.0f : __builtin_amdgcn_exp2f((m2 - M) * kLog2e);
+    s = s * a + s2 * b;
+    m = M;
+}
+
+struct LossPart {
+    float m, s;
+};
+
+struct LossStatsHook {
+    static constexpr bool kReplace = true, kAdd = false;
+    const int64_t* target;
+    LossPart* part;   // strips x tokens
+    float* picked;
+    int tokens, n;    // columns
+
+    template <int SJ>
+    __device__ __forceinline__ void finish(f32x16 (&acc)[4][SJ], int m0, int n0, int wm, int wn, char* lds, char*) const {
+        const int lane = threadIdx.x & 63, l32 = lane & 31, lh = lane >> 5;
+        LossPart* joined = reinterpret_cast<LossPart*>(lds);  // waves along n x 256 rows
+        const bool cut = n0 + 32 * SJ > n;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int row = m0 + 32 * i + l32;
+            float m = -INFINITY, s = 0.0f;
+            if (cut) {
+#pragma unroll
+                for (int j = 0; j < SJ; ++j)
+#pragma unroll
+                    for (int r = 0; r < 16; ++r)
+                        if (n0 + 32 * j + 8 * (r / 4) + 4 * lh + r % 4 >= n) acc[i][j][r] = -INFINITY;
+            }
+#pragma unroll
+            for (int j = 0; j < SJ; ++j)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) m = fmaxf(m, acc[i][j][r]);
+            if (__any(!(fabsf(m) < INFINITY))) {
+#pragma unroll
+                for (int j = 0; j < SJ; ++j)
+#pragma unroll
+                    for (int r = 0; r < 16; ++r)
+                        s += acc[i][j][r] == m ? 1.0f : __builtin_amdgcn_exp2f((acc[i][j][r] - m) * kLog2e);
+            } else {
+                const float c = -m * kLog2e;
+#pragma unroll
+                for (int j = 0; j < SJ; ++j)
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) s += __builtin_amdgcn_exp2f(fmaf(acc[i][j][r], kLog2e, c));
+            }
+            const int64_t at = row < tokens ? target[row] - n0 : -1;
+            const bool has = at >= 0 && at < 32 * SJ;
+            if (__any(has)) {
+                const int t = has ? (int)at - 4 * lh : -1;
+                float v = 0.0f;
+                bool mine = false;
+#pragma unroll
+                for (int j = 0; j < SJ; ++j)
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) {
+                        const bool hit = t == 32 * j + 8 * (r / 4) + r % 4;
+                        v = hit ? acc[i][j][r] : v;
+                        mine = mine || hit;
+                    }
+                if (mine && n0 + at < n) picked[row] = v;
+            }
+            loss_join(m, s, __shfl_xor(m, 32), __shfl_xor(s, 32));
+            if (lh == 0) joined[wn * 256 + wm * 128 + 32 * i + l32] = {m, s};
+        }
+        __syncthreads();
+        const int r = threadIdx.x, row = m0 - wm * 128 + r;
+        if (r < 256 && row < tokens) {
+            float m = joined[r].m, s = joined[r].s;
+#pragma unroll
+            for (int w = 1; w < 8 / SJ; ++w) loss_join(m, s, joined[w * 256 + r].m, joined[w * 256 + r].s);
+            part[(size_t)((n0 - wn * 32 * SJ) >> 8) * (size_t)tokens + row] = {m, s};
+        }
+    }
+};
+
+// The same of up to 64 rows: a strip is 16 columns.
+struct LossSkinnyEpi {
+    const int64_t* target;
+    LossPart* part;
+    float* picked;
+    int tokens, n;
+    __device__ __forceinline__ void operator()(int t, int c, f32x4 v) const {
+        const int left = n - c;
+        float m = -INFINITY, s = 0.0f;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            v[e] = e < left ? v[e] : -INFINITY;
+            m = fmaxf(m, v[e]);
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s += v[e] == m ? 1.0f : __builtin_amdgcn_exp2f((v[e] - m) * kLog2e);
+        const int64_t at = t < tokens ? target[t] - c : -1;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (at == e && e < left) picked[t] = v[e];
+#pragma unroll
+        for (int d = 16; d < 64; d <<= 1) loss_join(m, s, __shfl_xor(m, d), __shfl_xor(s, d));
+        if (t < tokens && (threadIdx.x & 63) < 16) part[(size_t)(c >> 4) * (size_t)tokens + t] = {m, s};
+    }
+};
+
+// Joins the strips of each row. A workgroup has `width` tokens (a power of two up to 64) and as
+// many threads to each as are left.
+static __global__ __launch_bounds__(1024) void loss_finish(const LossPart* part, int strips, int tokens, int width,
+                                                           const int64_t* target, int vocabulary, const float* picked,
+                                                           float* loss, float* lse) {
+    __shared__ LossPart buf[1024];
+    const int tid = threadIdx.x, t = (int)blockIdx.x * width + (tid & (width - 1)), groups = 1024 / width;
+    float m = -INFINITY, s = 0.0f;
+    if (t < tokens)
+#pragma unroll 4
+        for (int k = tid / width; k < strips; k += groups) {
+            const LossPart p = part[(size_t)k * (size_t)tokens + t];
+            loss_join(m, s, p.m, p.s);
+        }
+    buf[tid] = {m, s};
+    for (int half = 512; half >= width; half >>= 1) {
+        __syncthreads();
+        if (tid < half) {
+            loss_join(m, s, buf[tid + half].m, buf[tid + half].s);
+            buf[tid] = {m, s};
+        }
+    }
+    if (tid >= width || t >= tokens) return;
+    const float l = m + logf(s);
+    const int64_t k = target[t];
+    lse[t] = l;
+    loss[t] = k >= 0 && k < vocabulary ? l - picked[t] : 0.0f;
+}
+
+// d of a tile through LDS as 16-bit rows of 256: row r of a half of 128 at byte 512 r, its 16-byte
+// pieces permuted by r, so that neither the writes (32 rows of one piece) nor the whole-row reads
+// meet in a bank.
+template <int DT>
+struct LossGradHook {
+    static constexpr bool kReplace = true, kAdd = false;
+    const int64_t* target;
+    const float* lse;
+    const float* grad;
+    const float* factor;   // or NULL
+    uint16_t* d;           // tokens x n, or NULL
+    uint16_t* dt;          // n x lddt, or NULL
+    int64_t ldd, lddt;
+    int tokens, n, v0, vocabulary;
+
+    template <int SJ>
+    __device__ __forceinline__ void finish(f32x16 (&acc)[4][SJ], int m0, int n0, int wm, int wn, char* lds,
+                                           char* lds2) const {
+        const int lane = threadIdx.x & 63, l32 = lane & 31, lh = lane >> 5;
+        char* half = wm == 0 ? lds : lds2;
+        const float f = factor ? factor[0] : 1.0f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int row = m0 + 32 * i + l32, r = 32 * i + l32;
+            int64_t at = -1;
+            float g = 0.0f, c = 0.0f;
+            if (row < tokens) {
+                at = target[row];
+                if (at >= 0 && at < vocabulary) {
+                    g = grad[row] * f;
+                    c = -lse[row] * kLog2e;
+                    at -= (int64_t)v0 + n0;
+                } else {
+                    at = -1;
+                }
+            }
+            const bool live = g != 0.0f;  // a NaN is live
+            const int t = at >= 0 && at < 32 * SJ ? (int)at - 4 * lh : -1;
+#pragma unroll
+            for (int j = 0; j < SJ; ++j) {
+                asm volatile("" : "+a"(acc[i][j]));
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    uint32_t h[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float p = __builtin_amdgcn_exp2f(fmaf(acc[i][j][4 * q + e], kLog2e, c));
+                        const float v = live ? (p - (t == 32 * j + 8 * q + e ? 1.0f : 0.0f)) * g : 0.0f;
+                        h[e] = DT == DT_F16 ? (uint32_t)__builtin_bit_cast(uint16_t, (_Float16)v)
+                                            : (uint32_t)f32_to_bf16_rne(v);
+                    }
+                    const int piece = wn * (4 * SJ) + 4 * j + q;
+                    *reinterpret_cast<u32x2*>(half + r * 512 + ((piece ^ (r & 31)) << 4) + 8 * lh) =
+                        u32x2{h[0] | (h[1] << 16), h[2] | (h[3] << 16)};
+                }
+            }
+        }
+        __syncthreads();
+        const int wave = threadIdx.x >> 6, tile_m = m0 - wm * 128, tile_n = n0 - wn * 32 * SJ;
+        if (d) {
+            const int c = tile_n + 8 * l32, left = n - c;
+            for (int it = 0; it < 16; ++it) {
+                const int r = wave * 32 + 2 * it + lh, row = tile_m + r, rr = r & 127;
+                if (row >= tokens || left <= 0) continue;
+                const u32x4 v = *reinterpret_cast<const u32x4*>((r < 128 ? lds : lds2) + rr * 512 + ((l32 ^ (rr & 31)) << 4));
+                uint16_t* dst = d + (size_t)row * (size_t)ldd + c;
+                if (left >= 8) __builtin_memcpy(dst, &v, 16);
+                else
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        if (e < left) dst[e] = (uint16_t)(v[e >> 1] >> (16 * (e & 1)));
+            }
+        }
+        if (dt) {
+            // a wave: 32 columns, 32 rows at a time: 16 lanes get eight rows of 16 columns
+            const int l16 = lane & 15, lg = lane >> 4;
+#pragma unroll 2
+            for (int it = 0; it < 16; ++it) {
+                const int cb = wave * 32 + 16 * (it & 1), rb = 32 * (it >> 1) + 8 * lg;
+                u32x4 v;
+#pragma unroll
+                for (int hh = 0; hh < 2; ++hh) {
+                    const int r = rb + 4 * hh + (l16 >> 2), rr = r & 127, col = cb + 4 * (l16 & 3);
+                    char* p = (r < 128 ? lds : lds2) + rr * 512 + (((col >> 3) ^ (rr & 31)) << 4) + (col & 7) * 2;
+                    const u32x2 x = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4f16(DG_LDS_PTR(fp16x4_t, p)));
+                    v[2 * hh] = x[0];
+                    v[2 * hh + 1] = x[1];
+                }
+                const int c = tile_n + cb + l16, row = tile_m + rb;
+                if (c < n && row < lddt) __builtin_memcpy(dt + (size_t)c * (size_t)lddt + row, &v, 16);
+            }
+        }
+    }
+};
+
+template <int DT, bool REG>
+__global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) void loss_tiles(GemmArgs g, LossStatsHook h) {
+    mfma32_sp_body<DT, 1, 8, REG, false, false>(g, nullptr, h);
+}
+
+template <int DT, bool REG>
+__global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) void loss_grad_tiles(GemmArgs g,
+                                                                                                 LossGradHook<DT> h) {
+    mfma32_sp_body<DT, 1, 8, REG, false, false>(g, nullptr, h);
+}
+
+}  // namespace dg

@@ -10,6 +10,11 @@
 
 namespace dg {
 
+// A launcher of each 16-bit type.
+#define DG_16BIT(name, params)                                    \
+    int name##_f16 params;                                             \
+    int name##_bf16 params;
+
 constexpr int kMaxRank = 128;
 constexpr int kMaxAdapters = 32768;  // of a grid's second direction, with room for the chunks of their rows
 
@@ -53,6 +58,22 @@ struct LossArgs {
     void* dt;
     int64_t lddt;
 };
+
+// Fused forms for 16-bit matrices: x tokens x K, w (its rows from v0 on) n x K. `direct`: rows of
+// whole 16-byte pieces, 16-byte aligned.
+struct LossProduct {
+    const void* x;
+    const void* w;
+    int64_t ldx, ldw;
+    int tokens, n, K, group_m, direct;
+};
+struct LossPart;            // a row's maximum and sum over a strip of 256 columns (16 for up to 64 rows)
+constexpr int64_t kLossPartBytes = 8;
+DG_16BIT(launch_loss_skinny, (const LossProduct& p, const int64_t* target, void* part, float* picked, hipStream_t s))
+DG_16BIT(launch_loss_tiles, (const LossProduct& p, const int64_t* target, void* part, float* picked, hipStream_t s))
+DG_16BIT(launch_loss_grad_tiles, (const LossProduct& p, const LossArgs& a, hipStream_t s))
+int launch_loss_finish(const void* part, int strips, int tokens, const int64_t* target, int vocabulary,
+                       const float* picked, float* loss, float* lse, hipStream_t s);
 
 int launch_loss_stats(const LossArgs& a, hipStream_t s);
 int launch_loss_grad(const LossArgs& a, int dtype, hipStream_t s);
@@ -110,9 +131,6 @@ struct TurnArgs {
 
 // 16-bit matrices, on the matrix instructions, one function for each type:
 // out = x w + scale u m in one kernel, for up to 64 tokens (x w^T only) or in 256 x 256 tiles
-#define DG_16BIT(name, params)                                    \
-    int name##_f16 params;                                             \
-    int name##_bf16 params;
 DG_16BIT(launch_adapter_skinny, (const AdapterProduct& p, const AdapterArgs& a, hipStream_t s))
 DG_16BIT(launch_adapter_tiles, (const AdapterProduct& p, const AdapterArgs& a, int group_m, hipStream_t s))
 // the operators below, m with its long direction along memory in shrink and across it in expand

@@ -222,6 +222,7 @@ int64_t piece_of(int64_t tokens, int64_t vocabulary, int64_t each) {
 }
 
 struct LossSpace {
+    void* part = nullptr;   // fused: maxima and sums of strips
     float* logits = nullptr;
     float* top = nullptr;
     float* sum = nullptr;
@@ -235,9 +236,19 @@ struct LossSpace {
     int64_t piece = 0, lddt = 0, bytes = 0;
 };
 
-LossSpace loss_space(void* workspace, int64_t tokens, int64_t vocabulary) {
+// 16-bit logits are never stored but for the shortest sums.
+bool loss_fused(int64_t vocabulary, int64_t K, int dtype) { return dtype != GEMM_F32 && K >= 8 && vocabulary > 0; }
+int64_t loss_strip(int64_t tokens) { return tokens <= kSkinny ? 16 : 256; }
+
+LossSpace loss_space(void* workspace, int64_t tokens, int64_t vocabulary, int64_t K, int dtype) {
     LossSpace s;
     Parts p{static_cast<char*>(workspace)};
+    if (loss_fused(vocabulary, K, dtype)) {
+        s.part = p.take(ceil_div(vocabulary, loss_strip(tokens)) * tokens * dg::kLossPartBytes);
+        s.picked = static_cast<float*>(p.take(tokens * 4));
+        s.bytes = p.at;
+        return s;
+    }
     s.piece = piece_of(tokens, vocabulary, 4);
     s.logits = static_cast<float*>(p.take(tokens * s.piece * 4));
     s.top = static_cast<float*>(p.take(tokens * 4));
@@ -253,10 +264,10 @@ LossSpace loss_backward_space(void* workspace, int64_t tokens, int64_t vocabular
     LossSpace s;
     Parts p{static_cast<char*>(workspace)};
     const int64_t es = elem_size(dtype);
-    s.piece = piece > 0 ? std::min(piece, std::max<int64_t>(1, vocabulary)) : piece_of(tokens, vocabulary, 4 + 2 * es);
+    s.piece = piece > 0 ? std::min(piece, std::max<int64_t>(1, vocabulary)) : piece_of(tokens, vocabulary, loss_fused(vocabulary, K, dtype) ? 2 * es : 4 + 2 * es);
     s.lddt = (tokens + 31) / 32 * 32;
     s.factor = static_cast<float*>(p.take(8));
-    s.logits = static_cast<float*>(p.take(tokens * s.piece * 4));
+    if (!loss_fused(vocabulary, K, dtype)) s.logits = static_cast<float*>(p.take(tokens * s.piece * 4));
     if (x_grad) s.d = p.take(tokens * s.piece * es);
     if (w_grad) s.dt = p.take(s.piece * s.lddt * es);
     if (x_grad && dtype != GEMM_F32) s.x_acc = static_cast<float*>(p.take(tokens * K * 4));
@@ -264,6 +275,12 @@ LossSpace loss_backward_space(void* workspace, int64_t tokens, int64_t vocabular
     s.product = p.take(kProductWorkspace);
     s.bytes = p.at;
     return s;
+}
+
+dg::LossProduct loss_product(const void* x, int64_t ldx, const void* w, int64_t ldw, int64_t tokens, int64_t n,
+                             int64_t K, int dtype) {
+    return {x, w, ldx, ldw, (int)tokens, (int)n, (int)K, tile_group(tokens, n),
+            tiles_form(x, ldx, w, ldw, n, K, GEMM_OP_T, dtype) == 2};
 }
 
 // ---------------------------------------------------------------- activations
@@ -530,7 +547,7 @@ int gemm_adapters_backward(const void* grad, int64_t tokens, int64_t N, int64_t 
 // ---------------------------------------------------------------- loss
 int64_t gemm_loss_workspace(int64_t tokens, int64_t vocabulary, int64_t K, int dtype) {
     if (!sizes_ok({tokens, vocabulary, K}) || !is_wide(dtype)) return 0;
-    return loss_space(nullptr, tokens, vocabulary).bytes;
+    return loss_space(nullptr, tokens, vocabulary, K, dtype).bytes;
 }
 
 int gemm_loss(const void* x, int64_t tokens, int64_t K, int64_t ldx, const void* w, int64_t vocabulary, int64_t ldw,
@@ -545,7 +562,7 @@ int gemm_loss(const void* x, int64_t tokens, int64_t K, int64_t ldx, const void*
     DG_TRY(check_ld("ldw", ldw, K));
     if (tokens == 0) return GEMM_OK;
     const int64_t es = elem_size(dtype);
-    const LossSpace sp = loss_space(workspace, tokens, vocabulary);
+    const LossSpace sp = loss_space(workspace, tokens, vocabulary, K, dtype);
     if (K > 0) DG_TRY(check_pointer("x", x));
     if (K > 0 && vocabulary > 0) DG_TRY(check_pointer("w", w));
     DG_TRY(check_pointer("target", target));
@@ -558,7 +575,18 @@ int gemm_loss(const void* x, int64_t tokens, int64_t K, int64_t ldx, const void*
                          {range("x", x, span(tokens, K, ldx, es)), range("w", w, span(vocabulary, K, ldw, es)),
                           range("target", target, n4 * 2)}));
     DG_TRY(check_threads("tokens", tokens, 1, 256));
+    DG_TRY(check_threads("tiles of tokens * vocabulary", ceil_div(tokens, 256),
+                         ceil_div(vocabulary, loss_strip(tokens)), 512));
     DG_TRY(check_device());
+    if (sp.part) {
+        const hipStream_t s = (hipStream_t)stream;
+        const dg::LossProduct p = loss_product(x, ldx, w, ldw, tokens, vocabulary, K, dtype);
+        DG_TRY(launched(tokens <= kSkinny ? DG_BY_TYPE(launch_loss_skinny, dtype, p, target, sp.part, sp.picked, s)
+                                          : DG_BY_TYPE(launch_loss_tiles, dtype, p, target, sp.part, sp.picked, s),
+                        "loss"));
+        return launched(dg::launch_loss_finish(sp.part, (int)ceil_div(vocabulary, loss_strip(tokens)), (int)tokens,
+                                               target, (int)vocabulary, sp.picked, loss, lse, s), "loss");
+    }
     dg::LossArgs a;
     memset(&a, 0, sizeof a);
     a.logits = sp.logits;
@@ -652,9 +680,14 @@ int gemm_loss_backward(const float* grad, const void* x, int64_t tokens, int64_t
         a.v0 = (int)v0;
         const char* wp = static_cast<const char*>(w) + (size_t)v0 * ldw * es;
         if (tokens > 0 && a.n > 0) {
-            DG_TRY(product(GEMM_OP_T, tokens, a.n, K, x, ldx, wp, ldw, sp.logits, a.ld, dtype, GEMM_F32, 0.0f,
-                           sp.product, kProductWorkspace, stream));
-            DG_TRY(launched(dg::launch_loss_grad(a, dtype, s), "loss gradient"));
+            if (sp.logits) {
+                DG_TRY(product(GEMM_OP_T, tokens, a.n, K, x, ldx, wp, ldw, sp.logits, a.ld, dtype, GEMM_F32, 0.0f,
+                               sp.product, kProductWorkspace, stream));
+                DG_TRY(launched(dg::launch_loss_grad(a, dtype, s), "loss gradient"));
+            } else {
+                const dg::LossProduct p = loss_product(x, ldx, wp, ldw, tokens, a.n, K, dtype);
+                DG_TRY(launched(DG_BY_TYPE(launch_loss_grad_tiles, dtype, p, a, s), "loss gradient"));
+            }
         }
         if (x_grad)
             DG_TRY(product(GEMM_OP_N, tokens, K, a.n, sp.d, a.ldd, wp, ldw, xa, ldxa, dtype, GEMM_F32,

@@ -69,9 +69,10 @@ __global__ __launch_bounds__(256) void loss_grad(LossArgs a, int tiles_n) {
         float d = 0.0f;
         if (t < a.tokens && j < a.n) {
             const int64_t target = a.target[t];
-            if (target >= 0 && target < a.vocabulary) {
+            const float g = a.factor ? a.grad[t] * a.factor[0] : a.grad[t];
+            if (target >= 0 && target < a.vocabulary && g != 0.0f) {
                 const float p = __expf(a.logits[(size_t)t * (size_t)a.ld + j] - a.lse_in[t]);
-                d = (p - (target == a.v0 + j ? 1.0f : 0.0f)) * (a.factor ? a.grad[t] * a.factor[0] : a.grad[t]);
+                d = (p - (target == a.v0 + j ? 1.0f : 0.0f)) * g;
             }
             if (a.d) store_out(a.d, DT, (size_t)t * (size_t)a.ldd + j, d);
         }
