@@ -37,23 +37,23 @@ __device__ __forceinline__ void load_f8(float (&v)[8], const float* p, int valid
     }
 }
 
-// v as hi + lo; an infinite or NaN v is all in hi.
+// x as hi + lo; an infinite or NaN x is all in hi.
+template <int DT>
+__device__ __forceinline__ void split_one(float x, uint16_t& hi, uint16_t& lo) {
+    hi = DT == DT_F16 ? __builtin_bit_cast(uint16_t, (_Float16)x) : f32_to_bf16_rne(x);
+    float rest = x - decode<DT>(hi);
+    rest = fabsf(rest) < INFINITY ? rest : 0.0f;
+    lo = DT == DT_F16 ? __builtin_bit_cast(uint16_t, (_Float16)rest) : f32_to_bf16_rne(rest);
+}
 template <int DT>
 __device__ __forceinline__ void split_hi_lo(const float (&v)[8], u32x4& hi, u32x4& lo) {
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-        uint32_t h[2], l[2];
+        uint16_t h[2], l[2];
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            const float x = v[2 * e + k];
-            const uint16_t b = DT == DT_F16 ? __builtin_bit_cast(uint16_t, (_Float16)x) : f32_to_bf16_rne(x);
-            float rest = x - decode<DT>(b);
-            rest = fabsf(rest) < INFINITY ? rest : 0.0f;
-            h[k] = b;
-            l[k] = DT == DT_F16 ? __builtin_bit_cast(uint16_t, (_Float16)rest) : f32_to_bf16_rne(rest);
-        }
-        hi[e] = h[0] | (h[1] << 16);
-        lo[e] = l[0] | (l[1] << 16);
+        for (int k = 0; k < 2; ++k) split_one<DT>(v[2 * e + k], h[k], l[k]);
+        hi[e] = (uint32_t)h[0] | ((uint32_t)h[1] << 16);
+        lo[e] = (uint32_t)l[0] | ((uint32_t)l[1] << 16);
     }
 }
 
@@ -75,34 +75,56 @@ __device__ __forceinline__ f32x4 mfma_16(u32x4 p, u32x4 q, f32x4 c) {
 }
 
 // acc[j] += scale u m^T for rows m0 .. m0 + 31 and columns n0 + 32 j .. + 31 (m: columns x rank).
-// Lane l holds row m0 + l % 32; register r column 8 (r / 4) + 4 (l / 32) + r % 4 of a subtile.
+// Lane l holds row m0 + l % 32; register r column 8 (r / 4) + 4 (l / 32) + r % 4 of a subtile. Of
+// the adapters among the rows, every parts-th one from the part-th on.
 template <int DT, int SJ>
-__device__ __forceinline__ void adapter_add(f32x16 (&acc)[SJ], int m0, int n0, const AdapterArgs& a) {
+__device__ __forceinline__ void adapter_add(f32x16 (&acc)[SJ], int m0, int n0, const AdapterArgs& a, int part = 0,
+                                            int parts = 1) {
     const int lane = threadIdx.x & 63, l32 = lane & 31, lh = lane >> 5;
     const int row = m0 + l32;
     int mine = row < a.tokens ? a.index[row] : -1;
     if (mine >= a.adapters) mine = -1;
+    const uint16_t* us = a.us + (size_t)min(row, a.tokens - 1) * (size_t)(2 * a.rank_p) + 8 * lh;
+    const uint16_t* cols[SJ];
+#pragma unroll
+    for (int j = 0; j < SJ; ++j)
+        cols[j] = static_cast<const uint16_t*>(a.m) + (size_t)min(n0 + 32 * j + l32, a.cols - 1) * (size_t)a.ldm + 8 * lh;
     uint64_t todo = __ballot(mine >= 0);
-    while (todo) {
+    for (int turn = 0; todo; ++turn) {
         const int i = __builtin_amdgcn_readlane(mine, (int)__builtin_ctzll(todo));
         const bool here = mine == i;
-        const float scale = a.scale ? a.scale[i] : 1.0f;
-        const uint16_t* m = static_cast<const uint16_t*>(a.m) + (size_t)i * (size_t)a.stride_m;
+        todo &= ~__ballot(here);
+        if (turn % parts != part) continue;
+        const size_t at = (size_t)i * (size_t)a.stride_m;
         f32x16 d[SJ];
 #pragma unroll
         for (int j = 0; j < SJ; ++j) d[j] = f32x16{};
-        for (int r0 = 0; r0 < a.rank; r0 += 16) {
-            const int r = r0 + 8 * lh;
-            float v[8];
-            load_f8(v, a.u + (size_t)row * (size_t)a.rank + r, here ? a.rank - r : 0);
+        int r = 0;
+        // whole pieces of 32: the loads of both halves before the first product
+        for (; r + 32 <= a.rank_m; r += 32) {
+            u32x4 hi[2], lo[2], p[2][SJ];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] *= scale;
+            for (int h = 0; h < 2; ++h) {
+                __builtin_memcpy(&hi[h], us + r + 16 * h, 16);
+                __builtin_memcpy(&lo[h], us + a.rank_p + r + 16 * h, 16);
+#pragma unroll
+                for (int j = 0; j < SJ; ++j) __builtin_memcpy(&p[h][j], cols[j] + at + r + 16 * h, 16);
+            }
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int j = 0; j < SJ; ++j) {
+                    d[j] = mfma_32<DT>(p[h][j], hi[h], d[j]);
+                    d[j] = mfma_32<DT>(p[h][j], lo[h], d[j]);
+                }
+        }
+        for (; r < a.rank; r += 16) {
             u32x4 hi, lo;
-            split_hi_lo<DT>(v, hi, lo);
+            __builtin_memcpy(&hi, us + r, 16);
+            __builtin_memcpy(&lo, us + a.rank_p + r, 16);
 #pragma unroll
             for (int j = 0; j < SJ; ++j) {
-                const int col = n0 + 32 * j + l32;
-                const u32x4 p = load_frag8(m + (size_t)col * (size_t)a.ldm + r, col < a.cols ? a.rank_m - r : 0);
+                const u32x4 p = load_frag8(cols[j] + at + r, a.rank_m - r - 8 * lh);
                 d[j] = mfma_32<DT>(p, hi, d[j]);
                 d[j] = mfma_32<DT>(p, lo, d[j]);
             }
@@ -111,7 +133,6 @@ __device__ __forceinline__ void adapter_add(f32x16 (&acc)[SJ], int m0, int n0, c
         for (int j = 0; j < SJ; ++j)
 #pragma unroll
             for (int e = 0; e < 16; ++e) acc[j][e] += here ? d[j][e] : 0.0f;
-        todo &= ~__ballot(here);
     }
 }
 
@@ -134,81 +155,120 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
 }
 
 // ---------------------------------------------------------------- second product on its own
-// out = base + scale u m^T; a wave has 32 rows x 64 columns.
+// out = base + scale u m^T, 32 rows x 64 columns to a workgroup, whose four waves share the adapters
+// among the rows and are joined in LDS in their order.
 template <int DT>
 __global__ __launch_bounds__(256) void adapter_expand16(AdapterArgs a, int tiles_n) {
+    __shared__ __attribute__((aligned(16))) float sums[4][32][68];
     const int tm = (int)blockIdx.x / tiles_n, tn = (int)blockIdx.x - tm * tiles_n;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int m0 = tm * 32, n0 = tn * 256 + wave * 64;
-    const int row = m0 + (lane & 31), lh = lane >> 5;
-    f32x16 acc[2];
-    const float* base = a.base + (size_t)min(row, a.tokens - 1) * (size_t)a.ld_base;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, l32 = lane & 31, lh = lane >> 5;
+    const int m0 = tm * 32, n0 = tn * 64;
+    f32x16 acc[2] = {f32x16{}, f32x16{}};
+    adapter_add<DT, 2>(acc, m0, n0, a, wave, 4);
 #pragma unroll
     for (int j = 0; j < 2; ++j)
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            const int c = n0 + 32 * j + 8 * q + 4 * lh;
-            float v[4] = {0.f, 0.f, 0.f, 0.f};
-            if (c + 3 < a.cols) __builtin_memcpy(v, base + c, 16);
-            else
+        for (int q = 0; q < 4; ++q)
+            *reinterpret_cast<f32x4*>(&sums[wave][l32][32 * j + 8 * q + 4 * lh]) =
+                f32x4{acc[j][4 * q], acc[j][4 * q + 1], acc[j][4 * q + 2], acc[j][4 * q + 3]};
+    __syncthreads();
+    const int c = n0 + (threadIdx.x & 15) * 4, left = a.cols - c;
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    if (c + e < a.cols) v[e] = base[c + e];
+    for (int h = 0; h < 2; ++h) {
+        const int r = (threadIdx.x >> 4) + 16 * h, row = m0 + r;
+        if (row >= a.tokens || left <= 0) continue;
+        const float* base = a.base + (size_t)row * (size_t)a.ld_base + c;
+        f32x4 v = {0.f, 0.f, 0.f, 0.f};
+        if (left >= 4) __builtin_memcpy(&v, base, 16);
+        else
 #pragma unroll
-            for (int e = 0; e < 4; ++e) acc[j][4 * q + e] = v[e];
-        }
-    adapter_add<DT, 2>(acc, m0, n0, a);
-    if (row >= a.tokens) return;
+            for (int e = 0; e < 4; ++e)
+                if (e < left) v[e] = base[e];
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
+        for (int w = 0; w < 4; ++w) v += *reinterpret_cast<const f32x4*>(&sums[w][r][(threadIdx.x & 15) * 4]);
+        const size_t at = (size_t)row * (size_t)a.ldo + c;
+        if (left >= 4) store_out4(a.out, DT, at, v);
+        else
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            const int c = n0 + 32 * j + 8 * q + 4 * lh;
-            const size_t at = (size_t)row * (size_t)a.ldo + c;
-            const f32x4 v = {acc[j][4 * q], acc[j][4 * q + 1], acc[j][4 * q + 2], acc[j][4 * q + 3]};
-            if (c + 3 < a.cols) store_out4(a.out, DT, at, v);
-            else
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    if (c + e < a.cols) store_out(a.out, DT, at + e, v[e]);
-        }
+            for (int e = 0; e < 4; ++e)
+                if (e < left) store_out(a.out, DT, at + e, v[e]);
+    }
 }
 
 // ---------------------------------------------------------------- first product
-// A wave: one token and one of its rank numbers, 8 elements to a lane and step. For few tokens,
-// whose adapters mostly differ.
+// A wave: four rank numbers of one token, 8 elements to a lane and step. For tokens few enough
+// that each can read its adapter by itself: u and, where wanted, us (see adapter_shrink_finish).
 template <int DT>
-__global__ __launch_bounds__(256) void adapter_shrink_row(AdapterArgs a) {
-    const int64_t unit = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-    const int lane = threadIdx.x & 63;
-    if (unit >= (int64_t)a.tokens * a.rank) return;
-    const int t = (int)(unit / a.rank), j = (int)(unit - (int64_t)t * a.rank);
+__device__ __forceinline__ void adapter_shrink_wave(const AdapterArgs& a, int64_t unit) {
+    const int lane = threadIdx.x & 63, each = a.rank_p >> 2;
+    if (unit >= (int64_t)a.tokens * each) return;
+    const int t = (int)(unit / each), j = (int)(unit - (int64_t)t * each) * 4;
+    if (j >= a.rank && a.us == nullptr) return;
     const int i = a.index[t];
-    float sum = 0.0f;
-    if (i >= 0 && i < a.adapters) {
+    float sum[4] = {0.f, 0.f, 0.f, 0.f};
+    float scale = 1.0f;
+    if (i >= 0 && i < a.adapters && j < a.rank) {
         const uint16_t* x = static_cast<const uint16_t*>(a.x) + (size_t)t * (size_t)a.ldx;
-        const uint16_t* m = static_cast<const uint16_t*>(a.m) + (size_t)i * (size_t)a.stride_m + (size_t)j * (size_t)a.ldm;
-#pragma unroll 4
-        for (int64_t k = lane * 8; k < a.cols; k += 512) {
-            const int valid = (int)min((int64_t)8, a.cols - k);
-            const u32x4 p = load_frag8(x + k, valid), q = load_frag8(m + k, valid);
+        const uint16_t* m[4];
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+            m[r] = static_cast<const uint16_t*>(a.m) + (size_t)i * (size_t)a.stride_m +
+                   (size_t)min(j + r, a.rank - 1) * (size_t)a.ldm;
+        auto add = [&](u32x4 p, u32x4 q, float& s) {
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                sum = fmaf(decode<DT>((uint16_t)p[e]), decode<DT>((uint16_t)q[e]), sum);
-                sum = fmaf(decode<DT>((uint16_t)(p[e] >> 16)), decode<DT>((uint16_t)(q[e] >> 16)), sum);
+                s = fmaf(decode<DT>((uint16_t)p[e]), decode<DT>((uint16_t)q[e]), s);
+                s = fmaf(decode<DT>((uint16_t)(p[e] >> 16)), decode<DT>((uint16_t)(q[e] >> 16)), s);
             }
-        }
+        };
+        int64_t k = lane * 8;
+        for (; k + 3 * 512 + 8 <= a.cols; k += 4 * 512) {
+            u32x4 p[4], q[4][4];
 #pragma unroll
-        for (int d = 1; d < 64; d <<= 1) sum += __shfl_xor(sum, d);
-        if (a.scale) sum *= a.scale[i];
+            for (int e = 0; e < 4; ++e) {
+                __builtin_memcpy(&p[e], x + k + 512 * e, 16);
+#pragma unroll
+                for (int r = 0; r < 4; ++r) __builtin_memcpy(&q[r][e], m[r] + k + 512 * e, 16);
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) add(p[e], q[r][e], sum[r]);
+        }
+        for (; k < a.cols; k += 512) {
+            const int valid = (int)min((int64_t)8, a.cols - k);
+            const u32x4 p = load_frag8(x + k, valid);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) add(p, load_frag8(m[r] + k, valid), sum[r]);
+        }
+        if (a.scale) scale = a.scale[i];
     }
-    if (lane == 0) a.u[unit] = sum;
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) sum[r] += __shfl_xor(sum[r], d);
+    if (lane >= 4) return;
+    const float v = j + lane >= a.rank ? 0.0f : lane == 0 ? sum[0] : lane == 1 ? sum[1] : lane == 2 ? sum[2] : sum[3];
+    if (j + lane < a.rank) a.u[(size_t)t * (size_t)a.rank + j + lane] = a.fold ? v * scale : v;
+    if (a.us) {
+        uint16_t hi, lo;
+        split_one<DT>(v * scale, hi, lo);
+        uint16_t* us = a.us + (size_t)t * (size_t)(2 * a.rank_p) + j + lane;
+        us[0] = hi;
+        us[a.rank_p] = lo;
+    }
 }
 
-// A workgroup: 16 tokens against each adapter among them (the adapters shared out over grid y),
-// the sum over k cut over its eight waves in pieces of 64 and joined in LDS in their order.
+template <int DT>
+__global__ __launch_bounds__(256) void adapter_shrink_row(AdapterArgs a) {
+    adapter_shrink_wave<DT>(a, (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6));
+}
+
+// The same sums as kernel_stream.h's for any alignment, fragments loaded straight from memory: 16
+// tokens against each adapter among them (shared out over grid y), k cut over the workgroup's
+// eight waves in pieces of 64 and joined in LDS in their order. To part, tokens x 16 NT.
 template <int DT, int NT>
-__global__ __launch_bounds__(512) void adapter_shrink16(AdapterArgs a) {
+__global__ __launch_bounds__(512) void adapter_shrink_any(AdapterArgs a, float* part_out) {
     __shared__ __attribute__((aligned(16))) float part[8][NT][64][4];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int l16 = lane & 15, lg = lane >> 4;
@@ -216,8 +276,6 @@ __global__ __launch_bounds__(512) void adapter_shrink16(AdapterArgs a) {
     int mine = row < a.tokens ? a.index[row] : -1;
     if (mine >= a.adapters) mine = -1;
     const uint16_t* x = static_cast<const uint16_t*>(a.x) + (size_t)min(row, a.tokens - 1) * (size_t)a.ldx;
-    if (blockIdx.y == 0 && mine < 0 && row < a.tokens)
-        for (int j = wave * 4 + lg; j < a.rank; j += 32) a.u[(size_t)row * (size_t)a.rank + j] = 0.0f;
     uint32_t todo = (uint32_t)(__ballot(mine >= 0) & 0xffffu);
     for (uint32_t turn = 0; todo; ++turn) {
         const int i = __builtin_amdgcn_readlane(mine, (int)__builtin_ctz(todo));
@@ -232,29 +290,49 @@ __global__ __launch_bounds__(512) void adapter_shrink16(AdapterArgs a) {
             acc[n] = f32x4{0.f, 0.f, 0.f, 0.f};
             mr[n] = m + (size_t)min(16 * n + l16, a.rank - 1) * (size_t)a.ldm;  // past the rank: not stored
         }
-        int64_t k0 = wave * 64;
-        const int whole = a.cols & ~63;
-#pragma unroll 2
-        for (; k0 < whole; k0 += 512) {
-            u32x4 xv[2], mv[2][NT];
+        // pieces of 64 of k: wave, wave + 8, ..
+        const int whole = a.cols & ~63, all = whole >> 6;
+        const int cnt = wave < all ? (all - wave + 7) >> 3 : 0;
+        auto k_of = [&](int p) { return 64 * (wave + 8 * p) + 8 * lg; };
+        u32x4 xv[2][2], mv[2][2][NT];  // two pieces in turn
+        auto load = [&](int b, int p) {
+            const int k = k_of(p);
 #pragma unroll
             for (int s = 0; s < 2; ++s) {
-                __builtin_memcpy(&xv[s], x + k0 + 32 * s + 8 * lg, 16);
+                __builtin_memcpy(&xv[b][s], x + k + 32 * s, 16);
 #pragma unroll
-                for (int n = 0; n < NT; ++n) __builtin_memcpy(&mv[s][n], mr[n] + k0 + 32 * s + 8 * lg, 16);
+                for (int n = 0; n < NT; ++n) __builtin_memcpy(&mv[b][s][n], mr[n] + k + 32 * s, 16);
             }
+        };
+        auto use = [&](int b) {
 #pragma unroll
             for (int s = 0; s < 2; ++s)
 #pragma unroll
-                for (int n = 0; n < NT; ++n) acc[n] = mfma_16<DT>(mv[s][n], xv[s], acc[n]);
+                for (int n = 0; n < NT; ++n) acc[n] = mfma_16<DT>(mv[b][s][n], xv[b][s], acc[n]);
+        };
+        if (cnt > 0) load(0, 0);
+        int p = 0;
+        for (; p + 2 < cnt; p += 2) {
+            load(1, p + 1);
+            __builtin_amdgcn_sched_barrier(0);
+            use(0);
+            load(0, p + 2);
+            __builtin_amdgcn_sched_barrier(0);
+            use(1);
         }
-        if (k0 == whole && whole < a.cols)
+        if (p + 1 < cnt) {
+            load(1, p + 1);
+            use(0);
+            use(1);
+        } else if (p < cnt) {
+            use(0);
+        }
+        if (whole < a.cols && wave == (all & 7))
             for (int s = 0; s < 2; ++s) {
-                const int64_t k = k0 + 32 * s + 8 * lg;
-                const int valid = (int)max((int64_t)0, min((int64_t)8, a.cols - k));
-                const u32x4 xv = load_frag8(x + k, valid);
+                const int k = whole + 32 * s + 8 * lg, valid = max(0, min(8, a.cols - k));
+                const u32x4 xt = load_frag8(x + k, valid);
 #pragma unroll
-                for (int n = 0; n < NT; ++n) acc[n] = mfma_16<DT>(load_frag8(mr[n] + k, valid), xv, acc[n]);
+                for (int n = 0; n < NT; ++n) acc[n] = mfma_16<DT>(load_frag8(mr[n] + k, valid), xt, acc[n]);
             }
 #pragma unroll
         for (int n = 0; n < NT; ++n) *reinterpret_cast<f32x4*>(part[wave][n][lane]) = acc[n];
@@ -263,42 +341,129 @@ __global__ __launch_bounds__(512) void adapter_shrink16(AdapterArgs a) {
             f32x4 v = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int p = 0; p < 8; ++p) v += *reinterpret_cast<const f32x4*>(part[p][wave][lane]);
-            const float scale = a.scale ? a.scale[i] : 1.0f;
-            const int j = 16 * wave + 4 * lg;
-            float* u = a.u + (size_t)row * (size_t)a.rank + j;
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                if (j + e < a.rank) u[e] = v[e] * scale;
+            *reinterpret_cast<f32x4*>(part_out + (size_t)row * (16 * NT) + 16 * wave + 4 * lg) = v;
         }
         __syncthreads();
     }
 }
 
+// u = the sum of the slices (rows of ld numbers), zeros in rows without an adapter, as fp32 (a.u,
+// NULL: not wanted) and, times the scale, as hi and lo of the matrices' type (a.us: tokens x 2 x
+// rank_p, zeros past the rank). a.fold: the scale is in the fp32 numbers too. A thread: eight rank
+// numbers of one token.
+template <int DT>
+__global__ __launch_bounds__(64) void adapter_shrink_finish(AdapterArgs a, int slices, const float* part, int ld) {
+    const int rank_p = a.rank_p;
+    const int64_t at = (int64_t)blockIdx.x * 64 + threadIdx.x;
+    const int each = rank_p >> 3;
+    if (at >= (int64_t)a.tokens * each) return;
+    const int t = (int)(at / each), j = (int)(at - (int64_t)t * each) * 8;
+    const int i = a.index[t];
+    float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    float scale = 1.0f;
+    if (i >= 0 && i < a.adapters) {
+        const float* p = part + (size_t)t * (size_t)ld + j;
+        const size_t step = (size_t)a.tokens * (size_t)ld;
+        int s = 0;
+        for (; s + 4 <= slices; s += 4) {
+            float q[4][8];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) load_f8(q[k], p + (s + k) * step, ld - j);
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[e] += q[k][e];
+        }
+        for (; s < slices; ++s) {
+            float q[8];
+            load_f8(q, p + s * step, ld - j);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] += q[e];
+        }
+        if (a.scale) scale = a.scale[i];
+    }
+    float w[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        v[e] = j + e < a.rank ? v[e] : 0.0f;
+        w[e] = v[e] * scale;
+        if (a.u && j + e < a.rank) a.u[(size_t)t * (size_t)a.rank + j + e] = a.fold ? w[e] : v[e];
+    }
+    u32x4 hi, lo;
+    split_hi_lo<DT>(w, hi, lo);
+    uint16_t* us = a.us + (size_t)t * (size_t)(2 * rank_p) + j;
+    *reinterpret_cast<u32x4*>(us) = hi;
+    *reinterpret_cast<u32x4*>(us + rank_p) = lo;
+}
+
+// y = v + scale b_i u[t] for columns n .. n + 3 (a.m: cols x rank)
+template <int DT>
+__device__ __forceinline__ void adapter_row_add(const AdapterArgs& a, int t, int n, f32x4 v) {
+    const int i = a.index[t], left = a.cols - n;
+    if (i >= 0 && i < a.adapters) {
+        const uint16_t* m = static_cast<const uint16_t*>(a.m) + (size_t)i * (size_t)a.stride_m;
+        f32x4 d = {0.f, 0.f, 0.f, 0.f};
+        for (int j = 0; j < a.rank; j += 8) {
+            float u[8];
+            load_f8(u, a.u + (size_t)t * (size_t)a.rank + j, a.rank - j);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const u32x4 p = load_frag8(m + (size_t)(n + min(e, left - 1)) * (size_t)a.ldm + j, a.rank - j);
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    d[e] = fmaf(u[2 * q], decode<DT>((uint16_t)p[q]), d[e]);
+                    d[e] = fmaf(u[2 * q + 1], decode<DT>((uint16_t)(p[q] >> 16)), d[e]);
+                }
+            }
+        }
+        const float scale = a.scale ? a.scale[i] : 1.0f;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = fmaf(scale, d[e], v[e]);
+    }
+    const size_t at = (size_t)t * (size_t)a.ldo + n;
+    if (left >= 4) store_out4(a.out, DT, at, v);
+    else
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (e < left) store_out(a.out, DT, at + e, v[e]);
+}
+
 // ---------------------------------------------------------------- adapters' transposes
 // Each in_i (rows x cols) as its transpose of cols x out_ld, zeros past column `rows`. A
 // workgroup turns 64 x 64 through LDS.
-__device__ __forceinline__ void turn_tile(const TurnArgs& t, int tile, int i, uint16_t (*buf)[66]) {
+__device__ __forceinline__ void turn_tile(const TurnArgs& t, int tile, int i, uint16_t (*buf)[72]) {
     const int tr = tile / t.tiles_c, tc = tile - tr * t.tiles_c;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int c8 = (threadIdx.x & 7) * 8, r0 = threadIdx.x >> 3;
     const uint16_t* in = static_cast<const uint16_t*>(t.in) + (size_t)i * (size_t)t.stride;
     uint16_t* out = static_cast<uint16_t*>(t.out) + (size_t)i * (size_t)t.cols * (size_t)t.out_ld;
-    const int c = tc * 64 + lane;
-    for (int e = wave; e < 64; e += 4) {
-        const int r = tr * 64 + e;
-        buf[e][lane] = r < t.rows && c < t.cols ? in[(size_t)r * (size_t)t.ld + c] : (uint16_t)0;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const int r = tr * 64 + r0 + 32 * h, c = tc * 64 + c8;
+        *reinterpret_cast<u32x4*>(&buf[r0 + 32 * h][c8]) =
+            load_frag8(in + (size_t)min(r, t.rows - 1) * (size_t)t.ld + c, r < t.rows ? t.cols - c : 0);
     }
     __syncthreads();
-    const int r = tr * 64 + lane;
-    for (int e = wave; e < 64; e += 4) {
-        const int cc = tc * 64 + e;
-        if (cc < t.cols && r < t.out_ld) out[(size_t)cc * (size_t)t.out_ld + r] = buf[lane][e];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const int cc = tc * 64 + r0 + 32 * h, r = tr * 64 + c8, left = t.out_ld - r;
+        if (cc >= t.cols || left <= 0) continue;
+        u32x4 v;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            v[e] = (uint32_t)buf[c8 + 2 * e][r0 + 32 * h] | ((uint32_t)buf[c8 + 2 * e + 1][r0 + 32 * h] << 16);
+        uint16_t* dst = out + (size_t)cc * (size_t)t.out_ld + r;
+        if (left >= 8) __builtin_memcpy(dst, &v, 16);
+        else
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (e < left) dst[e] = (uint16_t)(v[e >> 1] >> (16 * (e & 1)));
     }
 }
 
 // Both of an adapter's matrices in one launch: grid x the tiles of one and then of the other,
 // grid y the adapters.
 static __global__ __launch_bounds__(256) void adapter_turn(TurnArgs p, TurnArgs q) {
-    __shared__ uint16_t buf[64][66];
+    __shared__ __attribute__((aligned(16))) uint16_t buf[64][72];
     const int first = p.tiles_r * p.tiles_c;
     if ((int)blockIdx.x < first) turn_tile(p, (int)blockIdx.x, (int)blockIdx.y, buf);
     else turn_tile(q, (int)blockIdx.x - first, (int)blockIdx.y, buf);
@@ -317,13 +482,22 @@ __device__ __forceinline__ AdapterSpan adapter_span(const AdapterArgs& a, int i)
 }
 
 // A workgroup: 64 columns of z (x or grad) and the whole rank, over an adapter's rows of a chunk
-// in steps of 32. z and h (v or u, split in two) lie in LDS by rows and are read transposed, so
-// that a lane gets eight consecutive rows of one column.
+// (at most kChunkMax) in steps of 32, loaded two steps ahead. z and h (v or u as hi and lo) lie in
+// LDS by rows and are read transposed, so that a lane gets eight consecutive rows of one column.
+constexpr int kChunkMax = 512;
+
+template <int NT>
+struct GradientLds {
+    uint16_t z[2][32 * 64];
+    uint16_t h[2][2][32 * NT * 16];
+    int rows[kChunkMax + 64];
+};
+
 template <int DT, int NT, bool TURNED>
-__global__ __launch_bounds__(256) void adapter_gradient16(AdapterArgs a) {
-    constexpr int HC = NT * 2;  // 16-byte chunks of a row of h
-    __shared__ __attribute__((aligned(16))) uint16_t sz[2][32 * 64];
-    __shared__ __attribute__((aligned(16))) uint16_t sh[2][2][32 * NT * 16];
+__device__ __forceinline__ void adapter_gradient_body(const AdapterArgs& a, GradientLds<NT>& lds) {
+    constexpr int HC = NT * 2;               // 16-byte pieces of a row of h
+    constexpr int HN = 32 * 2 * HC;          // pieces of a step: hi and lo
+    constexpr int HP = (HN + 255) / 256;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int l16 = lane & 15, lg = lane >> 4;
     const int slot = (int)blockIdx.y, c0 = (int)blockIdx.x * 64;
@@ -341,37 +515,36 @@ __global__ __launch_bounds__(256) void adapter_gradient16(AdapterArgs a) {
     const int from = max(sp.from, ch * a.chunk), to = (int)min((int64_t)sp.to, ((int64_t)ch + 1) * a.chunk);
     if (from >= to) return;
     const bool alone = (sp.to - 1) / a.chunk == first;
+    // the chunk's rows, -1 for padding and past its end
+    for (int e = tid; e < kChunkMax + 64; e += 256) {
+        int t = from + e < to ? a.rows[from + e] : -1;
+        lds.rows[e] = t >= 0 && t < a.tokens ? t : -1;
+    }
+    __syncthreads();
 
     const uint16_t* z = static_cast<const uint16_t*>(a.x);
     const int zr = tid >> 3, zc = tid & 7;   // the 16 bytes of z this thread moves
-    constexpr int HN = NT * 32 * 16 / 8;     // pieces of eight numbers of h
-    constexpr int HP = HN < 256 ? 1 : HN / 256;
-    u32x4 zreg;
-    float hreg[HP][8];
-    auto load = [&](int p0) {
-        int t = p0 + zr < to ? a.rows[p0 + zr] : -1;
-        if (t >= a.tokens) t = -1;
-        const int c = c0 + zc * 8;
-        zreg = load_frag8(z + (size_t)max(t, 0) * (size_t)a.ldx + c, t < 0 ? 0 : a.cols - c);
+    const int zleft = a.cols - (c0 + zc * 8);
+    struct Step {
+        u32x4 z, h[HP];
+    };
+    auto load = [&](Step& s, int p0) {
+        const int t = lds.rows[p0 + zr];
+        s.z = load_frag8(z + (size_t)max(t, 0) * (size_t)a.ldx + c0 + zc * 8, t < 0 ? 0 : zleft);
 #pragma unroll
         for (int q = 0; q < HP; ++q) {
-            const int piece = q * 256 + tid, r = piece / HC, j = (piece % HC) * 8;
-            int th = r < 32 && p0 + r < to ? a.rows[p0 + r] : -1;
-            if (th >= a.tokens) th = -1;
-            load_f8(hreg[q], a.u + (size_t)max(th, 0) * (size_t)a.rank + j, th < 0 ? 0 : a.rank - j);
+            const int piece = q * 256 + tid, r = (piece / (2 * HC)) & 31, c = piece % (2 * HC);
+            const int th = lds.rows[p0 + r];
+            s.h[q] = load_frag8(a.us + (size_t)max(th, 0) * (size_t)(2 * NT * 16) + c * 8, th < 0 ? 0 : 8);
         }
     };
-    auto put = [&](int b) {
-        *reinterpret_cast<u32x4*>(&sz[b][zr * 64 + ((zc ^ nmaj_swz<8>(zr)) << 3)]) = zreg;
+    auto put = [&](const Step& s, int b) {
+        *reinterpret_cast<u32x4*>(&lds.z[b][zr * 64 + ((zc ^ nmaj_swz<8>(zr)) << 3)]) = s.z;
 #pragma unroll
         for (int q = 0; q < HP; ++q) {
-            const int piece = q * 256 + tid, r = piece / HC, c = piece % HC;
+            const int piece = q * 256 + tid, r = piece / (2 * HC), c = piece % (2 * HC);
             if (HN < 256 && piece >= HN) break;
-            u32x4 hv, lv;
-            split_hi_lo<DT>(hreg[q], hv, lv);
-            const int at = r * (HC * 8) + ((c ^ nmaj_swz<HC>(r)) << 3);
-            *reinterpret_cast<u32x4*>(&sh[b][0][at]) = hv;
-            *reinterpret_cast<u32x4*>(&sh[b][1][at]) = lv;
+            *reinterpret_cast<u32x4*>(&lds.h[b][c / HC][r * (HC * 8) + (((c % HC) ^ nmaj_swz<HC>(r)) << 3)]) = s.h[q];
         }
     };
     // rows 8 lg .. + 7 of column c0 + l16 of a tile of CH chunks a row
@@ -392,18 +565,12 @@ __global__ __launch_bounds__(256) void adapter_gradient16(AdapterArgs a) {
     f32x4 acc[NT];
 #pragma unroll
     for (int n = 0; n < NT; ++n) acc[n] = f32x4{0.f, 0.f, 0.f, 0.f};
-    load(from);
-    put(0);
-    int b = 0;
-    for (int p0 = from; p0 < to; p0 += 32, b ^= 1) {
-        __syncthreads();
-        const bool more = p0 + 32 < to;
-        if (more) load(p0 + 32);
-        const u32x4 zf = turned(sz[b], wave * 16, std::integral_constant<int, 8>{});
+    auto use = [&](int b) {
+        const u32x4 zf = turned(lds.z[b], wave * 16, std::integral_constant<int, 8>{});
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-            const u32x4 hf = turned(sh[b][0], n * 16, std::integral_constant<int, HC>{});
-            const u32x4 lf = turned(sh[b][1], n * 16, std::integral_constant<int, HC>{});
+            const u32x4 hf = turned(lds.h[b][0], n * 16, std::integral_constant<int, HC>{});
+            const u32x4 lf = turned(lds.h[b][1], n * 16, std::integral_constant<int, HC>{});
             if (TURNED) {
                 acc[n] = mfma_16<DT>(hf, zf, acc[n]);
                 acc[n] = mfma_16<DT>(lf, zf, acc[n]);
@@ -412,15 +579,29 @@ __global__ __launch_bounds__(256) void adapter_gradient16(AdapterArgs a) {
                 acc[n] = mfma_16<DT>(zf, lf, acc[n]);
             }
         }
-        if (more) put(b ^ 1);
+    };
+    // steps two at a time; rows past the chunk's end load nothing and count as zeros
+    const int n = to - from;
+    Step s0, s1;
+    load(s0, 0);
+    load(s1, 32);
+    put(s0, 0);
+    for (int p = 0; p < n; p += 64) {
+        __syncthreads();
+        if (p + 64 < n) load(s0, p + 64);
+        use(0);
+        put(s1, 1);
+        __syncthreads();
+        if (p + 64 < n) load(s1, p + 96);
+        use(1);
+        if (p + 64 < n) put(s0, 0);
     }
     // TURNED: lane has column c0 + l16 and rank numbers 16 n + 4 lg .. + 3; else rank number
     // 16 n + l16 and columns c0 + 4 lg .. + 3
-    const float scale = a.scale ? a.scale[i] : 1.0f;
     const size_t each = (size_t)a.rank * (size_t)a.cols;
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-        const f32x4 v = acc[n] * scale;
+        const f32x4 v = acc[n];
         const int c = c0 + wave * 16 + (TURNED ? l16 : 4 * lg), j = 16 * n + (TURNED ? 4 * lg : l16);
         if (c >= a.cols || j >= a.rank) continue;
         const int left = TURNED ? a.rank - j : a.cols - c;
@@ -440,9 +621,21 @@ __global__ __launch_bounds__(256) void adapter_gradient16(AdapterArgs a) {
     }
 }
 
+// Both gradients in one launch: grid z 0 is a's, 1 b's.
+template <int DT, int NT>
+__global__ __launch_bounds__(256) void adapter_gradient16(AdapterArgs a, AdapterArgs b) {
+    __shared__ __attribute__((aligned(16))) GradientLds<NT> lds;
+    if (blockIdx.z == 0) {
+        if ((int64_t)blockIdx.x * 64 < a.cols) adapter_gradient_body<DT, NT, false>(a, lds);
+    } else {
+        if ((int64_t)blockIdx.x * 64 < b.cols) adapter_gradient_body<DT, NT, true>(b, lds);
+    }
+}
+
 // An adapter (grid y) of several chunks: the sum of its slots; one without rows: zeros.
 template <int DT>
-__global__ __launch_bounds__(256) void adapter_join(AdapterArgs a, int slots) {
+__global__ __launch_bounds__(256) void adapter_join(AdapterArgs p, AdapterArgs q, int slots) {
+    const AdapterArgs& a = blockIdx.z == 0 ? p : q;
     const int i = (int)blockIdx.y;
     const AdapterSpan sp = adapter_span(a, i);
     const bool none = sp.to <= sp.from;

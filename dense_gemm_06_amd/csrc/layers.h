@@ -95,6 +95,9 @@ struct AdapterArgs {
     const int* index;
     const float* scale;     // NULL: 1
     float* u;               // tokens x rank
+    uint16_t* us;           // scale u as hi and lo (tokens x 2 x rank_p)
+    int rank_p;             // 16, 32, 64 or 128
+    int fold;               // u holds scale u
     // expand: out = base + scale u m
     const float* base;
     int64_t ld_base;
@@ -132,11 +135,18 @@ struct TurnArgs {
 // 16-bit matrices, on the matrix instructions, one function for each type:
 // out = x w + scale u m in one kernel, for up to 64 tokens (x w^T only) or in 256 x 256 tiles
 DG_16BIT(launch_adapter_skinny, (const AdapterProduct& p, const AdapterArgs& a, hipStream_t s))
+// the same through `slices` of k (direct rows): u and part (slices x tokens x cols rounded up to 4)
+DG_16BIT(launch_adapter_decode, (const AdapterProduct& p, const AdapterArgs& u, const AdapterArgs& a, int slices, int slice_k, float* part, hipStream_t s))
 DG_16BIT(launch_adapter_tiles, (const AdapterProduct& p, const AdapterArgs& a, int group_m, hipStream_t s))
 // the operators below, m with its long direction along memory in shrink and across it in expand
-DG_16BIT(launch_adapter_shrink16, (const AdapterArgs& a, hipStream_t s))
+DG_16BIT(launch_adapter_shrink_row, (const AdapterArgs& a, hipStream_t s))
+// through part (slices x tokens x rank_p): u, us. direct: 16-byte rows
+DG_16BIT(launch_adapter_shrink16, (const AdapterArgs& a, int direct, int slices, int slice_k, float* part, hipStream_t s))
 DG_16BIT(launch_adapter_expand16, (const AdapterArgs& a, hipStream_t s))
-DG_16BIT(launch_adapter_gradient16, (const AdapterArgs& a, int slots, hipStream_t s))
+// both gradients from us: a's of v and x, b's of u and grad
+DG_16BIT(launch_adapter_gradient16, (const AdapterArgs& a, const AdapterArgs& b, int slots, hipStream_t s))
+// us (and u) from `slices` sums of rows of ld numbers
+DG_16BIT(launch_adapter_split, (const AdapterArgs& a, int slices, const float* part, int ld, hipStream_t s))
 int launch_adapter_turn(const TurnArgs& p, const TurnArgs& q, int adapters, hipStream_t s);
 
 // u[t][j] = scale sum_k x[t][k] m(j,k)

@@ -108,11 +108,17 @@ Range b_range(const gemm_adapter_set& s, int64_t N, int64_t es) {
 }
 Range scale_of(const gemm_adapter_set& s) { return range("set.scale", s.scale, (uint64_t)s.adapters * 4); }
 
+int64_t rank_padded(int64_t rank) { return rank <= 16 ? 16 : rank <= 32 ? 32 : rank <= 64 ? 64 : 128; }
+
+#define DG_BY_TYPE(name, dtype, ...) \
+    ((dtype) == GEMM_F16 ? dg::name##_f16(__VA_ARGS__) : dg::name##_bf16(__VA_ARGS__))
+
 dg::AdapterArgs adapter_args(const gemm_adapter_set& s, int64_t tokens, const int32_t* index) {
     dg::AdapterArgs a;
     memset(&a, 0, sizeof a);
     a.tokens = (int)tokens;
     a.rank = (int)s.rank;
+    a.rank_p = (int)rank_padded(s.rank);
     a.adapters = (int)s.adapters;
     a.index = index;
     return a;
@@ -142,15 +148,54 @@ constexpr int64_t kSkinny = 64;
 // the adapters to the product in its tiles.
 bool adapter_tiles(int64_t tokens, int64_t cols) { return ceil_div(tokens, 256) * ceil_div(cols, 256) >= 128; }
 
+int tile_group(int64_t rows, int64_t cols) {
+    const int64_t m = ceil_div(rows, 256);
+    return (int)std::max<int64_t>(1, std::min<int64_t>(dg::default_group_m(m, ceil_div(cols, 256)), m));
+}
+
+// How the kernels on 16-bit matrices read x (rows x len) and w (op T: cols x len, op N: len x cols):
+// 0 not at all, 1 through registers, 2 straight to LDS.
+bool whole_pieces(const void* p, int64_t ld, int64_t cols) {
+    return ((uintptr_t)p & 15) == 0 && ld % 8 == 0 && cols % 8 == 0;
+}
+int tiles_form(const void* x, int64_t ldx, const void* w, int64_t ldw, int64_t cols, int64_t len, int opb, int dtype) {
+    if (dtype == GEMM_F32 || len < 8 || (opb == GEMM_OP_N && cols < 8)) return 0;
+    return whole_pieces(x, ldx, len) && whole_pieces(w, ldw, opb == GEMM_OP_T ? len : cols) ? 2 : 1;
+}
+
+// k cut into slices of whole stages (128) so that `tiles` of them make two workgroups for each
+// compute unit.
+struct Slices {
+    int64_t count, k;
+};
+Slices slices_of(int64_t tiles, int64_t K) {
+    const int64_t stages = std::max<int64_t>(1, ceil_div(K, 128));
+    const int64_t want = std::min({ceil_div(2 * dg::kCus, std::max<int64_t>(1, tiles)), stages, (int64_t)32});
+    const int64_t k = ceil_div(stages, want) * 128;
+    return {std::max<int64_t>(1, ceil_div(K, k)), k};
+}
+
+
 struct AdapterSpace {
     float* base = nullptr;    // the shared product (16-bit matrices without a kernel for both)
     void* product = nullptr;
+    float* part = nullptr;    // sums of slices of k
+    uint16_t* us = nullptr;   // scale u (or v) as two 16-bit numbers
+    uint16_t* us_b = nullptr; // scale u in the backward pass
     float* v = nullptr;       // backward
     void* a_turned = nullptr; // adapters x K x rank_m, adapters x rank x N (16-bit matrices)
     void* b_turned = nullptr;
     float* sums = nullptr;    // the gradients' slots
+    Slices slices = {1, 0};
     int64_t rank_m = 0, chunk = 0, slots = 0, bytes = 0;
 };
+
+// What the first product over `len` of 16-bit matrices needs, and the second's u.
+void shrink_space(AdapterSpace& s, Parts& p, int64_t tokens, int64_t len, int64_t rank) {
+    s.slices = slices_of(ceil_div(tokens, 64), len);
+    s.part = static_cast<float*>(p.take(s.slices.count * tokens * rank_padded(rank) * 4));
+    s.us = static_cast<uint16_t*>(p.take(tokens * rank_padded(rank) * 4));
+}
 
 void product_space(AdapterSpace& s, Parts& p, int64_t tokens, int64_t cols, int dtype, bool one_kernel) {
     if (one_kernel) return;
@@ -158,32 +203,23 @@ void product_space(AdapterSpace& s, Parts& p, int64_t tokens, int64_t cols, int 
     s.product = p.take(kProductWorkspace);
 }
 
-int tile_group(int64_t rows, int64_t cols) {
-    const int64_t m = ceil_div(rows, 256);
-    return (int)std::max<int64_t>(1, std::min<int64_t>(dg::default_group_m(m, ceil_div(cols, 256)), m));
-}
-
-// How the kernels for both products read x (rows x len) and w (op T: cols x len, op N: len x cols):
-// 0 not at all, 1 through registers, 2 straight to LDS.
-int tiles_form(const void* x, int64_t ldx, const void* w, int64_t ldw, int64_t cols, int64_t len, int opb, int dtype) {
-    if (dtype == GEMM_F32 || len < 8 || (opb == GEMM_OP_N && cols < 8)) return 0;
-    const bool direct = (((uintptr_t)x | (uintptr_t)w) & 15) == 0 && ldx % 8 == 0 && ldw % 8 == 0 && len % 8 == 0 &&
-                        (opb == GEMM_OP_T || cols % 8 == 0);
-    return direct ? 2 : 1;
-}
-
-// A forward call of 16-bit matrices takes one kernel for both products, of few rows or in tiles.
-bool forward_fused(int64_t tokens, int64_t N, int64_t K, int dtype) {
-    return dtype != GEMM_F32 && K > 0 && (tokens <= kSkinny || (K >= 8 && adapter_tiles(tokens, N)));
-}
-bool backward_fused(int64_t tokens, int64_t N, int64_t K, int dtype) {
-    return dtype != GEMM_F32 && N >= 8 && K >= 8 && adapter_tiles(tokens, K);
+// A forward call of 16-bit matrices: few tokens
+bool few_tokens(int64_t tokens, int64_t K, int dtype) { return dtype != GEMM_F32 && K > 0 && tokens <= kSkinny; }
+// or one kernel for the product and the adapters in its tiles, in either direction
+bool in_tiles(int64_t tokens, int64_t cols, int64_t len, int dtype) {
+    return dtype != GEMM_F32 && cols >= 8 && len >= 8 && adapter_tiles(tokens, cols);
 }
 
 AdapterSpace adapter_space(void* workspace, int64_t tokens, int64_t N, int64_t K, int64_t rank, int dtype) {
     AdapterSpace s;
     Parts p{static_cast<char*>(workspace)};
-    product_space(s, p, tokens, N, dtype, forward_fused(tokens, N, K, dtype));
+    if (few_tokens(tokens, K, dtype)) {
+        s.slices = slices_of(ceil_div(N, 64), K);
+        s.part = static_cast<float*>(p.take(s.slices.count * tokens * ceil_div(N, 4) * 16));
+    } else {
+        product_space(s, p, tokens, N, dtype, in_tiles(tokens, N, K, dtype));
+        if (dtype != GEMM_F32) shrink_space(s, p, tokens, K, rank);
+    }
     s.bytes = p.at;
     return s;
 }
@@ -192,18 +228,19 @@ AdapterSpace adapter_backward_space(void* workspace, int64_t tokens, int64_t N, 
                                     int64_t rank, int dtype) {
     AdapterSpace s;
     Parts p{static_cast<char*>(workspace)};
-    product_space(s, p, tokens, K, dtype, backward_fused(tokens, N, K, dtype));
+    product_space(s, p, tokens, K, dtype, in_tiles(tokens, K, N, dtype));
     s.v = static_cast<float*>(p.take(tokens * rank * 4));
     if (dtype != GEMM_F32) {
+        shrink_space(s, p, tokens, N, rank);
         s.rank_m = ceil_div(rank, 16) * 16;
         s.a_turned = p.take(adapters * K * s.rank_m * 2);
         s.b_turned = p.take(adapters * N * rank * 2);
-        // chunks of 512 rows, fewer where that leaves compute units idle; at most 2^14 of them
+        // chunks of 512 rows (what the kernel holds), fewer where that leaves compute units idle
         s.chunk = 512;
-        while (s.chunk > 64 && ceil_div(tokens, s.chunk) * ceil_div(std::min(N, K), 64) < 512) s.chunk /= 2;
-        while (ceil_div(tokens, s.chunk) > (1 << 14)) s.chunk *= 2;
+        while (s.chunk > 64 && ceil_div(tokens, s.chunk) * (ceil_div(N, 64) + ceil_div(K, 64)) < 1024) s.chunk /= 2;
         s.slots = adapters + ceil_div(tokens, s.chunk);
-        s.sums = static_cast<float*>(p.take(s.slots * rank * std::max(N, K) * 4));
+        s.sums = static_cast<float*>(p.take(s.slots * rank * (N + K) * 4));
+        s.us_b = static_cast<uint16_t*>(p.take(tokens * rank_padded(rank) * 4));
     }
     s.bytes = p.at;
     return s;
@@ -211,6 +248,14 @@ AdapterSpace adapter_backward_space(void* workspace, int64_t tokens, int64_t N, 
 
 #define DG_BY_TYPE(name, dtype, ...) \
     ((dtype) == GEMM_F16 ? dg::name##_f16(__VA_ARGS__) : dg::name##_bf16(__VA_ARGS__))
+
+// u and us of 16-bit matrices for a.m of rank x cols.
+int shrink16(const dg::AdapterArgs& a, const AdapterSpace& sp, int dtype, hipStream_t s) {
+    // each token by itself where all of them together read no more than 8192 rows of the adapters
+    if ((int64_t)a.tokens * a.rank <= 8192) return DG_BY_TYPE(launch_adapter_shrink_row, dtype, a, s);
+    const bool direct = whole_pieces(a.x, a.ldx, a.cols) && whole_pieces(a.m, a.ldm, a.cols) && a.stride_m % 8 == 0;
+    return DG_BY_TYPE(launch_adapter_shrink16, dtype, a, direct, (int)sp.slices.count, (int)sp.slices.k, sp.part, s);
+}
 
 // ---------------------------------------------------------------- loss
 constexpr int64_t kPieceBytes = (int64_t)128 << 20;
@@ -360,33 +405,37 @@ int gemm_adapters_product(const void* x, int64_t tokens, int64_t K, int64_t ldx,
     a.ldx = ldx;
     a.u = u;
     with_a(a, *set, K);
-    const bool wide = dtype == GEMM_F32;
-    if (set->rank > 0)
-        DG_TRY(launched(wide ? dg::launch_adapter_shrink(a, dtype, s) : DG_BY_TYPE(launch_adapter_shrink16, dtype, a, s),
-                        "adapters' first product"));
-    if (N == 0) return GEMM_OK;
-    if (forward_fused(tokens, N, K, dtype)) {
-        with_b(a, *set, N);
-        a.scale = set->scale;
-        a.out = y;
-        a.ldo = ldy;
-        dg::AdapterProduct p{x, w, ldx, ldw, (int)N, (int)K, GEMM_OP_T,
-                             tiles_form(x, ldx, w, ldw, N, K, GEMM_OP_T, dtype) == 2};
-        return launched(tokens <= kSkinny ? DG_BY_TYPE(launch_adapter_skinny, dtype, p, a, s)
-                                          : DG_BY_TYPE(launch_adapter_tiles, dtype, p, a, tile_group(tokens, N), s),
+    const bool wide = dtype == GEMM_F32, few = few_tokens(tokens, K, dtype);
+    const int form = tiles_form(x, ldx, w, ldw, N, K, GEMM_OP_T, dtype);
+    const dg::AdapterProduct p{x, w, ldx, ldw, (int)N, (int)K, GEMM_OP_T, form == 2};
+    dg::AdapterArgs b = a;
+    with_b(b, *set, N);
+    b.scale = set->scale;
+    b.out = y;
+    b.ldo = ldy;
+    // the stream of w, where there is enough of it; kernel_skinny.h's otherwise
+    if (few && form == 2 && N >= 64)
+        return launched(DG_BY_TYPE(launch_adapter_decode, dtype, p, a, b, (int)sp.slices.count, (int)sp.slices.k, sp.part, s),
                         "adapters' products");
+    if (set->rank > 0) {
+        a.us = b.us = sp.us;
+        a.scale = wide ? nullptr : set->scale;
+        DG_TRY(launched(wide  ? dg::launch_adapter_shrink(a, dtype, s)
+                        : few ? DG_BY_TYPE(launch_adapter_shrink_row, dtype, a, s)
+                              : shrink16(a, sp, dtype, s),
+                        "adapters' first product"));
     }
+    if (N == 0) return GEMM_OK;
+    if (few) return launched(DG_BY_TYPE(launch_adapter_skinny, dtype, p, b, s), "adapters' products");
+    if (in_tiles(tokens, N, K, dtype))
+        return launched(DG_BY_TYPE(launch_adapter_tiles, dtype, p, b, tile_group(tokens, N), s), "adapters' products");
     float* base = dtype == GEMM_F32 ? static_cast<float*>(y) : sp.base;
     const int64_t ldb = dtype == GEMM_F32 ? ldy : N;
     DG_TRY(product(GEMM_OP_T, tokens, N, K, x, ldx, w, ldw, base, ldb, dtype, GEMM_F32, 0.0f, sp.product,
                    kProductWorkspace, stream));
-    with_b(a, *set, N);
-    a.scale = set->scale;
-    a.base = base;
-    a.ld_base = ldb;
-    a.out = y;
-    a.ldo = ldy;
-    return launched(wide ? dg::launch_adapter_expand(a, dtype, s) : DG_BY_TYPE(launch_adapter_expand16, dtype, a, s),
+    b.base = base;
+    b.ld_base = ldb;
+    return launched(wide ? dg::launch_adapter_expand(b, dtype, s) : DG_BY_TYPE(launch_adapter_expand16, dtype, b, s),
                     "adapters' second product");
 }
 
@@ -429,6 +478,11 @@ int gemm_adapters_backward(const void* grad, int64_t tokens, int64_t N, int64_t 
             set_error("plan.capacity = %lld must be at most the %lld tokens (a plan with align 1)",
                       (long long)plan->capacity, (long long)tokens);
             return GEMM_ERR_INVALID_VALUE;
+        }
+        if (dtype != GEMM_F32 && ceil_div(tokens, 512) + set->adapters > 65535) {
+            set_error("tokens = %lld with %lld adapters need more chunks than a launch holds", (long long)tokens,
+                      (long long)set->adapters);
+            return GEMM_ERR_UNSUPPORTED;
         }
         DG_TRY(check_pointer("plan.offsets", plan->offsets));
         DG_TRY(check_pointer("plan.counts", plan->counts));
@@ -475,6 +529,8 @@ int gemm_adapters_backward(const void* grad, int64_t tokens, int64_t N, int64_t 
     a.x = grad;
     a.ldx = ldg;
     a.u = sp.v;
+    a.us = sp.us;
+    a.fold = 1;
     a.scale = set->scale;
     with_b(a, *set, N);
     if (!wide) {
@@ -484,8 +540,7 @@ int gemm_adapters_backward(const void* grad, int64_t tokens, int64_t N, int64_t 
         a.turned = 0;
     }
     if (tokens > 0 && set->rank > 0)
-        DG_TRY(launched(wide ? dg::launch_adapter_shrink(a, dtype, s) : DG_BY_TYPE(launch_adapter_shrink16, dtype, a, s),
-                        "adapters' v"));
+        DG_TRY(launched(wide ? dg::launch_adapter_shrink(a, dtype, s) : shrink16(a, sp, dtype, s), "adapters' v"));
     if (x_grad && tokens > 0 && K > 0) {
         with_a(a, *set, K);
         if (!wide) {
@@ -498,7 +553,7 @@ int gemm_adapters_backward(const void* grad, int64_t tokens, int64_t N, int64_t 
         a.scale = nullptr;
         a.out = x_grad;
         a.ldo = ldxg;
-        if (backward_fused(tokens, N, K, dtype)) {
+        if (in_tiles(tokens, K, N, dtype)) {
             dg::AdapterProduct p{grad, w, ldg, ldw, (int)K, (int)N, GEMM_OP_N,
                                  tiles_form(grad, ldg, w, ldw, K, N, GEMM_OP_N, dtype) == 2};
             DG_TRY(launched(DG_BY_TYPE(launch_adapter_tiles, dtype, p, a, tile_group(tokens, K), s), "adapters' x_grad"));
@@ -520,28 +575,41 @@ int gemm_adapters_backward(const void* grad, int64_t tokens, int64_t N, int64_t 
     a.capacity = (int)plan->capacity;
     a.chunk = (int)sp.chunk;
     a.work = sp.sums;
-    auto gradient = [&](const char* what) {
-        return launched(wide ? dg::launch_adapter_gradient(a, dtype, s)
-                             : DG_BY_TYPE(launch_adapter_gradient16, dtype, a, (int)sp.slots, s), what);
-    };
-    if (K > 0) {
-        a.x = x;
-        a.ldx = ldx;
-        a.scale = nullptr;
-        with_a(a, *set, K);
-        a.out = a_grad;
-        DG_TRY(gradient("adapters' a_grad"));
-    }
-    if (N > 0) {
+    if (wide) {
+        if (K > 0) {
+            a.x = x;
+            a.ldx = ldx;
+            a.scale = nullptr;
+            with_a(a, *set, K);
+            a.out = a_grad;
+            DG_TRY(launched(dg::launch_adapter_gradient(a, dtype, s), "adapters' a_grad"));
+        }
+        if (N == 0) return GEMM_OK;
         a.x = grad;
         a.ldx = ldg;
         a.u = const_cast<float*>(u);
         a.scale = set->scale;
         with_b(a, *set, N);
         a.out = b_grad;
-        DG_TRY(gradient("adapters' b_grad"));
+        return launched(dg::launch_adapter_gradient(a, dtype, s), "adapters' b_grad");
     }
-    return GEMM_OK;
+    dg::AdapterArgs b = a;
+    a.x = x;
+    a.ldx = ldx;
+    with_a(a, *set, K);
+    a.out = a_grad;
+    b.x = grad;
+    b.ldx = ldg;
+    with_b(b, *set, N);
+    b.out = b_grad;
+    b.work = sp.sums + sp.slots * set->rank * K;
+    b.u = nullptr;
+    b.us = sp.us_b;
+    b.scale = set->scale;
+    if (tokens > 0)
+        DG_TRY(launched(DG_BY_TYPE(launch_adapter_split, dtype, b, 1, u, (int)set->rank, s), "adapters' u"));
+    if (N == 0 && K == 0) return GEMM_OK;
+    return launched(DG_BY_TYPE(launch_adapter_gradient16, dtype, a, b, (int)sp.slots, s), "adapters' gradients");
 }
 
 // ---------------------------------------------------------------- loss
