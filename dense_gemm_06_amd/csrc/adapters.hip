@@ -74,7 +74,23 @@ __global__ __launch_bounds__(256) void adapter_gradient(AdapterArgs a, int64_t n
         const int64_t from = max(0, min(a.offsets[i], a.capacity));
         const int64_t to = min((int64_t)a.capacity, from + max(0, a.counts[i]));
         float sum = 0.0f;
-        for (int64_t p = from; p < to; ++p) {
+        // rows eight at a time, all of their loads before the first product
+        int64_t p = from;
+        for (; p + 8 <= to; p += 8) {
+            float u[8], x[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const int t = a.rows[p + e];
+                const bool in = t >= 0 && t < a.tokens;
+                const size_t row = in ? (size_t)t : 0;
+                u[e] = a.u[row * a.rank + j];
+                x[e] = element<DT>(a.x, row * (size_t)a.ldx + k);
+                if (!in) u[e] = x[e] = 0.0f;
+            }
+#pragma unroll
+            for (int e = 0; e < 8; ++e) sum = fmaf(u[e], x[e], sum);
+        }
+        for (; p < to; ++p) {
             const int t = a.rows[p];
             if (t < 0 || t >= a.tokens) continue;
             sum = fmaf(a.u[(size_t)t * a.rank + j], element<DT>(a.x, (size_t)t * (size_t)a.ldx + k), sum);

@@ -155,7 +155,7 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
 }
 
 // ---------------------------------------------------------------- second product on its own
-// out = base + scale u m^T, 32 rows x 64 columns to a workgroup, whose four waves share the adapters
+// out = the slices' sum of base + scale u m^T, 32 rows x 64 columns to a workgroup, whose four waves share the adapters
 // among the rows and are joined in LDS in their order.
 template <int DT>
 __global__ __launch_bounds__(256) void adapter_expand16(AdapterArgs a, int tiles_n) {
@@ -177,13 +177,17 @@ __global__ __launch_bounds__(256) void adapter_expand16(AdapterArgs a, int tiles
     for (int h = 0; h < 2; ++h) {
         const int r = (threadIdx.x >> 4) + 16 * h, row = m0 + r;
         if (row >= a.tokens || left <= 0) continue;
-        const float* base = a.base + (size_t)row * (size_t)a.ld_base + c;
         f32x4 v = {0.f, 0.f, 0.f, 0.f};
-        if (left >= 4) __builtin_memcpy(&v, base, 16);
-        else
+        for (int k = 0; k < a.slices; ++k) {
+            const float* base = a.base + ((size_t)k * a.tokens + row) * (size_t)a.ld_base + c;
+            f32x4 b = {0.f, 0.f, 0.f, 0.f};
+            if (left >= 4) __builtin_memcpy(&b, base, 16);
+            else
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-                if (e < left) v[e] = base[e];
+                for (int e = 0; e < 4; ++e)
+                    if (e < left) b[e] = base[e];
+            v += b;
+        }
 #pragma unroll
         for (int w = 0; w < 4; ++w) v += *reinterpret_cast<const f32x4*>(&sums[w][r][(threadIdx.x & 15) * 4]);
         const size_t at = (size_t)row * (size_t)a.ldo + c;

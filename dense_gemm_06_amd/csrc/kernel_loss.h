@@ -8,6 +8,7 @@
 // turned for the product with x.
 #pragma once
 #include "device_common.h"
+#include "kernel_mid.h"
 #include "kernel_skinny.h"
 #include "kernel_sp.h"
 #include "layers.h"
@@ -34,15 +35,16 @@ struct LossStatsHook {
     const int64_t* target;
     LossPart* part;   // strips x tokens
     float* picked;
-    int tokens, n;    // columns
+    int tokens, n, v0;   // columns, and the first one's word
 
-    template <int SJ>
-    __device__ __forceinline__ void finish(f32x16 (&acc)[4][SJ], int m0, int n0, int wm, int wn, char* lds, char*) const {
+    template <int SI, int SJ, int WM, int WN>
+    __device__ __forceinline__ void finish(f32x16 (&acc)[SI][SJ], int m0, int n0, int wm, int wn, char* lds, char*) const {
+        constexpr int ROWS = WM * 32 * SI, COLS = WN * 32 * SJ;
         const int lane = threadIdx.x & 63, l32 = lane & 31, lh = lane >> 5;
-        LossPart* joined = reinterpret_cast<LossPart*>(lds);  // waves along n x 256 rows
+        LossPart* joined = reinterpret_cast<LossPart*>(lds);  // waves along n x rows
         const bool cut = n0 + 32 * SJ > n;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < SI; ++i) {
             const int row = m0 + 32 * i + l32;
             float m = -INFINITY, s = 0.0f;
             if (cut) {
@@ -69,7 +71,7 @@ struct LossStatsHook {
 #pragma unroll
                     for (int r = 0; r < 16; ++r) s += __builtin_amdgcn_exp2f(fmaf(acc[i][j][r], kLog2e, c));
             }
-            const int64_t at = row < tokens ? target[row] - n0 : -1;
+            const int64_t at = row < tokens ? target[row] - v0 - n0 : -1;
             const bool has = at >= 0 && at < 32 * SJ;
             if (__any(has)) {
                 const int t = has ? (int)at - 4 * lh : -1;
@@ -86,15 +88,15 @@ struct LossStatsHook {
                 if (mine && n0 + at < n) picked[row] = v;
             }
             loss_join(m, s, __shfl_xor(m, 32), __shfl_xor(s, 32));
-            if (lh == 0) joined[wn * 256 + wm * 128 + 32 * i + l32] = {m, s};
+            if (lh == 0) joined[wn * ROWS + wm * (32 * SI) + 32 * i + l32] = {m, s};
         }
         __syncthreads();
-        const int r = threadIdx.x, row = m0 - wm * 128 + r;
-        if (r < 256 && row < tokens) {
+        const int r = threadIdx.x, row = m0 - wm * (32 * SI) + r;
+        if (r < ROWS && row < tokens) {
             float m = joined[r].m, s = joined[r].s;
 #pragma unroll
-            for (int w = 1; w < 8 / SJ; ++w) loss_join(m, s, joined[w * 256 + r].m, joined[w * 256 + r].s);
-            part[(size_t)((n0 - wn * 32 * SJ) >> 8) * (size_t)tokens + row] = {m, s};
+            for (int w = 1; w < WN; ++w) loss_join(m, s, joined[w * ROWS + r].m, joined[w * ROWS + r].s);
+            part[(size_t)((n0 - wn * 32 * SJ) / COLS) * (size_t)tokens + row] = {m, s};
         }
     }
 };
@@ -154,9 +156,9 @@ static __global__ __launch_bounds__(1024) void loss_finish(const LossPart* part,
     loss[t] = k >= 0 && k < vocabulary ? l - picked[t] : 0.0f;
 }
 
-// d of a tile through LDS as 16-bit rows of 256: row r of a half of 128 at byte 512 r, its 16-byte
-// pieces permuted by r, so that neither the writes (32 rows of one piece) nor the whole-row reads
-// meet in a bank.
+// d of a tile through LDS as 16-bit rows (a half of the tile's rows to each half of LDS), their
+// 16-byte pieces permuted by the row, so that neither the writes (32 rows of one piece) nor the
+// whole-row reads meet in a bank.
 template <int DT>
 struct LossGradHook {
     static constexpr bool kReplace = true, kAdd = false;
@@ -169,14 +171,16 @@ struct LossGradHook {
     int64_t ldd, lddt;
     int tokens, n, v0, vocabulary;
 
-    template <int SJ>
-    __device__ __forceinline__ void finish(f32x16 (&acc)[4][SJ], int m0, int n0, int wm, int wn, char* lds,
+    template <int SI, int SJ, int WM, int WN>
+    __device__ __forceinline__ void finish(f32x16 (&acc)[SI][SJ], int m0, int n0, int wm, int wn, char* lds,
                                            char* lds2) const {
+        static_assert(WM == 2, "a half of LDS for each");
+        constexpr int HALF = 32 * SI, COLS = WN * 32 * SJ, PITCH = COLS * 2, PM = COLS / 8 - 1, WAVES = WM * WN;
         const int lane = threadIdx.x & 63, l32 = lane & 31, lh = lane >> 5;
         char* half = wm == 0 ? lds : lds2;
         const float f = factor ? factor[0] : 1.0f;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < SI; ++i) {
             const int row = m0 + 32 * i + l32, r = 32 * i + l32;
             int64_t at = -1;
             float g = 0.0f, c = 0.0f;
@@ -194,7 +198,7 @@ struct LossGradHook {
             const int t = at >= 0 && at < 32 * SJ ? (int)at - 4 * lh : -1;
 #pragma unroll
             for (int j = 0; j < SJ; ++j) {
-                asm volatile("" : "+a"(acc[i][j]));
+                if constexpr (SI == 4) asm volatile("" : "+a"(acc[i][j]));  // see full_epilogue
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
                     uint32_t h[4];
@@ -206,19 +210,21 @@ struct LossGradHook {
                                             : (uint32_t)f32_to_bf16_rne(v);
                     }
                     const int piece = wn * (4 * SJ) + 4 * j + q;
-                    *reinterpret_cast<u32x2*>(half + r * 512 + ((piece ^ (r & 31)) << 4) + 8 * lh) =
+                    *reinterpret_cast<u32x2*>(half + r * PITCH + ((piece ^ (r & PM)) << 4) + 8 * lh) =
                         u32x2{h[0] | (h[1] << 16), h[2] | (h[3] << 16)};
                 }
             }
         }
         __syncthreads();
-        const int wave = threadIdx.x >> 6, tile_m = m0 - wm * 128, tile_n = n0 - wn * 32 * SJ;
+        const int wave = threadIdx.x >> 6, tile_m = m0 - wm * HALF, tile_n = n0 - wn * 32 * SJ;
+        auto at = [&](int r, int piece) { return (r < HALF ? lds : lds2) + (r % HALF) * PITCH + ((piece ^ (r & PM)) << 4); };
         if (d) {
-            const int c = tile_n + 8 * l32, left = n - c;
-            for (int it = 0; it < 16; ++it) {
-                const int r = wave * 32 + 2 * it + lh, row = tile_m + r, rr = r & 127;
+            constexpr int RI = 64 / (COLS / 8), IT = 2 * HALF / WAVES / RI;  // rows of a load, loads of a wave
+            const int piece = lane % (COLS / 8), c = tile_n + 8 * piece, left = n - c;
+            for (int it = 0; it < IT; ++it) {
+                const int r = wave * (2 * HALF / WAVES) + RI * it + lane / (COLS / 8), row = tile_m + r;
                 if (row >= tokens || left <= 0) continue;
-                const u32x4 v = *reinterpret_cast<const u32x4*>((r < 128 ? lds : lds2) + rr * 512 + ((l32 ^ (rr & 31)) << 4));
+                const u32x4 v = *reinterpret_cast<const u32x4*>(at(r, piece));
                 uint16_t* dst = d + (size_t)row * (size_t)ldd + c;
                 if (left >= 8) __builtin_memcpy(dst, &v, 16);
                 else
@@ -229,15 +235,16 @@ struct LossGradHook {
         }
         if (dt) {
             // a wave: 32 columns, 32 rows at a time: 16 lanes get eight rows of 16 columns
+            static_assert(COLS / WAVES == 32, "columns of a wave");
             const int l16 = lane & 15, lg = lane >> 4;
 #pragma unroll 2
-            for (int it = 0; it < 16; ++it) {
+            for (int it = 0; it < 2 * (2 * HALF / 32); ++it) {
                 const int cb = wave * 32 + 16 * (it & 1), rb = 32 * (it >> 1) + 8 * lg;
                 u32x4 v;
 #pragma unroll
                 for (int hh = 0; hh < 2; ++hh) {
-                    const int r = rb + 4 * hh + (l16 >> 2), rr = r & 127, col = cb + 4 * (l16 & 3);
-                    char* p = (r < 128 ? lds : lds2) + rr * 512 + (((col >> 3) ^ (rr & 31)) << 4) + (col & 7) * 2;
+                    const int col = cb + 4 * (l16 & 3);
+                    char* p = at(rb + 4 * hh + (l16 >> 2), col >> 3) + (col & 7) * 2;
                     const u32x2 x = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4f16(DG_LDS_PTR(fp16x4_t, p)));
                     v[2 * hh] = x[0];
                     v[2 * hh + 1] = x[1];
@@ -258,6 +265,19 @@ template <int DT, bool REG>
 __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) void loss_grad_tiles(GemmArgs g,
                                                                                                  LossGradHook<DT> h) {
     mfma32_sp_body<DT, 1, 8, REG, false, false>(g, nullptr, h);
+}
+
+template <int DT>
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) void loss_mid(MidArgs g, LossStatsHook h) {
+    __shared__ __attribute__((aligned(1024))) MidLds lds;
+    mid_body<DT>(g, lds, h);
+}
+
+template <int DT>
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) void loss_grad_mid(MidArgs g,
+                                                                                               LossGradHook<DT> h) {
+    __shared__ __attribute__((aligned(1024))) MidLds lds;
+    mid_body<DT>(g, lds, h);
 }
 
 }  // namespace dg

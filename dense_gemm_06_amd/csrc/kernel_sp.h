@@ -114,7 +114,7 @@ __device__ __forceinline__ u32x4 keep_first8(u32x4 w, int v) {
 // problems as across tiles. g then holds only xcd_remap (and no fused epilogue).
 //
 // HOOK: what an operator built on the one-tile forms does with a finished wave tile. With
-// kReplace, h.finish(acc, m, n, wm, wn, lds, lds2) takes the accumulators (row 32 i + lane % 32 of
+// kReplace, h.finish<4, SJ, 2, waves along n>(acc, m, n, wm, wn, lds, lds2) takes the accumulators (row 32 i + lane % 32 of
 // the wave tile at row m, columns as laid out at full_epilogue, from column n) in place of the
 // store, with the whole LDS (two halves of 64 KB) to itself; else h.add(acc, m, n) adds to them before it.
 struct NoHook {
@@ -547,7 +547,7 @@ __device__ __forceinline__ void mfma32_sp_body(GemmArgs& g, const GroupArgs* ga,
         asm volatile("s_nop 7\n\ts_nop 7\n\ts_nop 3" ::: "memory");
         __syncthreads();
         if constexpr (HOOK::kReplace) {
-            h.finish(acc, s.m0 + wrow0, s.n0 + wcol0, wm, wn, reinterpret_cast<char*>(&sA[0][0]),
+            h.template finish<4, SJ, 2, WNN>(acc, s.m0 + wrow0, s.n0 + wcol0, wm, wn, reinterpret_cast<char*>(&sA[0][0]),
                      reinterpret_cast<char*>(&sB[0][0]));
             return;
         }

@@ -66,11 +66,12 @@ struct LossProduct {
     const void* w;
     int64_t ldx, ldw;
     int tokens, n, K, group_m, direct;
+    int strip;              // columns of a part: 256 and 128 (tiles), 16 (few rows)
 };
-struct LossPart;            // a row's maximum and sum over a strip of 256 columns (16 for up to 64 rows)
+struct LossPart;            // a row's maximum and sum over a strip of columns
 constexpr int64_t kLossPartBytes = 8;
 DG_16BIT(launch_loss_skinny, (const LossProduct& p, const int64_t* target, void* part, float* picked, hipStream_t s))
-DG_16BIT(launch_loss_tiles, (const LossProduct& p, const int64_t* target, void* part, float* picked, hipStream_t s))
+DG_16BIT(launch_loss_tiles, (const LossProduct& p, int v0, const int64_t* target, void* part, float* picked, hipStream_t s))
 DG_16BIT(launch_loss_grad_tiles, (const LossProduct& p, const LossArgs& a, hipStream_t s))
 int launch_loss_finish(const void* part, int strips, int tokens, const int64_t* target, int vocabulary,
                        const float* picked, float* loss, float* lse, hipStream_t s);
@@ -101,6 +102,7 @@ struct AdapterArgs {
     // expand: out = base + scale u m
     const float* base;
     int64_t ld_base;
+    int slices;             // of base, tokens rows apart
     void* out;
     int64_t ldo;
     // gradient: plan
@@ -138,6 +140,8 @@ DG_16BIT(launch_adapter_skinny, (const AdapterProduct& p, const AdapterArgs& a, 
 // the same through `slices` of k (direct rows): u and part (slices x tokens x cols rounded up to 4)
 DG_16BIT(launch_adapter_decode, (const AdapterProduct& p, const AdapterArgs& u, const AdapterArgs& a, int slices, int slice_k, float* part, hipStream_t s))
 DG_16BIT(launch_adapter_tiles, (const AdapterProduct& p, const AdapterArgs& a, int group_m, hipStream_t s))
+// part (slices x tokens x N rounded up to 4) = x w^T over slices of k, in 128 x 128 tiles (direct rows)
+DG_16BIT(launch_mid_part, (const AdapterProduct& p, int tokens, int group_m, int slices, int slice_k, float* part, hipStream_t s))
 // the operators below, m with its long direction along memory in shrink and across it in expand
 DG_16BIT(launch_adapter_shrink_row, (const AdapterArgs& a, hipStream_t s))
 // through part (slices x tokens x rank_p): u, us. direct: 16-byte rows

@@ -97,7 +97,7 @@ int check_adapters(const gemm_adapter_set* s, int64_t N, int64_t K) {
 
 int check_adapter_threads(int64_t tokens, int64_t cols, int64_t rank, int dtype) {
     if (dtype == GEMM_F32) return check_threads("tokens * rank", tokens, rank, 64);
-    return check_threads("blocks of tokens * columns", ceil_div(tokens, 32), ceil_div(cols, 256), 256);
+    return check_threads("blocks of tokens * columns", ceil_div(tokens, 32), ceil_div(cols, 64), 256);
 }
 
 Range a_range(const gemm_adapter_set& s, int64_t K, int64_t es) {
@@ -148,9 +148,9 @@ constexpr int64_t kSkinny = 64;
 // the adapters to the product in its tiles.
 bool adapter_tiles(int64_t tokens, int64_t cols) { return ceil_div(tokens, 256) * ceil_div(cols, 256) >= 128; }
 
-int tile_group(int64_t rows, int64_t cols) {
-    const int64_t m = ceil_div(rows, 256);
-    return (int)std::max<int64_t>(1, std::min<int64_t>(dg::default_group_m(m, ceil_div(cols, 256)), m));
+int tile_group(int64_t rows, int64_t cols, int64_t tile = 256) {
+    const int64_t m = ceil_div(rows, tile);
+    return (int)std::max<int64_t>(1, std::min<int64_t>(dg::default_group_m(m, ceil_div(cols, tile)), m));
 }
 
 // How the kernels on 16-bit matrices read x (rows x len) and w (op T: cols x len, op N: len x cols):
@@ -177,6 +177,7 @@ Slices slices_of(int64_t tiles, int64_t K) {
 
 
 struct AdapterSpace {
+    Slices mid = {0, 0};      // of the shared product in 128 x 128 tiles
     float* base = nullptr;    // the shared product (16-bit matrices without a kernel for both)
     void* product = nullptr;
     float* part = nullptr;    // sums of slices of k
@@ -197,9 +198,12 @@ void shrink_space(AdapterSpace& s, Parts& p, int64_t tokens, int64_t len, int64_
     s.us = static_cast<uint16_t*>(p.take(tokens * rank_padded(rank) * 4));
 }
 
-void product_space(AdapterSpace& s, Parts& p, int64_t tokens, int64_t cols, int dtype, bool one_kernel) {
+void product_space(AdapterSpace& s, Parts& p, int64_t tokens, int64_t cols, int64_t len, int dtype, bool one_kernel) {
     if (one_kernel) return;
-    if (dtype != GEMM_F32) s.base = static_cast<float*>(p.take(tokens * cols * 4));
+    if (dtype != GEMM_F32) {
+        s.mid = slices_of(ceil_div(tokens, 128) * ceil_div(cols, 128), len);
+        s.base = static_cast<float*>(p.take(s.mid.count * tokens * ceil_div(cols, 4) * 16));
+    }
     s.product = p.take(kProductWorkspace);
 }
 
@@ -217,7 +221,7 @@ AdapterSpace adapter_space(void* workspace, int64_t tokens, int64_t N, int64_t K
         s.slices = slices_of(ceil_div(N, 64), K);
         s.part = static_cast<float*>(p.take(s.slices.count * tokens * ceil_div(N, 4) * 16));
     } else {
-        product_space(s, p, tokens, N, dtype, in_tiles(tokens, N, K, dtype));
+        product_space(s, p, tokens, N, K, dtype, in_tiles(tokens, N, K, dtype));
         if (dtype != GEMM_F32) shrink_space(s, p, tokens, K, rank);
     }
     s.bytes = p.at;
@@ -228,7 +232,7 @@ AdapterSpace adapter_backward_space(void* workspace, int64_t tokens, int64_t N, 
                                     int64_t rank, int dtype) {
     AdapterSpace s;
     Parts p{static_cast<char*>(workspace)};
-    product_space(s, p, tokens, K, dtype, in_tiles(tokens, K, N, dtype));
+    product_space(s, p, tokens, K, N, dtype, in_tiles(tokens, K, N, dtype));
     s.v = static_cast<float*>(p.take(tokens * rank * 4));
     if (dtype != GEMM_F32) {
         shrink_space(s, p, tokens, N, rank);
@@ -260,10 +264,12 @@ int shrink16(const dg::AdapterArgs& a, const AdapterSpace& sp, int dtype, hipStr
 // ---------------------------------------------------------------- loss
 constexpr int64_t kPieceBytes = (int64_t)128 << 20;
 
-// Columns of a piece: whole blocks of 256, as many as kPieceBytes hold.
+// Columns of a piece: whole blocks of 256, as many as kPieceBytes hold, and of those as many as
+// make whole rounds of 256 x 256 tiles.
 int64_t piece_of(int64_t tokens, int64_t vocabulary, int64_t each) {
-    const int64_t n = kPieceBytes / std::max<int64_t>(1, tokens * each);
-    return std::max<int64_t>(1, std::min(std::max<int64_t>(256, n / 256 * 256), vocabulary));
+    const int64_t blocks = std::max<int64_t>(1, kPieceBytes / std::max<int64_t>(1, tokens * each) / 256);
+    const int64_t tm = std::max<int64_t>(1, ceil_div(tokens, 256)), rounds = tm * blocks / dg::kCus;
+    return std::max<int64_t>(1, std::min((rounds > 0 ? rounds * dg::kCus / tm : blocks) * 256, vocabulary));
 }
 
 struct LossSpace {
@@ -283,13 +289,34 @@ struct LossSpace {
 
 // 16-bit logits are never stored but for the shortest sums.
 bool loss_fused(int64_t vocabulary, int64_t K, int dtype) { return dtype != GEMM_F32 && K >= 8 && vocabulary > 0; }
-int64_t loss_strip(int64_t tokens) { return tokens <= kSkinny ? 16 : 256; }
+// How tokens x n logits are cut into tiles: the first `wide` columns in 256 x 256 ones, the rest in
+// 128 x 128 ones; up to 64 tokens need none. A round of 256 wide tiles takes about as long as three
+// of narrow ones (2048 long, 32768 columns: 62 us for 256 wide tiles, 31 for 256 narrow ones and 62
+// for 768), so a last round of few wide tiles, and wide tiles that are mostly empty, are done better
+// by narrow ones.
+struct LossTiles {
+    int64_t wide, strips;   // strips: wide ones and narrow ones
+};
+LossTiles loss_tiles(int64_t tokens, int64_t n, bool direct) {
+    const int64_t tm = ceil_div(tokens, 256), tn = ceil_div(n, 256), rounds = tm * tn / dg::kCus;
+    const int64_t part = std::min(tn, rounds * dg::kCus / tm);  // columns of tiles in whole rounds
+    auto narrow = [&](int64_t cols) { return ceil_div(ceil_div(tokens, 128) * ceil_div(cols, 128), dg::kCus); };
+    const int64_t all_wide = 3 * ceil_div(tm * tn, dg::kCus), all_narrow = narrow(n);
+    const int64_t both = part > 0 && part < tn ? 3 * rounds + narrow(n - part * 256) : all_wide;
+    if (!direct || (all_wide <= all_narrow && all_wide <= both)) return {n, tn};
+    if (all_narrow <= both) return {0, ceil_div(n, 128)};
+    return {part * 256, part + ceil_div(n - part * 256, 128)};
+}
+int64_t loss_strips(int64_t tokens, int64_t vocabulary) {
+    // either way of reading, the narrow tiles of all columns at the most
+    return tokens <= kSkinny ? ceil_div(vocabulary, 16) : ceil_div(vocabulary, 128);
+}
 
 LossSpace loss_space(void* workspace, int64_t tokens, int64_t vocabulary, int64_t K, int dtype) {
     LossSpace s;
     Parts p{static_cast<char*>(workspace)};
     if (loss_fused(vocabulary, K, dtype)) {
-        s.part = p.take(ceil_div(vocabulary, loss_strip(tokens)) * tokens * dg::kLossPartBytes);
+        s.part = p.take(loss_strips(tokens, vocabulary) * tokens * dg::kLossPartBytes);
         s.picked = static_cast<float*>(p.take(tokens * 4));
         s.bytes = p.at;
         return s;
@@ -323,9 +350,9 @@ LossSpace loss_backward_space(void* workspace, int64_t tokens, int64_t vocabular
 }
 
 dg::LossProduct loss_product(const void* x, int64_t ldx, const void* w, int64_t ldw, int64_t tokens, int64_t n,
-                             int64_t K, int dtype) {
-    return {x, w, ldx, ldw, (int)tokens, (int)n, (int)K, tile_group(tokens, n),
-            tiles_form(x, ldx, w, ldw, n, K, GEMM_OP_T, dtype) == 2};
+                             int64_t K, int dtype, int64_t tile) {
+    return {x, w, ldx, ldw, (int)tokens, (int)n, (int)K, tile_group(tokens, n, tile),
+            tiles_form(x, ldx, w, ldw, n, K, GEMM_OP_T, dtype) == 2, (int)tile};
 }
 
 // ---------------------------------------------------------------- activations
@@ -429,8 +456,17 @@ int gemm_adapters_product(const void* x, int64_t tokens, int64_t K, int64_t ldx,
     if (few) return launched(DG_BY_TYPE(launch_adapter_skinny, dtype, p, b, s), "adapters' products");
     if (in_tiles(tokens, N, K, dtype))
         return launched(DG_BY_TYPE(launch_adapter_tiles, dtype, p, b, tile_group(tokens, N), s), "adapters' products");
-    float* base = dtype == GEMM_F32 ? static_cast<float*>(y) : sp.base;
-    const int64_t ldb = dtype == GEMM_F32 ? ldy : N;
+    b.slices = 1;
+    if (form == 2) {
+        DG_TRY(launched(DG_BY_TYPE(launch_mid_part, dtype, p, (int)tokens, tile_group(tokens, N, 128), (int)sp.mid.count,
+                                   (int)sp.mid.k, sp.base, s), "adapters' shared product"));
+        b.base = sp.base;
+        b.ld_base = ceil_div(N, 4) * 4;
+        b.slices = (int)sp.mid.count;
+        return launched(DG_BY_TYPE(launch_adapter_expand16, dtype, b, s), "adapters' second product");
+    }
+    float* base = wide ? static_cast<float*>(y) : sp.base;
+    const int64_t ldb = wide ? ldy : N;
     DG_TRY(product(GEMM_OP_T, tokens, N, K, x, ldx, w, ldw, base, ldb, dtype, GEMM_F32, 0.0f, sp.product,
                    kProductWorkspace, stream));
     b.base = base;
@@ -564,6 +600,7 @@ int gemm_adapters_backward(const void* grad, int64_t tokens, int64_t N, int64_t 
                            kProductWorkspace, stream));
             a.base = base;
             a.ld_base = ldb;
+            a.slices = 1;
             DG_TRY(launched(wide ? dg::launch_adapter_expand(a, dtype, s) : DG_BY_TYPE(launch_adapter_expand16, dtype, a, s),
                             "adapters' x_grad"));
         }
@@ -644,16 +681,30 @@ int gemm_loss(const void* x, int64_t tokens, int64_t K, int64_t ldx, const void*
                           range("target", target, n4 * 2)}));
     DG_TRY(check_threads("tokens", tokens, 1, 256));
     DG_TRY(check_threads("tiles of tokens * vocabulary", ceil_div(tokens, 256),
-                         ceil_div(vocabulary, loss_strip(tokens)), 512));
+                         ceil_div(vocabulary, tokens <= kSkinny ? 16 : 256), 512));
     DG_TRY(check_device());
     if (sp.part) {
         const hipStream_t s = (hipStream_t)stream;
-        const dg::LossProduct p = loss_product(x, ldx, w, ldw, tokens, vocabulary, K, dtype);
-        DG_TRY(launched(tokens <= kSkinny ? DG_BY_TYPE(launch_loss_skinny, dtype, p, target, sp.part, sp.picked, s)
-                                          : DG_BY_TYPE(launch_loss_tiles, dtype, p, target, sp.part, sp.picked, s),
-                        "loss"));
-        return launched(dg::launch_loss_finish(sp.part, (int)ceil_div(vocabulary, loss_strip(tokens)), (int)tokens,
-                                               target, (int)vocabulary, sp.picked, loss, lse, s), "loss");
+        int64_t strips = loss_strips(tokens, vocabulary);
+        if (tokens <= kSkinny) {
+            const dg::LossProduct p = loss_product(x, ldx, w, ldw, tokens, vocabulary, K, dtype, 256);
+            DG_TRY(launched(DG_BY_TYPE(launch_loss_skinny, dtype, p, target, sp.part, sp.picked, s), "loss"));
+        } else {
+            const LossTiles t = loss_tiles(tokens, vocabulary, whole_pieces(x, ldx, K) && whole_pieces(w, ldw, K));
+            strips = t.strips;
+            if (t.wide > 0) {
+                const dg::LossProduct p = loss_product(x, ldx, w, ldw, tokens, t.wide, K, dtype, 256);
+                DG_TRY(launched(DG_BY_TYPE(launch_loss_tiles, dtype, p, 0, target, sp.part, sp.picked, s), "loss"));
+            }
+            if (t.wide < vocabulary) {
+                const dg::LossProduct p = loss_product(x, ldx, static_cast<const char*>(w) + (size_t)t.wide * ldw * es, ldw,
+                                                       tokens, vocabulary - t.wide, K, dtype, 128);
+                void* part = static_cast<char*>(sp.part) + t.wide / 256 * tokens * dg::kLossPartBytes;
+                DG_TRY(launched(DG_BY_TYPE(launch_loss_tiles, dtype, p, (int)t.wide, target, part, sp.picked, s), "loss"));
+            }
+        }
+        return launched(dg::launch_loss_finish(sp.part, (int)strips, (int)tokens, target, (int)vocabulary, sp.picked,
+                                               loss, lse, s), "loss");
     }
     dg::LossArgs a;
     memset(&a, 0, sizeof a);
@@ -753,7 +804,9 @@ int gemm_loss_backward(const float* grad, const void* x, int64_t tokens, int64_t
                                sp.product, kProductWorkspace, stream));
                 DG_TRY(launched(dg::launch_loss_grad(a, dtype, s), "loss gradient"));
             } else {
-                const dg::LossProduct p = loss_product(x, ldx, wp, ldw, tokens, a.n, K, dtype);
+                const bool direct = whole_pieces(x, ldx, K) && whole_pieces(wp, ldw, K);
+                const dg::LossProduct p = loss_product(x, ldx, wp, ldw, tokens, a.n, K, dtype,
+                                                       loss_tiles(tokens, a.n, direct).wide > 0 ? 256 : 128);
                 DG_TRY(launched(DG_BY_TYPE(launch_loss_grad_tiles, dtype, p, a, s), "loss gradient"));
             }
         }
