@@ -10,6 +10,7 @@
 #include "device_common.h"
 #include "kernel_mid.h"
 #include "kernel_skinny.h"
+#include "kernel_stream.h"
 #include "kernel_sp.h"
 #include "layers.h"
 
@@ -126,6 +127,21 @@ struct LossSkinnyEpi {
         if (t < tokens && (threadIdx.x & 63) < 16) part[(size_t)(c >> 4) * (size_t)tokens + t] = {m, s};
     }
 };
+
+// Few rows x against a stream of w, 64 words to a workgroup.
+template <int DT, int TT>
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) void loss_stream(StreamArgs a,
+                                                                                             LossSkinnyEpi epi) {
+    __shared__ __attribute__((aligned(1024))) StreamLds<TT> lds;
+    f32x4 acc[TT];
+#pragma unroll
+    for (int t = 0; t < TT; ++t) acc[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+    const int r0 = (int)blockIdx.x * kStreamRows, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    stream_sum<DT, TT, true>(acc, a, lds, r0, 0, a.K);
+    if (r0 + 16 * wave >= a.rows) return;
+#pragma unroll
+    for (int t = 0; t < TT; ++t) epi(16 * t + (lane & 15), r0 + 16 * wave + 4 * (lane >> 4), acc[t]);
+}
 
 // Joins the strips of each row. A workgroup has `width` tokens (a power of two up to 64) and as
 // many threads to each as are left.

@@ -19,6 +19,7 @@ itself (examples/adapter_step.py) or from its own torch.autograd.Function.
 from __future__ import annotations
 
 import ctypes
+import functools
 
 import dense_gemm_06_amd as _dg
 
@@ -75,6 +76,12 @@ def _lib():
     return _dg._lib or _dg.library()
 
 
+@functools.lru_cache(maxsize=1024)
+def _bytes(name, *sizes):
+    """A workspace's size, which the call's sizes and type alone tell."""
+    return getattr(_lib(), name)(*sizes)
+
+
 def _work(n, device):
     """A workspace of n bytes, which the caller keeps until the call is made (None for 0), and its address."""
     if not n:
@@ -95,28 +102,30 @@ def _same(t, what, dtype, shape):
 # ----------------------------------------------------------------------------- adapters
 def _batch(t, what):
     """Leading dimension and batch stride of a 3-D tensor."""
-    ld = _ld(t.shape, t.stride(), what)
-    if t.shape[0] > 1 and t.stride(0) < 0:
-        raise ValueError(f"{what}: negative strides")
-    return ld, t.stride(0) if t.shape[0] > 1 else 0
+    shape, strides = t.shape, t.stride()
+    if len(shape) != 3:
+        raise ValueError(f"{what} must be 3-D, not {tuple(shape)}")
+    ld = strides[1] if strides[2] == 1 and strides[1] >= shape[2] > 0 else _ld(shape, strides, what)
+    return ld, strides[0] if shape[0] > 1 else 0
 
 
 def _adapters(x, w, a, b, index, scale):
     """The call's type, leading dimensions of x and w, the set, index's pointer and the sizes."""
-    code = _wide_type(x.dtype, "x")
+    dt = x.dtype
+    code = _wide_type(dt, "x")
+    if w.dtype != dt or a.dtype != dt or b.dtype != dt:
+        raise TypeError(f"x, w, a and b must share one dtype, not {dt}, {w.dtype}, {a.dtype} and {b.dtype}")
     ldx, ldw = _matrix(x, "x"), _matrix(w, "w")
-    (T, K), N = x.shape, w.shape[0]
-    if w.dtype != x.dtype or a.dtype != x.dtype or b.dtype != x.dtype:
-        raise TypeError(f"x, w, a and b must share one dtype, not {x.dtype}, {w.dtype}, {a.dtype} and {b.dtype}")
-    if a.dim() != 3 or b.dim() != 3:
-        raise ValueError(f"a and b must be 3-D, not {tuple(a.shape)} and {tuple(b.shape)}")
-    R, rank = a.shape[0], a.shape[1]
-    if w.shape[1] != K or a.shape[2] != K or tuple(b.shape) != (R, N, rank):
-        raise ValueError(f"shape mismatch: x {tuple(x.shape)}, w {tuple(w.shape)}, a {tuple(a.shape)}, b {tuple(b.shape)}")
     (lda, sa), (ldb, sb) = _batch(a, "a"), _batch(b, "b")
-    s = _array(scale, "scale", torch.float32, (R,)) if scale is not None else None
+    (T, K), N = x.shape, w.shape[0]
+    R, rank, Ka = a.shape
+    if w.shape[1] != K or Ka != K or b.shape != (R, N, rank):
+        raise ValueError(f"shape mismatch: x {tuple(x.shape)}, w {tuple(w.shape)}, a {tuple(a.shape)}, b {tuple(b.shape)}")
     i = _array(index, "index", torch.int32, (T,))
-    at = _device(x, w, a, b, index) if scale is None else _device(x, w, a, b, index, scale)
+    if scale is None:
+        s, at = None, _device(x, w, a, b, index)
+    else:
+        s, at = _array(scale, "scale", torch.float32, (R,)), _device(x, w, a, b, index, scale)
     adapters = gemm_adapter_set(a.data_ptr(), b.data_ptr(), s, R, rank, lda, sa, ldb, sb)
     return code, ldx, ldw, adapters, i, at, (T, N, K, R, rank)
 
@@ -130,12 +139,13 @@ def gemm_adapters_tensors(x, w, a, b, index, scale=None, keep=False):
     code, ldx, ldw, adapters, i, at, (T, N, K, R, rank) = _adapters(x, w, a, b, index, scale)
     dev = x.device
     y = torch.empty((T, N), dtype=x.dtype, device=dev)
-    u = torch.empty((T, rank), dtype=torch.float32, device=dev)
+    u = torch.empty((T, rank), dtype=torch.float32, device=dev) if keep else None
     if T:
-        n = _lib().gemm_adapters_workspace(T, N, K, rank, code)
-        work, wp = _work(n, dev)
+        n = _bytes("gemm_adapters_workspace", T, N, K, rank, code)
+        head = 0 if keep else -(-T * rank // 64) * 256  # u lies before the workspace where it is not kept
+        work, wp = _work(head + n, dev)
         _call("gemm_adapters_product", at, x.data_ptr(), T, K, ldx, w.data_ptr(), N, ldw, code, adapters, i,
-              y.data_ptr(), N or 1, u.data_ptr(), wp, n)
+              y.data_ptr(), N or 1, u.data_ptr() if keep else wp, wp + head if n else None, n)
     return (y, u) if keep else y
 
 
@@ -161,7 +171,7 @@ def gemm_adapters_backward_tensors(grad, x, u, w, a, b, index, plan, scale=None,
     xg = torch.empty((T, K), dtype=x.dtype, device=dev) if x_grad else None
     ag = torch.empty((R, rank, K), dtype=x.dtype, device=dev)
     bg = torch.empty((R, N, rank), dtype=x.dtype, device=dev)
-    n = _lib().gemm_adapters_backward_workspace(T, N, K, R, rank, code)
+    n = _bytes("gemm_adapters_backward_workspace", T, N, K, R, rank, code)
     work, wp = _work(n, dev)
     _call("gemm_adapters_backward", at, grad.data_ptr(), T, N, ldg, x.data_ptr(), K, ldx, up, w.data_ptr(), ldw, code,
           adapters, i, p, xg.data_ptr() if x_grad else None, K or 1, ag.data_ptr(), bg.data_ptr(), wp, n)
@@ -191,7 +201,7 @@ def gemm_loss_tensors(x, w, target):
     loss = torch.empty(T, dtype=torch.float32, device=dev)
     lse = torch.empty(T, dtype=torch.float32, device=dev)
     if T:
-        n = _lib().gemm_loss_workspace(T, V, K, code)
+        n = _bytes("gemm_loss_workspace", T, V, K, code)
         work, wp = _work(n, dev)
         _call("gemm_loss", at, x.data_ptr(), T, K, ldx, w.data_ptr(), V, ldw, code, t, loss.data_ptr(),
               lse.data_ptr(), wp, n)
@@ -212,7 +222,7 @@ def gemm_loss_backward_tensors(grad, x, w, target, lse, x_grad=True, w_grad=True
         raise ValueError(f"piece = {piece} must be non-negative")
     xg = torch.empty((T, K), dtype=x.dtype, device=dev) if x_grad else None
     wg = torch.empty((V, K), dtype=x.dtype, device=dev) if w_grad else None
-    n = _lib().gemm_loss_backward_workspace(T, V, K, code, int(x_grad), int(w_grad), piece)
+    n = _bytes("gemm_loss_backward_workspace", T, V, K, code, int(x_grad), int(w_grad), piece)
     work, wp = _work(n, dev)
     _call("gemm_loss_backward", at, g, x.data_ptr(), T, K, ldx, w.data_ptr(), V, ldw, code, t, l,
           xg.data_ptr() if x_grad else None, K or 1, wg.data_ptr() if w_grad else None, K or 1, piece,
