@@ -137,20 +137,127 @@ __device__ __forceinline__ void adapter_add(f32x16 (&acc)[SJ], int m0, int n0, c
 }
 
 // ---------------------------------------------------------------- shared product and adapters in one
-template <int DT>
+// Up to rank 64, a tile's u (256 rows, hi and lo) and an adapter's rows of m (256 columns) are
+// brought to LDS by all waves together, whole lines at a time: fragments loaded by each wave
+// straight from memory touch a line for every two lanes, and each is loaded by several waves. The
+// adapters among 32 rows of each half of the tile take turns.
+// 16-byte piece c of row r of `pieces` pieces lies at piece c ^ swz: reads of 32 rows meet in no bank.
+__device__ __forceinline__ int rank_swz(int r, int pieces) {
+    return pieces == 16 ? r & 15 : pieces == 8 ? (r >> 1) & 7 : pieces == 4 ? (r >> 2) & 3 : (r >> 3) & 1;
+}
+
+template <int DT, bool STAGED>
 struct AdapterHook {
     static constexpr bool kReplace = false, kAdd = true;
     AdapterArgs a;
-    template <int SJ>
-    __device__ __forceinline__ void add(f32x16 (&acc)[4][SJ], int m, int n) const {
+    template <int SI, int SJ, int WM, int WN>
+    __device__ __forceinline__ void add(f32x16 (&acc)[SI][SJ], int m0, int n0, int wm, int wn, char* us_lds,
+                                        char* m_lds) const {
+        if constexpr (!STAGED) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) adapter_add<DT, SJ>(acc[i], m + 32 * i, n, a);
+            for (int i = 0; i < SI; ++i)
+                adapter_add<DT, SJ>(acc[i], m0 + wm * 32 * SI + 32 * i, n0 + wn * 32 * SJ, a);
+            return;
+        }
+        constexpr int ROWS = WM * 32 * SI, COLS = WN * 32 * SJ, THREADS = WM * WN * 64;
+        static_assert(WM == 2, "halves of the tile");
+        const int tid = threadIdx.x, lane = tid & 63, l32 = lane & 31, lh = lane >> 5;
+        const int mp = a.rank_p / 8, up = 2 * mp;  // pieces of a row of m, of u
+        const int lmp = 31 - __builtin_clz(mp);
+        // lanes 0-31: rows 32 b .. of the tile's first half, 32-63: of its second; the same in all waves
+        int of[SI];
+#pragma unroll
+        for (int b = 0; b < SI; ++b) {
+            const int row = m0 + lh * (32 * SI) + 32 * b + l32;
+            of[b] = row < a.tokens ? a.index[row] : -1;
+        }
+#pragma unroll
+        for (int b = 0; b < SI; ++b) of[b] = of[b] >= a.adapters ? -1 : of[b];
+        // n pieces, four loads of a thread in flight
+        auto bring = [&](int n, auto load, char* to, int lp) {
+            const int pieces = 1 << lp;
+            for (int e = tid; e < n; e += 4 * THREADS) {
+                u32x4 v[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const int at = min(e + k * THREADS, n - 1);
+                    v[k] = load(at >> lp, at & (pieces - 1));
+                }
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const int at = e + k * THREADS, r = at >> lp, c = at & (pieces - 1);
+                    if (at < n) *reinterpret_cast<u32x4*>(to + (size_t)(r * pieces + (c ^ rank_swz(r, pieces))) * 16) = v[k];
+                }
+            }
+        };
+        bring(
+            ROWS * up,
+            [&](int r, int c) {
+                u32x4 v;
+                __builtin_memcpy(&v, a.us + (size_t)min(m0 + r, a.tokens - 1) * (size_t)(2 * a.rank_p) + 8 * c, 16);
+                return v;
+            },
+            us_lds, lmp + 1);
+        // two adapters stay in LDS (2 x 32 KB at rank 64): a tile in which one request ends and the
+        // next begins brings each once
+        int staged[2] = {-1, -1}, next = 0;
+#pragma unroll
+        for (int b = 0; b < SI; ++b) {
+            uint64_t todo = __ballot(of[b] >= 0);
+            while (todo) {
+                const int i = __builtin_amdgcn_readlane(of[b], (int)__builtin_ctzll(todo));
+                const uint64_t rows = __ballot(of[b] == i);
+                todo &= ~rows;
+                int at = staged[0] == i ? 0 : 1;
+                if (staged[0] != i && staged[1] != i) {
+                    at = next;
+                    next ^= 1;
+                    __syncthreads();  // the last reads of that place are done
+                    const uint16_t* m = static_cast<const uint16_t*>(a.m) + (size_t)i * (size_t)a.stride_m;
+                    bring(
+                        COLS * mp,
+                        [&](int r, int c) {
+                            return load_frag8(m + (size_t)min(n0 + r, a.cols - 1) * (size_t)a.ldm + 8 * c,
+                                              a.rank_m - 8 * c);
+                        },
+                        m_lds + at * 32768, lmp);
+                    __syncthreads();
+                    if (at == 0) staged[0] = i;
+                    else staged[1] = i;
+                }
+                const char* m_at = m_lds + at * 32768;
+                const uint32_t own = (uint32_t)(wm == 0 ? rows : rows >> 32);
+                const bool here = (own >> l32) & 1;
+                const int ur = wm * 32 * SI + 32 * b + l32, us = rank_swz(ur, up);
+                const char* u_row = us_lds + (size_t)(ur * up) * 16;
+                f32x16 d[SJ];
+#pragma unroll
+                for (int j = 0; j < SJ; ++j) d[j] = f32x16{};
+                for (int c = own != 0 ? lh : mp; c < mp; c += 2) {
+                    const u32x4 hi = *reinterpret_cast<const u32x4*>(u_row + ((c ^ us) << 4));
+                    const u32x4 lo = *reinterpret_cast<const u32x4*>(u_row + (((mp + c) ^ us) << 4));
+#pragma unroll
+                    for (int j = 0; j < SJ; ++j) {
+                        const int mr = wn * 32 * SJ + 32 * j + l32;
+                        const u32x4 p =
+                            *reinterpret_cast<const u32x4*>(m_at + (size_t)(mr * mp + (c ^ rank_swz(mr, mp))) * 16);
+                        d[j] = mfma_32<DT>(p, hi, d[j]);
+                        d[j] = mfma_32<DT>(p, lo, d[j]);
+                    }
+                }
+#pragma unroll
+                for (int j = 0; j < SJ; ++j)
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) acc[b][j][e] += here ? d[j][e] : 0.0f;
+            }
+        }
+        __syncthreads();
     }
 };
 
-template <int DT, int OPB, bool REG>
+template <int DT, int OPB, bool REG, bool STAGED>
 __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) void adapter_product(
-    GemmArgs g, AdapterHook<DT> h) {
+    GemmArgs g, AdapterHook<DT, STAGED> h) {
     mfma32_sp_body<DT, OPB, 8, REG, false, false>(g, nullptr, h);
 }
 

@@ -193,7 +193,8 @@ struct AdapterSpace {
 
 // What the first product over `len` of 16-bit matrices needs, and the second's u.
 void shrink_space(AdapterSpace& s, Parts& p, int64_t tokens, int64_t len, int64_t rank) {
-    s.slices = slices_of(ceil_div(tokens, 64), len);
+    // half as many as elsewhere: a tile's second adapter has a workgroup of its own, which finds room
+    s.slices = slices_of(2 * ceil_div(tokens, 64), len);
     s.part = static_cast<float*>(p.take(s.slices.count * tokens * rank_padded(rank) * 4));
     s.us = static_cast<uint16_t*>(p.take(tokens * rank_padded(rank) * 4));
 }
