@@ -592,14 +592,14 @@ __device__ __forceinline__ AdapterSpan adapter_span(const AdapterArgs& a, int i)
     return {from, capped_sum(from, max(0, a.counts[i]), a.capacity)};
 }
 
-// A workgroup: 64 columns of z (x or grad) and the whole rank, over an adapter's rows of a chunk
+// A workgroup: 128 columns of z (x or grad) and the whole rank, over an adapter's rows of a chunk
 // (at most kChunkMax) in steps of 32, loaded two steps ahead. z and h (v or u as hi and lo) lie in
 // LDS by rows and are read transposed, so that a lane gets eight consecutive rows of one column.
-constexpr int kChunkMax = 512;
+constexpr int kChunkMax = 512, kGradientCols = 128;
 
 template <int NT>
 struct GradientLds {
-    uint16_t z[2][32 * 64];
+    uint16_t z[2][32 * kGradientCols];
     uint16_t h[2][2][32 * NT * 16];
     int rows[kChunkMax + 64];
 };
@@ -611,7 +611,7 @@ __device__ __forceinline__ void adapter_gradient_body(const AdapterArgs& a, Grad
     constexpr int HP = (HN + 255) / 256;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int l16 = lane & 15, lg = lane >> 4;
-    const int slot = (int)blockIdx.y, c0 = (int)blockIdx.x * 64;
+    const int slot = (int)blockIdx.y, c0 = (int)blockIdx.x * kGradientCols;
     // the adapter of this slot: the last one whose first slot is not past it
     int lo = 0, hi = a.adapters - 1;
     while (lo < hi) {
@@ -634,14 +634,17 @@ __device__ __forceinline__ void adapter_gradient_body(const AdapterArgs& a, Grad
     __syncthreads();
 
     const uint16_t* z = static_cast<const uint16_t*>(a.x);
-    const int zr = tid >> 3, zc = tid & 7;   // the 16 bytes of z this thread moves
-    const int zleft = a.cols - (c0 + zc * 8);
+    // the two 16-byte pieces of z that this thread moves: rows zr and zr + 16
+    const int zr = tid >> 4, zc = tid & 15, zleft = a.cols - (c0 + zc * 8);
     struct Step {
-        u32x4 z, h[HP];
+        u32x4 z[2], h[HP];
     };
     auto load = [&](Step& s, int p0) {
-        const int t = lds.rows[p0 + zr];
-        s.z = load_frag8(z + (size_t)max(t, 0) * (size_t)a.ldx + c0 + zc * 8, t < 0 ? 0 : zleft);
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            const int t = lds.rows[p0 + zr + 16 * q];
+            s.z[q] = load_frag8(z + (size_t)max(t, 0) * (size_t)a.ldx + c0 + zc * 8, t < 0 ? 0 : zleft);
+        }
 #pragma unroll
         for (int q = 0; q < HP; ++q) {
             const int piece = q * 256 + tid, r = (piece / (2 * HC)) & 31, c = piece % (2 * HC);
@@ -650,7 +653,11 @@ __device__ __forceinline__ void adapter_gradient_body(const AdapterArgs& a, Grad
         }
     };
     auto put = [&](const Step& s, int b) {
-        *reinterpret_cast<u32x4*>(&lds.z[b][zr * 64 + ((zc ^ nmaj_swz<8>(zr)) << 3)]) = s.z;
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            const int r = zr + 16 * q;
+            *reinterpret_cast<u32x4*>(&lds.z[b][r * kGradientCols + ((zc ^ nmaj_swz<16>(r)) << 3)]) = s.z[q];
+        }
 #pragma unroll
         for (int q = 0; q < HP; ++q) {
             const int piece = q * 256 + tid, r = piece / (2 * HC), c = piece % (2 * HC);
@@ -673,21 +680,21 @@ __device__ __forceinline__ void adapter_gradient_body(const AdapterArgs& a, Grad
         }
         return r;
     };
-    f32x4 acc[NT];
+    f32x4 acc[2][NT];  // of columns 32 wave .. + 15 and the 16 after them
 #pragma unroll
-    for (int n = 0; n < NT; ++n) acc[n] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int n = 0; n < NT; ++n) acc[0][n] = acc[1][n] = f32x4{0.f, 0.f, 0.f, 0.f};
     auto use = [&](int b) {
-        const u32x4 zf = turned(lds.z[b], wave * 16, std::integral_constant<int, 8>{});
+        u32x4 zf[2];
+#pragma unroll
+        for (int q = 0; q < 2; ++q) zf[q] = turned(lds.z[b], wave * 32 + 16 * q, std::integral_constant<int, 16>{});
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
             const u32x4 hf = turned(lds.h[b][0], n * 16, std::integral_constant<int, HC>{});
             const u32x4 lf = turned(lds.h[b][1], n * 16, std::integral_constant<int, HC>{});
-            if (TURNED) {
-                acc[n] = mfma_16<DT>(hf, zf, acc[n]);
-                acc[n] = mfma_16<DT>(lf, zf, acc[n]);
-            } else {
-                acc[n] = mfma_16<DT>(zf, hf, acc[n]);
-                acc[n] = mfma_16<DT>(zf, lf, acc[n]);
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                acc[q][n] = TURNED ? mfma_16<DT>(hf, zf[q], acc[q][n]) : mfma_16<DT>(zf[q], hf, acc[q][n]);
+                acc[q][n] = TURNED ? mfma_16<DT>(lf, zf[q], acc[q][n]) : mfma_16<DT>(zf[q], lf, acc[q][n]);
             }
         }
     };
@@ -707,29 +714,31 @@ __device__ __forceinline__ void adapter_gradient_body(const AdapterArgs& a, Grad
         use(1);
         if (p + 64 < n) put(s0, 0);
     }
-    // TURNED: lane has column c0 + l16 and rank numbers 16 n + 4 lg .. + 3; else rank number
-    // 16 n + l16 and columns c0 + 4 lg .. + 3
+    // TURNED: lane has column c + l16 and rank numbers 16 n + 4 lg .. + 3; else rank number
+    // 16 n + l16 and columns c + 4 lg .. + 3
     const size_t each = (size_t)a.rank * (size_t)a.cols;
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-        const f32x4 v = acc[n];
-        const int c = c0 + wave * 16 + (TURNED ? l16 : 4 * lg), j = 16 * n + (TURNED ? 4 * lg : l16);
-        if (c >= a.cols || j >= a.rank) continue;
-        const int left = TURNED ? a.rank - j : a.cols - c;
-        const size_t at = TURNED ? (size_t)c * (size_t)a.rank + j : (size_t)j * (size_t)a.cols + c;
-        float* w = a.work + (size_t)slot * each + at;
-        if (left >= 4) {
-            if (alone) store_out4(a.out, DT, (size_t)i * each + at, v);
-            else __builtin_memcpy(w, &v, 16);
-        } else {
+    for (int q = 0; q < 2; ++q)
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-                if (e < left) {
-                    if (alone) store_out(a.out, DT, (size_t)i * each + at + e, v[e]);
-                    else w[e] = v[e];
-                }
+        for (int n = 0; n < NT; ++n) {
+            const f32x4 v = acc[q][n];
+            const int c = c0 + wave * 32 + 16 * q + (TURNED ? l16 : 4 * lg), j = 16 * n + (TURNED ? 4 * lg : l16);
+            if (c >= a.cols || j >= a.rank) continue;
+            const int left = TURNED ? a.rank - j : a.cols - c;
+            const size_t at = TURNED ? (size_t)c * (size_t)a.rank + j : (size_t)j * (size_t)a.cols + c;
+            float* w = a.work + (size_t)slot * each + at;
+            if (left >= 4) {
+                if (alone) store_out4(a.out, DT, (size_t)i * each + at, v);
+                else __builtin_memcpy(w, &v, 16);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (e < left) {
+                        if (alone) store_out(a.out, DT, (size_t)i * each + at + e, v[e]);
+                        else w[e] = v[e];
+                    }
+            }
         }
-    }
 }
 
 // Both gradients in one launch: grid z 0 is a's, 1 b's.
@@ -737,9 +746,9 @@ template <int DT, int NT>
 __global__ __launch_bounds__(256) void adapter_gradient16(AdapterArgs a, AdapterArgs b) {
     __shared__ __attribute__((aligned(16))) GradientLds<NT> lds;
     if (blockIdx.z == 0) {
-        if ((int64_t)blockIdx.x * 64 < a.cols) adapter_gradient_body<DT, NT, false>(a, lds);
+        if ((int64_t)blockIdx.x * kGradientCols < a.cols) adapter_gradient_body<DT, NT, false>(a, lds);
     } else {
-        if ((int64_t)blockIdx.x * 64 < b.cols) adapter_gradient_body<DT, NT, true>(b, lds);
+        if ((int64_t)blockIdx.x * kGradientCols < b.cols) adapter_gradient_body<DT, NT, true>(b, lds);
     }
 }
 
