@@ -172,9 +172,47 @@ static __global__ __launch_bounds__(1024) void loss_finish(const LossPart* part,
     loss[t] = k >= 0 && k < vocabulary ? l - picked[t] : 0.0f;
 }
 
-// d of a tile through LDS as 16-bit rows (a half of the tile's rows to each half of LDS), their
-// 16-byte pieces permuted by the row, so that neither the writes (32 rows of one piece) nor the
-// whole-row reads meet in a bank.
+// A tile as 16-bit rows in LDS (a half of its rows to each half of LDS), their 16-byte pieces
+// permuted by the row, so that neither the writes (32 rows of one piece) nor the whole-row reads
+// meet in a bank. From there whole rows leave, 512 bytes of a 256 x 256 tile's at a time.
+template <int SI, int SJ, int WM, int WN>
+struct Tile16 {
+    static_assert(WM == 2, "a half of LDS for each");
+    static constexpr int HALF = 32 * SI, COLS = WN * 32 * SJ, PITCH = COLS * 2, PIECES = COLS / 8, WAVES = WM * WN;
+    char* lds;
+    char* lds2;
+    __device__ __forceinline__ char* at(int r, int piece) const {
+        return (r < HALF ? lds : lds2) + (r % HALF) * PITCH + ((piece ^ (r & (PIECES - 1))) << 4);
+    }
+    // columns 32 SJ wn + 32 j + 8 q + 4 lh .. + 3 of row r
+    template <int DT>
+    __device__ __forceinline__ void put(int r, int wn, int j, int q, int lh, const float (&v)[4]) const {
+        uint32_t h[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            h[e] = DT == DT_F16 ? (uint32_t)__builtin_bit_cast(uint16_t, (_Float16)v[e]) : (uint32_t)f32_to_bf16_rne(v[e]);
+        *reinterpret_cast<u32x2*>(at(r, wn * (4 * SJ) + 4 * j + q) + 8 * lh) = u32x2{h[0] | (h[1] << 16), h[2] | (h[3] << 16)};
+    }
+    // rows x cols of the tile at (m, n) to out
+    __device__ __forceinline__ void store(uint16_t* out, int64_t ld, int m, int n, int rows, int cols) const {
+        constexpr int RI = 64 / PIECES, IT = 2 * HALF / WAVES / RI;  // rows of a load, loads of a wave
+        const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+        const int piece = lane % PIECES, c = n + 8 * piece, left = cols - c;
+#pragma unroll 4
+        for (int it = 0; it < IT; ++it) {
+            const int r = wave * (2 * HALF / WAVES) + RI * it + lane / PIECES, row = m + r;
+            const u32x4 v = *reinterpret_cast<const u32x4*>(at(r, piece));
+            if (row >= rows || left <= 0) continue;
+            uint16_t* dst = out + (size_t)row * (size_t)ld + c;
+            if (left >= 8) __builtin_memcpy(dst, &v, 16);
+            else
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    if (e < left) dst[e] = (uint16_t)(v[e >> 1] >> (16 * (e & 1)));
+        }
+    }
+};
+
 template <int DT>
 struct LossGradHook {
     static constexpr bool kReplace = true, kAdd = false;
@@ -190,14 +228,13 @@ struct LossGradHook {
     template <int SI, int SJ, int WM, int WN>
     __device__ __forceinline__ void finish(f32x16 (&acc)[SI][SJ], int m0, int n0, int wm, int wn, char* lds,
                                            char* lds2) const {
-        static_assert(WM == 2, "a half of LDS for each");
-        constexpr int HALF = 32 * SI, COLS = WN * 32 * SJ, PITCH = COLS * 2, PM = COLS / 8 - 1, WAVES = WM * WN;
+        typedef Tile16<SI, SJ, WM, WN> Tile;
+        const Tile tile{lds, lds2};
         const int lane = threadIdx.x & 63, l32 = lane & 31, lh = lane >> 5;
-        char* half = wm == 0 ? lds : lds2;
         const float f = factor ? factor[0] : 1.0f;
 #pragma unroll
         for (int i = 0; i < SI; ++i) {
-            const int row = m0 + 32 * i + l32, r = 32 * i + l32;
+            const int r = wm * Tile::HALF + 32 * i + l32, row = m0 + 32 * i + l32;
             int64_t at = -1;
             float g = 0.0f, c = 0.0f;
             if (row < tokens) {
@@ -217,50 +254,31 @@ struct LossGradHook {
                 if constexpr (SI == 4) asm volatile("" : "+a"(acc[i][j]));  // see full_epilogue
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
-                    uint32_t h[4];
+                    float v[4];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         const float p = __builtin_amdgcn_exp2f(fmaf(acc[i][j][4 * q + e], kLog2e, c));
-                        const float v = live ? (p - (t == 32 * j + 8 * q + e ? 1.0f : 0.0f)) * g : 0.0f;
-                        h[e] = DT == DT_F16 ? (uint32_t)__builtin_bit_cast(uint16_t, (_Float16)v)
-                                            : (uint32_t)f32_to_bf16_rne(v);
+                        v[e] = live ? (p - (t == 32 * j + 8 * q + e ? 1.0f : 0.0f)) * g : 0.0f;
                     }
-                    const int piece = wn * (4 * SJ) + 4 * j + q;
-                    *reinterpret_cast<u32x2*>(half + r * PITCH + ((piece ^ (r & PM)) << 4) + 8 * lh) =
-                        u32x2{h[0] | (h[1] << 16), h[2] | (h[3] << 16)};
+                    tile.template put<DT>(r, wn, j, q, lh, v);
                 }
             }
         }
         __syncthreads();
-        const int wave = threadIdx.x >> 6, tile_m = m0 - wm * HALF, tile_n = n0 - wn * 32 * SJ;
-        auto at = [&](int r, int piece) { return (r < HALF ? lds : lds2) + (r % HALF) * PITCH + ((piece ^ (r & PM)) << 4); };
-        if (d) {
-            constexpr int RI = 64 / (COLS / 8), IT = 2 * HALF / WAVES / RI;  // rows of a load, loads of a wave
-            const int piece = lane % (COLS / 8), c = tile_n + 8 * piece, left = n - c;
-            for (int it = 0; it < IT; ++it) {
-                const int r = wave * (2 * HALF / WAVES) + RI * it + lane / (COLS / 8), row = tile_m + r;
-                if (row >= tokens || left <= 0) continue;
-                const u32x4 v = *reinterpret_cast<const u32x4*>(at(r, piece));
-                uint16_t* dst = d + (size_t)row * (size_t)ldd + c;
-                if (left >= 8) __builtin_memcpy(dst, &v, 16);
-                else
-#pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        if (e < left) dst[e] = (uint16_t)(v[e >> 1] >> (16 * (e & 1)));
-            }
-        }
+        const int wave = threadIdx.x >> 6, tile_m = m0 - wm * Tile::HALF, tile_n = n0 - wn * 32 * SJ;
+        if (d) tile.store(d, ldd, tile_m, tile_n, tokens, n);
         if (dt) {
             // a wave: 32 columns, 32 rows at a time: 16 lanes get eight rows of 16 columns
-            static_assert(COLS / WAVES == 32, "columns of a wave");
+            static_assert(Tile::COLS / Tile::WAVES == 32, "columns of a wave");
             const int l16 = lane & 15, lg = lane >> 4;
 #pragma unroll 2
-            for (int it = 0; it < 2 * (2 * HALF / 32); ++it) {
+            for (int it = 0; it < 2 * (2 * Tile::HALF / 32); ++it) {
                 const int cb = wave * 32 + 16 * (it & 1), rb = 32 * (it >> 1) + 8 * lg;
                 u32x4 v;
 #pragma unroll
                 for (int hh = 0; hh < 2; ++hh) {
                     const int col = cb + 4 * (l16 & 3);
-                    char* p = at(rb + 4 * hh + (l16 >> 2), col >> 3) + (col & 7) * 2;
+                    char* p = tile.at(rb + 4 * hh + (l16 >> 2), col >> 3) + (col & 7) * 2;
                     const u32x2 x = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4f16(DG_LDS_PTR(fp16x4_t, p)));
                     v[2 * hh] = x[0];
                     v[2 * hh + 1] = x[1];
@@ -269,6 +287,38 @@ struct LossGradHook {
                 if (c < n && row < lddt) __builtin_memcpy(dt + (size_t)c * (size_t)lddt + row, &v, 16);
             }
         }
+    }
+};
+
+// The product itself as 16-bit rows, times factor[1].
+template <int DT>
+struct RowsHook {
+    static constexpr bool kReplace = true, kAdd = false;
+    uint16_t* out;
+    int64_t ld;
+    int rows, cols;
+    const float* factor;   // or NULL
+    template <int SI, int SJ, int WM, int WN>
+    __device__ __forceinline__ void finish(f32x16 (&acc)[SI][SJ], int m0, int n0, int wm, int wn, char* lds,
+                                           char* lds2) const {
+        typedef Tile16<SI, SJ, WM, WN> Tile;
+        const Tile tile{lds, lds2};
+        const int lane = threadIdx.x & 63, l32 = lane & 31, lh = lane >> 5;
+        const float f = factor ? factor[1] : 1.0f;
+#pragma unroll
+        for (int i = 0; i < SI; ++i)
+#pragma unroll
+            for (int j = 0; j < SJ; ++j) {
+                if constexpr (SI == 4) asm volatile("" : "+a"(acc[i][j]));
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const float v[4] = {acc[i][j][4 * q] * f, acc[i][j][4 * q + 1] * f, acc[i][j][4 * q + 2] * f,
+                                        acc[i][j][4 * q + 3] * f};
+                    tile.template put<DT>(wm * Tile::HALF + 32 * i + l32, wn, j, q, lh, v);
+                }
+            }
+        __syncthreads();
+        tile.store(out, ld, m0 - wm * Tile::HALF, n0 - wn * 32 * SJ, rows, cols);
     }
 };
 
@@ -281,6 +331,12 @@ template <int DT, bool REG>
 __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) void loss_grad_tiles(GemmArgs g,
                                                                                                  LossGradHook<DT> h) {
     mfma32_sp_body<DT, 1, 8, REG, false, false>(g, nullptr, h);
+}
+
+// w's gradient: d^T (rows of whole stages) x
+template <int DT>
+__global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) void loss_w_tiles(GemmArgs g, RowsHook<DT> h) {
+    mfma32_sp_body<DT, 0, 8, false, false, false>(g, nullptr, h);
 }
 
 template <int DT>

@@ -289,7 +289,7 @@ struct LossSpace {
     float* x_acc = nullptr;
     float* w_acc = nullptr;
     void* product = nullptr;
-    int64_t piece = 0, lddt = 0, ldxp = 0, bytes = 0;
+    int64_t piece = 0, ldd = 0, lddt = 0, ldxp = 0, product_bytes = 0, bytes = 0;
 };
 
 // 16-bit logits are never stored but for the shortest sums.
@@ -336,6 +336,11 @@ LossSpace loss_space(void* workspace, int64_t tokens, int64_t vocabulary, int64_
     return s;
 }
 
+// Workspace of x_grad's product: its sum over a piece is cut into up to eight slices.
+int64_t x_product_bytes(int64_t tokens, int64_t K) {
+    return std::max(kProductWorkspace, std::min<int64_t>((int64_t)128 << 20, 8 * tokens * K * 4));
+}
+
 LossSpace loss_backward_space(void* workspace, int64_t tokens, int64_t vocabulary, int64_t K, int dtype, bool x_grad,
                               bool w_grad, int64_t piece) {
     LossSpace s;
@@ -345,14 +350,17 @@ LossSpace loss_backward_space(void* workspace, int64_t tokens, int64_t vocabular
     s.lddt = (tokens + 31) / 32 * 32;
     s.factor = static_cast<float*>(p.take(8));
     if (!loss_fused(vocabulary, K, dtype)) s.logits = static_cast<float*>(p.take(tokens * s.piece * 4));
-    if (x_grad) s.d = s.logits && dtype == GEMM_F32 ? s.logits : p.take(tokens * s.piece * es);  // in place in fp32
+    s.ldd = dtype == GEMM_F32 ? s.piece : ceil_div(s.piece, 8) * 8;
+    if (x_grad) s.d = s.logits && dtype == GEMM_F32 ? s.logits : p.take(tokens * s.ldd * es);  // in place in fp32
     if (w_grad) s.dt = p.take(s.piece * s.lddt * es);
-    // 16-bit sums over tokens run in whole stages of the products' kernels, over rows of zeros at their end
+    // 16-bit sums over tokens run in whole stages and pieces of 16 bytes, over a copy of x with zeros at
+    // its ends where x has others
     s.ldxp = ceil_div(K, 8) * 8;
-    if (w_grad && dtype != GEMM_F32 && tokens >= 64 && tokens % 32 != 0) s.xp = p.take(s.lddt * s.ldxp * es);
+    if (w_grad && loss_fused(vocabulary, K, dtype)) s.xp = p.take(s.lddt * s.ldxp * es);
     if (x_grad && dtype != GEMM_F32) s.x_acc = static_cast<float*>(p.take(tokens * K * 4));
-    if (w_grad && dtype != GEMM_F32) s.w_acc = static_cast<float*>(p.take(s.piece * K * 4));
-    s.product = p.take(kProductWorkspace);
+    if (w_grad && dtype == GEMM_F16 && !loss_fused(vocabulary, K, dtype)) s.w_acc = static_cast<float*>(p.take(s.piece * K * 4));
+    s.product_bytes = x_grad ? x_product_bytes(tokens, K) : kProductWorkspace;
+    s.product = p.take(s.product_bytes);
     s.bytes = p.at;
     return s;
 }
@@ -798,44 +806,69 @@ int gemm_loss_backward(const float* grad, const void* x, int64_t tokens, int64_t
     a.dt = sp.dt;
     a.lddt = sp.lddt;
     if (scaled) DG_TRY(launched(dg::launch_loss_factor(grad, (int)tokens, sp.factor, s), "loss gradient's factor"));
-    if (sp.xp) {
+    const void* xw = x;  // x for w_grad's product
+    int64_t ldxw = ldx;
+    if (sp.xp && tokens > 0 && (tokens % 32 != 0 || !whole_pieces(x, ldx, K))) {
         const dg::PackJob job{x, sp.xp, ldx, (int)tokens, (int)K, (int)sp.lddt, (int)sp.ldxp}, none_left{x, sp.xp, ldx, 0, 0, 0, 8};
         DG_TRY(launched(dg::launch_pack((int)es, job, none_left, s), "loss gradient's copy of x"));
+        xw = sp.xp;
+        ldxw = sp.ldxp;
     }
     float* xa = wide ? static_cast<float*>(x_grad) : sp.x_acc;
     const int64_t ldxa = wide ? ldxg : K;
     int64_t v0 = 0;
     do {
-        a.n = (int)std::min(sp.piece, vocabulary - v0);
-        a.ld = a.ldd = std::max(1, a.n);
+        const int64_t n = std::min(sp.piece, vocabulary - v0);
+        a.n = (int)n;
+        a.ld = std::max<int64_t>(1, n);
+        a.ldd = wide ? a.ld : sp.ldd;
         a.v0 = (int)v0;
         const char* wp = static_cast<const char*>(w) + (size_t)v0 * ldw * es;
-        if (tokens > 0 && a.n > 0) {
+        if (tokens > 0 && n > 0) {
             if (sp.logits) {
-                DG_TRY(product(GEMM_OP_T, tokens, a.n, K, x, ldx, wp, ldw, sp.logits, a.ld, dtype, GEMM_F32, 0.0f,
-                               sp.product, kProductWorkspace, stream));
+                DG_TRY(product(GEMM_OP_T, tokens, n, K, x, ldx, wp, ldw, sp.logits, a.ld, dtype, GEMM_F32, 0.0f,
+                               sp.product, sp.product_bytes, stream));
                 DG_TRY(launched(dg::launch_loss_grad(a, dtype, s), "loss gradient"));
             } else {
-                const bool direct = whole_pieces(x, ldx, K) && whole_pieces(wp, ldw, K);
-                const dg::LossProduct p = loss_product(x, ldx, wp, ldw, tokens, a.n, K, dtype,
-                                                       loss_tiles(tokens, a.n, direct).wide > 0 ? 256 : 128);
-                DG_TRY(launched(DG_BY_TYPE(launch_loss_grad_tiles, dtype, p, a, s), "loss gradient"));
+                const LossTiles t = loss_tiles(tokens, n, whole_pieces(x, ldx, K) && whole_pieces(wp, ldw, K));
+                for (int64_t c = 0; c < n; c = t.wide > c ? t.wide : n) {  // wide tiles and then narrow ones
+                    const bool is_wide = t.wide > c;
+                    dg::LossArgs b = a;
+                    b.n = (int)((is_wide ? t.wide : n) - c);
+                    b.v0 = (int)(v0 + c);
+                    if (b.d) b.d = static_cast<char*>(b.d) + c * es;
+                    if (b.dt) b.dt = static_cast<char*>(b.dt) + c * b.lddt * es;
+                    const dg::LossProduct p = loss_product(x, ldx, wp + (size_t)c * ldw * es, ldw, tokens, b.n, K, dtype,
+                                                           is_wide ? 256 : 128);
+                    DG_TRY(launched(DG_BY_TYPE(launch_loss_grad_tiles, dtype, p, b, s), "loss gradient"));
+                }
             }
         }
-        if (x_grad)
-            DG_TRY(product(GEMM_OP_N, tokens, K, a.n, sp.d, a.ldd, wp, ldw, xa, ldxa, dtype, GEMM_F32,
-                           v0 == 0 ? 0.0f : 1.0f, sp.product, kProductWorkspace, stream));
-        if (w_grad) {
-            char* wg = static_cast<char*>(w_grad) + (size_t)v0 * ldwg * es;
-            DG_TRY(product(GEMM_OP_N, a.n, K, sp.xp ? sp.lddt : tokens, sp.dt, sp.lddt, sp.xp ? sp.xp : x,
-                           sp.xp ? sp.ldxp : ldx, scaled ? (void*)sp.w_acc : wg,
-                           scaled ? K : ldwg, dtype, scaled ? GEMM_F32 : dtype, 0.0f, sp.product, kProductWorkspace,
-                           stream));
-            if (scaled && a.n > 0)
-                DG_TRY(launched(dg::launch_scaled_cast(sp.w_acc, K, a.n, (int)K, sp.factor, wg, ldwg, dtype, s),
-                                "loss gradient's rounding"));
+        if (x_grad) {
+            // of a 16-bit piece, whole stages first: rows of w beyond the last piece are not read
+            const int64_t main = !wide && n >= 32 ? n / 32 * 32 : n;
+            DG_TRY(product(GEMM_OP_N, tokens, K, main, sp.d, a.ldd, wp, ldw, xa, ldxa, dtype, GEMM_F32,
+                           v0 == 0 ? 0.0f : 1.0f, sp.product, sp.product_bytes, stream));
+            if (n > main)
+                DG_TRY(product(GEMM_OP_N, tokens, K, n - main, static_cast<const char*>(sp.d) + main * es, a.ldd,
+                               wp + (size_t)main * ldw * es, ldw, xa, ldxa, dtype, GEMM_F32, 1.0f, sp.product,
+                               sp.product_bytes, stream));
         }
-        v0 += a.n;
+        if (w_grad && n > 0) {
+            char* wg = static_cast<char*>(w_grad) + (size_t)v0 * ldwg * es;
+            if (sp.xp && tokens > 0) {
+                DG_TRY(launched(DG_BY_TYPE(launch_loss_w, dtype, sp.dt, sp.lddt, xw, ldxw, (int)n, (int)sp.lddt, (int)K,
+                                           tile_group(n, K), a.factor, wg, ldwg, s), "loss gradient of w"));
+            } else {
+                DG_TRY(product(GEMM_OP_N, n, K, tokens, sp.dt, sp.lddt, x, ldx, sp.w_acc ? (void*)sp.w_acc : wg,
+                               sp.w_acc ? K : ldwg, dtype, sp.w_acc ? GEMM_F32 : dtype, 0.0f, sp.product,
+                               sp.product_bytes, stream));
+                if (sp.w_acc)
+                    DG_TRY(launched(dg::launch_scaled_cast(sp.w_acc, K, (int)n, (int)K, sp.factor, wg, ldwg, dtype, s),
+                                    "loss gradient's rounding"));
+            }
+        }
+        v0 += n;
     } while (v0 < vocabulary);
     if (x_grad && !wide && tokens > 0)
         DG_TRY(launched(dg::launch_scaled_cast(sp.x_acc, K, (int)tokens, (int)K, a.factor, x_grad, ldxg, dtype, s),
