@@ -11,6 +11,7 @@
 #include "extents.h"
 #include "kernel_sp.h"
 #include "layers.h"
+#include "tile16.h"
 
 namespace dg {
 
@@ -137,7 +138,7 @@ __device__ __forceinline__ void adapter_add(f32x16 (&acc)[SJ], int m0, int n0, c
 }
 
 // ---------------------------------------------------------------- shared product and adapters in one
-// Up to rank 64, a tile's u (256 rows, hi and lo) and an adapter's rows of m (256 columns) are
+// A tile's u (256 rows, hi and lo) and an adapter's rows of m (256 columns), of rank up to 64, are
 // brought to LDS by all waves together, whole lines at a time: fragments loaded by each wave
 // straight from memory touch a line for every two lanes, and each is loaded by several waves. The
 // adapters among 32 rows of each half of the tile take turns.
@@ -146,19 +147,36 @@ __device__ __forceinline__ int rank_swz(int r, int pieces) {
     return pieces == 16 ? r & 15 : pieces == 8 ? (r >> 1) & 7 : pieces == 4 ? (r >> 2) & 3 : (r >> 3) & 1;
 }
 
-template <int DT, bool STAGED>
+template <int DT>
 struct AdapterHook {
-    static constexpr bool kReplace = false, kAdd = true;
+    static constexpr bool kReplace = true;
     AdapterArgs a;
+    template <int SI, int SJ, int WM, int WN>
+    __device__ __forceinline__ void finish(f32x16 (&acc)[SI][SJ], int m, int n, int wm, int wn, char* lds,
+                                           char* lds2) const {
+        typedef Tile16<SI, SJ, WM, WN> Tile;
+        const int m0 = m - wm * Tile::HALF, n0 = n - wn * 32 * SJ;
+        add<SI, SJ, WM, WN>(acc, m0, n0, wm, wn, lds, lds2);
+        __syncthreads();
+        const Tile tile{lds, lds2};
+        const int lane = threadIdx.x & 63, l32 = lane & 31, lh = lane >> 5;
+#pragma unroll
+        for (int i = 0; i < SI; ++i)
+#pragma unroll
+            for (int j = 0; j < SJ; ++j) {
+                asm volatile("" : "+a"(acc[i][j]));  // see full_epilogue
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const float v[4] = {acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
+                    tile.template put<DT>(wm * Tile::HALF + 32 * i + l32, wn, j, q, lh, v);
+                }
+            }
+        __syncthreads();
+        tile.store(static_cast<uint16_t*>(a.out), a.ldo, m0, n0, a.tokens, a.cols);
+    }
     template <int SI, int SJ, int WM, int WN>
     __device__ __forceinline__ void add(f32x16 (&acc)[SI][SJ], int m0, int n0, int wm, int wn, char* us_lds,
                                         char* m_lds) const {
-        if constexpr (!STAGED) {
-#pragma unroll
-            for (int i = 0; i < SI; ++i)
-                adapter_add<DT, SJ>(acc[i], m0 + wm * 32 * SI + 32 * i, n0 + wn * 32 * SJ, a);
-            return;
-        }
         constexpr int ROWS = WM * 32 * SI, COLS = WN * 32 * SJ, THREADS = WM * WN * 64;
         static_assert(WM == 2, "halves of the tile");
         const int tid = threadIdx.x, lane = tid & 63, l32 = lane & 31, lh = lane >> 5;
@@ -251,13 +269,12 @@ struct AdapterHook {
                     for (int e = 0; e < 16; ++e) acc[b][j][e] += here ? d[j][e] : 0.0f;
             }
         }
-        __syncthreads();
     }
 };
 
-template <int DT, int OPB, bool REG, bool STAGED>
+template <int DT, int OPB, bool REG>
 __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) void adapter_product(
-    GemmArgs g, AdapterHook<DT, STAGED> h) {
+    GemmArgs g, AdapterHook<DT> h) {
     mfma32_sp_body<DT, OPB, 8, REG, false, false>(g, nullptr, h);
 }
 

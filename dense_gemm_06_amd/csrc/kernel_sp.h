@@ -114,12 +114,11 @@ __device__ __forceinline__ u32x4 keep_first8(u32x4 w, int v) {
 // problems as across tiles. g then holds only xcd_remap (and no fused epilogue).
 //
 // HOOK: what an operator built on the one-tile forms does with a finished wave tile. With
-// kReplace, h.finish<4, SJ, 2, waves along n>(acc, m, n, wm, wn, lds, lds2) takes the accumulators (row 32 i + lane % 32 of
-// the wave tile at row m, columns as laid out at full_epilogue, from column n) in place of the
-// store, with the whole LDS (two halves of 64 KB) to itself; else h.add, of the output tile at
-// row m and column n, adds to them before it and leaves no read of LDS behind.
+// kReplace, h.finish<4, SJ, 2, waves along n>(acc, m, n, wm, wn, lds, lds2) takes the accumulators
+// (row 32 i + lane % 32 of the wave tile at row m, columns as laid out at full_epilogue, from
+// column n) in place of the store, with the whole LDS (two halves of 64 KB) to itself.
 struct NoHook {
-    static constexpr bool kReplace = false, kAdd = false;
+    static constexpr bool kReplace = false;
 };
 
 template <int DT, int OPB, int NW, bool REG, bool PERSIST, bool GROUPED, class HOOK = NoHook>
@@ -552,9 +551,6 @@ __device__ __forceinline__ void mfma32_sp_body(GemmArgs& g, const GroupArgs* ga,
                      reinterpret_cast<char*>(&sB[0][0]));
             return;
         }
-        if constexpr (HOOK::kAdd)
-            h.template add<4, SJ, 2, WNN>(acc, s.m0, s.n0, wm, wn, reinterpret_cast<char*>(&sA[0][0]),
-                                          reinterpret_cast<char*>(&sB[0][0]));
         constexpr int WT = 32 * SJ * 4;           // bytes per wave-tile row
         constexpr int CPR = WT / 16;              // 16-byte chunks per row
         constexpr int RPI = 64 / CPR;             // rows per read instruction

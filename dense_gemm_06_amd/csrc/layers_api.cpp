@@ -211,8 +211,8 @@ void product_space(AdapterSpace& s, Parts& p, int64_t tokens, int64_t cols, int6
 // A forward call of 16-bit matrices: few tokens
 bool few_tokens(int64_t tokens, int64_t K, int dtype) { return dtype != GEMM_F32 && K > 0 && tokens <= kSkinny; }
 // or one kernel for the product and the adapters in its tiles, in either direction
-bool in_tiles(int64_t tokens, int64_t cols, int64_t len, int dtype) {
-    return dtype != GEMM_F32 && cols >= 8 && len >= 8 && adapter_tiles(tokens, cols);
+bool in_tiles(int64_t tokens, int64_t cols, int64_t len, int64_t rank, int dtype) {
+    return dtype != GEMM_F32 && cols >= 8 && len >= 8 && rank <= 64 && adapter_tiles(tokens, cols);
 }
 
 AdapterSpace adapter_space(void* workspace, int64_t tokens, int64_t N, int64_t K, int64_t rank, int dtype) {
@@ -222,7 +222,7 @@ AdapterSpace adapter_space(void* workspace, int64_t tokens, int64_t N, int64_t K
         s.slices = slices_of(ceil_div(N, 64), K);
         s.part = static_cast<float*>(p.take(s.slices.count * tokens * ceil_div(N, 4) * 16));
     } else {
-        product_space(s, p, tokens, N, K, dtype, in_tiles(tokens, N, K, dtype));
+        product_space(s, p, tokens, N, K, dtype, in_tiles(tokens, N, K, rank, dtype));
         if (dtype != GEMM_F32) shrink_space(s, p, tokens, K, rank);
     }
     s.bytes = p.at;
@@ -233,7 +233,7 @@ AdapterSpace adapter_backward_space(void* workspace, int64_t tokens, int64_t N, 
                                     int64_t rank, int dtype) {
     AdapterSpace s;
     Parts p{static_cast<char*>(workspace)};
-    product_space(s, p, tokens, K, N, dtype, in_tiles(tokens, K, N, dtype));
+    product_space(s, p, tokens, K, N, dtype, in_tiles(tokens, K, N, rank, dtype));
     s.v = static_cast<float*>(p.take(tokens * rank * 4));
     if (dtype != GEMM_F32) {
         shrink_space(s, p, tokens, N, rank);
@@ -470,7 +470,7 @@ int gemm_adapters_product(const void* x, int64_t tokens, int64_t K, int64_t ldx,
     }
     if (N == 0) return GEMM_OK;
     if (few) return launched(DG_BY_TYPE(launch_adapter_skinny, dtype, p, b, s), "adapters' products");
-    if (in_tiles(tokens, N, K, dtype))
+    if (in_tiles(tokens, N, K, set->rank, dtype))
         return launched(DG_BY_TYPE(launch_adapter_tiles, dtype, p, b, tile_group(tokens, N), s), "adapters' products");
     b.slices = 1;
     if (form == 2) {
@@ -605,7 +605,7 @@ int gemm_adapters_backward(const void* grad, int64_t tokens, int64_t N, int64_t 
         a.scale = nullptr;
         a.out = x_grad;
         a.ldo = ldxg;
-        if (in_tiles(tokens, K, N, dtype)) {
+        if (in_tiles(tokens, K, N, set->rank, dtype)) {
             dg::AdapterProduct p{grad, w, ldg, ldw, (int)K, (int)N, GEMM_OP_N,
                                  tiles_form(grad, ldg, w, ldw, K, N, GEMM_OP_N, dtype) == 2};
             DG_TRY(launched(DG_BY_TYPE(launch_adapter_tiles, dtype, p, a, tile_group(tokens, K), s), "adapters' x_grad"));
