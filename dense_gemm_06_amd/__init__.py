@@ -384,5 +384,6 @@ from .experts import (  # noqa: E402,F401
 # ----------------------------------------------------------------------------- operators around a layer's products
 from . import layers as _layers  # noqa: E402
 from .layers import (  # noqa: E402,F401
-    GEMM_ACT_SILU, gemm_activation_backward_tensors, gemm_activation_tensors, gemm_adapter_set,
-    gemm_adapters_backward_tensors, gemm_adapters_tensors, gemm_loss_backward_tensors, gemm_loss_tensors)
+    GEMM_ACT_SILU, gemm_activation_backward_tensors, gemm_activation_tensors, gemm_activation_value_tensors,
+    gemm_adapter_set, gemm_adapters_backward_tensors, gemm_adapters_tensors, gemm_loss_backward_tensors,
+    gemm_loss_tensors)

@@ -203,13 +203,14 @@ __global__ __launch_bounds__(256) void activation_backward(ActArgs a, int64_t un
         if (c64 >= a.cols) continue;
         const int c = (int)c64, valid = a.cols - c;
         float v[8], w[8], gr[8], z1[8], z2[8], y[8];
-        load_row8<DT>(gr, a.grad, (size_t)row * (size_t)a.ldg + c, valid);
+        if (a.grad) load_row8<DT>(gr, a.grad, (size_t)row * (size_t)a.ldg + c, valid);
         decode_row8(v, a.codes, row, c, valid, a.cols);
         if (a.gated) decode_row8(w, a.codes, row, a.cols + c, valid, zcols);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
             float f, slope;
             act_value<true>(v[e], a.act, f, slope);
+            if (a.grad == nullptr) gr[e] = 0.0f;
             if (a.gated) {
                 z1[e] = gr[e] * w[e] * slope;
                 z2[e] = gr[e] * f;
@@ -220,8 +221,8 @@ __global__ __launch_bounds__(256) void activation_backward(ActArgs a, int64_t un
             }
         }
         const size_t at = (size_t)row * (size_t)a.ldzg + c;
-        store_row8<DT>(a.z_grad, at, z1, valid);
-        if (a.gated) store_row8<DT>(a.z_grad, at + a.cols, z2, valid);
+        if (a.grad) store_row8<DT>(a.z_grad, at, z1, valid);
+        if (a.grad && a.gated) store_row8<DT>(a.z_grad, at + a.cols, z2, valid);
         if (a.y) store_row8<DT>(a.y, (size_t)row * (size_t)a.ldy + c, y, valid);
     }
 }

@@ -926,14 +926,18 @@ int gemm_activation_backward(const gemm_block_matrix* codes, const void* grad, i
     DG_TRY(check_size("cols", cols));
     DG_TRY(check_activation(activation, cols, gated));
     const int64_t zcols = gated ? 2 * cols : cols, es = elem_size(dtype);
-    DG_TRY(check_ld("ldg", ldg, cols));
-    DG_TRY(check_ld("ldzg", ldzg, zcols));
+    if (grad || z_grad) {
+        DG_TRY(check_ld("ldg", ldg, cols));
+        DG_TRY(check_ld("ldzg", ldzg, zcols));
+    }
     if (y) DG_TRY(check_ld("ldy", ldy, cols));
     DG_TRY(check_block("codes", codes));
     DG_TRY(check_codes(*codes, rows, zcols));
     if (rows == 0 || cols == 0) return GEMM_OK;
-    DG_TRY(check_pointer("grad", grad));
-    DG_TRY(check_pointer("z_grad", z_grad));
+    if (grad || z_grad || y == nullptr) {
+        DG_TRY(check_pointer("grad", grad));
+        DG_TRY(check_pointer("z_grad", z_grad));
+    }
     DG_TRY(check_overlap({range("z_grad", z_grad, span(rows, zcols, ldzg, es)),
                           range("y", y, span(rows, cols, ldy, es))},
                          {range("grad", grad, span(rows, cols, ldg, es)), data_range("codes.data", *codes),

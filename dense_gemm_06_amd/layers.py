@@ -11,6 +11,7 @@ calls can be captured into a graph.
   gemm_loss_backward_tensors        its gradients, in pieces of the vocabulary
   gemm_activation_tensors           an activation, with or without a gate, and its input in 8 bits
   gemm_activation_backward_tensors  its gradient from the 8-bit codes
+  gemm_activation_value_tensors     the activation again from the codes
 
 Tensors need unit stride along their last dimension; other strides are free. Results carry no
 gradient, also of tensors that require one: a training step calls the gradients' operators
@@ -276,3 +277,21 @@ def gemm_activation_backward_tensors(grad, codes, activation, gated=False, value
         _call("gemm_activation_backward", at, c, grad.data_ptr(), T, F, ld, wide, act, int(gated), zg.data_ptr(), Z,
               y.data_ptr() if value else None, F)
     return zg, y
+
+
+def gemm_activation_value_tensors(codes, activation, gated=False, dtype=None):
+    """y (T, F) computed again from gemm_activation_tensors' codes, of type dtype (bfloat16 by default): as the
+    backward pass gives it, for where it is needed before the gradient of y is known."""
+    if torch is None:
+        _use_torch()
+    dtype = dtype or torch.bfloat16
+    wide, act, c = _wide_type(dtype, "dtype"), _activation(activation), _block(codes, "codes")
+    T, Z = c.rows, c.cols
+    if gated and Z % 2:
+        raise ValueError(f"codes of a gated activation have an even number of columns, not {Z}")
+    F = Z // 2 if gated else Z
+    at, dev = _device(codes.data, codes.scale), codes.data.device
+    y = torch.empty((T, F), dtype=dtype, device=dev)
+    if T and F:
+        _call("gemm_activation_backward", at, c, None, T, F, 0, wide, act, int(gated), None, 0, y.data_ptr(), F)
+    return y

@@ -115,7 +115,8 @@ int gemm_activation_forward(const void* z, int64_t rows, int64_t cols, int64_t l
 /*
  * gemm_activation_backward -- from grad (rows x cols, type dtype), the gradient of y, and the
  * codes of z: z_grad = grad f'(z), or gated [grad z2 f'(z1) | grad f(z1)], and y computed again
- * (NULL: not wanted) for the gradient of the weight that reads it, both of type dtype.
+ * (NULL: not wanted) for the gradient of the weight that reads it, both of type dtype. grad and
+ * z_grad are NULL together where y alone is wanted: it may be needed before grad is known.
  */
 int gemm_activation_backward(const gemm_block_matrix* codes, const void* grad, int64_t rows, int64_t cols, int64_t ldg,
                              int dtype, int activation, int gated, void* z_grad, int64_t ldzg, void* y, int64_t ldy,
