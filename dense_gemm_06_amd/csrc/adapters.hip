@@ -28,20 +28,21 @@ __device__ __forceinline__ size_t m_at(const AdapterArgs& a, int i, int j, int64
 // One wave: one token and one of its rank numbers.
 template <int DT>
 __global__ __launch_bounds__(256) void adapter_shrink(AdapterArgs a) {
-    const int64_t unit = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
     const int lane = threadIdx.x & 63;
-    if (unit >= (int64_t)a.tokens * a.rank) return;
-    const int t = (int)(unit / a.rank), j = (int)(unit - (int64_t)t * a.rank);
-    const int i = a.index[t];
-    float sum = 0.0f;
-    if (i >= 0 && i < a.adapters) {
-        for (int64_t k = lane; k < a.cols; k += 64)
-            sum = fmaf(element<DT>(a.x, (size_t)t * (size_t)a.ldx + k), element<DT>(a.m, m_at(a, i, j, k)), sum);
+    const int64_t units = (int64_t)a.tokens * a.rank;
+    for (int64_t unit = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); unit < units; unit += (int64_t)gridDim.x * 4) {
+        const int t = (int)(unit / a.rank), j = (int)(unit - (int64_t)t * a.rank);
+        const int i = a.index[t];
+        float sum = 0.0f;
+        if (i >= 0 && i < a.adapters) {
+            for (int64_t k = lane; k < a.cols; k += 64)
+                sum = fmaf(element<DT>(a.x, (size_t)t * (size_t)a.ldx + k), element<DT>(a.m, m_at(a, i, j, k)), sum);
 #pragma unroll
-        for (int d = 1; d < 64; d <<= 1) sum += __shfl_xor(sum, d);
-        if (a.scale) sum *= a.scale[i];
+            for (int d = 1; d < 64; d <<= 1) sum += __shfl_xor(sum, d);
+            if (a.scale) sum *= a.scale[i];
+        }
+        if (lane == 0) a.u[unit] = sum;
     }
-    if (lane == 0) a.u[unit] = sum;
 }
 
 // One thread: one element.
@@ -110,7 +111,7 @@ dim3 walk_grid(int64_t n) {
 }  // namespace
 
 int launch_adapter_shrink(const AdapterArgs& a, int dtype, hipStream_t s) {
-    const dim3 grid((unsigned)(((int64_t)a.tokens * a.rank + 3) / 4));
+    const dim3 grid = walk_grid((int64_t)a.tokens * a.rank * 64);
     if (dtype == DT_F32) return launch_status(adapter_shrink<DT_F32>, grid, dim3(256), s, a);
     if (dtype == DT_F16) return launch_status(adapter_shrink<DT_F16>, grid, dim3(256), s, a);
     return launch_status(adapter_shrink<DT_BF16>, grid, dim3(256), s, a);

@@ -95,8 +95,10 @@ int check_adapters(const gemm_adapter_set* s, int64_t N, int64_t K) {
     return GEMM_OK;
 }
 
+// Of 16-bit matrices; fp32 kernels walk their elements.
 int check_adapter_threads(int64_t tokens, int64_t cols, int64_t rank, int dtype) {
-    if (dtype == GEMM_F32) return check_threads("tokens * rank", tokens, rank, 64);
+    if (dtype == GEMM_F32) return GEMM_OK;
+    DG_TRY(check_threads("tokens * rank", tokens, ceil_div(rank, 16) * 2, 2));
     return check_threads("blocks of tokens * columns", ceil_div(tokens, 32), ceil_div(cols, 64), 256);
 }
 
@@ -313,8 +315,8 @@ LossTiles loss_tiles(int64_t tokens, int64_t n, bool direct) {
     return {part * 256, part + ceil_div(n - part * 256, 128)};
 }
 int64_t loss_strips(int64_t tokens, int64_t vocabulary) {
-    // either way of reading, the narrow tiles of all columns at the most
-    return tokens <= kSkinny ? ceil_div(vocabulary, 16) : ceil_div(vocabulary, 128);
+    if (tokens <= kSkinny) return ceil_div(vocabulary, 16);
+    return std::max(loss_tiles(tokens, vocabulary, false).strips, loss_tiles(tokens, vocabulary, true).strips);
 }
 
 LossSpace loss_space(void* workspace, int64_t tokens, int64_t vocabulary, int64_t K, int dtype) {

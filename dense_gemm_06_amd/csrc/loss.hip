@@ -106,13 +106,24 @@ __global__ __launch_bounds__(256) void loss_factor(const float* grad, int tokens
     factor[1] = __uint_as_float((uint32_t)(127 - 14 + e) << 23);
 }
 
+// Four columns of a row to a thread, rows over grid y.
 template <int DT>
-__global__ __launch_bounds__(256) void scaled_cast(const float* in, int64_t ldi, int64_t n, int cols,
+__global__ __launch_bounds__(256) void scaled_cast(const float* in, int64_t ldi, int rows, int cols,
                                                    const float* factor, void* out, int64_t ldo) {
     const float f = factor ? factor[1] : 1.0f;
-    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
-        const int64_t r = i / cols, c = i - r * cols;
-        store_out(out, DT, (size_t)r * (size_t)ldo + c, in[(size_t)r * (size_t)ldi + c] * f);
+    const int64_t c = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
+    const int left = (int)min((int64_t)4, cols - c);
+    if (left <= 0) return;
+    for (int64_t r = blockIdx.y; r < rows; r += gridDim.y) {
+        const float* src = in + (size_t)r * (size_t)ldi + c;
+        const size_t at = (size_t)r * (size_t)ldo + c;
+        if (left == 4) {
+            f32x4 v;
+            __builtin_memcpy(&v, src, 16);
+            store_out4(out, DT, at, v * f);
+        } else {
+            for (int e = 0; e < left; ++e) store_out(out, DT, at + e, src[e] * f);
+        }
     }
 }
 
@@ -134,11 +145,10 @@ int launch_loss_factor(const float* grad, int tokens, float* factor, hipStream_t
 
 int launch_scaled_cast(const float* in, int64_t ldi, int rows, int cols, const float* factor, void* out, int64_t ldo,
                        int dtype, hipStream_t s) {
-    const int64_t n = (int64_t)rows * cols, wgs = (n + 255) / 256;
-    const dim3 grid((unsigned)(wgs < (1 << 16) ? wgs : (1 << 16)));
-    if (dtype == DT_F32) return launch_status(scaled_cast<DT_F32>, grid, dim3(256), s, in, ldi, n, cols, factor, out, ldo);
-    if (dtype == DT_F16) return launch_status(scaled_cast<DT_F16>, grid, dim3(256), s, in, ldi, n, cols, factor, out, ldo);
-    return launch_status(scaled_cast<DT_BF16>, grid, dim3(256), s, in, ldi, n, cols, factor, out, ldo);
+    const dim3 grid((unsigned)(((int64_t)cols + 1023) / 1024), (unsigned)(rows < 32768 ? rows : 32768));
+    if (dtype == DT_F32) return launch_status(scaled_cast<DT_F32>, grid, dim3(256), s, in, ldi, rows, cols, factor, out, ldo);
+    if (dtype == DT_F16) return launch_status(scaled_cast<DT_F16>, grid, dim3(256), s, in, ldi, rows, cols, factor, out, ldo);
+    return launch_status(scaled_cast<DT_BF16>, grid, dim3(256), s, in, ldi, rows, cols, factor, out, ldo);
 }
 
 }  // namespace dg

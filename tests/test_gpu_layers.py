@@ -81,6 +81,21 @@ def test_adapters_tiles(dt):
     check_adapters(*adapter_inputs(2100, 4096, 512, 7, 16, dt, runs=True, seed=3))
 
 
+@pytest.mark.parametrize("dt", [BF16, F16])
+@pytest.mark.parametrize("pad", [0, 1])
+def test_adapters_tiles_of_odd_rows(pad, dt):
+    """Tiles whose rows start at any even byte, forward (many columns of y) and backward (of x)."""
+    check_adapters(*adapter_inputs(2100, 4099, 203, 5, 20, dt, pad=pad, runs=True, seed=4), grad_pad=pad)
+    check_adapters(*adapter_inputs(2100, 203, 4099, 5, 20, dt, pad=pad, runs=True, seed=5), grad_pad=pad)
+
+
+def test_adapters_many_in_a_tile():
+    """Every row of a tile another adapter's, and ranks on both sides of what the tiles hold."""
+    for rank in (64, 65):
+        x, w, a, b, index, scale = adapter_inputs(2050, 4096, 64, 40, rank, BF16, seed=rank)
+        check_adapters(x, w, a, b, index, scale, backward=rank == 64)
+
+
 def test_adapters_without_scale_and_without_rows():
     x, w, a, b, index, scale = adapter_inputs(40, 128, 128, 4, 16, BF16, seed=4)
     index = torch.where(index == 2, 1, index)  # adapter 2 has no rows
@@ -196,6 +211,18 @@ def test_loss_strided(pad, dt):
 def test_loss_tiles(dt):
     check_loss(*loss_inputs(520, 9000, 256, dt, seed=1))
     check_loss(*loss_inputs(1024, 4096, 512, dt, seed=2))
+
+
+@pytest.mark.parametrize("dt", [BF16, F16])
+def test_loss_wide_and_narrow_tiles(dt):
+    """A whole round of wide tiles and the rest in narrow ones."""
+    check_loss(*loss_inputs(2041, 9003, 64, dt, seed=8))
+
+
+@pytest.mark.parametrize("dt", [BF16, F16])
+@pytest.mark.parametrize("T,V,K,pad", [(100, 520, 77, 0), (300, 1029, 80, 1), (513, 300, 131, 3)])
+def test_loss_odd_rows(T, V, K, pad, dt):
+    check_loss(*loss_inputs(T, V, K, dt, pad=pad, seed=T))
 
 
 @pytest.mark.parametrize("dt", [BF16, F16, F32])
