@@ -49,13 +49,28 @@ __device__ __forceinline__ void act_value(float v, int act, float& f, float& slo
     }
 }
 
-template <int DT>
+// N 16-byte pieces at any address, past the caches with PASSING (no branch at run time:
+// one took half of the gain).
+template <int N, bool PASSING>
+__device__ __forceinline__ void load_pieces(void* to, const void* from) {
+    typedef u32x4 any_address __attribute__((aligned(1)));
+    if (!PASSING) {
+        __builtin_memcpy(to, from, 16 * N);
+    } else {
+        u32x4 q[N];
+#pragma unroll
+        for (int k = 0; k < N; ++k) q[k] = __builtin_nontemporal_load(static_cast<const any_address*>(from) + k);
+        __builtin_memcpy(to, q, sizeof q);
+    }
+}
+
+template <int DT, bool PASSING>
 __device__ __forceinline__ void load_row8(float (&v)[8], const void* p, size_t at, int valid) {
     typedef typename Elem<DT>::type T;
     const T* src = static_cast<const T*>(p) + at;
     T raw[8];
     if (valid >= 8) {
-        __builtin_memcpy(raw, src, sizeof raw);
+        load_pieces<sizeof raw / 16, PASSING>(raw, src);
     } else {
 #pragma unroll
         for (int e = 0; e < 8; ++e) raw[e] = e < valid ? src[e] : T(0);
@@ -64,11 +79,25 @@ __device__ __forceinline__ void load_row8(float (&v)[8], const void* p, size_t a
     for (int e = 0; e < 8; ++e) v[e] = decode<DT>(raw[e]);
 }
 
-template <int DT>
+// Eight results: past the caches where all of them together would not stay there (PASSING), as
+// one store of 16 bytes; else as two stores, since one made the whole pass 10% slower.
+template <int DT, bool PASSING>
 __device__ __forceinline__ void store_row8(void* p, size_t at, const float (&v)[8], int valid) {
     if (valid >= 8) {
-        store_out4(p, DT, at, f32x4{v[0], v[1], v[2], v[3]});
-        store_out4(p, DT, at + 4, f32x4{v[4], v[5], v[6], v[7]});
+        if constexpr (!PASSING) {
+            store_out4(p, DT, at, f32x4{v[0], v[1], v[2], v[3]});
+            store_out4(p, DT, at + 4, f32x4{v[4], v[5], v[6], v[7]});
+        } else if constexpr (DT == DT_F32) {
+            store_passing(static_cast<float*>(p) + at, f32x4{v[0], v[1], v[2], v[3]});
+            store_passing(static_cast<float*>(p) + at + 4, f32x4{v[4], v[5], v[6], v[7]});
+        } else {
+            uint32_t h[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                h[e] = DT == DT_F16 ? (uint32_t)__builtin_bit_cast(uint16_t, (_Float16)v[e]) : (uint32_t)f32_to_bf16_rne(v[e]);
+            store_passing(static_cast<uint16_t*>(p) + at, u32x4{h[0] | (h[1] << 16), h[2] | (h[3] << 16),
+                                                                h[4] | (h[5] << 16), h[6] | (h[7] << 16)});
+        }
     } else {
 #pragma unroll
         for (int e = 0; e < 8; ++e)
@@ -126,7 +155,7 @@ __device__ __forceinline__ void unit_of(int64_t first, int per, int& row, int& k
 // A unit is a block of 128 columns of y with the block(s) of z behind it. Where the second
 // half of z does not start with a block (SPLIT), a row's units are first the blocks of z,
 // which only make codes, and then the blocks of y.
-template <int DT, bool SPLIT>
+template <int DT, bool SPLIT, bool PASSING>
 __global__ __launch_bounds__(256) void activation_forward(ActArgs a, int64_t units, int per) {
     const int zcols = a.gated ? 2 * a.cols : a.cols;
     const int zblocks = SPLIT ? pieces<128>(zcols) : 0;
@@ -142,8 +171,8 @@ __global__ __launch_bounds__(256) void activation_forward(ActArgs a, int64_t uni
         const int valid = c64 < width ? (int)(width - c64) : 0, c = valid > 0 ? (int)c64 : 0;
         const size_t zrow = (size_t)row * (size_t)a.ldz;
         float v[8], w[8];
-        load_row8<DT>(v, a.z, zrow + c, valid);
-        if (a.gated && !code_unit) load_row8<DT>(w, a.z, zrow + a.cols + c, valid);
+        load_row8<DT, PASSING>(v, a.z, zrow + c, valid);
+        if (a.gated && !code_unit) load_row8<DT, PASSING>(w, a.z, zrow + a.cols + c, valid);
         if (!code_unit) {
             float y[8];
 #pragma unroll
@@ -152,7 +181,7 @@ __global__ __launch_bounds__(256) void activation_forward(ActArgs a, int64_t uni
                 act_value<false>(v[e], a.act, y[e], slope);
                 if (a.gated) y[e] *= w[e];
             }
-            store_row8<DT>(a.y, (size_t)row * (size_t)a.ldy + c, y, valid);
+            store_row8<DT, PASSING>(a.y, (size_t)row * (size_t)a.ldy + c, y, valid);
         }
         if (a.codes.q == nullptr) continue;
         if (!SPLIT || code_unit) quantize_block(a.codes, v, row, blk, c, valid);
@@ -191,7 +220,7 @@ __device__ __forceinline__ void decode_row8(float (&v)[8], const QuantOut& o, in
     }
 }
 
-template <int DT>
+template <int DT, bool PASSING>
 __global__ __launch_bounds__(256) void activation_backward(ActArgs a, int64_t units, int per) {
     const int zcols = a.gated ? 2 * a.cols : a.cols;
     const int groups = (int)blockDim.x >> 4, g = (int)threadIdx.x >> 4;
@@ -203,7 +232,7 @@ __global__ __launch_bounds__(256) void activation_backward(ActArgs a, int64_t un
         if (c64 >= a.cols) continue;
         const int c = (int)c64, valid = a.cols - c;
         float v[8], w[8], gr[8], z1[8], z2[8], y[8];
-        if (a.grad) load_row8<DT>(gr, a.grad, (size_t)row * (size_t)a.ldg + c, valid);
+        if (a.grad) load_row8<DT, PASSING>(gr, a.grad, (size_t)row * (size_t)a.ldg + c, valid);
         decode_row8(v, a.codes, row, c, valid, a.cols);
         if (a.gated) decode_row8(w, a.codes, row, a.cols + c, valid, zcols);
 #pragma unroll
@@ -221,9 +250,9 @@ __global__ __launch_bounds__(256) void activation_backward(ActArgs a, int64_t un
             }
         }
         const size_t at = (size_t)row * (size_t)a.ldzg + c;
-        if (a.grad) store_row8<DT>(a.z_grad, at, z1, valid);
-        if (a.grad && a.gated) store_row8<DT>(a.z_grad, at + a.cols, z2, valid);
-        if (a.y) store_row8<DT>(a.y, (size_t)row * (size_t)a.ldy + c, y, valid);
+        if (a.grad) store_row8<DT, PASSING>(a.z_grad, at, z1, valid);
+        if (a.grad && a.gated) store_row8<DT, PASSING>(a.z_grad, at + a.cols, z2, valid);
+        if (a.y) store_row8<DT, PASSING>(a.y, (size_t)row * (size_t)a.ldy + c, y, valid);
     }
 }
 
@@ -246,12 +275,16 @@ int launch_activation(const ActArgs& a, int dtype, hipStream_t s) {
     const int64_t units = (int64_t)a.rows * per;
     dim3 grid, block;
     shape(units, grid, block);
-#define DG_ACT(DT)                                                                                                  \
-    return split ? launch_status(activation_forward<DT, true>, grid, block, s, a, units, per)                      \
-                 : launch_status(activation_forward<DT, false>, grid, block, s, a, units, per)
-    if (dtype == DT_F32) DG_ACT(DT_F32);
-    if (dtype == DT_F16) DG_ACT(DT_F16);
-    DG_ACT(DT_BF16);
+#define DG_ACT(DT, PASSING)                                                                                   \
+    return split ? launch_status(activation_forward<DT, true, PASSING>, grid, block, s, a, units, per)        \
+                 : launch_status(activation_forward<DT, false, PASSING>, grid, block, s, a, units, per)
+#define DG_ACT_DT(DT)              \
+    if (a.passing) DG_ACT(DT, true); \
+    DG_ACT(DT, false)
+    if (dtype == DT_F32) { DG_ACT_DT(DT_F32); }
+    if (dtype == DT_F16) { DG_ACT_DT(DT_F16); }
+    DG_ACT_DT(DT_BF16);
+#undef DG_ACT_DT
 #undef DG_ACT
 }
 
@@ -260,9 +293,13 @@ int launch_activation_backward(const ActArgs& a, int dtype, hipStream_t s) {
     const int64_t units = (int64_t)a.rows * per;
     dim3 grid, block;
     shape(units, grid, block);
-    if (dtype == DT_F32) return launch_status(activation_backward<DT_F32>, grid, block, s, a, units, per);
-    if (dtype == DT_F16) return launch_status(activation_backward<DT_F16>, grid, block, s, a, units, per);
-    return launch_status(activation_backward<DT_BF16>, grid, block, s, a, units, per);
+#define DG_ACT(DT)                                                                                  \
+    return a.passing ? launch_status(activation_backward<DT, true>, grid, block, s, a, units, per) \
+                     : launch_status(activation_backward<DT, false>, grid, block, s, a, units, per)
+    if (dtype == DT_F32) DG_ACT(DT_F32);
+    if (dtype == DT_F16) DG_ACT(DT_F16);
+    DG_ACT(DT_BF16);
+#undef DG_ACT
 }
 
 }  // namespace dg

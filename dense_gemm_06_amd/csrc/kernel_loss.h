@@ -5,7 +5,8 @@
 // one row, so they take two passes over registers and one exchange; the four waves along a row
 // are joined in LDS. Backward: d = (exp(l - lse) - [target]) grad, rounded to the matrices' type
 // (fp16 after a power of two that keeps it in range), stored by rows for the product with w and
-// turned for the product with x.
+// turned for the product with x. Where the target's p is below 1/2 the rows hold p and not p - 1, and
+// x's gradient gets the rest, most of such a row's d, unrounded when it is rounded itself.
 #pragma once
 #include "device_common.h"
 #include "kernel_mid.h"
@@ -181,7 +182,8 @@ struct LossGradHook {
     const float* lse;
     const float* grad;
     const float* factor;   // or NULL
-    uint16_t* d;           // tokens x n, or NULL
+    uint16_t* d;           // tokens x n, or NULL: where p < 1/2 without the target's -1
+    float* apart;          // tokens, with d: 1 where it was left out, else 0
     uint16_t* dt;          // n x lddt, or NULL
     int64_t ldd, lddt;
     int tokens, n, v0, vocabulary;
@@ -193,6 +195,8 @@ struct LossGradHook {
         const Tile tile{lds, lds2};
         const int lane = threadIdx.x & 63, l32 = lane & 31, lh = lane >> 5;
         const float f = factor ? factor[0] : 1.0f;
+        uint32_t hit[SI];      // the target's (p - 1) grad, where this lane has it and d does not hold it,
+        int hit_at[SI];        // and its column in the wave's tile, or -1
 #pragma unroll
         for (int i = 0; i < SI; ++i) {
             const int r = wm * Tile::HALF + 32 * i + l32, row = m0 + 32 * i + l32;
@@ -209,7 +213,9 @@ struct LossGradHook {
                 }
             }
             const bool live = g != 0.0f;  // a NaN is live
-            const int t = at >= 0 && at < 32 * SJ ? (int)at - 4 * lh : -1;
+            const int t = live && at >= 0 && at < 32 * SJ ? (int)at - 4 * lh : -1;
+            float mine = 0.0f;
+            bool has = false, low = false;
 #pragma unroll
             for (int j = 0; j < SJ; ++j) {
                 if constexpr (SI == 4) asm volatile("" : "+a"(acc[i][j]));  // see full_epilogue
@@ -219,16 +225,32 @@ struct LossGradHook {
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         const float p = __builtin_amdgcn_exp2f(fmaf(acc[i][j][4 * q + e], kLog2e, c));
-                        v[e] = live ? (p - (t == 32 * j + 8 * q + e ? 1.0f : 0.0f)) * g : 0.0f;
+                        const bool here = t == 32 * j + 8 * q + e;
+                        const float all = (p - 1.0f) * g;
+                        v[e] = live ? (here && !(p < 0.5f) ? all : p * g) : 0.0f;
+                        mine = here ? all : mine;
+                        low = here ? p < 0.5f : low;
+                        has = has || here;
                     }
                     tile.template put<DT>(r, wn, j, q, lh, v);
                 }
             }
+            hit[i] = DT == DT_F16 ? (uint32_t)__builtin_bit_cast(uint16_t, (_Float16)mine) : (uint32_t)f32_to_bf16_rne(mine);
+            hit_at[i] = has && low ? (int)at : -1;
+            if (d && has) apart[row] = low ? 1.0f : 0.0f;
         }
         __syncthreads();
         const int wave = threadIdx.x >> 6, tile_m = m0 - wm * Tile::HALF, tile_n = n0 - wn * 32 * SJ;
         if (d) tile.store(d, ldd, tile_m, tile_n, tokens, n);
         if (dt) {
+            if (d) __syncthreads();
+#pragma unroll
+            for (int i = 0; i < SI; ++i)
+                if (hit_at[i] >= 0) {
+                    const int col = wn * 32 * SJ + hit_at[i];
+                    *reinterpret_cast<uint16_t*>(tile.at(wm * Tile::HALF + 32 * i + l32, col >> 3) + (col & 7) * 2) = (uint16_t)hit[i];
+                }
+            __syncthreads();
             // a wave: 32 columns, 32 rows at a time: 16 lanes get eight rows of 16 columns
             static_assert(Tile::COLS / Tile::WAVES == 32, "columns of a wave");
             const int l16 = lane & 15, lg = lane >> 4;

@@ -25,6 +25,7 @@ struct ActArgs {
     QuantOut codes;      // of z (q == NULL: forward without); backward reads them
     int rows, cols;      // of y; zcols = cols, or 2 cols with a gate
     int act, gated;
+    int passing;         // results leave past the caches
     void* y;             // NULL: not wanted (backward)
     int64_t ldy;
     const void* grad;    // backward
@@ -54,6 +55,7 @@ struct LossArgs {
     const float* grad;
     const float* factor;    // device: [0] what grad is multiplied with, [1] its inverse
     void* d;
+    float* apart;           // 16 bits: 1 where d leaves the target's -1 to x's gradient
     int64_t ldd;
     void* dt;
     int64_t lddt;
@@ -83,9 +85,10 @@ int launch_loss_stats(const LossArgs& a, hipStream_t s);
 int launch_loss_grad(const LossArgs& a, int dtype, hipStream_t s);
 // factor[0], factor[1]: powers of two that bring the largest finite |grad| near 2^14, and back
 int launch_loss_factor(const float* grad, int tokens, float* factor, hipStream_t s);
-// out (rows x cols, dtype) = in (fp32) * factor[1]
+// out (rows x cols, 16 bits) = in (fp32) * factor[1], less apart[t] grad[t] w[target[t]] in row t where w is given
 int launch_scaled_cast(const float* in, int64_t ldi, int rows, int cols, const float* factor, void* out, int64_t ldo,
-                       int dtype, hipStream_t s);
+                       const void* w, int64_t ldw, const int64_t* target, int vocabulary, const float* grad,
+                       const float* apart, int dtype, hipStream_t s);
 
 // ---------------------------------------------------------------- adapters
 struct AdapterArgs {

@@ -285,6 +285,7 @@ struct LossSpace {
     float* sum = nullptr;
     float* picked = nullptr;
     float* factor = nullptr;
+    float* apart = nullptr;
     void* d = nullptr;
     void* dt = nullptr;
     void* xp = nullptr;     // x with rows of zeros up to lddt
@@ -351,6 +352,7 @@ LossSpace loss_backward_space(void* workspace, int64_t tokens, int64_t vocabular
     s.piece = piece > 0 ? std::min(piece, std::max<int64_t>(1, vocabulary)) : piece_of(tokens, vocabulary, es);
     s.lddt = (tokens + 31) / 32 * 32;
     s.factor = static_cast<float*>(p.take(8));
+    s.apart = static_cast<float*>(p.take(tokens * 4));
     if (!loss_fused(vocabulary, K, dtype)) s.logits = static_cast<float*>(p.take(tokens * s.piece * 4));
     s.ldd = dtype == GEMM_F32 ? s.piece : ceil_div(s.piece, 8) * 8;
     if (x_grad) s.d = s.logits && dtype == GEMM_F32 ? s.logits : p.take(tokens * s.ldd * es);  // in place in fp32
@@ -393,6 +395,10 @@ int check_codes(const gemm_block_matrix& m, int64_t rows, int64_t zcols) {
               (long long)zcols);
     return GEMM_ERR_INVALID_VALUE;
 }
+
+// Matrices of 128 MB and more, half the last level of cache, pass it (8192 x 8192 gated bf16, both
+// ways: 254 to 233 us); smaller ones are found there (2001 x 5003 fp16: 35 us, past it 41).
+bool past_caches(int64_t rows, int64_t cols, int64_t es) { return rows * cols >= ((int64_t)128 << 20) / es; }
 
 dg::QuantOut codes_of(const gemm_block_matrix& m) {
     dg::QuantOut o;
@@ -805,6 +811,7 @@ int gemm_loss_backward(const float* grad, const void* x, int64_t tokens, int64_t
     a.grad = grad;
     a.factor = scaled ? sp.factor : nullptr;
     a.d = sp.d;
+    a.apart = sp.apart;
     a.dt = sp.dt;
     a.lddt = sp.lddt;
     if (scaled) DG_TRY(launched(dg::launch_loss_factor(grad, (int)tokens, sp.factor, s), "loss gradient's factor"));
@@ -866,14 +873,16 @@ int gemm_loss_backward(const float* grad, const void* x, int64_t tokens, int64_t
                                sp.w_acc ? K : ldwg, dtype, sp.w_acc ? GEMM_F32 : dtype, 0.0f, sp.product,
                                sp.product_bytes, stream));
                 if (sp.w_acc)
-                    DG_TRY(launched(dg::launch_scaled_cast(sp.w_acc, K, (int)n, (int)K, sp.factor, wg, ldwg, dtype, s),
-                                    "loss gradient's rounding"));
+                    DG_TRY(launched(dg::launch_scaled_cast(sp.w_acc, K, (int)n, (int)K, sp.factor, wg, ldwg, nullptr, 0,
+                                                           nullptr, 0, nullptr, nullptr, dtype, s), "loss gradient's rounding"));
             }
         }
         v0 += n;
     } while (v0 < vocabulary);
     if (x_grad && !wide && tokens > 0)
-        DG_TRY(launched(dg::launch_scaled_cast(sp.x_acc, K, (int)tokens, (int)K, a.factor, x_grad, ldxg, dtype, s),
+        DG_TRY(launched(dg::launch_scaled_cast(sp.x_acc, K, (int)tokens, (int)K, a.factor, x_grad, ldxg,
+                                               sp.logits ? nullptr : w, ldw, target, (int)vocabulary, grad, sp.apart,
+                                               dtype, s),
                         "loss gradient's rounding"));
     return GEMM_OK;
 }
@@ -916,6 +925,7 @@ int gemm_activation_forward(const void* z, int64_t rows, int64_t cols, int64_t l
     a.gated = gated != 0;
     a.y = y;
     a.ldy = ldy;
+    a.passing = past_caches(rows, cols, es);
     return launched(dg::launch_activation(a, dtype, (hipStream_t)stream), "activation");
 }
 
@@ -958,6 +968,7 @@ int gemm_activation_backward(const gemm_block_matrix* codes, const void* grad, i
     a.ldg = ldg;
     a.z_grad = z_grad;
     a.ldzg = ldzg;
+    a.passing = past_caches(rows, grad ? zcols : cols, es);
     return launched(dg::launch_activation_backward(a, dtype, (hipStream_t)stream), "activation's backward pass");
 }
 

@@ -106,10 +106,12 @@ __global__ __launch_bounds__(256) void loss_factor(const float* grad, int tokens
     factor[1] = __uint_as_float((uint32_t)(127 - 14 + e) << 23);
 }
 
-// Four columns of a row to a thread, rows over grid y.
+// out = in factor[1] - apart[t] grad[t] w[target[t]] for x's gradient (w NULL: without the second term). Four columns of a row to a thread, rows over grid y.
 template <int DT>
 __global__ __launch_bounds__(256) void scaled_cast(const float* in, int64_t ldi, int rows, int cols,
-                                                   const float* factor, void* out, int64_t ldo) {
+                                                   const float* factor, void* out, int64_t ldo, const void* w,
+                                                   int64_t ldw, const int64_t* target, int vocabulary,
+                                                   const float* grad, const float* apart) {
     const float f = factor ? factor[1] : 1.0f;
     const int64_t c = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
     const int left = (int)min((int64_t)4, cols - c);
@@ -117,12 +119,30 @@ __global__ __launch_bounds__(256) void scaled_cast(const float* in, int64_t ldi,
     for (int64_t r = blockIdx.y; r < rows; r += gridDim.y) {
         const float* src = in + (size_t)r * (size_t)ldi + c;
         const size_t at = (size_t)r * (size_t)ldo + c;
+        float g = 0.0f;
+        size_t row = 0;
+        if (w) {
+            const int64_t t = target[r];
+            if (t >= 0 && t < vocabulary && grad[r] != 0.0f && apart[r] != 0.0f) {
+                g = grad[r];
+                row = (size_t)t * (size_t)ldw + c;
+            }
+        }
         if (left == 4) {
             f32x4 v;
             __builtin_memcpy(&v, src, 16);
-            store_out4(out, DT, at, v * f);
+            v = v * f;
+            if (g != 0.0f) {
+                const f32x4 h = load_out4(w, DT, row);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) v[e] = fmaf(-g, h[e], v[e]);
+            }
+            store_out4(out, DT, at, v);
         } else {
-            for (int e = 0; e < left; ++e) store_out(out, DT, at + e, src[e] * f);
+            for (int e = 0; e < left; ++e) {
+                const float v = src[e] * f;
+                store_out(out, DT, at + e, g != 0.0f ? fmaf(-g, load_out(w, DT, row + e), v) : v);
+            }
         }
     }
 }
@@ -144,11 +164,13 @@ int launch_loss_factor(const float* grad, int tokens, float* factor, hipStream_t
 }
 
 int launch_scaled_cast(const float* in, int64_t ldi, int rows, int cols, const float* factor, void* out, int64_t ldo,
-                       int dtype, hipStream_t s) {
+                       const void* w, int64_t ldw, const int64_t* target, int vocabulary, const float* grad,
+                       const float* apart, int dtype, hipStream_t s) {
     const dim3 grid((unsigned)(((int64_t)cols + 1023) / 1024), (unsigned)(rows < 32768 ? rows : 32768));
-    if (dtype == DT_F32) return launch_status(scaled_cast<DT_F32>, grid, dim3(256), s, in, ldi, rows, cols, factor, out, ldo);
-    if (dtype == DT_F16) return launch_status(scaled_cast<DT_F16>, grid, dim3(256), s, in, ldi, rows, cols, factor, out, ldo);
-    return launch_status(scaled_cast<DT_BF16>, grid, dim3(256), s, in, ldi, rows, cols, factor, out, ldo);
+    return dtype == DT_F16 ? launch_status(scaled_cast<DT_F16>, grid, dim3(256), s, in, ldi, rows, cols, factor, out, ldo,
+                                           w, ldw, target, vocabulary, grad, apart)
+                           : launch_status(scaled_cast<DT_BF16>, grid, dim3(256), s, in, ldi, rows, cols, factor, out, ldo,
+                                           w, ldw, target, vocabulary, grad, apart);
 }
 
 }  // namespace dg
