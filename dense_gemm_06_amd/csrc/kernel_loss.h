@@ -301,7 +301,7 @@ struct RowsHook {
                 }
             }
         __syncthreads();
-        tile.store(out, ld, m0 - wm * Tile::HALF, n0 - wn * 32 * SJ, rows, cols);
+        tile.template store<true>(out, ld, m0 - wm * Tile::HALF, n0 - wn * 32 * SJ, rows, cols);
     }
 };
 

@@ -26,7 +26,8 @@ struct Tile16 {
             h[e] = DT == DT_F16 ? (uint32_t)__builtin_bit_cast(uint16_t, (_Float16)v[e]) : (uint32_t)f32_to_bf16_rne(v[e]);
         *reinterpret_cast<u32x2*>(at(r, wn * (4 * SJ) + 4 * j + q) + 8 * lh) = u32x2{h[0] | (h[1] << 16), h[2] | (h[3] << 16)};
     }
-    // rows x cols of the tile at (m, n) to out
+    // rows x cols of the tile at (m, n) to out, past the caches with PASSING
+    template <bool PASSING = false>
     __device__ __forceinline__ void store(uint16_t* out, int64_t ld, int m, int n, int rows, int cols) const {
         constexpr int RI = 64 / PIECES, IT = 2 * HALF / WAVES / RI;  // rows of a load, loads of a wave
         const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -37,11 +38,14 @@ struct Tile16 {
             const u32x4 v = *reinterpret_cast<const u32x4*>(at(r, piece));
             if (row >= rows || left <= 0) continue;
             uint16_t* dst = out + (size_t)row * (size_t)ld + c;
-            if (left >= 8) __builtin_memcpy(dst, &v, 16);
-            else
+            if (left >= 8) {
+                if constexpr (PASSING) store_passing(dst, v);
+                else __builtin_memcpy(dst, &v, 16);
+            } else {
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
                     if (e < left) dst[e] = (uint16_t)(v[e >> 1] >> (16 * (e & 1)));
+            }
         }
     }
 };
