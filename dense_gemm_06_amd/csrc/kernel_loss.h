@@ -185,6 +185,7 @@ struct LossGradHook {
     uint16_t* d;           // tokens x n, or NULL: where p < 1/2 without the target's -1
     float* apart;          // tokens, with d: 1 where it was left out, else 0
     uint16_t* dt;          // n x lddt, or NULL
+    float* rest;           // tokens, with dt: what rounding took from the target's d
     int64_t ldd, lddt;
     int tokens, n, v0, vocabulary;
 
@@ -213,7 +214,7 @@ struct LossGradHook {
                 }
             }
             const bool live = g != 0.0f;  // a NaN is live
-            const int t = live && at >= 0 && at < 32 * SJ ? (int)at - 4 * lh : -1;
+            const int t = at >= 0 && at < 32 * SJ ? (int)at - 4 * lh : -1;
             float mine = 0.0f;
             bool has = false, low = false;
 #pragma unroll
@@ -236,8 +237,10 @@ struct LossGradHook {
                 }
             }
             hit[i] = DT == DT_F16 ? (uint32_t)__builtin_bit_cast(uint16_t, (_Float16)mine) : (uint32_t)f32_to_bf16_rne(mine);
-            hit_at[i] = has && low ? (int)at : -1;
-            if (d && has) apart[row] = low ? 1.0f : 0.0f;
+            hit_at[i] = has && low && live ? (int)at : -1;
+            if (d && has) apart[row] = low && live ? 1.0f : 0.0f;
+            const float left = mine - decode<DT>((uint16_t)hit[i]);
+            if (dt && has) rest[row] = live && left == left ? left : 0.0f;  // an infinite d leaves nothing
         }
         __syncthreads();
         const int wave = threadIdx.x >> 6, tile_m = m0 - wm * Tile::HALF, tile_n = n0 - wn * 32 * SJ;
@@ -273,26 +276,115 @@ struct LossGradHook {
     }
 };
 
-// The product itself as 16-bit rows, times factor[1].
+// w's gradient of a tile (256 words from v0 on): the product, plus for each token whose target is
+// among the words what rounding took from its d, times its row of x: a word's gradient is mostly
+// its own tokens' d, so that the result is as near as its own rounding allows (relative error 0.0024
+// to 0.0017 in bf16; 4096 tokens, 65536 words, 4096 long, whole gradient: 7.38 to 7.57 ms). Rounding's rests are few to a tile: they are one more sum over the tokens that
+// the tile finds among all, 16 at a time on the matrix instructions.
 template <int DT>
-struct RowsHook {
+struct LossWHook {
     static constexpr bool kReplace = true;
     uint16_t* out;
     int64_t ld;
     int rows, cols;
     const float* factor;   // or NULL
+    const int64_t* target;
+    const float* rest;
+    const uint16_t* x;
+    int64_t ldx;
+    int tokens, v0;
+
     template <int SI, int SJ, int WM, int WN>
     __device__ __forceinline__ void finish(f32x16 (&acc)[SI][SJ], int m0, int n0, int wm, int wn, char* lds,
                                            char* lds2) const {
         typedef Tile16<SI, SJ, WM, WN> Tile;
+        constexpr int WAVES = WM * WN, BLOCK = WAVES * 512;  // tokens looked at together
         const Tile tile{lds, lds2};
-        const int lane = threadIdx.x & 63, l32 = lane & 31, lh = lane >> 5;
+        const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, l32 = lane & 31, lh = lane >> 5;
+        const int tile_m = m0 - wm * Tile::HALF;
+        int* token = reinterpret_cast<int*>(lds);                            // the tile's tokens in order
+        int* word = reinterpret_cast<int*>(lds + BLOCK * 4 + 64);            // and their rows
+        int* counts = reinterpret_cast<int*>(lds2);
+        const int64_t first = (int64_t)v0 + tile_m;
+        for (int64_t t0 = 0; t0 < tokens; t0 += BLOCK) {
+            uint64_t hit[8];
+            int row[8], mine = 0;
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+                const int64_t t = t0 + wave * 512 + 64 * q + lane;
+                const int64_t at = target[min(t, (int64_t)tokens - 1)] - first;  // all loads before the first wait
+                row[q] = t < tokens && at >= 0 && at < 2 * Tile::HALF && tile_m + at < rows ? (int)at : -1;
+            }
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+                hit[q] = __ballot(row[q] >= 0);
+                mine += (int)__popcll(hit[q]);
+            }
+            if (lane == 0) counts[wave] = mine;
+            __syncthreads();
+            int before = 0, all = 0;
+#pragma unroll
+            for (int w = 0; w < WAVES; ++w) {
+                before += w < wave ? counts[w] : 0;
+                all += counts[w];
+            }
+            all = __builtin_amdgcn_readfirstlane(all);
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+                if (row[q] >= 0) {
+                    const int at = before + (int)__popcll(hit[q] & (((uint64_t)1 << lane) - 1));
+                    token[at] = (int)(t0 + wave * 512 + 64 * q + lane);
+                    word[at] = row[q];
+                }
+                before += (int)__popcll(hit[q]);
+            }
+            if (threadIdx.x < 16) {  // the last 16 are filled up with none
+                token[all + threadIdx.x] = 0;
+                word[all + threadIdx.x] = -1;
+            }
+            __syncthreads();
+            for (int k0 = 0; k0 < all; k0 += 16) {
+                int w[8];
+                float left[8];
+                u32x4 p[SJ];
+                uint16_t xs[SJ][8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const int t = token[k0 + 8 * lh + k];
+                    w[k] = word[k0 + 8 * lh + k];
+                    left[k] = rest[t];
+                    const uint16_t* xr = x + (size_t)t * (size_t)ldx;
+#pragma unroll
+                    for (int j = 0; j < SJ; ++j) xs[j][k] = xr[min(n0 + 32 * j + l32, cols - 1)];
+                }
+                uint32_t r16[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    r16[k] = DT == DT_F16 ? (uint32_t)__builtin_bit_cast(uint16_t, (_Float16)left[k])
+                                          : (uint32_t)f32_to_bf16_rne(left[k]);
+#pragma unroll
+                for (int j = 0; j < SJ; ++j)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) p[j][e] = (uint32_t)xs[j][2 * e] | ((uint32_t)xs[j][2 * e + 1] << 16);
+#pragma unroll
+                for (int i = 0; i < SI; ++i) {
+                    const int r = wm * Tile::HALF + 32 * i + l32;
+                    u32x4 q;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        q[e] = (w[2 * e] == r ? r16[2 * e] : 0u) | (w[2 * e + 1] == r ? r16[2 * e + 1] << 16 : 0u);
+#pragma unroll
+                    for (int j = 0; j < SJ; ++j) acc[i][j] = mfma_32<DT>(p[j], q, acc[i][j]);
+                }
+            }
+            __syncthreads();
+        }
         const float f = factor ? factor[1] : 1.0f;
 #pragma unroll
         for (int i = 0; i < SI; ++i)
 #pragma unroll
             for (int j = 0; j < SJ; ++j) {
-                if constexpr (SI == 4) asm volatile("" : "+a"(acc[i][j]));
+                asm volatile("" : "+a"(acc[i][j]));  // see full_epilogue
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
                     const float v[4] = {acc[i][j][4 * q] * f, acc[i][j][4 * q + 1] * f, acc[i][j][4 * q + 2] * f,
@@ -301,7 +393,7 @@ struct RowsHook {
                 }
             }
         __syncthreads();
-        tile.template store<true>(out, ld, m0 - wm * Tile::HALF, n0 - wn * 32 * SJ, rows, cols);
+        tile.template store<true>(out, ld, tile_m, n0 - wn * 32 * SJ, rows, cols);
     }
 };
 
@@ -318,7 +410,7 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
 
 // w's gradient: d^T (rows of whole stages) x
 template <int DT>
-__global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) void loss_w_tiles(GemmArgs g, RowsHook<DT> h) {
+__global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) void loss_w_tiles(GemmArgs g, LossWHook<DT> h) {
     mfma32_sp_body<DT, 0, 8, false, false, false>(g, nullptr, h);
 }
 

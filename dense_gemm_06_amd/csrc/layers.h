@@ -58,6 +58,7 @@ struct LossArgs {
     float* apart;           // 16 bits: 1 where d leaves the target's -1 to x's gradient
     int64_t ldd;
     void* dt;
+    float* rest;            // 16 bits: what rounding took from the targets' d in dt
     int64_t lddt;
 };
 
@@ -75,9 +76,9 @@ constexpr int64_t kLossPartBytes = 8;
 DG_16BIT(launch_loss_skinny, (const LossProduct& p, const int64_t* target, void* part, float* picked, hipStream_t s))
 DG_16BIT(launch_loss_tiles, (const LossProduct& p, int v0, const int64_t* target, void* part, float* picked, hipStream_t s))
 DG_16BIT(launch_loss_grad_tiles, (const LossProduct& p, const LossArgs& a, hipStream_t s))
-// out (n x cols, 16 bits) = factor[1] dt x: dt n x len, x len x cols; both with rows of whole, aligned
-// 16-byte pieces, len a multiple of 32
-DG_16BIT(launch_loss_w, (const void* dt, int64_t lddt, const void* x, int64_t ldx, int n, int len, int cols, int group_m, const float* factor, void* out, int64_t ldo, hipStream_t s))
+// out (n x cols, 16 bits) = factor[1] (dt x + the targets' rests): dt n x lddt, x lddt x cols; both with
+// rows of whole, aligned 16-byte pieces, lddt a multiple of 32
+DG_16BIT(launch_loss_w, (const LossArgs& a, const void* x, int64_t ldx, int cols, int group_m, void* out, int64_t ldo, hipStream_t s))
 int launch_loss_finish(const void* part, int strips, int tokens, const int64_t* target, int vocabulary,
                        const float* picked, float* loss, float* lse, hipStream_t s);
 

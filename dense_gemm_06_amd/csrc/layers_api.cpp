@@ -286,6 +286,7 @@ struct LossSpace {
     float* picked = nullptr;
     float* factor = nullptr;
     float* apart = nullptr;
+    float* rest = nullptr;
     void* d = nullptr;
     void* dt = nullptr;
     void* xp = nullptr;     // x with rows of zeros up to lddt
@@ -353,6 +354,7 @@ LossSpace loss_backward_space(void* workspace, int64_t tokens, int64_t vocabular
     s.lddt = (tokens + 31) / 32 * 32;
     s.factor = static_cast<float*>(p.take(8));
     s.apart = static_cast<float*>(p.take(tokens * 4));
+    s.rest = static_cast<float*>(p.take(tokens * 4));
     if (!loss_fused(vocabulary, K, dtype)) s.logits = static_cast<float*>(p.take(tokens * s.piece * 4));
     s.ldd = dtype == GEMM_F32 ? s.piece : ceil_div(s.piece, 8) * 8;
     if (x_grad) s.d = s.logits && dtype == GEMM_F32 ? s.logits : p.take(tokens * s.ldd * es);  // in place in fp32
@@ -812,6 +814,7 @@ int gemm_loss_backward(const float* grad, const void* x, int64_t tokens, int64_t
     a.factor = scaled ? sp.factor : nullptr;
     a.d = sp.d;
     a.apart = sp.apart;
+    a.rest = sp.rest;
     a.dt = sp.dt;
     a.lddt = sp.lddt;
     if (scaled) DG_TRY(launched(dg::launch_loss_factor(grad, (int)tokens, sp.factor, s), "loss gradient's factor"));
@@ -866,8 +869,7 @@ int gemm_loss_backward(const float* grad, const void* x, int64_t tokens, int64_t
         if (w_grad && n > 0) {
             char* wg = static_cast<char*>(w_grad) + (size_t)v0 * ldwg * es;
             if (sp.xp && tokens > 0) {
-                DG_TRY(launched(DG_BY_TYPE(launch_loss_w, dtype, sp.dt, sp.lddt, xw, ldxw, (int)n, (int)sp.lddt, (int)K,
-                                           tile_group(n, K), a.factor, wg, ldwg, s), "loss gradient of w"));
+                DG_TRY(launched(DG_BY_TYPE(launch_loss_w, dtype, a, xw, ldxw, (int)K, tile_group(n, K), wg, ldwg, s), "loss gradient of w"));
             } else {
                 DG_TRY(product(GEMM_OP_N, n, K, tokens, sp.dt, sp.lddt, x, ldx, sp.w_acc ? (void*)sp.w_acc : wg,
                                sp.w_acc ? K : ldwg, dtype, sp.w_acc ? GEMM_F32 : dtype, 0.0f, sp.product,

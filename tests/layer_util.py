@@ -122,15 +122,22 @@ def loss_backward(grad, x, w, target, lse):
     d_err = scale * (p * (torch.expm1(l_err) + (4 * arg + 8) * F32) + (p + hit) * 3 * F32)
     # an exponential, or a d, below the smallest normal number 2^-126 may count as zero: off by less than that
     d_err = d_err + (scale + 1) * (scale > 0) * 2.0 ** -126
+    dx_err = dw_err = d_err
     if dt != torch.float32:
-        d_err = d_err + d.abs() * HALF[dt] * 1.01
+        # d is rounded. Rows of 8 and more: the target's -1 is left out of x's where p < 1/2 (p < 0.51 here:
+        # the kernel's p decides) and added in fp32, and w's gets what the target's rounding took, rounded
+        left_out = hit if x.shape[1] >= 8 else 0 * hit
+        dx_err = dx_err + (torch.where((left_out > 0) & (p < 0.49), p, (p - hit).abs()) * scale) * HALF[dt] * 1.01
+        dx_err = dx_err + left_out * ((p >= 0.49) & (p < 0.51)) * scale * HALF[dt] * 0.03
+        dw_err = dw_err + d.abs() * torch.where(left_out > 0, HALF[dt] ** 2, HALF[dt]) * 1.01
         if dt == torch.float16:
             # held times a power of two that brings the largest |g| to 2^13 .. 2^14
-            d_err = d_err + 2.0 ** -25 * 2.0 ** (math.frexp(float(g.abs().max()))[1] - 13) * (scale > 0)
+            low = 2.0 ** -25 * 2.0 ** (math.frexp(float(g.abs().max()))[1] - 13) * (scale > 0)
+            dx_err, dw_err = dx_err + low, dw_err + low
     grow = 1 + HALF[dt]
     xg, wg = d @ w, d.t() @ x
-    xg_err = d_err @ w.abs() * 1.01 + (d.abs() @ w.abs()) * (V + 40) * F32
-    wg_err = d_err.t() @ x.abs() * 1.01 + (d.abs().t() @ x.abs()) * (T + 4) * F32
+    xg_err = dx_err @ w.abs() * 1.01 + ((d.abs() + 2 * hit * scale) @ w.abs()) * (V + 40) * F32
+    wg_err = dw_err.t() @ x.abs() * 1.01 + (d.abs().t() @ x.abs()) * (T + 4) * F32
     return (xg, xg_err * grow + rounded(xg, dt)), (wg, wg_err * grow + rounded(wg, dt))
 
 

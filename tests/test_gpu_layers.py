@@ -288,6 +288,24 @@ def test_loss_gradient_scales(size):
     assert (dg.gemm_loss_backward_tensors(grad, x, w, target, lse)[0][5] == 0).all()
 
 
+@pytest.mark.parametrize("dt", [BF16, F16])
+def test_loss_rows_of_no_gradient(dt):
+    """Tokens of gradient 0, or of one that the fp16 scale brings to 0, add nothing to the word that is
+    their target, whatever the workspace held before."""
+    x, w, target, grad = loss_inputs(70, 300, 64, dt, seed=9)
+    target[::2] = 7
+    grad[::4], grad[1], grad[2] = 0, 2.0 ** 100, 2.0 ** -140
+    lse = dg.gemm_loss_tensors(x, w, target)[1]
+    held = [torch.full((2 ** k,), float("nan"), device="cuda") for k in range(8, 22) for _ in range(2)]
+    del held
+    _, wg = dg.gemm_loss_backward_tensors(grad, x, w, target, lse)
+    xg, only = dg.gemm_loss_backward_tensors(grad, x, w, target, lse)
+    (xr, xe), (wr, we) = lu.loss_backward(grad, x, w, target, lse)
+    lu.check(xg, xr, xe, "x_grad")
+    lu.check(wg, wr, we, "w_grad")
+    assert torch.equal(wg, only) and (xg[::4] == 0).all()
+
+
 def test_loss_differences():
     x, w, target, grad = loss_inputs(6, 11, 5, F32, seed=7)
     lse = dg.gemm_loss_tensors(x, w, target)[1]
