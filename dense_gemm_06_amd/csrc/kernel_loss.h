@@ -277,10 +277,11 @@ struct LossGradHook {
 };
 
 // w's gradient of a tile (256 words from v0 on): the product, plus for each token whose target is
-// among the words what rounding took from its d, times its row of x: a word's gradient is mostly
-// its own tokens' d, so that the result is as near as its own rounding allows (relative error 0.0024
-// to 0.0017 in bf16; 4096 tokens, 65536 words, 4096 long, whole gradient: 7.38 to 7.57 ms). Rounding's rests are few to a tile: they are one more sum over the tokens that
-// the tile finds among all, 16 at a time on the matrix instructions.
+// among the words what rounding took from its d, times its row of x. A word's gradient is mostly its
+// own tokens' d, so the result comes as near as its own rounding allows (relative error 0.0024 to
+// 0.0017 in bf16; the whole backward of 4096 tokens, 65536 words, 4096 long: 7.38 to 7.57 ms). The
+// rests are few to a tile: one more sum, over the tokens that the tile finds among all, 16 at a time
+// on the matrix instructions.
 template <int DT>
 struct LossWHook {
     static constexpr bool kReplace = true;

@@ -161,10 +161,10 @@ DG_16BIT(launch_adapter_split, (const AdapterArgs& a, int slices, const float* p
 int launch_adapter_turn(const TurnArgs& p, const TurnArgs& q, int adapters, hipStream_t s);
 
 // u[t][j] = scale sum_k x[t][k] m(j,k)
-int launch_adapter_shrink(const AdapterArgs& a, int dtype, hipStream_t s);
+int launch_adapter_shrink(const AdapterArgs& a, hipStream_t s);
 // out[t][k] = base[t][k] + sum_j scale u[t][j] m(j,k)
-int launch_adapter_expand(const AdapterArgs& a, int dtype, hipStream_t s);
+int launch_adapter_expand(const AdapterArgs& a, hipStream_t s);
 // out_i(j,k) = sum over the rows t of adapter i of scale u[t][j] x[t][k], laid out as m
-int launch_adapter_gradient(const AdapterArgs& a, int dtype, hipStream_t s);
+int launch_adapter_gradient(const AdapterArgs& a, hipStream_t s);
 
 }  // namespace dg

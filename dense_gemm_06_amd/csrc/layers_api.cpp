@@ -473,7 +473,7 @@ int gemm_adapters_product(const void* x, int64_t tokens, int64_t K, int64_t ldx,
     if (set->rank > 0) {
         a.us = b.us = sp.us;
         a.scale = wide ? nullptr : set->scale;
-        DG_TRY(launched(wide  ? dg::launch_adapter_shrink(a, dtype, s)
+        DG_TRY(launched(wide  ? dg::launch_adapter_shrink(a, s)
                         : few ? DG_BY_TYPE(launch_adapter_shrink_row, dtype, a, s)
                               : shrink16(a, sp, dtype, s),
                         "adapters' first product"));
@@ -497,7 +497,7 @@ int gemm_adapters_product(const void* x, int64_t tokens, int64_t K, int64_t ldx,
                    kProductWorkspace, stream));
     b.base = base;
     b.ld_base = ldb;
-    return launched(wide ? dg::launch_adapter_expand(b, dtype, s) : DG_BY_TYPE(launch_adapter_expand16, dtype, b, s),
+    return launched(wide ? dg::launch_adapter_expand(b, s) : DG_BY_TYPE(launch_adapter_expand16, dtype, b, s),
                     "adapters' second product");
 }
 
@@ -602,7 +602,7 @@ int gemm_adapters_backward(const void* grad, int64_t tokens, int64_t N, int64_t 
         a.turned = 0;
     }
     if (tokens > 0 && set->rank > 0)
-        DG_TRY(launched(wide ? dg::launch_adapter_shrink(a, dtype, s) : shrink16(a, sp, dtype, s), "adapters' v"));
+        DG_TRY(launched(wide ? dg::launch_adapter_shrink(a, s) : shrink16(a, sp, dtype, s), "adapters' v"));
     if (x_grad && tokens > 0 && K > 0) {
         with_a(a, *set, K);
         if (!wide) {
@@ -627,7 +627,7 @@ int gemm_adapters_backward(const void* grad, int64_t tokens, int64_t N, int64_t 
             a.base = base;
             a.ld_base = ldb;
             a.slices = 1;
-            DG_TRY(launched(wide ? dg::launch_adapter_expand(a, dtype, s) : DG_BY_TYPE(launch_adapter_expand16, dtype, a, s),
+            DG_TRY(launched(wide ? dg::launch_adapter_expand(a, s) : DG_BY_TYPE(launch_adapter_expand16, dtype, a, s),
                             "adapters' x_grad"));
         }
     }
@@ -645,7 +645,7 @@ int gemm_adapters_backward(const void* grad, int64_t tokens, int64_t N, int64_t 
             a.scale = nullptr;
             with_a(a, *set, K);
             a.out = a_grad;
-            DG_TRY(launched(dg::launch_adapter_gradient(a, dtype, s), "adapters' a_grad"));
+            DG_TRY(launched(dg::launch_adapter_gradient(a, s), "adapters' a_grad"));
         }
         if (N == 0) return GEMM_OK;
         a.x = grad;
@@ -654,7 +654,7 @@ int gemm_adapters_backward(const void* grad, int64_t tokens, int64_t N, int64_t 
         a.scale = set->scale;
         with_b(a, *set, N);
         a.out = b_grad;
-        return launched(dg::launch_adapter_gradient(a, dtype, s), "adapters' b_grad");
+        return launched(dg::launch_adapter_gradient(a, s), "adapters' b_grad");
     }
     dg::AdapterArgs b = a;
     a.x = x;

@@ -106,7 +106,8 @@ __global__ __launch_bounds__(256) void loss_factor(const float* grad, int tokens
     factor[1] = __uint_as_float((uint32_t)(127 - 14 + e) << 23);
 }
 
-// out = in factor[1] - apart[t] grad[t] w[target[t]] for x's gradient (w NULL: without the second term). Four columns of a row to a thread, rows over grid y.
+// out = in factor[1] - apart[t] grad[t] w[target[t]] for x's gradient (w NULL: without the second
+// term). Four columns of a row to a thread, rows over grid y.
 template <int DT>
 __global__ __launch_bounds__(256) void scaled_cast(const float* in, int64_t ldi, int rows, int cols,
                                                    const float* factor, void* out, int64_t ldo, const void* w,
