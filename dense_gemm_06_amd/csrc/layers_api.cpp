@@ -70,6 +70,26 @@ bool sizes_ok(std::initializer_list<int64_t> sizes) {
     return true;
 }
 
+struct Named {
+    const char* what;
+    int64_t value;
+};
+// What the products' kernels take: they count rows and columns in 32 bits with a tile to spare, and
+// address 256 rows of an operand from one place with 32 bits.
+int check_product(std::initializer_list<Named> sizes, std::initializer_list<Named> lds) {
+    for (const Named& n : sizes)
+        if (n.value >= (int64_t)1 << 30) {
+            set_error("%s = %lld must be below 2^30", n.what, (long long)n.value);
+            return GEMM_ERR_UNSUPPORTED;
+        }
+    for (const Named& n : lds)
+        if (n.value >= (int64_t)1 << 23) {
+            set_error("%s = %lld must be below 2^23", n.what, (long long)n.value);
+            return GEMM_ERR_UNSUPPORTED;
+        }
+    return GEMM_OK;
+}
+
 // ---------------------------------------------------------------- adapters
 int check_adapters(const gemm_adapter_set* s, int64_t N, int64_t K) {
     DG_TRY(check_pointer("set", s));
@@ -177,7 +197,6 @@ Slices slices_of(int64_t tiles, int64_t K) {
     return {std::max<int64_t>(1, ceil_div(K, k)), k};
 }
 
-
 struct AdapterSpace {
     Slices mid = {0, 0};      // of the shared product in 128 x 128 tiles
     float* base = nullptr;    // the shared product (16-bit matrices without a kernel for both)
@@ -269,13 +288,14 @@ int shrink16(const dg::AdapterArgs& a, const AdapterSpace& sp, int dtype, hipStr
 // gradient (4096 tokens, 65536 words of 4096, bf16: 7.90, 7.71 and 7.54 ms with 32, 64 and 128 MB),
 // and these still fit the last level of cache.
 constexpr int64_t kPieceBytes = (int64_t)128 << 20;
+constexpr int64_t kPieceMost = (int64_t)1 << 22;  // it is a leading dimension of a product
 
 // Columns of a piece: whole blocks of 256, as many as kPieceBytes hold, and of those as many as
 // make whole rounds of 256 x 256 tiles.
 int64_t piece_of(int64_t tokens, int64_t vocabulary, int64_t each) {
     const int64_t blocks = std::max<int64_t>(1, kPieceBytes / std::max<int64_t>(1, tokens * each) / 256);
     const int64_t tm = std::max<int64_t>(1, ceil_div(tokens, 256)), rounds = tm * blocks / dg::kCus;
-    return std::max<int64_t>(1, std::min((rounds > 0 ? rounds * dg::kCus / tm : blocks) * 256, vocabulary));
+    return std::max<int64_t>(1, std::min({(rounds > 0 ? rounds * dg::kCus / tm : blocks) * 256, vocabulary, kPieceMost}));
 }
 
 struct LossSpace {
@@ -350,7 +370,7 @@ LossSpace loss_backward_space(void* workspace, int64_t tokens, int64_t vocabular
     LossSpace s;
     Parts p{static_cast<char*>(workspace)};
     const int64_t es = elem_size(dtype);
-    s.piece = piece > 0 ? std::min(piece, std::max<int64_t>(1, vocabulary)) : piece_of(tokens, vocabulary, es);
+    s.piece = piece > 0 ? std::min({piece, std::max<int64_t>(1, vocabulary), kPieceMost}) : piece_of(tokens, vocabulary, es);
     s.lddt = (tokens + 31) / 32 * 32;
     s.factor = static_cast<float*>(p.take(8));
     s.apart = static_cast<float*>(p.take(tokens * 4));
@@ -436,6 +456,8 @@ int gemm_adapters_product(const void* x, int64_t tokens, int64_t K, int64_t ldx,
     DG_TRY(check_ld("ldw", ldw, K));
     DG_TRY(check_ld("ldy", ldy, N));
     DG_TRY(check_adapters(set, N, K));
+    DG_TRY(check_product({{"tokens", tokens}, {"K", K}, {"N", N}},
+                         {{"ldx", ldx}, {"ldw", ldw}, {"set.lda", set->lda}, {"set.ldb", set->ldb}}));
     if (tokens == 0) return GEMM_OK;
     const int64_t es = elem_size(dtype);
     const AdapterSpace sp = adapter_space(workspace, tokens, N, K, set->rank, dtype);
@@ -522,6 +544,8 @@ int gemm_adapters_backward(const void* grad, int64_t tokens, int64_t N, int64_t 
     DG_TRY(check_ld("ldw", ldw, K));
     if (x_grad) DG_TRY(check_ld("ldxg", ldxg, K));
     DG_TRY(check_adapters(set, N, K));
+    DG_TRY(check_product({{"tokens", tokens}, {"K", K}, {"N", N}},
+                         {{"ldg", ldg}, {"ldx", ldx}, {"ldw", ldw}, {"set.lda", set->lda}, {"set.ldb", set->ldb}}));
     if ((a_grad == nullptr) != (b_grad == nullptr) && set->adapters > 0 && N > 0 && K > 0) {
         set_error("a_grad and b_grad come together or are both NULL");
         return GEMM_ERR_NULL_POINTER;
@@ -691,6 +715,7 @@ int gemm_loss(const void* x, int64_t tokens, int64_t K, int64_t ldx, const void*
     DG_TRY(check_size("vocabulary", vocabulary));
     DG_TRY(check_ld("ldx", ldx, K));
     DG_TRY(check_ld("ldw", ldw, K));
+    DG_TRY(check_product({{"tokens", tokens}, {"K", K}, {"vocabulary", vocabulary}}, {{"ldx", ldx}, {"ldw", ldw}}));
     if (tokens == 0) return GEMM_OK;
     const int64_t es = elem_size(dtype);
     const LossSpace sp = loss_space(workspace, tokens, vocabulary, K, dtype);
@@ -778,6 +803,8 @@ int gemm_loss_backward(const float* grad, const void* x, int64_t tokens, int64_t
     DG_TRY(check_ld("ldw", ldw, K));
     if (x_grad) DG_TRY(check_ld("ldxg", ldxg, K));
     if (w_grad) DG_TRY(check_ld("ldwg", ldwg, K));
+    DG_TRY(check_product({{"tokens", tokens}, {"K", K}, {"vocabulary", vocabulary}},
+                         {{"ldx", ldx}, {"ldw", ldw}, {"tokens of w_grad", w_grad ? tokens + 31 : 0}}));
     if (K == 0 || (x_grad == nullptr && w_grad == nullptr)) return GEMM_OK;
     if ((tokens == 0 || x_grad == nullptr) && (vocabulary == 0 || w_grad == nullptr)) return GEMM_OK;
     const int64_t es = elem_size(dtype);

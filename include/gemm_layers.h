@@ -13,8 +13,10 @@
  *    call only). Work is enqueued on `stream`; the call returns without synchronizing,
  *    allocates nothing and can be captured into a HIP graph. Calls that share a workspace
  *    must be ordered.
- *  - Sizes are below 2^31 per dimension (GEMM_ERR_UNSUPPORTED otherwise); addresses are
- *    64 bits. Empty outputs are successful no-ops.
+ *  - Sizes are below 2^30 per dimension (2^31 for the activations), and the leading
+ *    dimensions of what enters a product below 2^23, as everywhere in this library
+ *    (GEMM_ERR_UNSUPPORTED otherwise); addresses are 64 bits. Empty outputs are successful
+ *    no-ops.
  *  - Index arrays come from the device and are not read by the host: an index out of range
  *    stands for none, and nothing outside the given arrays is read or written.
  *  - Every argument is validated before anything is enqueued. Outputs must not overlap
@@ -62,8 +64,8 @@ int64_t gemm_adapters_workspace(int64_t tokens, int64_t N, int64_t K, int64_t ra
  *     x_grad[t] = w^T grad[t] + a_i^T v[t]                  (tokens x K; NULL: not wanted)
  *     a_grad_i = sum over the rows t of adapter i of v[t] x[t]^T           (as a, contiguous)
  *     b_grad_i = sum over them of scale_i grad[t] u[t]^T                   (as b, contiguous)
- * plan is gemm_experts_dispatch's of index as tokens x 1 (top_k 1, align 1); an adapter without rows
- * gets zeros. a_grad and b_grad come together or are both NULL. Sums are fp32 in a fixed order.
+ * plan is gemm_experts_dispatch's of index as tokens x 1 (top_k 1, align 1; for up to 1024 adapters);
+ * an adapter without rows gets zeros. a_grad and b_grad come together or are both NULL. Sums are fp32 in a fixed order.
  */
 int gemm_adapters_backward(const void* grad, int64_t tokens, int64_t N, int64_t ldg, const void* x, int64_t K,
                            int64_t ldx, const float* u, const void* w, int64_t ldw, int dtype,

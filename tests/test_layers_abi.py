@@ -176,6 +176,22 @@ def test_empty_calls_need_no_device():
     assert act(T=0, codes=mat(0, 128)) == OK
 
 
+@pytest.mark.parametrize("call,kw", [(c, kw) for c, names in (
+    (forward, ("ldx", "ldw")), (backward, ("ldg", "ldx", "ldw")), (loss, ("ldx", "ldw")), (loss_backward, ("ldx", "ldw")))
+    for kw in [{n: 1 << 23} for n in names] + [{"T": 1 << 30}, {"K": 1 << 30, "ldx": 1 << 30, "ldw": 1 << 30, "ldxg": 1 << 30, "ldwg": 1 << 30, "set": adapters(lda=1 << 30)}]])
+def test_product_limits(call, kw):
+    """Operands whose rows lie too far apart for the products' 32-bit offsets, whatever form would take them."""
+    for T in (8, 100, 5000):
+        assert call(**{"T": T, "n": 1 << 60, **kw}) == UNSUPPORTED
+        assert "2^" in dg.gemm_last_error()
+
+
+def test_adapter_limits():
+    for call in (forward, backward):
+        assert call(set=adapters(lda=1 << 23)) == call(set=adapters(ldb=1 << 23)) == UNSUPPORTED
+    assert loss_backward(T=(1 << 23) - 31) == UNSUPPORTED and "w_grad" in dg.gemm_last_error()
+
+
 def test_workspaces():
     assert lib().gemm_loss_workspace(-1, 5, 5, 0) == 0 and lib().gemm_adapters_workspace(1, 1, 1, 1, 7) == 0
     small = lib().gemm_loss_backward_workspace(4096, 65536, 1024, dg.GEMM_BF16, 1, 1, 1024)
