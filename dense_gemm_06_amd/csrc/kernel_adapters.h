@@ -1,11 +1,11 @@
 // kernel_adapters.h -- low-rank adapters of fp16 and bf16 on the matrix instructions.
 //
 // The rows of a tile may belong to any adapters. Where u m^T is added to a product, 32 rows
-// are taken at a time and each adapter among them in turn: u's rows of other adapters count
-// as zeros, and what the instruction gives in their rows is dropped, so that nothing of one
-// adapter (a NaN least of all) reaches another's rows. u enters as the sum of two numbers of
-// the matrices' type, its rounding and what that leaves: off by 2^-16 (bf16) or 2^-22 of u,
-// against the single rounding of y that follows, for twice 2 T N rank operations.
+// are taken at a time and each adapter among them in turn, and what the instruction gives in the
+// other adapters' rows is dropped, so that nothing of one adapter (a NaN least of all) reaches
+// another's rows. u enters as the sum of two numbers of the matrices' type, its rounding and what
+// that leaves: off by 2^-16 (bf16) or 2^-22 of u, against the single rounding of y that follows,
+// for twice 2 T N rank operations.
 #pragma once
 #include "device_common.h"
 #include "extents.h"
@@ -279,8 +279,8 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
 }
 
 // ---------------------------------------------------------------- second product on its own
-// out = the slices' sum of base + scale u m^T, 32 rows x 64 columns to a workgroup, whose four waves share the adapters
-// among the rows and are joined in LDS in their order.
+// out = the slices' sum of base + scale u m^T, 32 rows x 64 columns to a workgroup, whose four waves
+// share the adapters among the rows and are joined in LDS in their order.
 template <int DT>
 __global__ __launch_bounds__(256) void adapter_expand16(AdapterArgs a, int tiles_n) {
     __shared__ __attribute__((aligned(16))) float sums[4][32][68];
@@ -790,7 +790,7 @@ __global__ __launch_bounds__(256) void adapter_join(AdapterArgs p, AdapterArgs q
                     __builtin_memcpy(&p, w, 16);
                     v += p;
                 } else {
-                    #pragma unroll
+#pragma unroll
                     for (int e = 0; e < 4; ++e)
                         if (e < left) v[e] += w[e];
                 }

@@ -3,8 +3,9 @@
 //
 // A workgroup of four waves has 64 rows of the tall matrix and up to 16 TT rows of the other, over
 // a range of k. Both come by direct copies, whole lines of a row at a time, into a ring of three to
-// five stages; two workgroups share a compute unit, which keeps about 100 KB in flight there. Loading fragments straight into registers instead touches 16
-// lines with every 16 lanes and reached a third of this on operands out of L2.
+// five stages; two workgroups share a compute unit, which keeps about 100 KB in flight there.
+// Loading fragments straight into registers instead touches 16 lines with every 16 lanes and
+// reached a third of this on operands out of L2.
 //
 // A row's pieces of 16 bytes lie permuted by the row's number, so that neither the copies nor
 // the fragment reads meet in a bank. Rows are 16-byte aligned and k a multiple of 8.
