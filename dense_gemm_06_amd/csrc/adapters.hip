@@ -9,6 +9,7 @@
 // each launch takes 8 to 9 us (512 tokens, 1024 x 1024, rank 12, 3 adapters, both ways: 78 us with the
 // shared products' 39; four rank numbers to a wave, read together where they are neighbours: 84).
 #include "device_common.h"
+#include "extents.h"
 #include "layers.h"
 #include "launch.h"
 
@@ -69,10 +70,9 @@ __global__ __launch_bounds__(256) void adapter_expand(AdapterArgs a) {
 // waves, eight at a time with all of their loads before the first product, and the waves' sums joined in
 // order. Indices from the device are kept inside their arrays.
 constexpr int kGradWaves = 8, kGradRank = 16;
-__global__ __launch_bounds__(64 * kGradWaves) void adapter_gradient(AdapterArgs a) {
-    __shared__ float part[kGradWaves][kGradRank][64];
+__device__ __forceinline__ void gradient_block(const AdapterArgs& a, int block, float (*part)[kGradRank][64]) {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int64_t k = (int64_t)blockIdx.x * 64 + lane;
+    const int64_t k = (int64_t)block * 64 + lane;
     const int i = (int)blockIdx.z, j0 = (int)blockIdx.y * kGradRank;
     const int64_t from = max(0, min(a.offsets[i], a.capacity));
     const int64_t to = min((int64_t)a.capacity, from + max(0, a.counts[i]));
@@ -122,6 +122,13 @@ __global__ __launch_bounds__(64 * kGradWaves) void adapter_gradient(AdapterArgs 
     }
 }
 
+// Both gradients in one launch: the first blocks along grid x are a's.
+__global__ __launch_bounds__(64 * kGradWaves) void adapter_gradient(AdapterArgs a, AdapterArgs b, int blocks) {
+    __shared__ float part[kGradWaves][kGradRank][64];
+    if ((int)blockIdx.x < blocks) gradient_block(a, (int)blockIdx.x, part);
+    else gradient_block(b, (int)blockIdx.x - blocks, part);
+}
+
 int launch_adapter_shrink(const AdapterArgs& a, hipStream_t s) {
     const dim3 grid((unsigned)(a.tokens < (1 << 20) ? a.tokens : (1 << 20)), (unsigned)((a.rank + 3) / 4));
     return launch_status(adapter_shrink, grid, dim3(256), s, a);
@@ -132,9 +139,10 @@ int launch_adapter_expand(const AdapterArgs& a, hipStream_t s) {
     return launch_status(adapter_expand, grid, dim3(256), s, a);
 }
 
-int launch_adapter_gradient(const AdapterArgs& a, hipStream_t s) {
-    const dim3 grid((unsigned)((a.cols + 63) / 64), (unsigned)((a.rank + kGradRank - 1) / kGradRank), (unsigned)a.adapters);
-    return launch_status(adapter_gradient, grid, dim3(64 * kGradWaves), s, a);
+int launch_adapter_gradient(const AdapterArgs& a, const AdapterArgs& b, hipStream_t s) {
+    const int blocks = pieces<64>(a.cols);
+    const dim3 grid((unsigned)(blocks + pieces<64>(b.cols)), (unsigned)pieces<kGradRank>(a.rank), (unsigned)a.adapters);
+    return launch_status(adapter_gradient, grid, dim3(64 * kGradWaves), s, a, b, blocks);
 }
 
 }  // namespace dg

@@ -480,9 +480,8 @@ __global__ __launch_bounds__(512) void adapter_shrink_any(AdapterArgs a, float* 
 // rank_p, zeros past the rank). a.fold: the scale is in the fp32 numbers too. A thread: eight rank
 // numbers of one token.
 template <int DT>
-__global__ __launch_bounds__(64) void adapter_shrink_finish(AdapterArgs a, int slices, const float* part, int ld) {
+__device__ __forceinline__ void adapter_split(const AdapterArgs& a, int slices, const float* part, int ld, int64_t at) {
     const int rank_p = a.rank_p;
-    const int64_t at = (int64_t)blockIdx.x * 64 + threadIdx.x;
     const int each = rank_p >> 3;
     if (at >= (int64_t)a.tokens * each) return;
     const int t = (int)(at / each), j = (int)(at - (int64_t)t * each) * 8;
@@ -522,6 +521,11 @@ __global__ __launch_bounds__(64) void adapter_shrink_finish(AdapterArgs a, int s
     uint16_t* us = a.us + (size_t)t * (size_t)(2 * rank_p) + j;
     *reinterpret_cast<u32x4*>(us) = hi;
     *reinterpret_cast<u32x4*>(us + rank_p) = lo;
+}
+
+template <int DT>
+__global__ __launch_bounds__(64) void adapter_shrink_finish(AdapterArgs a, int slices, const float* part, int ld) {
+    adapter_split<DT>(a, slices, part, ld, (int64_t)blockIdx.x * 64 + threadIdx.x);
 }
 
 // y = v + scale b_i u[t] for columns n .. n + 3 (a.m: cols x rank)
@@ -588,13 +592,22 @@ __device__ __forceinline__ void turn_tile(const TurnArgs& t, int tile, int i, ui
     }
 }
 
-// Both of an adapter's matrices in one launch: grid x the tiles of one and then of the other,
-// grid y the adapters.
-static __global__ __launch_bounds__(256) void adapter_turn(TurnArgs p, TurnArgs q) {
+// What the backward pass has to lay out before it starts, in one launch: both of an adapter's
+// matrices (grid y, grid x the tiles of one and then of the other) and, from grid y `adapters` on, the
+// forward pass's u as hi and lo.
+template <int DT>
+__global__ __launch_bounds__(256) void adapter_prepare(TurnArgs p, TurnArgs q, int adapters, AdapterArgs a,
+                                                       const float* u) {
     __shared__ __attribute__((aligned(16))) uint16_t buf[64][72];
-    const int first = p.tiles_r * p.tiles_c;
-    if ((int)blockIdx.x < first) turn_tile(p, (int)blockIdx.x, (int)blockIdx.y, buf);
-    else turn_tile(q, (int)blockIdx.x - first, (int)blockIdx.y, buf);
+    const int first = p.tiles_r * p.tiles_c, x = (int)blockIdx.x, y = (int)blockIdx.y;
+    if (y < adapters) {
+        if (x < first) turn_tile(p, x, y, buf);
+        else turn_tile(q, x - first, y, buf);
+        return;
+    }
+    const int64_t all = (int64_t)a.tokens * (a.rank_p >> 3), step = (int64_t)(gridDim.y - adapters) * gridDim.x * 256;
+    for (int64_t at = ((int64_t)(y - adapters) * gridDim.x + x) * 256 + threadIdx.x; at < all; at += step)
+        adapter_split<DT>(a, 1, u, a.rank, at);
 }
 
 // ---------------------------------------------------------------- gradients

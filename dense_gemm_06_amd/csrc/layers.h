@@ -156,15 +156,14 @@ DG_16BIT(launch_adapter_shrink16, (const AdapterArgs& a, int direct, int slices,
 DG_16BIT(launch_adapter_expand16, (const AdapterArgs& a, hipStream_t s))
 // both gradients from us: a's of v and x, b's of u and grad
 DG_16BIT(launch_adapter_gradient16, (const AdapterArgs& a, const AdapterArgs& b, int slots, hipStream_t s))
-// us (and u) from `slices` sums of rows of ld numbers
-DG_16BIT(launch_adapter_split, (const AdapterArgs& a, int slices, const float* part, int ld, hipStream_t s))
-int launch_adapter_turn(const TurnArgs& p, const TurnArgs& q, int adapters, hipStream_t s);
+// the adapters' transposes, and a.us from the forward pass's u (tokens x rank; a.tokens 0: none)
+DG_16BIT(launch_adapter_prepare, (const TurnArgs& p, const TurnArgs& q, int adapters, const AdapterArgs& a, const float* u, hipStream_t s))
 
 // u[t][j] = scale sum_k x[t][k] m(j,k)
 int launch_adapter_shrink(const AdapterArgs& a, hipStream_t s);
 // out[t][k] = base[t][k] + sum_j scale u[t][j] m(j,k)
 int launch_adapter_expand(const AdapterArgs& a, hipStream_t s);
-// out_i(j,k) = sum over the rows t of adapter i of scale u[t][j] x[t][k], laid out as m
-int launch_adapter_gradient(const AdapterArgs& a, hipStream_t s);
+// out_i(j,k) = sum over the rows t of adapter i of scale u[t][j] x[t][k], laid out as m; two at once
+int launch_adapter_gradient(const AdapterArgs& a, const AdapterArgs& b, hipStream_t s);
 
 }  // namespace dg

@@ -608,8 +608,14 @@ int gemm_adapters_backward(const void* grad, int64_t tokens, int64_t N, int64_t 
         };
         const dg::TurnArgs p = turn(set->a, set->lda, set->stride_a, set->rank, x_grad ? K : 0, sp.a_turned, sp.rank_m);
         const dg::TurnArgs q = turn(set->b, set->ldb, set->stride_b, N, set->rank, sp.b_turned, N);
+        // and u, for b's gradient
+        dg::AdapterArgs of_u = a;
+        of_u.u = nullptr;
+        of_u.us = sp.us_b;
+        of_u.scale = set->scale;
+        if (!adapters) of_u.tokens = 0;
         if (p.tiles_r * p.tiles_c + q.tiles_r * q.tiles_c > 0)
-            DG_TRY(launched(dg::launch_adapter_turn(p, q, (int)set->adapters, s), "adapters' layout"));
+            DG_TRY(launched(DG_BY_TYPE(launch_adapter_prepare, dtype, p, q, (int)set->adapters, of_u, u, s), "adapters' layout"));
     }
     // v = scale grad b
     a.x = grad;
@@ -662,41 +668,24 @@ int gemm_adapters_backward(const void* grad, int64_t tokens, int64_t N, int64_t 
     a.capacity = (int)plan->capacity;
     a.chunk = (int)sp.chunk;
     a.work = sp.sums;
-    if (wide) {
-        if (K > 0) {
-            a.x = x;
-            a.ldx = ldx;
-            a.scale = nullptr;
-            with_a(a, *set, K);
-            a.out = a_grad;
-            DG_TRY(launched(dg::launch_adapter_gradient(a, s), "adapters' a_grad"));
-        }
-        if (N == 0) return GEMM_OK;
-        a.x = grad;
-        a.ldx = ldg;
-        a.u = const_cast<float*>(u);
-        a.scale = set->scale;
-        with_b(a, *set, N);
-        a.out = b_grad;
-        return launched(dg::launch_adapter_gradient(a, s), "adapters' b_grad");
-    }
     dg::AdapterArgs b = a;
     a.x = x;
     a.ldx = ldx;
+    a.scale = nullptr;  // it is in v
     with_a(a, *set, K);
     a.out = a_grad;
     b.x = grad;
     b.ldx = ldg;
+    b.u = const_cast<float*>(u);
+    b.us = sp.us_b;
+    b.scale = wide ? set->scale : nullptr;  // us_b holds scale u
     with_b(b, *set, N);
     b.out = b_grad;
     b.work = sp.sums + sp.slots * set->rank * K;
-    b.u = nullptr;
-    b.us = sp.us_b;
-    b.scale = set->scale;
-    if (tokens > 0)
-        DG_TRY(launched(DG_BY_TYPE(launch_adapter_split, dtype, b, 1, u, (int)set->rank, s), "adapters' u"));
     if (N == 0 && K == 0) return GEMM_OK;
-    return launched(DG_BY_TYPE(launch_adapter_gradient16, dtype, a, b, (int)sp.slots, s), "adapters' gradients");
+    return launched(wide ? dg::launch_adapter_gradient(a, b, s)
+                         : DG_BY_TYPE(launch_adapter_gradient16, dtype, a, b, (int)sp.slots, s),
+                    "adapters' gradients");
 }
 
 // ---------------------------------------------------------------- loss
