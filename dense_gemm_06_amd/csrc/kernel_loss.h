@@ -385,7 +385,7 @@ struct LossWHook {
         for (int i = 0; i < SI; ++i)
 #pragma unroll
             for (int j = 0; j < SJ; ++j) {
-                asm volatile("" : "+a"(acc[i][j]));  // see full_epilogue
+                if constexpr (SI == 4) asm volatile("" : "+a"(acc[i][j]));  // see full_epilogue
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
                     const float v[4] = {acc[i][j][4 * q] * f, acc[i][j][4 * q + 1] * f, acc[i][j][4 * q + 2] * f,
@@ -413,6 +413,18 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
 template <int DT>
 __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) void loss_w_tiles(GemmArgs g, LossWHook<DT> h) {
     mfma32_sp_body<DT, 0, 8, false, false, false>(g, nullptr, h);
+}
+
+// The same in 128 x 128 tiles, of a transposed x.
+template <int DT>
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) void loss_w_mid(MidArgs g, LossWHook<DT> h) {
+    __shared__ __attribute__((aligned(1024))) MidLds lds;
+    mid_body<DT>(g, lds, h);
+}
+
+static __global__ __launch_bounds__(256) void loss_turn(TurnArgs t) {
+    __shared__ __attribute__((aligned(16))) uint16_t buf[64][72];
+    turn_tile(t, (int)blockIdx.x, 0, buf);
 }
 
 template <int DT>

@@ -76,9 +76,11 @@ constexpr int64_t kLossPartBytes = 8;
 DG_16BIT(launch_loss_skinny, (const LossProduct& p, const int64_t* target, void* part, float* picked, hipStream_t s))
 DG_16BIT(launch_loss_tiles, (const LossProduct& p, int v0, const int64_t* target, void* part, float* picked, hipStream_t s))
 DG_16BIT(launch_loss_grad_tiles, (const LossProduct& p, const LossArgs& a, hipStream_t s))
-// out (n x cols, 16 bits) = factor[1] (dt x + the targets' rests): dt n x lddt, x lddt x cols; both with
-// rows of whole, aligned 16-byte pieces, lddt a multiple of 32
-DG_16BIT(launch_loss_w, (const LossArgs& a, const void* x, int64_t ldx, int cols, int group_m, void* out, int64_t ldo, hipStream_t s))
+// out (n x cols, 16 bits) = factor[1] (dt x + the targets' rests), dt n x lddt (a multiple of 32), through
+// `copy`: x as lddt x cols or, turned, cols x lddt, with rows of whole, aligned 16-byte pieces
+DG_16BIT(launch_loss_w, (const LossArgs& a, const void* x, int64_t ldx, const void* copy, int64_t ld_copy, int turned, int cols, int group_m, void* out, int64_t ldo, hipStream_t s))
+// out (cols x ld) = x^T, zeros from column `tokens` on
+int launch_loss_turn(const void* x, int64_t ldx, int tokens, int cols, void* out, int64_t ld, hipStream_t s);
 int launch_loss_finish(const void* part, int strips, int tokens, const int64_t* target, int vocabulary,
                        const float* picked, float* loss, float* lse, hipStream_t s);
 

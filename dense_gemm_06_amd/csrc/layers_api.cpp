@@ -360,6 +360,15 @@ LossSpace loss_space(void* workspace, int64_t tokens, int64_t vocabulary, int64_
     return s;
 }
 
+// Whether w's gradient (n x K) takes 128 x 128 tiles, by the same rounds; these need x transposed, and
+// the others a copy where tokens are no multiple of 32 (d and w's gradient, bf16, wide against
+// narrow: 200 tokens, 4000 x 512: 28.2 and 22.4 us; 500, 8192 x 1024: 41.8 and 37.2; 512: 36.5 and 36.9;
+// 4000, 2000 x 512: 134 and 86).
+bool loss_w_narrow(int64_t n, int64_t K) {
+    return ceil_div(ceil_div(n, 128) * ceil_div(K, 128), dg::kCus) <
+           3 * ceil_div(ceil_div(n, 256) * ceil_div(K, 256), dg::kCus);
+}
+
 // Workspace of x_grad's product: its sum over a piece is cut into up to eight slices.
 int64_t x_product_bytes(int64_t tokens, int64_t K) {
     return std::max(kProductWorkspace, std::min<int64_t>((int64_t)128 << 20, 8 * tokens * K * 4));
@@ -836,7 +845,12 @@ int gemm_loss_backward(const float* grad, const void* x, int64_t tokens, int64_t
     if (scaled) DG_TRY(launched(dg::launch_loss_factor(grad, (int)tokens, sp.factor, s), "loss gradient's factor"));
     const void* xw = x;  // x for w_grad's product
     int64_t ldxw = ldx;
-    if (sp.xp && tokens > 0 && (tokens % 32 != 0 || !whole_pieces(x, ldx, K))) {
+    const bool narrow = loss_w_narrow(std::min(sp.piece, vocabulary), K);
+    if (sp.xp && tokens > 0 && narrow) {
+        DG_TRY(launched(dg::launch_loss_turn(x, ldx, (int)tokens, (int)K, sp.xp, sp.lddt, s), "loss gradient's copy of x"));
+        xw = sp.xp;
+        ldxw = sp.lddt;
+    } else if (sp.xp && tokens > 0 && (tokens % 32 != 0 || !whole_pieces(x, ldx, K))) {
         const dg::PackJob job{x, sp.xp, ldx, (int)tokens, (int)K, (int)sp.lddt, (int)sp.ldxp}, none_left{x, sp.xp, ldx, 0, 0, 0, 8};
         DG_TRY(launched(dg::launch_pack((int)es, job, none_left, s), "loss gradient's copy of x"));
         xw = sp.xp;
@@ -885,7 +899,8 @@ int gemm_loss_backward(const float* grad, const void* x, int64_t tokens, int64_t
         if (w_grad && n > 0) {
             char* wg = static_cast<char*>(w_grad) + (size_t)v0 * ldwg * es;
             if (sp.xp && tokens > 0) {
-                DG_TRY(launched(DG_BY_TYPE(launch_loss_w, dtype, a, xw, ldxw, (int)K, tile_group(n, K), wg, ldwg, s), "loss gradient of w"));
+                DG_TRY(launched(DG_BY_TYPE(launch_loss_w, dtype, a, x, ldx, xw, ldxw, narrow, (int)K,
+                                           tile_group(n, K, narrow ? 128 : 256), wg, ldwg, s), "loss gradient of w"));
             } else {
                 DG_TRY(product(GEMM_OP_N, n, K, tokens, sp.dt, sp.lddt, x, ldx, sp.w_acc ? (void*)sp.w_acc : wg,
                                sp.w_acc ? K : ldwg, dtype, sp.w_acc ? GEMM_F32 : dtype, 0.0f, sp.product,
