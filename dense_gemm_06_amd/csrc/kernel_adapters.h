@@ -302,16 +302,27 @@ __global__ __launch_bounds__(256) void adapter_expand16(AdapterArgs a, int tiles
         const int r = (threadIdx.x >> 4) + 16 * h, row = m0 + r;
         if (row >= a.tokens || left <= 0) continue;
         f32x4 v = {0.f, 0.f, 0.f, 0.f};
-        for (int k = 0; k < a.slices; ++k) {
-            const float* base = a.base + ((size_t)k * a.tokens + row) * (size_t)a.ld_base + c;
-            f32x4 b = {0.f, 0.f, 0.f, 0.f};
-            if (left >= 4) __builtin_memcpy(&b, base, 16);
-            else
+        const float* base = a.base + (size_t)row * (size_t)a.ld_base + c;
+        const size_t step = (size_t)a.tokens * (size_t)a.ld_base;
+        auto add = [&](auto n, int k) {  // n slices, loaded together
+            constexpr int U = decltype(n)::value;
+            f32x4 b[U];
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    if (e < left) b[e] = base[e];
-            v += b;
-        }
+            for (int e = 0; e < U; ++e) {
+                b[e] = f32x4{0.f, 0.f, 0.f, 0.f};
+                if (left >= 4) __builtin_memcpy(&b[e], base + (size_t)(k + e) * step, 16);
+                else
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                        if (q < left) b[e][q] = base[(size_t)(k + e) * step + q];
+            }
+#pragma unroll
+            for (int e = 0; e < U; ++e) v += b[e];
+        };
+        int k = 0;
+        for (; k + 8 <= a.slices; k += 8) add(std::integral_constant<int, 8>{}, k);
+        for (; k + 2 <= a.slices; k += 2) add(std::integral_constant<int, 2>{}, k);
+        if (k < a.slices) add(std::integral_constant<int, 1>{}, k);
 #pragma unroll
         for (int w = 0; w < 4; ++w) v += *reinterpret_cast<const f32x4*>(&sums[w][r][(threadIdx.x & 15) * 4]);
         const size_t at = (size_t)row * (size_t)a.ldo + c;
