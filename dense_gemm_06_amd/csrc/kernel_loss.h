@@ -131,9 +131,8 @@ struct LossSkinnyEpi {
 };
 
 // Few rows x against a stream of w, 64 words to a workgroup.
-template <int DT, int TT>
-__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) void loss_stream(StreamArgs a,
-                                                                                             LossSkinnyEpi epi) {
+template <int DT, int TT, class EPI>
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) void loss_stream(StreamArgs a, EPI epi) {
     __shared__ __attribute__((aligned(1024))) StreamLds<TT> lds;
     f32x4 acc[TT];
 #pragma unroll
@@ -273,6 +272,61 @@ struct LossGradHook {
                 if (c < n && row < lddt) __builtin_memcpy(dt + (size_t)c * (size_t)lddt + row, &v, 16);
             }
         }
+    }
+};
+
+// The same of up to 64 rows, 16 of them and four words to a lane's call.
+template <int DT>
+struct LossGradSkinnyEpi {
+    LossGradHook<DT> h;
+    __device__ __forceinline__ void operator()(int t, int c, f32x4 v) const {
+        const int left = h.n - c;
+        if (left <= 0) return;
+        int64_t at = -1;
+        float g = 0.0f, k = 0.0f;
+        if (t < h.tokens) {
+            at = h.target[t];
+            if (at >= 0 && at < h.vocabulary) {
+                g = h.factor ? h.grad[t] * h.factor[0] : h.grad[t];
+                k = -h.lse[t] * kLog2e;
+                at -= (int64_t)h.v0 + c;
+            } else {
+                at = -1;
+            }
+        }
+        const bool live = g != 0.0f;  // a NaN is live
+        uint32_t in_row[4], in_turn[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const float p = __builtin_amdgcn_exp2f(fmaf(v[e], kLog2e, k));
+            const bool here = at == e && e < left, low = here && p < 0.5f;
+            const float all = live ? (here ? p - 1.0f : p) * g : 0.0f, some = low && live ? p * g : all;
+            const uint16_t r = DT == DT_F16 ? __builtin_bit_cast(uint16_t, (_Float16)all) : f32_to_bf16_rne(all);
+            in_turn[e] = r;
+            in_row[e] = DT == DT_F16 ? __builtin_bit_cast(uint16_t, (_Float16)some) : f32_to_bf16_rne(some);
+            if (here) {
+                const float rest = all - decode<DT>(r);
+                if (h.d) h.apart[t] = low && live ? 1.0f : 0.0f;
+                if (h.dt) h.rest[t] = rest == rest ? rest : 0.0f;  // an infinite d leaves nothing
+            }
+        }
+        if (h.d && t < h.tokens) {
+            uint16_t* d = h.d + (size_t)t * (size_t)h.ldd + c;
+            const u32x2 two = {in_row[0] | (in_row[1] << 16), in_row[2] | (in_row[3] << 16)};
+            if (left >= 4) __builtin_memcpy(d, &two, 8);
+            else
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (e < left) d[e] = (uint16_t)in_row[e];
+        }
+        if (h.dt && t < h.lddt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (e < left) {
+                    uint16_t* turned = h.dt + (size_t)(c + e) * (size_t)h.lddt + t;
+                    *turned = (uint16_t)in_turn[e];
+                    if (h.tokens <= 16) turned[16] = 0;  // rows of dt are 32 long
+                }
     }
 };
 

@@ -360,6 +360,11 @@ LossSpace loss_space(void* workspace, int64_t tokens, int64_t vocabulary, int64_
     return s;
 }
 
+// Whether d comes from the stream of w, or from 128 x 128 tiles once these fill the card (backward
+// pass in bf16, tiles against stream: 1 token, 8192 x 1024: 39.4 and 31.2 us; 16, 32768 x 1024: 74 and 69;
+// 60, 8192 x 1024: 43.2 and 40.9; 60, 32768 x 2048: 116 and 120).
+bool loss_few(int64_t tokens, int64_t n) { return tokens <= 32 || (tokens <= kSkinny && ceil_div(n, 128) < dg::kCus); }
+
 // Whether w's gradient (n x K) takes 128 x 128 tiles, by the same rounds; these need x transposed, and
 // the others a copy where tokens are no multiple of 32 (d and w's gradient, bf16, wide against
 // narrow: 200 tokens, 4000 x 512: 28.2 and 22.4 us; 500, 8192 x 1024: 41.8 and 37.2; 512: 36.5 and 36.9;
@@ -872,8 +877,10 @@ int gemm_loss_backward(const float* grad, const void* x, int64_t tokens, int64_t
                                sp.product, sp.product_bytes, stream));
                 DG_TRY(launched(dg::launch_loss_grad(a, dtype, s), "loss gradient"));
             } else {
-                const LossTiles t = loss_tiles(tokens, n, whole_pieces(x, ldx, K) && whole_pieces(wp, ldw, K));
-                for (int64_t c = 0; c < n; c = t.wide > c ? t.wide : n) {  // wide tiles and then narrow ones
+                // few rows all at once; else wide tiles and then narrow ones
+                const bool few = loss_few(tokens, n);
+                const LossTiles t = few ? LossTiles{n, 0} : loss_tiles(tokens, n, whole_pieces(x, ldx, K) && whole_pieces(wp, ldw, K));
+                for (int64_t c = 0; c < n; c = t.wide > c ? t.wide : n) {
                     const bool is_wide = t.wide > c;
                     dg::LossArgs b = a;
                     b.n = (int)((is_wide ? t.wide : n) - c);
@@ -881,7 +888,7 @@ int gemm_loss_backward(const float* grad, const void* x, int64_t tokens, int64_t
                     if (b.d) b.d = static_cast<char*>(b.d) + c * es;
                     if (b.dt) b.dt = static_cast<char*>(b.dt) + c * b.lddt * es;
                     const dg::LossProduct p = loss_product(x, ldx, wp + (size_t)c * ldw * es, ldw, tokens, b.n, K, dtype,
-                                                           is_wide ? 256 : 128);
+                                                           few ? 16 : is_wide ? 256 : 128);
                     DG_TRY(launched(DG_BY_TYPE(launch_loss_grad_tiles, dtype, p, b, s), "loss gradient"));
                 }
             }

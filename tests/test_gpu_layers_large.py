@@ -179,3 +179,20 @@ def test_few_tokens_of_unaligned_rows(T, dt):
     ref, err, lse_ref, lse_err, _, _ = lu.loss(x, w, target)
     lu.check(lse, lse_ref, lse_err, "lse")
     lu.check(loss, ref, err, "loss")
+
+
+@pytest.mark.parametrize("T", [1, 15, 16, 17, 32, 33, 64])
+@pytest.mark.parametrize("V,K,dt", [(130, 72, BF16), (6150, 64, F16), (6147, 40, BF16), (33000, 16, BF16)])
+def test_loss_gradients_of_few_tokens(T, V, K, dt):
+    """Every form of d for few tokens, in one piece and in pieces whose last words are odd."""
+    g = gen(T + V)
+    x = torch.randn(T, K, generator=g, device="cuda").to(dt)
+    w = (torch.randn(V, K, generator=g, device="cuda") * 0.3).to(dt)
+    target = torch.randint(0, V, (T,), generator=g, device="cuda")
+    target[T // 2:: 5] = V - 1
+    target[1::7] = -100
+    grad = torch.rand(T, generator=g, device="cuda") - 0.5
+    lse = dg.gemm_loss_tensors(x, w, target)[1]
+    want = lu.loss_backward(grad, x, w, target, lse)
+    for piece in (0, V // 2 + 1):
+        check(dg.gemm_loss_backward_tensors(grad, x, w, target, lse, piece=piece), want, ("x_grad", "w_grad"))
