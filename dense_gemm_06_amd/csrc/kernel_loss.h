@@ -132,7 +132,7 @@ struct LossSkinnyEpi {
 
 // Few rows x against a stream of w, 64 words to a workgroup.
 template <int DT, int TT, class EPI>
-__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) void loss_stream(StreamArgs a, EPI epi) {
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 4))) void loss_stream(StreamArgs a, EPI epi) {
     __shared__ __attribute__((aligned(1024))) StreamLds<TT> lds;
     f32x4 acc[TT];
 #pragma unroll

@@ -2,8 +2,8 @@
 // once and bounds the time.
 //
 // A workgroup of four waves has 64 rows of the tall matrix and up to 16 TT rows of the other, over
-// a range of k. Both come by direct copies, whole lines of a row at a time, into a ring of three to
-// five stages; two workgroups share a compute unit, which keeps about 100 KB in flight there.
+// a range of k. Both come by direct copies, whole lines of a row at a time, into a ring of two or
+// three stages; two to four workgroups share a compute unit, which keeps about 100 KB in flight there.
 // Loading fragments straight into registers instead touches 16 lines with every 16 lanes and
 // reached a third of this on operands out of L2.
 //
@@ -23,11 +23,13 @@ struct StreamArgs {
 
 constexpr int kStreamRows = 64;
 
-// Stages of KS k: of 128, or 64 where the few rows are many; as many as let two workgroups share
-// a compute unit.
+// Stages of KS k: of 128, or 64 where the few rows are many. Workgroups side by side serve better
+// than deep rings: 16 tokens, 32768 words of 2048: 27.2 us with four stages, two workgroups to a
+// compute unit, 26.3 with two stages, four; the training step of 4096 tokens, rank 64 (64 few rows):
+// 325.8 with five stages of 64, 322.5 with two of 128, and 333.5 with three, one workgroup to a unit.
 template <int TT>
 struct StreamLds {
-    static constexpr int KS = TT <= 2 ? 128 : 64, S = TT == 1 ? 4 : TT == 4 ? 5 : 3;
+    static constexpr int KS = TT <= 4 ? 128 : 64, S = TT == 1 || TT == 4 ? 2 : 3;
     uint16_t tall[S][kStreamRows * KS];
     uint16_t few[S][TT * 16 * KS];
 };
@@ -129,7 +131,7 @@ __device__ __forceinline__ void stream_sum(f32x4 (&acc)[TT], const StreamArgs& a
 // The first `groups` workgroups: the shared product, 64 rows of w and a slice of k each, as sums to
 // part (slices x tokens x N); those after them: u (adapter_shrink_wave).
 template <int DT, int TT>
-__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) void adapter_decode(
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 4))) void adapter_decode(
     StreamArgs a, AdapterArgs u, int groups, int slices, int slice_k, float* part) {
     __shared__ __attribute__((aligned(1024))) StreamLds<TT> lds;
     const int bid = (int)blockIdx.x;
@@ -171,7 +173,7 @@ __global__ __launch_bounds__(64) void adapter_decode_finish(AdapterArgs a, int s
 // 64 tokens against each adapter among them, over a slice of k: sums to part (slices x tokens x
 // rank_p). The adapters of a tile are shared out over grid z.
 template <int DT, int TT>
-__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) void adapter_shrink_part(
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 4))) void adapter_shrink_part(
     StreamArgs a, AdapterArgs u, int slice_k, float* part) {
     __shared__ __attribute__((aligned(1024))) StreamLds<TT> lds;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
