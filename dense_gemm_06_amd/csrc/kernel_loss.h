@@ -133,7 +133,7 @@ struct LossSkinnyEpi {
 // Few rows x against a stream of w, 64 words to a workgroup.
 template <int DT, int TT, class EPI>
 __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 4))) void loss_stream(StreamArgs a, EPI epi) {
-    __shared__ __attribute__((aligned(1024))) StreamLds<TT> lds;
+    __shared__ __attribute__((aligned(1024))) StreamLds<TT, true> lds;
     f32x4 acc[TT];
 #pragma unroll
     for (int t = 0; t < TT; ++t) acc[t] = f32x4{0.f, 0.f, 0.f, 0.f};

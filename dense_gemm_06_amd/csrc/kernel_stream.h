@@ -2,8 +2,8 @@
 // once and bounds the time.
 //
 // A workgroup of four waves has 64 rows of the tall matrix and up to 16 TT rows of the other, over
-// a range of k. Both come by direct copies, whole lines of a row at a time, into a ring of two or
-// three stages; two to four workgroups share a compute unit, which keeps about 100 KB in flight there.
+// a range of k. Both come by direct copies, whole lines of a row at a time, into a ring of two to
+// five stages; two to four workgroups share a compute unit, which keeps about 100 KB in flight there.
 // Loading fragments straight into registers instead touches 16 lines with every 16 lanes and
 // reached a third of this on operands out of L2.
 //
@@ -23,13 +23,15 @@ struct StreamArgs {
 
 constexpr int kStreamRows = 64;
 
-// Stages of KS k: of 128, or 64 where the few rows are many. Workgroups side by side serve better
-// than deep rings: 16 tokens, 32768 words of 2048: 27.2 us with four stages, two workgroups to a
-// compute unit, 26.3 with two stages, four; the training step of 4096 tokens, rank 64 (64 few rows):
-// 325.8 with five stages of 64, 322.5 with two of 128, and 333.5 with three, one workgroup to a unit.
-template <int TT>
+// S stages of KS k: of 128, or 64 where the few rows are many. A large matrix out of HBM wants deep rings
+// (loss of 16 tokens, 32768 words of 2048: four stages, two workgroups to a compute unit, 62.5 us, two
+// stages, four workgroups, 66; adapters of 60 tokens, 14336 x 4096: five of 64 63.5, two of 128 66), one
+// token and the adapters' first product more workgroups or longer stages (1 token, 4096 x 4096: 23.5
+// against 25.1; training step of 4096 tokens, rank 64: 360 against 370, caches cold in each case).
+template <int TT, bool DEEP>
 struct StreamLds {
-    static constexpr int KS = TT <= 4 ? 128 : 64, S = TT == 1 || TT == 4 ? 2 : 3;
+    static constexpr int KS = TT <= 2 || (TT == 4 && !DEEP) ? 128 : 64;
+    static constexpr int S = TT == 1 ? (DEEP ? 4 : 2) : TT == 4 ? (DEEP ? 5 : 2) : 3;
     uint16_t tall[S][kStreamRows * KS];
     uint16_t few[S][TT * 16 * KS];
 };
@@ -49,10 +51,8 @@ __device__ __forceinline__ void stream_wait(int later) {
 // few rows 16 t + ..; TALL_FIRST: lane l has few row 16 t + l % 16 and tall rows 4 (l / 16) .. + 3
 // of the wave's 16, else tall row l % 16 and few rows 16 t + 4 (l / 16) .. + 3. Ends with every
 // wave past its reads.
-template <int DT, int TT, bool TALL_FIRST>
-__device__ __forceinline__ void stream_sum(f32x4 (&acc)[TT], const StreamArgs& a, StreamLds<TT>& lds, int r0, int k0,
-                                           int k1) {
-    typedef StreamLds<TT> L;
+template <int DT, int TT, bool TALL_FIRST, class L>
+__device__ __forceinline__ void stream_sum(f32x4 (&acc)[TT], const StreamArgs& a, L& lds, int r0, int k0, int k1) {
     constexpr int KS = L::KS, S = L::S, D = S - 1;
     constexpr int CH = KS / 8;               // 16-byte pieces of a stage's row
     constexpr int RC = 64 / CH;              // rows of one copy
@@ -133,7 +133,7 @@ __device__ __forceinline__ void stream_sum(f32x4 (&acc)[TT], const StreamArgs& a
 template <int DT, int TT>
 __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 4))) void adapter_decode(
     StreamArgs a, AdapterArgs u, int groups, int slices, int slice_k, float* part) {
-    __shared__ __attribute__((aligned(1024))) StreamLds<TT> lds;
+    __shared__ __attribute__((aligned(1024))) StreamLds<TT, (TT > 1)> lds;
     const int bid = (int)blockIdx.x;
     if (bid >= groups) {
         adapter_shrink_wave<DT>(u, (int64_t)(bid - groups) * 4 + (threadIdx.x >> 6));
@@ -175,7 +175,7 @@ __global__ __launch_bounds__(64) void adapter_decode_finish(AdapterArgs a, int s
 template <int DT, int TT>
 __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 4))) void adapter_shrink_part(
     StreamArgs a, AdapterArgs u, int slice_k, float* part) {
-    __shared__ __attribute__((aligned(1024))) StreamLds<TT> lds;
+    __shared__ __attribute__((aligned(1024))) StreamLds<TT, false> lds;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int r0 = (int)blockIdx.x * kStreamRows;
     int mine = r0 + lane < a.rows ? u.index[r0 + lane] : -1;  // of row r0 + lane
