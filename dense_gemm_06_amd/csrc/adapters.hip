@@ -6,8 +6,8 @@
 // The same kernels serve the backward pass with the roles of a and b exchanged, which differ
 // in the direction that lies along memory (`turned`). fp32 has no fast matrix instructions, and the
 // adapters' own work is small beside the shared product, so vector instructions do it. Bound by latency:
-// each launch takes 8 to 9 us (512 tokens, 1024 x 1024, rank 12, 3 adapters, both ways: 78 us with the
-// shared products' 39; four rank numbers to a wave, read together where they are neighbours: 84).
+// each launch takes 8 to 9 us (512 tokens, 1024 x 1024, rank 12, 3 adapters, both ways: 70 us with the
+// shared products' 39; four rank numbers to a wave, read together where they are neighbours: 6 us more).
 #include "device_common.h"
 #include "extents.h"
 #include "layers.h"
