@@ -333,7 +333,7 @@ struct LossGradSkinnyEpi {
 // w's gradient of a tile (256 words from v0 on): the product, plus for each token whose target is
 // among the words what rounding took from its d, times its row of x. A word's gradient is mostly its
 // own tokens' d, so the result comes as near as its own rounding allows (relative error 0.0024 to
-// 0.0017 in bf16; the whole backward of 4096 tokens, 65536 words, 4096 long: 7.38 to 7.57 ms). The
+// 0.0017 in bf16; the whole of 4096 tokens, 65536 words, 4096 long, both ways: 7.25 to 7.37 ms). The
 // rests are few to a tile: one more sum, over the tokens that the tile finds among all, 16 at a time
 // on the matrix instructions.
 template <int DT>
@@ -412,6 +412,7 @@ struct LossWHook {
 #pragma unroll
                     for (int j = 0; j < SJ; ++j) xs[j][k] = xr[min(n0 + 32 * j + l32, cols - 1)];
                 }
+                __builtin_amdgcn_sched_barrier(0);  // every load before the first wait
                 uint32_t r16[8];
 #pragma unroll
                 for (int k = 0; k < 8; ++k)
