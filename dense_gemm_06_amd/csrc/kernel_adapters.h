@@ -539,30 +539,43 @@ __global__ __launch_bounds__(64) void adapter_shrink_finish(AdapterArgs a, int s
     adapter_split<DT>(a, slices, part, ld, (int64_t)blockIdx.x * 64 + threadIdx.x);
 }
 
-// y = v + scale b_i u[t] for columns n .. n + 3 (a.m: cols x rank)
+// scale b_i u[t] for columns n .. n + 3 (a.m: cols x rank), i = index[t]. Sixteen rank numbers at a time, their
+// loads before the first product.
 template <int DT>
-__device__ __forceinline__ void adapter_row_add(const AdapterArgs& a, int t, int n, f32x4 v) {
-    const int i = a.index[t], left = a.cols - n;
-    if (i >= 0 && i < a.adapters) {
-        const uint16_t* m = static_cast<const uint16_t*>(a.m) + (size_t)i * (size_t)a.stride_m;
-        f32x4 d = {0.f, 0.f, 0.f, 0.f};
-        for (int j = 0; j < a.rank; j += 8) {
-            float u[8];
-            load_f8(u, a.u + (size_t)t * (size_t)a.rank + j, a.rank - j);
+__device__ __forceinline__ f32x4 adapter_row(const AdapterArgs& a, int i, int t, int n) {
+    f32x4 d = {0.f, 0.f, 0.f, 0.f};
+    if (i < 0 || i >= a.adapters) return d;
+    const int left = a.cols - n;
+    const uint16_t* m = static_cast<const uint16_t*>(a.m) + (size_t)i * (size_t)a.stride_m;
+    const float* ut = a.u + (size_t)t * (size_t)a.rank;
+    const float scale = a.scale ? a.scale[i] : 1.0f;
+    for (int j = 0; j < a.rank; j += 16) {
+        float u[2][8];
+        u32x4 p[2][4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const u32x4 p = load_frag8(m + (size_t)(n + min(e, left - 1)) * (size_t)a.ldm + j, a.rank - j);
+        for (int h = 0; h < 2; ++h) {
+            load_f8(u[h], ut + j + 8 * h, a.rank - j - 8 * h);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                p[h][e] = load_frag8(m + (size_t)(n + min(e, left - 1)) * (size_t)a.ldm + j + 8 * h, a.rank - j - 8 * h);
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
-                    d[e] = fmaf(u[2 * q], decode<DT>((uint16_t)p[q]), d[e]);
-                    d[e] = fmaf(u[2 * q + 1], decode<DT>((uint16_t)(p[q] >> 16)), d[e]);
+                    d[e] = fmaf(u[h][2 * q], decode<DT>((uint16_t)p[h][e][q]), d[e]);
+                    d[e] = fmaf(u[h][2 * q + 1], decode<DT>((uint16_t)(p[h][e][q] >> 16)), d[e]);
                 }
-            }
-        }
-        const float scale = a.scale ? a.scale[i] : 1.0f;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] = fmaf(scale, d[e], v[e]);
     }
+    return d * scale;
+}
+
+// Columns n .. n + 3 of row t of the result.
+template <int DT>
+__device__ __forceinline__ void adapter_row_store(const AdapterArgs& a, int t, int n, f32x4 v) {
+    const int left = a.cols - n;
     const size_t at = (size_t)t * (size_t)a.ldo + n;
     if (left >= 4) store_out4(a.out, DT, at, v);
     else

@@ -87,7 +87,7 @@ template <int DT>
 struct AdapterRowEpi {
     AdapterArgs a;  // m: cols x rank
     __device__ __forceinline__ void operator()(int t, int n, f32x4 v) const {
-        if (t < a.tokens && n < a.cols) adapter_row_add<DT>(a, t, n, v);
+        if (t < a.tokens && n < a.cols) adapter_row_store<DT>(a, t, n, v + adapter_row<DT>(a, a.index[t], t, n));
     }
 };
 

@@ -162,11 +162,19 @@ __global__ __launch_bounds__(64) void adapter_decode_finish(AdapterArgs a, int s
     const int t = (int)blockIdx.y, n = ((int)blockIdx.x * 64 + (int)threadIdx.x) * 4;
     if (n >= a.cols) return;
     const int ld = (a.cols + 3) & ~3;
-    f32x4 v = {0.f, 0.f, 0.f, 0.f};
+    const int i = a.index[t];
+    const float* p = part + (size_t)t * (size_t)ld + n;
+    const size_t step = (size_t)a.tokens * (size_t)ld;
+    f32x4 b[8], v = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int s = 0; s < 8; ++s) b[s] = *reinterpret_cast<const f32x4*>(p + (size_t)min(s, slices - 1) * step);
+    const f32x4 d = adapter_row<DT>(a, i, t, n);  // its loads join those in flight
+#pragma unroll
+    for (int s = 0; s < 8; ++s)
+        if (s < slices) v += b[s];
 #pragma unroll 8
-    for (int s = 0; s < slices; ++s)
-        v += *reinterpret_cast<const f32x4*>(part + ((size_t)s * a.tokens + t) * (size_t)ld + n);
-    adapter_row_add<DT>(a, t, n, v);
+    for (int s = 8; s < slices; ++s) v += *reinterpret_cast<const f32x4*>(p + (size_t)s * step);
+    adapter_row_store<DT>(a, t, n, v + d);
 }
 
 // ---------------------------------------------------------------- many tokens: u
