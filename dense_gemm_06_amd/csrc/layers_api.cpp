@@ -190,9 +190,13 @@ int tiles_form(const void* x, int64_t ldx, const void* w, int64_t ldw, int64_t c
 struct Slices {
     int64_t count, k;
 };
-Slices slices_of(int64_t tiles, int64_t K) {
-    const int64_t stages = std::max<int64_t>(1, ceil_div(K, 128));
-    const int64_t want = std::min({ceil_div(2 * dg::kCus, std::max<int64_t>(1, tiles)), stages, (int64_t)32});
+Slices slices_of(int64_t tiles, int64_t K, int64_t others = 0) {
+    const int64_t stages = std::max<int64_t>(1, ceil_div(K, 128)), most = 2 * dg::kCus;
+    int64_t want = ceil_div(most, std::max<int64_t>(1, tiles));
+    // room for `others` workgroups beside them, rather than after them (u's of 20 tokens, 4096 x 4096, 8
+    // adapters of rank 16: 25.5 to 23.2 us, of 64 tokens, 2048 x 2048: 20.0 to 16.0; 48 tokens as before)
+    if (others > 0 && want * tiles <= most && tiles <= most - others) want = (most - others) / tiles;
+    want = std::min({want, stages, (int64_t)32});
     const int64_t k = ceil_div(stages, want) * 128;
     return {std::max<int64_t>(1, ceil_div(K, k)), k};
 }
@@ -240,7 +244,7 @@ AdapterSpace adapter_space(void* workspace, int64_t tokens, int64_t N, int64_t K
     AdapterSpace s;
     Parts p{static_cast<char*>(workspace)};
     if (few_tokens(tokens, K, dtype)) {
-        s.slices = slices_of(ceil_div(N, 64), K);
+        s.slices = slices_of(ceil_div(N, 64), K, tokens > 16 ? tokens * rank_padded(rank) / 16 : 0);
         s.part = static_cast<float*>(p.take(s.slices.count * tokens * ceil_div(N, 4) * 16));
     } else {
         product_space(s, p, tokens, N, K, dtype, in_tiles(tokens, N, K, rank, dtype));
