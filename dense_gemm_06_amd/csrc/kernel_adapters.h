@@ -156,8 +156,10 @@ struct AdapterHook {
                                            char* lds2) const {
         typedef Tile16<SI, SJ, WM, WN> Tile;
         const int m0 = m - wm * Tile::HALF, n0 = n - wn * 32 * SJ;
-        add<SI, SJ, WM, WN>(acc, m0, n0, wm, wn, lds, lds2);
-        __syncthreads();
+        if (a.adapters > 0) {  // else there may be no u, and a rank of 0
+            add<SI, SJ, WM, WN>(acc, m0, n0, wm, wn, lds, lds2);
+            __syncthreads();
+        }
         const Tile tile{lds, lds2};
         const int lane = threadIdx.x & 63, l32 = lane & 31, lh = lane >> 5;
 #pragma unroll

@@ -1,0 +1,37 @@
+"""The adapters, the loss and the activations on the GPU at the edges of what their documentation
+allows: sets without adapters in every form, small and large numbers, infinities and NaN."""
+import pytest
+import torch
+
+import dense_gemm_06_amd as dg
+import layer_util as lu
+
+pytestmark = pytest.mark.gpu
+BF16, F16, F32 = torch.bfloat16, torch.float16, torch.float32
+
+
+def gen(seed):
+    return torch.Generator().manual_seed(seed)
+
+
+def normal(g, *shape, size=1.0, dt=F32):
+    return (torch.randn(*shape, generator=g) * size).to(dt).cuda()
+
+
+# ----------------------------------------------------------------------------- adapters
+@pytest.mark.parametrize("dt", [BF16, F16, F32])
+@pytest.mark.parametrize("rank", [0, 8])
+@pytest.mark.parametrize("T,N,K", [(20, 96, 64), (2049, 4096, 64), (2049, 64, 4096)])
+def test_no_adapters_in_any_form(T, N, K, rank, dt):
+    """A set without adapters, of rank 0 too, in tiles of y and of x's gradient: the shared product alone."""
+    g = gen(T + N)
+    x, w, grad = normal(g, T, K, dt=dt), normal(g, N, K, size=0.05, dt=dt), normal(g, T, N, size=0.1, dt=dt)
+    a, b = torch.zeros(0, rank, K, dtype=dt).cuda(), torch.zeros(0, N, rank, dtype=dt).cuda()
+    index = torch.randint(-1, 3, (T,), generator=g, dtype=torch.int32).cuda()
+    y, u = dg.gemm_adapters_tensors(x, w, a, b, index, None, keep=True)
+    ref, err, _, _ = lu.adapters(x, w, a, b, index, None)
+    lu.check(y, ref, err, "y")
+    assert u.shape == (T, rank) and not u.any()
+    xg, ag, bg = dg.gemm_adapters_backward_tensors(grad, x, u, w, a, b, index, None)
+    lu.check(xg, *lu.adapters_backward(grad, x, u, w, a, b, index, None)[0], "x_grad")
+    assert ag.shape == a.shape and bg.shape == b.shape
