@@ -192,7 +192,8 @@ struct Slices {
 };
 Slices slices_of(int64_t tiles, int64_t K, int64_t others = 0) {
     const int64_t stages = std::max<int64_t>(1, ceil_div(K, 128)), most = 2 * dg::kCus;
-    int64_t want = ceil_div(most, std::max<int64_t>(1, tiles));
+    tiles = std::max<int64_t>(1, tiles);  // none where the result is empty
+    int64_t want = ceil_div(most, tiles);
     // room for `others` workgroups beside them, rather than after them (u's of 20 tokens, 4096 x 4096, 8
     // adapters of rank 16: 25.5 to 23.2 us, of 64 tokens, 2048 x 2048: 20.0 to 16.0; 48 tokens as before)
     if (others > 0 && want * tiles <= most && tiles <= most - others) want = (most - others) / tiles;

@@ -35,3 +35,16 @@ def test_no_adapters_in_any_form(T, N, K, rank, dt):
     xg, ag, bg = dg.gemm_adapters_backward_tensors(grad, x, u, w, a, b, index, None)
     lu.check(xg, *lu.adapters_backward(grad, x, u, w, a, b, index, None)[0], "x_grad")
     assert ag.shape == a.shape and bg.shape == b.shape
+
+
+@pytest.mark.parametrize("dt", [BF16, F16, F32])
+@pytest.mark.parametrize("T", [1, 16, 20, 64, 70])
+def test_adapters_without_columns(T, dt):
+    """An empty y: u is written all the same."""
+    g = gen(T)
+    x, w, a, b = normal(g, T, 64, dt=dt), normal(g, 0, 64, dt=dt), normal(g, 3, 16, 64, dt=dt), normal(g, 3, 0, 16, dt=dt)
+    index = torch.randint(-1, 3, (T,), generator=g, dtype=torch.int32).cuda()
+    y, u = dg.gemm_adapters_tensors(x, w, a, b, index, None, keep=True)
+    _, _, ref, err = lu.adapters(x, w, a, b, index, None)
+    assert y.shape == (T, 0)
+    lu.check(u, ref, err, "u")
