@@ -565,11 +565,11 @@ int gemm_adapters_backward(const void* grad, int64_t tokens, int64_t N, int64_t 
     DG_TRY(check_adapters(set, N, K));
     DG_TRY(check_product({{"tokens", tokens}, {"K", K}, {"N", N}},
                          {{"ldg", ldg}, {"ldx", ldx}, {"ldw", ldw}, {"set.lda", set->lda}, {"set.ldb", set->ldb}}));
-    if ((a_grad == nullptr) != (b_grad == nullptr) && set->adapters > 0 && N > 0 && K > 0) {
+    const bool adapters = (a_grad || b_grad) && set->adapters > 0;
+    if (adapters && ((a_grad == nullptr && K > 0) || (b_grad == nullptr && N > 0))) {
         set_error("a_grad and b_grad come together or are both NULL");
         return GEMM_ERR_NULL_POINTER;
     }
-    const bool adapters = (a_grad || b_grad) && set->adapters > 0;
     const int64_t es = elem_size(dtype);
     if (adapters) {
         DG_TRY(check_plan(plan));

@@ -35,3 +35,28 @@ def test_loss_workspaces_of_empty_sizes(T, dtype):
             for want in ((0, 0), (0, 1), (1, 0), (1, 1)):
                 for piece in (0, 1, 1000):
                     assert lib().gemm_loss_backward_workspace(T, V, K, dtype, *want, piece) >= 0
+
+
+def adapters_backward(**kw):
+    v = dict(T=8, N=32, K=64, ld=64, dtype=dg.GEMM_BF16, x_grad=None, a_grad=7 * G, b_grad=8 * G, R=2, rank=16)
+    v.update(kw)
+    s = dg.gemm_adapter_set(G, 2 * G, None, v["R"], v["rank"], v["ld"], 0, v["ld"], 0)
+    plan = dg.gemm_expert_plan(3 * G, 4 * G, 5 * G, 6 * G, v["R"], v["T"], 1, v["T"])
+    return lib().gemm_adapters_backward(9 * G, v["T"], v["N"], v["ld"], 10 * G, v["K"], v["ld"], 11 * G, 12 * G, v["ld"],
+                                        v["dtype"], ctypes.byref(s), 13 * G, ctypes.byref(plan), v["x_grad"], v["ld"],
+                                        v["a_grad"], v["b_grad"], 14 * G, G, None)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_one_of_the_adapters_gradients_missing(dtype):
+    """Also beside an empty one, whose pointer may be anything."""
+    for kw in (dict(a_grad=None), dict(b_grad=None), dict(a_grad=None, N=0), dict(b_grad=None, K=0)):
+        assert adapters_backward(dtype=dtype, **kw) == NULL, kw
+        assert "come together" in dg.gemm_last_error()
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="made-up addresses")
+@pytest.mark.parametrize("dtype", TYPES)
+def test_an_empty_gradient_needs_no_pointer(dtype):
+    for kw in (dict(a_grad=None, K=0), dict(b_grad=None, N=0)):
+        assert adapters_backward(dtype=dtype, **kw) == DEVICE, kw
