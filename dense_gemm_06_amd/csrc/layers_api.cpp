@@ -115,10 +115,20 @@ int check_adapters(const gemm_adapter_set* s, int64_t N, int64_t K) {
     return GEMM_OK;
 }
 
-// Of 16-bit matrices; fp32 kernels walk their elements.
-int check_adapter_threads(int64_t tokens, int64_t cols, int64_t rank, int dtype) {
+// Threads of the first product's widest launch on 16-bit matrices (see shrink16); fp32 kernels walk their
+// tokens, as does the form for few tokens and ranks.
+bool shrink_by_rows(int64_t tokens, int64_t rank) { return tokens * rank <= 8192; }
+int check_shrink_threads(int64_t tokens, int64_t rank, int dtype, bool direct) {
+    if (dtype == GEMM_F32 || rank == 0 || shrink_by_rows(tokens, rank)) return GEMM_OK;
+    DG_TRY(check_threads("tokens * rank", tokens, ceil_div(rank, 16) * 2, 2));  // an eighth of the padded rank, or more
+    return check_threads("blocks of tokens", ceil_div(tokens, direct ? 64 : 16), 1, direct ? 256 : 512);
+}
+// And of the second's: in tiles, on its own, or with up to 64 tokens by strips of 16 columns (those of
+// 64 of the stream are no more).
+int check_expand_threads(int64_t tokens, int64_t cols, int dtype, bool tiles, bool few) {
     if (dtype == GEMM_F32) return GEMM_OK;
-    DG_TRY(check_threads("tokens * rank", tokens, ceil_div(rank, 16) * 2, 2));
+    if (few) return check_threads("blocks of columns", ceil_div(cols, 16), 1, 512);
+    if (tiles) return check_threads("tiles of tokens * columns", ceil_div(tokens, 256), ceil_div(cols, 256), 512);
     return check_threads("blocks of tokens * columns", ceil_div(tokens, 32), ceil_div(cols, 64), 256);
 }
 
@@ -280,12 +290,16 @@ AdapterSpace adapter_backward_space(void* workspace, int64_t tokens, int64_t N, 
 #define DG_BY_TYPE(name, dtype, ...) \
     ((dtype) == GEMM_F16 ? dg::name##_f16(__VA_ARGS__) : dg::name##_bf16(__VA_ARGS__))
 
+// Whether the first product's rows come by direct copies (a.m of rank x cols).
+bool shrink_direct(const dg::AdapterArgs& a) {
+    return whole_pieces(a.x, a.ldx, a.cols) && whole_pieces(a.m, a.ldm, a.cols) && a.stride_m % 8 == 0;
+}
+
 // u and us of 16-bit matrices for a.m of rank x cols.
 int shrink16(const dg::AdapterArgs& a, const AdapterSpace& sp, int dtype, hipStream_t s) {
     // each token by itself where all of them together read no more than 8192 rows of the adapters
-    if ((int64_t)a.tokens * a.rank <= 8192) return DG_BY_TYPE(launch_adapter_shrink_row, dtype, a, s);
-    const bool direct = whole_pieces(a.x, a.ldx, a.cols) && whole_pieces(a.m, a.ldm, a.cols) && a.stride_m % 8 == 0;
-    return DG_BY_TYPE(launch_adapter_shrink16, dtype, a, direct, (int)sp.slices.count, (int)sp.slices.k, sp.part, s);
+    if (shrink_by_rows(a.tokens, a.rank)) return DG_BY_TYPE(launch_adapter_shrink_row, dtype, a, s);
+    return DG_BY_TYPE(launch_adapter_shrink16, dtype, a, shrink_direct(a), (int)sp.slices.count, (int)sp.slices.k, sp.part, s);
 }
 
 // ---------------------------------------------------------------- loss
@@ -491,15 +505,16 @@ int gemm_adapters_product(const void* x, int64_t tokens, int64_t K, int64_t ldx,
                          {range("x", x, span(tokens, K, ldx, es)), range("w", w, span(N, K, ldw, es)),
                           a_range(*set, K, es), b_range(*set, N, es), scale_of(*set),
                           range("index", index, (uint64_t)tokens * 4)}));
-    DG_TRY(check_adapter_threads(tokens, N, set->rank, dtype));
-    DG_TRY(check_device());
-    const hipStream_t s = (hipStream_t)stream;
     dg::AdapterArgs a = adapter_args(*set, tokens, index);
     a.x = x;
     a.ldx = ldx;
     a.u = u;
     with_a(a, *set, K);
-    const bool wide = dtype == GEMM_F32, few = few_tokens(tokens, K, dtype);
+    const bool wide = dtype == GEMM_F32, few = few_tokens(tokens, K, dtype), tiles = in_tiles(tokens, N, K, set->rank, dtype);
+    if (!few) DG_TRY(check_shrink_threads(tokens, set->rank, dtype, shrink_direct(a)));
+    DG_TRY(check_expand_threads(tokens, N, dtype, tiles, few));
+    DG_TRY(check_device());
+    const hipStream_t s = (hipStream_t)stream;
     const int form = tiles_form(x, ldx, w, ldw, N, K, GEMM_OP_T, dtype);
     const dg::AdapterProduct p{x, w, ldx, ldw, (int)N, (int)K, GEMM_OP_T, form == 2};
     dg::AdapterArgs b = a;
@@ -521,7 +536,7 @@ int gemm_adapters_product(const void* x, int64_t tokens, int64_t K, int64_t ldx,
     }
     if (N == 0) return GEMM_OK;
     if (few) return launched(DG_BY_TYPE(launch_adapter_skinny, dtype, p, b, s), "adapters' products");
-    if (in_tiles(tokens, N, K, set->rank, dtype))
+    if (tiles)
         return launched(DG_BY_TYPE(launch_adapter_tiles, dtype, p, b, tile_group(tokens, N), s), "adapters' products");
     b.slices = 1;
     if (form == 2) {
@@ -614,29 +629,10 @@ int gemm_adapters_backward(const void* grad, int64_t tokens, int64_t N, int64_t 
          adapters ? range("plan.offsets", plan->offsets, (uint64_t)(plan->experts + 1) * 4) : none,
          adapters ? range("plan.counts", plan->counts, (uint64_t)plan->experts * 4) : none,
          adapters ? range("plan.rows", plan->rows, (uint64_t)plan->capacity * 4) : none}));
-    DG_TRY(check_threads("tokens * rank", tokens, set->rank, 64));
-    DG_TRY(check_device());
-    const hipStream_t s = (hipStream_t)stream;
-    dg::AdapterArgs a = adapter_args(*set, tokens, index);
     const bool wide = dtype == GEMM_F32, any = set->adapters > 0 && set->rank > 0;
-    if (!wide && any && (N > 0 || K > 0)) {
-        // the adapters' other layout: a as K x rank_m for x_grad, b as rank x N for v
-        auto turn = [](const void* in, int64_t ld, int64_t stride, int64_t rows, int64_t cols, void* out, int64_t out_ld) {
-            return dg::TurnArgs{in,          ld, stride, (int)rows, (int)cols, out, (int)out_ld, (int)ceil_div(out_ld, 64),
-                                (int)ceil_div(cols, 64)};
-        };
-        const dg::TurnArgs p = turn(set->a, set->lda, set->stride_a, set->rank, x_grad ? K : 0, sp.a_turned, sp.rank_m);
-        const dg::TurnArgs q = turn(set->b, set->ldb, set->stride_b, N, set->rank, sp.b_turned, N);
-        // and u, for b's gradient
-        dg::AdapterArgs of_u = a;
-        of_u.u = nullptr;
-        of_u.us = sp.us_b;
-        of_u.scale = set->scale;
-        if (!adapters) of_u.tokens = 0;
-        if (p.tiles_r * p.tiles_c + q.tiles_r * q.tiles_c > 0)
-            DG_TRY(launched(DG_BY_TYPE(launch_adapter_prepare, dtype, p, q, (int)set->adapters, of_u, u, s), "adapters' layout"));
-    }
+    const bool tiles = in_tiles(tokens, K, N, set->rank, dtype);
     // v = scale grad b
+    dg::AdapterArgs a = adapter_args(*set, tokens, index);
     a.x = grad;
     a.ldx = ldg;
     a.u = sp.v;
@@ -649,6 +645,27 @@ int gemm_adapters_backward(const void* grad, int64_t tokens, int64_t N, int64_t 
         a.ldm = N;
         a.stride_m = set->rank * N;
         a.turned = 0;
+    }
+    DG_TRY(check_shrink_threads(tokens, set->rank, dtype, shrink_direct(a)));
+    if (x_grad) DG_TRY(check_expand_threads(tokens, K, dtype, tiles, false));
+    if (any) DG_TRY(check_threads("blocks of N + K", ceil_div(N, 64) + ceil_div(K, 64), 2, 256));  // layout, gradients
+    DG_TRY(check_device());
+    const hipStream_t s = (hipStream_t)stream;
+    if (!wide && any && (N > 0 || K > 0)) {
+        // the adapters' other layout: a as K x rank_m for x_grad, b as rank x N for v
+        auto turn = [](const void* in, int64_t ld, int64_t stride, int64_t rows, int64_t cols, void* out, int64_t out_ld) {
+            return dg::TurnArgs{in,          ld, stride, (int)rows, (int)cols, out, (int)out_ld, (int)ceil_div(out_ld, 64),
+                                (int)ceil_div(cols, 64)};
+        };
+        const dg::TurnArgs p = turn(set->a, set->lda, set->stride_a, set->rank, x_grad ? K : 0, sp.a_turned, sp.rank_m);
+        const dg::TurnArgs q = turn(set->b, set->ldb, set->stride_b, N, set->rank, sp.b_turned, N);
+        // and u, for b's gradient, as hi and lo only
+        dg::AdapterArgs of_u = adapter_args(*set, tokens, index);
+        of_u.us = sp.us_b;
+        of_u.scale = set->scale;
+        if (!adapters) of_u.tokens = 0;
+        if (p.tiles_r * p.tiles_c + q.tiles_r * q.tiles_c > 0)
+            DG_TRY(launched(DG_BY_TYPE(launch_adapter_prepare, dtype, p, q, (int)set->adapters, of_u, u, s), "adapters' layout"));
     }
     if (tokens > 0 && set->rank > 0)
         DG_TRY(launched(wide ? dg::launch_adapter_shrink(a, s) : shrink16(a, sp, dtype, s), "adapters' v"));
@@ -664,7 +681,7 @@ int gemm_adapters_backward(const void* grad, int64_t tokens, int64_t N, int64_t 
         a.scale = nullptr;
         a.out = x_grad;
         a.ldo = ldxg;
-        if (in_tiles(tokens, K, N, set->rank, dtype)) {
+        if (tiles) {
             dg::AdapterProduct p{grad, w, ldg, ldw, (int)K, (int)N, GEMM_OP_N,
                                  tiles_form(grad, ldg, w, ldw, K, N, GEMM_OP_N, dtype) == 2};
             DG_TRY(launched(DG_BY_TYPE(launch_adapter_tiles, dtype, p, a, tile_group(tokens, K), s), "adapters' x_grad"));
@@ -738,7 +755,7 @@ int gemm_loss(const void* x, int64_t tokens, int64_t K, int64_t ldx, const void*
                           range("workspace", workspace, (uint64_t)workspace_bytes)},
                          {range("x", x, span(tokens, K, ldx, es)), range("w", w, span(vocabulary, K, ldw, es)),
                           range("target", target, n4 * 2)}));
-    DG_TRY(check_threads("tokens", tokens, 1, 256));
+    DG_TRY(check_threads("tokens", tokens, 1, sp.part ? 16 : 256));
     DG_TRY(check_threads("tiles of tokens * vocabulary", ceil_div(tokens, 256),
                          ceil_div(vocabulary, tokens <= kSkinny ? 16 : 256), 512));
     DG_TRY(check_device());
@@ -834,6 +851,7 @@ int gemm_loss_backward(const float* grad, const void* x, int64_t tokens, int64_t
                           range("w", w, span(vocabulary, K, ldw, es)), range("target", target, n4 * 2),
                           range("lse", lse, n4)}));
     DG_TRY(check_threads("blocks of tokens * piece", ceil_div(tokens, 64), ceil_div(sp.piece, 64), 256));
+    if (sp.xp) DG_TRY(check_threads("blocks of tokens * K", ceil_div(sp.lddt, 64), ceil_div(K, 64), 256));
     DG_TRY(check_device());
     const hipStream_t s = (hipStream_t)stream;
     // fp16 holds d times a power of two that brings the largest |grad| near 2^14

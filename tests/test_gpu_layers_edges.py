@@ -48,3 +48,21 @@ def test_adapters_without_columns(T, dt):
     _, _, ref, err = lu.adapters(x, w, a, b, index, None)
     assert y.shape == (T, 0)
     lu.check(u, ref, err, "u")
+
+
+@pytest.mark.parametrize("dt", [BF16, F16, F32])
+def test_adapters_of_a_million_tokens(dt):
+    """2^20 tokens of rank 64: what one launch with a wave to each token and rank number would not hold."""
+    T, N, K, R, rank = 2 ** 20, 8, 8, 2, 64
+    g = gen(1)
+    x, w, grad = normal(g, T, K, dt=dt), normal(g, N, K, dt=dt), normal(g, T, N, size=0.1, dt=dt)
+    a, b = normal(g, R, rank, K, size=0.3, dt=dt), normal(g, R, N, rank, size=0.3, dt=dt)
+    index = torch.randint(-1, R, (T,), generator=g, dtype=torch.int32).sort().values.cuda()
+    plan = dg.gemm_experts_dispatch_tensors(index[:, None].contiguous(), R)
+    y, u = dg.gemm_adapters_tensors(x, w, a, b, index, None, keep=True)
+    ref, err, _, _ = lu.adapters(x, w, a, b, index, None)
+    lu.check(y, ref, err, "y")
+    got = dg.gemm_adapters_backward_tensors(grad, x, u, w, a, b, index, plan)
+    for name, have, (ref, err) in zip(("x_grad", "a_grad", "b_grad"), got,
+                                      lu.adapters_backward(grad, x, u, w, a, b, index, None)):
+        lu.check(have, ref, err, name)

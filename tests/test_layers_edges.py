@@ -60,3 +60,31 @@ def test_one_of_the_adapters_gradients_missing(dtype):
 def test_an_empty_gradient_needs_no_pointer(dtype):
     for kw in (dict(a_grad=None, K=0), dict(b_grad=None, N=0)):
         assert adapters_backward(dtype=dtype, **kw) == DEVICE, kw
+
+
+def adapters_forward(**kw):
+    v = dict(T=8, N=32, K=64, ld=64, dtype=dg.GEMM_BF16, R=2, rank=16)
+    v.update(kw)
+    s = dg.gemm_adapter_set(G, 2 * G, None, v["R"], v["rank"], v["ld"], 0, v["ld"], 0)
+    return lib().gemm_adapters_product(9 * G, v["T"], v["K"], v["ld"], 12 * G, v["N"], v["ld"], v["dtype"], ctypes.byref(s),
+                                       13 * G, 10 * G, v["N"], 11 * G, 14 * G, G, None)
+
+
+def test_more_threads_than_a_launch_holds():
+    """Refused before anything is enqueued: 16 tokens to 512 threads for rows of odd lengths, 32 tokens by 64
+    columns to 256, 16 columns to 512 for few tokens."""
+    for call, kw in ((adapters_forward, dict(T=1 << 27, K=9, ld=65)), (adapters_backward, dict(T=1 << 27, N=9, ld=65, a_grad=None, b_grad=None)),
+                     (adapters_forward, dict(T=1 << 20, N=1 << 15, rank=65, ld=72)),
+                     (adapters_backward, dict(T=1 << 20, K=1 << 15, rank=65, ld=1 << 15, x_grad=15 * G)),
+                     (adapters_forward, dict(T=1, N=1 << 27, ld=65))):
+        assert call(**kw) == UNSUPPORTED, kw
+        assert "threads" in dg.gemm_last_error()
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="made-up addresses")
+@pytest.mark.parametrize("dtype", TYPES)
+def test_many_tokens_of_a_high_rank(dtype):
+    """What a launch holds is not refused: a million tokens of rank 64, and y of 2^35 elements in tiles."""
+    assert adapters_forward(T=1 << 20, rank=64, dtype=dtype) == DEVICE
+    assert adapters_backward(T=1 << 20, rank=64, dtype=dtype, x_grad=15 * G) == DEVICE
+    assert adapters_forward(T=1 << 20, N=1 << 15, rank=64, dtype=dtype) == DEVICE
