@@ -213,7 +213,7 @@ Slices slices_of(int64_t tiles, int64_t K, int64_t others = 0) {
 }
 
 struct AdapterSpace {
-    Slices mid = {0, 0};      // of the shared product in 128 x 128 tiles
+    Slices mid = {1, 0};      // of the shared product in 128 x 128 tiles
     float* base = nullptr;    // the shared product (16-bit matrices without a kernel for both)
     void* product = nullptr;
     float* part = nullptr;    // sums of slices of k
@@ -235,10 +235,11 @@ void shrink_space(AdapterSpace& s, Parts& p, int64_t tokens, int64_t len, int64_
     s.us = static_cast<uint16_t*>(p.take(tokens * rank_padded(rank) * 4));
 }
 
-void product_space(AdapterSpace& s, Parts& p, int64_t tokens, int64_t cols, int64_t len, int dtype, bool one_kernel) {
+// The shared product of a call without one kernel for both (sliced: it may come in slices of k).
+void product_space(AdapterSpace& s, Parts& p, int64_t tokens, int64_t cols, int64_t len, int dtype, bool one_kernel, bool sliced) {
     if (one_kernel) return;
     if (dtype != GEMM_F32) {
-        s.mid = slices_of(ceil_div(tokens, 128) * ceil_div(cols, 128), len);
+        if (sliced) s.mid = slices_of(ceil_div(tokens, 128) * ceil_div(cols, 128), len);
         s.base = static_cast<float*>(p.take(s.mid.count * tokens * ceil_div(cols, 4) * 16));
     }
     s.product = p.take(kProductWorkspace);
@@ -258,7 +259,7 @@ AdapterSpace adapter_space(void* workspace, int64_t tokens, int64_t N, int64_t K
         s.slices = slices_of(ceil_div(N, 64), K, tokens > 16 ? tokens * rank_padded(rank) / 16 : 0);
         s.part = static_cast<float*>(p.take(s.slices.count * tokens * ceil_div(N, 4) * 16));
     } else {
-        product_space(s, p, tokens, N, K, dtype, in_tiles(tokens, N, K, rank, dtype));
+        product_space(s, p, tokens, N, K, dtype, in_tiles(tokens, N, K, rank, dtype), true);
         if (dtype != GEMM_F32) shrink_space(s, p, tokens, K, rank);
     }
     s.bytes = p.at;
@@ -269,7 +270,7 @@ AdapterSpace adapter_backward_space(void* workspace, int64_t tokens, int64_t N, 
                                     int64_t rank, int dtype) {
     AdapterSpace s;
     Parts p{static_cast<char*>(workspace)};
-    product_space(s, p, tokens, K, N, dtype, in_tiles(tokens, K, N, rank, dtype));
+    product_space(s, p, tokens, K, N, dtype, in_tiles(tokens, K, N, rank, dtype), false);
     s.v = static_cast<float*>(p.take(tokens * rank * 4));
     if (dtype != GEMM_F32) {
         shrink_space(s, p, tokens, N, rank);

@@ -88,3 +88,12 @@ def test_many_tokens_of_a_high_rank(dtype):
     assert adapters_forward(T=1 << 20, rank=64, dtype=dtype) == DEVICE
     assert adapters_backward(T=1 << 20, rank=64, dtype=dtype, x_grad=15 * G) == DEVICE
     assert adapters_forward(T=1 << 20, N=1 << 15, rank=64, dtype=dtype) == DEVICE
+
+
+def test_workspace_of_the_adapters_backward_pass():
+    """x's gradient in fp32 once, not once for every slice of k that only the forward pass cuts."""
+    T, N, K, rank = 512, 8192, 2048, 16
+    rest = lib().gemm_adapters_backward_workspace(T, N, 0, 4, rank, dg.GEMM_BF16)  # without x's gradient and a's
+    whole = lib().gemm_adapters_backward_workspace(T, N, K, 4, rank, dg.GEMM_BF16)
+    slots = 4 + T // 64
+    assert whole - rest <= T * K * 4 + 4 * K * rank * 2 + slots * rank * K * 4 + 4096
