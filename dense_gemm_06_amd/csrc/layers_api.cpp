@@ -64,10 +64,14 @@ int product(int opB, int64_t M, int64_t N, int64_t K, const void* A, int64_t lda
                            dtype, ep, nullptr, ws, ws_bytes, stream);
 }
 
+// Sizes that the calls take (check_product, check_adapters); for others a workspace's size is 0.
 bool sizes_ok(std::initializer_list<int64_t> sizes) {
     for (int64_t n : sizes)
-        if (n < 0 || n > kMaxDim) return false;
+        if (n < 0 || n >= (int64_t)1 << 30) return false;
     return true;
+}
+bool adapters_ok(int64_t adapters, int64_t rank) {
+    return adapters >= 0 && adapters <= dg::kMaxAdapters && rank >= 0 && rank <= dg::kMaxRank;
 }
 
 struct Named {
@@ -396,7 +400,8 @@ bool loss_w_narrow(int64_t n, int64_t K) {
 
 // Workspace of x_grad's product: its sum over a piece is cut into up to eight slices.
 int64_t x_product_bytes(int64_t tokens, int64_t K) {
-    return std::max(kProductWorkspace, std::min<int64_t>((int64_t)128 << 20, 8 * tokens * K * 4));
+    const int64_t most = (int64_t)128 << 20;
+    return std::max(kProductWorkspace, tokens * K < most / 32 ? 8 * tokens * K * 4 : most);
 }
 
 LossSpace loss_backward_space(void* workspace, int64_t tokens, int64_t vocabulary, int64_t K, int dtype, bool x_grad,
@@ -474,7 +479,7 @@ extern "C" {
 
 // ---------------------------------------------------------------- adapters
 int64_t gemm_adapters_workspace(int64_t tokens, int64_t N, int64_t K, int64_t rank, int dtype) {
-    if (!sizes_ok({tokens, N, K, rank}) || !is_wide(dtype)) return 0;
+    if (!sizes_ok({tokens, N, K}) || !adapters_ok(0, rank) || !is_wide(dtype)) return 0;
     return adapter_space(nullptr, tokens, N, K, rank, dtype).bytes;
 }
 
@@ -560,7 +565,7 @@ int gemm_adapters_product(const void* x, int64_t tokens, int64_t K, int64_t ldx,
 
 int64_t gemm_adapters_backward_workspace(int64_t tokens, int64_t N, int64_t K, int64_t adapters, int64_t rank,
                                          int dtype) {
-    if (!sizes_ok({tokens, N, K, adapters, rank}) || !is_wide(dtype)) return 0;
+    if (!sizes_ok({tokens, N, K}) || !adapters_ok(adapters, rank) || !is_wide(dtype)) return 0;
     return adapter_backward_space(nullptr, tokens, N, K, adapters, rank, dtype).bytes;
 }
 
@@ -811,7 +816,7 @@ int gemm_loss(const void* x, int64_t tokens, int64_t K, int64_t ldx, const void*
 
 int64_t gemm_loss_backward_workspace(int64_t tokens, int64_t vocabulary, int64_t K, int dtype, int want_x_grad,
                                      int want_w_grad, int64_t piece) {
-    if (!sizes_ok({tokens, vocabulary, K, piece}) || !is_wide(dtype)) return 0;
+    if (!sizes_ok({tokens, vocabulary, K}) || piece < 0 || piece > kMaxDim || !is_wide(dtype)) return 0;
     return loss_backward_space(nullptr, tokens, vocabulary, K, dtype, want_x_grad != 0, want_w_grad != 0, piece).bytes;
 }
 

@@ -21,7 +21,7 @@
  *    stands for none, and nothing outside the given arrays is read or written.
  *  - Every argument is validated before anything is enqueued. Outputs must not overlap
  *    inputs, the workspace or each other. A workspace is 16-byte aligned; the call that
- *    tells its size gives the bytes that the call needs.
+ *    tells its size gives the bytes that the call needs (0 for sizes that the call refuses).
  */
 #ifndef DENSE_GEMM_06_AMD_GEMM_LAYERS_H
 #define DENSE_GEMM_06_AMD_GEMM_LAYERS_H

@@ -97,3 +97,22 @@ def test_workspace_of_the_adapters_backward_pass():
     whole = lib().gemm_adapters_backward_workspace(T, N, K, 4, rank, dg.GEMM_BF16)
     slots = 4 + T // 64
     assert whole - rest <= T * K * 4 + 4 * K * rank * 2 + slots * rank * K * 4 + 4096
+
+
+def test_workspaces_of_the_largest_sizes():
+    """No wrap at the largest sizes that the calls take, and 0 for sizes that they refuse."""
+    L = lib()
+    top, over = (1 << 30) - 1, 1 << 30
+    for dtype in TYPES:
+        ad, back = L.gemm_adapters_workspace, L.gemm_adapters_backward_workspace
+        assert ad(top, top, top, 128, dtype) > (0 if dtype == dg.GEMM_F32 else top)  # fp32: the product's alone
+        assert back(top, top, top, 32768, 128, dtype) > 128 * top
+        for T, N, K in ((over, 1, 1), (1, over, 1), (1, 1, over), (-1, 1, 1)):
+            assert ad(T, N, K, 1, dtype) == back(T, N, K, 1, 1, dtype) == 0
+            assert L.gemm_loss_workspace(T, N, K, dtype) == L.gemm_loss_backward_workspace(T, N, K, dtype, 1, 1, 0) == 0
+        assert ad(1, 1, 1, 129, dtype) == ad(1, 1, 1, 2 ** 31 - 1, dtype) == ad(1, 1, 1, -1, dtype) == 0
+        assert back(top, top, top, 2 ** 31 - 1, 2 ** 31 - 1, dtype) == back(1, 1, 1, 32769, 1, dtype) == 0
+        assert L.gemm_loss_workspace(top, top, top, dtype) > top
+        assert L.gemm_loss_backward_workspace(top, top, top, dtype, 1, 0, 0) > top
+        assert L.gemm_loss_backward_workspace(top, top, top, dtype, 1, 1, 2 ** 31 - 1) > top
+        assert L.gemm_loss_backward_workspace(1, 1, 1, dtype, 1, 1, -1) == 0
