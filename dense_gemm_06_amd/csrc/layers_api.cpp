@@ -315,11 +315,12 @@ constexpr int64_t kPieceBytes = (int64_t)128 << 20;
 constexpr int64_t kPieceMost = (int64_t)1 << 22;  // it is a leading dimension of a product
 
 // Columns of a piece: whole blocks of 256, as many as kPieceBytes hold, and of those as many as
-// make whole rounds of 256 x 256 tiles.
+// make whole rounds of 256 x 256 tiles, but one block at least.
 int64_t piece_of(int64_t tokens, int64_t vocabulary, int64_t each) {
     const int64_t blocks = std::max<int64_t>(1, kPieceBytes / std::max<int64_t>(1, tokens * each) / 256);
     const int64_t tm = std::max<int64_t>(1, ceil_div(tokens, 256)), rounds = tm * blocks / dg::kCus;
-    return std::max<int64_t>(1, std::min({(rounds > 0 ? rounds * dg::kCus / tm : blocks) * 256, vocabulary, kPieceMost}));
+    const int64_t whole = rounds > 0 ? std::max<int64_t>(1, rounds * dg::kCus / tm) : blocks;
+    return std::max<int64_t>(1, std::min({whole * 256, vocabulary, kPieceMost}));
 }
 
 struct LossSpace {

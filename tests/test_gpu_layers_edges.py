@@ -66,3 +66,20 @@ def test_adapters_of_a_million_tokens(dt):
     for name, have, (ref, err) in zip(("x_grad", "a_grad", "b_grad"), got,
                                       lu.adapters_backward(grad, x, u, w, a, b, index, None)):
         lu.check(have, ref, err, name)
+
+
+# ----------------------------------------------------------------------------- loss
+@pytest.mark.parametrize("T,dt", [(66001, F32), (131101, BF16)])
+def test_loss_of_many_tokens(T, dt):
+    """So many tokens that a piece of the vocabulary is a single block of columns."""
+    V, K = 270, 8
+    g = gen(2)
+    x, w = normal(g, T, K, dt=dt), normal(g, V, K, dt=dt)
+    target, grad = torch.randint(-9, V, (T,), generator=g).cuda(), torch.rand(T, generator=g).cuda()
+    loss, lse = dg.gemm_loss_tensors(x, w, target)
+    ref, err, lse_ref, lse_err, _, _ = lu.loss(x, w, target)
+    lu.check(lse, lse_ref, lse_err, "lse")
+    lu.check(loss, ref, err, "loss")
+    for name, have, (ref, err) in zip(("x_grad", "w_grad"), dg.gemm_loss_backward_tensors(grad, x, w, target, lse),
+                                      lu.loss_backward(grad, x, w, target, lse)):
+        lu.check(have, ref, err, name)

@@ -116,3 +116,13 @@ def test_workspaces_of_the_largest_sizes():
         assert L.gemm_loss_backward_workspace(top, top, top, dtype, 1, 0, 0) > top
         assert L.gemm_loss_backward_workspace(top, top, top, dtype, 1, 1, 2 ** 31 - 1) > top
         assert L.gemm_loss_backward_workspace(1, 1, 1, dtype, 1, 1, -1) == 0
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("T", [65537, 70000, 131073, 140000, 262145, 1000001])
+def test_pieces_of_many_tokens(T, dtype):
+    """A piece of the vocabulary has 256 columns at least, however many tokens there are."""
+    V, K, es = 50000, 8, 4 if dtype == dg.GEMM_F32 else 2
+    d = T * 256 * es
+    assert lib().gemm_loss_backward_workspace(T, V, K, dtype, 1, 0, 0) >= d
+    assert lib().gemm_loss_workspace(T, V, 4, dtype) >= T * 256 * 4  # the logits' own piece
