@@ -33,8 +33,8 @@ __device__ __forceinline__ float exp_exact(float x) {
 template <bool SLOPE>
 __device__ __forceinline__ void act_value(float v, int act, float& f, float& slope) {
     if (act == ACT_RELU) {
-        f = v > 0.0f ? v : 0.0f;
-        slope = v > 0.0f ? 1.0f : 0.0f;
+        f = v <= 0.0f ? 0.0f : v;  // a NaN stays one
+        slope = v > 0.0f ? 1.0f : f;
         return;
     }
     const bool gelu = act == ACT_GELU_TANH;

@@ -110,7 +110,8 @@ enum { GEMM_ACT_SILU = 3 };
  * gemm_activation_forward -- y = f(z) (rows x cols), or with gated y = f(z1) * z2 for z =
  * [z1 | z2] (rows x 2 cols), f one of GEMM_ACT_RELU, GEMM_ACT_GELU_TANH and GEMM_ACT_SILU in
  * fp32, and z itself as codes (NULL: not wanted), exactly gemm_block_quantize's natural
- * result with block_rows 1: what the backward pass keeps of z.
+ * result with block_rows 1: what the backward pass keeps of z. A NaN in z is one in y, relu's too
+ * (gemm_activation's gives 0).
  */
 int gemm_activation_forward(const void* z, int64_t rows, int64_t cols, int64_t ldz, int dtype, int activation,
                             int gated, void* y, int64_t ldy, const gemm_block_matrix* codes, void* stream);

@@ -83,3 +83,30 @@ def test_loss_of_many_tokens(T, dt):
     for name, have, (ref, err) in zip(("x_grad", "w_grad"), dg.gemm_loss_backward_tensors(grad, x, w, target, lse),
                                       lu.loss_backward(grad, x, w, target, lse)):
         lu.check(have, ref, err, name)
+
+
+# ----------------------------------------------------------------------------- activations
+@pytest.mark.parametrize("dt", [BF16, F16, F32])
+@pytest.mark.parametrize("kind", ["relu", "gelu_tanh", "silu"])
+@pytest.mark.parametrize("gated", [False, True])
+def test_activation_of_a_nan(gated, kind, dt):
+    """A NaN in z is one in y, and one in the codes in everything that is computed from them."""
+    F = 256
+    z = normal(gen(3), 5, 2 * F if gated else F, dt=dt)
+    plain, _ = dg.gemm_activation_tensors(z, kind, gated, torch.float8_e4m3fn)
+    z[1, 7] = float("nan")
+    y, codes = dg.gemm_activation_tensors(z, kind, gated, torch.float8_e4m3fn)
+    same = torch.ones_like(y, dtype=torch.bool)
+    same[1, 7] = False
+    assert y[1, 7].isnan() and torch.equal(y[same], plain[same])
+    held = codes.data.float()[:, :F].isnan()
+    assert held[1, 7] and not held[0].any()
+    grad = normal(gen(4), 5, F, dt=dt)
+    zg, again = dg.gemm_activation_backward_tensors(grad, codes, kind, gated)
+    assert torch.equal(again.isnan(), held) and torch.equal(zg[:, :F].isnan(), held)
+    assert torch.equal(dg.gemm_activation_value_tensors(codes, kind, gated, dt).isnan(), held)
+
+
+def test_relu_of_infinities():
+    z = torch.tensor([[float("inf"), float("-inf"), 0.0, -1.0, 2.0]]).cuda()
+    assert torch.equal(dg.gemm_activation_tensors(z, "relu")[0].cpu(), torch.tensor([[float("inf"), 0.0, 0.0, 0.0, 2.0]]))
