@@ -45,7 +45,9 @@ __device__ __forceinline__ void act_value(float v, int act, float& f, float& slo
     if (SLOPE) {
         // where e overflows s is 0, and so is the slope
         const float c = v * (fminf(e, 1e30f) * s);
-        slope = gelu ? fmaf(c * s, 1.5957691216057308f * fmaf(0.134145f * v, v, 1.0f), s) : s * (1.0f + c);
+        // past 2^40 c is 0, and v^2 must not be infinite
+        const float q = fminf(fabsf(v), 1.09951163e12f);
+        slope = gelu ? fmaf(c * s, 1.5957691216057308f * fmaf(0.134145f * q, q, 1.0f), s) : s * (1.0f + c);
     }
 }
 

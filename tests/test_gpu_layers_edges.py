@@ -110,3 +110,18 @@ def test_activation_of_a_nan(gated, kind, dt):
 def test_relu_of_infinities():
     z = torch.tensor([[float("inf"), float("-inf"), 0.0, -1.0, 2.0]]).cuda()
     assert torch.equal(dg.gemm_activation_tensors(z, "relu")[0].cpu(), torch.tensor([[float("inf"), 0.0, 0.0, 0.0, 2.0]]))
+
+
+@pytest.mark.parametrize("kind", ["relu", "gelu_tanh", "silu"])
+@pytest.mark.parametrize("dt", [BF16, F32])
+def test_slope_of_huge_values(kind, dt):
+    """Slopes of 1 and 0 far out, where squares of the values leave fp32."""
+    z = torch.tensor([[s * 2.0 ** e for s in (1, -1)] for e in (6, 12, 20, 40, 62, 64, 65, 80, 100, 120, 126)])
+    z = z.reshape(-1, 1).to(dt).cuda()  # a row, and a scale, to each
+    y, codes = dg.gemm_activation_tensors(z, kind, False, torch.float8_e5m2)
+    grad = torch.full_like(z, 3.0)
+    zg, again = dg.gemm_activation_backward_tensors(grad, codes, kind)
+    up = (z > 0).to(dt)
+    # silu and its slope at -64, the only value between: -64 e^-64 and -63 e^-64, of which e^-64 < 2^-92
+    for have, want in ((zg, 3 * up), (y, z * up), (again, z * up)):
+        assert ((have - want).abs() <= 64 * 3 * 2.0 ** -92).all() and torch.equal(have[2:], want[2:])
