@@ -5,7 +5,10 @@
 // other adapters' rows is dropped, so that nothing of one adapter (a NaN least of all) reaches
 // another's rows. u enters as the sum of two numbers of the matrices' type, its rounding and what
 // that leaves: off by 2^-16 (bf16) or 2^-22 of u, against the single rounding of y that follows,
-// for twice 2 T N rank operations.
+// for twice 2 T N rank operations. fp16 would hold a small u, or v of the backward pass, by its
+// subnormal numbers, and a large one not at all, so there each token's numbers come after a power of
+// two that brings the largest near 2^14 (what lies below it is off by 2^-39 of it at most; backward passes of
+// up to 700 tokens take 1 to 2 us longer for it, of 4096 tokens 0.7%).
 #pragma once
 #include "device_common.h"
 #include "extents.h"
@@ -46,6 +49,19 @@ __device__ __forceinline__ void split_one(float x, uint16_t& hi, uint16_t& lo) {
     rest = fabsf(rest) < INFINITY ? rest : 0.0f;
     lo = DT == DT_F16 ? __builtin_bit_cast(uint16_t, (_Float16)rest) : f32_to_bf16_rne(rest);
 }
+// The power of two by which a token's numbers are divided before fp16 holds them: the largest finite
+// magnitude, of bits `top`, comes to 2^14 .. 2^15.
+__device__ __forceinline__ float split_unit(uint32_t top) {
+    const int e = top == 0 ? 0 : max((int)(top >> 23) - 127 - 14, -100);
+    return __uint_as_float((uint32_t)(e + 127) << 23);
+}
+// The bits of a finite |x|, else 0.
+__device__ __forceinline__ uint32_t finite_bits(float x) {
+    const uint32_t b = __float_as_uint(x) & 0x7fffffffu;
+    return b < 0x7f800000u ? b : 0u;
+}
+// 1 / unit, a power of two
+__device__ __forceinline__ float over(float unit) { return __uint_as_float((254u << 23) - __float_as_uint(unit)); }
 template <int DT>
 __device__ __forceinline__ void split_hi_lo(const float (&v)[8], u32x4& hi, u32x4& lo) {
 #pragma unroll
@@ -75,6 +91,12 @@ __device__ __forceinline__ f32x4 mfma_16(u32x4 p, u32x4 q, f32x4 c) {
                                                    0, 0);
 }
 
+// sum + d unit, d being a product with us
+template <int DT>
+__device__ __forceinline__ float adapter_sum(float sum, float d, float unit) {
+    return DT == DT_F16 ? fmaf(d, unit, sum) : sum + d;
+}
+
 // acc[j] += scale u m^T for rows m0 .. m0 + 31 and columns n0 + 32 j .. + 31 (m: columns x rank).
 // Lane l holds row m0 + l % 32; register r column 8 (r / 4) + 4 (l / 32) + r % 4 of a subtile. Of
 // the adapters among the rows, every parts-th one from the part-th on.
@@ -86,6 +108,7 @@ __device__ __forceinline__ void adapter_add(f32x16 (&acc)[SJ], int m0, int n0, c
     int mine = row < a.tokens ? a.index[row] : -1;
     if (mine >= a.adapters) mine = -1;
     const uint16_t* us = a.us + (size_t)min(row, a.tokens - 1) * (size_t)(2 * a.rank_p) + 8 * lh;
+    const float unit = DT == DT_F16 && mine >= 0 ? a.unit[row] : 1.0f;
     const uint16_t* cols[SJ];
 #pragma unroll
     for (int j = 0; j < SJ; ++j)
@@ -133,7 +156,7 @@ __device__ __forceinline__ void adapter_add(f32x16 (&acc)[SJ], int m0, int n0, c
 #pragma unroll
         for (int j = 0; j < SJ; ++j)
 #pragma unroll
-            for (int e = 0; e < 16; ++e) acc[j][e] += here ? d[j][e] : 0.0f;
+            for (int e = 0; e < 16; ++e) acc[j][e] = adapter_sum<DT>(acc[j][e], here ? d[j][e] : 0.0f, unit);
     }
 }
 
@@ -186,10 +209,12 @@ struct AdapterHook {
         const int lmp = 31 - __builtin_clz(mp);
         // lanes 0-31: rows 32 b .. of the tile's first half, 32-63: of its second; the same in all waves
         int of[SI];
+        float unit[SI];  // of this wave's rows
 #pragma unroll
         for (int b = 0; b < SI; ++b) {
             const int row = m0 + lh * (32 * SI) + 32 * b + l32;
             of[b] = row < a.tokens ? a.index[row] : -1;
+            unit[b] = DT == DT_F16 ? a.unit[min(m0 + wm * (32 * SI) + 32 * b + l32, a.tokens - 1)] : 1.0f;
         }
 #pragma unroll
         for (int b = 0; b < SI; ++b) of[b] = of[b] >= a.adapters ? -1 : of[b];
@@ -268,7 +293,7 @@ struct AdapterHook {
 #pragma unroll
                 for (int j = 0; j < SJ; ++j)
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) acc[b][j][e] += here ? d[j][e] : 0.0f;
+                    for (int e = 0; e < 16; ++e) acc[b][j][e] = adapter_sum<DT>(acc[b][j][e], here ? d[j][e] : 0.0f, unit[b]);
             }
         }
     }
@@ -337,17 +362,12 @@ __global__ __launch_bounds__(256) void adapter_expand16(AdapterArgs a, int tiles
 }
 
 // ---------------------------------------------------------------- first product
-// A wave: four rank numbers of one token, 8 elements to a lane and step. For tokens few enough
-// that each can read its adapter by itself: u and, where wanted, us (see adapter_shrink_finish).
+// A wave: rank numbers j .. j + 3 of token t, whose adapter is i, 8 elements to a lane and step: lane l
+// up to 3 returns that of j + l, unscaled (zero without an adapter and past the rank).
 template <int DT>
-__device__ __forceinline__ void adapter_shrink_wave(const AdapterArgs& a, int64_t unit) {
-    const int lane = threadIdx.x & 63, each = a.rank_p >> 2;
-    if (unit >= (int64_t)a.tokens * each) return;
-    const int t = (int)(unit / each), j = (int)(unit - (int64_t)t * each) * 4;
-    if (j >= a.rank && a.us == nullptr) return;
-    const int i = a.index[t];
+__device__ __forceinline__ float adapter_shrink_four(const AdapterArgs& a, int t, int i, int j) {
+    const int lane = threadIdx.x & 63;
     float sum[4] = {0.f, 0.f, 0.f, 0.f};
-    float scale = 1.0f;
     if (i >= 0 && i < a.adapters && j < a.rank) {
         const uint16_t* x = static_cast<const uint16_t*>(a.x) + (size_t)t * (size_t)a.ldx;
         const uint16_t* m[4];
@@ -382,14 +402,26 @@ __device__ __forceinline__ void adapter_shrink_wave(const AdapterArgs& a, int64_
 #pragma unroll
             for (int r = 0; r < 4; ++r) add(p, load_frag8(m[r] + k, valid), sum[r]);
         }
-        if (a.scale) scale = a.scale[i];
     }
 #pragma unroll
     for (int r = 0; r < 4; ++r)
 #pragma unroll
         for (int d = 1; d < 64; d <<= 1) sum[r] += __shfl_xor(sum[r], d);
+    return j + lane >= a.rank ? 0.0f : lane == 0 ? sum[0] : lane == 1 ? sum[1] : lane == 2 ? sum[2] : sum[3];
+}
+
+// For tokens few enough that each can read its adapter by itself: u and, in bf16 where wanted, us (see
+// adapter_shrink_finish). A wave has four rank numbers of one token.
+template <int DT>
+__device__ __forceinline__ void adapter_shrink_wave(const AdapterArgs& a, int64_t unit) {
+    const int lane = threadIdx.x & 63, each = a.rank_p >> 2;
+    if (unit >= (int64_t)a.tokens * each) return;
+    const int t = (int)(unit / each), j = (int)(unit - (int64_t)t * each) * 4;
+    if (j >= a.rank && a.us == nullptr) return;
+    const int i = a.index[t];
+    const float scale = a.scale && i >= 0 && i < a.adapters ? a.scale[i] : 1.0f;
+    const float v = adapter_shrink_four<DT>(a, t, i, j);
     if (lane >= 4) return;
-    const float v = j + lane >= a.rank ? 0.0f : lane == 0 ? sum[0] : lane == 1 ? sum[1] : lane == 2 ? sum[2] : sum[3];
     if (j + lane < a.rank) a.u[(size_t)t * (size_t)a.rank + j + lane] = a.fold ? v * scale : v;
     if (a.us) {
         uint16_t hi, lo;
@@ -403,6 +435,35 @@ __device__ __forceinline__ void adapter_shrink_wave(const AdapterArgs& a, int64_
 template <int DT>
 __global__ __launch_bounds__(256) void adapter_shrink_row(AdapterArgs a) {
     adapter_shrink_wave<DT>(a, (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6));
+}
+
+// The same with us in fp16, whose power of two is the whole token's: a workgroup to a token.
+template <int DT>
+__global__ __launch_bounds__(1024) void adapter_shrink_token(AdapterArgs a) {
+    __shared__ float sums[kMaxRank];
+    const int t = (int)blockIdx.x, tid = threadIdx.x, lane = tid & 63;
+    const int i = a.index[t];
+    const float scale = a.scale && i >= 0 && i < a.adapters ? a.scale[i] : 1.0f;
+    for (int j = (tid >> 6) * 4; j < a.rank_p; j += (int)blockDim.x >> 4) {
+        const float v = adapter_shrink_four<DT>(a, t, i, j);
+        if (lane < 4) sums[j + lane] = v;
+    }
+    __syncthreads();
+    if (tid >= a.rank_p && tid >= 64) return;  // every wave left has whole rows of the exchange
+    uint32_t top = 0;
+    for (int j = lane; j < a.rank_p; j += 64) top = max(top, finite_bits(sums[j] * scale));
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) top = max(top, (uint32_t)__shfl_xor((int)top, d));
+    const float unit = split_unit(top);
+    if (tid == 0) a.unit[t] = unit;
+    if (tid >= a.rank_p) return;
+    const float v = sums[tid], w = v * scale;
+    if (tid < a.rank) a.u[(size_t)t * (size_t)a.rank + tid] = a.fold ? w : v;
+    uint16_t hi, lo;
+    split_one<DT>(w * over(unit), hi, lo);
+    uint16_t* us = a.us + (size_t)t * (size_t)(2 * a.rank_p) + tid;
+    us[0] = hi;
+    us[a.rank_p] = lo;
 }
 
 // The same sums as kernel_stream.h's for any alignment, fragments loaded straight from memory: 16
@@ -490,8 +551,8 @@ __global__ __launch_bounds__(512) void adapter_shrink_any(AdapterArgs a, float* 
 
 // u = the sum of the slices (rows of ld numbers), zeros in rows without an adapter, as fp32 (a.u,
 // NULL: not wanted) and, times the scale, as hi and lo of the matrices' type (a.us: tokens x 2 x
-// rank_p, zeros past the rank). a.fold: the scale is in the fp32 numbers too. A thread: eight rank
-// numbers of one token.
+// rank_p, zeros past the rank; fp16 after a.unit). a.fold: the scale is in the fp32 numbers too. A
+// thread: eight rank numbers of one token, whose threads are neighbours.
 template <int DT>
 __device__ __forceinline__ void adapter_split(const AdapterArgs& a, int slices, const float* part, int ld, int64_t at) {
     const int rank_p = a.rank_p;
@@ -528,6 +589,16 @@ __device__ __forceinline__ void adapter_split(const AdapterArgs& a, int slices, 
         v[e] = j + e < a.rank ? v[e] : 0.0f;
         w[e] = v[e] * scale;
         if (a.u && j + e < a.rank) a.u[(size_t)t * (size_t)a.rank + j + e] = a.fold ? w[e] : v[e];
+    }
+    if constexpr (DT == DT_F16) {
+        uint32_t top = 0;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) top = max(top, finite_bits(w[e]));
+        for (int d = 1; d < each; d <<= 1) top = max(top, (uint32_t)__shfl_xor((int)top, d));
+        const float unit = split_unit(top), down = over(unit);
+        if (j == 0) a.unit[t] = unit;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) w[e] *= down;
     }
     u32x4 hi, lo;
     split_hi_lo<DT>(w, hi, lo);
@@ -660,8 +731,23 @@ struct GradientLds {
     int rows[kChunkMax + 64];
 };
 
+// fp16: the powers of two that the rows of h leave out, as one for the whole chunk (the largest, in
+// `unit`) and the rest of each row, of which h is multiplied with two factors of fp16's range.
+struct GradientUnits {
+    float row[kChunkMax + 64];
+    float top[4];
+};
+__device__ __forceinline__ u32x4 scaled_f16(u32x4 h, float f) {
+    const float first = fmaxf(f, 6.103515625e-05f);  // 2^-14
+    const _Float16 p = (_Float16)first, q = (_Float16)(f * over(first));
+    f16x8 v = __builtin_bit_cast(f16x8, h);
+    v = v * p;
+    v = v * q;
+    return __builtin_bit_cast(u32x4, v);
+}
+
 template <int DT, int NT, bool TURNED>
-__device__ __forceinline__ void adapter_gradient_body(const AdapterArgs& a, GradientLds<NT>& lds) {
+__device__ __forceinline__ void adapter_gradient_body(const AdapterArgs& a, GradientLds<NT>& lds, GradientUnits* units) {
     constexpr int HC = NT * 2;               // 16-byte pieces of a row of h
     constexpr int HN = 32 * 2 * HC;          // pieces of a step: hi and lo
     constexpr int HP = (HN + 255) / 256;
@@ -683,11 +769,28 @@ __device__ __forceinline__ void adapter_gradient_body(const AdapterArgs& a, Grad
     if (from >= to) return;
     const bool alone = (sp.to - 1) / a.chunk == first;
     // the chunk's rows, -1 for padding and past its end
+    float unit = 0.0f;
     for (int e = tid; e < kChunkMax + 64; e += 256) {
         int t = from + e < to ? a.rows[from + e] : -1;
-        lds.rows[e] = t >= 0 && t < a.tokens ? t : -1;
+        t = t >= 0 && t < a.tokens ? t : -1;
+        lds.rows[e] = t;
+        if constexpr (DT == DT_F16) {
+            const float u = t >= 0 ? a.unit[t] : 0.0f;
+            units->row[e] = u;
+            unit = fmaxf(unit, u);
+        }
+    }
+    if constexpr (DT == DT_F16) {
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) unit = fmaxf(unit, __shfl_xor(unit, d));
+        if (lane == 0) units->top[wave] = unit;
     }
     __syncthreads();
+    if constexpr (DT == DT_F16) {
+        unit = fmaxf(fmaxf(units->top[0], units->top[1]), fmaxf(units->top[2], units->top[3]));
+        if (unit == 0.0f) unit = 1.0f;  // a chunk of padding
+    }
+    const float down = DT == DT_F16 ? over(unit) : 1.0f;
 
     const uint16_t* z = static_cast<const uint16_t*>(a.x);
     // the two 16-byte pieces of z that this thread moves: rows zr and zr + 16
@@ -708,7 +811,7 @@ __device__ __forceinline__ void adapter_gradient_body(const AdapterArgs& a, Grad
             s.h[q] = load_frag8(a.us + (size_t)max(th, 0) * (size_t)(2 * NT * 16) + c * 8, th < 0 ? 0 : 8);
         }
     };
-    auto put = [&](const Step& s, int b) {
+    auto put = [&](const Step& s, int b, int p0) {
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
             const int r = zr + 16 * q;
@@ -718,7 +821,9 @@ __device__ __forceinline__ void adapter_gradient_body(const AdapterArgs& a, Grad
         for (int q = 0; q < HP; ++q) {
             const int piece = q * 256 + tid, r = piece / (2 * HC), c = piece % (2 * HC);
             if (HN < 256 && piece >= HN) break;
-            *reinterpret_cast<u32x4*>(&lds.h[b][c / HC][r * (HC * 8) + (((c % HC) ^ nmaj_swz<HC>(r)) << 3)]) = s.h[q];
+            u32x4 h = s.h[q];
+            if constexpr (DT == DT_F16) h = scaled_f16(h, units->row[p0 + r] * down);
+            *reinterpret_cast<u32x4*>(&lds.h[b][c / HC][r * (HC * 8) + (((c % HC) ^ nmaj_swz<HC>(r)) << 3)]) = h;
         }
     };
     // rows 8 lg .. + 7 of column c0 + l16 of a tile of CH chunks a row
@@ -759,16 +864,16 @@ __device__ __forceinline__ void adapter_gradient_body(const AdapterArgs& a, Grad
     Step s0, s1;
     load(s0, 0);
     load(s1, 32);
-    put(s0, 0);
+    put(s0, 0, 0);
     for (int p = 0; p < n; p += 64) {
         __syncthreads();
         if (p + 64 < n) load(s0, p + 64);
         use(0);
-        put(s1, 1);
+        put(s1, 1, p + 32);
         __syncthreads();
         if (p + 64 < n) load(s1, p + 96);
         use(1);
-        if (p + 64 < n) put(s0, 0);
+        if (p + 64 < n) put(s0, 0, p + 64);
     }
     // TURNED: lane has column c + l16 and rank numbers 16 n + 4 lg .. + 3; else rank number
     // 16 n + l16 and columns c + 4 lg .. + 3
@@ -777,7 +882,7 @@ __device__ __forceinline__ void adapter_gradient_body(const AdapterArgs& a, Grad
     for (int q = 0; q < 2; ++q)
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-            const f32x4 v = acc[q][n];
+            const f32x4 v = DT == DT_F16 ? acc[q][n] * unit : acc[q][n];
             const int c = c0 + wave * 32 + 16 * q + (TURNED ? l16 : 4 * lg), j = 16 * n + (TURNED ? 4 * lg : l16);
             if (c >= a.cols || j >= a.rank) continue;
             const int left = TURNED ? a.rank - j : a.cols - c;
@@ -801,10 +906,15 @@ __device__ __forceinline__ void adapter_gradient_body(const AdapterArgs& a, Grad
 template <int DT, int NT>
 __global__ __launch_bounds__(256) void adapter_gradient16(AdapterArgs a, AdapterArgs b) {
     __shared__ __attribute__((aligned(16))) GradientLds<NT> lds;
+    GradientUnits* units = nullptr;
+    if constexpr (DT == DT_F16) {
+        __shared__ GradientUnits space;
+        units = &space;
+    }
     if (blockIdx.z == 0) {
-        if ((int64_t)blockIdx.x * kGradientCols < a.cols) adapter_gradient_body<DT, NT, false>(a, lds);
+        if ((int64_t)blockIdx.x * kGradientCols < a.cols) adapter_gradient_body<DT, NT, false>(a, lds, units);
     } else {
-        if ((int64_t)blockIdx.x * kGradientCols < b.cols) adapter_gradient_body<DT, NT, true>(b, lds);
+        if ((int64_t)blockIdx.x * kGradientCols < b.cols) adapter_gradient_body<DT, NT, true>(b, lds, units);
     }
 }
 

@@ -106,6 +106,7 @@ struct AdapterArgs {
     const float* scale;     // NULL: 1
     float* u;               // tokens x rank
     uint16_t* us;           // scale u as hi and lo (tokens x 2 x rank_p)
+    float* unit;            // fp16: the power of two of each token that us leaves out
     int rank_p;             // 16, 32, 64 or 128
     int fold;               // u holds scale u
     // expand: out = base + scale u m

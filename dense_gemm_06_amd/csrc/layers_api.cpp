@@ -223,6 +223,8 @@ struct AdapterSpace {
     float* part = nullptr;    // sums of slices of k
     uint16_t* us = nullptr;   // scale u (or v) as two 16-bit numbers
     uint16_t* us_b = nullptr; // scale u in the backward pass
+    float* unit = nullptr;    // fp16: their powers of two
+    float* unit_b = nullptr;
     float* v = nullptr;       // backward
     void* a_turned = nullptr; // adapters x K x rank_m, adapters x rank x N (16-bit matrices)
     void* b_turned = nullptr;
@@ -232,11 +234,12 @@ struct AdapterSpace {
 };
 
 // What the first product over `len` of 16-bit matrices needs, and the second's u.
-void shrink_space(AdapterSpace& s, Parts& p, int64_t tokens, int64_t len, int64_t rank) {
+void shrink_space(AdapterSpace& s, Parts& p, int64_t tokens, int64_t len, int64_t rank, int dtype) {
     // half as many as elsewhere: a tile's second adapter has a workgroup of its own, which finds room
     s.slices = slices_of(2 * ceil_div(tokens, 64), len);
     s.part = static_cast<float*>(p.take(s.slices.count * tokens * rank_padded(rank) * 4));
     s.us = static_cast<uint16_t*>(p.take(tokens * rank_padded(rank) * 4));
+    if (dtype == GEMM_F16) s.unit = static_cast<float*>(p.take(tokens * 4));
 }
 
 // The shared product of a call without one kernel for both (sliced: it may come in slices of k).
@@ -264,7 +267,7 @@ AdapterSpace adapter_space(void* workspace, int64_t tokens, int64_t N, int64_t K
         s.part = static_cast<float*>(p.take(s.slices.count * tokens * ceil_div(N, 4) * 16));
     } else {
         product_space(s, p, tokens, N, K, dtype, in_tiles(tokens, N, K, rank, dtype), true);
-        if (dtype != GEMM_F32) shrink_space(s, p, tokens, K, rank);
+        if (dtype != GEMM_F32) shrink_space(s, p, tokens, K, rank, dtype);
     }
     s.bytes = p.at;
     return s;
@@ -277,7 +280,7 @@ AdapterSpace adapter_backward_space(void* workspace, int64_t tokens, int64_t N, 
     product_space(s, p, tokens, K, N, dtype, in_tiles(tokens, K, N, rank, dtype), false);
     s.v = static_cast<float*>(p.take(tokens * rank * 4));
     if (dtype != GEMM_F32) {
-        shrink_space(s, p, tokens, N, rank);
+        shrink_space(s, p, tokens, N, rank, dtype);
         s.rank_m = ceil_div(rank, 16) * 16;
         s.a_turned = p.take(adapters * K * s.rank_m * 2);
         s.b_turned = p.take(adapters * N * rank * 2);
@@ -287,6 +290,7 @@ AdapterSpace adapter_backward_space(void* workspace, int64_t tokens, int64_t N, 
         s.slots = adapters + ceil_div(tokens, s.chunk);
         s.sums = static_cast<float*>(p.take(s.slots * rank * (N + K) * 4));
         s.us_b = static_cast<uint16_t*>(p.take(tokens * rank_padded(rank) * 4));
+        if (dtype == GEMM_F16) s.unit_b = static_cast<float*>(p.take(tokens * 4));
     }
     s.bytes = p.at;
     return s;
@@ -535,6 +539,7 @@ int gemm_adapters_product(const void* x, int64_t tokens, int64_t K, int64_t ldx,
                         "adapters' products");
     if (set->rank > 0) {
         a.us = b.us = sp.us;
+        a.unit = b.unit = sp.unit;
         a.scale = wide ? nullptr : set->scale;
         DG_TRY(launched(wide  ? dg::launch_adapter_shrink(a, s)
                         : few ? DG_BY_TYPE(launch_adapter_shrink_row, dtype, a, s)
@@ -644,6 +649,7 @@ int gemm_adapters_backward(const void* grad, int64_t tokens, int64_t N, int64_t 
     a.ldx = ldg;
     a.u = sp.v;
     a.us = sp.us;
+    a.unit = sp.unit;
     a.fold = 1;
     a.scale = set->scale;
     with_b(a, *set, N);
@@ -669,6 +675,7 @@ int gemm_adapters_backward(const void* grad, int64_t tokens, int64_t N, int64_t 
         // and u, for b's gradient, as hi and lo only
         dg::AdapterArgs of_u = adapter_args(*set, tokens, index);
         of_u.us = sp.us_b;
+        of_u.unit = sp.unit_b;
         of_u.scale = set->scale;
         if (!adapters) of_u.tokens = 0;
         if (p.tiles_r * p.tiles_c + q.tiles_r * q.tiles_c > 0)
@@ -721,6 +728,7 @@ int gemm_adapters_backward(const void* grad, int64_t tokens, int64_t N, int64_t 
     b.ldx = ldg;
     b.u = const_cast<float*>(u);
     b.us = sp.us_b;
+    b.unit = sp.unit_b;
     b.scale = wide ? set->scale : nullptr;  // us_b holds scale u
     with_b(b, *set, N);
     b.out = b_grad;

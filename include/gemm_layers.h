@@ -51,7 +51,7 @@ typedef struct gemm_adapter_set {
  * gemm_adapters_product -- y (tokens x N) and u (tokens x rank, contiguous, fp32; zeros in
  * rows without an adapter), which the backward pass takes. Products are summed in fp32;
  * u enters the second product in fp32, or with 16-bit matrices as the sum of two numbers of
- * their type (so fp16's range, 65504, holds for scale * u).
+ * their type (fp16 after a power of two for each row, so that any size of scale * u will do).
  */
 int gemm_adapters_product(const void* x, int64_t tokens, int64_t K, int64_t ldx, const void* w, int64_t N, int64_t ldw,
                           int dtype, const gemm_adapter_set* set, const int32_t* index, void* y, int64_t ldy, float* u,
@@ -65,7 +65,7 @@ int64_t gemm_adapters_workspace(int64_t tokens, int64_t N, int64_t K, int64_t ra
  *     a_grad_i = sum over the rows t of adapter i of v[t] x[t]^T           (as a, contiguous)
  *     b_grad_i = sum over them of scale_i grad[t] u[t]^T                   (as b, contiguous)
  * plan is gemm_experts_dispatch's of index as tokens x 1 (top_k 1, align 1; for up to 1024 adapters);
- * an adapter without rows gets zeros. a_grad and b_grad come together or are both NULL (an empty one
+ * v enters its products as u does. An adapter without rows gets zeros. a_grad and b_grad come together or are both NULL (an empty one
  * may be). Sums are fp32 in a fixed order.
  */
 int gemm_adapters_backward(const void* grad, int64_t tokens, int64_t N, int64_t ldg, const void* x, int64_t K,

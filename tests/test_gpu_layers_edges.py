@@ -68,6 +68,48 @@ def test_adapters_of_a_million_tokens(dt):
         lu.check(have, ref, err, name)
 
 
+def kept_to(of):
+    """How far a number v held as two fp16 numbers after a power of two may be off: 2^-22 of itself and half of
+    fp16's smallest step, 2^-25, of a unit that brings the largest number that shares it to 2^14 .. 2^15 (`of` gives
+    that number for each v): 2^-39 of it. Numbers brought to a common unit afterwards round hi and lo twice more."""
+    return lambda v, dt: v.abs() * 2.0 ** -21 + of(v.abs()) * 2.0 ** -37
+
+
+ROW = kept_to(lambda v: v.amax(1, keepdim=True))   # a token's own unit
+ALL = kept_to(lambda v: v.amax())                  # one unit for an adapter's tokens
+
+
+@pytest.mark.parametrize("T,N,K,R,rank", [(1, 256, 256, 2, 16), (20, 256, 264, 3, 3), (100, 256, 264, 3, 16),
+                                          (100, 256, 264, 2, 40), (70, 256, 256, 2, 100), (700, 256, 256, 3, 16),
+                                          (700, 251, 203, 3, 33), (700, 256, 256, 2, 128), (2100, 4096, 64, 3, 24),
+                                          (2100, 64, 4096, 3, 64)])
+@pytest.mark.parametrize("x,a,b,g", [(1.0, 0.06, 1e-4, 1e-3), (1.0, 0.06, 1e-4, 2.0 ** -12), (1e-3, 1e-5, 100.0, 100.0),
+                                     (100.0, 50.0, 1e-5, 1e-4)])
+@pytest.mark.parametrize("mixed", [False, True])
+def test_adapters_of_small_and_large_numbers_in_fp16(x, a, b, g, T, N, K, R, rank, mixed, monkeypatch):
+    """u and v far outside of what fp16 holds, and tokens of very different sizes side by side, keep their digits."""
+    r = gen(T + rank)
+    size = 2.0 ** -torch.randint(0, 12, (T, 1), generator=r).float() if mixed else torch.ones(T, 1)
+    X = (torch.randn(T, K, generator=r) * x * size).half().cuda()
+    G = (torch.randn(T, N, generator=r) * g * size.flip(0)).half().cuda()
+    W, A, B = normal(r, N, K, size=0.05, dt=F16), normal(r, R, rank, K, size=a, dt=F16), normal(r, R, N, rank, size=b, dt=F16)
+    scale = torch.rand(R, generator=r).cuda() + 0.5
+    index = torch.randint(-1, R, (T,), generator=r, dtype=torch.int32)
+    index = (index.sort().values if T > 1000 else index).cuda()
+    y, u = dg.gemm_adapters_tensors(X, W, A, B, index, scale, keep=True)
+    monkeypatch.setattr(lu, "kept_as", ROW)
+    ref, err, u_ref, u_err = lu.adapters(X, W, A, B, index, scale)
+    lu.check(u, u_ref, u_err, "u")
+    lu.check(y, ref, err, "y")
+    plan = dg.gemm_experts_dispatch_tensors(index[:, None].contiguous(), R)
+    xg, ag, bg = dg.gemm_adapters_backward_tensors(G, X, u, W, A, B, index, plan, scale)
+    lu.check(xg, *lu.adapters_backward(G, X, u, W, A, B, index, scale)[0], "x_grad")
+    monkeypatch.setattr(lu, "kept_as", ALL)
+    _, wa, wb = lu.adapters_backward(G, X, u, W, A, B, index, scale)
+    lu.check(ag, *wa, "a_grad")
+    lu.check(bg, *wb, "b_grad")
+
+
 # ----------------------------------------------------------------------------- loss
 @pytest.mark.parametrize("T,dt", [(66001, F32), (131101, BF16)])
 def test_loss_of_many_tokens(T, dt):
