@@ -74,6 +74,25 @@ __device__ __forceinline__ void split_hi_lo(const float (&v)[8], u32x4& hi, u32x
     }
 }
 
+// The other operand's infinities meet hi alone, since lo is 0 or may have the other sign: lo's product
+// takes them as zeros.
+// Not 0 where one of the eight is infinite or NaN.
+template <int DT>
+__device__ __forceinline__ uint32_t has_special(u32x4 p) {
+    const uint32_t up = DT == DT_F16 ? 0x04000400u : 0x00800080u;  // a full exponent carries into the sign's place
+    uint32_t r = 0;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) r |= (p[e] & 0x7fff7fffu) + up;
+    return r & 0x80008000u;
+}
+template <int DT>
+__device__ __forceinline__ u32x4 without_special(u32x4 p) {
+    const uint32_t up = DT == DT_F16 ? 0x04000400u : 0x00800080u;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) p[e] &= ~(((((p[e] & 0x7fff7fffu) + up) >> 15) & 0x00010001u) * 0xffffu);
+    return p;
+}
+
 template <int DT>
 __device__ __forceinline__ f32x16 mfma_32(u32x4 p, u32x4 q, f32x16 c) {
     if (DT == DT_F16)
@@ -134,13 +153,23 @@ __device__ __forceinline__ void adapter_add(f32x16 (&acc)[SJ], int m0, int n0, c
 #pragma unroll
                 for (int j = 0; j < SJ; ++j) __builtin_memcpy(&p[h][j], cols[j] + at + r + 16 * h, 16);
             }
+            uint32_t special = 0;
 #pragma unroll
             for (int h = 0; h < 2; ++h)
 #pragma unroll
                 for (int j = 0; j < SJ; ++j) {
                     d[j] = mfma_32<DT>(p[h][j], hi[h], d[j]);
-                    d[j] = mfma_32<DT>(p[h][j], lo[h], d[j]);
+                    special |= has_special<DT>(p[h][j]);
                 }
+            if (__any(special != 0))
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int j = 0; j < SJ; ++j) p[h][j] = without_special<DT>(p[h][j]);
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int j = 0; j < SJ; ++j) d[j] = mfma_32<DT>(p[h][j], lo[h], d[j]);
         }
         for (; r < a.rank; r += 16) {
             u32x4 hi, lo;
@@ -150,7 +179,7 @@ __device__ __forceinline__ void adapter_add(f32x16 (&acc)[SJ], int m0, int n0, c
             for (int j = 0; j < SJ; ++j) {
                 const u32x4 p = load_frag8(cols[j] + at + r, a.rank_m - r - 8 * lh);
                 d[j] = mfma_32<DT>(p, hi, d[j]);
-                d[j] = mfma_32<DT>(p, lo, d[j]);
+                d[j] = mfma_32<DT>(without_special<DT>(p), lo, d[j]);
             }
         }
 #pragma unroll
@@ -218,9 +247,10 @@ struct AdapterHook {
         }
 #pragma unroll
         for (int b = 0; b < SI; ++b) of[b] = of[b] >= a.adapters ? -1 : of[b];
-        // n pieces, four loads of a thread in flight
+        // n pieces, four loads of a thread in flight; whether this thread's hold infinities
         auto bring = [&](int n, auto load, char* to, int lp) {
             const int pieces = 1 << lp;
+            uint32_t special = 0;
             for (int e = tid; e < n; e += 4 * THREADS) {
                 u32x4 v[4];
 #pragma unroll
@@ -232,8 +262,10 @@ struct AdapterHook {
                 for (int k = 0; k < 4; ++k) {
                     const int at = e + k * THREADS, r = at >> lp, c = at & (pieces - 1);
                     if (at < n) *reinterpret_cast<u32x4*>(to + (size_t)(r * pieces + (c ^ rank_swz(r, pieces))) * 16) = v[k];
+                    special |= has_special<DT>(v[k]);
                 }
             }
+            return special;
         };
         bring(
             ROWS * up,
@@ -246,6 +278,8 @@ struct AdapterHook {
         // two adapters stay in LDS (2 x 32 KB at rank 64): a tile in which one request ends and the
         // next begins brings each once
         int staged[2] = {-1, -1}, next = 0;
+        uint32_t infinite[2] = {0, 0};               // of each place
+        __shared__ uint32_t special[2][WM * WN];     // and wave
 #pragma unroll
         for (int b = 0; b < SI; ++b) {
             uint64_t todo = __ballot(of[b] >= 0);
@@ -259,18 +293,24 @@ struct AdapterHook {
                     next ^= 1;
                     __syncthreads();  // the last reads of that place are done
                     const uint16_t* m = static_cast<const uint16_t*>(a.m) + (size_t)i * (size_t)a.stride_m;
-                    bring(
+                    const bool any = __any(bring(
                         COLS * mp,
                         [&](int r, int c) {
                             return load_frag8(m + (size_t)min(n0 + r, a.cols - 1) * (size_t)a.ldm + 8 * c,
                                               a.rank_m - 8 * c);
                         },
-                        m_lds + at * 32768, lmp);
+                        m_lds + at * 32768, lmp) != 0);
+                    if (lane == 0) special[at][wm * WN + wn] = any;
                     __syncthreads();
-                    if (at == 0) staged[0] = i;
-                    else staged[1] = i;
+                    uint32_t all = 0;
+#pragma unroll
+                    for (int w = 0; w < WM * WN; ++w) all |= special[at][w];
+                    all = __builtin_amdgcn_readfirstlane(all);
+                    if (at == 0) staged[0] = i, infinite[0] = all;
+                    else staged[1] = i, infinite[1] = all;
                 }
                 const char* m_at = m_lds + at * 32768;
+                const bool clear = (at == 0 ? infinite[0] : infinite[1]) != 0;
                 const uint32_t own = (uint32_t)(wm == 0 ? rows : rows >> 32);
                 const bool here = (own >> l32) & 1;
                 const int ur = wm * 32 * SI + 32 * b + l32, us = rank_swz(ur, up);
@@ -278,18 +318,22 @@ struct AdapterHook {
                 f32x16 d[SJ];
 #pragma unroll
                 for (int j = 0; j < SJ; ++j) d[j] = f32x16{};
-                for (int c = own != 0 ? lh : mp; c < mp; c += 2) {
-                    const u32x4 hi = *reinterpret_cast<const u32x4*>(u_row + ((c ^ us) << 4));
-                    const u32x4 lo = *reinterpret_cast<const u32x4*>(u_row + (((mp + c) ^ us) << 4));
-#pragma unroll
-                    for (int j = 0; j < SJ; ++j) {
-                        const int mr = wn * 32 * SJ + 32 * j + l32;
-                        const u32x4 p =
-                            *reinterpret_cast<const u32x4*>(m_at + (size_t)(mr * mp + (c ^ rank_swz(mr, mp))) * 16);
-                        d[j] = mfma_32<DT>(p, hi, d[j]);
-                        d[j] = mfma_32<DT>(p, lo, d[j]);
+                auto products = [&](auto special_tag) {
+                    for (int c = own != 0 ? lh : mp; c < mp; c += 2) {
+                        const u32x4 hi = *reinterpret_cast<const u32x4*>(u_row + ((c ^ us) << 4));
+                        const u32x4 lo = *reinterpret_cast<const u32x4*>(u_row + (((mp + c) ^ us) << 4));
+    #pragma unroll
+                        for (int j = 0; j < SJ; ++j) {
+                            const int mr = wn * 32 * SJ + 32 * j + l32;
+                            const u32x4 p =
+                                *reinterpret_cast<const u32x4*>(m_at + (size_t)(mr * mp + (c ^ rank_swz(mr, mp))) * 16);
+                            d[j] = mfma_32<DT>(p, hi, d[j]);
+                            d[j] = mfma_32<DT>(decltype(special_tag)::value ? without_special<DT>(p) : p, lo, d[j]);
+                        }
                     }
-                }
+                };
+                if (clear) products(std::true_type{});
+                else products(std::false_type{});
 #pragma unroll
                 for (int j = 0; j < SJ; ++j)
 #pragma unroll
@@ -729,6 +773,7 @@ struct GradientLds {
     uint16_t z[2][32 * kGradientCols];
     uint16_t h[2][2][32 * NT * 16];
     int rows[kChunkMax + 64];
+    int odd[4];            // of each wave
 };
 
 // fp16: the powers of two that the rows of h leave out, as one for the whole chunk (the largest, in
@@ -842,12 +887,14 @@ __device__ __forceinline__ void adapter_gradient_body(const AdapterArgs& a, Grad
         return r;
     };
     f32x4 acc[2][NT];  // of columns 32 wave .. + 15 and the 16 after them
-#pragma unroll
-    for (int n = 0; n < NT; ++n) acc[0][n] = acc[1][n] = f32x4{0.f, 0.f, 0.f, 0.f};
-    auto use = [&](int b) {
+    auto use = [&](int b, auto clear) {
         u32x4 zf[2];
 #pragma unroll
         for (int q = 0; q < 2; ++q) zf[q] = turned(lds.z[b], wave * 32 + 16 * q, std::integral_constant<int, 16>{});
+        u32x4 zl[2] = {zf[0], zf[1]};  // with lo
+        if constexpr (decltype(clear)::value)
+#pragma unroll
+            for (int q = 0; q < 2; ++q) zl[q] = without_special<DT>(zf[q]);
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
             const u32x4 hf = turned(lds.h[b][0], n * 16, std::integral_constant<int, HC>{});
@@ -855,26 +902,39 @@ __device__ __forceinline__ void adapter_gradient_body(const AdapterArgs& a, Grad
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
                 acc[q][n] = TURNED ? mfma_16<DT>(hf, zf[q], acc[q][n]) : mfma_16<DT>(zf[q], hf, acc[q][n]);
-                acc[q][n] = TURNED ? mfma_16<DT>(lf, zf[q], acc[q][n]) : mfma_16<DT>(zf[q], lf, acc[q][n]);
+                acc[q][n] = TURNED ? mfma_16<DT>(lf, zl[q], acc[q][n]) : mfma_16<DT>(zl[q], lf, acc[q][n]);
             }
         }
     };
     // steps two at a time; rows past the chunk's end load nothing and count as zeros
     const int n = to - from;
     Step s0, s1;
-    load(s0, 0);
-    load(s1, 32);
-    put(s0, 0, 0);
-    for (int p = 0; p < n; p += 64) {
-        __syncthreads();
-        if (p + 64 < n) load(s0, p + 64);
-        use(0);
-        put(s1, 1, p + 32);
-        __syncthreads();
-        if (p + 64 < n) load(s1, p + 96);
-        use(1);
-        if (p + 64 < n) put(s0, 0, p + 64);
-    }
+    auto run = [&](auto clear) {
+#pragma unroll
+        for (int k = 0; k < NT; ++k) acc[0][k] = acc[1][k] = f32x4{0.f, 0.f, 0.f, 0.f};
+        load(s0, 0);
+        load(s1, 32);
+        put(s0, 0, 0);
+        for (int p = 0; p < n; p += 64) {
+            __syncthreads();
+            if (p + 64 < n) load(s0, p + 64);
+            use(0, clear);
+            put(s1, 1, p + 32);
+            __syncthreads();
+            if (p + 64 < n) load(s1, p + 96);
+            use(1, clear);
+            if (p + 64 < n) put(s0, 0, p + 64);
+        }
+    };
+    run(std::false_type{});
+    // where a sum is infinite or NaN a second time, z's infinities with hi alone
+    f32x4 nan = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int k = 0; k < NT; ++k) nan += (acc[0][k] - acc[0][k]) + (acc[1][k] - acc[1][k]);
+    const bool odd = __any((nan[0] + nan[1]) + (nan[2] + nan[3]) != 0.0f);
+    if (lane == 0) lds.odd[wave] = odd;
+    __syncthreads();
+    if (lds.odd[0] | lds.odd[1] | lds.odd[2] | lds.odd[3]) run(std::true_type{});
     // TURNED: lane has column c + l16 and rank numbers 16 n + 4 lg .. + 3; else rank number
     // 16 n + l16 and columns c + 4 lg .. + 3
     const size_t each = (size_t)a.rank * (size_t)a.cols;

@@ -110,6 +110,63 @@ def test_adapters_of_small_and_large_numbers_in_fp16(x, a, b, g, T, N, K, R, ran
     lu.check(bg, *wb, "b_grad")
 
 
+@pytest.mark.parametrize("dt", [BF16, F16, F32])
+@pytest.mark.parametrize("T,N,K,rank", [(1, 256, 256, 16), (40, 256, 264, 12), (40, 255, 131, 12), (100, 256, 264, 16),
+                                        (700, 256, 256, 16), (700, 251, 203, 33), (700, 256, 256, 128), (2100, 4096, 64, 24),
+                                        (2100, 64, 4096, 64)])
+def test_infinities_of_adapters(T, N, K, rank, dt):
+    """An infinite weight of an adapter, or element of x or of y's gradient, makes results infinite, with the sign of
+    what it is multiplied by, and leaves the others as they were."""
+    R, g, inf = 2, gen(T + rank), float("inf")
+    x, w, grad = normal(g, T, K, dt=dt), normal(g, N, K, size=0.05, dt=dt), normal(g, T, N, size=0.1, dt=dt)
+    a, b = normal(g, R, rank, K, size=0.1, dt=dt), normal(g, R, N, rank, size=0.1, dt=dt)
+    index = (torch.arange(T) * 3 // T - 1).abs().int().cuda()  # runs of adapters 1, 0 and 1
+    scale = torch.tensor([0.75, 1.5]).cuda()
+    mine = index == 1
+    plan = dg.gemm_experts_dispatch_tensors(index[:, None].contiguous(), R)
+    y, u = dg.gemm_adapters_tensors(x, w, a, b, index, scale, keep=True)
+    grads = dg.gemm_adapters_backward_tensors(grad, x, u, w, a, b, index, plan, scale)
+    v = grad.double() @ b[1].double()
+    j = rank - 1
+
+    def check(have, plain, where, of, what):
+        want = plain.clone()
+        want[where] = (of.sign() * inf).to(dt)
+        assert torch.equal(have, want), what
+
+    b2 = b.clone()
+    b2[1, N - 2, j] = inf
+    at = torch.zeros(T, N, dtype=torch.bool, device="cuda")
+    at[mine, N - 2] = True
+    have, u2 = dg.gemm_adapters_tensors(x, w, a, b2, index, scale, keep=True)
+    check(have, y, at, u[mine, j], "y")
+    assert torch.equal(u2, u)
+
+    a2 = a.clone()
+    a2[1, j, K - 3] = -inf
+    at = torch.zeros(T, K, dtype=torch.bool, device="cuda")
+    at[mine, K - 3] = True
+    have = dg.gemm_adapters_backward_tensors(grad, x, u, w, a2, b, index, plan, scale)
+    check(have[0], grads[0], at, -v[mine, j], "x_grad")
+    assert torch.equal(have[1], grads[1]) and torch.equal(have[2], grads[2])
+
+    t = int(mine.nonzero()[0])
+    x2 = x.clone()
+    x2[t, K - 3] = inf
+    at = torch.zeros(R, rank, K, dtype=torch.bool, device="cuda")
+    at[1, :, K - 3] = True
+    have = dg.gemm_adapters_backward_tensors(grad, x2, u, w, a, b, index, plan, scale)
+    check(have[1], grads[1], at, v[t], "a_grad")
+    assert torch.equal(have[0], grads[0]) and torch.equal(have[2], grads[2])
+
+    grad2 = grad.clone()
+    grad2[t, N - 2] = -inf
+    at = torch.zeros(R, N, rank, dtype=torch.bool, device="cuda")
+    at[1, N - 2] = True
+    have = dg.gemm_adapters_backward_tensors(grad2, x, u, w, a, b, index, plan, scale)
+    check(have[2], grads[2], at, -u[t], "b_grad")
+
+
 # ----------------------------------------------------------------------------- loss
 @pytest.mark.parametrize("T,dt", [(66001, F32), (131101, BF16)])
 def test_loss_of_many_tokens(T, dt):
