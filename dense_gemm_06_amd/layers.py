@@ -106,7 +106,7 @@ def _batch(t, what):
     shape, strides = t.shape, t.stride()
     if len(shape) != 3:
         raise ValueError(f"{what} must be 3-D, not {tuple(shape)}")
-    ld = strides[1] if strides[2] == 1 and strides[1] >= shape[2] > 0 else _ld(shape, strides, what)
+    ld = strides[1] if strides[2] == 1 and strides[1] >= shape[2] > 0 and shape[1] > 1 else _ld(shape, strides, what)
     return ld, strides[0] if shape[0] > 1 else 0
 
 

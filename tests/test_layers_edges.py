@@ -126,3 +126,11 @@ def test_pieces_of_many_tokens(T, dtype):
     d = T * 256 * es
     assert lib().gemm_loss_backward_workspace(T, V, K, dtype, 1, 0, 0) >= d
     assert lib().gemm_loss_workspace(T, V, 4, dtype) >= T * 256 * 4  # the logits' own piece
+
+
+def test_batches_of_single_rows():
+    """The stride of a matrix's only row is anything: adapters of rank 1 stored as 1 x R x K."""
+    a = torch.empty(1, 3, 2 ** 22, device="meta").transpose(0, 1)
+    assert a.stride(1) > 2 ** 23 and dg.layers._batch(a, "a") == (2 ** 22, 2 ** 22)
+    b = torch.empty(4, 1, 8)
+    assert dg.layers._batch(b, "b") == (8, 8)
