@@ -204,13 +204,23 @@ int tiles_form(const void* x, int64_t ldx, const void* w, int64_t ldw, int64_t c
 struct Slices {
     int64_t count, k;
 };
-Slices slices_of(int64_t tiles, int64_t K, int64_t others = 0) {
+Slices slices_of(int64_t tiles, int64_t K, int64_t others = 0, bool equal = false) {
     const int64_t stages = std::max<int64_t>(1, ceil_div(K, 128)), most = 2 * dg::kCus;
     tiles = std::max<int64_t>(1, tiles);  // none where the result is empty
     int64_t want = ceil_div(most, tiles);
-    // room for `others` workgroups beside them, rather than after them (u's of 20 tokens, 4096 x 4096, 8
-    // adapters of rank 16: 25.5 to 23.2 us, of 64 tokens, 2048 x 2048: 20.0 to 16.0; 48 tokens as before)
-    if (others > 0 && want * tiles <= most && tiles <= most - others) want = (most - others) / tiles;
+    // room for `others` workgroups beside them, rather than after them, and with many rows of x, whose
+    // copies take longer, slices of equally many stages or nearly so (17, 33 and 64 tokens of 4096 x 4096,
+    // rank 16: 14.4, 17.0, 18.9 us without the room, 13.0, 16.5, 18.7 with it in 7 slices, 13.0, 16.0, 17.4 in 4;
+    // rank 64: 17.5, 21.5, 25.8, then 16.3, 23.4, 24.3, then 16.4, 20.5, 24.9; 4096 x 14336: 28.3, 33.3, 35.1,
+    // then 25.3, 33.7, 35.3; 32 tokens of 4096 x 4096 in 4 slices 13.9, in 7 13.3)
+    if (others > 0 && want * tiles <= most && tiles <= most - others) {
+        want = (most - others) / tiles;
+        for (int64_t n = want; equal && n >= 2 && 2 * n >= want; --n)
+            if (16 * (n * ceil_div(stages, n) - stages) <= stages) {
+                want = n;
+                break;
+            }
+    }
     want = std::min({want, stages, (int64_t)32});
     const int64_t k = ceil_div(stages, want) * 128;
     return {std::max<int64_t>(1, ceil_div(K, k)), k};
@@ -263,7 +273,7 @@ AdapterSpace adapter_space(void* workspace, int64_t tokens, int64_t N, int64_t K
     AdapterSpace s;
     Parts p{static_cast<char*>(workspace)};
     if (few_tokens(tokens, K, dtype)) {
-        s.slices = slices_of(ceil_div(N, 64), K, tokens > 16 ? tokens * rank_padded(rank) / 16 : 0);
+        s.slices = slices_of(ceil_div(N, 64), K, tokens > 16 ? tokens * rank_padded(rank) / 16 : 0, tokens > 32);
         s.part = static_cast<float*>(p.take(s.slices.count * tokens * ceil_div(N, 4) * 16));
     } else {
         product_space(s, p, tokens, N, K, dtype, in_tiles(tokens, N, K, rank, dtype), true);
