@@ -15,8 +15,8 @@
  *    must be ordered.
  *  - Sizes are below 2^30 per dimension (2^31 for the activations), and the leading
  *    dimensions of what enters a product below 2^23, as everywhere in this library
- *    (GEMM_ERR_UNSUPPORTED otherwise); addresses are 64 bits. Empty outputs are successful
- *    no-ops.
+ *    (GEMM_ERR_UNSUPPORTED otherwise, as where a launch would need 2^32 threads); addresses are
+ *    64 bits. Empty outputs are successful no-ops.
  *  - Index arrays come from the device and are not read by the host: an index out of range
  *    stands for none, and nothing outside the given arrays is read or written.
  *  - Every argument is validated before anything is enqueued. Outputs must not overlap
@@ -64,7 +64,8 @@ int64_t gemm_adapters_workspace(int64_t tokens, int64_t N, int64_t K, int64_t ra
  *     x_grad[t] = w^T grad[t] + a_i^T v[t]                  (tokens x K; NULL: not wanted)
  *     a_grad_i = sum over the rows t of adapter i of v[t] x[t]^T           (as a, contiguous)
  *     b_grad_i = sum over them of scale_i grad[t] u[t]^T                   (as b, contiguous)
- * plan is gemm_experts_dispatch's of index as tokens x 1 (top_k 1, align 1; for up to 1024 adapters);
+ * plan is gemm_experts_dispatch's of index as tokens x 1 (top_k 1, align 1; for up to 1024 adapters, and
+ * with 16-bit matrices 2^25 tokens less 512 for each adapter);
  * v enters its products as u does. An adapter without rows gets zeros. a_grad and b_grad come together or are both NULL (an empty one
  * may be). Sums are fp32 in a fixed order.
  */
@@ -93,8 +94,10 @@ int64_t gemm_loss_workspace(int64_t tokens, int64_t vocabulary, int64_t K, int d
  *     d[t][v] = grad[t] (exp(l[t][v] - lse[t]) - [v = target[t]])
  * (zeros where the target lies outside), x_grad = d w and w_grad = d^T x, in the matrices'
  * type; either may be NULL. The vocabulary is taken `piece` columns at a time (0: the
- * library's choice), whose d are held in the workspace in the matrices' type and summed in
- * fp32; smaller pieces need less workspace.
+ * library's choice), whose d are held in the workspace in the matrices' type (fp16: times a power
+ * of two that brings the largest |grad| near 2^14, so that d of tokens whose |grad| is below 2^-20 of
+ * it has fewer digits) and summed in fp32; smaller pieces need less workspace. w_grad takes up to
+ * 2^23 - 32 tokens.
  */
 int gemm_loss_backward(const float* grad, const void* x, int64_t tokens, int64_t K, int64_t ldx, const void* w,
                        int64_t vocabulary, int64_t ldw, int dtype, const int64_t* target, const float* lse, void* x_grad,
