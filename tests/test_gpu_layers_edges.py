@@ -184,6 +184,21 @@ def test_loss_of_many_tokens(T, dt):
         lu.check(have, ref, err, name)
 
 
+@pytest.mark.parametrize("dt", [BF16, F16, F32])
+@pytest.mark.parametrize("T,V,K", [(0, 9, 8), (0, 0, 8), (0, 9, 0), (5, 9, 0), (5, 0, 8), (5, 0, 0), (70, 9, 0), (70, 0, 64)])
+def test_loss_of_empty_sizes(T, V, K, dt):
+    """Without a sum's terms every logit is 0; without words lse is -inf and no target counts."""
+    x, w = torch.zeros(T, K, dtype=dt, device="cuda"), torch.zeros(V, K, dtype=dt, device="cuda")
+    target, grad = torch.arange(T).cuda() % 5, torch.ones(T, device="cuda")
+    loss, lse = dg.gemm_loss_tensors(x, w, target)
+    want = torch.logsumexp(torch.zeros(T, V, dtype=torch.float64), 1)
+    # a logarithm of a whole number: four steps of it
+    lu.check(lse, want, want.abs().nan_to_num(posinf=0) * 4 * lu.F32, "lse")
+    lu.check(loss, want if V else torch.zeros(T).double(), want.abs().nan_to_num(posinf=0) * 4 * lu.F32, "loss")
+    for name, have, like in zip(("x_grad", "w_grad"), dg.gemm_loss_backward_tensors(grad, x, w, target, lse), (x, w)):
+        assert have.shape == like.shape and have.dtype == dt and not have.any(), name
+
+
 # ----------------------------------------------------------------------------- activations
 @pytest.mark.parametrize("dt", [BF16, F16, F32])
 @pytest.mark.parametrize("kind", ["relu", "gelu_tanh", "silu"])
