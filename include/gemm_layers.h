@@ -64,10 +64,10 @@ int64_t gemm_adapters_workspace(int64_t tokens, int64_t N, int64_t K, int64_t ra
  *     x_grad[t] = w^T grad[t] + a_i^T v[t]                  (tokens x K; NULL: not wanted)
  *     a_grad_i = sum over the rows t of adapter i of v[t] x[t]^T           (as a, contiguous)
  *     b_grad_i = sum over them of scale_i grad[t] u[t]^T                   (as b, contiguous)
- * plan is gemm_experts_dispatch's of index as tokens x 1 (top_k 1, align 1; for up to 1024 adapters, and
- * with 16-bit matrices 2^25 tokens less 512 for each adapter);
- * v enters its products as u does. An adapter without rows gets zeros. a_grad and b_grad come together or are both NULL (an empty one
- * may be). Sums are fp32 in a fixed order.
+ * v enters its products as u does. plan is gemm_experts_dispatch's of index as tokens x 1 (top_k 1,
+ * align 1; for up to 1024 adapters, and with 16-bit matrices 2^25 tokens less 512 for each adapter);
+ * an adapter without rows gets zeros. a_grad and b_grad come together or are both NULL (an empty
+ * one may be NULL by itself). Sums are fp32 in a fixed order.
  */
 int gemm_adapters_backward(const void* grad, int64_t tokens, int64_t N, int64_t ldg, const void* x, int64_t K,
                            int64_t ldx, const float* u, const void* w, int64_t ldw, int dtype,
